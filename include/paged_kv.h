@@ -93,6 +93,7 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1 } pkv_dtype_t;
 #define PKV_DEV_BAD_PAIR        0x8u  /* copy pair with src or dst outside the pool */
 #define PKV_DEV_WAIT_TIMEOUT    0x10u /* a bounded wait on a copy gave up */
 #define PKV_DEV_BAD_PLAN        0x20u /* a planned decode found no plan of its batch size */
+#define PKV_DEV_OUT_OF_BLOCKS   0x40u /* extend_block_tables: the free stack holds too few blocks */
 
 typedef struct CUstream_st* pkv_stream_t; /* same type as cudaStream_t */
 
@@ -499,6 +500,196 @@ pkv_status_t pkv_copy_blocks_int8(
     int8_t* k_cache, int8_t* v_cache, float* k_scale, float* v_scale,
     const int64_t* src_dst_pairs, int num_pairs, int num_kv_heads, int head_dim,
     int num_blocks, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 4-bit KV cache ([G] "他のKVキャッシュ最適化との組み合わせ": quantised      */
+/* caches combine with paging)                                               */
+/* ------------------------------------------------------------------------ */
+/*
+ * The page names no scheme for fewer than 8 bits; this library takes the
+ * asymmetric per-group reading. Every stored row (block, KV head, slot) of K
+ * and of V is cut into groups of 64 head dims, and a group x keeps 4-bit codes
+ * c and a pair {s, z} of the row's type T (fp16 or bf16):
+ *     z = min x,   s = round_T((0.5 max x - 0.5 z) / 7.5),
+ *     c = clamp(rint((0.5 x - 0.5 z) / (0.5 s)), 0, 15)   (0 where s = 0),
+ * in IEEE fp32 (rint: ties to even), so that x ~= z + c s with an error of at
+ * most s / 2 for x <= z + 15 s; rounding s down moves the largest x past that
+ * by at most 15 s 2^-9 for bf16 (2^-12 for fp16). A group that holds an
+ * infinity or NaN reads as NaN. 4.5 bits an element: 18 * head_dim bytes hold
+ * the K and V of 16 tokens of one KV head, against 64 * head_dim in 16 bits.
+ *
+ *   kv_cache : uint8[num_blocks][num_kv_heads][18 * head_dim], 16-byte aligned,
+ *              K and V of one (block, KV head) together: K codes, V codes, K
+ *              pairs, V pairs. The order inside a tile is the library's own
+ *              (csrc/int4_layout.cuh); pkv_reshape_and_cache_int4 writes it and
+ *              pkv_gather_cache_int4 reads it back. T is the dtype of every
+ *              call on one cache; the cache does not record it.
+ * head_dim is 64, 128 or 256.
+ */
+
+/* Bytes of one (block, KV head) tile: 18 * head_dim; 0 for other head_dims. */
+size_t pkv_int4_tile_bytes(int head_dim);
+
+/* Quantising cache write: as pkv_reshape_and_cache, each row quantised as
+ * above (bit-exact to the definition). Slots < 0 are skipped; slots >=
+ * num_blocks*16 are skipped and flagged (PKV_DEV_BAD_SLOT). Two tokens with
+ * the same slot race (unspecified winner, element by element). */
+pkv_status_t pkv_reshape_and_cache_int4(
+    const void* k, const void* v, pkv_dtype_t dtype, void* kv_cache,
+    const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
+    int num_blocks, pkv_stream_t stream);
+
+/* Reads stored rows back: for each t and KV head g, k[t][g] (v likewise)
+ * receives round_T(z + c s) of the row at slot_mapping[t], zeros for slots < 0
+ * and (flagged, PKV_DEV_BAD_SLOT) for slots >= num_blocks*16. For prompt
+ * attention over a cached prefix, and for moving rows to another cache. */
+pkv_status_t pkv_gather_cache_int4(
+    void* k, void* v, pkv_dtype_t dtype, const void* kv_cache,
+    const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
+    int num_blocks, pkv_stream_t stream);
+
+/* Copy-on-write block copies of a 4-bit cache (rules of pkv_copy_blocks).
+ * Pairs (-1, -1) are padding: skipped without a flag, so a list of fixed size
+ * (cow_pairs of pkv_extend_block_tables) can be passed whole. */
+pkv_status_t pkv_copy_blocks_int4(
+    void* kv_cache, const int64_t* src_dst_pairs, int num_pairs, int num_kv_heads,
+    int head_dim, int num_blocks, pkv_stream_t stream);
+
+/*
+ * Decode over the 4-bit cache: pkv_paged_attention_decode with every K and V
+ * row read as z + c s (in fp32, not rounded to T). q and out are T = dtype.
+ * sliding_window as for pkv_paged_attention_decode_sliding (<= 0: none).
+ * partition_size 0, -1 or N > 0; the balanced (-2) and shared-prefix (-5)
+ * schedules return PKV_ERR_UNSUPPORTED. Workspace:
+ * pkv_paged_attention_workspace_size, or with a window
+ * pkv_paged_attention_sliding_workspace_size, with the same arguments.
+ */
+pkv_status_t pkv_paged_attention_decode_int4(
+    void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+    int head_dim, int max_blocks_per_seq, int num_blocks, float scale,
+    pkv_dtype_t dtype, int sliding_window, int partition_size, void* workspace,
+    size_t workspace_bytes, pkv_stream_t stream);
+
+/* The same without a window, with the launch plan that pkv_paged_attention_plan
+ * left in `workspace` (see pkv_paged_attention_decode_int8_planned). */
+pkv_status_t pkv_paged_attention_decode_int4_planned(
+    void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+    int head_dim, int max_blocks_per_seq, int num_blocks, float scale,
+    pkv_dtype_t dtype, int partition_size, void* workspace,
+    size_t workspace_bytes, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Latent attention: one shared row per token                                */
+/* ------------------------------------------------------------------------ */
+/*
+ * In latent attention a token's keys and values of all heads are linear maps
+ * of one latent vector c (512 elements), and a rotary part r (64 elements)
+ * shared by all heads joins the keys: k_h = [U_h c, r], v_h = W_h c. Absorbing
+ * U_h into the query (q_h = [U_h^T qn_h, qr_h], 576 elements) and W_h into the
+ * output projection leaves attention of every head over the same rows [c, r]:
+ *     out[s][h] = softmax_p( scale * <q[s][h], row_p> ) . c_p,  p < L.
+ * These calls keep and read those rows; the two absorbed projections are
+ * matrix products of the caller's.
+ *   cache : T[num_blocks][16][576], the latent part first; 16-byte aligned
+ *   q     : T[num_seqs][num_heads][576];  out : T[num_seqs][num_heads][512]
+ * Block tables, lengths, slots and pools as everywhere else; T is fp16 or bf16.
+ */
+
+/* Writes each new token's row: cache[slot/16][slot%16] = [latent[t], rope[t]]
+ * (a bit copy). latent: T[num_tokens][512] with rows latent_stride elements
+ * apart, rope: T[num_tokens][64] with rows rope_stride apart (both multiples
+ * of 8: slices of one projection's output need no copy). Slots as for
+ * pkv_reshape_and_cache. */
+pkv_status_t pkv_latent_cache_write(
+    const void* latent, const void* rope, int64_t latent_stride, int64_t rope_stride,
+    pkv_dtype_t dtype, void* cache, const int64_t* slot_mapping, int num_tokens,
+    int num_blocks, pkv_stream_t stream);
+
+/* Copy-on-write block copies of a latent cache (see pkv_copy_blocks_int4). */
+pkv_status_t pkv_copy_blocks_latent(
+    void* cache, const int64_t* src_dst_pairs, int num_pairs, int num_blocks,
+    pkv_stream_t stream);
+
+/*
+ * Latent decode, one query token per sequence, for 1..1024 heads. Softmax
+ * statistics and sums in fp32; a length of 0 writes zeros. The workspace (of
+ * pkv_latent_workspace_size bytes, 16-byte aligned, NULL when that is 0) needs
+ * no initialisation; calls that use one workspace must not overlap on the GPU.
+ */
+pkv_status_t pkv_paged_latent_decode(
+    void* out, const void* q, const void* cache, const int32_t* block_tables,
+    const int32_t* context_lens, int num_seqs, int num_heads, int max_blocks_per_seq,
+    int num_blocks, float scale, pkv_dtype_t dtype, void* workspace,
+    size_t workspace_bytes, pkv_stream_t stream);
+
+size_t pkv_latent_workspace_size(int num_seqs, int num_heads, int max_blocks_per_seq);
+
+/* ------------------------------------------------------------------------ */
+/* Block tables and slot maps on the device ([S] "KV キャッシュマネージャ")    */
+/* ------------------------------------------------------------------------ */
+/*
+ * The block manager's append and release for a batch, on `stream`: a captured
+ * decode loop needs no host round trip. The state is the caller's device
+ * memory:
+ *   block_tables : int32[num_seqs][max_blocks_per_seq]
+ *   context_lens : int32[num_seqs], tokens held
+ *   free_stack   : int32[num_blocks], the free ids at the bottom
+ *                  (free_stack[0 .. *free_count), the top is taken first)
+ *   refcounts    : int32[num_blocks], tables that hold each block; NULL when
+ *                  no block is ever shared
+ */
+
+/*
+ * Reserves new_tokens[s] (>= 0) more tokens for every sequence: blocks are
+ * taken from the stack and entered into the tables, and the slot of every new
+ * token, sequence after sequence, goes to slot_mapping (what the cache writes
+ * take); entries past the batch's tokens become -1, so num_slots may be a
+ * fixed capacity. A sequence that starts inside a block still shared takes a
+ * copy of it first (copy-on-write): its (src, dst) pair is packed into
+ * cow_pairs (int64[num_seqs][2], the rest (-1, -1)) and must be copied before
+ * the new tokens are written; fresh blocks get refcount 1, src loses one.
+ * Blocks are taken, and pairs made, as pkv_bm_append_slot makes them when
+ * called new_tokens[s] times for s = 0, 1, ...
+ * new_lens and new_free_count receive the state after the call; each may be
+ * context_lens or free_count itself. Reading old arrays and writing new ones,
+ * a call can be repeated (where nothing is shared).
+ * info (int32[4], may be NULL): {PKV_DEV_* flags that failed the call or 0,
+ * tokens, blocks taken, pairs}.
+ * All or nothing: when the stack holds too few blocks (PKV_DEV_OUT_OF_BLOCKS),
+ * a length is negative or passes the table (PKV_DEV_BAD_CONTEXT_LEN), the
+ * tokens exceed num_slots (PKV_DEV_BAD_SLOT) or *free_count is out of range
+ * (PKV_DEV_BAD_BLOCK_ID), the flag is raised, tables and refcounts stay as
+ * they were, new_lens and new_free_count repeat the old state, and every slot
+ * and pair is -1. A stack or table entry outside the pool is flagged
+ * (PKV_DEV_BAD_BLOCK_ID) and its tokens get slot -1.
+ * Workspace: pkv_extend_workspace_size bytes, as for the other calls.
+ */
+pkv_status_t pkv_extend_block_tables(
+    int32_t* block_tables, const int32_t* context_lens, const int32_t* new_tokens,
+    int num_seqs, int max_blocks_per_seq, const int32_t* free_stack,
+    const int32_t* free_count, int num_blocks, int32_t* refcounts, int32_t* new_lens,
+    int32_t* new_free_count, int64_t* slot_mapping, int num_slots, int64_t* cow_pairs,
+    int32_t* info, void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+size_t pkv_extend_workspace_size(int num_seqs, int num_slots);
+
+/*
+ * Drops every sequence s with finished[s] != 0 (int32): its table entries
+ * become -1 and its length 0, each block loses one hold, and the blocks that
+ * nothing holds any more are pushed onto the free stack in ascending order of
+ * id (the host manager pushes in table order; the set is the same). Entries
+ * below 0 (released before) are skipped. Flagged with PKV_DEV_BAD_BLOCK_ID
+ * and not pushed twice: an id outside the pool, a block without a hold, a
+ * block that two sequences own without refcounts.
+ */
+pkv_status_t pkv_release_sequences(
+    int32_t* block_tables, int32_t* context_lens, const int32_t* finished, int num_seqs,
+    int max_blocks_per_seq, int32_t* free_stack, int32_t* free_count, int num_blocks,
+    int32_t* refcounts, void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+size_t pkv_release_workspace_size(int num_blocks);
 
 /* ------------------------------------------------------------------------ */
 /* Host block manager ([S] "KV キャッシュマネージャ", [B] "OSの知恵をGPUへ")  */

@@ -15,13 +15,24 @@ from .binding import (  # noqa: F401
     copy_blocks,
     describe_device_flags,
     device_status,
+    copy_blocks_int4,
     copy_blocks_int8,
+    copy_blocks_latent,
+    extend_block_tables,
+    gather_cache_int4,
+    int4_tile_bytes,
+    latent_cache_write,
+    latent_workspace_size,
     paged_attention_decode,
+    paged_attention_decode_int4,
     paged_attention_decode_int8,
     paged_attention_decode_noalloc,
     paged_attention_decode_sliding,
     paged_attention_plan,
+    paged_latent_decode,
+    release_sequences,
     reshape_and_cache,
+    reshape_and_cache_int4,
     reshape_and_cache_int8,
     sliding_workspace_size,
     resolved_partition,

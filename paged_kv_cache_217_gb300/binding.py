@@ -27,7 +27,8 @@ BALANCED = -2                      # pkv_paged_attention_partition: balanced per
 SHARED_PREFIX = -5                 # pkv_paged_attention_partition: shared-prefix schedule
 
 DEV_FLAGS = {0x1: "BAD_BLOCK_ID", 0x2: "BAD_CONTEXT_LEN", 0x4: "BAD_SLOT", 0x8: "BAD_PAIR",
-             0x10: "WAIT_TIMEOUT", 0x20: "BAD_PLAN"}
+             0x10: "WAIT_TIMEOUT", 0x20: "BAD_PLAN", 0x40: "OUT_OF_BLOCKS"}
+LATENT_DIM, ROPE_DIM = 512, 64     # a latent cache row: the latent vector, then the shared rotary part
 
 
 class LibraryNotBuilt(RuntimeError):
@@ -73,6 +74,23 @@ _SIGS = {
     "pkv_paged_attention_decode_int8_planned": ([_c_p] * 8 + [_c_int] * 6 + [_c_f, _c_int, _c_int, _c_p, _c_sz,
                                                                             _c_p], _c_int),
     "pkv_copy_blocks_int8": ([_c_p] * 5 + [_c_int] * 4 + [_c_p], _c_int),
+    "pkv_int4_tile_bytes": ([_c_int], _c_sz),
+    "pkv_reshape_and_cache_int4": ([_c_p, _c_p, _c_int, _c_p, _c_p] + [_c_int] * 4 + [_c_p], _c_int),
+    "pkv_gather_cache_int4": ([_c_p, _c_p, _c_int, _c_p, _c_p] + [_c_int] * 4 + [_c_p], _c_int),
+    "pkv_copy_blocks_int4": ([_c_p, _c_p] + [_c_int] * 4 + [_c_p], _c_int),
+    "pkv_paged_attention_decode_int4": ([_c_p] * 5 + [_c_int] * 6 + [_c_f, _c_int, _c_int, _c_int, _c_p, _c_sz, _c_p],
+                                        _c_int),
+    "pkv_paged_attention_decode_int4_planned": ([_c_p] * 5 + [_c_int] * 6 + [_c_f, _c_int, _c_int, _c_p, _c_sz, _c_p],
+                                                _c_int),
+    "pkv_latent_cache_write": ([_c_p, _c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_int, _c_int, _c_p], _c_int),
+    "pkv_copy_blocks_latent": ([_c_p, _c_p, _c_int, _c_int, _c_p], _c_int),
+    "pkv_paged_latent_decode": ([_c_p] * 5 + [_c_int] * 4 + [_c_f, _c_int, _c_p, _c_sz, _c_p], _c_int),
+    "pkv_latent_workspace_size": ([_c_int] * 3, _c_sz),
+    "pkv_extend_block_tables": ([_c_p] * 3 + [_c_int] * 2 + [_c_p] * 2 + [_c_int] + [_c_p] * 4 +
+                                [_c_int, _c_p, _c_p, _c_p, _c_sz, _c_p], _c_int),
+    "pkv_extend_workspace_size": ([_c_int] * 2, _c_sz),
+    "pkv_release_sequences": ([_c_p] * 3 + [_c_int] * 2 + [_c_p] * 2 + [_c_int, _c_p, _c_p, _c_sz, _c_p], _c_int),
+    "pkv_release_workspace_size": ([_c_int], _c_sz),
     "pkv_selftest_bounded_wait": ([ctypes.c_uint32, _c_p], _c_int),
     "pkv_trace_enabled": ([], _c_int),
     "pkv_set_trace_buffer": ([_c_p, _c_int], _c_int),
@@ -431,6 +449,260 @@ def copy_blocks_int8(k_cache, v_cache, k_scale, v_scale, src_dst_pairs):
             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), src_dst_pairs.data_ptr(), src_dst_pairs.shape[0],
             hkv, D, nb)
+
+
+# ---------------------------------------------------------------------------
+# 4-bit KV cache: uint8 [num_blocks, Hkv, 18 * D], K and V of a (block, KV head) in one tile
+# ---------------------------------------------------------------------------
+def _scratch(device, nbytes):
+    """Workspace of one call: a torch allocation of the current stream, which its allocator hands out
+    again only to later work of that stream (and, under capture, only inside the captured graph)."""
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _ptr_bytes(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def int4_tile_bytes(head_dim):
+    """Bytes of one (block, KV head) tile of the 4-bit cache (18 * head_dim); 0 for head dims it does not take."""
+    return int(lib().pkv_int4_tile_bytes(int(head_dim)))
+
+
+def _check_int4(k, v, kv_cache, slot_mapping):
+    import torch
+    _need_cuda(k, v, kv_cache, slot_mapping)
+    dt = _dtype_code(k)
+    if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be [T, Hkv, D] of one dtype")
+    T, hkv, D = k.shape
+    if kv_cache.dtype != torch.uint8 or slot_mapping.dtype != torch.int64:
+        raise TypeError("kv_cache must be uint8, slot_mapping int64")
+    if kv_cache.dim() != 3 or tuple(kv_cache.shape[1:]) != (hkv, 18 * D) or tuple(slot_mapping.shape) != (T,):
+        raise ValueError("kv_cache: [num_blocks, Hkv, 18 * D]; slot_mapping: [T]")
+    return dt, T, hkv, D, kv_cache.shape[0]
+
+
+def reshape_and_cache_int4(k, v, kv_cache, slot_mapping):
+    """Quantise each new K/V row to 4 bits (per 64 head dims: offset min x, scale (max x - min x) / 15 in k's
+    dtype) into its slot of the 4-bit cache; slots < 0 are skipped."""
+    dt, T, hkv, D, nb = _check_int4(k, v, kv_cache, slot_mapping)
+    _launch(k.device, "reshape_and_cache_int4", lib().pkv_reshape_and_cache_int4, k.data_ptr(), v.data_ptr(), dt,
+            kv_cache.data_ptr(), slot_mapping.data_ptr(), T, hkv, D, nb)
+
+
+def gather_cache_int4(k, v, kv_cache, slot_mapping):
+    """The rows stored at slot_mapping, read back into k and v [T, Hkv, D] (in place; zeros for slots < 0)."""
+    dt, T, hkv, D, nb = _check_int4(k, v, kv_cache, slot_mapping)
+    _launch(k.device, "gather_cache_int4", lib().pkv_gather_cache_int4, k.data_ptr(), v.data_ptr(), dt,
+            kv_cache.data_ptr(), slot_mapping.data_ptr(), T, hkv, D, nb)
+
+
+def copy_blocks_int4(kv_cache, src_dst_pairs):
+    """copy_blocks for the 4-bit cache; pairs (-1, -1) are padding."""
+    import torch
+    _need_cuda(kv_cache, src_dst_pairs)
+    if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 3 or kv_cache.shape[2] % 18:
+        raise ValueError("kv_cache must be uint8 [num_blocks, Hkv, 18 * D]")
+    if src_dst_pairs.dtype != torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+        raise ValueError("src_dst_pairs must be int64 [n, 2]")
+    nb, hkv, tile = kv_cache.shape
+    _launch(kv_cache.device, "copy_blocks_int4", lib().pkv_copy_blocks_int4, kv_cache.data_ptr(),
+            src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], hkv, tile // 18, nb)
+
+
+def paged_attention_decode_int4(out, q, kv_cache, block_tables, context_lens, scale, sliding_window=0,
+                                partition_size=0, workspace=None, planned=False):
+    """paged_attention_decode over the 4-bit cache (K and V read as offset + code * scale per 64 head dims).
+
+    q, out: [S, Hq, D] of the dtype the cache was written from; kv_cache: uint8
+    [num_blocks, Hkv, 18 * D]. ``sliding_window`` > 0 attends over the last
+    tokens only; ``planned`` (without a window) uses the launch plan that
+    paged_attention_plan left in the same workspace."""
+    import torch
+    _need_cuda(out, q, kv_cache, block_tables, context_lens)
+    dt = _dtype_code(q)
+    if out.dtype != q.dtype:
+        raise TypeError("q and out must share one dtype")
+    if kv_cache.dtype != torch.uint8:
+        raise TypeError("kv_cache must be uint8")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if q.dim() != 3 or kv_cache.dim() != 3 or out.shape != q.shape or kv_cache.shape[2] != 18 * q.shape[2] \
+            or block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0] \
+            or tuple(context_lens.shape) != (q.shape[0],):
+        raise ValueError("shape mismatch among out, q, kv_cache, block_tables and context_lens")
+    window = max(0, int(sliding_window))
+    if planned and window:
+        raise ValueError("a planned call takes no sliding window")
+    S, Hq, D = q.shape
+    nb, hkv = kv_cache.shape[0], kv_cache.shape[1]
+    mb = block_tables.shape[1]
+    need = sliding_workspace_size(S, Hq, hkv, D, mb, window, partition_size)
+    if workspace is None and need:
+        workspace = _workspace(q.device, need) if planned else _scratch(q.device, need)
+    ws_ptr, ws_bytes = _ptr_bytes(workspace if need else None)
+    args = (out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Hq,
+            hkv, D, mb, nb, float(scale), dt)
+    if planned:
+        _launch(q.device, "paged_attention_decode_int4_planned", lib().pkv_paged_attention_decode_int4_planned, *args,
+                int(partition_size), ws_ptr, ws_bytes)
+    else:
+        _launch(q.device, "paged_attention_decode_int4", lib().pkv_paged_attention_decode_int4, *args, window,
+                int(partition_size), ws_ptr, ws_bytes)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# latent attention: one row [latent 512, rotary 64] per token, cache [num_blocks, 16, 576]
+# ---------------------------------------------------------------------------
+def _check_latent_cache(cache):
+    if cache.dim() != 3 or tuple(cache.shape[1:]) != (BLOCK_SIZE, LATENT_DIM + ROPE_DIM):
+        raise ValueError("a latent cache is [num_blocks, 16, 576]")
+
+
+def latent_cache_write(latent, rope, cache, slot_mapping):
+    """cache[slot // 16, slot % 16] = [latent[t], rope[t]] for every token t with slot >= 0. latent [T, 512]
+    and rope [T, 64] may be slices of one tensor (rows a multiple of 8 elements apart)."""
+    import torch
+    _need_cuda(cache, slot_mapping)
+    dt = _dtype_code(cache)
+    _check_latent_cache(cache)
+    if latent.dtype != cache.dtype or rope.dtype != cache.dtype:
+        raise TypeError("latent, rope and cache must share one dtype")
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if latent.device != cache.device or rope.device != cache.device or slot_mapping.dim() != 1:
+        raise ValueError("tensors must be on one device, slot_mapping [T]")
+    T = slot_mapping.shape[0]
+    if tuple(latent.shape) != (T, LATENT_DIM) or tuple(rope.shape) != (T, ROPE_DIM):
+        raise ValueError("latent must be [T, 512] and rope [T, 64]")
+    if T and (latent.stride(1) != 1 or rope.stride(1) != 1):
+        raise ValueError("rows of latent and rope must be contiguous")
+    _launch(cache.device, "latent_cache_write", lib().pkv_latent_cache_write, latent.data_ptr(), rope.data_ptr(),
+            latent.stride(0), rope.stride(0), dt, cache.data_ptr(), slot_mapping.data_ptr(), T, cache.shape[0])
+
+
+def copy_blocks_latent(cache, src_dst_pairs):
+    """copy_blocks for a latent cache; pairs (-1, -1) are padding."""
+    import torch
+    _need_cuda(cache, src_dst_pairs)
+    _dtype_code(cache)
+    _check_latent_cache(cache)
+    if src_dst_pairs.dtype != torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+        raise ValueError("src_dst_pairs must be int64 [n, 2]")
+    _launch(cache.device, "copy_blocks_latent", lib().pkv_copy_blocks_latent, cache.data_ptr(),
+            src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], cache.shape[0])
+
+
+def latent_workspace_size(num_seqs, num_heads, max_blocks_per_seq):
+    return int(lib().pkv_latent_workspace_size(int(num_seqs), int(num_heads), int(max_blocks_per_seq)))
+
+
+def paged_latent_decode(out, q, cache, block_tables, context_lens, scale, workspace=None):
+    """out[s, h] = softmax(scale * R_s q[s, h]) C_s, with R_s the sequence's cache rows (576 elements) and C_s
+    their first 512 (latent attention, absorbed form). q: [S, H, 576]; out: [S, H, 512]; cache:
+    [num_blocks, 16, 576]."""
+    import torch
+    _need_cuda(out, q, cache, block_tables, context_lens)
+    dt = _dtype_code(q)
+    _check_latent_cache(cache)
+    if out.dtype != q.dtype or cache.dtype != q.dtype:
+        raise TypeError("q, out and cache must share one dtype")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if q.dim() != 3 or q.shape[2] != LATENT_DIM + ROPE_DIM or tuple(out.shape) != (*q.shape[:2], LATENT_DIM) \
+            or block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0] \
+            or tuple(context_lens.shape) != (q.shape[0],):
+        raise ValueError("q: [S, H, 576]; out: [S, H, 512]; block_tables: [S, max_blocks]; context_lens: [S]")
+    S, H, _ = q.shape
+    mb = block_tables.shape[1]
+    need = latent_workspace_size(S, H, mb)
+    if workspace is None:
+        workspace = _scratch(q.device, need)
+    ws_ptr, ws_bytes = _ptr_bytes(workspace if need else None)
+    _launch(q.device, "paged_latent_decode", lib().pkv_paged_latent_decode, out.data_ptr(), q.data_ptr(),
+            cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, H, mb, cache.shape[0], float(scale),
+            dt, ws_ptr, ws_bytes)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# block tables and slot maps on the device
+# ---------------------------------------------------------------------------
+def _need_int(dtype_name, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if t.dtype != getattr(torch, dtype_name):
+            raise TypeError(f"{name} must be {dtype_name}")
+
+
+def extend_block_tables(block_tables, context_lens, new_tokens, free_stack, free_count, slot_mapping, refcounts=None,
+                        cow_pairs=None, info=None, new_lens=None, new_free_count=None, workspace=None):
+    """Reserves new_tokens[s] more tokens per sequence on the device: takes blocks from the free stack into
+    block_tables, writes every new token's slot (sequence after sequence, then -1) into slot_mapping, and the
+    lengths and free count after the call into new_lens and new_free_count (default: in place). With
+    ``refcounts`` (int32 [num_blocks]) shared last blocks are replaced and their (src, dst) pairs packed into
+    ``cow_pairs`` (int64 [S, 2]). All or nothing; see pkv_extend_block_tables for ``info`` (int32 [4]) and flags."""
+    new_lens = context_lens if new_lens is None else new_lens
+    new_free_count = free_count if new_free_count is None else new_free_count
+    _need_cuda(block_tables, context_lens, new_tokens, free_stack, free_count, slot_mapping, new_lens, new_free_count,
+               *[t for t in (refcounts, cow_pairs, info) if t is not None])
+    _need_int("int32", block_tables=block_tables, context_lens=context_lens, new_tokens=new_tokens,
+              free_stack=free_stack, free_count=free_count, new_lens=new_lens, new_free_count=new_free_count)
+    _need_int("int64", slot_mapping=slot_mapping)
+    if block_tables.dim() != 2 or slot_mapping.dim() != 1 or free_stack.dim() != 1:
+        raise ValueError("block_tables: [S, max_blocks]; slot_mapping: [n]; free_stack: [num_blocks]")
+    S, mb = block_tables.shape
+    if any(tuple(t.shape) != (S,) for t in (context_lens, new_tokens, new_lens)):
+        raise ValueError("context_lens, new_tokens and new_lens must be [S]")
+    if free_count.numel() != 1 or new_free_count.numel() != 1:
+        raise ValueError("free_count and new_free_count hold one value")
+    if (refcounts is None) != (cow_pairs is None):
+        raise ValueError("refcounts and cow_pairs come together")
+    if refcounts is not None:
+        _need_int("int32", refcounts=refcounts)
+        _need_int("int64", cow_pairs=cow_pairs)
+        if refcounts.shape != free_stack.shape or tuple(cow_pairs.shape) != (S, 2):
+            raise ValueError("refcounts: [num_blocks]; cow_pairs: [S, 2]")
+    if info is not None:
+        _need_int("int32", info=info)
+        if info.numel() != 4:
+            raise ValueError("info holds four values")
+    n = slot_mapping.shape[0]
+    need = int(lib().pkv_extend_workspace_size(S, n))
+    if workspace is None:
+        workspace = _scratch(block_tables.device, need)
+    ws_ptr, ws_bytes = _ptr_bytes(workspace if need else None)
+    _launch(block_tables.device, "extend_block_tables", lib().pkv_extend_block_tables, block_tables.data_ptr(),
+            context_lens.data_ptr(), new_tokens.data_ptr(), S, mb, free_stack.data_ptr(), free_count.data_ptr(),
+            free_stack.shape[0], None if refcounts is None else refcounts.data_ptr(), new_lens.data_ptr(),
+            new_free_count.data_ptr(), slot_mapping.data_ptr(), n, None if cow_pairs is None else cow_pairs.data_ptr(),
+            None if info is None else info.data_ptr(), ws_ptr, ws_bytes)
+
+
+def release_sequences(block_tables, context_lens, finished, free_stack, free_count, refcounts=None, workspace=None):
+    """Drops every sequence with finished[s] != 0 on the device: tables to -1, lengths to 0, and the blocks that
+    nothing holds any more onto the free stack in ascending order."""
+    _need_cuda(block_tables, context_lens, finished, free_stack, free_count,
+               *[t for t in (refcounts,) if t is not None])
+    _need_int("int32", block_tables=block_tables, context_lens=context_lens, finished=finished, free_stack=free_stack,
+              free_count=free_count, **({} if refcounts is None else {"refcounts": refcounts}))
+    if block_tables.dim() != 2 or free_stack.dim() != 1 or free_count.numel() != 1:
+        raise ValueError("block_tables: [S, max_blocks]; free_stack: [num_blocks]; free_count holds one value")
+    S, mb = block_tables.shape
+    if any(tuple(t.shape) != (S,) for t in (context_lens, finished)):
+        raise ValueError("context_lens and finished must be [S]")
+    if refcounts is not None and refcounts.shape != free_stack.shape:
+        raise ValueError("refcounts must be [num_blocks]")
+    nb = free_stack.shape[0]
+    if workspace is None:
+        workspace = _scratch(block_tables.device, int(lib().pkv_release_workspace_size(nb)))
+    ws_ptr, ws_bytes = _ptr_bytes(workspace)
+    _launch(block_tables.device, "release_sequences", lib().pkv_release_sequences, block_tables.data_ptr(),
+            context_lens.data_ptr(), finished.data_ptr(), S, mb, free_stack.data_ptr(), free_count.data_ptr(), nb,
+            None if refcounts is None else refcounts.data_ptr(), ws_ptr, ws_bytes)
 
 
 def check_copy_pairs(pairs, num_blocks):

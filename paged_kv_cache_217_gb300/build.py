@@ -29,6 +29,10 @@ SOURCES = [
     "decode_bf16.cu",
     "decode_int8.cu",
     "cache_ops.cu",
+    "cache_int4.cu",
+    "decode_int4.cu",
+    "latent.cu",
+    "tables.cu",
     "diag.cu",
     "block_manager.cpp",
     "status.cpp",

@@ -21,8 +21,10 @@ namespace {
 // Device status word: PKV_DEV_* flags raised by the kernels' index checks.
 __device__ unsigned int g_pkv_status = 0u;
 
+}  // namespace
+
 // Device address of g_pkv_status, looked up once per device with that device current.
-pkv_status_t status_word(unsigned int** out) {
+pkv_status_t pkv::status_word(unsigned int** out) {
   static std::mutex mu;
   static unsigned int* addr[pkv::kMaxDevices] = {};
   int dev = 0;
@@ -39,6 +41,10 @@ pkv_status_t status_word(unsigned int** out) {
   *out = addr[dev];
   return PKV_OK;
 }
+
+namespace {
+
+using pkv::status_word;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -831,6 +837,343 @@ pkv_status_t pkv_paged_attention_decode_int8_planned(void* out, const void* q, c
   return decode_int8_impl(out, q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, num_seqs,
                           num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, num_blocks, scale, dtype,
                           partition_size, workspace, workspace_bytes, true, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+pkv_status_t decode_int4_impl(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
+                              const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                              int head_dim, int max_blocks_per_seq, int num_blocks, float scale, pkv_dtype_t dtype,
+                              int window, int partition_size, void* workspace, size_t workspace_bytes, bool planned,
+                              cudaStream_t stream) {
+  if (num_seqs < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs < 0");
+  if (num_seqs == 0) return pkv::ok();
+  if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
+                     num_q_heads, num_kv_heads);
+  const int group = num_q_heads / num_kv_heads;
+  if (group > 8) return pkv::fail(PKV_ERR_UNSUPPORTED, "query heads per KV head %d > 8", group);
+  if (!supported_head_dim(head_dim)) return pkv::fail(PKV_ERR_UNSUPPORTED, "head_dim %d (64, 128 or 256)", head_dim);
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return pkv::fail(PKV_ERR_UNSUPPORTED, "dtype %d", int(dtype));
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq and num_blocks must be > 0");
+  if (num_seqs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
+  if (!std::isfinite(scale)) return pkv::fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (!out || !q || !kv_cache || !block_tables || !context_lens)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(kv_cache, 16))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "out, q and kv_cache must be 16-byte aligned");
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "block_tables and context_lens must be 4-byte aligned");
+  const int plan_blocks = window_blocks(max_blocks_per_seq, window);
+  const int p = choose_partition(num_seqs, num_q_heads, num_kv_heads, head_dim, plan_blocks, partition_size);
+  if (p == kBalanced || p == kSharedPrefix)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "the 4-bit cache has no balanced or shared-prefix schedule");
+  Plan plan;
+  pkv_status_t st = plan_decode(plan_blocks, p, &plan);
+  if (st != PKV_OK) return st;
+  const SplitLayout lay = split_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, plan.max_parts);
+  const size_t ord = plan_bytes(num_seqs, num_kv_heads, plan.max_parts);
+  const size_t need = lay.total + ord;
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
+                     need, workspace_bytes, workspace);
+  unsigned int* status = nullptr;
+  st = status_word(&status);
+  if (st != PKV_OK) return st;
+
+  pkv::DecodeArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_pool = kv_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.part_o = lay.total > 0 ? static_cast<float*>(workspace) : nullptr;
+  a.part_ml = lay.total > 0 ? reinterpret_cast<float2*>(static_cast<char*>(workspace) + lay.ml_offset) : nullptr;
+  a.counters = lay.total > 0 ? reinterpret_cast<unsigned int*>(static_cast<char*>(workspace) + lay.counter_offset)
+                             : nullptr;
+  int4* plan_hdr = ord > 0 ? reinterpret_cast<int4*>(static_cast<char*>(workspace) + lay.total) : nullptr;
+  const bool make_plan = plan_hdr && !planned && num_seqs >= kOrderKernelMinSeqs;
+  const bool use_plan = plan_hdr && (planned || make_plan);
+  a.order = use_plan ? reinterpret_cast<const int32_t*>(plan_hdr + 1) : nullptr;
+  a.plan = use_plan ? plan_hdr : nullptr;
+  a.status = status;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = group;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.part_tokens = plan.part_tokens;
+  a.max_parts = plan.max_parts;
+  a.long_first = long_first_grid(num_seqs, num_kv_heads, plan.max_parts) ? 1 : 0;
+  a.window = window > 0 ? window : 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  cudaError_t err = cudaSuccess;
+  if (lay.total > 0) {
+    err = cudaMemsetAsync(a.counters, 0, lay.counter_bytes, stream);
+    if (err != cudaSuccess) return cuda_status(err, "clear split-K counters");
+  }
+  if (make_plan) {
+    err = pkv::launch_seq_order(context_lens, num_seqs, max_blocks_per_seq * PKV_BLOCK_SIZE, a.window, true, plan_hdr,
+                                block_tables, max_blocks_per_seq, plan_rows_of(plan_hdr, num_seqs), stream);
+    if (err != cudaSuccess) return cuda_status(err, "launch plan");
+  }
+  err = pkv::launch_decode_int4(a, dtype == PKV_BF16, head_dim, round_pow2_group(group), stream);
+  return cuda_status(err, "paged_attention_decode_int4 launch");
+}
+
+pkv_status_t cache_int4(bool gather, const char* what, const void* k, const void* v, pkv_dtype_t dtype,
+                        const void* kv_cache, const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                        int head_dim, int num_blocks, cudaStream_t stream) {
+  if (num_tokens < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_tokens < 0");
+  if (num_tokens == 0) return pkv::ok();
+  if (num_kv_heads <= 0 || num_blocks <= 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_kv_heads and num_blocks must be > 0");
+  if (!supported_head_dim(head_dim)) return pkv::fail(PKV_ERR_UNSUPPORTED, "head_dim %d (64, 128 or 256)", head_dim);
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return pkv::fail(PKV_ERR_UNSUPPORTED, "dtype %d", int(dtype));
+  if (!k || !v || !kv_cache || !slot_mapping) return pkv::fail(PKV_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_cache, 16) || !aligned(slot_mapping, 8))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "k, v and kv_cache must be 16-byte aligned, slot_mapping 8-byte aligned");
+  if (int64_t(num_tokens) * num_kv_heads > int64_t(INT32_MAX) * 8)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "too many tokens for one launch");
+  unsigned int* status = nullptr;
+  pkv_status_t st = status_word(&status);
+  if (st != PKV_OK) return st;
+  return cuda_status(pkv::launch_cache_int4(gather, const_cast<void*>(k), const_cast<void*>(v), dtype == PKV_BF16,
+                                            const_cast<void*>(kv_cache), slot_mapping, num_tokens, num_kv_heads,
+                                            head_dim, num_blocks, status, stream),
+                     what);
+}
+
+pkv_status_t copy_pool(const char* what, void* pool, const int64_t* src_dst_pairs, int num_pairs, int64_t block_bytes,
+                       int num_blocks, cudaStream_t stream) {
+  if (num_pairs < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_pairs < 0");
+  if (num_pairs == 0) return pkv::ok();
+  if (num_pairs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_pairs %d > 65535", num_pairs);
+  if (num_blocks <= 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_blocks must be > 0");
+  if (!pool || !src_dst_pairs) return pkv::fail(PKV_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(pool, 16) || !aligned(src_dst_pairs, 8))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "the cache must be 16-byte aligned, pairs 8-byte aligned");
+  unsigned int* status = nullptr;
+  pkv_status_t st = status_word(&status);
+  if (st != PKV_OK) return st;
+  return cuda_status(pkv::launch_copy_blocks_pool(pool, src_dst_pairs, num_pairs, block_bytes, num_blocks, status, stream),
+                     what);
+}
+
+}  // namespace
+
+size_t pkv_int4_tile_bytes(int head_dim) { return supported_head_dim(head_dim) ? size_t(18) * head_dim : 0; }
+
+pkv_status_t pkv_reshape_and_cache_int4(const void* k, const void* v, pkv_dtype_t dtype, void* kv_cache,
+                                        const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
+                                        int num_blocks, pkv_stream_t stream) {
+  return cache_int4(false, "reshape_and_cache_int4 launch", k, v, dtype, kv_cache, slot_mapping, num_tokens,
+                    num_kv_heads, head_dim, num_blocks, stream);
+}
+
+pkv_status_t pkv_gather_cache_int4(void* k, void* v, pkv_dtype_t dtype, const void* kv_cache,
+                                   const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_dim,
+                                   int num_blocks, pkv_stream_t stream) {
+  return cache_int4(true, "gather_cache_int4 launch", k, v, dtype, kv_cache, slot_mapping, num_tokens, num_kv_heads,
+                    head_dim, num_blocks, stream);
+}
+
+pkv_status_t pkv_copy_blocks_int4(void* kv_cache, const int64_t* src_dst_pairs, int num_pairs, int num_kv_heads,
+                                  int head_dim, int num_blocks, pkv_stream_t stream) {
+  if (num_kv_heads <= 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_kv_heads must be > 0");
+  if (!supported_head_dim(head_dim)) return pkv::fail(PKV_ERR_UNSUPPORTED, "head_dim %d (64, 128 or 256)", head_dim);
+  return copy_pool("copy_blocks_int4 launch", kv_cache, src_dst_pairs, num_pairs, int64_t(18) * head_dim * num_kv_heads,
+                   num_blocks, stream);
+}
+
+pkv_status_t pkv_paged_attention_decode_int4(void* out, const void* q, const void* kv_cache,
+                                             const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
+                                             int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                                             int num_blocks, float scale, pkv_dtype_t dtype, int sliding_window,
+                                             int partition_size, void* workspace, size_t workspace_bytes,
+                                             pkv_stream_t stream) {
+  return decode_int4_impl(out, q, kv_cache, block_tables, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                          max_blocks_per_seq, num_blocks, scale, dtype, sliding_window, partition_size, workspace,
+                          workspace_bytes, false, stream);
+}
+
+pkv_status_t pkv_paged_attention_decode_int4_planned(void* out, const void* q, const void* kv_cache,
+                                                     const int32_t* block_tables, const int32_t* context_lens,
+                                                     int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                                     int max_blocks_per_seq, int num_blocks, float scale,
+                                                     pkv_dtype_t dtype, int partition_size, void* workspace,
+                                                     size_t workspace_bytes, pkv_stream_t stream) {
+  return decode_int4_impl(out, q, kv_cache, block_tables, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                          max_blocks_per_seq, num_blocks, scale, dtype, 0, partition_size, workspace, workspace_bytes,
+                          true, stream);
+}
+
+pkv_status_t pkv_latent_cache_write(const void* latent, const void* rope, int64_t latent_stride, int64_t rope_stride,
+                                    pkv_dtype_t dtype, void* cache, const int64_t* slot_mapping, int num_tokens,
+                                    int num_blocks, pkv_stream_t stream) {
+  if (num_tokens < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_tokens < 0");
+  if (num_tokens == 0) return pkv::ok();
+  if (num_blocks <= 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_blocks must be > 0");
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return pkv::fail(PKV_ERR_UNSUPPORTED, "dtype %d", int(dtype));
+  if (!latent || !rope || !cache || !slot_mapping) return pkv::fail(PKV_ERR_INVALID_ARG, "NULL pointer");
+  if (latent_stride < 0 || rope_stride < 0 || latent_stride % 8 || rope_stride % 8)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "row strides must be non-negative multiples of 8 elements");
+  if (!aligned(latent, 16) || !aligned(rope, 16) || !aligned(cache, 16) || !aligned(slot_mapping, 8))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "latent, rope and cache must be 16-byte aligned, slot_mapping 8-byte aligned");
+  unsigned int* status = nullptr;
+  pkv_status_t st = status_word(&status);
+  if (st != PKV_OK) return st;
+  return cuda_status(pkv::launch_latent_write(latent, rope, cache, slot_mapping, num_tokens, latent_stride, rope_stride,
+                                              num_blocks, status, stream),
+                     "latent_cache_write launch");
+}
+
+pkv_status_t pkv_copy_blocks_latent(void* cache, const int64_t* src_dst_pairs, int num_pairs, int num_blocks,
+                                    pkv_stream_t stream) {
+  return copy_pool("copy_blocks_latent launch", cache, src_dst_pairs, num_pairs,
+                   int64_t(2) * PKV_BLOCK_SIZE * pkv::kLatentRow, num_blocks, stream);
+}
+
+size_t pkv_latent_workspace_size(int num_seqs, int num_heads, int max_blocks_per_seq) {
+  if (num_seqs <= 0 || num_heads <= 0 || max_blocks_per_seq <= 0) return 0;
+  return pkv::latent_workspace_bytes(num_seqs, num_heads, max_blocks_per_seq);
+}
+
+pkv_status_t pkv_paged_latent_decode(void* out, const void* q, const void* cache, const int32_t* block_tables,
+                                     const int32_t* context_lens, int num_seqs, int num_heads, int max_blocks_per_seq,
+                                     int num_blocks, float scale, pkv_dtype_t dtype, void* workspace,
+                                     size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_seqs < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs < 0");
+  if (num_seqs == 0) return pkv::ok();
+  if (num_heads <= 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_heads must be > 0");
+  if (num_heads > 1024) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_heads %d > 1024", num_heads);
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return pkv::fail(PKV_ERR_UNSUPPORTED, "dtype %d", int(dtype));
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq and num_blocks must be > 0");
+  if (int64_t(max_blocks_per_seq) * PKV_BLOCK_SIZE > INT32_MAX / 2)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq too large");
+  if (num_seqs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
+  if (int64_t(num_blocks) * PKV_BLOCK_SIZE > INT32_MAX)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "num_blocks * 16 exceeds 2^31 rows");
+  if (!std::isfinite(scale)) return pkv::fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (!out || !q || !cache || !block_tables || !context_lens)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(cache, 16))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "out, q and cache must be 16-byte aligned");
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "block_tables and context_lens must be 4-byte aligned");
+  const size_t need = pkv::latent_workspace_bytes(num_seqs, num_heads, max_blocks_per_seq);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
+                     need, workspace_bytes, workspace);
+  pkv::LatentArgs a{};
+  pkv_status_t st = status_word(&a.status);
+  if (st != PKV_OK) return st;
+  a.out = out;
+  a.q = q;
+  a.cache = cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.workspace = workspace;
+  a.num_seqs = num_seqs;
+  a.num_heads = num_heads;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return cuda_status(pkv::launch_latent_decode(a, dtype == PKV_BF16, stream), "paged_latent_decode launch");
+}
+
+size_t pkv_extend_workspace_size(int num_seqs, int num_slots) {
+  return num_seqs < 0 || num_slots < 0 ? 0 : pkv::extend_workspace_bytes(num_seqs, num_slots);
+}
+
+pkv_status_t pkv_extend_block_tables(int32_t* block_tables, const int32_t* context_lens, const int32_t* new_tokens,
+                                     int num_seqs, int max_blocks_per_seq, const int32_t* free_stack,
+                                     const int32_t* free_count, int num_blocks, int32_t* refcounts, int32_t* new_lens,
+                                     int32_t* new_free_count, int64_t* slot_mapping, int num_slots, int64_t* cow_pairs,
+                                     int32_t* info, void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_seqs < 0 || num_slots < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs and num_slots must be >= 0");
+  if (num_seqs == 0 && num_slots == 0) return pkv::ok();
+  if (num_seqs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq and num_blocks must be > 0");
+  if (int64_t(max_blocks_per_seq) * PKV_BLOCK_SIZE > INT32_MAX / 2)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq too large");
+  // (arrays of no sequences may be NULL)
+  if (!free_stack || !free_count || !new_free_count || (num_slots > 0 && !slot_mapping) ||
+      (num_seqs > 0 && (!block_tables || !context_lens || !new_tokens || !new_lens)))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "NULL pointer");
+  if (num_seqs > 0 && (refcounts == nullptr) != (cow_pairs == nullptr))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "refcounts and cow_pairs come together");
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(new_tokens, 4) || !aligned(free_stack, 4) ||
+      !aligned(free_count, 4) || !aligned(refcounts, 4) || !aligned(new_lens, 4) || !aligned(new_free_count, 4) ||
+      !aligned(info, 4) || !aligned(slot_mapping, 8) || !aligned(cow_pairs, 8))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "int32 arrays must be 4-byte, int64 arrays 8-byte aligned");
+  const size_t need = pkv::extend_workspace_bytes(num_seqs, num_slots);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
+                     need, workspace_bytes, workspace);
+  pkv::ExtendArgs a{};
+  pkv_status_t st = status_word(&a.status);
+  if (st != PKV_OK) return st;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.new_tokens = new_tokens;
+  a.free_stack = free_stack;
+  a.free_count = free_count;
+  a.refcounts = refcounts;
+  a.new_lens = new_lens;
+  a.new_free_count = new_free_count;
+  a.slot_mapping = slot_mapping;
+  a.cow_pairs = cow_pairs;
+  a.info = info;
+  a.workspace = static_cast<int32_t*>(workspace);
+  a.num_seqs = num_seqs;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.num_slots = num_slots;
+  a.slots_aligned = aligned(slot_mapping, 16) ? 1 : 0;
+  return cuda_status(pkv::launch_extend_block_tables(a, stream), "extend_block_tables launch");
+}
+
+size_t pkv_release_workspace_size(int num_blocks) {
+  return num_blocks <= 0 ? 0 : (pkv::release_workspace_bytes(num_blocks) + 15) / 16 * 16;
+}
+
+pkv_status_t pkv_release_sequences(int32_t* block_tables, int32_t* context_lens, const int32_t* finished, int num_seqs,
+                                   int max_blocks_per_seq, int32_t* free_stack, int32_t* free_count, int num_blocks,
+                                   int32_t* refcounts, void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_seqs < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs < 0");
+  if (num_seqs == 0) return pkv::ok();
+  if (num_seqs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq and num_blocks must be > 0");
+  if (int64_t(max_blocks_per_seq) * PKV_BLOCK_SIZE > INT32_MAX / 2)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq too large");
+  if (!block_tables || !context_lens || !finished || !free_stack || !free_count)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(finished, 4) || !aligned(free_stack, 4) ||
+      !aligned(free_count, 4) || !aligned(refcounts, 4))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "arrays must be 4-byte aligned");
+  const size_t need = pkv_release_workspace_size(num_blocks);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+    return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
+                     need, workspace_bytes, workspace);
+  pkv::ReleaseArgs a{};
+  pkv_status_t st = status_word(&a.status);
+  if (st != PKV_OK) return st;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.finished = finished;
+  a.free_stack = free_stack;
+  a.free_count = free_count;
+  a.refcounts = refcounts;
+  a.bitmap = static_cast<unsigned int*>(workspace);
+  a.num_seqs = num_seqs;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  return cuda_status(pkv::launch_release_sequences(a, stream), "release_sequences launch");
 }
 
 pkv_status_t pkv_reshape_and_cache_int8(const void* k, const void* v, pkv_dtype_t dtype, int8_t* k_cache,

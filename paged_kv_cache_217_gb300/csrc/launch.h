@@ -80,4 +80,81 @@ bool decode_int8_uses_tensor_maps();
 cudaError_t launch_decode_int8(const DecodeArgs& a, bool bf16, int head_dim, int gpad, const CUtensorMap* kmap,
                                const CUtensorMap* vmap, cudaStream_t stream);
 
+// 4-bit KV cache (int4_layout.cuh): quantising write, or read back of the rows
+// at `slots` into k and v (gather); decode with DecodeArgs::k_pool the cache.
+cudaError_t launch_cache_int4(bool gather, void* k, void* v, bool bf16, void* cache, const int64_t* slots,
+                              int num_tokens, int num_kv_heads, int head_dim, int num_blocks, unsigned int* status,
+                              cudaStream_t stream);
+cudaError_t launch_decode_int4(const DecodeArgs& a, bool bf16, int head_dim, int gpad, cudaStream_t stream);
+// Block copy of one pool whose blocks are bytes_per_block bytes (a multiple of 16).
+cudaError_t launch_copy_blocks_pool(void* pool, const int64_t* pairs, int num_pairs, int64_t bytes_per_block,
+                                    int num_blocks, unsigned int* status, cudaStream_t stream);
+
+// Latent attention: rows of kLatentDim latent and kRopeDim rotary elements.
+constexpr int kLatentDim = 512;
+constexpr int kRopeDim = 64;
+constexpr int kLatentRow = kLatentDim + kRopeDim;
+
+struct LatentArgs {
+  void* out;
+  const void* q;
+  const void* cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  unsigned int* status;
+  void* workspace;
+  int num_seqs;
+  int num_heads;
+  int max_blocks_per_seq;
+  int num_blocks;
+  float scale_log2;  // scale * log2(e)
+};
+
+cudaError_t launch_latent_write(const void* latent, const void* rope, void* cache, const int64_t* slots,
+                                int num_tokens, int64_t latent_stride, int64_t rope_stride, int num_blocks,
+                                unsigned int* status, cudaStream_t stream);
+size_t latent_workspace_bytes(int num_seqs, int num_heads, int max_blocks_per_seq);
+cudaError_t launch_latent_decode(const LatentArgs& a, bool bf16, cudaStream_t stream);
+
+// Block tables on the device (tables.cu).
+struct ExtendArgs {
+  int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* new_tokens;
+  const int32_t* free_stack;
+  const int32_t* free_count;
+  int32_t* refcounts;       // or null: nothing is shared
+  int32_t* new_lens;        // may be context_lens
+  int32_t* new_free_count;  // may be free_count
+  int64_t* slot_mapping;
+  int64_t* cow_pairs;       // [S][2], with refcounts
+  int32_t* info;            // {flags, tokens, blocks, pairs}, or null
+  int32_t* workspace;       // extend_workspace_bytes
+  unsigned int* status;
+  int num_seqs;
+  int max_blocks;
+  int num_blocks;
+  int num_slots;
+  int slots_aligned;        // slot_mapping is 16-byte aligned
+};
+
+struct ReleaseArgs {
+  int32_t* block_tables;
+  int32_t* context_lens;
+  const int32_t* finished;
+  int32_t* free_stack;
+  int32_t* free_count;
+  int32_t* refcounts;  // or null
+  unsigned int* bitmap;
+  unsigned int* status;
+  int num_seqs;
+  int max_blocks;
+  int num_blocks;
+};
+
+size_t extend_workspace_bytes(int num_seqs, int num_slots);
+inline size_t release_workspace_bytes(int num_blocks) { return (size_t(num_blocks) + 31) / 32 * 4; }
+cudaError_t launch_extend_block_tables(const ExtendArgs& a, cudaStream_t stream);
+cudaError_t launch_release_sequences(const ReleaseArgs& a, cudaStream_t stream);
+
 }  // namespace pkv

@@ -1,0 +1,381 @@
+// Block tables and slot maps on the device: what the host block manager does
+// for a batch (append with copy-on-write, release), as kernels, so that a
+// captured decode loop needs no host round trip ([S] "KV キャッシュマネージャ":
+// tokens fill the last block, a new block is taken when it is full, blocks go
+// back on finish; [S] "並列サンプリングやビームサーチでの共有": a shared block
+// is copied when a write reaches it).
+//
+// pkv_extend_block_tables, with L = context_lens[s], n = new_tokens[s]:
+//   cow_s   = n > 0, L % 16 != 0 and the last block still shared when s's turn
+//             comes: of the batch's k-th earlier sequence with that last block
+//             (each took a copy), refcount - k > 1
+//   fresh_s = ceil((L + n) / 16) - ceil(L / 16)
+//   first_s = sum over earlier sequences of cow + fresh (an exclusive scan)
+//   the i-th block of s (its copy first, then its new blocks in order) is
+//   free_stack[count - 1 - first_s - i]
+// -- exactly the blocks that the host manager pops for the same appends in
+// batch order. Two phases: one CTA scans the batch (phase 1: offsets into the
+// workspace, and the all-or-nothing checks), then every table entry and slot
+// is filled independently (phase 2), each thread finding its sequence by a
+// binary search of the offsets. Bound by launch latency for a decode step and
+// by the slot map's 8 bytes a token for prompts. A batch of at most
+// kFusedSeqs sequences and kFusedSlots slots runs both phases in one CTA, with
+// the offsets in shared memory.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "device_common.cuh"
+#include "launch.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kFusedSeqs = 1024;
+constexpr int kFusedSlots = 4096;
+constexpr int kSlotsPerThread = 4;
+
+// Per-batch results of phase 1, in the workspace (or shared memory).
+struct Scan {
+  int32_t* len;    // [S] lengths before the call
+  int32_t* tok;    // [S + 1] first new token of each sequence
+  int32_t* blk;    // [S + 1] first taken block of each sequence
+  int32_t* cow;    // [S] the block to copy from, or -1
+  int32_t* pair;   // [S] index of the sequence's copy pair
+  int32_t* last;   // [S] shared last block of a sequence that appends into it, or -1
+  int32_t* head;   // {ok, free count, pairs, 0}
+};
+
+__host__ __device__ inline size_t scan_ints(int S) { return size_t(6) * S + 2 + 4; }
+
+__device__ __forceinline__ Scan scan_of(int32_t* p, int S) {
+  return Scan{p, p + S, p + 2 * S + 1, p + 3 * S + 2, p + 4 * S + 2, p + 5 * S + 2, p + 6 * S + 2};
+}
+
+// Exclusive scan over the CTA; every thread calls it. total: the CTA's sum.
+template <typename V>
+__device__ __forceinline__ V cta_exclusive(V v, V* warp_sum, V& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  V x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const V n = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += n;
+  }
+  __syncthreads();  // earlier readers of warp_sum are done
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    V w = lane < kThreads / 32 ? warp_sum[lane] : V(0);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const V n = __shfl_up_sync(kFull, w, o);
+      if (lane >= o) w += n;
+    }
+    warp_sum[lane] = w;
+  }
+  __syncthreads();
+  total = warp_sum[kThreads / 32 - 1];
+  return x - v + (warp ? warp_sum[warp - 1] : V(0));
+}
+
+// Phase 1, one CTA of kThreads threads.
+__device__ __forceinline__ void scan_batch(const ExtendArgs& a, const Scan& w) {
+  __shared__ long long wsum[32];
+  __shared__ unsigned int flags;
+  const int S = a.num_seqs;
+  const long long max_len = (long long)a.max_blocks * kBlock;
+  if (threadIdx.x == 0) flags = 0u;
+  __syncthreads();
+  unsigned int bad = 0u;
+  bool sharing = false;
+  for (int s = threadIdx.x; s < S; s += kThreads) {
+    const long long L = a.context_lens[s], n = a.new_tokens[s];
+    const bool ok = L >= 0 && n >= 0 && L + n <= max_len;
+    if (!ok) bad |= PKV_DEV_BAD_CONTEXT_LEN;
+    int last = -1;
+    if (ok && a.refcounts && n > 0 && L % kBlock) {
+      const int b = a.block_tables[size_t(s) * a.max_blocks + L / kBlock];
+      if (b >= 0 && b < a.num_blocks && a.refcounts[b] > 1) last = b;  // a bad id is flagged where it is used
+    }
+    sharing |= last >= 0;
+    w.len[s] = ok ? int(L) : 0;
+    w.last[s] = last;
+  }
+  const int count = *a.free_count;
+  if (count < 0 || count > a.num_blocks) bad |= PKV_DEV_BAD_BLOCK_ID;
+  if (bad) atomicOr(&flags, bad);
+  const bool any_sharing = __syncthreads_or(sharing);
+
+  long long tok0 = 0, blk0 = 0, pair0 = 0;
+  for (int base = 0; base < S; base += kThreads) {
+    const int s = base + threadIdx.x;
+    long long n = 0, fresh = 0;
+    int cow = 0;
+    if (s < S) {
+      const long long L = a.context_lens[s];
+      n = a.new_tokens[s];
+      if (L < 0 || n < 0 || L + n > max_len) n = 0;  // the call fails
+      else fresh = (L + n + kBlock - 1) / kBlock - (L + kBlock - 1) / kBlock;
+      const int b = any_sharing ? w.last[s] : -1;
+      if (b >= 0) {
+        int rank = 0;
+        for (int e = 0; e < s; ++e) rank += w.last[e] == b ? 1 : 0;
+        cow = a.refcounts[b] - rank > 1 ? 1 : 0;
+      }
+    }
+    long long total;
+    const long long t = tok0 + cta_exclusive<long long>(n, wsum, total);
+    tok0 += total;
+    const long long bl = blk0 + cta_exclusive<long long>(fresh + cow, wsum, total);
+    blk0 += total;
+    long long pr = pair0;
+    if (any_sharing) {
+      pr += cta_exclusive<long long>(cow, wsum, total);
+      pair0 += total;
+    }
+    if (s < S) {
+      w.tok[s] = int(t < INT_MAX ? t : INT_MAX);
+      w.blk[s] = int(bl < INT_MAX ? bl : INT_MAX);
+      w.cow[s] = cow ? w.last[s] : -1;
+      w.pair[s] = int(pr);
+    }
+  }
+  if (threadIdx.x == 0) {
+    unsigned int f = flags;
+    if (tok0 > a.num_slots) f |= PKV_DEV_BAD_SLOT;
+    if (blk0 > count && !(f & PKV_DEV_BAD_BLOCK_ID)) f |= PKV_DEV_OUT_OF_BLOCKS;
+    if (f) flag(a.status, f);
+    const bool ok = f == 0u;
+    w.tok[S] = ok ? int(tok0) : 0;
+    w.blk[S] = ok ? int(blk0) : 0;
+    w.head[0] = ok ? 1 : 0;
+    w.head[1] = count;
+    w.head[2] = ok ? int(pair0) : 0;
+    w.head[3] = int(f);
+  }
+}
+
+// The last s in [0, S) with off[s] <= i (off ascending, off[0] = 0).
+__device__ __forceinline__ int owner(const int32_t* off, int S, int i) {
+  int lo = 0, hi = S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// The i-th block taken by the batch, or -1 (flagged) if the stack holds none.
+__device__ __forceinline__ int taken(const ExtendArgs& a, int count, int i) {
+  const int b = a.free_stack[count - 1 - i];
+  if (b >= 0 && b < a.num_blocks) return b;
+  flag(a.status, PKV_DEV_BAD_BLOCK_ID);
+  return -1;
+}
+
+// Phase 2: thread `tid` of `threads`.
+__device__ __forceinline__ void fill(const ExtendArgs& a, const Scan& w, int64_t tid, int64_t threads) {
+  const int S = a.num_seqs;
+  const bool ok = w.head[0] != 0;
+  const int count = w.head[1], tokens = w.tok[S], blocks = w.blk[S];
+  for (int64_t i0 = tid * kSlotsPerThread; i0 < a.num_slots; i0 += threads * kSlotsPerThread) {
+    int64_t slot[kSlotsPerThread];
+    int s = i0 < tokens ? owner(w.tok, S, int(i0)) : 0;
+    int at = -1, phys = -1;  // block index and id of the previous token
+#pragma unroll
+    for (int u = 0; u < kSlotsPerThread; ++u) {
+      const int64_t i = i0 + u;
+      slot[u] = -1;
+      if (i >= tokens) continue;
+      while (i >= w.tok[s + 1]) {
+        ++s;
+        at = -1;
+      }
+      const int L = w.len[s], pos = L + int(i - w.tok[s]), j = pos / kBlock;
+      if (j != at) {
+        const int have = (L + kBlock - 1) / kBlock, copied = w.cow[s] >= 0 ? 1 : 0;
+        at = j;
+        if (j >= have) {
+          phys = taken(a, count, w.blk[s] + copied + j - have);
+        } else if (copied) {
+          phys = taken(a, count, w.blk[s]);
+        } else {
+          phys = a.block_tables[size_t(s) * a.max_blocks + j];
+          if (phys < 0 || phys >= a.num_blocks) {
+            flag(a.status, PKV_DEV_BAD_BLOCK_ID);
+            phys = -1;
+          }
+        }
+      }
+      if (phys >= 0) slot[u] = int64_t(phys) * kBlock + pos % kBlock;
+    }
+    if (i0 + kSlotsPerThread <= a.num_slots && a.slots_aligned) {
+      longlong2* dst = reinterpret_cast<longlong2*>(a.slot_mapping + i0);
+#pragma unroll
+      for (int u = 0; u < kSlotsPerThread; u += 2) dst[u / 2] = make_longlong2(slot[u], slot[u + 1]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kSlotsPerThread; ++u)
+        if (i0 + u < a.num_slots) a.slot_mapping[i0 + u] = slot[u];
+    }
+  }
+  for (int64_t i = tid; i < blocks; i += threads) {
+    const int s = owner(w.blk, S, int(i));
+    const int k = int(i) - w.blk[s], src = w.cow[s], have = (w.len[s] + kBlock - 1) / kBlock;
+    const int b = taken(a, count, int(i));
+    const int j = src >= 0 ? have - 1 + k : have + k;
+    a.block_tables[size_t(s) * a.max_blocks + j] = b;
+    if (a.refcounts && b >= 0) a.refcounts[b] = 1;
+    if (src >= 0 && k == 0) {
+      atomicSub(a.refcounts + src, 1);
+      a.cow_pairs[2 * size_t(w.pair[s])] = src;
+      a.cow_pairs[2 * size_t(w.pair[s]) + 1] = b;
+    }
+  }
+  for (int64_t s = tid; s < S; s += threads) {
+    // (a failed call leaves the lengths as they were, valid or not)
+    if (ok) a.new_lens[s] = w.len[s] + (w.tok[s + 1] - w.tok[s]);
+    else if (a.new_lens != a.context_lens) a.new_lens[s] = a.context_lens[s];
+    if (a.cow_pairs && s >= w.head[2]) a.cow_pairs[2 * s] = a.cow_pairs[2 * s + 1] = -1;
+  }
+  if (tid == 0) {
+    *a.new_free_count = count - blocks;
+    if (a.info) {
+      a.info[0] = w.head[3];
+      a.info[1] = tokens;
+      a.info[2] = blocks;
+      a.info[3] = w.head[2];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) scan_kernel(const ExtendArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  scan_batch(a, scan_of(a.workspace, a.num_seqs));
+}
+
+__global__ void __launch_bounds__(256) fill_kernel(const ExtendArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  fill(a, scan_of(a.workspace, a.num_seqs), int64_t(blockIdx.x) * blockDim.x + threadIdx.x,
+       int64_t(gridDim.x) * blockDim.x);
+}
+
+__global__ void __launch_bounds__(kThreads) fused_kernel(const ExtendArgs a) {
+  __shared__ int32_t ws[6 * kFusedSeqs + 6];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Scan w = scan_of(ws, a.num_seqs);
+  scan_batch(a, w);
+  __syncthreads();
+  fill(a, w, threadIdx.x, kThreads);
+}
+
+// ---- release ---------------------------------------------------------------
+// One warp per sequence: drops the holds of the finished ones and marks the
+// blocks that nothing holds any more in a bitmap of the pool.
+__global__ void __launch_bounds__(256) drop_kernel(const ReleaseArgs a) {
+  const int s = int((int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+  if (s >= a.num_seqs || !a.finished[s]) return;
+  long long L = a.context_lens[s];
+  if (L < 0 || L > (long long)a.max_blocks * kBlock) {
+    if (lane == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+    L = L < 0 ? 0 : (long long)a.max_blocks * kBlock;
+  }
+  const int nb = int((L + kBlock - 1) / kBlock);
+  int32_t* row = a.block_tables + size_t(s) * a.max_blocks;
+  for (int j = lane; j < nb; j += 32) {
+    const int b = row[j];
+    row[j] = -1;
+    if (b < 0) continue;  // released before (sliding window)
+    if (b >= a.num_blocks) {
+      flag(a.status, PKV_DEV_BAD_BLOCK_ID);
+      continue;
+    }
+    bool free_now = true;
+    if (a.refcounts) {
+      const int old = atomicSub(a.refcounts + b, 1);
+      if (old <= 0) {  // nothing held it
+        atomicAdd(a.refcounts + b, 1);
+        flag(a.status, PKV_DEV_BAD_BLOCK_ID);
+      }
+      free_now = old == 1;
+    }
+    if (free_now && (atomicOr(a.bitmap + b / 32, 1u << (b % 32)) >> (b % 32) & 1u))
+      flag(a.status, PKV_DEV_BAD_BLOCK_ID);  // two sequences own it without reference counts
+  }
+  __syncwarp();
+  if (lane == 0) a.context_lens[s] = 0;
+}
+
+// Pushes the marked blocks onto the free stack in ascending order (whatever
+// order the atomics above took). One CTA.
+__global__ void __launch_bounds__(kThreads) push_kernel(const ReleaseArgs a) {
+  __shared__ int wsum[32];
+  const int words = (a.num_blocks + 31) / 32;
+  int count = *a.free_count;
+  __syncthreads();
+  if (count < 0 || count > a.num_blocks) {
+    if (threadIdx.x == 0) flag(a.status, PKV_DEV_BAD_BLOCK_ID);
+    return;
+  }
+  for (int base = 0; base < words; base += kThreads) {
+    const int i = base + threadIdx.x;
+    unsigned int m = i < words ? a.bitmap[i] : 0u;
+    int total;
+    int at = count + cta_exclusive<int>(__popc(m), wsum, total);
+    for (; m; m &= m - 1u, ++at) {
+      if (at < a.num_blocks) a.free_stack[at] = 32 * i + __ffs(int(m)) - 1;
+      else flag(a.status, PKV_DEV_BAD_BLOCK_ID);  // more blocks than the pool has
+    }
+    count += total;
+  }
+  if (threadIdx.x == 0) *a.free_count = count < a.num_blocks ? count : a.num_blocks;
+}
+
+template <typename K, typename A>
+cudaError_t launch_after(K kern, unsigned ctas, unsigned threads, cudaStream_t stream, const A& a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
+size_t extend_workspace_bytes(int num_seqs, int num_slots) {
+  if (num_seqs <= kFusedSeqs && num_slots <= kFusedSlots) return 0;
+  return (scan_ints(num_seqs) * sizeof(int32_t) + 15) / 16 * 16;
+}
+
+cudaError_t launch_extend_block_tables(const ExtendArgs& a, cudaStream_t stream) {
+  if (a.num_seqs <= kFusedSeqs && a.num_slots <= kFusedSlots)
+    return launch_after(fused_kernel, 1u, unsigned(kThreads), stream, a);
+  cudaError_t err = launch_after(scan_kernel, 1u, unsigned(kThreads), stream, a);
+  if (err != cudaSuccess) return err;
+  // one thread per kSlotsPerThread slots, at most 8 CTAs per SM of a GB300
+  int64_t threads = (int64_t(a.num_slots) + kSlotsPerThread - 1) / kSlotsPerThread;
+  if (threads < a.num_seqs) threads = a.num_seqs;
+  int64_t ctas = (threads + 255) / 256;
+  if (ctas > 8 * 152) ctas = 8 * 152;
+  return launch_after(fill_kernel, unsigned(ctas < 1 ? 1 : ctas), 256u, stream, a);
+}
+
+cudaError_t launch_release_sequences(const ReleaseArgs& a, cudaStream_t stream) {
+  cudaError_t err = cudaMemsetAsync(a.bitmap, 0, release_workspace_bytes(a.num_blocks), stream);
+  if (err != cudaSuccess) return err;
+  drop_kernel<<<unsigned((int64_t(a.num_seqs) * 32 + 255) / 256), 256, 0, stream>>>(a);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  push_kernel<<<1, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace pkv
