@@ -7,32 +7,41 @@
 // so the codes enter the products as they are and the pairs touch only scores
 // and weights: no element is dequantised.
 //
-// Per 16-token tile, two chains of mma.sync m16n8k16 (fp16 in, fp32 out) with
-// the 8 columns of N taken by the KV head's query heads (zero past the group):
-//  * S^T = C_K Q~^T: tokens on M. A quad's lane t holds words 8 g + 2 t, + 1 of
-//    its two token rows (one shared load a row). A word's 8 nibbles become four
-//    fp16 pairs by masking alone: nibble j (bits 0-3 of a half) is the fp16
-//    subnormal c 2^-24, the one above it (bits 4-7) c 2^-20, both exact in the
-//    tensor cores' products, so 5 integer instructions convert 8 codes. Q~
-//    holds the query of the odd dims divided by 16 to match, and is scaled by
-//    a power of two per head that brings max |q| to [2^13, 2^14): bf16 and
-//    fp16 queries are exact (elements below 2^-24 of the largest lose bits).
+// Two 16-token tiles a step, as mma.sync with fp32 accumulators; the 8 columns
+// of N belong to the KV head's query heads:
+//  * S^T = C_K Q^T: tokens on M. A quad's lane t holds words 8 g + 2 t, + 1 of
+//    its two token rows (one shared load a row).
+//    1 or 2 heads: m16n8k32 on e4m3. A nibble alone in a byte is the e4m3
+//    value c 2^-9, exactly, for c = 0..15 (its first two exponents share one
+//    step), so two masks and a shift convert 8 codes. A query element, scaled
+//    by a power of two per head to a largest magnitude in [2^7, 2^8), is the
+//    sum of four e4m3 digits (each the rounding of what the earlier ones
+//    leave: 2^-10 at the end, at most 2^-17 of the largest element); the
+//    digits take four columns a head, which the scores then add up.
+//    The tensor cores add e4m3 products to fp32 without loss (checked).
+//    3 to 8 heads: m16n8k16 on fp16, a column a head. Masking makes fp16
+//    pairs of a word's nibbles: nibble j (bits 0-3 of a half) is the
+//    subnormal c 2^-24, the one above it (bits 4-7) c 2^-20, both exact; 5
+//    instructions convert 8 codes. The query of the odd dims is divided by 16
+//    to match, and scaled to [2^13, 2^14) (elements below 2^-24 of the
+//    largest lose bits).
 //    The fp32 sums of each group are then multiplied by s and joined by
 //    z * sum q.
-//  * O^T += C_V^T P~: head dims on M, tokens on K. V words of tokens t and
-//    t + 4 (t + 8 and t + 12) are merged by halves and masked the same way.
+//  * O^T += C_V^T P~: head dims on M, tokens on K, fp16. V words of tokens t
+//    and t + 4 (t + 8 and t + 12) are merged by halves and masked as above.
 //    P~ = p s 2^e rounded to fp16 once (2^-11 relative, far below the codes'
 //    own step), e a power of two per warp that keeps P~ below 2^15; the score
 //    fragment becomes the weight operand through movmatrix. The offsets' part
 //    sum p z is kept in fp32 per (head, group).
 //  * The running maximum is only a reference: it moves when a score exceeds it
-//    by more than 8 (weights up to 2^8; one vote a tile), so most tiles need no
+//    by more than 8 (weights up to 2^8; one vote a step), so most steps need no
 //    cross-lane maximum and no rescaling. Sums and the accumulator are fp32.
 // One bulk copy (18 D bytes, contiguous) brings a tile; each warp runs its own
-// ring of stages, as in the other decode kernels.
+// ring of stages of two tiles.
 #pragma once
 
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "decode.cuh"
 #include "decode_mma.cuh"
@@ -44,7 +53,8 @@ template <int D, int NW, int STAGES>
 struct I4Cfg {
   static constexpr int GROUPS = D / kInt4Group;
   static constexpr int TILE_BYTES = kv4_tile_bytes(D);
-  static constexpr size_t RING_BYTES = size_t(NW) * STAGES * TILE_BYTES;
+  static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr size_t RING_BYTES = size_t(NW) * STAGES * STAGE_BYTES;
   static constexpr size_t SMEM_BYTES = RING_BYTES + size_t(NW) * STAGES * 8;
 };
 
@@ -99,25 +109,65 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&p)[4]) {
   p[3] = w & 0x00f000f0u;
 }
 
-// The query operand of one lane: head gr, and the per-head factors of heads
-// 2t, 2t + 1 (the columns of this lane's scores).
-template <int D>
-struct I4Query {
-  uint32_t b[D / 16][2];        // k-step 2 (2 g + i) + j: word 8 g + 2 t + i, nibbles (2j, 2j + 4), (2j + 1, 2j + 5)
-  float sum[D / kInt4Group][2]; // sum of the scaled query over a group, times 2^-24
-  float mul[2];                 // scores to the log2 domain: scale log2(e) / the power of two (times 2^24, applied apart)
+// d = a b + c. Plain functions of their operands (not volatile), so that the
+// compiler may interleave the chains of a step.
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// Layout of the query heads over a quad's lanes. H: heads the kernel takes (2
+// or 8, the group padded up). PER_LANE score columns a lane keeps (1 after its
+// digits are added up), the head of lane t's column c.
+template <int H>
+struct I4Heads {
+  static_assert(H == 2 || H == 8, "2 heads of four digits, or 8 heads");
+  static constexpr bool FP8 = H == 2;
+  static constexpr int PER_LANE = H == 8 ? 2 : 1;
+  static __device__ __forceinline__ int head(int t, int c) { return H == 2 ? t >> 1 : 2 * t + c; }
 };
 
-template <typename T, int D>
-__device__ __forceinline__ void i4_query(const T* qrow, int lane, float scale_log2, I4Query<D>& q) {
+// The query operand of one lane (column gr of N), and the factors of the heads
+// whose scores it keeps.
+template <int D, int H>
+struct I4Query {
+  static constexpr int REGS = I4Heads<H>::FP8 ? D / 32 : D / 16;
+  uint32_t b[REGS][2];                            // e4m3: word 2 g + i; fp16: k-step 2 (2 g + i) + j
+  float sum[D / kInt4Group][I4Heads<H>::PER_LANE];  // sum of the scaled query over a group, in the scores' unit
+  float mul[I4Heads<H>::PER_LANE];                // scale log2(e) / the power of two; the unit is applied apart
+};
+
+// The unit of the integer sums: codes enter as c 2^-9 (e4m3) or c 2^-24 (fp16).
+template <int H>
+constexpr float i4_unit() { return I4Heads<H>::FP8 ? 0x1p-9f : 0x1p-24f; }
+template <int H>
+constexpr float i4_unit_inv() { return I4Heads<H>::FP8 ? 0x1p9f : 0x1p24f; }
+
+// q0: the group's first query row. Lane (gr, t) reads dims 64 g + 16 t .. + 15
+// of its column's head (words 8 g + 2 t, + 1).
+template <typename T, int D, int H>
+__device__ __forceinline__ void i4_query(const T* q0, int group, int lane, float scale_log2, I4Query<D, H>& q) {
+  using HL = I4Heads<H>;
   constexpr int GROUPS = D / kInt4Group;
-  const int t = lane & 3;
+  const int t = lane & 3, gr = lane >> 2;
+  const int head = gr * H / 8;
   float f[GROUPS][16], m = 0.f;
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g) {
     uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (qrow) {
-      const uint4* src = reinterpret_cast<const uint4*>(qrow + 64 * g + 16 * t);
+    if (head < group) {
+      const uint4* src = reinterpret_cast<const uint4*>(q0 + size_t(head) * D + 64 * g + 16 * t);
       u[0] = __ldg(src);
       u[1] = __ldg(src + 1);
     }
@@ -134,59 +184,91 @@ __device__ __forceinline__ void i4_query(const T* qrow, int lane, float scale_lo
   }
   m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
   m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-  // m < 2^E (E from m's exponent field, clamped for tiny or zero q): times 2^(14 - E)
+  // m < 2^E (E from m's exponent field, clamped for tiny or zero q): times 2^(TOP - E)
+  constexpr int TOP = HL::FP8 ? 8 : 14;
   const int E = max(int((__float_as_uint(m) >> 23) & 0xffu) - 126, -100);
-  const float up = __uint_as_float(uint32_t(127 + 14 - E) << 23);
-  const float mul = scale_log2 * __uint_as_float(uint32_t(127 - 14 + E) << 23);
-  q.mul[0] = __shfl_sync(kFull, mul, 8 * t);
-  q.mul[1] = __shfl_sync(kFull, mul, 8 * t + 4);
+  const float up = __uint_as_float(uint32_t(127 + TOP - E) << 23);
+  const float mul = scale_log2 * __uint_as_float(uint32_t(127 - TOP + E) << 23);
+#pragma unroll
+  for (int c = 0; c < HL::PER_LANE; ++c) q.mul[c] = __shfl_sync(kFull, mul, 4 * (HL::head(t, c) * 8 / H));
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float* x = &f[g][8 * i];
+      float x[8];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const __half2 even = __floats2half2_rn(x[2 * j] * up, x[2 * j + 4] * up);
-        const __half2 odd = __floats2half2_rn(x[2 * j + 1] * (up * 0.0625f), x[2 * j + 5] * (up * 0.0625f));
-        q.b[2 * (2 * g + i) + j][0] = *reinterpret_cast<const uint32_t*>(&even);
-        q.b[2 * (2 * g + i) + j][1] = *reinterpret_cast<const uint32_t*>(&odd);
+      for (int e = 0; e < 8; ++e) {
+        x[e] = f[g][8 * i + e] * up;
+        sum += x[e];
       }
+      if constexpr (HL::FP8) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += x[e] * up;
+        for (int dig = 0; dig < 4; ++dig) {
+          // digit `dig` of the 8 elements (even dims, then odd dims); taken off
+          // even where another column keeps it
+          uint32_t w[2];
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const __nv_fp8x2_storage_t lo =
+                __nv_cvt_float2_to_fp8x2(make_float2(x[o], x[o + 2]), __NV_SATFINITE, __NV_E4M3);
+            const __nv_fp8x2_storage_t hi =
+                __nv_cvt_float2_to_fp8x2(make_float2(x[o + 4], x[o + 6]), __NV_SATFINITE, __NV_E4M3);
+            w[o] = uint32_t(lo) | (uint32_t(hi) << 16);
+            const float2 l = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(lo, __NV_E4M3)));
+            const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
+            x[o] -= l.x, x[o + 2] -= l.y, x[o + 4] -= h.x, x[o + 6] -= h.y;
+          }
+          if (dig == gr % 4) {
+            q.b[2 * g + i][0] = w[0];
+            q.b[2 * g + i][1] = w[1];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const __half2 even = __floats2half2_rn(x[2 * j], x[2 * j + 4]);
+          const __half2 odd = __floats2half2_rn(x[2 * j + 1] * 0.0625f, x[2 * j + 5] * 0.0625f);
+          q.b[2 * (2 * g + i) + j][0] = *reinterpret_cast<const uint32_t*>(&even);
+          q.b[2 * (2 * g + i) + j][1] = *reinterpret_cast<const uint32_t*>(&odd);
+        }
+      }
     }
     sum += __shfl_xor_sync(kFull, sum, 1);
     sum += __shfl_xor_sync(kFull, sum, 2);
-    sum *= 0x1p-24f;
-    q.sum[g][0] = __shfl_sync(kFull, sum, 8 * t);
-    q.sum[g][1] = __shfl_sync(kFull, sum, 8 * t + 4);
+    sum *= i4_unit<H>();
+#pragma unroll
+    for (int c = 0; c < HL::PER_LANE; ++c) q.sum[g][c] = __shfl_sync(kFull, sum, 4 * (HL::head(t, c) * 8 / H));
   }
 }
 
-// Running state of a warp: columns are heads 2t, 2t + 1.
-template <int D>
+// Running state of a warp. The accumulator's columns 2t, 2t + 1 are this lane's
+// heads (H = 8), or both its one head.
+template <int D, int H>
 struct I4State {
-  float o[D / 16][4];                 // O^T fragments, in units of 2^-24 (2^-20 for odd ones) / vmul
-  float z[D / kInt4Group][2];         // this lane's part of sum p z
-  float m[2], l[2];                   // reference maximum (log2 domain), this lane's part of sum p
-  float vbound, vmul;                 // P~ = p s vmul, for s below vbound
+  static constexpr int PL = I4Heads<H>::PER_LANE;
+  float o[D / 16][4];            // O^T fragments, in units of 2^-24 (2^-20 for odd ones) / vmul
+  float z[D / kInt4Group][PL];   // this lane's part of sum p z
+  float m[PL], l[PL];            // reference maximum (log2 domain), this lane's part of sum p
+  float vbound, vmul;            // P~ = p s vmul, for s below vbound
 };
 
-template <typename T, int D, bool MASK>
-__device__ __forceinline__ void i4_tile(uint32_t tile, int lo, int rows, const I4Query<D>& q, I4State<D>& st,
-                                        int lane) {
-  constexpr int GROUPS = D / kInt4Group;
+// The scores (log2 domain) of tile rows gr (x[0]) and gr + 8 (x[1]).
+template <typename T, int D, int H>
+__device__ __forceinline__ void i4_scores(uint32_t tile, const I4Query<D, H>& q, float (&x)[2][I4Heads<H>::PER_LANE],
+                                          int lane) {
+  using HL = I4Heads<H>;
+  constexpr int GROUPS = D / kInt4Group, PL = HL::PER_LANE;
   const int t = lane & 3, gr = lane >> 2;
-
-  // S^T by groups: rows gr and gr + 8 of the tile.
-  uint32_t kp0[GROUPS], kp1[GROUPS], vp0[GROUPS], vp1[GROUPS];
-  lds_words<GROUPS>(tile + 16 * D + gr * (D / 16), kp0);
-  lds_words<GROUPS>(tile + 16 * D + (gr + 8) * (D / 16), kp1);
-  lds_words<GROUPS>(tile + 17 * D + gr * (D / 16), vp0);
-  lds_words<GROUPS>(tile + 17 * D + (gr + 8) * (D / 16), vp1);
+  uint32_t kp[2][GROUPS];
+  lds_words<GROUPS>(tile + 16 * D + gr * (D / 16), kp[0]);
+  lds_words<GROUPS>(tile + 16 * D + (gr + 8) * (D / 16), kp[1]);
   constexpr int PER = D == 64 ? 2 : 4;  // words a shared load brings
-  float x[4] = {0.f, 0.f, 0.f, 0.f};
+  float lane_x[2] = {0.f, 0.f};         // e4m3: sums over this lane's digits
+#pragma unroll
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int c = 0; c < PL; ++c) x[r][c] = 0.f;
 #pragma unroll
   for (int c = 0; c < D / 32 / PER; ++c) {
     uint32_t w0[PER], w1[PER];
@@ -196,48 +278,97 @@ __device__ __forceinline__ void i4_tile(uint32_t tile, int lo, int rows, const I
 #pragma unroll
     for (int h = 0; h < PER / 2; ++h) {
       const int g = c * (PER / 2) + h;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      float s[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        uint32_t a[4], b[4];
-        nibbles(w0[2 * h + i], a);
-        nibbles(w1[2 * h + i], b);
-        Mma<__half>::run(s, a[0], b[0], a[1], b[1], q.b[2 * (2 * g + i)][0], q.b[2 * (2 * g + i)][1]);
-        Mma<__half>::run(s, a[2], b[2], a[3], b[3], q.b[2 * (2 * g + i) + 1][0], q.b[2 * (2 * g + i) + 1][1]);
+        const uint32_t wa = w0[2 * h + i], wb = w1[2 * h + i];
+        if constexpr (HL::FP8) {
+          const uint32_t a0 = wa & 0x0f0f0f0fu, a2 = (wa >> 4) & 0x0f0f0f0fu;
+          const uint32_t a1 = wb & 0x0f0f0f0fu, a3 = (wb >> 4) & 0x0f0f0f0fu;
+          const uint32_t* b = q.b[2 * g + i];
+          if (i == 0) mma_e4m3(s, a0, a1, a2, a3, b[0], b[1], 0.f, 0.f, 0.f, 0.f);
+          else mma_e4m3(s, a0, a1, a2, a3, b[0], b[1], s[0], s[1], s[2], s[3]);
+        } else {
+          uint32_t a[4], b[4];
+          nibbles(wa, a);
+          nibbles(wb, b);
+          const uint32_t* b0 = q.b[2 * (2 * g + i)];
+          const uint32_t* b1 = q.b[2 * (2 * g + i) + 1];
+          if (i == 0) mma_f16(s, a[0], b[0], a[1], b[1], b0[0], b0[1], 0.f, 0.f, 0.f, 0.f);
+          else mma_f16(s, a[0], b[0], a[1], b[1], b0[0], b0[1], s[0], s[1], s[2], s[3]);
+          mma_f16(s, a[2], b[2], a[3], b[3], b1[0], b1[1], s[0], s[1], s[2], s[3]);
+        }
       }
-      const float2 k0 = pair_of<T>(kp0[g]), k1 = pair_of<T>(kp1[g]);
-      x[0] = fmaf(s[0], k0.x, fmaf(k0.y, q.sum[g][0], x[0]));
-      x[1] = fmaf(s[1], k0.x, fmaf(k0.y, q.sum[g][1], x[1]));
-      x[2] = fmaf(s[2], k1.x, fmaf(k1.y, q.sum[g][0], x[2]));
-      x[3] = fmaf(s[3], k1.x, fmaf(k1.y, q.sum[g][1], x[3]));
+      const float2 k0 = pair_of<T>(kp[0][g]), k1 = pair_of<T>(kp[1][g]);
+      if constexpr (HL::FP8) {
+        lane_x[0] = fmaf(s[0] + s[1], k0.x, lane_x[0]);
+        lane_x[1] = fmaf(s[2] + s[3], k1.x, lane_x[1]);
+        x[0][0] = fmaf(k0.y, q.sum[g][0], x[0][0]);
+        x[1][0] = fmaf(k1.y, q.sum[g][0], x[1][0]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < PL; ++e) {
+          x[0][e] = fmaf(s[e], k0.x, fmaf(k0.y, q.sum[g][e], x[0][e]));
+          x[1][e] = fmaf(s[2 + e], k1.x, fmaf(k1.y, q.sum[g][e], x[1][e]));
+        }
+      }
     }
   }
-  float2 v0[GROUPS], v1[GROUPS];
-  float smax = 0.f;
-  bool on0 = true, on1 = true;
-  if (MASK) {
-    const int tok = 4 * (gr & 1) + (gr >> 1);  // the token of tile row gr (gr + 8: 8 more)
-    on0 = tok >= lo && tok < rows;
-    on1 = tok + 8 >= lo && tok + 8 < rows;
+  if constexpr (HL::FP8) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      lane_x[r] += __shfl_xor_sync(kFull, lane_x[r], 1);  // digits 0, 1 and 2, 3
+      x[r][0] += lane_x[r];
+    }
   }
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    v0[g] = MASK && !on0 ? make_float2(0.f, 0.f) : pair_of<T>(vp0[g]);
-    v1[g] = MASK && !on1 ? make_float2(0.f, 0.f) : pair_of<T>(vp1[g]);
-    smax = fmaxf(smax, fmaxf(v0[g].x, v1[g].x));
-  }
-  x[0] = on0 ? x[0] * q.mul[0] * 0x1p24f : -INFINITY;
-  x[1] = on0 ? x[1] * q.mul[1] * 0x1p24f : -INFINITY;
-  x[2] = on1 ? x[2] * q.mul[0] * 0x1p24f : -INFINITY;
-  x[3] = on1 ? x[3] * q.mul[1] * 0x1p24f : -INFINITY;
+  for (int r = 0; r < 2; ++r)
+#pragma unroll
+    for (int e = 0; e < PL; ++e) x[r][e] = x[r][e] * q.mul[e] * i4_unit_inv<H>();
+}
 
-  const float m0 = fmaxf(x[0], x[2]), m1 = fmaxf(x[1], x[3]);
-  if (__any_sync(kFull, m0 > st.m[0] + kInt4Lazy || m1 > st.m[1] + kInt4Lazy || smax >= st.vbound)) {
-    float n0 = m0, n1 = m1;
+// Two tiles (32 tokens from a multiple of 16); with MASK only tokens [lo, rows)
+// of the 32 count, whatever the rest of the stage holds.
+template <typename T, int D, int H, bool MASK>
+__device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const I4Query<D, H>& q, I4State<D, H>& st,
+                                        int lane) {
+  constexpr int GROUPS = D / kInt4Group, PL = I4Heads<H>::PER_LANE, TILE = kv4_tile_bytes(D);
+  const int t = lane & 3, gr = lane >> 2;
+  float x[4][PL];  // rows gr, gr + 8 of the first tile, then of the second
+  float2 v[4][GROUPS];
+  float smax = 0.f;
+#pragma unroll
+  for (int n = 0; n < 2; ++n) {
+    const uint32_t tile = stage + n * TILE;
+    float y[2][PL];
+    i4_scores<T, D, H>(tile, q, y, lane);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      uint32_t vp[GROUPS];
+      lds_words<GROUPS>(tile + 17 * D + (gr + 8 * r) * (D / 16), vp);
+      const int tok = 16 * n + 8 * r + 4 * (gr & 1) + (gr >> 1);  // the token of tile row gr + 8 r
+      const bool on = !MASK || (tok >= lo && tok < rows);
+#pragma unroll
+      for (int e = 0; e < PL; ++e) x[2 * n + r][e] = on ? y[r][e] : -INFINITY;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        v[2 * n + r][g] = on ? pair_of<T>(vp[g]) : make_float2(0.f, 0.f);
+        smax = fmaxf(smax, v[2 * n + r][g].x);
+      }
+    }
+  }
+  float mx[PL];
+  bool move = smax >= st.vbound;
+#pragma unroll
+  for (int e = 0; e < PL; ++e) {
+    mx[e] = fmaxf(fmaxf(x[0][e], x[1][e]), fmaxf(x[2][e], x[3][e]));
+    move |= mx[e] > st.m[e] + kInt4Lazy;
+  }
+  if (__any_sync(kFull, move)) {
 #pragma unroll
     for (int off = 4; off < 32; off <<= 1) {
-      n0 = fmaxf(n0, __shfl_xor_sync(kFull, n0, off));
-      n1 = fmaxf(n1, __shfl_xor_sync(kFull, n1, off));
+#pragma unroll
+      for (int e = 0; e < PL; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], off));
       smax = fmaxf(smax, __shfl_xor_sync(kFull, smax, off));
     }
     float ratio = 1.f;
@@ -248,87 +379,99 @@ __device__ __forceinline__ void i4_tile(uint32_t tile, int lo, int rows, const I
       st.vmul = mul;
       st.vbound = __uint_as_float(uint32_t(127 + E) << 23);
     }
-    n0 = fmaxf(n0, st.m[0]);
-    n1 = fmaxf(n1, st.m[1]);
-    // a head without a score yet has nothing to rescale
-    const float a0 = st.m[0] == -INFINITY ? 0.f : fast_exp2(st.m[0] - n0);
-    const float a1 = st.m[1] == -INFINITY ? 0.f : fast_exp2(st.m[1] - n1);
-    st.m[0] = n0;
-    st.m[1] = n1;
-    st.l[0] *= a0;
-    st.l[1] *= a1;
+    float r[PL];
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      st.z[g][0] *= a0;
-      st.z[g][1] *= a1;
+    for (int e = 0; e < PL; ++e) {
+      mx[e] = fmaxf(mx[e], st.m[e]);
+      // a head without a score yet has nothing to rescale
+      const float al = st.m[e] == -INFINITY ? 0.f : fast_exp2(st.m[e] - mx[e]);
+      st.m[e] = mx[e];
+      st.l[e] *= al;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) st.z[g][e] *= al;
+      r[e] = al * ratio;
     }
-    const float r0 = a0 * ratio, r1 = a1 * ratio;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      st.o[i][0] *= r0;
-      st.o[i][1] *= r1;
-      st.o[i][2] *= r0;
-      st.o[i][3] *= r1;
+      st.o[i][0] *= r[0];
+      st.o[i][1] *= r[PL - 1];
+      st.o[i][2] *= r[0];
+      st.o[i][3] *= r[PL - 1];
     }
   }
-  // (a tile of nothing but -inf scores leaves the reference at -inf)
-  const float ref0 = st.m[0] == -INFINITY ? 0.f : st.m[0], ref1 = st.m[1] == -INFINITY ? 0.f : st.m[1];
-  float p[4] = {fast_exp2(x[0] - ref0), fast_exp2(x[1] - ref1), fast_exp2(x[2] - ref0), fast_exp2(x[3] - ref1)};
-  st.l[0] += p[0] + p[2];
-  st.l[1] += p[1] + p[3];
-  uint32_t pb[GROUPS][2];
+  float p[4][PL];
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    st.z[g][0] = fmaf(p[0], v0[g].y, fmaf(p[2], v1[g].y, st.z[g][0]));
-    st.z[g][1] = fmaf(p[1], v0[g].y, fmaf(p[3], v1[g].y, st.z[g][1]));
-    const float s0 = v0[g].x * st.vmul, s1 = v1[g].x * st.vmul;
-    const __half2 h0 = __floats2half2_rn(p[0] * s0, p[1] * s0), h1 = __floats2half2_rn(p[2] * s1, p[3] * s1);
-    pb[g][0] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h0));
-    pb[g][1] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h1));
+  for (int e = 0; e < PL; ++e) {
+    // (nothing but -inf scores so far leaves the reference at -inf)
+    const float ref = st.m[e] == -INFINITY ? 0.f : st.m[e];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) p[r][e] = fast_exp2(x[r][e] - ref);
+    st.l[e] += (p[0][e] + p[1][e]) + (p[2][e] + p[3][e]);
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) st.z[g][e] = fmaf(p[r][e], v[r][g].y, st.z[g][e]);
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int e = 0; e < PL; ++e) p[r][e] *= st.vmul;  // p 2^(7 - E): s < 2^E keeps P~ below 2^15
 
-  // O^T += C_V^T P~: K slot 2t + b + 8h is token 8h + 4b + t.
+  // O^T += C_V^T P~: K slot 2t + b + 8h of a tile is token 8h + 4b + t.
   const int turn = D == 64 ? 0 : D == 128 ? 4 * (t >> 1) : 2 * t;
-  const uint32_t vt = tile + 8 * D + t * (D / 2) + (D / 16) * (gr ^ turn);
-  uint32_t wa[GROUPS], wb[GROUPS], wc[GROUPS], wd[GROUPS];
-  lds_words<GROUPS>(vt, wa);
-  lds_words<GROUPS>(vt + 4 * (D / 2), wb);
-  lds_words<GROUPS>(vt + 8 * (D / 2), wc);
-  lds_words<GROUPS>(vt + 12 * (D / 2), wd);
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
+  for (int n = 0; n < 2; ++n) {
+    const uint32_t vt = stage + n * TILE + 8 * D + t * (D / 2) + (D / 16) * (gr ^ turn);
+    uint32_t wa[GROUPS], wb[GROUPS], wc[GROUPS], wd[GROUPS];
+    lds_words<GROUPS>(vt, wa);
+    lds_words<GROUPS>(vt + 4 * (D / 2), wb);
+    lds_words<GROUPS>(vt + 8 * (D / 2), wc);
+    lds_words<GROUPS>(vt + 12 * (D / 2), wd);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // nibbles 0..3, then 4..7
-      uint32_t ab[4], cd[4];
-      nibbles(__byte_perm(wa[g], wb[g], h ? 0x7632 : 0x5410), ab);
-      nibbles(__byte_perm(wc[g], wd[g], h ? 0x7632 : 0x5410), cd);
-      Mma<__half>::run(st.o[4 * g + 2 * h], ab[0], ab[2], cd[0], cd[2], pb[g][0], pb[g][1]);
-      Mma<__half>::run(st.o[4 * g + 2 * h + 1], ab[1], ab[3], cd[1], cd[3], pb[g][0], pb[g][1]);
+    for (int g = 0; g < GROUPS; ++g) {
+      uint32_t pb[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float s = v[2 * n + r][g].x;
+        const __half2 h = __floats2half2_rn(p[2 * n + r][0] * s, p[2 * n + r][PL - 1] * s);
+        pb[r] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h));
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // nibbles 0..3, then 4..7
+        uint32_t ab[4], cd[4];
+        nibbles(__byte_perm(wa[g], wb[g], h ? 0x7632 : 0x5410), ab);
+        nibbles(__byte_perm(wc[g], wd[g], h ? 0x7632 : 0x5410), cd);
+        float(&o0)[4] = st.o[4 * g + 2 * h];
+        float(&o1)[4] = st.o[4 * g + 2 * h + 1];
+        mma_f16(o0, ab[0], ab[2], cd[0], cd[2], pb[0], pb[1], o0[0], o0[1], o0[2], o0[3]);
+        mma_f16(o1, ab[1], ab[3], cd[1], cd[3], pb[0], pb[1], o1[0], o1[1], o1[2], o1[3]);
+      }
     }
   }
 }
 
-// Publishes a warp's (acc[G][D], m[G], l[G]) in head-dim order, powers of two
+// Publishes a warp's (acc[H][D], m[H], l[H]) in head-dim order, powers of two
 // taken out: row gr of fragment 4 g + 2 h + b is dim 64 g + 8 gr + 4 h + b, row
 // gr + 8 the dim after the next.
-template <int D, int G>
-__device__ __forceinline__ void i4_publish(float* wsm, I4State<D>& st, int lane) {
-  constexpr int GROUPS = D / kInt4Group;
+template <int D, int H>
+__device__ __forceinline__ void i4_publish(float* wsm, I4State<D, H>& st, int lane) {
+  using HL = I4Heads<H>;
+  constexpr int GROUPS = D / kInt4Group, PL = HL::PER_LANE;
   const int t = lane & 3, gr = lane >> 2;
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < PL; ++c) {
       st.l[c] += __shfl_xor_sync(kFull, st.l[c], off);
 #pragma unroll
       for (int g = 0; g < GROUPS; ++g) st.z[g][c] += __shfl_xor_sync(kFull, st.z[g][c], off);
     }
   }
   const float even = 0x1p24f / st.vmul, odd = 0x1p20f / st.vmul;
+  if (H == 2 && (t & 1)) return;  // its neighbour holds the same head
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const int head = 2 * t + c;
-    if (head >= G) continue;
+  for (int c = 0; c < PL; ++c) {
+    const int head = HL::head(t, c);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
       const int dim = 64 * (i / 4) + 8 * gr + 4 * ((i / 2) & 1) + (i & 1);
@@ -337,28 +480,29 @@ __device__ __forceinline__ void i4_publish(float* wsm, I4State<D>& st, int lane)
       wsm[head * D + dim + 2] = fmaf(st.o[i][2 + c], f, st.z[i / 4][c]);
     }
     if (gr == 0) {
-      wsm[G * D + head] = st.m[c];
-      wsm[G * D + G + head] = st.l[c];
+      wsm[H * D + head] = st.m[c];
+      wsm[H * D + H + head] = st.l[c];
     }
   }
 }
 
-template <typename T, int D, int G, int NW, int STAGES>
-__global__ void __launch_bounds__(NW * 32) paged_decode_int4_kernel(const DecodeArgs a) {
+template <typename T, int D, int H, int NW, int STAGES>
+// (128 registers: 16 warps per SM)
+__global__ void __launch_bounds__(NW * 32, D <= 128 ? 16 / NW : 0) paged_decode_int4_kernel(const DecodeArgs a) {
   using C = I4Cfg<D, NW, STAGES>;
-  static_assert(size_t(2 * G + G * D) * 4 <= size_t(STAGES) * C::TILE_BYTES, "merge area fits the ring");
-  extern __shared__ __align__(128) unsigned char smem[];
+  static_assert(size_t(2 * H + H * D) * 4 <= size_t(STAGES) * C::STAGE_BYTES, "merge area fits the ring");
+  extern __shared__ __align__(1024) unsigned char smem[];
   wait_for_predecessor();
   const int g = blockIdx.x, part = blockIdx.z;
   const int s = long_first_seq<NW>(a, blockIdx.y);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hq0 = g * a.group;
 
-  // Without a window the first 32 block ids of this warp's tiles do not depend
-  // on the length: read them together with it.
+  // Without a window the first 32 block ids of this warp's tile pairs do not
+  // depend on the length: read them together with it.
   int ids_early = 0;
   if (a.window == 0) {
-    const int j0 = (part * a.part_tokens) / kBlock + warp + lane * NW;
+    const int j0 = (part * a.part_tokens) / kBlock + 2 * (warp + (lane >> 1) * NW) + (lane & 1);
     if (j0 < a.max_blocks_per_seq) ids_early = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + j0);
   }
   int L = a.context_lens[s];
@@ -381,7 +525,7 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int4_kernel(const Decode
   const int nb = (ntok + kBlock - 1) / kBlock;
   const int head = part == 0 ? tr.first - tr.aligned : 0;
 
-  unsigned char* ring = smem + size_t(warp) * STAGES * C::TILE_BYTES;
+  unsigned char* ring = smem + size_t(warp) * STAGES * C::STAGE_BYTES;
   const uint32_t ring_s = smem_addr(ring);
   const uint32_t bar_s = smem_addr(smem + C::RING_BYTES) + warp * STAGES * 8;
   if (lane == 0) {
@@ -391,50 +535,55 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int4_kernel(const Decode
   }
   __syncwarp();
 
-  const int n_my = nb > warp ? (nb - warp + NW - 1) / NW : 0;
+  // Tile pairs of this warp: warp + k NW, k < n_my. Lanes 2 (k % 16), + 1 of
+  // `ids` hold the blocks of pair k (batches of 16, the next one prefetched).
+  const int npairs = (nb + 1) / 2;
+  const int n_my = npairs > warp ? (npairs - warp + NW - 1) / NW : 0;
   const int32_t* trow = a.block_tables + size_t(s) * a.max_blocks_per_seq + t0 / kBlock;
-  auto checked = [&](int id) {
+  auto load_ids = [&](int batch) -> int {
+    const int j = 2 * (warp + (batch * 16 + (lane >> 1)) * NW) + (lane & 1);
+    if (j >= nb) return 0;
+    const int id = batch == 0 && a.window == 0 ? ids_early : __ldg(trow + j);
     if (id >= 0 && id < a.num_blocks) return id;
     flag(a.status, PKV_DEV_BAD_BLOCK_ID);
     return 0;
   };
-  auto load_ids = [&](int batch) -> int {
-    const int k = batch * 32 + lane;
-    return k < n_my ? checked(__ldg(trow + warp + k * NW)) : 0;
-  };
-  int ids = lane < n_my ? checked(a.window == 0 ? ids_early : __ldg(trow + warp + lane * NW)) : 0;
-  int ids_next = n_my > 32 ? load_ids(1) : 0;
+  int ids = load_ids(0);
+  int ids_next = n_my > 16 ? load_ids(1) : 0;
   int id_batch = 0;
   const unsigned char* base = static_cast<const unsigned char*>(a.k_pool) + size_t(g) * C::TILE_BYTES;
   const size_t block_stride = size_t(a.num_kv_heads) * C::TILE_BYTES;
   auto issue = [&](int k) {  // warp-uniform; k increases by one per call
-    if ((k >> 5) != id_batch) {
+    if ((k >> 4) != id_batch) {
       ids = ids_next;
       ++id_batch;
-      ids_next = (id_batch + 1) * 32 < n_my ? load_ids(id_batch + 1) : 0;
+      ids_next = (id_batch + 1) * 16 < n_my ? load_ids(id_batch + 1) : 0;
     }
-    const int id = __shfl_sync(kFull, ids, k & 31);
+    const int id0 = __shfl_sync(kFull, ids, 2 * (k & 15)), id1 = __shfl_sync(kFull, ids, 2 * (k & 15) + 1);
     if (lane == 0) {
       const int st = k % STAGES;
-      mbar_arrive_expect_tx(bar_s + 8 * st, C::TILE_BYTES);
-      bulk_g2s(ring_s + st * C::TILE_BYTES, base + size_t(id) * block_stride, C::TILE_BYTES, bar_s + 8 * st);
+      const uint32_t bar = bar_s + 8 * st, dst = ring_s + st * C::STAGE_BYTES;
+      const bool both = 2 * (warp + k * NW) + 1 < nb;
+      mbar_arrive_expect_tx(bar, both ? C::STAGE_BYTES : C::TILE_BYTES);
+      bulk_g2s(dst, base + size_t(id0) * block_stride, C::TILE_BYTES, bar);
+      if (both) bulk_g2s(dst + C::TILE_BYTES, base + size_t(id1) * block_stride, C::TILE_BYTES, bar);
     }
   };
   const int pre = n_my < STAGES ? n_my : STAGES;
   for (int k = 0; k < pre; ++k) issue(k);
 
-  I4Query<D> q;
-  i4_query<T, D>((lane >> 2) < a.group
-                     ? static_cast<const T*>(a.q) + (size_t(s) * a.num_q_heads + hq0 + (lane >> 2)) * D
-                     : nullptr,
-                 lane, a.scale_log2, q);
-  I4State<D> st;
+  I4Query<D, H> q;
+  i4_query<T, D, H>(static_cast<const T*>(a.q) + (size_t(s) * a.num_q_heads + hq0) * D, a.group, lane, a.scale_log2, q);
+  I4State<D, H> st;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
 #pragma unroll
-  for (int i = 0; i < C::GROUPS; ++i) st.z[i][0] = st.z[i][1] = 0.f;
-  st.m[0] = st.m[1] = -INFINITY;
-  st.l[0] = st.l[1] = 0.f;
+  for (int e = 0; e < I4Heads<H>::PER_LANE; ++e) {
+    st.m[e] = -INFINITY;
+    st.l[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < C::GROUPS; ++i) st.z[i][e] = 0.f;
+  }
   st.vbound = 0x1p-98f;
   st.vmul = 0x1p105f;
 
@@ -448,20 +597,20 @@ __global__ void __launch_bounds__(NW * 32) paged_decode_int4_kernel(const Decode
       for (int kk = k; kk < last; ++kk) mbar_wait_bounded(bar_s + 8 * (kk % STAGES), (kk / STAGES) & 1);
       break;
     }
-    const int j = warp + k * NW;
-    const int rows = min(kBlock, ntok - j * kBlock);
+    const int j = 2 * (warp + k * NW);
+    const int rows = ntok - j * kBlock;
     const int lo = j == 0 ? head : 0;
-    const uint32_t tile = ring_s + stage * C::TILE_BYTES;
-    if (rows == kBlock && lo == 0)
-      i4_tile<T, D, false>(tile, 0, rows, q, st, lane);
+    const uint32_t at = ring_s + stage * C::STAGE_BYTES;
+    if (rows >= 2 * kBlock && lo == 0)
+      i4_step<T, D, H, false>(at, 0, 2 * kBlock, q, st, lane);
     else
-      i4_tile<T, D, true>(tile, lo, rows, q, st, lane);
+      i4_step<T, D, H, true>(at, lo, rows, q, st, lane);
     __syncwarp();
     if (k + STAGES < n_my) issue(k + STAGES);
   }
-  i4_publish<D, G>(reinterpret_cast<float*>(ring), st, lane);
+  i4_publish<D, H>(reinterpret_cast<float*>(ring), st, lane);
   __syncthreads();
-  finish_chunk<T, D, G, NW>(a, smem, size_t(STAGES) * C::TILE_BYTES, s, g, part, nparts);
+  finish_chunk<T, D, H, NW>(a, smem, size_t(STAGES) * C::STAGE_BYTES, s, g, part, nparts);
 }
 
 }  // namespace pkv
