@@ -270,6 +270,24 @@ pkv_status_t pool_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, i
   return PKV_OK;
 }
 
+// The queries [num_seqs][num_heads][width] of latent attention as a 3-D
+// tensor, read in boxes of one sequence x box_heads heads x 64 columns.
+pkv_status_t query_tensor_map(CUtensorMap* map, const void* q, int num_seqs, int num_heads, int width,
+                              pkv_dtype_t dtype, int box_heads) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {cuuint64_t(width), cuuint64_t(num_heads), cuuint64_t(num_seqs)};
+  const cuuint64_t strides[2] = {cuuint64_t(width) * 2, cuuint64_t(width) * 2 * cuuint64_t(num_heads)};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), 1};
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  const CUresult r = enc(map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         3, const_cast<void*>(q), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed (CUresult %d)", int(r));
+  return PKV_OK;
+}
+
 // An INT8 code pool seen as a 2-D uint8 tensor of num_blocks*num_kv_heads*16
 // rows by head_dim columns, read in boxes of 16 rows x min(head_dim, 128)
 // bytes with the 128-byte swizzle (the 64-byte one for 64-byte rows).
@@ -1081,7 +1099,14 @@ pkv_status_t pkv_paged_latent_decode(void* out, const void* q, const void* cache
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = num_blocks;
   a.scale_log2 = scale * 1.4426950408889634f;
-  return cuda_status(pkv::launch_latent_decode(a, dtype == PKV_BF16, stream), "paged_latent_decode launch");
+  alignas(64) CUtensorMap cache_map, q_map;
+  st = pool_tensor_map(&cache_map, cache, int64_t(num_blocks) * PKV_BLOCK_SIZE, pkv::kLatentRow, dtype, PKV_BLOCK_SIZE);
+  if (st != PKV_OK) return st;
+  st = query_tensor_map(&q_map, q, num_seqs, num_heads, pkv::kLatentRow, dtype,
+                        pkv::latent_query_box(num_seqs, num_heads, max_blocks_per_seq));
+  if (st != PKV_OK) return st;
+  return cuda_status(pkv::launch_latent_decode(a, dtype == PKV_BF16, cache_map, q_map, stream),
+                     "paged_latent_decode launch");
 }
 
 size_t pkv_extend_workspace_size(int num_seqs, int num_slots) {

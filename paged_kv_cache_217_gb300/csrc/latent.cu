@@ -1,12 +1,11 @@
 // Latent attention over a paged cache of one shared row per token: the cache
-// write and the decode (absorbed form). The decode here is a plain kernel that
-// is right for every case (one CTA per (sequence, 8 heads), CUDA-core
-// products).
+// write, and the launch of the decode (latent_decode.cuh).
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
-#include "device_common.cuh"
+#include "decode_launch.cuh"
+#include "latent_decode.cuh"
 #include "launch.h"
 
 namespace pkv {
@@ -34,94 +33,50 @@ latent_write_kernel(const uint4* __restrict__ latent, const uint4* __restrict__ 
   cache[slot * VECS + c] = x;
 }
 
-constexpr int kHeads = 8;
-constexpr int kThreads = 256;
+// Heads per CTA: all of them in blocks of at most 64, evenly.
+struct LatentShape {
+  int blocks, heads, n, ranges;
+};
+LatentShape latent_shape(int num_seqs, int num_heads, int max_blocks_per_seq) {
+  LatentShape p;
+  p.blocks = (num_heads + 63) / 64;
+  p.heads = (num_heads + p.blocks - 1) / p.blocks;
+  p.n = p.heads <= 16 ? 16 : p.heads <= 32 ? 32 : 64;
+  const int64_t tiles =
+      int64_t(num_seqs) * ((int64_t(max_blocks_per_seq) * kBlock + kLatentTile - 1) / kLatentTile);
+  p.ranges = kLatentSms / p.blocks > 0 ? kLatentSms / p.blocks : 1;
+  if (tiles < p.ranges) p.ranges = int(tiles);
+  return p;
+}
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) latent_decode_kernel(const LatentArgs a) {
-  extern __shared__ float sm[];
-  float(*rows)[kLatentRow + 1] = reinterpret_cast<float(*)[kLatentRow + 1]>(sm);
-  float(*qs)[kLatentRow] = reinterpret_cast<float(*)[kLatentRow]>(sm + kBlock * (kLatentRow + 1));
-  __shared__ float x[kHeads][kBlock], part[2][kHeads][kBlock], mrun[kHeads], lrun[kHeads], alpha[kHeads];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int s = blockIdx.y, h0 = blockIdx.x * kHeads, tid = threadIdx.x;
-  const int heads = min(kHeads, a.num_heads - h0);
-  int L = a.context_lens[s];
-  const int max_len = a.max_blocks_per_seq * kBlock;
-  if (L < 0 || L > max_len) {
-    if (tid == 0 && h0 == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-    L = L < 0 ? 0 : max_len;
-  }
-  const T* q = static_cast<const T*>(a.q) + (size_t(s) * a.num_heads + h0) * kLatentRow;
-  for (int i = tid; i < heads * kLatentRow; i += kThreads)
-    qs[i / kLatentRow][i % kLatentRow] = float(q[i]) * a.scale_log2;
-  if (tid < kHeads) mrun[tid] = -INFINITY, lrun[tid] = 0.f;
-  float acc[kHeads][2] = {};
-  for (int t0 = 0; t0 < L; t0 += kBlock) {
-    int id = a.block_tables[size_t(s) * a.max_blocks_per_seq + t0 / kBlock];
-    if (id < 0 || id >= a.num_blocks) {
-      if (tid == 0) flag(a.status, PKV_DEV_BAD_BLOCK_ID);
-      id = 0;
-    }
-    __syncthreads();
-    const T* src = static_cast<const T*>(a.cache) + size_t(id) * kBlock * kLatentRow;
-    for (int i = tid; i < kBlock * kLatentRow; i += kThreads) {
-      const int r = i / kLatentRow;
-      rows[r][i % kLatentRow] = t0 + r < L ? float(src[i]) : 0.f;
-    }
-    __syncthreads();
-    {
-      const int half = tid / 128, h = tid % 128 / kBlock, r = tid % kBlock;
-      float dot = 0.f;
-      if (h < heads)
-        for (int d = half * (kLatentRow / 2); d < (half + 1) * (kLatentRow / 2); ++d) dot = fmaf(qs[h][d], rows[r][d], dot);
-      part[half][h][r] = dot;
-    }
-    __syncthreads();
-    if (tid < heads) {
-      float m = mrun[tid];
-      for (int r = 0; r < kBlock; ++r) {
-        x[tid][r] = t0 + r < L ? part[0][tid][r] + part[1][tid][r] : -INFINITY;
-        m = fmaxf(m, x[tid][r]);
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-      alpha[tid] = fast_exp2(mrun[tid] - ref);
-      float l = lrun[tid] * alpha[tid];
-      for (int r = 0; r < kBlock; ++r) {
-        x[tid][r] = fast_exp2(x[tid][r] - ref);
-        l += x[tid][r];
-      }
-      mrun[tid] = m;
-      lrun[tid] = l;
-    }
-    __syncthreads();
-    for (int h = 0; h < heads; ++h) {
-      float o0 = acc[h][0] * alpha[h], o1 = acc[h][1] * alpha[h];
-      for (int r = 0; r < kBlock; ++r) {
-        o0 = fmaf(x[h][r], rows[r][tid], o0);
-        o1 = fmaf(x[h][r], rows[r][tid + kThreads], o1);
-      }
-      acc[h][0] = o0;
-      acc[h][1] = o1;
-    }
-  }
-  __syncthreads();
-  T* out = static_cast<T*>(a.out) + (size_t(s) * a.num_heads + h0) * kLatentDim;
-  for (int h = 0; h < heads; ++h) {
-    const float inv = L == 0 ? 0.f : 1.f / lrun[h];
-    out[h * kLatentDim + tid] = T(acc[h][0] * inv);
-    out[h * kLatentDim + tid + kThreads] = T(acc[h][1] * inv);
-  }
+template <typename T, int N>
+cudaError_t launch_n(LatentArgs a, const LatentShape& p, const CUtensorMap& cache_map, const CUtensorMap& q_map,
+                     cudaStream_t stream) {
+  using C = LatentCfg<N>;
+  static bool configured[kMaxDevices] = {};
+  cudaError_t err = configure_once(latent_decode_kernel<T, N>, C::SMEM_BYTES, configured);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(latent_decode_kernel<T, N>, dim3(unsigned(p.blocks * p.ranges)), dim3(kLatentThreads), C::SMEM_BYTES,
+                   stream, a, cache_map, q_map);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(latent_merge_kernel<T>, dim3(unsigned(p.ranges), unsigned((a.num_heads + 1) / 2)), dim3(256), 0,
+                    stream, a);
 }
 
 template <typename T>
-cudaError_t launch_t(const LatentArgs& a, cudaStream_t stream) {
-  const size_t smem = (size_t(kBlock) * (kLatentRow + 1) + kHeads * kLatentRow) * sizeof(float);
-  cudaError_t err = cudaFuncSetAttribute(latent_decode_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (err != cudaSuccess) return err;
-  latent_decode_kernel<T><<<dim3(unsigned((a.num_heads + kHeads - 1) / kHeads), unsigned(a.num_seqs)), kThreads, smem,
-                            stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_t(LatentArgs a, const CUtensorMap& cache_map, const CUtensorMap& q_map, cudaStream_t stream) {
+  const LatentShape p = latent_shape(a.num_seqs, a.num_heads, a.max_blocks_per_seq);
+  a.ranges = p.ranges;
+  a.head_blocks = p.blocks;
+  a.block_heads = p.heads;
+  a.desc = static_cast<int2*>(a.workspace);
+  a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + latent_desc_bytes(p.ranges));
+  a.part_o = reinterpret_cast<float*>(a.part_ml + size_t(2) * p.ranges * ((a.num_heads + 1) / 2 * 2));
+  switch (p.n) {
+    case 16: return launch_n<T, 16>(a, p, cache_map, q_map, stream);
+    case 32: return launch_n<T, 32>(a, p, cache_map, q_map, stream);
+    default: return launch_n<T, 64>(a, p, cache_map, q_map, stream);
+  }
 }
 
 }  // namespace
@@ -136,10 +91,21 @@ cudaError_t launch_latent_write(const void* latent, const void* rope, void* cach
   return cudaGetLastError();
 }
 
-size_t latent_workspace_bytes(int, int, int) { return 0; }
+// Range descriptors, then per range two partial results of every head: (max,
+// sum) pairs and fp32 accumulators.
+size_t latent_workspace_bytes(int num_seqs, int num_heads, int max_blocks_per_seq) {
+  const LatentShape p = latent_shape(num_seqs, num_heads, max_blocks_per_seq);
+  return latent_desc_bytes(p.ranges) + size_t(2) * p.ranges * ((num_heads + 1) / 2 * 2) * sizeof(float2) +
+         size_t(2) * p.ranges * num_heads * kLatentDim * sizeof(float);
+}
 
-cudaError_t launch_latent_decode(const LatentArgs& a, bool bf16, cudaStream_t stream) {
-  return bf16 ? launch_t<__nv_bfloat16>(a, stream) : launch_t<__half>(a, stream);
+int latent_query_box(int num_seqs, int num_heads, int max_blocks_per_seq) {
+  return latent_shape(num_seqs, num_heads, max_blocks_per_seq).n;
+}
+
+cudaError_t launch_latent_decode(const LatentArgs& a, bool bf16, const CUtensorMap& cache_map,
+                                 const CUtensorMap& q_map, cudaStream_t stream) {
+  return bf16 ? launch_t<__nv_bfloat16>(a, cache_map, q_map, stream) : launch_t<__half>(a, cache_map, q_map, stream);
 }
 
 }  // namespace pkv

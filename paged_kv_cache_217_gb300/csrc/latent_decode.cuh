@@ -1,0 +1,668 @@
+// Latent attention decode (absorbed form) on the 5th-generation tensor cores.
+//
+// Every head h of a sequence attends over the same rows [c_p, r_p] (512 latent
+// and 64 rotary elements):
+//     x_hp = scale q_h . [c_p, r_p],   out_h = sum_p softmax(x_h)_p c_p,
+// so a row is read once for all heads and used twice, as key and as value:
+// 2 (576 + 512) operations per head and 1152 bytes per token.
+//
+// One CTA (1 per SM) takes up to N = 16, 32 or 64 heads and a range of 64-token
+// tiles; both products run transposed, heads on the MMA's N:
+//  * S^T[64 tokens, N] = K Q^T: A the tile's rows as they lie in shared memory
+//    (9 chunks of 64 tokens x 64 elements, 128-byte swizzle, K-major), B the
+//    queries (loaded once per sequence);
+//  * O^T[512, N] += V^T P^T: A the same chunks read along the other axis
+//    (MN-major), 4 products of 128 dims, B the weights P (16 bits, [N, 64]).
+// With heads on M instead, O would need all 512 columns of tensor memory and
+// leave none for S; transposed it takes 4 N columns, and S^T 2 N (two buffers).
+// Rows arrive by TMA (16 x 64 boxes through the block table; blocks past the
+// end read the zero fill) into a ring of 128-dim pairs, 16 KB each, and a small
+// ring for the rotary chunk; a pair is released as soon as its product is done.
+//
+// Warps: 0-3 softmax and output, 4 copies, 5 MMA issue. S^T of tile i + 1 is
+// issued before O^T of tile i, so that the tensor cores work while the softmax
+// of tile i runs. The running maximum is a reference that moves only when a
+// score exceeds it by 2^8 (one vote a tile); moving it rescales O^T in tensor
+// memory. Weights are rounded to the cache's type (bf16: 2^-8 relative, one per
+// weight, which averages out over the tokens; their sum is taken before the
+// rounding in fp32).
+//
+// Work: the batch's tiles are one list cut into equal ranges, one per CTA (per
+// block of heads), whatever the lengths. A sequence inside one range is written
+// directly; the pieces of one that crosses ranges go to the workspace as fp32
+// (max, sum, O) and latent_merge_kernel joins them by log-sum-exp.
+#pragma once
+
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "decode_mma.cuh"
+#include "device_common.cuh"
+#include "launch.h"
+
+namespace pkv {
+
+constexpr int kLatentSms = 152;       // CTAs a wave holds (one per SM of a GB300)
+constexpr int kLatentTile = 64;       // tokens per tile
+constexpr int kLatentThreads = 192;
+constexpr float kLatentLazy = 8.f;
+constexpr int kLatentChunk = kLatentTile * 128;  // bytes of 64 tokens x 64 elements
+constexpr int kLatentPairs = kLatentDim / 128;   // 128-dim pairs per tile
+
+inline size_t latent_desc_bytes(int ranges) { return (size_t(ranges) * sizeof(int2) + 15) / 16 * 16; }
+
+template <int N>
+struct LatentCfg {
+  static constexpr int Q_BYTES = N * kLatentRow * 2;
+  static constexpr int P_BYTES = N * kLatentTile * 2;
+  static constexpr int ROPE_SLOTS = 2;
+  static constexpr int MISC = 2048;  // barriers, statistics
+  static constexpr int PAIR_SLOTS =
+      (227 * 1024 - 1024 - MISC - Q_BYTES - P_BYTES - ROPE_SLOTS * kLatentChunk) / (2 * kLatentChunk);
+  static constexpr size_t SMEM_BYTES =
+      1024 + MISC + Q_BYTES + P_BYTES + ROPE_SLOTS * kLatentChunk + size_t(PAIR_SLOTS) * 2 * kLatentChunk;
+  static constexpr int TMEM_COLS = 8 * N;  // 4 N for O^T, 2 N for S^T, a power of two
+  static_assert(PAIR_SLOTS >= 2 * kLatentPairs, "two tiles in flight");
+};
+
+// ---- tcgen05 ----------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// Shared-memory matrix descriptor, 128-byte swizzle: start address, leading and
+// stride byte offsets in 16-byte units, version 1, layout 2.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((addr >> 4) & 0x3fffu) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+// Instruction descriptor of kind::f16: fp32 accumulator, A and B of T, A
+// MN-major when a_mn.
+template <typename T>
+__device__ constexpr uint32_t tc_idesc(int m, int n, bool a_mn) {
+  const uint32_t type = sizeof(T) == 2 && !std::is_same<T, __half>::value ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | (uint32_t(a_mn) << 15) | (uint32_t(n >> 3) << 17) |
+         (uint32_t(m >> 4) << 24);
+}
+
+// 16 lanes x 16 columns: thread l holds rows l / 4 and l / 4 + 8, columns
+// 2 (l % 4), + 1 of each 8 (the layout of an mma.sync accumulator).
+__device__ __forceinline__ void tc_ld_16x16(uint32_t addr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+               : "r"(addr));
+}
+// 32 lanes (one a thread) x 16 columns.
+__device__ __forceinline__ void tc_ld_32x16(uint32_t addr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st_32x16(uint32_t addr, const float* r) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+// Barrier of the four softmax warps.
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool softmax_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(v ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ---- work -------------------------------------------------------------------
+__device__ __forceinline__ int latent_len(const LatentArgs& a, int s) {
+  const int L = __ldg(a.context_lens + s), most = a.max_blocks_per_seq * kBlock;
+  return L < 0 ? 0 : L > most ? most : L;
+}
+__device__ __forceinline__ int latent_tiles(int L) { return (L + kLatentTile - 1) / kLatentTile; }
+
+// Shared state of a CTA outside the operand buffers.
+template <int N>
+struct LatentShared {
+  uint64_t pair_full[LatentCfg<N>::PAIR_SLOTS], pair_empty[LatentCfg<N>::PAIR_SLOTS];
+  uint64_t rope_full[2], rope_empty[2];
+  uint64_t q_full, q_empty, s_full[2], p_full, pv_done;
+  uint32_t tmem;
+  int stop;  // a wait gave up: every role leaves
+  int first_seq;
+  long long first_tile, begin, end, total;  // first_tile: list index of first_seq's first tile
+  uint64_t drain;                            // after a wait gave up
+  float stat[4][N], alpha[N], mref[N];       // per warp and head; rescale factors; references
+};
+
+// Waits for a phase; false when the limit ran out or another role gave up.
+__device__ __forceinline__ bool latent_wait(uint32_t bar, uint32_t parity, volatile int* stop, unsigned int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*stop) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *stop = 1;
+      flag(status, PKV_DEV_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// Walks a CTA's range [begin, end) of the tile list as segments of one sequence.
+struct LatentWalk {
+  int s;                    // sequence
+  long long at, end;        // list index of the next segment's first tile, and the range's end
+  long long base;           // list index of sequence s's first tile
+  int L, first, last, n;    // the segment: length, its tiles [first, last), all tiles of the sequence
+  __device__ __forceinline__ bool next(const LatentArgs& a) {
+    if (at >= end) return false;
+    for (;; ++s) {
+      L = latent_len(a, s);
+      n = latent_tiles(L);
+      if (base + n > at) break;
+      base += n;
+    }
+    first = int(at - base);
+    last = base + n < end ? n : int(end - base);
+    at = base + last;
+    return true;
+  }
+};
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kLatentThreads, 1)
+latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cache_map,
+                     const __grid_constant__ CUtensorMap q_map) {
+  using C = LatentCfg<N>;
+  static_assert(sizeof(LatentShared<N>) <= C::MISC, "shared state");
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
+  unsigned char* q_mem = base;                       // 9 chunks of [N][64]
+  unsigned char* p_mem = q_mem + C::Q_BYTES;         // [N][64 tokens]
+  unsigned char* rope_mem = p_mem + C::P_BYTES;      // ROPE_SLOTS chunks
+  unsigned char* pair_mem = rope_mem + C::ROPE_SLOTS * kLatentChunk;
+  LatentShared<N>& sh = *reinterpret_cast<LatentShared<N>*>(pair_mem + size_t(C::PAIR_SLOTS) * 2 * kLatentChunk);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hb = int(blockIdx.x) % a.head_blocks, range = int(blockIdx.x) / a.head_blocks;
+  const int h0 = hb * a.block_heads, heads = min(a.block_heads, a.num_heads - h0);
+
+  if (tid == 0) {
+    for (int i = 0; i < C::PAIR_SLOTS; ++i) {
+      mbar_init(smem_addr(&sh.pair_full[i]), 1);
+      mbar_init(smem_addr(&sh.pair_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.rope_full[i]), 1);
+      mbar_init(smem_addr(&sh.rope_empty[i]), 1);
+      mbar_init(smem_addr(&sh.s_full[i]), 1);
+    }
+    mbar_init(smem_addr(&sh.q_full), 1);
+    mbar_init(smem_addr(&sh.q_empty), 1);
+    mbar_init(smem_addr(&sh.p_full), 128);
+    mbar_init(smem_addr(&sh.pv_done), 1);
+    mbar_init_fence();
+    sh.stop = 0;
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
+                 "r"(uint32_t(C::TMEM_COLS))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // The tile list: each thread sums a run of sequences, a scan of the sums
+  // gives every run's place in the list, and the thread whose run holds this
+  // range's first tile finds its sequence.
+  const int per = (a.num_seqs + kLatentThreads - 1) / kLatentThreads;
+  const int run0 = min(a.num_seqs, tid * per), run1 = min(a.num_seqs, run0 + per);
+  long long mine = 0;
+  for (int s = run0; s < run1; ++s) {
+    const int raw = __ldg(a.context_lens + s);
+    if ((raw < 0 || raw > a.max_blocks_per_seq * kBlock) && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+    mine += latent_tiles(latent_len(a, s));
+  }
+  long long* scan = reinterpret_cast<long long*>(pair_mem);  // (before any copy)
+  scan[tid] = mine;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int i = 0; i < kLatentThreads; ++i) {
+    if (i < tid) before += scan[i];
+    total += scan[i];
+  }
+  const long long used = total < a.ranges ? total : a.ranges;  // ranges that get tiles
+  const long long begin = range < used ? range * total / used : 0, end = range < used ? (range + 1) * total / used : 0;
+  if (begin < end && begin >= before && begin < before + mine) {
+    long long at = before;
+    int s = run0;
+    for (;; ++s) {
+      const int n = latent_tiles(latent_len(a, s));
+      if (at + n > begin) break;
+      at += n;
+    }
+    sh.first_seq = s;
+    sh.first_tile = at;
+  }
+  // Sequences without tokens: zeros, spread over the CTAs.
+  for (int s = int(blockIdx.x); s < a.num_seqs; s += int(gridDim.x)) {
+    if (latent_len(a, s) > 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + size_t(s) * a.num_heads * kLatentDim);
+    for (int i = tid; i < a.num_heads * kLatentDim / 8; i += kLatentThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scan's words are overwritten by copies
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  LatentWalk walk;
+  walk.s = sh.first_seq;
+  walk.at = begin;
+  walk.end = end;
+  walk.base = sh.first_tile;
+  volatile int* stop = &sh.stop;
+
+  if (warp == 4) {
+    // ---- copies ----
+    int pair = 0, tile = 0, seg = 0;
+    bool ok = true;  // warp-uniform
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+      return bool(__all_sync(kFull, latent_wait(bar, parity, stop, a.status)));
+    };
+    while (ok && walk.next(a)) {
+      if (seg > 0) ok = wait_all(smem_addr(&sh.q_empty), (seg - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.q_full), C::Q_BYTES);
+      __syncwarp();
+      if (lane < 9)
+        tma_load_3d(smem_addr(q_mem) + lane * (N * 128), &q_map, 64 * lane, h0, walk.s, smem_addr(&sh.q_full));
+      const int nb = (walk.L + kBlock - 1) / kBlock;
+      const int32_t* row = a.block_tables + size_t(walk.s) * a.max_blocks_per_seq;
+      int ids = 0, ids_from = -1;  // lane l: the block of index ids_from + l
+      for (int t = walk.first; ok && t < walk.last; ++t, ++tile) {
+        if (ids_from < 0 || 4 * t + 4 > ids_from + 32) {
+          ids_from = 4 * t;
+          const int j = ids_from + lane;
+          ids = a.num_blocks;  // past the end: rows outside the tensor read as zeros
+          if (j < nb) {
+            ids = __ldg(row + j);
+            if (ids < 0 || ids >= a.num_blocks) {
+              flag(a.status, PKV_DEV_BAD_BLOCK_ID);
+              ids = 0;
+            }
+          }
+        }
+        const int id = __shfl_sync(kFull, ids, 4 * t - ids_from + (lane & 3));  // lane & 3: block of the tile
+        const int y = id * kBlock, off = (lane & 3) * kBlock * 128;
+        const int rs = tile & 1;
+        if (tile >= 2) ok = wait_all(smem_addr(&sh.rope_empty[rs]), ((tile >> 1) - 1) & 1);
+        if (!ok) break;
+        const uint32_t rb = smem_addr(&sh.rope_full[rs]);
+        if (lane == 0) mbar_arrive_expect_tx(rb, kLatentChunk);
+        __syncwarp();
+        if (lane < 4) tma_load_2d(smem_addr(rope_mem) + rs * kLatentChunk + off, &cache_map, kLatentDim, y, rb);
+        for (int j = 0; j < kLatentPairs; ++j, ++pair) {
+          const int slot = pair % C::PAIR_SLOTS, use = pair / C::PAIR_SLOTS;
+          if (use > 0) ok = wait_all(smem_addr(&sh.pair_empty[slot]), (use - 1) & 1);
+          if (!ok) break;
+          const uint32_t pb = smem_addr(&sh.pair_full[slot]);
+          if (lane == 0) mbar_arrive_expect_tx(pb, 2 * kLatentChunk);
+          __syncwarp();
+          if (lane < 8)
+            tma_load_2d(smem_addr(pair_mem) + slot * 2 * kLatentChunk + (lane >> 2) * kLatentChunk + off, &cache_map,
+                        128 * j + 64 * (lane >> 2), y, pb);
+        }
+      }
+      ++seg;
+    }
+    if (*stop) {  // wait (bounded) for the copies in flight: the last use of every slot
+      for (int i = 0; i < C::PAIR_SLOTS; ++i) {
+        const int uses = pair > i ? (pair - 1 - i) / C::PAIR_SLOTS + 1 : 0;
+        if (uses > 0) mbar_wait_bounded(smem_addr(&sh.pair_full[i]), (uses - 1) & 1, 10000000ull);
+      }
+      for (int i = 0; i < 2; ++i) {
+        const int uses = tile > i ? (tile - 1 - i) / 2 + 1 : 0;
+        if (uses > 0) mbar_wait_bounded(smem_addr(&sh.rope_full[i]), (uses - 1) & 1, 10000000ull);
+      }
+      if (seg > 0) mbar_wait_bounded(smem_addr(&sh.q_full), (seg - 1) & 1, 10000000ull);
+    }
+  } else if (warp == 5) {
+    // ---- MMA issue: one lane ----
+    if (lane == 0) {
+      constexpr uint32_t id_s = tc_idesc<T>(kLatentTile, N, false), id_o = tc_idesc<T>(128, N, true);
+      const uint64_t q_desc = tc_desc(smem_addr(q_mem), 16, 1024), p_desc = tc_desc(smem_addr(p_mem), 16, 1024);
+      const uint64_t rope_desc = tc_desc(smem_addr(rope_mem), 16, 1024);
+      const uint64_t key_desc = tc_desc(smem_addr(pair_mem), 16, 1024);
+      const uint64_t val_desc = tc_desc(smem_addr(pair_mem), kLatentChunk, 1024);
+      bool ok = true;
+      int tile = 0, seg = 0;  // of S^T
+      // S^T of the next tile: the rotary chunk, then the pairs as they arrive
+      auto scores = [&](bool last) {
+        const int rs = tile & 1;
+        const uint32_t d = tmem + 4 * N + (tile & 1) * N;
+        ok = ok && latent_wait(smem_addr(&sh.rope_full[rs]), (tile >> 1) & 1, stop, a.status);
+        if (!ok) return;
+        tc_fence_after();
+        for (int k = 0; k < 4; ++k)
+          tc_mma(d, rope_desc + rs * (kLatentChunk >> 4) + 2 * k, q_desc + 8 * (N * 128 >> 4) + 2 * k, id_s, k > 0);
+        tc_commit(smem_addr(&sh.rope_empty[rs]));
+        for (int j = 0; j < kLatentPairs; ++j) {
+          const int pr = tile * kLatentPairs + j, slot = pr % C::PAIR_SLOTS;
+          ok = ok && latent_wait(smem_addr(&sh.pair_full[slot]), (pr / C::PAIR_SLOTS) & 1, stop, a.status);
+          if (!ok) return;
+          tc_fence_after();
+          for (int c = 0; c < 2; ++c)
+            for (int k = 0; k < 4; ++k)
+              tc_mma(d, key_desc + (slot * 2 + c) * (kLatentChunk >> 4) + 2 * k,
+                     q_desc + (2 * j + c) * (N * 128 >> 4) + 2 * k, id_s, true);
+        }
+        tc_commit(smem_addr(&sh.s_full[tile & 1]));
+        if (last) tc_commit(smem_addr(&sh.q_empty));
+        ++tile;
+      };
+      // O^T of tile i
+      auto outputs = [&](int i, bool first) {
+        ok = ok && latent_wait(smem_addr(&sh.p_full), i & 1, stop, a.status);
+        if (!ok) return;
+        tc_fence_after();
+        for (int j = 0; j < kLatentPairs; ++j) {
+          const int slot = (i * kLatentPairs + j) % C::PAIR_SLOTS;
+          for (int k = 0; k < 4; ++k)
+            tc_mma(tmem + j * N, val_desc + slot * 2 * (kLatentChunk >> 4) + k * (16 * 128 >> 4), p_desc + 2 * k, id_o,
+                   !(first && k == 0));
+          tc_commit(smem_addr(&sh.pair_empty[slot]));
+        }
+        tc_commit(smem_addr(&sh.pv_done));
+      };
+      int done = 0;             // tiles whose O^T is issued
+      bool pending_first = true;  // whether tile `done` starts a segment
+      while (ok && walk.next(a)) {
+        ok = latent_wait(smem_addr(&sh.q_full), seg & 1, stop, a.status);
+        if (!ok) break;
+        ++seg;
+        for (int t = walk.first; ok && t < walk.last; ++t) {
+          const bool first = t == walk.first;
+          scores(t == walk.last - 1);
+          if (ok && tile > 1) outputs(done++, pending_first);
+          pending_first = first;
+        }
+      }
+      if (ok && tile > 0) outputs(done, pending_first);
+      if (*stop) {  // let the products in flight end before the tensor memory is freed
+        const uint32_t bar = smem_addr(&sh.drain);
+        mbar_init(bar, 1);
+        mbar_init_fence();
+        tc_commit(bar);
+        mbar_wait_bounded(bar, 0, 10000000ull);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax and output ----
+    constexpr int G8 = N / 8;  // groups of 8 heads: this thread keeps heads 8 i + 2 t, + 1
+    const int t = lane & 3, gr = lane >> 2;
+    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    int tile = 0, seg = 0;
+    bool ok = true;
+    while (ok && walk.next(a)) {
+      float m[G8][2], l[G8][2];
+#pragma unroll
+      for (int i = 0; i < G8; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+      for (int u = walk.first; u < walk.last; ++u, ++tile) {
+        ok = latent_wait(smem_addr(&sh.s_full[tile & 1]), (tile >> 1) & 1, stop, a.status);
+        if (softmax_any(!ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float x[G8][4];  // rows gr (0, 1) and gr + 8 (2, 3) of this warp's 16 tokens
+#pragma unroll
+        for (int i = 0; i < G8; i += 2) tc_ld_16x16(tmem + lanes + 4 * N + (tile & 1) * N + 8 * i, &x[i][0]);
+        tc_wait_ld();
+        const int left = walk.L - u * kLatentTile;  // tokens of this tile
+        const bool on0 = 16 * warp + gr < left, on1 = 16 * warp + gr + 8 < left;
+        bool move = false;
+#pragma unroll
+        for (int i = 0; i < G8; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[i][e] = on0 ? x[i][e] * a.scale_log2 : -INFINITY;
+            x[i][2 + e] = on1 ? x[i][2 + e] * a.scale_log2 : -INFINITY;
+            move |= fmaxf(x[i][e], x[i][2 + e]) > m[i][e] + kLatentLazy;
+          }
+        const bool moving = softmax_any(move);
+        if (moving) {
+#pragma unroll
+          for (int i = 0; i < G8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = fmaxf(x[i][e], x[i][2 + e]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+              if (gr == 0) sh.stat[warp][8 * i + 2 * t + e] = v;
+            }
+          softmax_sync();
+#pragma unroll
+          for (int i = 0; i < G8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int h = 8 * i + 2 * t + e;
+              const float v = fmaxf(fmaxf(fmaxf(sh.stat[0][h], sh.stat[1][h]), fmaxf(sh.stat[2][h], sh.stat[3][h])),
+                                    m[i][e]);
+              // a head without a score yet has nothing to rescale
+              const float al = m[i][e] == -INFINITY ? 0.f : fast_exp2(m[i][e] - v);
+              m[i][e] = v;
+              l[i][e] *= al;
+              if (warp == 0 && gr == 0) sh.alpha[h] = al;
+            }
+          softmax_sync();
+        }
+        float p[G8][4];
+#pragma unroll
+        for (int i = 0; i < G8; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ref = m[i][e] == -INFINITY ? 0.f : m[i][e];
+            p[i][e] = fast_exp2(x[i][e] - ref);
+            p[i][2 + e] = fast_exp2(x[i][2 + e] - ref);
+            l[i][e] += p[i][e] + p[i][2 + e];
+          }
+        // P and O^T are free once the previous tile's product is done
+        if (tile > 0) ok = latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
+        if (softmax_any(!ok)) {
+          ok = false;
+          break;
+        }
+        if (moving && u > walk.first) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4 * N; c += 16) {
+            float o[16];
+            tc_ld_32x16(tmem + lanes + c, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= sh.alpha[(c + i) % N];
+            tc_st_32x16(tmem + lanes + c, o);
+          }
+          tc_wait_st();
+        }
+        if (left < kLatentTile) {
+          // rows past the end hold whatever the block holds (NaN included): as
+          // values they must be zeros
+          const int dead = min(kLatentTile, (left + kBlock - 1) / kBlock * kBlock) - left;
+          for (int i = tid; i < dead * 2 * kLatentPairs * 8; i += 128) {
+            const int v = i % 8, c = i / 8 % (2 * kLatentPairs), r = left + i / (16 * kLatentPairs);
+            const int slot = (tile * kLatentPairs + c / 2) % C::PAIR_SLOTS;
+            reinterpret_cast<uint4*>(pair_mem + size_t(slot * 2 + c % 2) * kLatentChunk + r * 128)[v] =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < G8; i += 2) {
+          // matrix lane / 8: tokens 8 (b & 1), heads 8 (i + b / 2); row lane % 8 a head
+          const int b = lane >> 3, head = 8 * (i + (b >> 1)) + (lane & 7), chunk = 2 * warp + (b & 1);
+          stsm_x4_trans(smem_addr(p_mem) + head * 128 + ((chunk ^ (head & 7)) << 4), pack2<T>(p[i][0], p[i][1]),
+                        pack2<T>(p[i][2], p[i][3]), pack2<T>(p[i + 1][0], p[i + 1][1]),
+                        pack2<T>(p[i + 1][2], p[i + 1][3]));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(smem_addr(&sh.p_full));
+      }
+      if (!ok) break;
+      ++seg;
+      // The segment's sums, then its output: thread = dim, columns = heads.
+#pragma unroll
+      for (int i = 0; i < G8; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(kFull, l[i][e], o);
+          if (gr == 0) {
+            sh.stat[warp][8 * i + 2 * t + e] = l[i][e];
+            if (warp == 0) sh.mref[8 * i + 2 * t + e] = m[i][e];
+          }
+        }
+      const bool whole = walk.first == 0 && walk.last == walk.n;
+      const int slot = 2 * range + (walk.first == 0 ? 1 : 0);
+      softmax_sync();
+      if (tid < N) {
+        const float sum = (sh.stat[0][tid] + sh.stat[1][tid]) + (sh.stat[2][tid] + sh.stat[3][tid]);
+        sh.alpha[tid] = whole ? 1.f / sum : 1.f;
+        if (!whole && tid < heads) a.part_ml[size_t(slot) * ((a.num_heads + 1) / 2 * 2) + h0 + tid] = make_float2(sh.mref[tid], sum);
+      }
+      if (tid == 0 && hb == 0 && !whole && walk.first == 0) {
+        // the ranges that hold the rest of this sequence: up to the one with its last tile
+        const long long last = walk.base + walk.n - 1;
+        long long r = last * used / total;
+        while ((r + 1) * total / used <= last) ++r;
+        while (r * total / used > last) --r;
+        a.desc[range] = make_int2(walk.s, int(r));
+      }
+      ok = latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
+      if (softmax_any(!ok)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 4 * N; c += 16) {
+        float o[16];
+        tc_ld_32x16(tmem + lanes + c, o);
+        tc_wait_ld();
+        const int dim = (c / N) * 128 + warp * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int h = c % N + i;
+          if (h >= heads) continue;
+          if (whole)
+            static_cast<T*>(a.out)[(size_t(walk.s) * a.num_heads + h0 + h) * kLatentDim + dim] = T(o[i] * sh.alpha[h]);
+          else
+            a.part_o[(size_t(slot) * a.num_heads + h0 + h) * kLatentDim + dim] = o[i];
+        }
+      }
+      tc_fence_before();  // the next segment's O^T comes after these reads
+      softmax_sync();     // statistics are read: the next segment may write them
+    }
+  }
+  // A range without a sequence that goes on past it says so.
+  if (tid == 0 && hb == 0) {
+    LatentWalk w;
+    w.s = sh.first_seq;
+    w.at = begin;
+    w.end = end;
+    w.base = sh.first_tile;
+    bool open = false;
+    while (w.next(a)) open = w.first == 0 && w.last < w.n;
+    if (!open) a.desc[range] = make_int2(-1, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(uint32_t(C::TMEM_COLS)));
+  }
+}
+
+// Joins the pieces of the sequence that starts in a range and goes on past it:
+// out = sum_i w_i o_i / sum_i w_i l_i with w_i = 2^(m_i - max m). Two heads per
+// CTA, 4 dims per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int r0 = blockIdx.x, h = 2 * int(blockIdx.y) + int(threadIdx.x >> 7), d = int(threadIdx.x & 127) * 4;
+  const int2 desc = __ldcg(a.desc + r0);
+  if (desc.x < 0 || h >= a.num_heads) return;
+  const int stride = (a.num_heads + 1) / 2 * 2;
+  auto slot = [&](int r) { return size_t(2) * r + (r == r0 ? 1 : 0); };
+  float M = -INFINITY;
+  for (int r = r0; r <= desc.y; ++r) M = fmaxf(M, __ldcg(&a.part_ml[slot(r) * stride + h].x));
+  const float ref = M == -INFINITY ? 0.f : M;
+  float den = 0.f;
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int r = r0; r <= desc.y; ++r) {
+    const float2 ml = __ldcg(&a.part_ml[slot(r) * stride + h]);
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(r) * a.num_heads + h) * kLatentDim + d));
+    const float w = fast_exp2(ml.x - ref);
+    den = fmaf(w, ml.y, den);
+    num.x = fmaf(w, o.x, num.x);
+    num.y = fmaf(w, o.y, num.y);
+    num.z = fmaf(w, o.z, num.z);
+    num.w = fmaf(w, o.w, num.w);
+  }
+  const float inv = 1.f / den;
+  uint2 v = make_uint2(pack2<T>(num.x * inv, num.y * inv), pack2<T>(num.z * inv, num.w * inv));
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(desc.x) * a.num_heads + h) * kLatentDim + d) = v;
+}
+
+}  // namespace pkv

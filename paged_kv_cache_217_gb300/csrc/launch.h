@@ -108,13 +108,24 @@ struct LatentArgs {
   int max_blocks_per_seq;
   int num_blocks;
   float scale_log2;  // scale * log2(e)
+  // set by the launcher: work ranges, blocks of heads, heads per block, and the workspace's parts
+  int ranges, head_blocks, block_heads;
+  int2* desc;
+  float2* part_ml;
+  float* part_o;
 };
 
 cudaError_t launch_latent_write(const void* latent, const void* rope, void* cache, const int64_t* slots,
                                 int num_tokens, int64_t latent_stride, int64_t rope_stride, int num_blocks,
                                 unsigned int* status, cudaStream_t stream);
 size_t latent_workspace_bytes(int num_seqs, int num_heads, int max_blocks_per_seq);
-cudaError_t launch_latent_decode(const LatentArgs& a, bool bf16, cudaStream_t stream);
+// Rows of the query's tensor-map box (query heads a CTA takes, padded).
+int latent_query_box(int num_seqs, int num_heads, int max_blocks_per_seq);
+// cache_map: the cache as [num_blocks * 16, 576], boxes of 16 rows x 64
+// columns; q_map: q as [num_seqs, num_heads, 576], boxes of 1 x
+// latent_query_box x 64; both with the 128-byte swizzle and zero fill.
+cudaError_t launch_latent_decode(const LatentArgs& a, bool bf16, const CUtensorMap& cache_map,
+                                 const CUtensorMap& q_map, cudaStream_t stream);
 
 // Block tables on the device (tables.cu).
 struct ExtendArgs {
