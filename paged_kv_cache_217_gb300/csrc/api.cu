@@ -270,6 +270,25 @@ pkv_status_t pool_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, i
   return PKV_OK;
 }
 
+// A latent cache [num_blocks][16][576] as a 4-D tensor {64 elements, 8 rows, 9
+// chunks of 64, 2 * num_blocks groups of 8 rows}, read a block at a time: the
+// copy lays a block out as two groups of 9 swizzled 8-row x 128-byte atoms.
+pkv_status_t latent_tensor_map(CUtensorMap* map, const void* cache, int num_blocks, pkv_dtype_t dtype) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t row = cuuint64_t(pkv::kLatentRow) * 2;
+  const cuuint64_t dims[4] = {64, 8, pkv::kLatentRow / 64, cuuint64_t(num_blocks) * 2};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {64, 8, pkv::kLatentRow / 64, 2};
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         4, const_cast<void*>(cache), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled (latent rows) failed (CUresult %d)", int(r));
+  return PKV_OK;
+}
+
 // The queries [num_seqs][num_heads][width] of latent attention as a 3-D
 // tensor, read in boxes of one sequence x box_heads heads x 64 columns.
 pkv_status_t query_tensor_map(CUtensorMap* map, const void* q, int num_seqs, int num_heads, int width,
@@ -1100,7 +1119,7 @@ pkv_status_t pkv_paged_latent_decode(void* out, const void* q, const void* cache
   a.num_blocks = num_blocks;
   a.scale_log2 = scale * 1.4426950408889634f;
   alignas(64) CUtensorMap cache_map, q_map;
-  st = pool_tensor_map(&cache_map, cache, int64_t(num_blocks) * PKV_BLOCK_SIZE, pkv::kLatentRow, dtype, PKV_BLOCK_SIZE);
+  st = latent_tensor_map(&cache_map, cache, num_blocks, dtype);
   if (st != PKV_OK) return st;
   st = query_tensor_map(&q_map, q, num_seqs, num_heads, pkv::kLatentRow, dtype,
                         pkv::latent_query_box(num_seqs, num_heads, max_blocks_per_seq));

@@ -59,7 +59,7 @@ cudaError_t launch_n(LatentArgs a, const LatentShape& p, const CUtensorMap& cach
   err = launch_pdl(latent_decode_kernel<T, N>, dim3(unsigned(p.blocks * p.ranges)), dim3(kLatentThreads), C::SMEM_BYTES,
                    stream, a, cache_map, q_map);
   if (err != cudaSuccess) return err;
-  return launch_pdl(latent_merge_kernel<T>, dim3(unsigned(p.ranges), unsigned((a.num_heads + 1) / 2)), dim3(256), 0,
+  return launch_pdl(latent_merge_kernel<T>, dim3(unsigned(p.ranges), unsigned(a.num_heads)), dim3(256), 0,
                     stream, a);
 }
 

@@ -9,23 +9,31 @@
 // One CTA (1 per SM) takes up to N = 16, 32 or 64 heads and a range of 64-token
 // tiles; both products run transposed, heads on the MMA's N:
 //  * S^T[64 tokens, N] = K Q^T: A the tile's rows as they lie in shared memory
-//    (9 chunks of 64 tokens x 64 elements, 128-byte swizzle, K-major), B the
-//    queries (loaded once per sequence);
-//  * O^T[512, N] += V^T P^T: A the same chunks read along the other axis
-//    (MN-major), 4 products of 128 dims, B the weights P (16 bits, [N, 64]).
+//    (K-major, 128-byte swizzle), B the queries (loaded once per sequence);
+//  * O^T[512, N] += V^T P^T: A the same rows read along the other axis
+//    (MN-major), 4 products of 128 dims per 16 tokens, B the weights P (16
+//    bits, [N, 64]).
 // With heads on M instead, O would need all 512 columns of tensor memory and
 // leave none for S; transposed it takes 4 N columns, and S^T 2 N (two buffers).
-// Rows arrive by TMA (16 x 64 boxes through the block table; blocks past the
-// end read the zero fill) into a ring of 128-dim pairs, 16 KB each, and a small
-// ring for the rotary chunk; a pair is released as soon as its product is done.
+// A 16-token block (18 KB) arrives by one TMA copy of a 4-D view of the cache,
+// {64 elements, 8 rows, 9 chunks, 8-row groups}, which lays it out as groups of
+// 9 swizzle atoms of 8 rows x 128 bytes: both products step over tokens in
+// strides of 9 KB and over elements in strides of 1 KB. (36 copies of 16 x 64
+// boxes a tile instead took one warp 2700 cycles to issue.) Blocks past the end
+// read the zero fill. The ring holds two tiles; a block's place is free as soon
+// as its 16 tokens have entered O^T.
 //
-// Warps: 0-3 softmax and output, 4 copies, 5 MMA issue. S^T of tile i + 1 is
-// issued before O^T of tile i, so that the tensor cores work while the softmax
-// of tile i runs. The running maximum is a reference that moves only when a
-// score exceeds it by 2^8 (one vote a tile); moving it rescales O^T in tensor
-// memory. Weights are rounded to the cache's type (bf16: 2^-8 relative, one per
-// weight, which averages out over the tokens; their sum is taken before the
-// rounding in fp32).
+// Warps: 0-3 softmax and output, 4 copies, 5 MMA issue. The MMA warp issues
+// S^T of the next tile when its rows have landed, else O^T of the current one
+// when its weights are there: with slow rows the ring drains early, with slow
+// products the softmax of tile i overlaps S^T of tile i + 1. Measured issue
+// cost per MMA (M 64: 23 cycles at N 16, 32 at N 64; M 128: 39 and 48) against
+// 16 and 32 cycles to read the A operand at 128 bytes a cycle.
+// The running maximum is a reference that moves only when a score exceeds it
+// by 2^8 (one vote a tile); moving it rescales O^T in tensor memory. Weights
+// are rounded to the cache's type (bf16: 2^-8 relative, one per weight, which
+// averages out over the tokens; their sum is taken before the rounding in
+// fp32).
 //
 // Work: the batch's tiles are one list cut into equal ranges, one per CTA (per
 // block of heads), whatever the lengths. A sequence inside one range is written
@@ -47,8 +55,10 @@ constexpr int kLatentSms = 152;       // CTAs a wave holds (one per SM of a GB30
 constexpr int kLatentTile = 64;       // tokens per tile
 constexpr int kLatentThreads = 192;
 constexpr float kLatentLazy = 8.f;
-constexpr int kLatentChunk = kLatentTile * 128;  // bytes of 64 tokens x 64 elements
-constexpr int kLatentPairs = kLatentDim / 128;   // 128-dim pairs per tile
+constexpr int kLatentAtom = 1024;                        // 8 rows x 128 bytes
+constexpr int kLatentGroup = kLatentRow / 64 * kLatentAtom;  // 8 tokens: 9 atoms
+constexpr int kLatentBlockBytes = 2 * kLatentGroup;      // 16 tokens
+constexpr int kLatentTileBytes = 4 * kLatentBlockBytes;
 
 inline size_t latent_desc_bytes(int ranges) { return (size_t(ranges) * sizeof(int2) + 15) / 16 * 16; }
 
@@ -56,14 +66,10 @@ template <int N>
 struct LatentCfg {
   static constexpr int Q_BYTES = N * kLatentRow * 2;
   static constexpr int P_BYTES = N * kLatentTile * 2;
-  static constexpr int ROPE_SLOTS = 2;
   static constexpr int MISC = 2048;  // barriers, statistics
-  static constexpr int PAIR_SLOTS =
-      (227 * 1024 - 1024 - MISC - Q_BYTES - P_BYTES - ROPE_SLOTS * kLatentChunk) / (2 * kLatentChunk);
-  static constexpr size_t SMEM_BYTES =
-      1024 + MISC + Q_BYTES + P_BYTES + ROPE_SLOTS * kLatentChunk + size_t(PAIR_SLOTS) * 2 * kLatentChunk;
+  static constexpr size_t SMEM_BYTES = 1024 + MISC + Q_BYTES + P_BYTES + 2 * kLatentTileBytes;
   static constexpr int TMEM_COLS = 8 * N;  // 4 N for O^T, 2 N for S^T, a power of two
-  static_assert(PAIR_SLOTS >= 2 * kLatentPairs, "two tiles in flight");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
 // ---- tcgen05 ----------------------------------------------------------------
@@ -124,6 +130,14 @@ __device__ __forceinline__ void tc_st_32x16(uint32_t addr, const float* r) {
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -138,6 +152,14 @@ __device__ __forceinline__ void stsm_x4_trans(uint32_t addr, uint32_t a, uint32_
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
                "r"(c), "r"(d)
                : "memory");
+}
+// One lane of a converged warp. The compiler knows that a branch on it is taken
+// by one lane: tcgen05.mma's operands then stay in uniform registers (a branch
+// on the lane index issued one MMA in 155 cycles, this one in 23 to 48).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // Barrier of the four softmax warps.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -174,8 +196,7 @@ __device__ __forceinline__ int latent_tiles(int L) { return (L + kLatentTile - 1
 // Shared state of a CTA outside the operand buffers.
 template <int N>
 struct LatentShared {
-  uint64_t pair_full[LatentCfg<N>::PAIR_SLOTS], pair_empty[LatentCfg<N>::PAIR_SLOTS];
-  uint64_t rope_full[2], rope_empty[2];
+  uint64_t tile_full[2], block_empty[8];
   uint64_t q_full, q_empty, s_full[2], p_full, pv_done;
   uint32_t tmem;
   int stop;  // a wait gave up: every role leaves
@@ -231,21 +252,16 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
   unsigned char* q_mem = base;                       // 9 chunks of [N][64]
   unsigned char* p_mem = q_mem + C::Q_BYTES;         // [N][64 tokens]
-  unsigned char* rope_mem = p_mem + C::P_BYTES;      // ROPE_SLOTS chunks
-  unsigned char* pair_mem = rope_mem + C::ROPE_SLOTS * kLatentChunk;
-  LatentShared<N>& sh = *reinterpret_cast<LatentShared<N>*>(pair_mem + size_t(C::PAIR_SLOTS) * 2 * kLatentChunk);
+  unsigned char* ring = p_mem + C::P_BYTES;          // two tiles
+  LatentShared<N>& sh = *reinterpret_cast<LatentShared<N>*>(ring + 2 * kLatentTileBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hb = int(blockIdx.x) % a.head_blocks, range = int(blockIdx.x) / a.head_blocks;
   const int h0 = hb * a.block_heads, heads = min(a.block_heads, a.num_heads - h0);
 
   if (tid == 0) {
-    for (int i = 0; i < C::PAIR_SLOTS; ++i) {
-      mbar_init(smem_addr(&sh.pair_full[i]), 1);
-      mbar_init(smem_addr(&sh.pair_empty[i]), 1);
-    }
+    for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&sh.block_empty[i]), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&sh.rope_full[i]), 1);
-      mbar_init(smem_addr(&sh.rope_empty[i]), 1);
+      mbar_init(smem_addr(&sh.tile_full[i]), 1);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
     }
     mbar_init(smem_addr(&sh.q_full), 1);
@@ -275,7 +291,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     if ((raw < 0 || raw > a.max_blocks_per_seq * kBlock) && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
     mine += latent_tiles(latent_len(a, s));
   }
-  long long* scan = reinterpret_cast<long long*>(pair_mem);  // (before any copy)
+  long long* scan = reinterpret_cast<long long*>(ring);  // (before any copy)
   scan[tid] = mine;
   __syncthreads();
   long long before = 0, total = 0;
@@ -316,7 +332,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
 
   if (warp == 4) {
     // ---- copies ----
-    int pair = 0, tile = 0, seg = 0;
+    int tile = 0, seg = 0;
     bool ok = true;  // warp-uniform
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
       return bool(__all_sync(kFull, latent_wait(bar, parity, stop, a.status)));
@@ -324,15 +340,19 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     while (ok && walk.next(a)) {
       if (seg > 0) ok = wait_all(smem_addr(&sh.q_empty), (seg - 1) & 1);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.q_full), C::Q_BYTES);
-      __syncwarp();
-      if (lane < 9)
-        tma_load_3d(smem_addr(q_mem) + lane * (N * 128), &q_map, 64 * lane, h0, walk.s, smem_addr(&sh.q_full));
+      if (elect_one()) {
+        const uint32_t qb = smem_addr(&sh.q_full);
+        mbar_arrive_expect_tx(qb, C::Q_BYTES);
+#pragma unroll
+        for (int c = 0; c < kLatentRow / 64; ++c)
+          tma_load_3d(smem_addr(q_mem) + c * (N * 128), &q_map, 64 * c, h0, walk.s, qb);
+      }
+      ++seg;
       const int nb = (walk.L + kBlock - 1) / kBlock;
       const int32_t* row = a.block_tables + size_t(walk.s) * a.max_blocks_per_seq;
-      int ids = 0, ids_from = -1;  // lane l: the block of index ids_from + l
+      int ids = 0, ids_from = -32;  // lane l: the block of index ids_from + l
       for (int t = walk.first; ok && t < walk.last; ++t, ++tile) {
-        if (ids_from < 0 || 4 * t + 4 > ids_from + 32) {
+        if (4 * t + 4 > ids_from + 32) {
           ids_from = 4 * t;
           const int j = ids_from + lane;
           ids = a.num_blocks;  // past the end: rows outside the tensor read as zeros
@@ -344,102 +364,95 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
             }
           }
         }
-        const int id = __shfl_sync(kFull, ids, 4 * t - ids_from + (lane & 3));  // lane & 3: block of the tile
-        const int y = id * kBlock, off = (lane & 3) * kBlock * 128;
-        const int rs = tile & 1;
-        if (tile >= 2) ok = wait_all(smem_addr(&sh.rope_empty[rs]), ((tile >> 1) - 1) & 1);
-        if (!ok) break;
-        const uint32_t rb = smem_addr(&sh.rope_full[rs]);
-        if (lane == 0) mbar_arrive_expect_tx(rb, kLatentChunk);
-        __syncwarp();
-        if (lane < 4) tma_load_2d(smem_addr(rope_mem) + rs * kLatentChunk + off, &cache_map, kLatentDim, y, rb);
-        for (int j = 0; j < kLatentPairs; ++j, ++pair) {
-          const int slot = pair % C::PAIR_SLOTS, use = pair / C::PAIR_SLOTS;
-          if (use > 0) ok = wait_all(smem_addr(&sh.pair_empty[slot]), (use - 1) & 1);
-          if (!ok) break;
-          const uint32_t pb = smem_addr(&sh.pair_full[slot]);
-          if (lane == 0) mbar_arrive_expect_tx(pb, 2 * kLatentChunk);
+        const uint32_t fb = smem_addr(&sh.tile_full[tile & 1]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int slot = 4 * (tile & 1) + j;
+          const int id = __shfl_sync(kFull, ids, 4 * t - ids_from + j);
+          if (ok && tile >= 2) ok = wait_all(smem_addr(&sh.block_empty[slot]), ((tile >> 1) - 1) & 1);
+          if (ok && elect_one()) {
+            if (j == 0) mbar_arrive_expect_tx(fb, kLatentTileBytes);
+            tma_load_4d(smem_addr(ring) + slot * kLatentBlockBytes, &cache_map, 0, 0, 0, 2 * id, fb);
+          }
           __syncwarp();
-          if (lane < 8)
-            tma_load_2d(smem_addr(pair_mem) + slot * 2 * kLatentChunk + (lane >> 2) * kLatentChunk + off, &cache_map,
-                        128 * j + 64 * (lane >> 2), y, pb);
         }
+        if (!ok) break;
       }
-      ++seg;
     }
-    if (*stop) {  // wait (bounded) for the copies in flight: the last use of every slot
-      for (int i = 0; i < C::PAIR_SLOTS; ++i) {
-        const int uses = pair > i ? (pair - 1 - i) / C::PAIR_SLOTS + 1 : 0;
-        if (uses > 0) mbar_wait_bounded(smem_addr(&sh.pair_full[i]), (uses - 1) & 1, 10000000ull);
-      }
+    if (*stop) {
+      // Wait (bounded) for the copies in flight. A tile whose copies were not
+      // all issued never completes its phase: its wait runs to the limit.
       for (int i = 0; i < 2; ++i) {
-        const int uses = tile > i ? (tile - 1 - i) / 2 + 1 : 0;
-        if (uses > 0) mbar_wait_bounded(smem_addr(&sh.rope_full[i]), (uses - 1) & 1, 10000000ull);
+        const int uses = tile >= i ? (tile - i) / 2 + 1 : 0;
+        if (uses > 0) mbar_wait_bounded(smem_addr(&sh.tile_full[i]), (uses - 1) & 1, 10000000ull);
       }
       if (seg > 0) mbar_wait_bounded(smem_addr(&sh.q_full), (seg - 1) & 1, 10000000ull);
     }
   } else if (warp == 5) {
     // ---- MMA issue: one lane ----
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t id_s = tc_idesc<T>(kLatentTile, N, false), id_o = tc_idesc<T>(128, N, true);
       const uint64_t q_desc = tc_desc(smem_addr(q_mem), 16, 1024), p_desc = tc_desc(smem_addr(p_mem), 16, 1024);
-      const uint64_t rope_desc = tc_desc(smem_addr(rope_mem), 16, 1024);
-      const uint64_t key_desc = tc_desc(smem_addr(pair_mem), 16, 1024);
-      const uint64_t val_desc = tc_desc(smem_addr(pair_mem), kLatentChunk, 1024);
-      bool ok = true;
-      int tile = 0, seg = 0;  // of S^T
-      // S^T of the next tile: the rotary chunk, then the pairs as they arrive
-      auto scores = [&](bool last) {
-        const int rs = tile & 1;
-        const uint32_t d = tmem + 4 * N + (tile & 1) * N;
-        ok = ok && latent_wait(smem_addr(&sh.rope_full[rs]), (tile >> 1) & 1, stop, a.status);
-        if (!ok) return;
-        tc_fence_after();
-        for (int k = 0; k < 4; ++k)
-          tc_mma(d, rope_desc + rs * (kLatentChunk >> 4) + 2 * k, q_desc + 8 * (N * 128 >> 4) + 2 * k, id_s, k > 0);
-        tc_commit(smem_addr(&sh.rope_empty[rs]));
-        for (int j = 0; j < kLatentPairs; ++j) {
-          const int pr = tile * kLatentPairs + j, slot = pr % C::PAIR_SLOTS;
-          ok = ok && latent_wait(smem_addr(&sh.pair_full[slot]), (pr / C::PAIR_SLOTS) & 1, stop, a.status);
-          if (!ok) return;
+      const uint64_t key_desc = tc_desc(smem_addr(ring), 16, kLatentGroup);
+      const uint64_t val_desc = tc_desc(smem_addr(ring), kLatentAtom, kLatentGroup);
+      const int n = int(end - begin);
+      int qk = 0, pv = 0, seg = 0;      // tiles whose S^T, O^T are issued; segments whose queries are waited for
+      bool seg_first = true;            // tile qk starts a segment
+      uint32_t starts = 0;              // bit t & 1: tile t starts a segment (t = pv, pv + 1)
+      int t = 0;                        // tile qk within its sequence
+      if (n > 0) {
+        walk.next(a);
+        t = walk.first;
+      }
+      unsigned long long idle = 0;
+      while (pv < n) {
+        // S^T of tile qk: its buffer is free once O^T of tile qk - 2 is issued
+        if (qk < n && qk < pv + 2 && mbar_try_wait(smem_addr(&sh.tile_full[qk & 1]), (qk >> 1) & 1) &&
+            (!seg_first || mbar_try_wait(smem_addr(&sh.q_full), seg & 1))) {
           tc_fence_after();
-          for (int c = 0; c < 2; ++c)
+          const uint32_t d = tmem + 4 * N + (qk & 1) * N;
+          const uint64_t key = key_desc + (qk & 1) * (kLatentTileBytes >> 4);
+#pragma unroll
+          for (int c = 0; c < kLatentRow / 64; ++c)
+#pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma(d, key_desc + (slot * 2 + c) * (kLatentChunk >> 4) + 2 * k,
-                     q_desc + (2 * j + c) * (N * 128 >> 4) + 2 * k, id_s, true);
-        }
-        tc_commit(smem_addr(&sh.s_full[tile & 1]));
-        if (last) tc_commit(smem_addr(&sh.q_empty));
-        ++tile;
-      };
-      // O^T of tile i
-      auto outputs = [&](int i, bool first) {
-        ok = ok && latent_wait(smem_addr(&sh.p_full), i & 1, stop, a.status);
-        if (!ok) return;
-        tc_fence_after();
-        for (int j = 0; j < kLatentPairs; ++j) {
-          const int slot = (i * kLatentPairs + j) % C::PAIR_SLOTS;
-          for (int k = 0; k < 4; ++k)
-            tc_mma(tmem + j * N, val_desc + slot * 2 * (kLatentChunk >> 4) + k * (16 * 128 >> 4), p_desc + 2 * k, id_o,
-                   !(first && k == 0));
-          tc_commit(smem_addr(&sh.pair_empty[slot]));
-        }
-        tc_commit(smem_addr(&sh.pv_done));
-      };
-      int done = 0;             // tiles whose O^T is issued
-      bool pending_first = true;  // whether tile `done` starts a segment
-      while (ok && walk.next(a)) {
-        ok = latent_wait(smem_addr(&sh.q_full), seg & 1, stop, a.status);
-        if (!ok) break;
-        ++seg;
-        for (int t = walk.first; ok && t < walk.last; ++t) {
-          const bool first = t == walk.first;
-          scores(t == walk.last - 1);
-          if (ok && tile > 1) outputs(done++, pending_first);
-          pending_first = first;
+              tc_mma(d, key + c * (kLatentAtom >> 4) + 2 * k, q_desc + c * (N * 128 >> 4) + 2 * k, id_s, c + k > 0);
+          tc_commit(smem_addr(&sh.s_full[qk & 1]));
+          starts = (starts & ~(1u << (qk & 1))) | (uint32_t(seg_first) << (qk & 1));
+          seg += seg_first ? 1 : 0;
+          seg_first = ++t == walk.last;
+          if (seg_first) {
+            tc_commit(smem_addr(&sh.q_empty));
+            if (walk.next(a)) t = walk.first;
+          }
+          ++qk;
+          idle = 0;
+        } else if (pv < qk && mbar_try_wait(smem_addr(&sh.p_full), pv & 1)) {
+          tc_fence_after();
+          const uint64_t val = val_desc + (pv & 1) * (kLatentTileBytes >> 4);
+          const bool first = (starts >> (pv & 1)) & 1u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // 16 tokens: one block
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // 128 dims
+              tc_mma(tmem + j * N, val + k * (kLatentBlockBytes >> 4) + j * (2 * kLatentAtom >> 4), p_desc + 2 * k, id_o,
+                     !(first && k == 0));
+            tc_commit(smem_addr(&sh.block_empty[4 * (pv & 1) + k]));
+          }
+          tc_commit(smem_addr(&sh.pv_done));
+          ++pv;
+          idle = 0;
+        } else {
+          const unsigned long long now = global_timer_ns();
+          if (idle == 0) idle = now;
+          if (*stop) break;
+          if (now - idle > kWaitLimitNs) {
+            *stop = 1;
+            flag(a.status, PKV_DEV_WAIT_TIMEOUT);
+            break;
+          }
         }
       }
-      if (ok && tile > 0) outputs(done, pending_first);
       if (*stop) {  // let the products in flight end before the tensor memory is freed
         const uint32_t bar = smem_addr(&sh.drain);
         mbar_init(bar, 1);
@@ -454,18 +467,15 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     constexpr int G8 = N / 8;  // groups of 8 heads: this thread keeps heads 8 i + 2 t, + 1
     const int t = lane & 3, gr = lane >> 2;
     const uint32_t lanes = uint32_t(warp * 32) << 16;
-    int tile = 0, seg = 0;
-    bool ok = true;
-    while (ok && walk.next(a)) {
+    // (After a wait gave up, `stop` lets every later wait return at once: these
+    // warps then run out their loops, together and without further waiting.)
+    int tile = 0;
+    while (walk.next(a)) {
       float m[G8][2], l[G8][2];
 #pragma unroll
       for (int i = 0; i < G8; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
       for (int u = walk.first; u < walk.last; ++u, ++tile) {
-        ok = latent_wait(smem_addr(&sh.s_full[tile & 1]), (tile >> 1) & 1, stop, a.status);
-        if (softmax_any(!ok)) {
-          ok = false;
-          break;
-        }
+        latent_wait(smem_addr(&sh.s_full[tile & 1]), (tile >> 1) & 1, stop, a.status);
         tc_fence_after();
         float x[G8][4];  // rows gr (0, 1) and gr + 8 (2, 3) of this warp's 16 tokens
 #pragma unroll
@@ -520,11 +530,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
             l[i][e] += p[i][e] + p[i][2 + e];
           }
         // P and O^T are free once the previous tile's product is done
-        if (tile > 0) ok = latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
-        if (softmax_any(!ok)) {
-          ok = false;
-          break;
-        }
+        if (tile > 0) latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
         if (moving && u > walk.first) {
           tc_fence_after();
 #pragma unroll 1
@@ -542,11 +548,10 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
           // rows past the end hold whatever the block holds (NaN included): as
           // values they must be zeros
           const int dead = min(kLatentTile, (left + kBlock - 1) / kBlock * kBlock) - left;
-          for (int i = tid; i < dead * 2 * kLatentPairs * 8; i += 128) {
-            const int v = i % 8, c = i / 8 % (2 * kLatentPairs), r = left + i / (16 * kLatentPairs);
-            const int slot = (tile * kLatentPairs + c / 2) % C::PAIR_SLOTS;
-            reinterpret_cast<uint4*>(pair_mem + size_t(slot * 2 + c % 2) * kLatentChunk + r * 128)[v] =
-                make_uint4(0u, 0u, 0u, 0u);
+          for (int i = tid; i < dead * (kLatentDim / 8); i += 128) {
+            const int v = i % (kLatentDim / 8), r = left + i / (kLatentDim / 8);
+            *reinterpret_cast<uint4*>(ring + (tile & 1) * kLatentTileBytes + r / 8 * kLatentGroup + v / 8 * kLatentAtom +
+                                      r % 8 * 128 + v % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
 #pragma unroll
@@ -561,8 +566,6 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         tc_fence_before();
         mbar_arrive(smem_addr(&sh.p_full));
       }
-      if (!ok) break;
-      ++seg;
       // The segment's sums, then its output: thread = dim, columns = heads.
 #pragma unroll
       for (int i = 0; i < G8; ++i)
@@ -591,23 +594,38 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         while (r * total / used > last) --r;
         a.desc[range] = make_int2(walk.s, int(r));
       }
-      ok = latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
-      if (softmax_any(!ok)) break;
+      latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
+      softmax_sync();
       tc_fence_after();
+      T* const out = static_cast<T*>(a.out) + (size_t(walk.s) * a.num_heads + h0) * kLatentDim;
+      float* const part = a.part_o + (size_t(slot) * a.num_heads + h0) * kLatentDim + warp * 32 + lane;
 #pragma unroll 1
-      for (int c = 0; c < 4 * N; c += 16) {
-        float o[16];
-        tc_ld_32x16(tmem + lanes + c, o);
-        tc_wait_ld();
-        const int dim = (c / N) * 128 + warp * 32 + lane;
+      for (int j = 0; j < kLatentDim / 128; ++j) {
+        float o[2][16];
+        tc_ld_32x16(tmem + lanes + j * N, o[0]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int h = c % N + i;
-          if (h >= heads) continue;
-          if (whole)
-            static_cast<T*>(a.out)[(size_t(walk.s) * a.num_heads + h0 + h) * kLatentDim + dim] = T(o[i] * sh.alpha[h]);
-          else
-            a.part_o[(size_t(slot) * a.num_heads + h0 + h) * kLatentDim + dim] = o[i];
+        for (int c = 0; c < N / 16; ++c) {
+          tc_wait_ld();
+          if (c + 1 < N / 16) tc_ld_32x16(tmem + lanes + j * N + 16 * (c + 1), o[(c + 1) & 1]);
+          float(&x)[16] = o[c & 1];
+          if (whole) {
+            // two heads a step: even lanes take the first one's dims lane, lane +
+            // 1, odd lanes the second one's dims lane - 1, lane
+            const int dim = j * 128 + warp * 32 + (lane & ~1);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float e = x[i] * sh.alpha[16 * c + i], f = x[i + 1] * sh.alpha[16 * c + i + 1];
+              const float g = __shfl_xor_sync(kFull, lane & 1 ? e : f, 1);
+              const int h = 16 * c + i + (lane & 1);
+              if (h < heads)
+                *reinterpret_cast<uint32_t*>(out + size_t(h) * kLatentDim + dim) =
+                    lane & 1 ? pack2<T>(g, f) : pack2<T>(e, g);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (16 * c + i < heads) part[(16 * c + i) * kLatentDim + j * 128] = x[i];
+          }
         }
       }
       tc_fence_before();  // the next segment's O^T comes after these reads
@@ -634,34 +652,57 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
 }
 
 // Joins the pieces of the sequence that starts in a range and goes on past it:
-// out = sum_i w_i o_i / sum_i w_i l_i with w_i = 2^(m_i - max m). Two heads per
-// CTA, 4 dims per thread.
+// out = sum_i w_i o_i / sum_i w_i l_i with w_i = 2^(m_i - max m). One head per
+// CTA: the weights of all pieces first, then two halves of the CTA take every
+// other piece, 4 dims per thread, several pieces' loads in flight.
 template <typename T>
 __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
+  __shared__ float weight[kLatentSms], red[8];
+  __shared__ float4 other[128];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r0 = blockIdx.x, h = 2 * int(blockIdx.y) + int(threadIdx.x >> 7), d = int(threadIdx.x & 127) * 4;
+  const int r0 = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, half = tid >> 7, d = (tid & 127) * 4;
   const int2 desc = __ldcg(a.desc + r0);
-  if (desc.x < 0 || h >= a.num_heads) return;
-  const int stride = (a.num_heads + 1) / 2 * 2;
-  auto slot = [&](int r) { return size_t(2) * r + (r == r0 ? 1 : 0); };
-  float M = -INFINITY;
-  for (int r = r0; r <= desc.y; ++r) M = fmaxf(M, __ldcg(&a.part_ml[slot(r) * stride + h].x));
-  const float ref = M == -INFINITY ? 0.f : M;
-  float den = 0.f;
+  if (desc.x < 0) return;
+  const int n = desc.y - r0 + 1, stride = (a.num_heads + 1) / 2 * 2;
+  auto slot = [&](int i) { return size_t(2) * (r0 + i) + (i == 0 ? 1 : 0); };
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (tid < n) ml = __ldcg(&a.part_ml[slot(tid) * stride + h]);
+  float M = ml.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  if ((tid & 31) == 0) red[tid >> 5] = M;
+  __syncthreads();
+  M = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) M = fmaxf(M, red[i]);
+  const float w = tid < n ? fast_exp2(ml.x - (M == -INFINITY ? 0.f : M)) : 0.f;
+  if (tid < n) weight[tid] = w;
+  float den = w * ml.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
+  __syncthreads();
+  if ((tid & 31) == 0) red[tid >> 5] = den;
+  __syncthreads();
+  den = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) den += red[i];
   float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int r = r0; r <= desc.y; ++r) {
-    const float2 ml = __ldcg(&a.part_ml[slot(r) * stride + h]);
-    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(r) * a.num_heads + h) * kLatentDim + d));
-    const float w = fast_exp2(ml.x - ref);
-    den = fmaf(w, ml.y, den);
-    num.x = fmaf(w, o.x, num.x);
-    num.y = fmaf(w, o.y, num.y);
-    num.z = fmaf(w, o.z, num.z);
-    num.w = fmaf(w, o.w, num.w);
+#pragma unroll 8
+  for (int i = half; i < n; i += 2) {
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * a.num_heads + h) * kLatentDim + d));
+    const float wi = weight[i];
+    num.x = fmaf(wi, o.x, num.x);
+    num.y = fmaf(wi, o.y, num.y);
+    num.z = fmaf(wi, o.z, num.z);
+    num.w = fmaf(wi, o.w, num.w);
   }
+  if (half) other[tid & 127] = num;
+  __syncthreads();
+  if (half) return;
+  const float4 x = other[tid];
   const float inv = 1.f / den;
-  uint2 v = make_uint2(pack2<T>(num.x * inv, num.y * inv), pack2<T>(num.z * inv, num.w * inv));
+  const uint2 v = make_uint2(pack2<T>((num.x + x.x) * inv, (num.y + x.y) * inv),
+                             pack2<T>((num.z + x.z) * inv, (num.w + x.w) * inv));
   *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(desc.x) * a.num_heads + h) * kLatentDim + d) = v;
 }
 

@@ -121,9 +121,9 @@ cudaError_t launch_latent_write(const void* latent, const void* rope, void* cach
 size_t latent_workspace_bytes(int num_seqs, int num_heads, int max_blocks_per_seq);
 // Rows of the query's tensor-map box (query heads a CTA takes, padded).
 int latent_query_box(int num_seqs, int num_heads, int max_blocks_per_seq);
-// cache_map: the cache as [num_blocks * 16, 576], boxes of 16 rows x 64
-// columns; q_map: q as [num_seqs, num_heads, 576], boxes of 1 x
-// latent_query_box x 64; both with the 128-byte swizzle and zero fill.
+// cache_map: the cache as {64 elements, 8 rows, 9 chunks, 2 * num_blocks
+// groups}, boxes of one block; q_map: q as [num_seqs, num_heads, 576], boxes of
+// 1 x latent_query_box x 64; both with the 128-byte swizzle and zero fill.
 cudaError_t launch_latent_decode(const LatentArgs& a, bool bf16, const CUtensorMap& cache_map,
                                  const CUtensorMap& q_map, cudaStream_t stream);
 
