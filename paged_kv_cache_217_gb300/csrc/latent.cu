@@ -59,8 +59,11 @@ cudaError_t launch_n(LatentArgs a, const LatentShape& p, const CUtensorMap& cach
   err = launch_pdl(latent_decode_kernel<T, N>, dim3(unsigned(p.blocks * p.ranges)), dim3(kLatentThreads), C::SMEM_BYTES,
                    stream, a, cache_map, q_map);
   if (err != cudaSuccess) return err;
-  return launch_pdl(latent_merge_kernel<T>, dim3(unsigned(p.ranges), unsigned(a.num_heads)), dim3(256), 0,
-                    stream, a);
+  if (p.ranges == 1) return cudaSuccess;  // one range: nothing crosses
+  const unsigned ranges = unsigned(p.ranges), heads = unsigned(a.num_heads);
+  if (a.num_seqs <= p.ranges / 4)  // four or more pieces a sequence
+    return launch_pdl(latent_merge_kernel<T, N, 4>, dim3(ranges, heads, 4), dim3(256), 0, stream, a);
+  return launch_pdl(latent_merge_kernel<T, N, 1>, dim3(ranges, heads), dim3(256), 0, stream, a);
 }
 
 template <typename T>
@@ -71,7 +74,7 @@ cudaError_t launch_t(LatentArgs a, const CUtensorMap& cache_map, const CUtensorM
   a.block_heads = p.heads;
   a.desc = static_cast<int2*>(a.workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + latent_desc_bytes(p.ranges));
-  a.part_o = reinterpret_cast<float*>(a.part_ml + size_t(2) * p.ranges * ((a.num_heads + 1) / 2 * 2));
+  a.part_o = reinterpret_cast<float*>(a.part_ml + size_t(2) * p.ranges * p.blocks * p.n);
   switch (p.n) {
     case 16: return launch_n<T, 16>(a, p, cache_map, q_map, stream);
     case 32: return launch_n<T, 32>(a, p, cache_map, q_map, stream);
@@ -95,8 +98,8 @@ cudaError_t launch_latent_write(const void* latent, const void* rope, void* cach
 // sum) pairs and fp32 accumulators.
 size_t latent_workspace_bytes(int num_seqs, int num_heads, int max_blocks_per_seq) {
   const LatentShape p = latent_shape(num_seqs, num_heads, max_blocks_per_seq);
-  return latent_desc_bytes(p.ranges) + size_t(2) * p.ranges * ((num_heads + 1) / 2 * 2) * sizeof(float2) +
-         size_t(2) * p.ranges * num_heads * kLatentDim * sizeof(float);
+  return latent_desc_bytes(p.ranges) +
+         size_t(2) * p.ranges * p.blocks * p.n * (sizeof(float2) + kLatentDim * sizeof(float));
 }
 
 int latent_query_box(int num_seqs, int num_heads, int max_blocks_per_seq) {

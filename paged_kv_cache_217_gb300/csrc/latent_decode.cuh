@@ -55,6 +55,7 @@ constexpr int kLatentSms = 152;       // CTAs a wave holds (one per SM of a GB30
 constexpr int kLatentTile = 64;       // tokens per tile
 constexpr int kLatentThreads = 192;
 constexpr float kLatentLazy = 8.f;
+constexpr int kLatentAhead = 2;       // tiles between a copy and the prefetch of a later one
 constexpr int kLatentAtom = 1024;                        // 8 rows x 128 bytes
 constexpr int kLatentGroup = kLatentRow / 64 * kLatentAtom;  // 8 tokens: 9 atoms
 constexpr int kLatentBlockBytes = 2 * kLatentGroup;      // 16 tokens
@@ -138,6 +139,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(y),
+               "r"(z), "r"(w)
+               : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -201,7 +207,8 @@ struct LatentShared {
   uint32_t tmem;
   int stop;  // a wait gave up: every role leaves
   int first_seq;
-  long long first_tile, begin, end, total;  // first_tile: list index of first_seq's first tile
+  long long first_tile;                      // list index of first_seq's first tile
+  long long scan[kLatentThreads / 32];
   uint64_t drain;                            // after a wait gave up
   float stat[4][N], alpha[N], mref[N];       // per warp and head; rescale factors; references
 };
@@ -222,18 +229,31 @@ __device__ __forceinline__ bool latent_wait(uint32_t bar, uint32_t parity, volat
 }
 
 // Walks a CTA's range [begin, end) of the tile list as segments of one sequence.
+// The next sequence's length is read one segment ahead.
 struct LatentWalk {
   int s;                    // sequence
+  int L, ahead;             // its length, and the next sequence's
   long long at, end;        // list index of the next segment's first tile, and the range's end
   long long base;           // list index of sequence s's first tile
-  int L, first, last, n;    // the segment: length, its tiles [first, last), all tiles of the sequence
+  int first, last, n;       // the segment: its tiles [first, last) of the n of the sequence
+  __device__ __forceinline__ void start(const LatentArgs& a, int seq, long long tile0, long long b, long long e) {
+    s = seq;
+    base = tile0;
+    at = b;
+    end = e;
+    L = ahead = 0;
+    if (b < e) {
+      L = latent_len(a, s);
+      if (s + 1 < a.num_seqs) ahead = latent_len(a, s + 1);
+    }
+  }
   __device__ __forceinline__ bool next(const LatentArgs& a) {
     if (at >= end) return false;
-    for (;; ++s) {
-      L = latent_len(a, s);
-      n = latent_tiles(L);
-      if (base + n > at) break;
+    while (base + (n = latent_tiles(L)) <= at) {
       base += n;
+      ++s;
+      L = ahead;
+      ahead = s + 1 < a.num_seqs ? latent_len(a, s + 1) : 0;
     }
     first = int(at - base);
     last = base + n < end ? n : int(end - base);
@@ -291,13 +311,19 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     if ((raw < 0 || raw > a.max_blocks_per_seq * kBlock) && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
     mine += latent_tiles(latent_len(a, s));
   }
-  long long* scan = reinterpret_cast<long long*>(ring);  // (before any copy)
-  scan[tid] = mine;
+  long long upto = mine;  // inclusive scan over the warp, then over the warps
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) sh.scan[warp] = upto;
   __syncthreads();
-  long long before = 0, total = 0;
-  for (int i = 0; i < kLatentThreads; ++i) {
-    if (i < tid) before += scan[i];
-    total += scan[i];
+  long long before = upto - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < kLatentThreads / 32; ++i) {
+    if (i < warp) before += sh.scan[i];
+    total += sh.scan[i];
   }
   const long long used = total < a.ranges ? total : a.ranges;  // ranges that get tiles
   const long long begin = range < used ? range * total / used : 0, end = range < used ? (range + 1) * total / used : 0;
@@ -318,21 +344,19 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + size_t(s) * a.num_heads * kLatentDim);
     for (int i = tid; i < a.num_heads * kLatentDim / 8; i += kLatentThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scan's words are overwritten by copies
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   LatentWalk walk;
-  walk.s = sh.first_seq;
-  walk.at = begin;
-  walk.end = end;
-  walk.base = sh.first_tile;
+  walk.start(a, sh.first_seq, sh.first_tile, begin, end);
   volatile int* stop = &sh.stop;
+  bool open = false;  // (thread 0) the range's last sequence starts in it and goes on past it
 
   if (warp == 4) {
     // ---- copies ----
     int tile = 0, seg = 0;
+    int next_seq = -1, next_ids = 0;
     bool ok = true;  // warp-uniform
     auto wait_all = [&](uint32_t bar, uint32_t parity) {
       return bool(__all_sync(kFull, latent_wait(bar, parity, stop, a.status)));
@@ -348,35 +372,68 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
           tma_load_3d(smem_addr(q_mem) + c * (N * 128), &q_map, 64 * c, h0, walk.s, qb);
       }
       ++seg;
+      // Block ids of the segment, 32 at a time and the next 32 ahead: lane l of
+      // `ids` holds the id of block ids_from + l, of `ids_ahead` the one 32 on.
+      // Blocks past the end name rows outside the tensor, which read as zeros.
       const int nb = (walk.L + kBlock - 1) / kBlock;
       const int32_t* row = a.block_tables + size_t(walk.s) * a.max_blocks_per_seq;
-      int ids = 0, ids_from = -32;  // lane l: the block of index ids_from + l
+      auto load_ids = [&](int from) {
+        const int j = from + lane;
+        return j < nb ? __ldg(row + j) : a.num_blocks;
+      };
+      auto checked = [&](int id, int j) {
+        if (id >= 0 && (id < a.num_blocks || j >= nb)) return id;
+        flag(a.status, PKV_DEV_BAD_BLOCK_ID);
+        return 0;
+      };
+      int ids_from = 4 * walk.first;
+      int ids = next_seq == walk.s && ids_from == 0 ? (lane < nb ? next_ids : a.num_blocks) : load_ids(ids_from);
+      ids = checked(ids, ids_from + lane);
+      int ids_ahead = load_ids(ids_from + 32);
+      // the next sequence's first ids, for its rows' way into L2
+      next_seq = walk.s + 1;
+      next_ids = next_seq < a.num_seqs && lane < a.max_blocks_per_seq
+                     ? __ldg(a.block_tables + size_t(next_seq) * a.max_blocks_per_seq + lane)
+                     : 0;
+      const int next_nb = walk.at < walk.end && next_seq < a.num_seqs ? (walk.ahead + kBlock - 1) / kBlock : 0;
       for (int t = walk.first; ok && t < walk.last; ++t, ++tile) {
-        if (4 * t + 4 > ids_from + 32) {
-          ids_from = 4 * t;
-          const int j = ids_from + lane;
-          ids = a.num_blocks;  // past the end: rows outside the tensor read as zeros
-          if (j < nb) {
-            ids = __ldg(row + j);
-            if (ids < 0 || ids >= a.num_blocks) {
-              flag(a.status, PKV_DEV_BAD_BLOCK_ID);
-              ids = 0;
-            }
-          }
+        if (4 * t >= ids_from + 32) {
+          ids_from += 32;
+          ids = checked(ids_ahead, ids_from + lane);
+          ids_ahead = load_ids(ids_from + 32);
         }
-        const uint32_t fb = smem_addr(&sh.tile_full[tile & 1]);
+        // ids of the tile, and of the one kLatentAhead on (-1: none)
+        int id[4], far_id[4];
+        const int over = t + kLatentAhead - walk.last, far = 4 * (t + kLatentAhead) - ids_from;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int slot = 4 * (tile & 1) + j;
-          const int id = __shfl_sync(kFull, ids, 4 * t - ids_from + j);
-          if (ok && tile >= 2) ok = wait_all(smem_addr(&sh.block_empty[slot]), ((tile >> 1) - 1) & 1);
-          if (ok && elect_one()) {
-            if (j == 0) mbar_arrive_expect_tx(fb, kLatentTileBytes);
-            tma_load_4d(smem_addr(ring) + slot * kLatentBlockBytes, &cache_map, 0, 0, 0, 2 * id, fb);
-          }
-          __syncwarp();
+          id[j] = __shfl_sync(kFull, ids, 4 * t - ids_from + j);
+          const int x = __shfl_sync(kFull, over >= 0 ? next_ids : far < 32 ? ids : ids_ahead,
+                                    (over >= 0 ? 4 * over + j : far + j) & 31);
+          far_id[j] = x < a.num_blocks && (over < 0 || 4 * over + j < next_nb) ? x : -1;
         }
-        if (!ok) break;
+        if (elect_one()) {
+          const uint32_t fb = smem_addr(&sh.tile_full[tile & 1]);
+          const uint32_t dst = smem_addr(ring) + (tile & 1) * kLatentTileBytes;
+          const uint32_t eb = smem_addr(&sh.block_empty[4 * (tile & 1)]);
+          bool go = true;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (tile >= 2) go = go && latent_wait(eb + 8 * j, ((tile >> 1) - 1) & 1, stop, a.status);
+            // (announced only now: block_empty says that the last use's copies,
+            // and with them that phase of tile_full, are over)
+            if (go && j == 0) mbar_arrive_expect_tx(fb, kLatentTileBytes);
+            if (go) tma_load_4d(dst + j * kLatentBlockBytes, &cache_map, 0, 0, 0, 2 * id[j], fb);
+          }
+          // rows that a later copy takes start their way into L2 now, so that the
+          // copy, issued when a place is free, waits for L2 only
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (far_id[j] >= 0) tma_prefetch_4d(&cache_map, 0, 0, 0, 2 * far_id[j]);
+        }
+        __syncwarp();
+        ok = !*stop;
+        ok = __all_sync(kFull, ok);
       }
     }
     if (*stop) {
@@ -406,8 +463,24 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       }
       unsigned long long idle = 0;
       while (pv < n) {
-        // S^T of tile qk: its buffer is free once O^T of tile qk - 2 is issued
-        if (qk < n && qk < pv + 2 && mbar_try_wait(smem_addr(&sh.tile_full[qk & 1]), (qk >> 1) & 1) &&
+        // O^T first: it frees the ring
+        if (pv < qk && mbar_try_wait(smem_addr(&sh.p_full), pv & 1)) {
+          tc_fence_after();
+          const uint64_t val = val_desc + (pv & 1) * (kLatentTileBytes >> 4);
+          const bool first = (starts >> (pv & 1)) & 1u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // 16 tokens: one block
+#pragma unroll
+            for (int j = 0; j < 4; ++j)  // 128 dims
+              tc_mma(tmem + j * N, val + k * (kLatentBlockBytes >> 4) + j * (2 * kLatentAtom >> 4), p_desc + 2 * k, id_o,
+                     !(first && k == 0));
+            tc_commit(smem_addr(&sh.block_empty[4 * (pv & 1) + k]));
+          }
+          tc_commit(smem_addr(&sh.pv_done));
+          ++pv;
+          idle = 0;
+        } else if (qk < n && qk < pv + 2 &&  // (S^T's buffer: O^T of tile qk - 2 is issued)
+                   mbar_try_wait(smem_addr(&sh.tile_full[qk & 1]), (qk >> 1) & 1) &&
             (!seg_first || mbar_try_wait(smem_addr(&sh.q_full), seg & 1))) {
           tc_fence_after();
           const uint32_t d = tmem + 4 * N + (qk & 1) * N;
@@ -426,21 +499,6 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
             if (walk.next(a)) t = walk.first;
           }
           ++qk;
-          idle = 0;
-        } else if (pv < qk && mbar_try_wait(smem_addr(&sh.p_full), pv & 1)) {
-          tc_fence_after();
-          const uint64_t val = val_desc + (pv & 1) * (kLatentTileBytes >> 4);
-          const bool first = (starts >> (pv & 1)) & 1u;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 16 tokens: one block
-#pragma unroll
-            for (int j = 0; j < 4; ++j)  // 128 dims
-              tc_mma(tmem + j * N, val + k * (kLatentBlockBytes >> 4) + j * (2 * kLatentAtom >> 4), p_desc + 2 * k, id_o,
-                     !(first && k == 0));
-            tc_commit(smem_addr(&sh.block_empty[4 * (pv & 1) + k]));
-          }
-          tc_commit(smem_addr(&sh.pv_done));
-          ++pv;
           idle = 0;
         } else {
           const unsigned long long now = global_timer_ns();
@@ -584,7 +642,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       if (tid < N) {
         const float sum = (sh.stat[0][tid] + sh.stat[1][tid]) + (sh.stat[2][tid] + sh.stat[3][tid]);
         sh.alpha[tid] = whole ? 1.f / sum : 1.f;
-        if (!whole && tid < heads) a.part_ml[size_t(slot) * ((a.num_heads + 1) / 2 * 2) + h0 + tid] = make_float2(sh.mref[tid], sum);
+        if (!whole) a.part_ml[(size_t(slot) * a.head_blocks + hb) * N + tid] = make_float2(sh.mref[tid], sum);
       }
       if (tid == 0 && hb == 0 && !whole && walk.first == 0) {
         // the ranges that hold the rest of this sequence: up to the one with its last tile
@@ -593,12 +651,13 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         while ((r + 1) * total / used <= last) ++r;
         while (r * total / used > last) --r;
         a.desc[range] = make_int2(walk.s, int(r));
+        open = true;
       }
       latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
       softmax_sync();
       tc_fence_after();
       T* const out = static_cast<T*>(a.out) + (size_t(walk.s) * a.num_heads + h0) * kLatentDim;
-      float* const part = a.part_o + (size_t(slot) * a.num_heads + h0) * kLatentDim + warp * 32 + lane;
+      float* const part = a.part_o + (size_t(slot) * a.head_blocks + hb) * N * kLatentDim + warp * 32 + lane;
 #pragma unroll 1
       for (int j = 0; j < kLatentDim / 128; ++j) {
         float o[2][16];
@@ -623,8 +682,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (16 * c + i < heads) part[(16 * c + i) * kLatentDim + j * 128] = x[i];
+            for (int i = 0; i < 16; ++i) part[(16 * c + i) * kLatentDim + j * 128] = x[i];  // (padding heads too)
           }
         }
       }
@@ -634,13 +692,6 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   }
   // A range without a sequence that goes on past it says so.
   if (tid == 0 && hb == 0) {
-    LatentWalk w;
-    w.s = sh.first_seq;
-    w.at = begin;
-    w.end = end;
-    w.base = sh.first_tile;
-    bool open = false;
-    while (w.next(a)) open = w.first == 0 && w.last < w.n;
     if (!open) a.desc[range] = make_int2(-1, 0);
   }
   tc_fence_before();
@@ -652,21 +703,24 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
 }
 
 // Joins the pieces of the sequence that starts in a range and goes on past it:
-// out = sum_i w_i o_i / sum_i w_i l_i with w_i = 2^(m_i - max m). One head per
-// CTA: the weights of all pieces first, then two halves of the CTA take every
-// other piece, 4 dims per thread, several pieces' loads in flight.
-template <typename T>
+// out = sum_i w_i o_i / sum_i w_i l_i with w_i = 2^(m_i - max m). A CTA takes one
+// head, all its dims or (Z = 4, few sequences of many pieces) a quarter of them:
+// the weights of all pieces first, then 2 Z groups of threads take every 2 Z-th
+// piece, 4 dims per thread, with several pieces' loads in flight.
+template <typename T, int N, int Z>
 __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
+  constexpr int LANES = kLatentDim / 4 / Z, GROUPS = 256 / LANES;
   __shared__ float weight[kLatentSms], red[8];
-  __shared__ float4 other[128];
+  __shared__ float4 other[GROUPS - 1][LANES];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r0 = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, half = tid >> 7, d = (tid & 127) * 4;
+  const int r0 = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, group = tid / LANES;
+  const int d = (int(blockIdx.z) * LANES + tid % LANES) * 4;
   const int2 desc = __ldcg(a.desc + r0);
   if (desc.x < 0) return;
-  const int n = desc.y - r0 + 1, stride = (a.num_heads + 1) / 2 * 2;
-  auto slot = [&](int i) { return size_t(2) * (r0 + i) + (i == 0 ? 1 : 0); };
+  const int n = desc.y - r0 + 1, hb = h / a.block_heads, row = hb * N + h - hb * a.block_heads;
+  auto slot = [&](int i) { return (size_t(2) * (r0 + i) + (i == 0 ? 1 : 0)) * a.head_blocks * N + row; };
   float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < n) ml = __ldcg(&a.part_ml[slot(tid) * stride + h]);
+  if (tid < n) ml = __ldcg(a.part_ml + slot(tid));
   float M = ml.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
@@ -688,21 +742,27 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
   for (int i = 1; i < 8; ++i) den += red[i];
   float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = half; i < n; i += 2) {
-    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + (slot(i) * a.num_heads + h) * kLatentDim + d));
+  for (int i = group; i < n; i += GROUPS) {
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * kLatentDim + d));
     const float wi = weight[i];
     num.x = fmaf(wi, o.x, num.x);
     num.y = fmaf(wi, o.y, num.y);
     num.z = fmaf(wi, o.z, num.z);
     num.w = fmaf(wi, o.w, num.w);
   }
-  if (half) other[tid & 127] = num;
+  if (group) other[group - 1][tid % LANES] = num;
   __syncthreads();
-  if (half) return;
-  const float4 x = other[tid];
+  if (group) return;
+#pragma unroll
+  for (int i = 0; i < GROUPS - 1; ++i) {
+    const float4 x = other[i][tid];
+    num.x += x.x;
+    num.y += x.y;
+    num.z += x.z;
+    num.w += x.w;
+  }
   const float inv = 1.f / den;
-  const uint2 v = make_uint2(pack2<T>((num.x + x.x) * inv, (num.y + x.y) * inv),
-                             pack2<T>((num.z + x.z) * inv, (num.w + x.w) * inv));
+  const uint2 v = make_uint2(pack2<T>(num.x * inv, num.y * inv), pack2<T>(num.z * inv, num.w * inv));
   *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(desc.x) * a.num_heads + h) * kLatentDim + d) = v;
 }
 
