@@ -60,10 +60,10 @@ cudaError_t launch_n(LatentArgs a, const LatentShape& p, const CUtensorMap& cach
                    stream, a, cache_map, q_map);
   if (err != cudaSuccess) return err;
   if (p.ranges == 1) return cudaSuccess;  // one range: nothing crosses
-  const unsigned ranges = unsigned(p.ranges), heads = unsigned(a.num_heads);
-  if (a.num_seqs <= p.ranges / 4)  // four or more pieces a sequence
-    return launch_pdl(latent_merge_kernel<T, N, 4>, dim3(ranges, heads, 4), dim3(256), 0, stream, a);
-  return launch_pdl(latent_merge_kernel<T, N, 1>, dim3(ranges, heads), dim3(256), 0, stream, a);
+  const unsigned items = unsigned(a.desc_by_seq ? a.num_seqs : p.ranges), heads = unsigned(a.num_heads);
+  if (int64_t(items) * heads <= 2 * kLatentSms)  // few heads to join, of many pieces each
+    return launch_pdl(latent_merge_kernel<T, N, 4>, dim3(items, heads, 4), dim3(256), 0, stream, a);
+  return launch_pdl(latent_merge_kernel<T, N, 1>, dim3(items, heads), dim3(256), 0, stream, a);
 }
 
 template <typename T>
@@ -72,6 +72,7 @@ cudaError_t launch_t(LatentArgs a, const CUtensorMap& cache_map, const CUtensorM
   a.ranges = p.ranges;
   a.head_blocks = p.blocks;
   a.block_heads = p.heads;
+  a.desc_by_seq = a.num_seqs <= p.ranges;
   a.desc = static_cast<int2*>(a.workspace);
   a.part_ml = reinterpret_cast<float2*>(static_cast<char*>(a.workspace) + latent_desc_bytes(p.ranges));
   a.part_o = reinterpret_cast<float*>(a.part_ml + size_t(2) * p.ranges * p.blocks * p.n);

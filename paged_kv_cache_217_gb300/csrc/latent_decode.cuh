@@ -23,10 +23,11 @@
 // read the zero fill. The ring holds two tiles; a block's place is free as soon
 // as its 16 tokens have entered O^T.
 //
-// Warps: 0-3 softmax and output, 4 copies, 5 MMA issue. The MMA warp issues
-// S^T of the next tile when its rows have landed, else O^T of the current one
-// when its weights are there: with slow rows the ring drains early, with slow
-// products the softmax of tile i overlaps S^T of tile i + 1. Measured issue
+// Warps: 0-7 softmax and output (two of every quarter of tensor memory's lanes,
+// each with half of the heads), 8 copies, 9 MMA issue. The MMA warp issues O^T
+// of the current tile as soon as its weights are there (it frees the ring), also
+// in the middle of S^T of the next, which it issues when its rows have landed:
+// the softmax of tile i overlaps S^T of tile i + 1. Measured issue
 // cost per MMA (M 64: 23 cycles at N 16, 32 at N 64; M 128: 39 and 48) against
 // 16 and 32 cycles to read the A operand at 128 bytes a cycle.
 // The running maximum is a reference that moves only when a score exceeds it
@@ -53,7 +54,8 @@ namespace pkv {
 
 constexpr int kLatentSms = 152;       // CTAs a wave holds (one per SM of a GB300)
 constexpr int kLatentTile = 64;       // tokens per tile
-constexpr int kLatentThreads = 192;
+constexpr int kLatentSoftmax = 256;   // threads of the softmax warps
+constexpr int kLatentThreads = kLatentSoftmax + 64;
 constexpr float kLatentLazy = 8.f;
 constexpr int kLatentAhead = 2;       // tiles between a copy and the prefetch of a later one
 constexpr int kLatentAtom = 1024;                        // 8 rows x 128 bytes
@@ -61,6 +63,9 @@ constexpr int kLatentGroup = kLatentRow / 64 * kLatentAtom;  // 8 tokens: 9 atom
 constexpr int kLatentBlockBytes = 2 * kLatentGroup;      // 16 tokens
 constexpr int kLatentTileBytes = 4 * kLatentBlockBytes;
 
+// Descriptors of the sequences that cross ranges: one per sequence {first range,
+// last range} where there are at most as many sequences as ranges, else one per
+// range {sequence that starts in it and goes on, last range}; -1: none.
 inline size_t latent_desc_bytes(int ranges) { return (size_t(ranges) * sizeof(int2) + 15) / 16 * 16; }
 
 template <int N>
@@ -109,24 +114,18 @@ __device__ __forceinline__ void tc_ld_16x16(uint32_t addr, float* r) {
                : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
                : "r"(addr));
 }
-// 32 lanes (one a thread) x 16 columns.
-__device__ __forceinline__ void tc_ld_32x16(uint32_t addr, float* r) {
+// 32 lanes (one a thread) x 8 columns.
+__device__ __forceinline__ void tc_ld_32x8(uint32_t addr, float* r) {
   uint32_t* u = reinterpret_cast<uint32_t*>(r);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
-        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-      : "r"(addr));
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+               : "r"(addr));
 }
-__device__ __forceinline__ void tc_st_32x16(uint32_t addr, const float* r) {
+__device__ __forceinline__ void tc_st_32x8(uint32_t addr, const float* r) {
   const uint32_t* u = reinterpret_cast<const uint32_t*>(r);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(addr),
-      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(u[0]),
+               "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -167,14 +166,24 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// Barrier of the four softmax warps.
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool softmax_any(bool v) {
+// 16 lanes x 8 columns.
+__device__ __forceinline__ void tc_ld_16x8(uint32_t addr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void stsm_x2_trans(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+// Barrier of the four softmax warps of one half of the heads.
+__device__ __forceinline__ void softmax_sync(int half) { asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory"); }
+__device__ __forceinline__ bool softmax_any(int half, bool v) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(v ? 1u : 0u)
+      : "r"(1 + half), "r"(v ? 1u : 0u)
       : "memory");
   return r != 0;
 }
@@ -286,12 +295,12 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     }
     mbar_init(smem_addr(&sh.q_full), 1);
     mbar_init(smem_addr(&sh.q_empty), 1);
-    mbar_init(smem_addr(&sh.p_full), 128);
+    mbar_init(smem_addr(&sh.p_full), kLatentSoftmax);
     mbar_init(smem_addr(&sh.pv_done), 1);
     mbar_init_fence();
     sh.stop = 0;
   }
-  if (warp == 5) {
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
                  "r"(uint32_t(C::TMEM_COLS))
                  : "memory");
@@ -343,6 +352,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     if (latent_len(a, s) > 0) continue;
     uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + size_t(s) * a.num_heads * kLatentDim);
     for (int i = tid; i < a.num_heads * kLatentDim / 8; i += kLatentThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0 && a.desc_by_seq) a.desc[s] = make_int2(-1, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -353,7 +363,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   volatile int* stop = &sh.stop;
   bool open = false;  // (thread 0) the range's last sequence starts in it and goes on past it
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ---- copies ----
     int tile = 0, seg = 0;
     int next_seq = -1, next_ids = 0;
@@ -445,7 +455,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       }
       if (seg > 0) mbar_wait_bounded(smem_addr(&sh.q_full), (seg - 1) & 1, 10000000ull);
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ---- MMA issue: one lane ----
     if (elect_one()) {
       constexpr uint32_t id_s = tc_idesc<T>(kLatentTile, N, false), id_o = tc_idesc<T>(128, N, true);
@@ -461,35 +471,41 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         walk.next(a);
         t = walk.first;
       }
+      // O^T of tile pv, if its weights are there
+      auto outputs = [&]() {
+        if (pv >= qk || !mbar_try_wait(smem_addr(&sh.p_full), pv & 1)) return false;
+        tc_fence_after();
+        const uint64_t val = val_desc + (pv & 1) * (kLatentTileBytes >> 4);
+        const bool first = (starts >> (pv & 1)) & 1u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // 16 tokens: one block
+#pragma unroll
+          for (int j = 0; j < 4; ++j)  // 128 dims
+            tc_mma(tmem + j * N, val + k * (kLatentBlockBytes >> 4) + j * (2 * kLatentAtom >> 4), p_desc + 2 * k, id_o,
+                   !(first && k == 0));
+          tc_commit(smem_addr(&sh.block_empty[4 * (pv & 1) + k]));
+        }
+        tc_commit(smem_addr(&sh.pv_done));
+        ++pv;
+        return true;
+      };
       unsigned long long idle = 0;
       while (pv < n) {
-        // O^T first: it frees the ring
-        if (pv < qk && mbar_try_wait(smem_addr(&sh.p_full), pv & 1)) {
-          tc_fence_after();
-          const uint64_t val = val_desc + (pv & 1) * (kLatentTileBytes >> 4);
-          const bool first = (starts >> (pv & 1)) & 1u;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 16 tokens: one block
-#pragma unroll
-            for (int j = 0; j < 4; ++j)  // 128 dims
-              tc_mma(tmem + j * N, val + k * (kLatentBlockBytes >> 4) + j * (2 * kLatentAtom >> 4), p_desc + 2 * k, id_o,
-                     !(first && k == 0));
-            tc_commit(smem_addr(&sh.block_empty[4 * (pv & 1) + k]));
-          }
-          tc_commit(smem_addr(&sh.pv_done));
-          ++pv;
+        if (outputs()) {
           idle = 0;
         } else if (qk < n && qk < pv + 2 &&  // (S^T's buffer: O^T of tile qk - 2 is issued)
                    mbar_try_wait(smem_addr(&sh.tile_full[qk & 1]), (qk >> 1) & 1) &&
-            (!seg_first || mbar_try_wait(smem_addr(&sh.q_full), seg & 1))) {
+                   (!seg_first || mbar_try_wait(smem_addr(&sh.q_full), seg & 1))) {
           tc_fence_after();
           const uint32_t d = tmem + 4 * N + (qk & 1) * N;
           const uint64_t key = key_desc + (qk & 1) * (kLatentTileBytes >> 4);
 #pragma unroll
-          for (int c = 0; c < kLatentRow / 64; ++c)
+          for (int c = 0; c < kLatentRow / 64; ++c) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               tc_mma(d, key + c * (kLatentAtom >> 4) + 2 * k, q_desc + c * (N * 128 >> 4) + 2 * k, id_s, c + k > 0);
+            if (c == 2 || c == 5) outputs();
+          }
           tc_commit(smem_addr(&sh.s_full[qk & 1]));
           starts = (starts & ~(1u << (qk & 1))) | (uint32_t(seg_first) << (qk & 1));
           seg += seg_first ? 1 : 0;
@@ -522,9 +538,12 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     __syncwarp();
   } else {
     // ---- softmax and output ----
-    constexpr int G8 = N / 8;  // groups of 8 heads: this thread keeps heads 8 i + 2 t, + 1
-    const int t = lane & 3, gr = lane >> 2;
-    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    // Warps w and w + 4 read lanes 32 (w % 4) .. of tensor memory (tokens 16 (w %
+    // 4) .. + 15 of S^T, dims 32 (w % 4) .. + 31 of each product of O^T), for
+    // heads HALF (w / 4) .. . This thread keeps heads 8 i + 2 t, + 1 of its half.
+    constexpr int HALF = N / 2, G8 = HALF / 8;
+    const int t = lane & 3, gr = lane >> 2, quarter = warp & 3, half = warp >> 2, hs = half * HALF;
+    const uint32_t lanes = uint32_t(quarter * 32) << 16;
     // (After a wait gave up, `stop` lets every later wait return at once: these
     // warps then run out their loops, together and without further waiting.)
     int tile = 0;
@@ -536,11 +555,16 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         latent_wait(smem_addr(&sh.s_full[tile & 1]), (tile >> 1) & 1, stop, a.status);
         tc_fence_after();
         float x[G8][4];  // rows gr (0, 1) and gr + 8 (2, 3) of this warp's 16 tokens
+        const uint32_t s_at = tmem + lanes + 4 * N + (tile & 1) * N + hs;
+        if constexpr (G8 == 1) {
+          tc_ld_16x8(s_at, &x[0][0]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < G8; i += 2) tc_ld_16x16(tmem + lanes + 4 * N + (tile & 1) * N + 8 * i, &x[i][0]);
+          for (int i = 0; i < G8; i += 2) tc_ld_16x16(s_at + 8 * i, &x[i][0]);
+        }
         tc_wait_ld();
         const int left = walk.L - u * kLatentTile;  // tokens of this tile
-        const bool on0 = 16 * warp + gr < left, on1 = 16 * warp + gr + 8 < left;
+        const bool on0 = 16 * quarter + gr < left, on1 = 16 * quarter + gr + 8 < left;
         bool move = false;
 #pragma unroll
         for (int i = 0; i < G8; ++i)
@@ -550,7 +574,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
             x[i][2 + e] = on1 ? x[i][2 + e] * a.scale_log2 : -INFINITY;
             move |= fmaxf(x[i][e], x[i][2 + e]) > m[i][e] + kLatentLazy;
           }
-        const bool moving = softmax_any(move);
+        const bool moving = softmax_any(half, move);
         if (moving) {
 #pragma unroll
           for (int i = 0; i < G8; ++i)
@@ -559,23 +583,23 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
               float v = fmaxf(x[i][e], x[i][2 + e]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-              if (gr == 0) sh.stat[warp][8 * i + 2 * t + e] = v;
+              if (gr == 0) sh.stat[quarter][hs + 8 * i + 2 * t + e] = v;
             }
-          softmax_sync();
+          softmax_sync(half);
 #pragma unroll
           for (int i = 0; i < G8; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int h = 8 * i + 2 * t + e;
+              const int h = hs + 8 * i + 2 * t + e;
               const float v = fmaxf(fmaxf(fmaxf(sh.stat[0][h], sh.stat[1][h]), fmaxf(sh.stat[2][h], sh.stat[3][h])),
                                     m[i][e]);
               // a head without a score yet has nothing to rescale
               const float al = m[i][e] == -INFINITY ? 0.f : fast_exp2(m[i][e] - v);
               m[i][e] = v;
               l[i][e] *= al;
-              if (warp == 0 && gr == 0) sh.alpha[h] = al;
+              if (quarter == 0 && gr == 0) sh.alpha[h] = al;
             }
-          softmax_sync();
+          softmax_sync(half);
         }
         float p[G8][4];
 #pragma unroll
@@ -592,13 +616,16 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         if (moving && u > walk.first) {
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4 * N; c += 16) {
-            float o[16];
-            tc_ld_32x16(tmem + lanes + c, o);
-            tc_wait_ld();
+          for (int j = 0; j < kLatentDim / 128; ++j) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] *= sh.alpha[(c + i) % N];
-            tc_st_32x16(tmem + lanes + c, o);
+            for (int c = 0; c < HALF; c += 8) {
+              float o[8];
+              tc_ld_32x8(tmem + lanes + j * N + hs + c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] *= sh.alpha[hs + c + i];
+              tc_st_32x8(tmem + lanes + j * N + hs + c, o);
+            }
           }
           tc_wait_st();
         }
@@ -606,19 +633,27 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
           // rows past the end hold whatever the block holds (NaN included): as
           // values they must be zeros
           const int dead = min(kLatentTile, (left + kBlock - 1) / kBlock * kBlock) - left;
-          for (int i = tid; i < dead * (kLatentDim / 8); i += 128) {
+          for (int i = tid; i < dead * (kLatentDim / 8); i += kLatentSoftmax) {
             const int v = i % (kLatentDim / 8), r = left + i / (kLatentDim / 8);
             *reinterpret_cast<uint4*>(ring + (tile & 1) * kLatentTileBytes + r / 8 * kLatentGroup + v / 8 * kLatentAtom +
                                       r % 8 * 128 + v % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
+        // P: row a head, 16-byte chunk 8 tokens. Matrix b = lane / 8: tokens 8 (b &
+        // 1), heads 8 (i + b / 2); its row lane % 8 a head.
+        const int b = lane >> 3, chunk = 2 * quarter + (b & 1);
+        if constexpr (G8 == 1) {
+          const int head = hs + (lane & 7);
+          stsm_x2_trans(smem_addr(p_mem) + head * 128 + ((chunk ^ (head & 7)) << 4), pack2<T>(p[0][0], p[0][1]),
+                        pack2<T>(p[0][2], p[0][3]));
+        } else {
 #pragma unroll
-        for (int i = 0; i < G8; i += 2) {
-          // matrix lane / 8: tokens 8 (b & 1), heads 8 (i + b / 2); row lane % 8 a head
-          const int b = lane >> 3, head = 8 * (i + (b >> 1)) + (lane & 7), chunk = 2 * warp + (b & 1);
-          stsm_x4_trans(smem_addr(p_mem) + head * 128 + ((chunk ^ (head & 7)) << 4), pack2<T>(p[i][0], p[i][1]),
-                        pack2<T>(p[i][2], p[i][3]), pack2<T>(p[i + 1][0], p[i + 1][1]),
-                        pack2<T>(p[i + 1][2], p[i + 1][3]));
+          for (int i = 0; i < G8; i += 2) {
+            const int head = hs + 8 * (i + (b >> 1)) + (lane & 7);
+            stsm_x4_trans(smem_addr(p_mem) + head * 128 + ((chunk ^ (head & 7)) << 4), pack2<T>(p[i][0], p[i][1]),
+                          pack2<T>(p[i][2], p[i][3]), pack2<T>(p[i + 1][0], p[i + 1][1]),
+                          pack2<T>(p[i + 1][2], p[i + 1][3]));
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
@@ -632,71 +667,78 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l[i][e] += __shfl_xor_sync(kFull, l[i][e], o);
           if (gr == 0) {
-            sh.stat[warp][8 * i + 2 * t + e] = l[i][e];
-            if (warp == 0) sh.mref[8 * i + 2 * t + e] = m[i][e];
+            sh.stat[quarter][hs + 8 * i + 2 * t + e] = l[i][e];
+            if (quarter == 0) sh.mref[hs + 8 * i + 2 * t + e] = m[i][e];
           }
         }
       const bool whole = walk.first == 0 && walk.last == walk.n;
       const int slot = 2 * range + (walk.first == 0 ? 1 : 0);
-      softmax_sync();
-      if (tid < N) {
-        const float sum = (sh.stat[0][tid] + sh.stat[1][tid]) + (sh.stat[2][tid] + sh.stat[3][tid]);
-        sh.alpha[tid] = whole ? 1.f / sum : 1.f;
-        if (!whole) a.part_ml[(size_t(slot) * a.head_blocks + hb) * N + tid] = make_float2(sh.mref[tid], sum);
+      softmax_sync(half);
+      const int th = tid & 127;
+      if (th < HALF) {
+        const int h = hs + th;
+        const float sum = (sh.stat[0][h] + sh.stat[1][h]) + (sh.stat[2][h] + sh.stat[3][h]);
+        sh.alpha[h] = 1.f / sum;
+        if (!whole) a.part_ml[(size_t(slot) * a.head_blocks + hb) * N + h] = make_float2(sh.mref[h], sum);
       }
-      if (tid == 0 && hb == 0 && !whole && walk.first == 0) {
+      if (tid == 0 && hb == 0 && walk.first == 0) {
         // the ranges that hold the rest of this sequence: up to the one with its last tile
-        const long long last = walk.base + walk.n - 1;
-        long long r = last * used / total;
-        while ((r + 1) * total / used <= last) ++r;
-        while (r * total / used > last) --r;
-        a.desc[range] = make_int2(walk.s, int(r));
-        open = true;
+        int2 d = make_int2(-1, 0);
+        if (!whole) {
+          const long long last = walk.base + walk.n - 1;
+          long long r = last * used / total;
+          while ((r + 1) * total / used <= last) ++r;
+          while (r * total / used > last) --r;
+          d = a.desc_by_seq ? make_int2(range, int(r)) : make_int2(walk.s, int(r));
+          open = true;
+        }
+        if (a.desc_by_seq) a.desc[walk.s] = d;
+        else if (!whole) a.desc[range] = d;
       }
       latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
-      softmax_sync();
+      softmax_sync(half);
       tc_fence_after();
-      T* const out = static_cast<T*>(a.out) + (size_t(walk.s) * a.num_heads + h0) * kLatentDim;
-      float* const part = a.part_o + (size_t(slot) * a.head_blocks + hb) * N * kLatentDim + warp * 32 + lane;
+      T* const out = static_cast<T*>(a.out) + (size_t(walk.s) * a.num_heads + h0 + hs) * kLatentDim;
+      float* const part = a.part_o + ((size_t(slot) * a.head_blocks + hb) * N + hs) * kLatentDim + quarter * 32 + lane;
 #pragma unroll 1
       for (int j = 0; j < kLatentDim / 128; ++j) {
-        float o[2][16];
-        tc_ld_32x16(tmem + lanes + j * N, o[0]);
+        float o[2][8];
+        tc_ld_32x8(tmem + lanes + j * N + hs, o[0]);
 #pragma unroll
-        for (int c = 0; c < N / 16; ++c) {
+        for (int c = 0; c < HALF / 8; ++c) {
           tc_wait_ld();
-          if (c + 1 < N / 16) tc_ld_32x16(tmem + lanes + j * N + 16 * (c + 1), o[(c + 1) & 1]);
-          float(&x)[16] = o[c & 1];
+          if (c + 1 < HALF / 8) tc_ld_32x8(tmem + lanes + j * N + hs + 8 * (c + 1), o[(c + 1) & 1]);
+          float(&x)[8] = o[c & 1];
           if (whole) {
             // two heads a step: even lanes take the first one's dims lane, lane +
             // 1, odd lanes the second one's dims lane - 1, lane
-            const int dim = j * 128 + warp * 32 + (lane & ~1);
+            const int dim = j * 128 + quarter * 32 + (lane & ~1);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float e = x[i] * sh.alpha[16 * c + i], f = x[i + 1] * sh.alpha[16 * c + i + 1];
+            for (int i = 0; i < 8; i += 2) {
+              const float e = x[i] * sh.alpha[hs + 8 * c + i], f = x[i + 1] * sh.alpha[hs + 8 * c + i + 1];
               const float g = __shfl_xor_sync(kFull, lane & 1 ? e : f, 1);
-              const int h = 16 * c + i + (lane & 1);
-              if (h < heads)
+              const int h = 8 * c + i + (lane & 1);
+              if (hs + h < heads)
                 *reinterpret_cast<uint32_t*>(out + size_t(h) * kLatentDim + dim) =
                     lane & 1 ? pack2<T>(g, f) : pack2<T>(e, g);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) part[(16 * c + i) * kLatentDim + j * 128] = x[i];  // (padding heads too)
+            for (int i = 0; i < 8; ++i) part[(8 * c + i) * kLatentDim + j * 128] = x[i];  // (padding heads too)
           }
         }
       }
-      tc_fence_before();  // the next segment's O^T comes after these reads
-      softmax_sync();     // statistics are read: the next segment may write them
+      tc_fence_before();   // the next segment's O^T comes after these reads
+      softmax_sync(half);  // statistics are read: the next segment may write them
     }
   }
   // A range without a sequence that goes on past it says so.
   if (tid == 0 && hb == 0) {
-    if (!open) a.desc[range] = make_int2(-1, 0);
+    if (!open && !a.desc_by_seq) a.desc[range] = make_int2(-1, 0);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(uint32_t(C::TMEM_COLS)));
   }
@@ -713,10 +755,11 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
   __shared__ float weight[kLatentSms], red[8];
   __shared__ float4 other[GROUPS - 1][LANES];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int r0 = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, group = tid / LANES;
+  const int h = blockIdx.y, tid = threadIdx.x, group = tid / LANES;
   const int d = (int(blockIdx.z) * LANES + tid % LANES) * 4;
-  const int2 desc = __ldcg(a.desc + r0);
+  const int2 desc = __ldcg(a.desc + blockIdx.x);
   if (desc.x < 0) return;
+  const int r0 = a.desc_by_seq ? desc.x : int(blockIdx.x), s = a.desc_by_seq ? int(blockIdx.x) : desc.x;
   const int n = desc.y - r0 + 1, hb = h / a.block_heads, row = hb * N + h - hb * a.block_heads;
   auto slot = [&](int i) { return (size_t(2) * (r0 + i) + (i == 0 ? 1 : 0)) * a.head_blocks * N + row; };
   float2 ml = make_float2(-INFINITY, 0.f);
@@ -763,7 +806,7 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
   }
   const float inv = 1.f / den;
   const uint2 v = make_uint2(pack2<T>(num.x * inv, num.y * inv), pack2<T>(num.z * inv, num.w * inv));
-  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(desc.x) * a.num_heads + h) * kLatentDim + d) = v;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_heads + h) * kLatentDim + d) = v;
 }
 
 }  // namespace pkv

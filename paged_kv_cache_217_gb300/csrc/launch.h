@@ -109,7 +109,7 @@ struct LatentArgs {
   int num_blocks;
   float scale_log2;  // scale * log2(e)
   // set by the launcher: work ranges, blocks of heads, heads per block, and the workspace's parts
-  int ranges, head_blocks, block_heads;
+  int ranges, head_blocks, block_heads, desc_by_seq;
   int2* desc;
   float2* part_ml;
   float* part_o;
