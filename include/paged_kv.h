@@ -558,27 +558,23 @@ pkv_status_t pkv_copy_blocks_int4(
 /*
  * Decode over the 4-bit cache: pkv_paged_attention_decode with every K and V
  * row read as z + c s (in fp32, not rounded to T). q and out are T = dtype.
- * sliding_window as for pkv_paged_attention_decode_sliding (<= 0: none).
- * partition_size 0, -1 or N > 0; the balanced (-2) and shared-prefix (-5)
- * schedules return PKV_ERR_UNSUPPORTED. Workspace:
- * pkv_paged_attention_workspace_size, or with a window
- * pkv_paged_attention_sliding_workspace_size, with the same arguments.
+ * sliding_window as for pkv_paged_attention_decode_sliding (<= 0: none). One
+ * schedule for all batches: the batch's tiles are cut into equal shares
+ * whatever the lengths, so there is no partition size and no launch plan.
+ * Workspace: pkv_int4_workspace_size bytes for the same arguments (16-byte
+ * aligned, NULL when that is 0), without initialisation; calls that use one
+ * workspace must not overlap on the GPU. The same inputs give the same bits.
  */
 pkv_status_t pkv_paged_attention_decode_int4(
     void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
     const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
     int head_dim, int max_blocks_per_seq, int num_blocks, float scale,
-    pkv_dtype_t dtype, int sliding_window, int partition_size, void* workspace,
-    size_t workspace_bytes, pkv_stream_t stream);
+    pkv_dtype_t dtype, int sliding_window, void* workspace, size_t workspace_bytes,
+    pkv_stream_t stream);
 
-/* The same without a window, with the launch plan that pkv_paged_attention_plan
- * left in `workspace` (see pkv_paged_attention_decode_int8_planned). */
-pkv_status_t pkv_paged_attention_decode_int4_planned(
-    void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
-    const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
-    int head_dim, int max_blocks_per_seq, int num_blocks, float scale,
-    pkv_dtype_t dtype, int partition_size, void* workspace,
-    size_t workspace_bytes, pkv_stream_t stream);
+size_t pkv_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads,
+                               int head_dim, int max_blocks_per_seq,
+                               int sliding_window);
 
 /* ------------------------------------------------------------------------ */
 /* Latent attention: one shared row per token                                */

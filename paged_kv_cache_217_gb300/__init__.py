@@ -21,6 +21,7 @@ from .binding import (  # noqa: F401
     extend_block_tables,
     gather_cache_int4,
     int4_tile_bytes,
+    int4_workspace_size,
     latent_cache_write,
     latent_workspace_size,
     paged_attention_decode,

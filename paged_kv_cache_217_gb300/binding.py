@@ -78,10 +78,8 @@ _SIGS = {
     "pkv_reshape_and_cache_int4": ([_c_p, _c_p, _c_int, _c_p, _c_p] + [_c_int] * 4 + [_c_p], _c_int),
     "pkv_gather_cache_int4": ([_c_p, _c_p, _c_int, _c_p, _c_p] + [_c_int] * 4 + [_c_p], _c_int),
     "pkv_copy_blocks_int4": ([_c_p, _c_p] + [_c_int] * 4 + [_c_p], _c_int),
-    "pkv_paged_attention_decode_int4": ([_c_p] * 5 + [_c_int] * 6 + [_c_f, _c_int, _c_int, _c_int, _c_p, _c_sz, _c_p],
-                                        _c_int),
-    "pkv_paged_attention_decode_int4_planned": ([_c_p] * 5 + [_c_int] * 6 + [_c_f, _c_int, _c_int, _c_p, _c_sz, _c_p],
-                                                _c_int),
+    "pkv_paged_attention_decode_int4": ([_c_p] * 5 + [_c_int] * 6 + [_c_f, _c_int, _c_int, _c_p, _c_sz, _c_p], _c_int),
+    "pkv_int4_workspace_size": ([_c_int] * 6, _c_sz),
     "pkv_latent_cache_write": ([_c_p, _c_p, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_int, _c_int, _c_p], _c_int),
     "pkv_copy_blocks_latent": ([_c_p, _c_p, _c_int, _c_int, _c_p], _c_int),
     "pkv_paged_latent_decode": ([_c_p] * 5 + [_c_int] * 4 + [_c_f, _c_int, _c_p, _c_sz, _c_p], _c_int),
@@ -512,14 +510,19 @@ def copy_blocks_int4(kv_cache, src_dst_pairs):
             src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], hkv, tile // 18, nb)
 
 
+def int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sliding_window=0):
+    return int(lib().pkv_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                             sliding_window))
+
+
 def paged_attention_decode_int4(out, q, kv_cache, block_tables, context_lens, scale, sliding_window=0,
-                                partition_size=0, workspace=None, planned=False):
+                                workspace=None):
     """paged_attention_decode over the 4-bit cache (K and V read as offset + code * scale per 64 head dims).
 
     q, out: [S, Hq, D] of the dtype the cache was written from; kv_cache: uint8
     [num_blocks, Hkv, 18 * D]. ``sliding_window`` > 0 attends over the last
-    tokens only; ``planned`` (without a window) uses the launch plan that
-    paged_attention_plan left in the same workspace."""
+    tokens only. ``workspace`` (uint8 CUDA tensor of int4_workspace_size bytes)
+    overrides the binding's own."""
     import torch
     _need_cuda(out, q, kv_cache, block_tables, context_lens)
     dt = _dtype_code(q)
@@ -534,23 +537,16 @@ def paged_attention_decode_int4(out, q, kv_cache, block_tables, context_lens, sc
             or tuple(context_lens.shape) != (q.shape[0],):
         raise ValueError("shape mismatch among out, q, kv_cache, block_tables and context_lens")
     window = max(0, int(sliding_window))
-    if planned and window:
-        raise ValueError("a planned call takes no sliding window")
     S, Hq, D = q.shape
     nb, hkv = kv_cache.shape[0], kv_cache.shape[1]
     mb = block_tables.shape[1]
-    need = sliding_workspace_size(S, Hq, hkv, D, mb, window, partition_size)
-    if workspace is None and need:
-        workspace = _workspace(q.device, need) if planned else _scratch(q.device, need)
+    need = int4_workspace_size(S, Hq, hkv, D, mb, window)
+    if workspace is None:
+        workspace = _scratch(q.device, need)
     ws_ptr, ws_bytes = _ptr_bytes(workspace if need else None)
-    args = (out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Hq,
-            hkv, D, mb, nb, float(scale), dt)
-    if planned:
-        _launch(q.device, "paged_attention_decode_int4_planned", lib().pkv_paged_attention_decode_int4_planned, *args,
-                int(partition_size), ws_ptr, ws_bytes)
-    else:
-        _launch(q.device, "paged_attention_decode_int4", lib().pkv_paged_attention_decode_int4, *args, window,
-                int(partition_size), ws_ptr, ws_bytes)
+    _launch(q.device, "paged_attention_decode_int4", lib().pkv_paged_attention_decode_int4, out.data_ptr(),
+            q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Hq, hkv, D, mb, nb,
+            float(scale), dt, window, ws_ptr, ws_bytes)
     return out
 
 

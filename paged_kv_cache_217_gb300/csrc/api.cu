@@ -878,88 +878,6 @@ pkv_status_t pkv_paged_attention_decode_int8_planned(void* out, const void* q, c
 
 namespace {
 
-pkv_status_t decode_int4_impl(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
-                              const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
-                              int head_dim, int max_blocks_per_seq, int num_blocks, float scale, pkv_dtype_t dtype,
-                              int window, int partition_size, void* workspace, size_t workspace_bytes, bool planned,
-                              cudaStream_t stream) {
-  if (num_seqs < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs < 0");
-  if (num_seqs == 0) return pkv::ok();
-  if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
-    return pkv::fail(PKV_ERR_INVALID_ARG, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
-                     num_q_heads, num_kv_heads);
-  const int group = num_q_heads / num_kv_heads;
-  if (group > 8) return pkv::fail(PKV_ERR_UNSUPPORTED, "query heads per KV head %d > 8", group);
-  if (!supported_head_dim(head_dim)) return pkv::fail(PKV_ERR_UNSUPPORTED, "head_dim %d (64, 128 or 256)", head_dim);
-  if (dtype != PKV_F16 && dtype != PKV_BF16) return pkv::fail(PKV_ERR_UNSUPPORTED, "dtype %d", int(dtype));
-  if (max_blocks_per_seq <= 0 || num_blocks <= 0)
-    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq and num_blocks must be > 0");
-  if (num_seqs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
-  if (!std::isfinite(scale)) return pkv::fail(PKV_ERR_INVALID_ARG, "scale is not finite");
-  if (!out || !q || !kv_cache || !block_tables || !context_lens)
-    return pkv::fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
-  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(kv_cache, 16))
-    return pkv::fail(PKV_ERR_INVALID_ARG, "out, q and kv_cache must be 16-byte aligned");
-  if (!aligned(block_tables, 4) || !aligned(context_lens, 4))
-    return pkv::fail(PKV_ERR_INVALID_ARG, "block_tables and context_lens must be 4-byte aligned");
-  const int plan_blocks = window_blocks(max_blocks_per_seq, window);
-  const int p = choose_partition(num_seqs, num_q_heads, num_kv_heads, head_dim, plan_blocks, partition_size);
-  if (p == kBalanced || p == kSharedPrefix)
-    return pkv::fail(PKV_ERR_UNSUPPORTED, "the 4-bit cache has no balanced or shared-prefix schedule");
-  Plan plan;
-  pkv_status_t st = plan_decode(plan_blocks, p, &plan);
-  if (st != PKV_OK) return st;
-  const SplitLayout lay = split_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, plan.max_parts);
-  const size_t ord = plan_bytes(num_seqs, num_kv_heads, plan.max_parts);
-  const size_t need = lay.total + ord;
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
-    return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
-                     need, workspace_bytes, workspace);
-  unsigned int* status = nullptr;
-  st = status_word(&status);
-  if (st != PKV_OK) return st;
-
-  pkv::DecodeArgs a{};
-  a.out = out;
-  a.q = q;
-  a.k_pool = kv_cache;
-  a.block_tables = block_tables;
-  a.context_lens = context_lens;
-  a.part_o = lay.total > 0 ? static_cast<float*>(workspace) : nullptr;
-  a.part_ml = lay.total > 0 ? reinterpret_cast<float2*>(static_cast<char*>(workspace) + lay.ml_offset) : nullptr;
-  a.counters = lay.total > 0 ? reinterpret_cast<unsigned int*>(static_cast<char*>(workspace) + lay.counter_offset)
-                             : nullptr;
-  int4* plan_hdr = ord > 0 ? reinterpret_cast<int4*>(static_cast<char*>(workspace) + lay.total) : nullptr;
-  const bool make_plan = plan_hdr && !planned && num_seqs >= kOrderKernelMinSeqs;
-  const bool use_plan = plan_hdr && (planned || make_plan);
-  a.order = use_plan ? reinterpret_cast<const int32_t*>(plan_hdr + 1) : nullptr;
-  a.plan = use_plan ? plan_hdr : nullptr;
-  a.status = status;
-  a.num_seqs = num_seqs;
-  a.num_q_heads = num_q_heads;
-  a.num_kv_heads = num_kv_heads;
-  a.group = group;
-  a.max_blocks_per_seq = max_blocks_per_seq;
-  a.num_blocks = num_blocks;
-  a.part_tokens = plan.part_tokens;
-  a.max_parts = plan.max_parts;
-  a.long_first = long_first_grid(num_seqs, num_kv_heads, plan.max_parts) ? 1 : 0;
-  a.window = window > 0 ? window : 0;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  cudaError_t err = cudaSuccess;
-  if (lay.total > 0) {
-    err = cudaMemsetAsync(a.counters, 0, lay.counter_bytes, stream);
-    if (err != cudaSuccess) return cuda_status(err, "clear split-K counters");
-  }
-  if (make_plan) {
-    err = pkv::launch_seq_order(context_lens, num_seqs, max_blocks_per_seq * PKV_BLOCK_SIZE, a.window, true, plan_hdr,
-                                block_tables, max_blocks_per_seq, plan_rows_of(plan_hdr, num_seqs), stream);
-    if (err != cudaSuccess) return cuda_status(err, "launch plan");
-  }
-  err = pkv::launch_decode_int4(a, dtype == PKV_BF16, head_dim, round_pow2_group(group), stream);
-  return cuda_status(err, "paged_attention_decode_int4 launch");
-}
-
 pkv_status_t cache_int4(bool gather, const char* what, const void* k, const void* v, pkv_dtype_t dtype,
                         const void* kv_cache, const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
                         int head_dim, int num_blocks, cudaStream_t stream) {
@@ -1024,26 +942,67 @@ pkv_status_t pkv_copy_blocks_int4(void* kv_cache, const int64_t* src_dst_pairs, 
                    num_blocks, stream);
 }
 
+size_t pkv_int4_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                               int sliding_window) {
+  if (num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+      !supported_head_dim(head_dim) || max_blocks_per_seq <= 0)
+    return 0;
+  return pkv::int4_workspace_bytes(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, head_dim,
+                                   window_blocks(max_blocks_per_seq, sliding_window));
+}
+
 pkv_status_t pkv_paged_attention_decode_int4(void* out, const void* q, const void* kv_cache,
                                              const int32_t* block_tables, const int32_t* context_lens, int num_seqs,
                                              int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
                                              int num_blocks, float scale, pkv_dtype_t dtype, int sliding_window,
-                                             int partition_size, void* workspace, size_t workspace_bytes,
-                                             pkv_stream_t stream) {
-  return decode_int4_impl(out, q, kv_cache, block_tables, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
-                          max_blocks_per_seq, num_blocks, scale, dtype, sliding_window, partition_size, workspace,
-                          workspace_bytes, false, stream);
-}
-
-pkv_status_t pkv_paged_attention_decode_int4_planned(void* out, const void* q, const void* kv_cache,
-                                                     const int32_t* block_tables, const int32_t* context_lens,
-                                                     int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                                                     int max_blocks_per_seq, int num_blocks, float scale,
-                                                     pkv_dtype_t dtype, int partition_size, void* workspace,
-                                                     size_t workspace_bytes, pkv_stream_t stream) {
-  return decode_int4_impl(out, q, kv_cache, block_tables, context_lens, num_seqs, num_q_heads, num_kv_heads, head_dim,
-                          max_blocks_per_seq, num_blocks, scale, dtype, 0, partition_size, workspace, workspace_bytes,
-                          true, stream);
+                                             void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_seqs < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs < 0");
+  if (num_seqs == 0) return pkv::ok();
+  if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
+                     num_q_heads, num_kv_heads);
+  const int group = num_q_heads / num_kv_heads;
+  if (group > 8) return pkv::fail(PKV_ERR_UNSUPPORTED, "query heads per KV head %d > 8", group);
+  if (!supported_head_dim(head_dim)) return pkv::fail(PKV_ERR_UNSUPPORTED, "head_dim %d (64, 128 or 256)", head_dim);
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return pkv::fail(PKV_ERR_UNSUPPORTED, "dtype %d", int(dtype));
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq and num_blocks must be > 0");
+  if (int64_t(max_blocks_per_seq) * PKV_BLOCK_SIZE > INT32_MAX / 2)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq too large");
+  if (num_seqs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
+  if (int64_t(num_blocks) * num_kv_heads > INT32_MAX || int64_t(num_seqs) * num_kv_heads > INT32_MAX ||
+      int64_t(max_blocks_per_seq) * num_kv_heads > INT32_MAX)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "num_blocks, num_seqs or max_blocks_per_seq times num_kv_heads exceeds 2^31");
+  if (!std::isfinite(scale)) return pkv::fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (!out || !q || !kv_cache || !block_tables || !context_lens)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(kv_cache, 16))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "out, q and kv_cache must be 16-byte aligned");
+  if (!aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "block_tables and context_lens must be 4-byte aligned");
+  const int blocks = window_blocks(max_blocks_per_seq, sliding_window);
+  const size_t need = pkv::int4_workspace_bytes(num_seqs, num_kv_heads, group, head_dim, blocks);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
+                     need, workspace_bytes, workspace);
+  pkv::Int4Args a{};
+  pkv_status_t st = status_word(&a.status);
+  if (st != PKV_OK) return st;
+  a.out = out;
+  a.q = q;
+  a.cache = kv_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = group;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.window = sliding_window > 0 ? sliding_window : 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return cuda_status(pkv::launch_decode_int4(a, dtype == PKV_BF16, head_dim, blocks, workspace, stream),
+                     "paged_attention_decode_int4 launch");
 }
 
 pkv_status_t pkv_latent_cache_write(const void* latent, const void* rope, int64_t latent_stride, int64_t rope_stride,

@@ -5,46 +5,79 @@
 namespace pkv {
 namespace {
 
-// Warps per CTA and stages (of two tiles) per warp. Measured on GB300, 128
-// dims: 40-head layer, 64 sequences 74.4 us with 4 warps, 78.2 with 2; 32/8
-// heads, 256 sequences 26.2 with 4, 22.8 with 2.
-template <int H>
-constexpr int i4_warps() { return H == 8 ? 2 : 4; }
 constexpr int kInt4Stages = 2;
+// Batches of at most kItemCtas items (sequences x KV heads) whose tables hold at
+// most kItemPairs pairs of tiles give each item a CTA.
+constexpr int64_t kItemCtas = 304;
+constexpr int kItemPairs = 64;
+constexpr int kMinPairs = 2;  // pairs a warp should have at least, where there are few
+
+int max_ctas(int head_dim) { return 152 * (head_dim == 256 ? 8 : 16) / kInt4Warps; }
+
+bool item_ctas(int num_seqs, int num_kv_heads, int blocks) {
+  return int64_t(num_seqs) * num_kv_heads <= kItemCtas && (blocks + 1) / 2 <= kItemPairs;
+}
+
+// CTAs of the list schedule: one wave, fewer where the tables cannot hold
+// kMinPairs pairs for every warp.
+int list_ctas(int num_seqs, int num_kv_heads, int head_dim, int blocks) {
+  const int64_t pairs = int64_t(num_seqs) * num_kv_heads * ((blocks + 1) / 2);
+  const int64_t want = (pairs + kInt4Warps * kMinPairs - 1) / (kInt4Warps * kMinPairs);
+  return want < max_ctas(head_dim) ? int(want) : max_ctas(head_dim);
+}
 
 template <typename T, int D, int H>
-cudaError_t launch_int4_dh(const DecodeArgs& a, cudaStream_t stream) {
-  using C = I4Cfg<D, i4_warps<H>(), kInt4Stages>;
-  auto kern = paged_decode_int4_kernel<T, D, H, i4_warps<H>(), kInt4Stages>;
+cudaError_t launch_int4_dh(const Int4Args& a, cudaStream_t stream) {
+  using C = I4Cfg<D, H, kInt4Warps, kInt4Stages>;
+  static_assert(C::SMEM_BYTES <= 227 * 1024 * kInt4Warps / i4_warps_per_sm<D>() - 1024, "CTAs per SM");
+  static_assert(sizeof(I4Shared<kInt4Warps>) <= kInt4Warps * 36, "shared state");
+  auto kern = paged_decode_int4_kernel<T, D, H, kInt4Warps, kInt4Stages>;
   static bool configured[kMaxDevices] = {};
   cudaError_t err = configure_once(kern, C::SMEM_BYTES, configured);
   if (err != cudaSuccess) return err;
-  const dim3 grid(unsigned(a.num_kv_heads), unsigned(a.num_seqs), unsigned(a.max_parts));
-  err = launch_pdl(kern, grid, dim3(i4_warps<H>() * 32), C::SMEM_BYTES, stream, a);
-  if (err != cudaSuccess) return err;
-  return cudaGetLastError();
+  err = launch_pdl(kern, dim3(unsigned(a.ctas)), dim3(kInt4Warps * 32), C::SMEM_BYTES, stream, a);
+  if (err != cudaSuccess || a.item_ctas || a.ctas == 1) return err;
+  return launch_pdl(int4_merge_kernel<T, D>, dim3(unsigned(a.ctas), unsigned(a.group)), dim3(256), 0, stream, a);
 }
 
 template <typename T, int D>
-cudaError_t launch_int4_d(const DecodeArgs& a, int gpad, cudaStream_t stream) {
-  return gpad <= 2 ? launch_int4_dh<T, D, 2>(a, stream) : launch_int4_dh<T, D, 8>(a, stream);
+cudaError_t launch_int4_d(const Int4Args& a, cudaStream_t stream) {
+  return a.group <= 2 ? launch_int4_dh<T, D, 2>(a, stream) : launch_int4_dh<T, D, 8>(a, stream);
 }
 
 template <typename T>
-cudaError_t launch_int4_t(const DecodeArgs& a, int head_dim, int gpad, cudaStream_t stream) {
+cudaError_t launch_int4_t(const Int4Args& a, int head_dim, cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return launch_int4_d<T, 64>(a, gpad, stream);
-    case 128: return launch_int4_d<T, 128>(a, gpad, stream);
-    case 256: return launch_int4_d<T, 256>(a, gpad, stream);
+    case 64: return launch_int4_d<T, 64>(a, stream);
+    case 128: return launch_int4_d<T, 128>(a, stream);
+    case 256: return launch_int4_d<T, 256>(a, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_decode_int4(const DecodeArgs& a, bool bf16, int head_dim, int gpad, cudaStream_t stream) {
-  return bf16 ? launch_int4_t<__nv_bfloat16>(a, head_dim, gpad, stream)
-              : launch_int4_t<__half>(a, head_dim, gpad, stream);
+// Descriptors {item, last CTA} per CTA, then two partial results per CTA: (max,
+// sum) and fp32 rows of every query head of a group.
+size_t int4_workspace_bytes(int num_seqs, int num_kv_heads, int group, int head_dim, int blocks) {
+  if (item_ctas(num_seqs, num_kv_heads, blocks)) return 0;
+  const size_t ctas = size_t(list_ctas(num_seqs, num_kv_heads, head_dim, blocks));
+  return (ctas * sizeof(int2) + 15) / 16 * 16 + (2 * ctas * group * sizeof(float2) + 15) / 16 * 16 +
+         2 * ctas * group * head_dim * sizeof(float);
+}
+
+cudaError_t launch_decode_int4(Int4Args a, bool bf16, int head_dim, int blocks, void* workspace, cudaStream_t stream) {
+  a.item_ctas = item_ctas(a.num_seqs, a.num_kv_heads, blocks) ? 1 : 0;
+  a.ctas = a.item_ctas ? a.num_seqs * a.num_kv_heads : list_ctas(a.num_seqs, a.num_kv_heads, head_dim, blocks);
+  if (!a.item_ctas) {
+    char* w = static_cast<char*>(workspace);
+    a.desc = reinterpret_cast<int2*>(w);
+    w += (size_t(a.ctas) * sizeof(int2) + 15) / 16 * 16;
+    a.part_ml = reinterpret_cast<float2*>(w);
+    w += (size_t(2) * a.ctas * a.group * sizeof(float2) + 15) / 16 * 16;
+    a.part_o = reinterpret_cast<float*>(w);
+  }
+  return bf16 ? launch_int4_t<__nv_bfloat16>(a, head_dim, stream) : launch_int4_t<__half>(a, head_dim, stream);
 }
 
 }  // namespace pkv

@@ -28,7 +28,8 @@
 //    The fp32 sums of each group are then multiplied by s and joined by
 //    z * sum q.
 //  * O^T += C_V^T P~: head dims on M, tokens on K, fp16. V words of tokens t
-//    and t + 4 (t + 8 and t + 12) are merged by halves and masked as above.
+//    and t + 4 (t + 8 and t + 12) are merged by halves and masked: 10
+//    instructions for 16 codes (nibble_sums).
 //    P~ = p s 2^e rounded to fp16 once (2^-11 relative, far below the codes'
 //    own step), e a power of two per warp that keeps P~ below 2^15; the score
 //    fragment becomes the weight operand through movmatrix. The offsets' part
@@ -38,25 +39,47 @@
 //    cross-lane maximum and no rescaling. Sums and the accumulator are fp32.
 // One bulk copy (18 D bytes, contiguous) brings a tile; each warp runs its own
 // ring of stages of two tiles.
+//
+// Work: the batch's tile pairs, by sequence, KV head and position, are one list,
+// cut into equal ranges for the CTAs and their warps; a warp streams its range
+// without a pause, its ring filled across items, so that a short sequence costs
+// no start-up of its own. An item (sequence, KV head) inside one warp's range is
+// written from registers; the pieces of one that spans warps meet in shared
+// memory, of one that spans CTAs in the workspace (int4_merge_kernel). Small
+// batches instead give each item a CTA of its own, without that second kernel.
+// One CTA per item for all batches started up for 3.5 us an item: 74.4 us against
+// INT4_MHA_US for 40 heads and 64 sequences, 22.8 against INT4_GQA_US for 8 KV
+// heads and 256 short ones.
 #pragma once
 
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "decode.cuh"
-#include "decode_mma.cuh"
+#include "device_common.cuh"
 #include "int4_layout.cuh"
+#include "launch.h"
 
 namespace pkv {
 
-template <int D, int NW, int STAGES>
+template <int D, int H, int NW, int STAGES>
 struct I4Cfg {
-  static constexpr int GROUPS = D / kInt4Group;
   static constexpr int TILE_BYTES = kv4_tile_bytes(D);
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
+  static constexpr int PIECE_FLOATS = H * (D + 2);  // acc[H][D], m[H], l[H] of a piece
   static constexpr size_t RING_BYTES = size_t(NW) * STAGES * STAGE_BYTES;
-  static constexpr size_t SMEM_BYTES = RING_BYTES + size_t(NW) * STAGES * 8;
+  static constexpr size_t PIECE_BYTES = size_t(NW) * PIECE_FLOATS * sizeof(float);
+  static constexpr size_t BAR_BYTES = size_t(NW) * STAGES * 8;
+  static constexpr size_t SMEM_BYTES = RING_BYTES + PIECE_BYTES + BAR_BYTES + NW * 36;
+  static_assert(PIECE_FLOATS * 4 <= STAGES * STAGE_BYTES, "a piece fits a warp's ring");
+  static_assert(PIECE_FLOATS % 4 == 0, "pieces are 16-byte aligned");
 };
+
+// Warps that an SM holds (registers: 128 a thread, 255 at head_dim 256).
+template <int D>
+constexpr int i4_warps_per_sm() { return D == 256 ? 8 : 16; }
+constexpr int kInt4Warps = 8;                       // per CTA
+constexpr int kInt4MaxCtas = 152 * 16 / kInt4Warps;  // one wave of a GB300
 
 // Scores past the reference by more than this move it.
 constexpr float kInt4Lazy = 8.f;
@@ -97,6 +120,17 @@ __device__ __forceinline__ float2 pair_of<__nv_bfloat16>(uint32_t u) {
 template <>
 __device__ __forceinline__ float2 pair_of<__half>(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// A word of two tokens' halves (nibbles 0..3 of each) as fp16 pairs in units of
+// 2^-24: n0, n0 + 16 n1, n2, n2 + 16 n3. The upper nibbles are never taken
+// alone: the products of n0 + 16 n1 less those of n0 are 16 times theirs, which
+// the epilogue sorts out once (16 integer instructions fewer per 32 tokens).
+__device__ __forceinline__ void nibble_sums(uint32_t w, uint32_t (&p)[4]) {
+  p[0] = w & 0x000f000fu;
+  p[1] = w & 0x00ff00ffu;
+  p[3] = __byte_perm(w, 0, 0x4341);  // (w >> 8) & 0x00ff00ff
+  p[2] = p[3] & 0x000f000fu;
 }
 
 // A word's eight nibbles as fp16 pairs: (0, 4) and (2, 6) times 2^-24, (1, 5)
@@ -247,7 +281,7 @@ __device__ __forceinline__ void i4_query(const T* q0, int group, int lane, float
 template <int D, int H>
 struct I4State {
   static constexpr int PL = I4Heads<H>::PER_LANE;
-  float o[D / 16][4];            // O^T fragments, in units of 2^-24 (2^-20 for odd ones) / vmul
+  float o[D / 16][4];            // O^T fragments in units of 2^-24 / vmul; odd ones hold even + 16 * odd nibbles
   float z[D / kInt4Group][PL];   // this lane's part of sum p z
   float m[PL], l[PL];            // reference maximum (log2 domain), this lane's part of sum p
   float vbound, vmul;            // P~ = p s vmul, for s below vbound
@@ -439,8 +473,8 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // nibbles 0..3, then 4..7
         uint32_t ab[4], cd[4];
-        nibbles(__byte_perm(wa[g], wb[g], h ? 0x7632 : 0x5410), ab);
-        nibbles(__byte_perm(wc[g], wd[g], h ? 0x7632 : 0x5410), cd);
+        nibble_sums(__byte_perm(wa[g], wb[g], h ? 0x7632 : 0x5410), ab);
+        nibble_sums(__byte_perm(wc[g], wd[g], h ? 0x7632 : 0x5410), cd);
         float(&o0)[4] = st.o[4 * g + 2 * h];
         float(&o1)[4] = st.o[4 * g + 2 * h + 1];
         mma_f16(o0, ab[0], ab[2], cd[0], cd[2], pb[0], pb[1], o0[0], o0[1], o0[2], o0[3]);
@@ -450,131 +484,73 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
   }
 }
 
-// Publishes a warp's (acc[H][D], m[H], l[H]) in head-dim order, powers of two
-// taken out: row gr of fragment 4 g + 2 h + b is dim 64 g + 8 gr + 4 h + b, row
-// gr + 8 the dim after the next.
+// Sums over a quad's rows what the warp keeps by lane.
 template <int D, int H>
-__device__ __forceinline__ void i4_publish(float* wsm, I4State<D, H>& st, int lane) {
-  using HL = I4Heads<H>;
-  constexpr int GROUPS = D / kInt4Group, PL = HL::PER_LANE;
-  const int t = lane & 3, gr = lane >> 2;
+__device__ __forceinline__ void i4_reduce(I4State<D, H>& st) {
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
 #pragma unroll
-    for (int c = 0; c < PL; ++c) {
+    for (int c = 0; c < I4Heads<H>::PER_LANE; ++c) {
       st.l[c] += __shfl_xor_sync(kFull, st.l[c], off);
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g) st.z[g][c] += __shfl_xor_sync(kFull, st.z[g][c], off);
-    }
-  }
-  const float even = 0x1p24f / st.vmul, odd = 0x1p20f / st.vmul;
-  if (H == 2 && (t & 1)) return;  // its neighbour holds the same head
-#pragma unroll
-  for (int c = 0; c < PL; ++c) {
-    const int head = HL::head(t, c);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const int dim = 64 * (i / 4) + 8 * gr + 4 * ((i / 2) & 1) + (i & 1);
-      const float f = i & 1 ? odd : even;
-      wsm[head * D + dim] = fmaf(st.o[i][c], f, st.z[i / 4][c]);
-      wsm[head * D + dim + 2] = fmaf(st.o[i][2 + c], f, st.z[i / 4][c]);
-    }
-    if (gr == 0) {
-      wsm[H * D + head] = st.m[c];
-      wsm[H * D + H + head] = st.l[c];
+      for (int g = 0; g < D / kInt4Group; ++g) st.z[g][c] += __shfl_xor_sync(kFull, st.z[g][c], off);
     }
   }
 }
 
-template <typename T, int D, int H, int NW, int STAGES>
-// (128 registers: 16 warps per SM)
-__global__ void __launch_bounds__(NW * 32, D <= 128 ? 16 / NW : 0) paged_decode_int4_kernel(const DecodeArgs a) {
-  using C = I4Cfg<D, NW, STAGES>;
-  static_assert(size_t(2 * H + H * D) * 4 <= size_t(STAGES) * C::STAGE_BYTES, "merge area fits the ring");
-  extern __shared__ __align__(1024) unsigned char smem[];
-  wait_for_predecessor();
-  const int g = blockIdx.x, part = blockIdx.z;
-  const int s = long_first_seq<NW>(a, blockIdx.y);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hq0 = g * a.group;
-
-  // Without a window the first 32 block ids of this warp's tile pairs do not
-  // depend on the length: read them together with it.
-  int ids_early = 0;
-  if (a.window == 0) {
-    const int j0 = (part * a.part_tokens) / kBlock + 2 * (warp + (lane >> 1) * NW) + (lane & 1);
-    if (j0 < a.max_blocks_per_seq) ids_early = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + j0);
-  }
-  int L = a.context_lens[s];
-  const int max_len = a.max_blocks_per_seq * kBlock;
-  if (L < 0 || L > max_len) {
-    if (threadIdx.x == 0 && part == 0 && g == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-    L = L < 0 ? 0 : max_len;
-  }
-  const TokenRange tr = token_range(L, a.window);
-  const int nparts = L == 0 ? 1 : (L - tr.aligned + a.part_tokens - 1) / a.part_tokens;
-  if (part >= nparts) return;
-  if (L == 0) {
-    T* o = static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + hq0) * D;
-    for (int i = threadIdx.x; i < a.group * D / 8; i += NW * 32)
-      reinterpret_cast<uint4*>(o)[i] = make_uint4(0u, 0u, 0u, 0u);
-    return;
-  }
-  const int t0 = tr.aligned + part * a.part_tokens;
-  const int ntok = min(L, t0 + a.part_tokens) - t0;
-  const int nb = (ntok + kBlock - 1) / kBlock;
-  const int head = part == 0 ? tr.first - tr.aligned : 0;
-
-  unsigned char* ring = smem + size_t(warp) * STAGES * C::STAGE_BYTES;
-  const uint32_t ring_s = smem_addr(ring);
-  const uint32_t bar_s = smem_addr(smem + C::RING_BYTES) + warp * STAGES * 8;
-  if (lane == 0) {
+// The reduced state's values of column c: calls f(dim, four values of dims dim ..
+// dim + 3). Row gr of fragment 4 g + 2 h is dim 64 g + 8 gr + 4 h, of the next
+// one the dim after it, row gr + 8 two dims on.
+template <int D, int H, typename F>
+__device__ __forceinline__ void i4_values(const I4State<D, H>& st, int c, int gr, F f) {
+  const float even = 0x1p24f / st.vmul, odd = 0x1p20f / st.vmul;
 #pragma unroll
-    for (int st = 0; st < STAGES; ++st) mbar_init(bar_s + 8 * st, 1);
-    mbar_init_fence();
+  for (int i = 0; i < D / 16; i += 2) {
+    const float z = st.z[i / 4][c];
+    f(64 * (i / 4) + 8 * gr + 4 * ((i / 2) & 1),
+      make_float4(fmaf(st.o[i][c], even, z), fmaf(st.o[i + 1][c] - st.o[i][c], odd, z), fmaf(st.o[i][2 + c], even, z),
+                  fmaf(st.o[i + 1][2 + c] - st.o[i][2 + c], odd, z)));
   }
-  __syncwarp();
+}
 
-  // Tile pairs of this warp: warp + k NW, k < n_my. Lanes 2 (k % 16), + 1 of
-  // `ids` hold the blocks of pair k (batches of 16, the next one prefetched).
-  const int npairs = (nb + 1) / 2;
-  const int n_my = npairs > warp ? (npairs - warp + NW - 1) / NW : 0;
-  const int32_t* trow = a.block_tables + size_t(s) * a.max_blocks_per_seq + t0 / kBlock;
-  auto load_ids = [&](int batch) -> int {
-    const int j = 2 * (warp + (batch * 16 + (lane >> 1)) * NW) + (lane & 1);
-    if (j >= nb) return 0;
-    const int id = batch == 0 && a.window == 0 ? ids_early : __ldg(trow + j);
-    if (id >= 0 && id < a.num_blocks) return id;
-    flag(a.status, PKV_DEV_BAD_BLOCK_ID);
-    return 0;
-  };
-  int ids = load_ids(0);
-  int ids_next = n_my > 16 ? load_ids(1) : 0;
-  int id_batch = 0;
-  const unsigned char* base = static_cast<const unsigned char*>(a.k_pool) + size_t(g) * C::TILE_BYTES;
-  const size_t block_stride = size_t(a.num_kv_heads) * C::TILE_BYTES;
-  auto issue = [&](int k) {  // warp-uniform; k increases by one per call
-    if ((k >> 4) != id_batch) {
-      ids = ids_next;
-      ++id_batch;
-      ids_next = (id_batch + 1) * 16 < n_my ? load_ids(id_batch + 1) : 0;
+// A piece of an item in shared memory: acc[H][D], m[H], l[H].
+template <int D, int H>
+__device__ __forceinline__ void i4_publish(float* piece, I4State<D, H>& st, int lane) {
+  using HL = I4Heads<H>;
+  const int t = lane & 3, gr = lane >> 2;
+  i4_reduce<D, H>(st);
+  if (H == 2 && (t & 1)) return;  // its neighbour holds the same head
+#pragma unroll
+  for (int c = 0; c < HL::PER_LANE; ++c) {
+    const int head = HL::head(t, c);
+    i4_values<D, H>(st, c, gr, [&](int dim, const float4& v) { *reinterpret_cast<float4*>(piece + head * D + dim) = v; });
+    if (gr == 0) {
+      piece[H * D + head] = st.m[c];
+      piece[H * D + H + head] = st.l[c];
     }
-    const int id0 = __shfl_sync(kFull, ids, 2 * (k & 15)), id1 = __shfl_sync(kFull, ids, 2 * (k & 15) + 1);
-    if (lane == 0) {
-      const int st = k % STAGES;
-      const uint32_t bar = bar_s + 8 * st, dst = ring_s + st * C::STAGE_BYTES;
-      const bool both = 2 * (warp + k * NW) + 1 < nb;
-      mbar_arrive_expect_tx(bar, both ? C::STAGE_BYTES : C::TILE_BYTES);
-      bulk_g2s(dst, base + size_t(id0) * block_stride, C::TILE_BYTES, bar);
-      if (both) bulk_g2s(dst + C::TILE_BYTES, base + size_t(id1) * block_stride, C::TILE_BYTES, bar);
-    }
-  };
-  const int pre = n_my < STAGES ? n_my : STAGES;
-  for (int k = 0; k < pre; ++k) issue(k);
+  }
+}
 
-  I4Query<D, H> q;
-  i4_query<T, D, H>(static_cast<const T*>(a.q) + (size_t(s) * a.num_q_heads + hq0) * D, a.group, lane, a.scale_log2, q);
-  I4State<D, H> st;
+// A whole item's output rows.
+template <typename T, int D, int H>
+__device__ __forceinline__ void i4_write(T* out, int group, I4State<D, H>& st, int lane) {
+  using HL = I4Heads<H>;
+  const int t = lane & 3, gr = lane >> 2;
+  i4_reduce<D, H>(st);
+#pragma unroll
+  for (int c = 0; c < HL::PER_LANE; ++c) {
+    const int head = HL::head(t, c);
+    if (head >= group || (H == 2 && (t & 1))) continue;
+    const float inv = 1.f / st.l[c];
+    i4_values<D, H>(st, c, gr, [&](int dim, const float4& v) {
+      T x[4] = {T(v.x * inv), T(v.y * inv), T(v.z * inv), T(v.w * inv)};
+      *reinterpret_cast<uint2*>(out + size_t(head) * D + dim) = *reinterpret_cast<const uint2*>(x);
+    });
+  }
+}
+
+template <int D, int H>
+__device__ __forceinline__ void i4_clear(I4State<D, H>& st) {
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
 #pragma unroll
@@ -582,35 +558,404 @@ __global__ void __launch_bounds__(NW * 32, D <= 128 ? 16 / NW : 0) paged_decode_
     st.m[e] = -INFINITY;
     st.l[e] = 0.f;
 #pragma unroll
-    for (int i = 0; i < C::GROUPS; ++i) st.z[i][e] = 0.f;
+    for (int i = 0; i < D / kInt4Group; ++i) st.z[i][e] = 0.f;
   }
   st.vbound = 0x1p-98f;
   st.vmul = 0x1p105f;
+}
 
-  for (int k = 0; k < n_my; ++k) {
-    const int stage = k % STAGES;
-    const bool ok = mbar_wait_bounded(bar_s + 8 * stage, (k / STAGES) & 1);
-    if (!__all_sync(kFull, ok)) {
-      // a copy never completed: record it, wait (bounded) for the others in flight, stop consuming
-      if (lane == 0) flag(a.status, PKV_DEV_WAIT_TIMEOUT);
-      const int last = min(n_my, k + STAGES);
-      for (int kk = k; kk < last; ++kk) mbar_wait_bounded(bar_s + 8 * (kk % STAGES), (kk / STAGES) & 1);
-      break;
+// ---- work ---------------------------------------------------------------------
+// A sequence's tiles and pairs of tiles (with a sliding window those that it
+// touches).
+struct I4Seq {
+  int L, t0, nt, np, head;  // length, first tile, tiles, pairs, rows of the first tile before the window
+};
+__device__ __forceinline__ int i4_len(const Int4Args& a, int s) {
+  const int L = __ldg(a.context_lens + s), most = a.max_blocks_per_seq * kBlock;
+  return L < 0 ? 0 : L > most ? most : L;
+}
+__device__ __forceinline__ I4Seq i4_seq(const Int4Args& a, int L) {
+  const TokenRange tr = token_range(L, a.window);
+  I4Seq q;
+  q.L = L;
+  q.t0 = tr.aligned / kBlock;
+  q.nt = (L + kBlock - 1) / kBlock - q.t0;
+  q.np = (q.nt + 1) / 2;
+  q.head = tr.first - tr.aligned;
+  return q;
+}
+
+template <int NW>
+struct I4Shared {
+  long long scan[NW], base[NW];  // per warp: where its first sequence starts in the list
+  int seq[NW], len[NW];          // ... that sequence and its length
+  int fitem[NW], fend[NW], litem[NW];
+};
+
+constexpr int kInt4NoPiece = -1, kInt4NoWork = -2;
+
+// Joins pieces (piece(i), i < n) of one item: output rows, or a partial result
+// for the merge across CTAs. One warp.
+template <typename T, int D, int H, typename P>
+__device__ __forceinline__ void i4_join(const Int4Args& a, int item, int n, P piece, int slot, int lane) {
+  const int s = item / a.num_kv_heads, g = item - s * a.num_kv_heads;
+  for (int h = 0; h < a.group; ++h) {
+    float M = -INFINITY;
+    for (int i = 0; i < n; ++i) M = fmaxf(M, piece(i)[H * D + h]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    for (int d = 4 * lane; d < D; d += 128) {
+      float den = 0.f;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < n; ++i) {
+        const float* p = piece(i);
+        const float w = fast_exp2(p[H * D + h] - ref);
+        const float4 x = *reinterpret_cast<const float4*>(p + h * D + d);
+        den = fmaf(w, p[H * D + H + h], den);
+        num.x = fmaf(w, x.x, num.x);
+        num.y = fmaf(w, x.y, num.y);
+        num.z = fmaf(w, x.z, num.z);
+        num.w = fmaf(w, x.w, num.w);
+      }
+      if (slot < 0) {
+        const float inv = 1.f / den;
+        T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + g * a.group + h) * D + d) =
+            *reinterpret_cast<const uint2*>(x);
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (size_t(slot) * a.group + h) * D + d) = num;
+        if (d == 0) a.part_ml[size_t(slot) * a.group + h] = make_float2(M, den);
+      }
     }
-    const int j = 2 * (warp + k * NW);
-    const int rows = ntok - j * kBlock;
-    const int lo = j == 0 ? head : 0;
-    const uint32_t at = ring_s + stage * C::STAGE_BYTES;
-    if (rows >= 2 * kBlock && lo == 0)
-      i4_step<T, D, H, false>(at, 0, 2 * kBlock, q, st, lane);
-    else
-      i4_step<T, D, H, true>(at, lo, rows, q, st, lane);
-    __syncwarp();
-    if (k + STAGES < n_my) issue(k + STAGES);
   }
-  i4_publish<D, H>(reinterpret_cast<float*>(ring), st, lane);
+}
+
+template <typename T, int D, int H, int NW, int STAGES>
+__global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_decode_int4_kernel(const Int4Args a) {
+  using C = I4Cfg<D, H, NW, STAGES>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  I4Shared<NW>& sh = *reinterpret_cast<I4Shared<NW>*>(smem + C::RING_BYTES + C::PIECE_BYTES + C::BAR_BYTES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const int Hkv = a.num_kv_heads;
+  unsigned char* ring = smem + size_t(warp) * STAGES * C::STAGE_BYTES;
+  float* const first_piece = reinterpret_cast<float*>(smem + C::RING_BYTES) + warp * C::PIECE_FLOATS;
+  const uint32_t ring_s = smem_addr(ring);
+  const uint32_t bar_s = smem_addr(smem + C::RING_BYTES + C::PIECE_BYTES) + warp * STAGES * 8;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) mbar_init(bar_s + 8 * i, 1);
+    mbar_init_fence();
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // This CTA's range [cb, ce) of the list of total pairs, this warp's [wb, we),
+  // and the sequence in which the latter starts.
+  long long cb, ce, total, base;
+  int s, L;
+  auto warp_begin = [&](int w) { return cb + (ce - cb) * w / NW; };
+  if (a.item_ctas) {  // one item: the list is its own
+    s = int(blockIdx.x) / Hkv;
+    const int raw = __ldg(a.context_lens + s), g = int(blockIdx.x) - s * Hkv;
+    L = i4_len(a, s);
+    if (raw != L && g == 0 && tid == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+    const int np = i4_seq(a, L).np;
+    if (np == 0) {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + g * a.group) * D);
+      for (int i = tid; i < a.group * D / 8; i += NW * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
+    base = -(long long)g * np;
+    cb = 0;
+    ce = total = np;
+  } else {
+    // Each thread sums a run of sequences, a scan of the sums gives every run's
+    // place in the list, and the thread whose run holds a warp's first pair
+    // finds its sequence.
+    int zero_len = int(blockIdx.x) < a.num_seqs ? i4_len(a, int(blockIdx.x)) : 1;  // (read along with the others)
+    const int per = (a.num_seqs + NW * 32 - 1) / (NW * 32);
+    const int run0 = min(a.num_seqs, tid * per), run1 = min(a.num_seqs, run0 + per);
+    long long mine = 0;
+    for (int i = run0; i < run1; ++i) {
+      const int raw = __ldg(a.context_lens + i), len = i4_len(a, i);
+      if (raw != len && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+      mine += (long long)i4_seq(a, len).np * Hkv;
+    }
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) sh.scan[warp] = upto;
+    __syncthreads();
+    long long before = upto - mine;
+    total = 0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      if (i < warp) before += sh.scan[i];
+      total += sh.scan[i];
+    }
+    cb = int(blockIdx.x) * total / a.ctas;
+    ce = (int(blockIdx.x) + 1) * total / a.ctas;
+    for (int w = 0; w < NW; ++w) {
+      const long long x = warp_begin(w);
+      if (x < before || x >= before + mine) continue;
+      long long at = before;
+      for (int i = run0;; ++i) {
+        const int len = i4_len(a, i);
+        const long long n = (long long)i4_seq(a, len).np * Hkv;
+        if (at + n > x) {
+          sh.seq[w] = i;
+          sh.len[w] = len;
+          sh.base[w] = at;
+          break;
+        }
+        at += n;
+      }
+    }
+    // Sequences without tokens: zeros, spread over the CTAs.
+    for (int i = int(blockIdx.x); i < a.num_seqs;) {
+      if (zero_len == 0) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + size_t(i) * a.num_q_heads * D);
+        for (int j = tid; j < a.num_q_heads * D / 8; j += NW * 32) o[j] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      i += int(gridDim.x);
+      if (i < a.num_seqs) zero_len = i4_len(a, i);
+    }
+    __syncthreads();
+    s = sh.seq[warp];
+    L = sh.len[warp];
+    base = sh.base[warp];
+  }
+  const long long wb = warp_begin(warp), we = warp_begin(warp + 1);
+  int item = 0, ahead = 0;  // the item at hand; the next sequence's length
+  I4Seq sq{};
+  int g = 0, pr = 0;        // its KV head, the pair at hand
+  int fitem = kInt4NoWork, fend = 0, litem = kInt4NoWork;
+  if (wb < we) {
+    fitem = litem = kInt4NoPiece;
+    sq = i4_seq(a, L);
+    g = int((wb - base) / sq.np);
+    pr = int(wb - base - (long long)g * sq.np);
+    if (!a.item_ctas && s + 1 < a.num_seqs) ahead = i4_len(a, s + 1);
+
+    // Copies: lanes 2 (k % 16), + 1 of `tiles` hold the pool tiles of the warp's
+    // k-th pair (batches of 16, the next one read ahead; -1: none). Each lane
+    // walks the list by itself.
+    int cs = s, cL = L;
+    long long cbase = base;
+    auto load_tiles = [&](int batch) -> int {
+      const long long x = wb + batch * 16 + (lane >> 1);
+      if (x >= we) return -1;
+      I4Seq c = i4_seq(a, cL);
+      while (x >= cbase + (long long)c.np * Hkv) {
+        cbase += (long long)c.np * Hkv;
+        cL = i4_len(a, ++cs);
+        c = i4_seq(a, cL);
+      }
+      const int at = int(x - cbase), cg = at / c.np, j = 2 * (at - cg * c.np) + (lane & 1);
+      if (j >= c.nt) return -1;
+      int id = __ldg(a.block_tables + size_t(cs) * a.max_blocks_per_seq + c.t0 + j);
+      if (id < 0 || id >= a.num_blocks) {
+        flag(a.status, PKV_DEV_BAD_BLOCK_ID);
+        id = 0;
+      }
+      return id * Hkv + cg;
+    };
+    const int n_my = int(we - wb);
+    int tiles = load_tiles(0), tiles_next = n_my > 16 ? load_tiles(1) : -1, batch = 0;
+    auto issue = [&](int k) {  // warp-uniform; k increases by one per call
+      if ((k >> 4) != batch) {
+        tiles = tiles_next;
+        ++batch;
+        tiles_next = (batch + 1) * 16 < n_my ? load_tiles(batch + 1) : -1;
+      }
+      const int i0 = __shfl_sync(kFull, tiles, 2 * (k & 15)), i1 = __shfl_sync(kFull, tiles, 2 * (k & 15) + 1);
+      if (lane == 0) {
+        const int st = k % STAGES;
+        const uint32_t bar = bar_s + 8 * st, dst = ring_s + st * C::STAGE_BYTES;
+        const unsigned char* cache = static_cast<const unsigned char*>(a.cache);
+        mbar_arrive_expect_tx(bar, i1 >= 0 ? C::STAGE_BYTES : C::TILE_BYTES);
+        bulk_g2s(dst, cache + size_t(i0) * C::TILE_BYTES, C::TILE_BYTES, bar);
+        if (i1 >= 0) bulk_g2s(dst + C::TILE_BYTES, cache + size_t(i1) * C::TILE_BYTES, C::TILE_BYTES, bar);
+      }
+    };
+    for (int k = 0; k < STAGES && k < n_my; ++k) issue(k);
+
+    I4State<D, H> st;
+    int k = 0;
+    bool ok = true;
+    while (k < n_my) {
+      item = s * Hkv + g;
+      const size_t row = size_t(s) * a.num_q_heads + g * a.group;
+      I4Query<D, H> q;
+      i4_query<T, D, H>(static_cast<const T*>(a.q) + row * D, a.group, lane, a.scale_log2, q);
+      i4_clear<D, H>(st);
+      const bool mid = pr > 0;  // the item began in another warp's range
+      const int stop = min(sq.np, pr + n_my - k);
+      for (; pr < stop; ++pr, ++k) {
+        const int stage = k % STAGES;
+        ok = ok && __all_sync(kFull, mbar_wait_bounded(bar_s + 8 * stage, (k / STAGES) & 1));
+        if (!ok) break;
+        const int rows = sq.L - (sq.t0 + 2 * pr) * kBlock;
+        const int lo = pr == 0 ? sq.head : 0;
+        const uint32_t at = ring_s + stage * C::STAGE_BYTES;
+        if (rows >= 2 * kBlock && lo == 0)
+          i4_step<T, D, H, false>(at, 0, 2 * kBlock, q, st, lane);
+        else
+          i4_step<T, D, H, true>(at, lo, rows, q, st, lane);
+        __syncwarp();
+        if (k + STAGES < n_my) issue(k + STAGES);
+      }
+      if (!ok) {
+        // a copy never completed: record it, wait (bounded) for the others in flight, stop
+        if (lane == 0) flag(a.status, PKV_DEV_WAIT_TIMEOUT);
+        const int last = min(n_my, k + STAGES);
+        for (int kk = k; kk < last; ++kk) mbar_wait_bounded(bar_s + 8 * (kk % STAGES), (kk / STAGES) & 1);
+        break;
+      }
+      const bool done = pr == sq.np;
+      if (mid) {
+        i4_publish<D, H>(first_piece, st, lane);
+        fitem = item;
+        fend = done ? 1 : 0;
+      } else if (done) {
+        i4_write<T, D, H>(static_cast<T*>(a.out) + row * D, a.group, st, lane);
+      } else {  // the range ends inside the item: every copy has landed, the ring is free
+        i4_publish<D, H>(reinterpret_cast<float*>(ring), st, lane);
+        litem = item;
+      }
+      if (done && k < n_my) {
+        pr = 0;
+        if (++g == Hkv) {
+          g = 0;
+          do {  // (sequences without tokens have no place in the list)
+            base += (long long)sq.np * Hkv;
+            ++s;
+            sq = i4_seq(a, ahead);
+            ahead = s + 1 < a.num_seqs ? i4_len(a, s + 1) : 0;
+          } while (sq.np == 0);
+        }
+      }
+    }
+  }
+  if (lane == 0) {
+    sh.fitem[warp] = fitem;
+    sh.fend[warp] = fend;
+    sh.litem[warp] = litem;
+  }
   __syncthreads();
-  finish_chunk<T, D, H, NW>(a, smem, size_t(STAGES) * C::STAGE_BYTES, s, g, part, nparts);
+  // Pieces that belong together follow one another: a warp's last piece, or the
+  // CTA's first one, and the first pieces of the warps after it.
+  auto first_of = [&](int w) {
+    return reinterpret_cast<const float*>(smem + C::RING_BYTES) + w * C::PIECE_FLOATS;
+  };
+  auto join = [&](int id, const float* head, int w) {  // `head`, then first pieces from warp w on
+    const float* list[NW + 1];
+    int n = 0;
+    bool end = false;
+    if (head) list[n++] = head;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      if (i < w || end) continue;
+      if (sh.fitem[i] == kInt4NoWork) continue;
+      if (sh.fitem[i] != id) break;
+      list[n++] = first_of(i);
+      end = sh.fend[i] != 0;
+    }
+    const int slot = !head ? 2 * int(blockIdx.x) : end ? -1 : 2 * int(blockIdx.x) + 1;
+    i4_join<T, D, H>(a, id, n, [&](int i) { return list[i]; }, slot, lane);
+    return end;
+  };
+  bool open = false;
+  if (litem >= 0) open = !join(litem, reinterpret_cast<const float*>(ring), warp + 1);
+  if (warp == 0 && !a.item_ctas) {
+    // the item that began in an earlier CTA
+    int w = 0;
+    while (w < NW && sh.fitem[w] == kInt4NoWork) ++w;
+    if (w < NW && sh.fitem[w] >= 0) join(sh.fitem[w], nullptr, w);
+  }
+  if (!a.item_ctas) {
+    // the descriptor for the merge: an item that starts here and goes on, and the
+    // CTA that holds its last pair
+    if (open && lane == 0) {
+      const long long last = base + (long long)(g + 1) * sq.np - 1;
+      long long c = last * a.ctas / total;
+      while ((c + 1) * total / a.ctas <= last) ++c;
+      while (c * total / a.ctas > last) --c;
+      a.desc[blockIdx.x] = make_int2(item, int(c));
+    }
+    if (!__syncthreads_or(open) && tid == 0) a.desc[blockIdx.x] = make_int2(-1, 0);
+  }
+}
+
+// Joins the pieces of the item that starts in CTA blockIdx.x's range and goes on
+// past it, one query head per CTA here: the weights of all pieces first, then 8
+// (D = 64: 16) groups of threads take every 8th piece, 4 dims per thread.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
+  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+  __shared__ float weight[kInt4MaxCtas], red[8];
+  __shared__ float4 other[GROUPS][LANES];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c0 = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, group = tid / LANES, d = tid % LANES * 4;
+  const int2 desc = __ldcg(a.desc + c0);
+  if (desc.x < 0) return;
+  const int n = desc.y - c0 + 1;
+  auto slot = [&](int i) { return (size_t(2) * (c0 + i) + (i == 0 ? 1 : 0)) * a.group + h; };
+  float M = -INFINITY;
+  for (int i = tid; i < n; i += 256) {
+    weight[i] = __ldcg(&a.part_ml[slot(i)].x);
+    M = fmaxf(M, weight[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+  if ((tid & 31) == 0) red[tid >> 5] = M;
+  __syncthreads();
+  M = red[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) M = fmaxf(M, red[i]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float den = 0.f;
+  for (int i = tid; i < n; i += 256) {
+    const float w = fast_exp2(weight[i] - ref);
+    weight[i] = w;
+    den = fmaf(w, __ldcg(&a.part_ml[slot(i)].y), den);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
+  __syncthreads();
+  if ((tid & 31) == 0) red[tid >> 5] = den;
+  __syncthreads();
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = group; i < n; i += GROUPS) {
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D + d));
+    const float w = weight[i];
+    num.x = fmaf(w, o.x, num.x);
+    num.y = fmaf(w, o.y, num.y);
+    num.z = fmaf(w, o.z, num.z);
+    num.w = fmaf(w, o.w, num.w);
+  }
+  other[group][tid % LANES] = num;
+  __syncthreads();
+  if (group) return;
+  den = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) den += red[i];
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) {
+    const float4 x = other[i][tid];
+    num.x += x.x;
+    num.y += x.y;
+    num.z += x.z;
+    num.w += x.w;
+  }
+  const float inv = 1.f / den;
+  const int s = desc.x / a.num_kv_heads, g = desc.x - s * a.num_kv_heads;
+  T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + g * a.group + h) * D + d) =
+      *reinterpret_cast<const uint2*>(x);
 }
 
 }  // namespace pkv

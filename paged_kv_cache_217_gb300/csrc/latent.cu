@@ -63,7 +63,7 @@ cudaError_t launch_n(LatentArgs a, const LatentShape& p, const CUtensorMap& cach
   const unsigned items = unsigned(a.desc_by_seq ? a.num_seqs : p.ranges), heads = unsigned(a.num_heads);
   if (int64_t(items) * heads <= 2 * kLatentSms)  // few heads to join, of many pieces each
     return launch_pdl(latent_merge_kernel<T, N, 4>, dim3(items, heads, 4), dim3(256), 0, stream, a);
-  return launch_pdl(latent_merge_kernel<T, N, 1>, dim3(items, heads), dim3(256), 0, stream, a);
+  return launch_pdl(latent_merge_kernel<T, N, 1>, dim3(items, (heads + 1) / 2), dim3(256), 0, stream, a);
 }
 
 template <typename T>

@@ -215,7 +215,7 @@ struct LatentShared {
   uint64_t q_full, q_empty, s_full[2], p_full, pv_done;
   uint32_t tmem;
   int stop;  // a wait gave up: every role leaves
-  int first_seq;
+  int first_seq, first_len;
   long long first_tile;                      // list index of first_seq's first tile
   long long scan[kLatentThreads / 32];
   uint64_t drain;                            // after a wait gave up
@@ -245,16 +245,14 @@ struct LatentWalk {
   long long at, end;        // list index of the next segment's first tile, and the range's end
   long long base;           // list index of sequence s's first tile
   int first, last, n;       // the segment: its tiles [first, last) of the n of the sequence
-  __device__ __forceinline__ void start(const LatentArgs& a, int seq, long long tile0, long long b, long long e) {
+  __device__ __forceinline__ void start(const LatentArgs& a, int seq, int len, long long tile0, long long b,
+                                        long long e) {
     s = seq;
     base = tile0;
     at = b;
     end = e;
-    L = ahead = 0;
-    if (b < e) {
-      L = latent_len(a, s);
-      if (s + 1 < a.num_seqs) ahead = latent_len(a, s + 1);
-    }
+    L = len;
+    ahead = b < e && s + 1 < a.num_seqs ? latent_len(a, s + 1) : 0;
   }
   __device__ __forceinline__ bool next(const LatentArgs& a) {
     if (at >= end) return false;
@@ -299,6 +297,8 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     mbar_init(smem_addr(&sh.pv_done), 1);
     mbar_init_fence();
     sh.stop = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&cache_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&q_map) : "memory");
   }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
@@ -314,11 +314,14 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   // range's first tile finds its sequence.
   const int per = (a.num_seqs + kLatentThreads - 1) / kLatentThreads;
   const int run0 = min(a.num_seqs, tid * per), run1 = min(a.num_seqs, run0 + per);
+  int zero_len = int(blockIdx.x) < a.num_seqs ? latent_len(a, int(blockIdx.x)) : 1;  // (read along with the others)
   long long mine = 0;
+  int len = 0;  // of the run's last sequence
   for (int s = run0; s < run1; ++s) {
-    const int raw = __ldg(a.context_lens + s);
-    if ((raw < 0 || raw > a.max_blocks_per_seq * kBlock) && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-    mine += latent_tiles(latent_len(a, s));
+    const int raw = __ldg(a.context_lens + s), most = a.max_blocks_per_seq * kBlock;
+    if ((raw < 0 || raw > most) && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+    len = raw < 0 ? 0 : raw > most ? most : raw;
+    mine += latent_tiles(len);
   }
   long long upto = mine;  // inclusive scan over the warp, then over the warps
 #pragma unroll
@@ -339,27 +342,33 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   if (begin < end && begin >= before && begin < before + mine) {
     long long at = before;
     int s = run0;
-    for (;; ++s) {
-      const int n = latent_tiles(latent_len(a, s));
-      if (at + n > begin) break;
-      at += n;
+    if (per > 1) {
+      for (;; ++s) {
+        len = latent_len(a, s);
+        if (at + latent_tiles(len) > begin) break;
+        at += latent_tiles(len);
+      }
     }
     sh.first_seq = s;
+    sh.first_len = len;
     sh.first_tile = at;
   }
   // Sequences without tokens: zeros, spread over the CTAs.
-  for (int s = int(blockIdx.x); s < a.num_seqs; s += int(gridDim.x)) {
-    if (latent_len(a, s) > 0) continue;
-    uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + size_t(s) * a.num_heads * kLatentDim);
-    for (int i = tid; i < a.num_heads * kLatentDim / 8; i += kLatentThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (tid == 0 && a.desc_by_seq) a.desc[s] = make_int2(-1, 0);
+  for (int s = int(blockIdx.x); s < a.num_seqs;) {
+    if (zero_len == 0) {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + size_t(s) * a.num_heads * kLatentDim);
+      for (int i = tid; i < a.num_heads * kLatentDim / 8; i += kLatentThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (tid == 0 && a.desc_by_seq) a.desc[s] = make_int2(-1, 0);
+    }
+    s += int(gridDim.x);
+    if (s < a.num_seqs) zero_len = latent_len(a, s);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   LatentWalk walk;
-  walk.start(a, sh.first_seq, sh.first_tile, begin, end);
+  walk.start(a, sh.first_seq, sh.first_len, sh.first_tile, begin, end);
   volatile int* stop = &sh.stop;
   bool open = false;  // (thread 0) the range's last sequence starts in it and goes on past it
 
@@ -744,69 +753,114 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   }
 }
 
-// Joins the pieces of the sequence that starts in a range and goes on past it:
-// out = sum_i w_i o_i / sum_i w_i l_i with w_i = 2^(m_i - max m). A CTA takes one
-// head, all its dims or (Z = 4, few sequences of many pieces) a quarter of them:
-// the weights of all pieces first, then 2 Z groups of threads take every 2 Z-th
-// piece, 4 dims per thread, with several pieces' loads in flight.
+// Joins the pieces of a sequence that crosses ranges:
+// out = sum_i w_i o_i / sum_i w_i l_i with w_i = 2^(m_i - max m). A CTA takes two
+// heads (one with Z = 4). Few pieces (at most kFewPieces): one round of loads,
+// each half of the CTA a head, 4 dims per thread. Many: head after head -- the
+// weights of all pieces first, then 2 Z groups of threads take every 2 Z-th
+// piece, with several pieces' loads in flight; Z = 4 cuts the dims over 4 CTAs
+// (few heads in all).
+constexpr int kFewPieces = 8;
 template <typename T, int N, int Z>
 __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
   constexpr int LANES = kLatentDim / 4 / Z, GROUPS = 256 / LANES;
   __shared__ float weight[kLatentSms], red[8];
   __shared__ float4 other[GROUPS - 1][LANES];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int h = blockIdx.y, tid = threadIdx.x, group = tid / LANES;
-  const int d = (int(blockIdx.z) * LANES + tid % LANES) * 4;
+  const int tid = threadIdx.x;
   const int2 desc = __ldcg(a.desc + blockIdx.x);
   if (desc.x < 0) return;
   const int r0 = a.desc_by_seq ? desc.x : int(blockIdx.x), s = a.desc_by_seq ? int(blockIdx.x) : desc.x;
-  const int n = desc.y - r0 + 1, hb = h / a.block_heads, row = hb * N + h - hb * a.block_heads;
-  auto slot = [&](int i) { return (size_t(2) * (r0 + i) + (i == 0 ? 1 : 0)) * a.head_blocks * N + row; };
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < n) ml = __ldcg(a.part_ml + slot(tid));
-  float M = ml.x;
+  const int n = desc.y - r0 + 1;
+  auto slot = [&](int i, int h) {
+    const int hb = h / a.block_heads;
+    return (size_t(2) * (r0 + i) + (i == 0 ? 1 : 0)) * a.head_blocks * N + hb * N + h - hb * a.block_heads;
+  };
+  auto write = [&](int h, int d, const float4& x, float den) {
+    const float inv = 1.f / den;
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_heads + h) * kLatentDim + d) =
+        make_uint2(pack2<T>(x.x * inv, x.y * inv), pack2<T>(x.z * inv, x.w * inv));
+  };
+  if (Z == 1 && n <= kFewPieces) {
+    const int h = 2 * int(blockIdx.y) + (tid >> 7), d = (tid & 127) * 4;
+    if (h >= a.num_heads) return;
+    float2 ml[kFewPieces];
+    float4 o[kFewPieces];
+    float M = -INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
-  if ((tid & 31) == 0) red[tid >> 5] = M;
-  __syncthreads();
-  M = red[0];
+    for (int i = 0; i < kFewPieces; ++i) {
+      ml[i] = make_float2(-INFINITY, 0.f);
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        ml[i] = __ldcg(a.part_ml + slot(i, h));
+        o[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i, h) * kLatentDim + d));
+      }
+    }
 #pragma unroll
-  for (int i = 1; i < 8; ++i) M = fmaxf(M, red[i]);
-  const float w = tid < n ? fast_exp2(ml.x - (M == -INFINITY ? 0.f : M)) : 0.f;
-  if (tid < n) weight[tid] = w;
-  float den = w * ml.y;
+    for (int i = 0; i < kFewPieces; ++i) M = fmaxf(M, ml[i].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
-  __syncthreads();
-  if ((tid & 31) == 0) red[tid >> 5] = den;
-  __syncthreads();
-  den = red[0];
+    for (int i = 0; i < kFewPieces; ++i) {
+      const float w = fast_exp2(ml[i].x - ref);
+      den = fmaf(w, ml[i].y, den);
+      num.x = fmaf(w, o[i].x, num.x);
+      num.y = fmaf(w, o[i].y, num.y);
+      num.z = fmaf(w, o[i].z, num.z);
+      num.w = fmaf(w, o[i].w, num.w);
+    }
+    write(h, d, num, den);
+    return;
+  }
+  const int group = tid / LANES, d = (int(blockIdx.z) * LANES + tid % LANES) * 4;
+  constexpr int HEADS = Z == 1 ? 2 : 1;
+  for (int h = HEADS * int(blockIdx.y); h < min(a.num_heads, HEADS * int(blockIdx.y) + HEADS); ++h) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (tid < n) ml = __ldcg(a.part_ml + slot(tid, h));
+    float M = ml.x;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) den += red[i];
-  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    __syncthreads();  // the last head's readers are done
+    if ((tid & 31) == 0) red[tid >> 5] = M;
+    __syncthreads();
+    M = red[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) M = fmaxf(M, red[i]);
+    const float w = tid < n ? fast_exp2(ml.x - (M == -INFINITY ? 0.f : M)) : 0.f;
+    if (tid < n) weight[tid] = w;
+    float den = w * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
+    __syncthreads();
+    if ((tid & 31) == 0) red[tid >> 5] = den;
+    __syncthreads();
+    den = red[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) den += red[i];
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int i = group; i < n; i += GROUPS) {
-    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * kLatentDim + d));
-    const float wi = weight[i];
-    num.x = fmaf(wi, o.x, num.x);
-    num.y = fmaf(wi, o.y, num.y);
-    num.z = fmaf(wi, o.z, num.z);
-    num.w = fmaf(wi, o.w, num.w);
-  }
-  if (group) other[group - 1][tid % LANES] = num;
-  __syncthreads();
-  if (group) return;
+    for (int i = group; i < n; i += GROUPS) {
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i, h) * kLatentDim + d));
+      const float wi = weight[i];
+      num.x = fmaf(wi, o.x, num.x);
+      num.y = fmaf(wi, o.y, num.y);
+      num.z = fmaf(wi, o.z, num.z);
+      num.w = fmaf(wi, o.w, num.w);
+    }
+    if (group) other[group - 1][tid % LANES] = num;
+    __syncthreads();
+    if (group) continue;
 #pragma unroll
-  for (int i = 0; i < GROUPS - 1; ++i) {
-    const float4 x = other[i][tid];
-    num.x += x.x;
-    num.y += x.y;
-    num.z += x.z;
-    num.w += x.w;
+    for (int i = 0; i < GROUPS - 1; ++i) {
+      const float4 x = other[i][tid];
+      num.x += x.x;
+      num.y += x.y;
+      num.z += x.z;
+      num.w += x.w;
+    }
+    write(h, d, num, den);
   }
-  const float inv = 1.f / den;
-  const uint2 v = make_uint2(pack2<T>(num.x * inv, num.y * inv), pack2<T>(num.z * inv, num.w * inv));
-  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_heads + h) * kLatentDim + d) = v;
 }
 
 }  // namespace pkv

@@ -81,11 +81,31 @@ cudaError_t launch_decode_int8(const DecodeArgs& a, bool bf16, int head_dim, int
                                const CUtensorMap* vmap, cudaStream_t stream);
 
 // 4-bit KV cache (int4_layout.cuh): quantising write, or read back of the rows
-// at `slots` into k and v (gather); decode with DecodeArgs::k_pool the cache.
+// at `slots` into k and v (gather); decode.
 cudaError_t launch_cache_int4(bool gather, void* k, void* v, bool bf16, void* cache, const int64_t* slots,
                               int num_tokens, int num_kv_heads, int head_dim, int num_blocks, unsigned int* status,
                               cudaStream_t stream);
-cudaError_t launch_decode_int4(const DecodeArgs& a, bool bf16, int head_dim, int gpad, cudaStream_t stream);
+struct Int4Args {
+  void* out;
+  const void* q;
+  const void* cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  unsigned int* status;
+  int num_seqs, num_q_heads, num_kv_heads;
+  int group;           // query heads per KV head
+  int max_blocks_per_seq, num_blocks;
+  int window;          // attend over the last `window` tokens (0 = all)
+  float scale_log2;    // scale * log2(e)
+  // set by the launcher: CTAs, whether each takes one item, and the workspace's parts
+  int ctas, item_ctas;
+  int2* desc;
+  float2* part_ml;
+  float* part_o;
+};
+// `blocks`: the most table entries of a sequence that a call reads (fewer with a window).
+size_t int4_workspace_bytes(int num_seqs, int num_kv_heads, int group, int head_dim, int blocks);
+cudaError_t launch_decode_int4(Int4Args a, bool bf16, int head_dim, int blocks, void* workspace, cudaStream_t stream);
 // Block copy of one pool whose blocks are bytes_per_block bytes (a multiple of 16).
 cudaError_t launch_copy_blocks_pool(void* pool, const int64_t* pairs, int num_pairs, int64_t bytes_per_block,
                                     int num_blocks, unsigned int* status, cudaStream_t stream);

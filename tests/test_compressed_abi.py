@@ -18,14 +18,15 @@ def _call(name, spec, kw):
 
 
 DECODE = dict(out=FAKE, q=FAKE, cache=FAKE, bt=FAKE, cl=FAKE, S=4, hq=8, hkv=4, D=128, mb=4, nb=64, scale=0.1, dt=0,
-              window=0, part=0, ws=FAKE, wsb=1 << 20)
+              window=0, ws=FAKE, wsb=1 << 24)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(S=-1), 1), (dict(hq=6, hkv=4), 1), (dict(hq=0), 1), (dict(hq=36, hkv=4), 2), (dict(D=96), 2),
     (dict(dt=2), 2), (dict(mb=0), 1), (dict(nb=0), 1), (dict(S=65536), 2), (dict(scale=float("nan")), 1),
     (dict(out=None), 1), (dict(q=FAKE + 2), 1), (dict(cache=FAKE + 8), 1), (dict(bt=FAKE + 2), 1), (dict(cl=FAKE + 1), 1),
-    (dict(part=-2), 2), (dict(part=-5), 2), (dict(part=24), 1), (dict(ws=None), 5), (dict(wsb=16), 5), (dict(ws=FAKE + 8), 5),
+    (dict(mb=1 << 27), 1), (dict(nb=1 << 30), 2), (dict(S=200, ws=None), 5), (dict(S=200, wsb=16), 5),
+    (dict(S=200, ws=FAKE + 8), 5),
 ])
 def test_decode_int4_refusals(kw, status):
     st, msg = _call("pkv_paged_attention_decode_int4", DECODE, kw)
@@ -133,6 +134,10 @@ def test_empty_calls_do_nothing():
 
 def test_sizes():
     assert [B.int4_tile_bytes(d) for d in (64, 128, 256, 96)] == [1152, 2304, 4608, 0]
+    assert B.int4_workspace_size(4, 32, 8, 128, 128) == 0       # 32 items of at most 64 tile pairs: a CTA each
+    assert B.int4_workspace_size(256, 32, 8, 128, 64) >= 2 * 304 * 4 * 128 * 4
+    assert B.int4_workspace_size(4, 32, 8, 128, 4096, 512) == 0  # the window bounds the tiles
+    assert B.int4_workspace_size(4, 32, 8, 96, 4096) == 0        # no such head_dim
     assert B.lib().pkv_extend_workspace_size(64, 64) == 0
     assert B.lib().pkv_extend_workspace_size(2000, 64) >= 4 * 6 * 2000
     assert B.lib().pkv_release_workspace_size(129) == 32

@@ -193,23 +193,41 @@ def test_decode(dtype, D, hq, hkv):
     assert B.device_status(clear=True) == 0
 
 
-@pytest.mark.parametrize("partition", [-1, 16, 32, 64, 1024])
-@pytest.mark.parametrize("hq,hkv,D", [(2, 2, 128), (8, 2, 64), (3, 1, 256)])
-def test_partitions(partition, hq, hkv, D):
-    c = Case([1, 300, 0, 16, 511, 33], hq, hkv, D, "bf16", 5, extra_cols=3)
-    c.check(c.run(partition_size=partition))
+MANY = [1, 300, 0, 16, 511, 33, 0, 0, 64, 31, 32, 2, 700, 15] + [5, 40] * 20
+
+
+@pytest.mark.parametrize("dtype,hq,hkv,D", [("bf16", 12, 12, 128), ("bf16", 48, 12, 64), ("f16", 36, 12, 256),
+                                            ("f16", 24, 24, 64), ("bf16", 80, 10, 128)])
+def test_list_schedule(dtype, hq, hkv, D):
+    # more items than CTAs of their own: shares that start and end anywhere, items over warps and CTAs
+    c = Case(MANY, hq, hkv, D, dtype, 5, extra_cols=3)
+    assert B.int4_workspace_size(len(MANY), hq, hkv, D, c.tables.shape[1]) > 0
+    c.check(c.run())
+    assert B.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(1, 1, 128), (8, 1, 64), (3, 1, 256)])
+def test_one_long_sequence_over_all_ctas(hq, hkv, D):
+    c = Case([9001, 0, 40], hq, hkv, D, "bf16", 6)
+    assert B.int4_workspace_size(3, hq, hkv, D, c.tables.shape[1]) > 0
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("window", [1, 33, 100])
+def test_list_schedule_with_a_window(window):
+    c = Case(MANY, 12, 12, 64, "bf16", 8)
+    c.check(c.run(sliding_window=window), window)
 
 
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 31, 100, 4096])
-@pytest.mark.parametrize("partition", [0, 16, 48])
-def test_windows(window, partition):
+def test_windows(window):
     c = Case([1, 300, 0, 16, 117, 33], 4, 2, 128, "f16", 7)
     first = np.maximum(c.lens_np - window, 0) // 16
     t = c.tables_np.copy()
     for s, j in enumerate(first):
         t[s, :j] = -1                             # blocks before the window are never read
     c.tables = _cuda(t)
-    c.check(c.run(sliding_window=window, partition_size=partition), window)
+    c.check(c.run(sliding_window=window), window)
     assert B.device_status(clear=True) == 0
 
 
@@ -231,7 +249,6 @@ def test_rows_past_the_end_may_hold_anything(dtype, D, hq, hkv):
             tiles[dead, :, base + row * (D // 16):base + (row + 1) * (D // 16)] = 0xFF
     c.cache = _cuda(tiles)
     c.check(c.run())
-    c.check(c.run(partition_size=16))
 
 
 def test_nan_in_a_live_row_shows():
@@ -282,7 +299,6 @@ def test_growing_scores_move_the_running_maximum():
     c.q[:, 1] = -1
     c.scale = 0.02
     c.check(c.run())
-    c.check(c.run(partition_size=64))
 
 
 def test_bad_ids_and_lengths_are_flagged():
@@ -323,24 +339,19 @@ def test_a_pool_past_four_gigabytes():
     assert torch.equal(cache[int(far[0])], cache[int(far[0]) - 1])
 
 
-@pytest.mark.parametrize("S", [2, 127, 128, 300])
-def test_planned_calls(S):
-    lens = np.random.default_rng(S).integers(0, 90, S)
-    c = Case(lens, 8, 2, 64, "bf16", 19)
-    free = c.run()
-    c.check(free)
-    ws = torch.empty(max(16, B.workspace_size(S, 8, 2, 64, c.tables.shape[1])), dtype=torch.uint8, device="cuda")
-    B.paged_attention_plan(c.lens, c.tables, 8, 2, 64, workspace=ws)
-    c.check(c.run(planned=True, workspace=ws))
-    ws.zero_()
-    if S <= 1024 and S * 2 <= 4096:
-        c.check(c.run(planned=True, workspace=ws))   # no plan: flagged, natural order
-        assert B.device_status(clear=True) == 0x20
-
-
 def test_calls_are_reproducible():
-    c = Case([300, 1000, 77], 8, 2, 128, "bf16", 20)
-    for part in (0, -1, 64):
-        first = c.run(partition_size=part)
+    for lens, hq, hkv in (([300, 1000, 77], 8, 2), (MANY, 24, 12)):
+        c = Case(lens, hq, hkv, 128, "bf16", 20)
+        first = c.run()
         for _ in range(3):
-            assert torch.equal(c.run(partition_size=part), first)
+            assert torch.equal(c.run(), first)
+
+
+def test_a_workspace_of_the_callers():
+    c = Case(MANY, 12, 12, 64, "bf16", 21)
+    ws = torch.full((B.int4_workspace_size(len(MANY), 12, 12, 64, c.tables.shape[1]) + 64,), 0xFF, dtype=torch.uint8,
+                    device="cuda")
+    c.check(c.run(workspace=ws))
+    assert (ws[-64:] == 0xFF).all()
+    with pytest.raises(B.PagedKVError, match="workspace"):
+        c.run(workspace=ws[:-65])
