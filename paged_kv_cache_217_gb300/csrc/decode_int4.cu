@@ -12,7 +12,8 @@ constexpr int64_t kItemCtas = 304;
 constexpr int kItemPairs = 64;
 constexpr int kMinPairs = 2;  // pairs a warp should have at least, where there are few
 
-int max_ctas(int head_dim) { return 152 * (head_dim == 256 ? 8 : 16) / kInt4Warps; }
+int max_ctas(int head_dim) { return 152 * (head_dim == 256 ? i4_ctas_per_sm<256>() : i4_ctas_per_sm<128>()); }
+int warps(int head_dim) { return head_dim == 256 ? i4_warps<256>() : i4_warps<128>(); }
 
 bool item_ctas(int num_seqs, int num_kv_heads, int blocks) {
   return int64_t(num_seqs) * num_kv_heads <= kItemCtas && (blocks + 1) / 2 <= kItemPairs;
@@ -22,27 +23,28 @@ bool item_ctas(int num_seqs, int num_kv_heads, int blocks) {
 // kMinPairs pairs for every warp.
 int list_ctas(int num_seqs, int num_kv_heads, int head_dim, int blocks) {
   const int64_t pairs = int64_t(num_seqs) * num_kv_heads * ((blocks + 1) / 2);
-  const int64_t want = (pairs + kInt4Warps * kMinPairs - 1) / (kInt4Warps * kMinPairs);
+  const int64_t share = warps(head_dim) * kMinPairs, want = (pairs + share - 1) / share;
   return want < max_ctas(head_dim) ? int(want) : max_ctas(head_dim);
 }
 
 template <typename T, int D, int H>
 cudaError_t launch_int4_dh(const Int4Args& a, cudaStream_t stream) {
-  using C = I4Cfg<D, H, kInt4Warps, kInt4Stages>;
-  static_assert(C::SMEM_BYTES <= 227 * 1024 * kInt4Warps / i4_warps_per_sm<D>() - 1024, "CTAs per SM");
-  static_assert(sizeof(I4Shared<kInt4Warps>) <= kInt4Warps * 36, "shared state");
-  auto kern = paged_decode_int4_kernel<T, D, H, kInt4Warps, kInt4Stages>;
+  constexpr int NW = i4_warps<D>();
+  using C = I4Cfg<D, H, NW, kInt4Stages>;
+  static_assert(C::SMEM_BYTES <= 228 * 1024 / i4_ctas_per_sm<D>() - 1024, "CTAs per SM");
+  static_assert(sizeof(I4Shared<NW>) <= C::SMEM_BYTES - C::RING_BYTES - C::PIECE_BYTES - C::BAR_BYTES, "shared state");
+  auto kern = paged_decode_int4_kernel<T, D, H, NW, kInt4Stages>;
   static bool configured[kMaxDevices] = {};
   cudaError_t err = configure_once(kern, C::SMEM_BYTES, configured);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(kern, dim3(unsigned(a.ctas)), dim3(kInt4Warps * 32), C::SMEM_BYTES, stream, a);
+  err = launch_pdl(kern, dim3(unsigned(a.ctas)), dim3(NW * 32), C::SMEM_BYTES, stream, a);
   if (err != cudaSuccess || a.item_ctas || a.ctas == 1) return err;
   return launch_pdl(int4_merge_kernel<T, D>, dim3(unsigned(a.ctas), unsigned(a.group)), dim3(256), 0, stream, a);
 }
 
 template <typename T, int D>
 cudaError_t launch_int4_d(const Int4Args& a, cudaStream_t stream) {
-  return a.group <= 2 ? launch_int4_dh<T, D, 2>(a, stream) : launch_int4_dh<T, D, 8>(a, stream);
+  return a.group <= 4 ? launch_int4_dh<T, D, 4>(a, stream) : launch_int4_dh<T, D, 8>(a, stream);
 }
 
 template <typename T>

@@ -7,24 +7,22 @@
 // so the codes enter the products as they are and the pairs touch only scores
 // and weights: no element is dequantised.
 //
-// Two 16-token tiles a step, as mma.sync with fp32 accumulators; the 8 columns
-// of N belong to the KV head's query heads:
+// Two 16-token tiles a step, as mma.sync m16n8k16 with fp16 inputs and fp32
+// accumulators; the 8 columns of N belong to the KV head's query heads:
 //  * S^T = C_K Q^T: tokens on M. A quad's lane t holds words 8 g + 2 t, + 1 of
-//    its two token rows (one shared load a row).
-//    1 or 2 heads: m16n8k32 on e4m3. A nibble alone in a byte is the e4m3
-//    value c 2^-9, exactly, for c = 0..15 (its first two exponents share one
-//    step), so two masks and a shift convert 8 codes. A query element, scaled
-//    by a power of two per head to a largest magnitude in [2^7, 2^8), is the
-//    sum of four e4m3 digits (each the rounding of what the earlier ones
-//    leave: 2^-10 at the end, at most 2^-17 of the largest element); the
-//    digits take four columns a head, which the scores then add up.
-//    The tensor cores add e4m3 products to fp32 without loss (checked).
-//    3 to 8 heads: m16n8k16 on fp16, a column a head. Masking makes fp16
-//    pairs of a word's nibbles: nibble j (bits 0-3 of a half) is the
-//    subnormal c 2^-24, the one above it (bits 4-7) c 2^-20, both exact; 5
-//    instructions convert 8 codes. The query of the odd dims is divided by 16
-//    to match, and scaled to [2^13, 2^14) (elements below 2^-24 of the
-//    largest lose bits).
+//    its two token rows (one shared load a row). Codes become fp16 by masking
+//    alone: a nibble in bits 0-3 of a half is the subnormal c 2^-24, and the
+//    byte c0 + 16 c1 above and including it is exact too (a half's low 11 bits
+//    are linear), both without loss in the tensor cores' products.
+//    Up to 4 heads take two columns each: with A = (c0, c0 + 16 c1), column a
+//    has (q0, q1 / 16) and column b (q1 / 16, 0), and a - b = q0 c0 + q1 c1: 4
+//    integer instructions convert 8 codes. 5 to 8 heads, a column each, take c0
+//    and c1 16 by a mask each: 5 instructions. The query is scaled by a power of
+//    two per head that brings max |q| to [2^13, 2^14): bf16 and fp16 queries are
+//    exact (elements below 2^-24 of the largest lose bits).
+//    (e4m3 holds a nibble in a byte exactly, c 2^-9, in 3 instructions per 8
+//    codes; but mma.sync on e4m3 cost 110 instructions a tile more here, as many
+//    as it takes to convert to fp16.)
 //    The fp32 sums of each group are then multiplied by s and joined by
 //    z * sum q.
 //  * O^T += C_V^T P~: head dims on M, tokens on K, fp16. V words of tokens t
@@ -53,7 +51,6 @@
 #pragma once
 
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 #include "decode.cuh"
 #include "device_common.cuh"
@@ -70,16 +67,21 @@ struct I4Cfg {
   static constexpr size_t RING_BYTES = size_t(NW) * STAGES * STAGE_BYTES;
   static constexpr size_t PIECE_BYTES = size_t(NW) * PIECE_FLOATS * sizeof(float);
   static constexpr size_t BAR_BYTES = size_t(NW) * STAGES * 8;
-  static constexpr size_t SMEM_BYTES = RING_BYTES + PIECE_BYTES + BAR_BYTES + NW * 36;
+  static constexpr size_t SMEM_BYTES = RING_BYTES + PIECE_BYTES + BAR_BYTES + NW * 32 * 12 + NW * 64 + 64;
   static_assert(PIECE_FLOATS * 4 <= STAGES * STAGE_BYTES, "a piece fits a warp's ring");
   static_assert(PIECE_FLOATS % 4 == 0, "pieces are 16-byte aligned");
 };
 
-// Warps that an SM holds (registers: 128 a thread, 255 at head_dim 256).
+// Warps per CTA, and CTAs that an SM holds. Measured on GB300 at head_dim 128:
+// 2 x 6 warps (168 registers) 61.2 us, 2 x 8 (128, some spilled) 65.1 on the
+// 40-head layer, 115.8 against 118.9 on 96 heads x 3 long sequences; at 256 one
+// CTA of 8 (255 registers) 60.4 us against 67.8 with 6. A prefetch of later tiles
+// into L2 made all of them 5-18 % slower.
 template <int D>
-constexpr int i4_warps_per_sm() { return D == 256 ? 8 : 16; }
-constexpr int kInt4Warps = 8;                       // per CTA
-constexpr int kInt4MaxCtas = 152 * 16 / kInt4Warps;  // one wave of a GB300
+constexpr int i4_warps() { return D == 256 ? 8 : 6; }
+template <int D>
+constexpr int i4_ctas_per_sm() { return D == 256 ? 1 : 2; }
+constexpr int kInt4MaxCtas = 2 * 152;  // one wave of a GB300
 
 // Scores past the reference by more than this move it.
 constexpr float kInt4Lazy = 8.f;
@@ -122,10 +124,10 @@ __device__ __forceinline__ float2 pair_of<__half>(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-// A word of two tokens' halves (nibbles 0..3 of each) as fp16 pairs in units of
-// 2^-24: n0, n0 + 16 n1, n2, n2 + 16 n3. The upper nibbles are never taken
-// alone: the products of n0 + 16 n1 less those of n0 are 16 times theirs, which
-// the epilogue sorts out once (16 integer instructions fewer per 32 tokens).
+// A word's halves (nibbles 0..3 of each) as fp16 pairs in units of 2^-24: n0, n0
+// + 16 n1, n2, n2 + 16 n3. The upper nibbles are never taken alone: the products
+// of n0 + 16 n1 less those of n0 are 16 times theirs, which is sorted out where
+// the products are read.
 __device__ __forceinline__ void nibble_sums(uint32_t w, uint32_t (&p)[4]) {
   p[0] = w & 0x000f000fu;
   p[1] = w & 0x00ff00ffu;
@@ -143,16 +145,8 @@ __device__ __forceinline__ void nibbles(uint32_t w, uint32_t (&p)[4]) {
   p[3] = w & 0x00f000f0u;
 }
 
-// d = a b + c. Plain functions of their operands (not volatile), so that the
+// d = a b + c. A plain function of its operands (not volatile), so that the
 // compiler may interleave the chains of a step.
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -161,116 +155,93 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// Layout of the query heads over a quad's lanes. H: heads the kernel takes (2
-// or 8, the group padded up). PER_LANE score columns a lane keeps (1 after its
-// digits are added up), the head of lane t's column c.
+// Layout of the query heads over a quad's lanes. H: heads the kernel takes (4 or
+// 8, the group padded up). PER_LANE heads whose scores a lane keeps, the head of
+// its c-th one.
 template <int H>
 struct I4Heads {
-  static_assert(H == 2 || H == 8, "2 heads of four digits, or 8 heads");
-  static constexpr bool FP8 = H == 2;
-  static constexpr int PER_LANE = H == 8 ? 2 : 1;
-  static __device__ __forceinline__ int head(int t, int c) { return H == 2 ? t >> 1 : 2 * t + c; }
+  static_assert(H == 4 || H == 8, "4 heads of two columns, or 8 heads");
+  static constexpr int PER_LANE = H / 4;
+  static __device__ __forceinline__ int head(int t, int c) { return H == 4 ? t : 2 * t + c; }
 };
 
 // The query operand of one lane (column gr of N), and the factors of the heads
 // whose scores it keeps.
 template <int D, int H>
 struct I4Query {
-  static constexpr int REGS = I4Heads<H>::FP8 ? D / 32 : D / 16;
-  uint32_t b[REGS][2];                            // e4m3: word 2 g + i; fp16: k-step 2 (2 g + i) + j
-  float sum[D / kInt4Group][I4Heads<H>::PER_LANE];  // sum of the scaled query over a group, in the scores' unit
-  float mul[I4Heads<H>::PER_LANE];                // scale log2(e) / the power of two; the unit is applied apart
+  uint32_t b[D / 16][2];                            // k-step 2 (2 g + i) + j: word 8 g + 2 t + i
+  float sum[D / kInt4Group][I4Heads<H>::PER_LANE];  // sum of the scaled query over a group, times 2^-24
+  float mul[I4Heads<H>::PER_LANE];                  // scale log2(e) / the power of two (2^24 is applied apart)
 };
 
-// The unit of the integer sums: codes enter as c 2^-9 (e4m3) or c 2^-24 (fp16).
-template <int H>
-constexpr float i4_unit() { return I4Heads<H>::FP8 ? 0x1p-9f : 0x1p-24f; }
-template <int H>
-constexpr float i4_unit_inv() { return I4Heads<H>::FP8 ? 0x1p9f : 0x1p24f; }
-
-// q0: the group's first query row. Lane (gr, t) reads dims 64 g + 16 t .. + 15
-// of its column's head (words 8 g + 2 t, + 1).
+// The 16-bit query elements of a lane: dims 64 g + 16 t .. + 15 of its column's
+// head (words 8 g + 2 t, + 1).
+template <int D>
+struct I4Raw {
+  uint4 u[D / kInt4Group][2];
+};
 template <typename T, int D, int H>
-__device__ __forceinline__ void i4_query(const T* q0, int group, int lane, float scale_log2, I4Query<D, H>& q) {
-  using HL = I4Heads<H>;
-  constexpr int GROUPS = D / kInt4Group;
-  const int t = lane & 3, gr = lane >> 2;
-  const int head = gr * H / 8;
-  float f[GROUPS][16], m = 0.f;
+__device__ __forceinline__ void i4_load_query(const T* q0, int group, int lane, I4Raw<D>& raw) {
+  const int t = lane & 3, head = (lane >> 2) * H / 8;
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g) {
-    uint4 u[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  for (int g = 0; g < D / kInt4Group; ++g) {
+    raw.u[g][0] = raw.u[g][1] = make_uint4(0, 0, 0, 0);
     if (head < group) {
       const uint4* src = reinterpret_cast<const uint4*>(q0 + size_t(head) * D + 64 * g + 16 * t);
-      u[0] = __ldg(src);
-      u[1] = __ldg(src + 1);
+      raw.u[g][0] = __ldg(src);
+      raw.u[g][1] = __ldg(src + 1);
     }
+  }
+}
+
+template <typename T, int D, int H>
+__device__ __forceinline__ void i4_query(const I4Raw<D>& raw, int lane, float scale_log2, I4Query<D, H>& q) {
+  using HL = I4Heads<H>;
+  constexpr int GROUPS = D / kInt4Group;
+  const int t = lane & 3;
+  float m = 0.f;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float x[8];
-      Vec8<T>::to_float(u[i], x);
+      Vec8<T>::to_float(raw.u[g][i], x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        f[g][8 * i + e] = x[e];
-        m = fmaxf(m, fabsf(x[e]));
-      }
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
     }
-  }
   m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
   m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-  // m < 2^E (E from m's exponent field, clamped for tiny or zero q): times 2^(TOP - E)
-  constexpr int TOP = HL::FP8 ? 8 : 14;
+  // m < 2^E (E from m's exponent field, clamped for tiny or zero q): times 2^(14 - E)
   const int E = max(int((__float_as_uint(m) >> 23) & 0xffu) - 126, -100);
-  const float up = __uint_as_float(uint32_t(127 + TOP - E) << 23);
-  const float mul = scale_log2 * __uint_as_float(uint32_t(127 - TOP + E) << 23);
+  const float up = __uint_as_float(uint32_t(127 + 14 - E) << 23);
+  const float mul = scale_log2 * __uint_as_float(uint32_t(127 - 14 + E) << 23);
 #pragma unroll
   for (int c = 0; c < HL::PER_LANE; ++c) q.mul[c] = __shfl_sync(kFull, mul, 4 * (HL::head(t, c) * 8 / H));
+  const bool col_b = H == 4 && (lane & 4);
 #pragma unroll
   for (int g = 0; g < GROUPS; ++g) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float x[8];
+      Vec8<T>::to_float(raw.u[g][i], x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = f[g][8 * i + e] * up;
+        x[e] *= up;
         sum += x[e];
       }
-      if constexpr (HL::FP8) {
 #pragma unroll
-        for (int dig = 0; dig < 4; ++dig) {
-          // digit `dig` of the 8 elements (even dims, then odd dims); taken off
-          // even where another column keeps it
-          uint32_t w[2];
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const __nv_fp8x2_storage_t lo =
-                __nv_cvt_float2_to_fp8x2(make_float2(x[o], x[o + 2]), __NV_SATFINITE, __NV_E4M3);
-            const __nv_fp8x2_storage_t hi =
-                __nv_cvt_float2_to_fp8x2(make_float2(x[o + 4], x[o + 6]), __NV_SATFINITE, __NV_E4M3);
-            w[o] = uint32_t(lo) | (uint32_t(hi) << 16);
-            const float2 l = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(lo, __NV_E4M3)));
-            const float2 h = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(hi, __NV_E4M3)));
-            x[o] -= l.x, x[o + 2] -= l.y, x[o + 4] -= h.x, x[o + 6] -= h.y;
-          }
-          if (dig == gr % 4) {
-            q.b[2 * g + i][0] = w[0];
-            q.b[2 * g + i][1] = w[1];
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const __half2 even = __floats2half2_rn(x[2 * j], x[2 * j + 4]);
-          const __half2 odd = __floats2half2_rn(x[2 * j + 1] * 0.0625f, x[2 * j + 5] * 0.0625f);
-          q.b[2 * (2 * g + i) + j][0] = *reinterpret_cast<const uint32_t*>(&even);
-          q.b[2 * (2 * g + i) + j][1] = *reinterpret_cast<const uint32_t*>(&odd);
-        }
+      for (int j = 0; j < 2; ++j) {
+        const __half2 even = __floats2half2_rn(x[2 * j], x[2 * j + 4]);
+        const __half2 odd = __floats2half2_rn(x[2 * j + 1] * 0.0625f, x[2 * j + 5] * 0.0625f);
+        const uint32_t e = *reinterpret_cast<const uint32_t*>(&even), o = *reinterpret_cast<const uint32_t*>(&odd);
+        q.b[2 * (2 * g + i) + j][0] = col_b ? o : e;
+        q.b[2 * (2 * g + i) + j][1] = col_b ? 0u : o;
       }
     }
     sum += __shfl_xor_sync(kFull, sum, 1);
     sum += __shfl_xor_sync(kFull, sum, 2);
-    sum *= i4_unit<H>();
+    sum *= 0x1p-24f;
 #pragma unroll
     for (int c = 0; c < HL::PER_LANE; ++c) q.sum[g][c] = __shfl_sync(kFull, sum, 4 * (HL::head(t, c) * 8 / H));
   }
@@ -291,14 +262,12 @@ struct I4State {
 template <typename T, int D, int H>
 __device__ __forceinline__ void i4_scores(uint32_t tile, const I4Query<D, H>& q, float (&x)[2][I4Heads<H>::PER_LANE],
                                           int lane) {
-  using HL = I4Heads<H>;
-  constexpr int GROUPS = D / kInt4Group, PL = HL::PER_LANE;
+  constexpr int GROUPS = D / kInt4Group, PL = I4Heads<H>::PER_LANE;
   const int t = lane & 3, gr = lane >> 2;
   uint32_t kp[2][GROUPS];
   lds_words<GROUPS>(tile + 16 * D + gr * (D / 16), kp[0]);
   lds_words<GROUPS>(tile + 16 * D + (gr + 8) * (D / 16), kp[1]);
   constexpr int PER = D == 64 ? 2 : 4;  // words a shared load brings
-  float lane_x[2] = {0.f, 0.f};         // e4m3: sums over this lane's digits
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -315,50 +284,33 @@ __device__ __forceinline__ void i4_scores(uint32_t tile, const I4Query<D, H>& q,
       float s[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint32_t wa = w0[2 * h + i], wb = w1[2 * h + i];
-        if constexpr (HL::FP8) {
-          const uint32_t a0 = wa & 0x0f0f0f0fu, a2 = (wa >> 4) & 0x0f0f0f0fu;
-          const uint32_t a1 = wb & 0x0f0f0f0fu, a3 = (wb >> 4) & 0x0f0f0f0fu;
-          const uint32_t* b = q.b[2 * g + i];
-          if (i == 0) mma_e4m3(s, a0, a1, a2, a3, b[0], b[1], 0.f, 0.f, 0.f, 0.f);
-          else mma_e4m3(s, a0, a1, a2, a3, b[0], b[1], s[0], s[1], s[2], s[3]);
+        uint32_t a[4], b[4];
+        if constexpr (H == 4) {
+          nibble_sums(w0[2 * h + i], a);
+          nibble_sums(w1[2 * h + i], b);
         } else {
-          uint32_t a[4], b[4];
-          nibbles(wa, a);
-          nibbles(wb, b);
-          const uint32_t* b0 = q.b[2 * (2 * g + i)];
-          const uint32_t* b1 = q.b[2 * (2 * g + i) + 1];
-          if (i == 0) mma_f16(s, a[0], b[0], a[1], b[1], b0[0], b0[1], 0.f, 0.f, 0.f, 0.f);
-          else mma_f16(s, a[0], b[0], a[1], b[1], b0[0], b0[1], s[0], s[1], s[2], s[3]);
-          mma_f16(s, a[2], b[2], a[3], b[3], b1[0], b1[1], s[0], s[1], s[2], s[3]);
+          nibbles(w0[2 * h + i], a);
+          nibbles(w1[2 * h + i], b);
         }
+        const uint32_t* b0 = q.b[2 * (2 * g + i)];
+        const uint32_t* b1 = q.b[2 * (2 * g + i) + 1];
+        if (i == 0) mma_f16(s, a[0], b[0], a[1], b[1], b0[0], b0[1], 0.f, 0.f, 0.f, 0.f);
+        else mma_f16(s, a[0], b[0], a[1], b[1], b0[0], b0[1], s[0], s[1], s[2], s[3]);
+        mma_f16(s, a[2], b[2], a[3], b[3], b1[0], b1[1], s[0], s[1], s[2], s[3]);
       }
       const float2 k0 = pair_of<T>(kp[0][g]), k1 = pair_of<T>(kp[1][g]);
-      if constexpr (HL::FP8) {
-        lane_x[0] = fmaf(s[0] + s[1], k0.x, lane_x[0]);
-        lane_x[1] = fmaf(s[2] + s[3], k1.x, lane_x[1]);
-        x[0][0] = fmaf(k0.y, q.sum[g][0], x[0][0]);
-        x[1][0] = fmaf(k1.y, q.sum[g][0], x[1][0]);
-      } else {
 #pragma unroll
-        for (int e = 0; e < PL; ++e) {
-          x[0][e] = fmaf(s[e], k0.x, fmaf(k0.y, q.sum[g][e], x[0][e]));
-          x[1][e] = fmaf(s[2 + e], k1.x, fmaf(k1.y, q.sum[g][e], x[1][e]));
-        }
+      for (int e = 0; e < PL; ++e) {
+        const float y0 = H == 4 ? s[0] - s[1] : s[e], y1 = H == 4 ? s[2] - s[3] : s[2 + e];
+        x[0][e] = fmaf(y0, k0.x, fmaf(k0.y, q.sum[g][e], x[0][e]));
+        x[1][e] = fmaf(y1, k1.x, fmaf(k1.y, q.sum[g][e], x[1][e]));
       }
-    }
-  }
-  if constexpr (HL::FP8) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      lane_x[r] += __shfl_xor_sync(kFull, lane_x[r], 1);  // digits 0, 1 and 2, 3
-      x[r][0] += lane_x[r];
     }
   }
 #pragma unroll
   for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int e = 0; e < PL; ++e) x[r][e] = x[r][e] * q.mul[e] * i4_unit_inv<H>();
+    for (int e = 0; e < PL; ++e) x[r][e] = x[r][e] * q.mul[e] * 0x1p24f;
 }
 
 // Two tiles (32 tokens from a multiple of 16); with MASK only tokens [lo, rows)
@@ -519,7 +471,6 @@ __device__ __forceinline__ void i4_publish(float* piece, I4State<D, H>& st, int 
   using HL = I4Heads<H>;
   const int t = lane & 3, gr = lane >> 2;
   i4_reduce<D, H>(st);
-  if (H == 2 && (t & 1)) return;  // its neighbour holds the same head
 #pragma unroll
   for (int c = 0; c < HL::PER_LANE; ++c) {
     const int head = HL::head(t, c);
@@ -540,7 +491,7 @@ __device__ __forceinline__ void i4_write(T* out, int group, I4State<D, H>& st, i
 #pragma unroll
   for (int c = 0; c < HL::PER_LANE; ++c) {
     const int head = HL::head(t, c);
-    if (head >= group || (H == 2 && (t & 1))) continue;
+    if (head >= group) continue;
     const float inv = 1.f / st.l[c];
     i4_values<D, H>(st, c, gr, [&](int dim, const float4& v) {
       T x[4] = {T(v.x * inv), T(v.y * inv), T(v.z * inv), T(v.w * inv)};
@@ -585,52 +536,26 @@ __device__ __forceinline__ I4Seq i4_seq(const Int4Args& a, int L) {
   return q;
 }
 
+// Pieces of one item in a CTA: a warp's last piece (or none: the item began in an
+// earlier CTA), then the first pieces of warps [from, to). slot: where the joined
+// result goes in the workspace, or -1: it is the output.
+struct I4Run {
+  int item, head, from, to, slot;
+};
+
 template <int NW>
 struct I4Shared {
-  long long scan[NW], base[NW];  // per warp: where its first sequence starts in the list
-  int seq[NW], len[NW];          // ... that sequence and its length
+  long long before[NW * 32];     // per thread: where its run of sequences starts in the list
+  long long scan[NW], last[NW];  // per warp: ... and the last pair of the item of its last piece
+  int len[NW * 32];              // per thread: the length of its run's last sequence
   int fitem[NW], fend[NW], litem[NW];
+  I4Run run[NW + 1];
 };
 
 constexpr int kInt4NoPiece = -1, kInt4NoWork = -2;
 
-// Joins pieces (piece(i), i < n) of one item: output rows, or a partial result
-// for the merge across CTAs. One warp.
-template <typename T, int D, int H, typename P>
-__device__ __forceinline__ void i4_join(const Int4Args& a, int item, int n, P piece, int slot, int lane) {
-  const int s = item / a.num_kv_heads, g = item - s * a.num_kv_heads;
-  for (int h = 0; h < a.group; ++h) {
-    float M = -INFINITY;
-    for (int i = 0; i < n; ++i) M = fmaxf(M, piece(i)[H * D + h]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    for (int d = 4 * lane; d < D; d += 128) {
-      float den = 0.f;
-      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int i = 0; i < n; ++i) {
-        const float* p = piece(i);
-        const float w = fast_exp2(p[H * D + h] - ref);
-        const float4 x = *reinterpret_cast<const float4*>(p + h * D + d);
-        den = fmaf(w, p[H * D + H + h], den);
-        num.x = fmaf(w, x.x, num.x);
-        num.y = fmaf(w, x.y, num.y);
-        num.z = fmaf(w, x.z, num.z);
-        num.w = fmaf(w, x.w, num.w);
-      }
-      if (slot < 0) {
-        const float inv = 1.f / den;
-        T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + g * a.group + h) * D + d) =
-            *reinterpret_cast<const uint2*>(x);
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + (size_t(slot) * a.group + h) * D + d) = num;
-        if (d == 0) a.part_ml[size_t(slot) * a.group + h] = make_float2(M, den);
-      }
-    }
-  }
-}
-
 template <typename T, int D, int H, int NW, int STAGES>
-__global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_decode_int4_kernel(const Int4Args a) {
+__global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int4_kernel(const Int4Args a) {
   using C = I4Cfg<D, H, NW, STAGES>;
   extern __shared__ __align__(1024) unsigned char smem[];
   I4Shared<NW>& sh = *reinterpret_cast<I4Shared<NW>*>(smem + C::RING_BYTES + C::PIECE_BYTES + C::BAR_BYTES);
@@ -669,16 +594,17 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
     ce = total = np;
   } else {
     // Each thread sums a run of sequences, a scan of the sums gives every run's
-    // place in the list, and the thread whose run holds a warp's first pair
-    // finds its sequence.
+    // place in the list, and each warp searches the places for its own start.
     int zero_len = int(blockIdx.x) < a.num_seqs ? i4_len(a, int(blockIdx.x)) : 1;  // (read along with the others)
-    const int per = (a.num_seqs + NW * 32 - 1) / (NW * 32);
+    const int per = (a.num_seqs + NW * 32 - 1) / (NW * 32), most = a.max_blocks_per_seq * kBlock;
     const int run0 = min(a.num_seqs, tid * per), run1 = min(a.num_seqs, run0 + per);
     long long mine = 0;
+    int run_len = 0;
     for (int i = run0; i < run1; ++i) {
-      const int raw = __ldg(a.context_lens + i), len = i4_len(a, i);
-      if (raw != len && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-      mine += (long long)i4_seq(a, len).np * Hkv;
+      const int raw = __ldg(a.context_lens + i);
+      run_len = raw < 0 ? 0 : raw > most ? most : raw;
+      if (raw != run_len && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+      mine += (long long)i4_seq(a, run_len).np * Hkv;
     }
     long long upto = mine;
 #pragma unroll
@@ -695,24 +621,10 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
       if (i < warp) before += sh.scan[i];
       total += sh.scan[i];
     }
+    sh.before[tid] = before;
+    sh.len[tid] = run_len;
     cb = int(blockIdx.x) * total / a.ctas;
     ce = (int(blockIdx.x) + 1) * total / a.ctas;
-    for (int w = 0; w < NW; ++w) {
-      const long long x = warp_begin(w);
-      if (x < before || x >= before + mine) continue;
-      long long at = before;
-      for (int i = run0;; ++i) {
-        const int len = i4_len(a, i);
-        const long long n = (long long)i4_seq(a, len).np * Hkv;
-        if (at + n > x) {
-          sh.seq[w] = i;
-          sh.len[w] = len;
-          sh.base[w] = at;
-          break;
-        }
-        at += n;
-      }
-    }
     // Sequences without tokens: zeros, spread over the CTAs.
     for (int i = int(blockIdx.x); i < a.num_seqs;) {
       if (zero_len == 0) {
@@ -723,9 +635,23 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
       if (i < a.num_seqs) zero_len = i4_len(a, i);
     }
     __syncthreads();
-    s = sh.seq[warp];
-    L = sh.len[warp];
-    base = sh.base[warp];
+    // the last run that starts at or before the warp's first pair holds it (runs
+    // that hold nothing start where the next one does)
+    const long long x = warp_begin(warp);
+    int r = -1;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) r += __popc(__ballot_sync(kFull, sh.before[32 * i + lane] <= x));
+    s = min(a.num_seqs, r * per);
+    base = sh.before[r];
+    L = sh.len[r];
+    if (per > 1 && x < total) {
+      for (;; ++s) {
+        L = i4_len(a, s);
+        const long long n = (long long)i4_seq(a, L).np * Hkv;
+        if (base + n > x) break;
+        base += n;
+      }
+    }
   }
   const long long wb = warp_begin(warp), we = warp_begin(warp + 1);
   int item = 0, ahead = 0;  // the item at hand; the next sequence's length
@@ -734,26 +660,28 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
   int fitem = kInt4NoWork, fend = 0, litem = kInt4NoWork;
   if (wb < we) {
     fitem = litem = kInt4NoPiece;
+    const int n_my = int(we - wb);
     sq = i4_seq(a, L);
     g = int((wb - base) / sq.np);
     pr = int(wb - base - (long long)g * sq.np);
     if (!a.item_ctas && s + 1 < a.num_seqs) ahead = i4_len(a, s + 1);
 
+    I4Raw<D> raw;
+    i4_load_query<T, D, H>(static_cast<const T*>(a.q) + (size_t(s) * a.num_q_heads + g * a.group) * D, a.group, lane, raw);
+
     // Copies: lanes 2 (k % 16), + 1 of `tiles` hold the pool tiles of the warp's
     // k-th pair (batches of 16, the next one read ahead; -1: none). Each lane
     // walks the list by itself.
-    int cs = s, cL = L;
-    long long cbase = base;
+    int cs = s, cfrom = int(base - wb);  // a lane's sequence and its place, from the warp's first pair
+    I4Seq c = sq;
     auto load_tiles = [&](int batch) -> int {
-      const long long x = wb + batch * 16 + (lane >> 1);
-      if (x >= we) return -1;
-      I4Seq c = i4_seq(a, cL);
-      while (x >= cbase + (long long)c.np * Hkv) {
-        cbase += (long long)c.np * Hkv;
-        cL = i4_len(a, ++cs);
-        c = i4_seq(a, cL);
+      const int x = batch * 16 + (lane >> 1);
+      if (x >= n_my) return -1;
+      while (x >= cfrom + c.np * Hkv) {
+        cfrom += c.np * Hkv;
+        c = i4_seq(a, i4_len(a, ++cs));
       }
-      const int at = int(x - cbase), cg = at / c.np, j = 2 * (at - cg * c.np) + (lane & 1);
+      const int at = x - cfrom, cg = at / c.np, j = 2 * (at - cg * c.np) + (lane & 1);
       if (j >= c.nt) return -1;
       int id = __ldg(a.block_tables + size_t(cs) * a.max_blocks_per_seq + c.t0 + j);
       if (id < 0 || id >= a.num_blocks) {
@@ -762,7 +690,7 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
       }
       return id * Hkv + cg;
     };
-    const int n_my = int(we - wb);
+    const unsigned char* cache = static_cast<const unsigned char*>(a.cache);
     int tiles = load_tiles(0), tiles_next = n_my > 16 ? load_tiles(1) : -1, batch = 0;
     auto issue = [&](int k) {  // warp-uniform; k increases by one per call
       if ((k >> 4) != batch) {
@@ -770,14 +698,15 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
         ++batch;
         tiles_next = (batch + 1) * 16 < n_my ? load_tiles(batch + 1) : -1;
       }
-      const int i0 = __shfl_sync(kFull, tiles, 2 * (k & 15)), i1 = __shfl_sync(kFull, tiles, 2 * (k & 15) + 1);
-      if (lane == 0) {
-        const int st = k % STAGES;
-        const uint32_t bar = bar_s + 8 * st, dst = ring_s + st * C::STAGE_BYTES;
-        const unsigned char* cache = static_cast<const unsigned char*>(a.cache);
-        mbar_arrive_expect_tx(bar, i1 >= 0 ? C::STAGE_BYTES : C::TILE_BYTES);
-        bulk_g2s(dst, cache + size_t(i0) * C::TILE_BYTES, C::TILE_BYTES, bar);
-        if (i1 >= 0) bulk_g2s(dst + C::TILE_BYTES, cache + size_t(i1) * C::TILE_BYTES, C::TILE_BYTES, bar);
+      // the two lanes that hold the pair's tiles copy them
+      const int i1 = __shfl_sync(kFull, tiles, 2 * (k & 15) + 1);
+      if ((lane >> 1) == (k & 15)) {
+        const int st = k % STAGES, b = lane & 1;
+        const uint32_t bar = bar_s + 8 * st;
+        if (b == 0) mbar_arrive_expect_tx(bar, i1 >= 0 ? C::STAGE_BYTES : C::TILE_BYTES);
+        if (tiles >= 0)
+          bulk_g2s(ring_s + st * C::STAGE_BYTES + b * C::TILE_BYTES, cache + size_t(tiles) * C::TILE_BYTES,
+                   C::TILE_BYTES, bar);
       }
     };
     for (int k = 0; k < STAGES && k < n_my; ++k) issue(k);
@@ -789,7 +718,7 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
       item = s * Hkv + g;
       const size_t row = size_t(s) * a.num_q_heads + g * a.group;
       I4Query<D, H> q;
-      i4_query<T, D, H>(static_cast<const T*>(a.q) + row * D, a.group, lane, a.scale_log2, q);
+      i4_query<T, D, H>(raw, lane, a.scale_log2, q);
       i4_clear<D, H>(st);
       const bool mid = pr > 0;  // the item began in another warp's range
       const int stop = min(sq.np, pr + n_my - k);
@@ -815,17 +744,7 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
         break;
       }
       const bool done = pr == sq.np;
-      if (mid) {
-        i4_publish<D, H>(first_piece, st, lane);
-        fitem = item;
-        fend = done ? 1 : 0;
-      } else if (done) {
-        i4_write<T, D, H>(static_cast<T*>(a.out) + row * D, a.group, st, lane);
-      } else {  // the range ends inside the item: every copy has landed, the ring is free
-        i4_publish<D, H>(reinterpret_cast<float*>(ring), st, lane);
-        litem = item;
-      }
-      if (done && k < n_my) {
+      if (done && k < n_my) {  // on to the next item: its query is read while this one is written
         pr = 0;
         if (++g == Hkv) {
           g = 0;
@@ -836,6 +755,18 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
             ahead = s + 1 < a.num_seqs ? i4_len(a, s + 1) : 0;
           } while (sq.np == 0);
         }
+        i4_load_query<T, D, H>(static_cast<const T*>(a.q) + (size_t(s) * a.num_q_heads + g * a.group) * D, a.group, lane,
+                               raw);
+      }
+      if (mid) {
+        i4_publish<D, H>(first_piece, st, lane);
+        fitem = item;
+        fend = done ? 1 : 0;
+      } else if (done) {
+        i4_write<T, D, H>(static_cast<T*>(a.out) + row * D, a.group, st, lane);
+      } else {  // the range ends inside the item: every copy has landed, the ring is free
+        i4_publish<D, H>(reinterpret_cast<float*>(ring), st, lane);
+        litem = item;
       }
     }
   }
@@ -843,49 +774,86 @@ __global__ void __launch_bounds__(NW * 32, i4_warps_per_sm<D>() / NW) paged_deco
     sh.fitem[warp] = fitem;
     sh.fend[warp] = fend;
     sh.litem[warp] = litem;
+    sh.last[warp] = base + (long long)(g + 1) * sq.np - 1;
   }
   __syncthreads();
-  // Pieces that belong together follow one another: a warp's last piece, or the
-  // CTA's first one, and the first pieces of the warps after it.
-  auto first_of = [&](int w) {
-    return reinterpret_cast<const float*>(smem + C::RING_BYTES) + w * C::PIECE_FLOATS;
-  };
-  auto join = [&](int id, const float* head, int w) {  // `head`, then first pieces from warp w on
-    const float* list[NW + 1];
-    int n = 0;
+  // The CTA's runs of pieces: one from each warp's last piece, and (thread NW) the
+  // one of an item that began in an earlier CTA.
+  if (tid <= NW) {
+    I4Run run{kInt4NoPiece, -1, 0, 0, 2 * int(blockIdx.x)};
     bool end = false;
-    if (head) list[n++] = head;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      if (i < w || end) continue;
-      if (sh.fitem[i] == kInt4NoWork) continue;
-      if (sh.fitem[i] != id) break;
-      list[n++] = first_of(i);
-      end = sh.fend[i] != 0;
-    }
-    const int slot = !head ? 2 * int(blockIdx.x) : end ? -1 : 2 * int(blockIdx.x) + 1;
-    i4_join<T, D, H>(a, id, n, [&](int i) { return list[i]; }, slot, lane);
-    return end;
-  };
-  bool open = false;
-  if (litem >= 0) open = !join(litem, reinterpret_cast<const float*>(ring), warp + 1);
-  if (warp == 0 && !a.item_ctas) {
-    // the item that began in an earlier CTA
     int w = 0;
-    while (w < NW && sh.fitem[w] == kInt4NoWork) ++w;
-    if (w < NW && sh.fitem[w] >= 0) join(sh.fitem[w], nullptr, w);
-  }
-  if (!a.item_ctas) {
-    // the descriptor for the merge: an item that starts here and goes on, and the
-    // CTA that holds its last pair
-    if (open && lane == 0) {
-      const long long last = base + (long long)(g + 1) * sq.np - 1;
-      long long c = last * a.ctas / total;
-      while ((c + 1) * total / a.ctas <= last) ++c;
-      while (c * total / a.ctas > last) --c;
-      a.desc[blockIdx.x] = make_int2(item, int(c));
+    if (tid < NW) {
+      run.item = sh.litem[tid];
+      run.head = tid;
+      w = tid + 1;
+    } else {
+      while (w < NW && sh.fitem[w] == kInt4NoWork) ++w;
+      if (w < NW) run.item = sh.fitem[w];
     }
-    if (!__syncthreads_or(open) && tid == 0) a.desc[blockIdx.x] = make_int2(-1, 0);
+    if (run.item >= 0) {
+      run.from = run.to = w;
+      for (; w < NW && !end; ++w) {
+        if (sh.fitem[w] == kInt4NoWork) continue;
+        if (sh.fitem[w] != run.item) break;
+        run.to = w + 1;
+        end = sh.fend[w] != 0;
+      }
+      if (tid < NW) {
+        run.slot = end || a.item_ctas ? -1 : 2 * int(blockIdx.x) + 1;
+        if (!end && !a.item_ctas) {
+          // the merge's descriptor: an item that starts here and goes on, and the
+          // CTA that holds its last pair
+          const long long last = sh.last[tid];
+          long long to = last * a.ctas / total;
+          while ((to + 1) * total / a.ctas <= last) ++to;
+          while (to * total / a.ctas > last) --to;
+          a.desc[blockIdx.x] = make_int2(run.item, int(to));
+        }
+      }
+    }
+    sh.run[tid] = run;
+    // (whoever found an item that goes on has written the descriptor)
+    const unsigned open = __ballot_sync((1u << (NW + 1)) - 1u, run.item >= 0 && tid < NW && !end);
+    if (tid == 0 && open == 0u && !a.item_ctas) a.desc[blockIdx.x] = make_int2(-1, 0);
+  }
+  __syncthreads();
+  const int rows = a.group * (D / 4);
+  for (int e = tid; e < (NW + 1) * rows; e += NW * 32) {
+    const I4Run run = sh.run[e / rows];
+    if (run.item < 0) continue;
+    const int h = e % rows / (D / 4), d = e % (D / 4) * 4;
+    float M = -INFINITY, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = run.head >= 0 ? run.from - 1 : run.from; w < run.to; ++w) {
+      const float* p;
+      if (w < run.from) {
+        p = reinterpret_cast<const float*>(smem + size_t(run.head) * STAGES * C::STAGE_BYTES);
+      } else {
+        if (sh.fitem[w] == kInt4NoWork) continue;
+        p = reinterpret_cast<const float*>(smem + C::RING_BYTES) + w * C::PIECE_FLOATS;
+      }
+      const float m = p[H * D + h], l = p[H * D + H + h];
+      const float4 x = *reinterpret_cast<const float4*>(p + h * D + d);
+      const float top = fmaxf(M, m), ref = top == -INFINITY ? 0.f : top;
+      const float wa = fast_exp2(M - ref), wb2 = fast_exp2(m - ref);
+      M = top;
+      den = den * wa + l * wb2;
+      num.x = num.x * wa + x.x * wb2;
+      num.y = num.y * wa + x.y * wb2;
+      num.z = num.z * wa + x.z * wb2;
+      num.w = num.w * wa + x.w * wb2;
+    }
+    const int is = run.item / Hkv, ig = run.item - is * Hkv;
+    if (run.slot < 0) {
+      const float inv = 1.f / den;
+      T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(is) * a.num_q_heads + ig * a.group + h) * D + d) =
+          *reinterpret_cast<const uint2*>(x);
+    } else {
+      *reinterpret_cast<float4*>(a.part_o + (size_t(run.slot) * a.group + h) * D + d) = num;
+      if (d == 0) a.part_ml[size_t(run.slot) * a.group + h] = make_float2(M, den);
+    }
   }
 }
 
