@@ -889,7 +889,8 @@ pkv_status_t cache_int4(bool gather, const char* what, const void* k, const void
   if (!k || !v || !kv_cache || !slot_mapping) return pkv::fail(PKV_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(kv_cache, 16) || !aligned(slot_mapping, 8))
     return pkv::fail(PKV_ERR_INVALID_ARG, "k, v and kv_cache must be 16-byte aligned, slot_mapping 8-byte aligned");
-  if (int64_t(num_tokens) * num_kv_heads > int64_t(INT32_MAX) * 8)
+  // (a thread takes 8 elements of a K or V row, and has a 32-bit index)
+  if (int64_t(num_tokens) * num_kv_heads * (head_dim / 4) > int64_t(INT32_MAX))
     return pkv::fail(PKV_ERR_UNSUPPORTED, "too many tokens for one launch");
   unsigned int* status = nullptr;
   pkv_status_t st = status_word(&status);

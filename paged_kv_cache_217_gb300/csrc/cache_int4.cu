@@ -2,13 +2,16 @@
 // write, the read of stored rows back to 16 bits, and the copy of blocks of a
 // cache held in one pool.
 //
-// Write and read take one warp per (token, KV head): lane l holds D/32
-// consecutive dims, so the 64 dims of a group sit in 2048/D neighbouring lanes
-// whose minimum and maximum are joined by shuffles. Both are bound by bytes
-// (4 D read and 9 D / 4 written per row pair, or the reverse).
+// Write and read give a row of K or V D/8 lanes of 8 dims (one code word) each:
+// 16-byte accesses of the 16-bit rows, and a warp holds the K and V rows of one
+// (token, KV head) at D = 128 (of two at 64; one of the two rows at 256). The 64
+// dims of a group sit in 8 lanes. One lane per D/32 dims of both rows, with the
+// IEEE division of every element, took 190 instructions a row and 63 us for
+// writing and reading back 12k tokens of 8 heads, against INT4_RW_US.
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "int4_layout.cuh"
@@ -18,158 +21,197 @@ namespace pkv {
 namespace {
 
 template <typename T>
-__device__ __forceinline__ float to_f32(T x);
+__device__ __forceinline__ uint16_t round_bits(float x);  // x rounded to T, its bits
 template <>
-__device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
+__device__ __forceinline__ uint16_t round_bits<__half>(float x) { return __half_as_ushort(__float2half_rn(x)); }
 template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ uint16_t round_bits<__nv_bfloat16>(float x) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
 template <typename T>
-__device__ __forceinline__ T from_f32(float x);
+__device__ __forceinline__ float from_bits(uint16_t b);
 template <>
-__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+__device__ __forceinline__ float from_bits<__half>(uint16_t b) { return __half2float(__ushort_as_half(b)); }
 template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+__device__ __forceinline__ float from_bits<__nv_bfloat16>(uint16_t b) {
+  return __uint_as_float(uint32_t(b) << 16);
+}
 
-template <int BYTES>
-struct Piece;  // a register of BYTES bytes
-template <> struct Piece<1> { using type = unsigned char; };
-template <> struct Piece<2> { using type = unsigned short; };
-template <> struct Piece<4> { using type = uint32_t; };
-template <> struct Piece<8> { using type = uint2; };
-template <> struct Piece<16> { using type = uint4; };
+// Division of n < 2^31 by a fixed d: (n * mul) >> (32 + shift) with mul = floor(2^(31
+// + l) / d) + 1 and l = ceil(log2 d) = shift + 1 (d = 1 by itself).
+struct Divisor {
+  uint32_t d, mul, shift;
+  explicit Divisor(uint32_t div) : d(div), mul(0), shift(0) {
+    uint32_t l = 0;
+    while ((uint64_t(1) << l) < d) ++l;
+    if (l == 0) return;
+    mul = uint32_t((uint64_t(1) << (31 + l)) / d + 1);
+    shift = l - 1;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return d == 1 ? n : __umulhi(n, mul) >> shift; }
+};
 
-// One lane's D/32 dims of a row quantised with its group, as packed codes
-// (dim i in bits 4 i), and the group's {s, z}.
-template <typename T, int D>
-__device__ __forceinline__ uint32_t quantize_group(const T* xs, T& s_out, T& z_out) {
-  constexpr int E = D / 32;
-  float x[E], lo = INFINITY, hi = -INFINITY;
-  bool bad = false;
+// Which row and word a thread has: K and V rows alternate.
+struct Int4Place {
+  uint32_t token, head, v;  // v: 0 K, 1 V
+  int word;
+};
+template <int D>
+__device__ __forceinline__ Int4Place int4_place(const Divisor& heads) {
+  constexpr uint32_t LPR = D / 8;  // lanes of a row
+  const uint32_t i = blockIdx.x * 256u + threadIdx.x, row = i / LPR;
+  Int4Place p;
+  p.word = int(i % LPR);
+  p.v = row & 1u;
+  p.token = heads(row >> 1);
+  p.head = (row >> 1) - p.token * heads.d;
+  return p;
+}
+
+// Pairs of T.
+template <typename T>
+struct Pair2;
+template <>
+struct Pair2<__half> {
+  using type = __half2;
+  static __device__ __forceinline__ type make(__half a, __half b) { return __halves2half2(a, b); }
+};
+template <>
+struct Pair2<__nv_bfloat16> {
+  using type = __nv_bfloat162;
+  static __device__ __forceinline__ type make(__nv_bfloat16 a, __nv_bfloat16 b) { return __halves2bfloat162(a, b); }
+};
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: adding it to 0 <= x < 2^22 rounds x to an integer, ties to even
+
+// Eight dims of a row quantised with their group (8 neighbouring lanes): codes,
+// and the group's {s, z}. Minimum and maximum are taken in T (exactly, NaN
+// spreading), as one pair (min, -max) across the lanes. The quotient a / b of the
+// definition is a times an approximate 1 / b, whose error (a few 2^-24 of at most
+// 15) matters only next to a half, where the IEEE quotient decides; so it does
+// for subnormal s, which can send x past code 15.
+template <typename T>
+__device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
+  using T2 = typename Pair2<T>::type;
+  const T2* e = reinterpret_cast<const T2*>(&u);
+  const T2 mn = __hmin2_nan(__hmin2_nan(e[0], e[1]), __hmin2_nan(e[2], e[3]));
+  const T2 mx = __hmax2_nan(__hmax2_nan(e[0], e[1]), __hmax2_nan(e[2], e[3]));
+  T2 both = Pair2<T>::make(__hmin_nan(mn.x, mn.y), __hneg(__hmax_nan(mx.x, mx.y)));
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    x[i] = to_f32<T>(xs[i]);
-    bad |= !(fabsf(x[i]) < INFINITY);
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
+  for (int m = 1; m < 8; m <<= 1) {
+    const uint32_t other = __shfl_xor_sync(kFull, *reinterpret_cast<const uint32_t*>(&both), m);
+    both = __hmin2_nan(both, *reinterpret_cast<const T2*>(&other));
   }
-  constexpr int LANES = kInt4Group / E;  // lanes of a group
-#pragma unroll
-  for (int m = 1; m < LANES; m <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(kFull, lo, m));
-    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, m));
-  }
-  const unsigned groups = __ballot_sync(kFull, bad);
-  const unsigned mine = LANES == 32 ? kFull : ((1u << (LANES & 31)) - 1u) << ((threadIdx.x & 31) / LANES * LANES & 31);
-  if (groups & mine) {
-    s_out = z_out = from_f32<T>(NAN);
-    return 0u;
-  }
-  s_out = from_f32<T>(__fdiv_rn(__fsub_rn(0.5f * hi, 0.5f * lo), 7.5f));
-  z_out = from_f32<T>(lo);
-  const float half_s = 0.5f * to_f32<T>(s_out), half_z = 0.5f * lo;
+  const float half_z = 0.5f * float(both.x), range = -0.5f * float(both.y) - half_z;  // 0.5 max - 0.5 min
+  const bool finite = fabsf(range) < INFINITY;
+  const uint16_t s = round_bits<T>(__fdiv_rn(range, 7.5f));
+  const uint32_t nan = round_bits<T>(NAN);
+  pair = finite ? uint32_t(s) | (uint32_t(round_bits<T>(float(both.x))) << 16) : nan | (nan << 16);
+  const float half_s = 0.5f * from_bits<T>(s);
+  const float inv = __fdividef(1.f, half_s);
+  float x[8];
+  Vec8<T>::to_float(u, x);
   uint32_t codes = 0;
-  if (half_s > 0.f) {
+  bool near = !(half_s >= (sizeof(T) == 2 && std::is_same<T, __half>::value ? 0x1p-14f : 0x1p-100f));
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(0.5f * x[i], half_z), half_s)), 0.f), 15.f);
-      codes |= uint32_t(c) << (4 * i);
+  for (int i = 7; i >= 0; --i) {
+    const float q = fmaf(x[i], 0.5f, -half_z) * inv, r = q + kMagic;
+    near |= fabsf(q - (r - kMagic)) > 0.49999f;
+    codes = codes * 16u + __float_as_uint(r);  // r's bits are those of kMagic plus the code
+  }
+  codes -= 0x4B400000u * 0x11111111u;
+  if (near) {
+    codes = 0;
+    if (half_s > 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float c = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(0.5f * x[i], half_z), half_s)), 0.f), 15.f);
+        codes |= uint32_t(c) << (4 * i);
+      }
     }
   }
-  return codes;
+  return finite ? codes : 0u;
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t pack_pair(T s, T z) {
-  unsigned short a, b;
-  memcpy(&a, &s, 2);
-  memcpy(&b, &z, 2);
-  return uint32_t(a) | (uint32_t(b) << 16);
+// Byte offsets in a tile of a thread's word and of its group's pair, for slot r.
+template <int D>
+__device__ __forceinline__ int word_offset(const Int4Place& p, int r) {
+  return p.v ? kv4_v_word<D>(r, p.word) : kv4_k_word<D>(r, p.word);
+}
+template <int D>
+__device__ __forceinline__ int pair_offset(const Int4Place& p, int r) {
+  return (16 + p.v) * D + kv4_row(r) * (D / 16) + 4 * (p.word / 8);
 }
 
-template <typename T, int D>
+// U tokens per thread, `stride` apart, all their loads in flight together: large
+// calls take 4, small ones 1 (more CTAs).
+template <typename T, int D, int U>
 __global__ void __launch_bounds__(256)
-reshape_and_cache_int4_kernel(const T* __restrict__ k, const T* __restrict__ v, unsigned char* __restrict__ cache,
-                              const int64_t* __restrict__ slots, int64_t rows, int num_kv_heads, int64_t num_slots,
-                              unsigned int* status) {
+reshape_and_cache_int4_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
+                              unsigned char* __restrict__ cache, const int64_t* __restrict__ slots, uint32_t tokens,
+                              uint32_t stride, const Divisor heads, int64_t num_slots, unsigned int* status) {
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int E = D / 32;
-  using In = typename Piece<2 * E>::type;
-  const int64_t row = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;  // warp-uniform
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int g = int(row % num_kv_heads);
-  const int64_t t = row / num_kv_heads;
-  const int64_t slot = __ldg(slots + t);
-  const In kx = __ldg(reinterpret_cast<const In*>(k + row * D) + lane);
-  const In vx = __ldg(reinterpret_cast<const In*>(v + row * D) + lane);
-  if (slot < 0) return;
-  if (slot >= num_slots) {
-    if (g == 0 && lane == 0) flag(status, PKV_DEV_BAD_SLOT);
-    return;
-  }
-  unsigned char* tile = cache + ((slot / kBlock) * num_kv_heads + g) * kv4_tile_bytes(D);
-  const int r = int(slot % kBlock);
-  T ks, kz, vs, vz;
-  const uint32_t kc = quantize_group<T, D>(reinterpret_cast<const T*>(&kx), ks, kz);
-  const uint32_t vc = quantize_group<T, D>(reinterpret_cast<const T*>(&vx), vs, vz);
-  using Out = typename Piece<E / 2>::type;
-  constexpr int LPW = 8 / E;  // lanes of one word
-  const int w = lane / LPW, sub = (lane % LPW) * (E / 2);
-  *reinterpret_cast<Out*>(tile + kv4_k_word<D>(r, w) + sub) = Out(kc);
-  *reinterpret_cast<Out*>(tile + kv4_v_word<D>(r, w) + sub) = Out(vc);
-  constexpr int LANES = kInt4Group / E;
-  if (lane % LANES == 0) {
-    *reinterpret_cast<uint32_t*>(tile + kv4_k_pair<D>(r, lane / LANES)) = pack_pair<T>(ks, kz);
-    *reinterpret_cast<uint32_t*>(tile + kv4_v_pair<D>(r, lane / LANES)) = pack_pair<T>(vs, vz);
-  }
-}
-
-// One lane's D/32 dims of a stored row, rounded once to T.
-template <typename T, int D>
-__device__ __forceinline__ typename Piece<D / 16>::type read_group(uint32_t codes, uint32_t pair) {
-  constexpr int E = D / 32;
-  typename Piece<2 * E>::type out;
-  T* o = reinterpret_cast<T*>(&out);
-  unsigned short a = (unsigned short)(pair & 0xffffu), b = (unsigned short)(pair >> 16);
-  T s, z;
-  memcpy(&s, &a, 2);
-  memcpy(&z, &b, 2);
-  const float sf = to_f32<T>(s), zf = to_f32<T>(z);
+  const Int4Place p = int4_place<D>(heads);
+  const uint4* src = (p.v ? v : k) + p.head * (D / 8) + p.word;
+  int64_t slot[U];
+  uint4 x[U];
 #pragma unroll
-  for (int i = 0; i < E; ++i) o[i] = from_f32<T>(fmaf(float((codes >> (4 * i)) & 15u), sf, zf));
-  return out;
+  for (int u = 0; u < U; ++u) {
+    const uint32_t t = p.token + u * stride;
+    const bool in = p.token < stride && t < tokens;  // (whole groups of 8 lanes; the others help the shuffles)
+    slot[u] = in ? __ldg(slots + t) : -1;
+    x[u] = in ? __ldg(src + size_t(t) * heads.d * (D / 8)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t pair;
+    const uint32_t codes = quantize8<T>(x[u], pair);
+    if (slot[u] < 0) continue;
+    if (slot[u] >= num_slots) {
+      if (p.head == 0 && p.word == 0) flag(status, PKV_DEV_BAD_SLOT);
+      continue;
+    }
+    unsigned char* tile = cache + ((slot[u] / kBlock) * heads.d + p.head) * kv4_tile_bytes(D);
+    const int r = int(slot[u] % kBlock);
+    *reinterpret_cast<uint32_t*>(tile + word_offset<D>(p, r)) = codes;
+    if (p.word % 8 == 0) *reinterpret_cast<uint32_t*>(tile + pair_offset<D>(p, r)) = pair;
+  }
 }
 
-template <typename T, int D>
+template <typename T, int D, int U>
 __global__ void __launch_bounds__(256)
-gather_cache_int4_kernel(T* __restrict__ k, T* __restrict__ v, const unsigned char* __restrict__ cache,
-                         const int64_t* __restrict__ slots, int64_t rows, int num_kv_heads, int64_t num_slots,
-                         unsigned int* status) {
-  constexpr int E = D / 32;
-  using Row = typename Piece<2 * E>::type;
-  using In = typename Piece<E / 2>::type;
-  const int64_t row = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const int g = int(row % num_kv_heads);
-  const int64_t slot = __ldg(slots + row / num_kv_heads);
-  Row kx{}, vx{};
-  if (slot >= num_slots) {
-    if (g == 0 && lane == 0) flag(status, PKV_DEV_BAD_SLOT);
-  } else if (slot >= 0) {
-    const unsigned char* tile = cache + ((slot / kBlock) * num_kv_heads + g) * kv4_tile_bytes(D);
-    const int r = int(slot % kBlock);
-    constexpr int LPW = 8 / E, LANES = kInt4Group / E;
-    const int w = lane / LPW, sub = (lane % LPW) * (E / 2);
-    const uint32_t kc = *reinterpret_cast<const In*>(tile + kv4_k_word<D>(r, w) + sub);
-    const uint32_t vc = *reinterpret_cast<const In*>(tile + kv4_v_word<D>(r, w) + sub);
-    const uint32_t kp = *reinterpret_cast<const uint32_t*>(tile + kv4_k_pair<D>(r, lane / LANES));
-    const uint32_t vp = *reinterpret_cast<const uint32_t*>(tile + kv4_v_pair<D>(r, lane / LANES));
-    kx = read_group<T, D>(kc, kp);
-    vx = read_group<T, D>(vc, vp);
+gather_cache_int4_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const unsigned char* __restrict__ cache,
+                         const int64_t* __restrict__ slots, uint32_t tokens, uint32_t stride, const Divisor heads,
+                         int64_t num_slots, unsigned int* status) {
+  const Int4Place p = int4_place<D>(heads);
+  if (p.token >= stride) return;
+  uint4* dst = (p.v ? v : k) + p.head * (D / 8) + p.word;
+  int64_t slot[U];
+  uint32_t codes[U], pair[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) slot[u] = p.token + u * stride < tokens ? __ldg(slots + p.token + u * stride) : -1;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    codes[u] = pair[u] = 0u;  // zeros for slots < 0
+    if (slot[u] >= num_slots) {
+      if (p.head == 0 && p.word == 0) flag(status, PKV_DEV_BAD_SLOT);
+    } else if (slot[u] >= 0) {
+      const unsigned char* tile = cache + ((slot[u] / kBlock) * heads.d + p.head) * kv4_tile_bytes(D);
+      const int r = int(slot[u] % kBlock);
+      codes[u] = *reinterpret_cast<const uint32_t*>(tile + word_offset<D>(p, r));
+      pair[u] = *reinterpret_cast<const uint32_t*>(tile + pair_offset<D>(p, r));
+    }
   }
-  reinterpret_cast<Row*>(k + row * D)[lane] = kx;
-  reinterpret_cast<Row*>(v + row * D)[lane] = vx;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint32_t t = p.token + u * stride;
+    if (t >= tokens) continue;
+    const float s = from_bits<T>(uint16_t(pair[u] & 0xffffu)), z = from_bits<T>(uint16_t(pair[u] >> 16));
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // (a code as a float: its bits under those of 2^23)
+      x[i] = fmaf(__uint_as_float(((codes[u] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f, s, z);
+    dst[size_t(t) * heads.d * (D / 8)] = Vec8<T>::from_float(x);
+  }
 }
 
 constexpr int kCopyThreads = 256;
@@ -198,29 +240,42 @@ copy_blocks_pool_kernel(uint4* __restrict__ pool, const int64_t* __restrict__ pa
   }
 }
 
-template <typename T, int D>
-cudaError_t write_or_gather(bool gather, void* k, void* v, void* cache, const int64_t* slots, int64_t rows,
-                            int num_kv_heads, int64_t num_slots, unsigned int* status, cudaStream_t stream) {
-  const unsigned ctas = unsigned((rows + 7) / 8);  // 8 warps (rows) per CTA
+template <typename T, int D, int U>
+cudaError_t write_or_gather_u(bool gather, void* k, void* v, void* cache, const int64_t* slots, uint32_t tokens,
+                              uint32_t heads, int64_t num_slots, unsigned int* status, cudaStream_t stream) {
+  const uint32_t stride = (tokens + U - 1) / U;
+  const unsigned ctas = unsigned((uint64_t(stride) * heads * 2 * (D / 8) + 255) / 256);
   if (gather)
-    gather_cache_int4_kernel<T, D><<<ctas, 256, 0, stream>>>(static_cast<T*>(k), static_cast<T*>(v),
-                                                             static_cast<const unsigned char*>(cache), slots, rows,
-                                                             num_kv_heads, num_slots, status);
+    gather_cache_int4_kernel<T, D, U><<<ctas, 256, 0, stream>>>(
+        static_cast<uint4*>(k), static_cast<uint4*>(v), static_cast<const unsigned char*>(cache), slots, tokens, stride,
+        Divisor(heads), num_slots, status);
   else
-    reshape_and_cache_int4_kernel<T, D><<<ctas, 256, 0, stream>>>(static_cast<const T*>(k), static_cast<const T*>(v),
-                                                                  static_cast<unsigned char*>(cache), slots, rows,
-                                                                  num_kv_heads, num_slots, status);
+    reshape_and_cache_int4_kernel<T, D, U><<<ctas, 256, 0, stream>>>(
+        static_cast<const uint4*>(k), static_cast<const uint4*>(v), static_cast<unsigned char*>(cache), slots, tokens,
+        stride, Divisor(heads), num_slots, status);
   return cudaGetLastError();
 }
 
+// Calls of more than kFewThreads threads at one token each (two waves of full
+// SMs) take 4 tokens a thread.
+constexpr uint64_t kFewThreads = 2ull * 152 * 2048;
+
+template <typename T, int D>
+cudaError_t write_or_gather(bool gather, void* k, void* v, void* cache, const int64_t* slots, uint32_t tokens,
+                            uint32_t heads, int64_t num_slots, unsigned int* status, cudaStream_t stream) {
+  return uint64_t(tokens) * heads * 2 * (D / 8) <= kFewThreads
+             ? write_or_gather_u<T, D, 1>(gather, k, v, cache, slots, tokens, heads, num_slots, status, stream)
+             : write_or_gather_u<T, D, 4>(gather, k, v, cache, slots, tokens, heads, num_slots, status, stream);
+}
+
 template <typename T>
-cudaError_t write_or_gather_t(bool gather, void* k, void* v, void* cache, const int64_t* slots, int64_t rows,
-                              int num_kv_heads, int head_dim, int64_t num_slots, unsigned int* status,
+cudaError_t write_or_gather_t(bool gather, void* k, void* v, void* cache, const int64_t* slots, uint32_t tokens,
+                              uint32_t heads, int head_dim, int64_t num_slots, unsigned int* status,
                               cudaStream_t stream) {
   switch (head_dim) {
-    case 64: return write_or_gather<T, 64>(gather, k, v, cache, slots, rows, num_kv_heads, num_slots, status, stream);
-    case 128: return write_or_gather<T, 128>(gather, k, v, cache, slots, rows, num_kv_heads, num_slots, status, stream);
-    case 256: return write_or_gather<T, 256>(gather, k, v, cache, slots, rows, num_kv_heads, num_slots, status, stream);
+    case 64: return write_or_gather<T, 64>(gather, k, v, cache, slots, tokens, heads, num_slots, status, stream);
+    case 128: return write_or_gather<T, 128>(gather, k, v, cache, slots, tokens, heads, num_slots, status, stream);
+    case 256: return write_or_gather<T, 256>(gather, k, v, cache, slots, tokens, heads, num_slots, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -230,10 +285,11 @@ cudaError_t write_or_gather_t(bool gather, void* k, void* v, void* cache, const 
 cudaError_t launch_cache_int4(bool gather, void* k, void* v, bool bf16, void* cache, const int64_t* slots,
                               int num_tokens, int num_kv_heads, int head_dim, int num_blocks, unsigned int* status,
                               cudaStream_t stream) {
-  const int64_t rows = int64_t(num_tokens) * num_kv_heads, num_slots = int64_t(num_blocks) * kBlock;
-  return bf16 ? write_or_gather_t<__nv_bfloat16>(gather, k, v, cache, slots, rows, num_kv_heads, head_dim, num_slots,
-                                                 status, stream)
-              : write_or_gather_t<__half>(gather, k, v, cache, slots, rows, num_kv_heads, head_dim, num_slots, status,
+  const int64_t num_slots = int64_t(num_blocks) * kBlock;
+  const uint32_t tokens = uint32_t(num_tokens), heads = uint32_t(num_kv_heads);
+  return bf16 ? write_or_gather_t<__nv_bfloat16>(gather, k, v, cache, slots, tokens, heads, head_dim, num_slots, status,
+                                                 stream)
+              : write_or_gather_t<__half>(gather, k, v, cache, slots, tokens, heads, head_dim, num_slots, status,
                                           stream);
 }
 
