@@ -54,92 +54,112 @@ __device__ __forceinline__ Scan scan_of(int32_t* p, int S) {
   return Scan{p, p + S, p + 2 * S + 1, p + 3 * S + 2, p + 4 * S + 2, p + 5 * S + 2, p + 6 * S + 2};
 }
 
-// Exclusive scan over the CTA; every thread calls it. total: the CTA's sum.
-template <typename V>
-__device__ __forceinline__ V cta_exclusive(V v, V* warp_sum, V& total) {
+// Exclusive scans of C values over the CTA; every thread calls it. total: the
+// CTA's sums.
+template <typename V, int C>
+__device__ __forceinline__ void cta_exclusive(V (&v)[C], V (*warp_sum)[C], V (&total)[C]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  V x = v;
+  V x[C];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const V n = __shfl_up_sync(kFull, x, o);
-    if (lane >= o) x += n;
+  for (int c = 0; c < C; ++c) {
+    x[c] = v[c];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const V n = __shfl_up_sync(kFull, x[c], o);
+      if (lane >= o) x[c] += n;
+    }
   }
   __syncthreads();  // earlier readers of warp_sum are done
-  if (lane == 31) warp_sum[warp] = x;
+  if (lane == 31) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) warp_sum[warp][c] = x[c];
+  }
   __syncthreads();
-  if (warp == 0) {
-    V w = lane < kThreads / 32 ? warp_sum[lane] : V(0);
+  if (warp < C) {  // warp c scans value c of the warps' sums
+    V w = warp_sum[lane][warp];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const V n = __shfl_up_sync(kFull, w, o);
       if (lane >= o) w += n;
     }
-    warp_sum[lane] = w;
+    warp_sum[lane][warp] = w;
   }
   __syncthreads();
-  total = warp_sum[kThreads / 32 - 1];
-  return x - v + (warp ? warp_sum[warp - 1] : V(0));
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    total[c] = warp_sum[kThreads / 32 - 1][c];
+    v[c] = x[c] - v[c] + (warp ? warp_sum[warp - 1][c] : V(0));
+  }
 }
 
 // Phase 1, one CTA of kThreads threads.
 __device__ __forceinline__ void scan_batch(const ExtendArgs& a, const Scan& w) {
-  __shared__ long long wsum[32];
+  __shared__ long long wsum[32][2];
   __shared__ unsigned int flags;
   const int S = a.num_seqs;
   const long long max_len = (long long)a.max_blocks * kBlock;
   if (threadIdx.x == 0) flags = 0u;
   __syncthreads();
-  unsigned int bad = 0u;
+  const int count = *a.free_count;
+  unsigned int bad = count < 0 || count > a.num_blocks ? PKV_DEV_BAD_BLOCK_ID : 0u;
   bool sharing = false;
+  int n = 0, L = 0, last = -1;  // (kept for a batch of one sequence a thread)
   for (int s = threadIdx.x; s < S; s += kThreads) {
-    const long long L = a.context_lens[s], n = a.new_tokens[s];
-    const bool ok = L >= 0 && n >= 0 && L + n <= max_len;
-    if (!ok) bad |= PKV_DEV_BAD_CONTEXT_LEN;
-    int last = -1;
-    if (ok && a.refcounts && n > 0 && L % kBlock) {
+    L = a.context_lens[s];
+    n = a.new_tokens[s];
+    const bool ok = L >= 0 && n >= 0 && (long long)L + n <= max_len;
+    if (!ok) {
+      bad |= PKV_DEV_BAD_CONTEXT_LEN;
+      L = n = 0;  // the call fails
+    }
+    last = -1;
+    if (a.refcounts && n > 0 && L % kBlock) {
       const int b = a.block_tables[size_t(s) * a.max_blocks + L / kBlock];
       if (b >= 0 && b < a.num_blocks && a.refcounts[b] > 1) last = b;  // a bad id is flagged where it is used
     }
     sharing |= last >= 0;
-    w.len[s] = ok ? int(L) : 0;
+    w.len[s] = L;
     w.last[s] = last;
   }
-  const int count = *a.free_count;
-  if (count < 0 || count > a.num_blocks) bad |= PKV_DEV_BAD_BLOCK_ID;
   if (bad) atomicOr(&flags, bad);
   const bool any_sharing = __syncthreads_or(sharing);
 
   long long tok0 = 0, blk0 = 0, pair0 = 0;
   for (int base = 0; base < S; base += kThreads) {
     const int s = base + threadIdx.x;
-    long long n = 0, fresh = 0;
+    long long v[2] = {0, 0}, total[2];
     int cow = 0;
     if (s < S) {
-      const long long L = a.context_lens[s];
-      n = a.new_tokens[s];
-      if (L < 0 || n < 0 || L + n > max_len) n = 0;  // the call fails
-      else fresh = (L + n + kBlock - 1) / kBlock - (L + kBlock - 1) / kBlock;
-      const int b = any_sharing ? w.last[s] : -1;
-      if (b >= 0) {
-        int rank = 0;
-        for (int e = 0; e < s; ++e) rank += w.last[e] == b ? 1 : 0;
-        cow = a.refcounts[b] - rank > 1 ? 1 : 0;
+      if (S > kThreads) {
+        L = w.len[s];
+        last = w.last[s];
+        n = a.new_tokens[s];
+        const long long raw = a.context_lens[s];
+        if (raw < 0 || n < 0 || raw + n > max_len) n = 0;
       }
+      if (any_sharing && last >= 0) {
+        int rank = 0;
+        for (int e = 0; e < s; ++e) rank += w.last[e] == last ? 1 : 0;
+        cow = a.refcounts[last] - rank > 1 ? 1 : 0;
+      }
+      v[0] = n;
+      v[1] = (L + n + kBlock - 1) / kBlock - (L + kBlock - 1) / kBlock + cow;
     }
-    long long total;
-    const long long t = tok0 + cta_exclusive<long long>(n, wsum, total);
-    tok0 += total;
-    const long long bl = blk0 + cta_exclusive<long long>(fresh + cow, wsum, total);
-    blk0 += total;
+    cta_exclusive<long long, 2>(v, wsum, total);
+    const long long t = tok0 + v[0], bl = blk0 + v[1];
+    tok0 += total[0];
+    blk0 += total[1];
     long long pr = pair0;
     if (any_sharing) {
-      pr += cta_exclusive<long long>(cow, wsum, total);
-      pair0 += total;
+      long long c[2] = {cow, 0}, all[2];
+      cta_exclusive<long long, 2>(c, wsum, all);
+      pr += c[0];
+      pair0 += all[0];
     }
     if (s < S) {
       w.tok[s] = int(t < INT_MAX ? t : INT_MAX);
       w.blk[s] = int(bl < INT_MAX ? bl : INT_MAX);
-      w.cow[s] = cow ? w.last[s] : -1;
+      w.cow[s] = cow ? last : -1;
       w.pair[s] = int(pr);
     }
   }
@@ -312,7 +332,7 @@ __global__ void __launch_bounds__(256) drop_kernel(const ReleaseArgs a) {
 // Pushes the marked blocks onto the free stack in ascending order (whatever
 // order the atomics above took). One CTA.
 __global__ void __launch_bounds__(kThreads) push_kernel(const ReleaseArgs a) {
-  __shared__ int wsum[32];
+  __shared__ int wsum[32][1];
   const int words = (a.num_blocks + 31) / 32;
   int count = *a.free_count;
   __syncthreads();
@@ -323,13 +343,14 @@ __global__ void __launch_bounds__(kThreads) push_kernel(const ReleaseArgs a) {
   for (int base = 0; base < words; base += kThreads) {
     const int i = base + threadIdx.x;
     unsigned int m = i < words ? a.bitmap[i] : 0u;
-    int total;
-    int at = count + cta_exclusive<int>(__popc(m), wsum, total);
+    int v[1] = {__popc(m)}, total[1];
+    cta_exclusive<int, 1>(v, wsum, total);
+    int at = count + v[0];
     for (; m; m &= m - 1u, ++at) {
       if (at < a.num_blocks) a.free_stack[at] = 32 * i + __ffs(int(m)) - 1;
       else flag(a.status, PKV_DEV_BAD_BLOCK_ID);  // more blocks than the pool has
     }
-    count += total;
+    count += total[0];
   }
   if (threadIdx.x == 0) *a.free_count = count < a.num_blocks ? count : a.num_blocks;
 }
