@@ -271,15 +271,16 @@ pkv_status_t pool_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, i
 }
 
 // A latent cache [num_blocks][16][576] as a 4-D tensor {64 elements, 8 rows, 9
-// chunks of 64, 2 * num_blocks groups of 8 rows}, read a block at a time: the
-// copy lays a block out as two groups of 9 swizzled 8-row x 128-byte atoms.
+// chunks of 64, 2 * num_blocks groups of 8 rows}, read a third of a block (3
+// chunks) at a time, which lands as two groups of 3 swizzled 8-row x 128-byte
+// atoms.
 pkv_status_t latent_tensor_map(CUtensorMap* map, const void* cache, int num_blocks, pkv_dtype_t dtype) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t row = cuuint64_t(pkv::kLatentRow) * 2;
   const cuuint64_t dims[4] = {64, 8, pkv::kLatentRow / 64, cuuint64_t(num_blocks) * 2};
   const cuuint64_t strides[3] = {row, 128, 8 * row};
-  const cuuint32_t box[4] = {64, 8, pkv::kLatentRow / 64, 2};
+  const cuuint32_t box[4] = {64, 8, 3, 2};
   const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                          4, const_cast<void*>(cache), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -289,18 +290,19 @@ pkv_status_t latent_tensor_map(CUtensorMap* map, const void* cache, int num_bloc
   return PKV_OK;
 }
 
-// The queries [num_seqs][num_heads][width] of latent attention as a 3-D
-// tensor, read in boxes of one sequence x box_heads heads x 64 columns.
+// The queries [num_seqs][num_heads][width] of latent attention as a 4-D tensor
+// {64 columns, heads, width / 64 chunks, sequences}, read in boxes of all chunks
+// of box_heads heads of one sequence.
 pkv_status_t query_tensor_map(CUtensorMap* map, const void* q, int num_seqs, int num_heads, int width,
                               pkv_dtype_t dtype, int box_heads) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint64_t dims[3] = {cuuint64_t(width), cuuint64_t(num_heads), cuuint64_t(num_seqs)};
-  const cuuint64_t strides[2] = {cuuint64_t(width) * 2, cuuint64_t(width) * 2 * cuuint64_t(num_heads)};
-  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), 1};
-  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  const cuuint64_t dims[4] = {64, cuuint64_t(num_heads), cuuint64_t(width / 64), cuuint64_t(num_seqs)};
+  const cuuint64_t strides[3] = {cuuint64_t(width) * 2, 128, cuuint64_t(width) * 2 * cuuint64_t(num_heads)};
+  const cuuint32_t box[4] = {64, cuuint32_t(box_heads), cuuint32_t(width / 64), 1};
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                         3, const_cast<void*>(q), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         4, const_cast<void*>(q), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled (queries) failed (CUresult %d)", int(r));
@@ -892,6 +894,8 @@ pkv_status_t cache_int4(bool gather, const char* what, const void* k, const void
   // (a thread takes 8 elements of a K or V row, and has a 32-bit index)
   if (int64_t(num_tokens) * num_kv_heads * (head_dim / 4) > int64_t(INT32_MAX))
     return pkv::fail(PKV_ERR_UNSUPPORTED, "too many tokens for one launch");
+  if (int64_t(num_kv_heads) * 18 * head_dim > int64_t(UINT32_MAX))
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "a block of %d heads is over 4 GB", num_kv_heads);
   unsigned int* status = nullptr;
   pkv_status_t st = status_word(&status);
   if (st != PKV_OK) return st;

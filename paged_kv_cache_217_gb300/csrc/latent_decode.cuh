@@ -15,21 +15,26 @@
 //    bits, [N, 64]).
 // With heads on M instead, O would need all 512 columns of tensor memory and
 // leave none for S; transposed it takes 4 N columns, and S^T 2 N (two buffers).
-// A 16-token block (18 KB) arrives by one TMA copy of a 4-D view of the cache,
-// {64 elements, 8 rows, 9 chunks, 8-row groups}, which lays it out as groups of
-// 9 swizzle atoms of 8 rows x 128 bytes: both products step over tokens in
-// strides of 9 KB and over elements in strides of 1 KB. (36 copies of 16 x 64
-// boxes a tile instead took one warp 2700 cycles to issue.) Blocks past the end
-// read the zero fill. The ring holds two tiles; a block's place is free as soon
-// as its 16 tokens have entered O^T.
+// A tile arrives in thirds of 192 elements (3 chunks of 64), each by 4 TMA copies
+// (one a 16-token block) of a 4-D view of the cache {64 elements, 8 rows, 9
+// chunks, 8-row groups}, which lays a third out as groups of 3 swizzle atoms of 8
+// rows x 128 bytes: both products step over tokens in strides of 3 KB and over
+// elements in strides of 1 KB. Blocks past the end read the zero fill. The ring
+// holds two tiles; O^T runs dims outermost, so that a third's place is free, and
+// its next copy under way, while the product still reads the others, and S^T
+// starts on the third that has landed. (Whole blocks at a time, freed by tokens,
+// took 64.6 us for 32 sequences x 4000 tokens x 128 heads against 62.6; 36 copies
+// of 16 x 64 boxes a tile took one warp 2700 cycles to issue.)
 //
 // Warps: 0-7 softmax and output (two of every quarter of tensor memory's lanes,
-// each with half of the heads), 8 copies, 9 MMA issue. The MMA warp issues O^T
-// of the current tile as soon as its weights are there (it frees the ring), also
-// in the middle of S^T of the next, which it issues when its rows have landed:
-// the softmax of tile i overlaps S^T of tile i + 1. Measured issue
-// cost per MMA (M 64: 23 cycles at N 16, 32 at N 64; M 128: 39 and 48) against
-// 16 and 32 cycles to read the A operand at 128 bytes a cycle.
+// each with half of the heads), 8 copies, 9 MMA issue. The MMA warp issues S^T of
+// the next tile as its thirds land, and O^T of the current one as soon as its
+// weights are there, also in the middle of that S^T: the softmax of tile i
+// overlaps S^T of tile i + 1. An MMA reads both operands from shared memory at
+// 128 bytes a cycle: S^T's M 64 takes 32 cycles at N 64, O^T's M 128 48; with the
+// copies' writes a tile costs 2500 cycles of shared memory there, and a CTA
+// measures 2600 a tile, which bounds 64 heads a CTA. With 16 heads (1450 cycles
+// of products a tile) the cache's bytes bound it.
 // The running maximum is a reference that moves only when a score exceeds it
 // by 2^8 (one vote a tile); moving it rescales O^T in tensor memory. Weights
 // are rounded to the cache's type (bf16: 2^-8 relative, one per weight, which
@@ -58,10 +63,12 @@ constexpr int kLatentSoftmax = 256;   // threads of the softmax warps
 constexpr int kLatentThreads = kLatentSoftmax + 64;
 constexpr float kLatentLazy = 8.f;
 constexpr int kLatentAhead = 2;       // tiles between a copy and the prefetch of a later one
-constexpr int kLatentAtom = 1024;                        // 8 rows x 128 bytes
-constexpr int kLatentGroup = kLatentRow / 64 * kLatentAtom;  // 8 tokens: 9 atoms
-constexpr int kLatentBlockBytes = 2 * kLatentGroup;      // 16 tokens
-constexpr int kLatentTileBytes = 4 * kLatentBlockBytes;
+constexpr int kLatentAtom = 1024;                 // 8 rows x 128 bytes
+constexpr int kLatentGroup = 3 * kLatentAtom;     // 8 tokens of a third
+constexpr int kLatentThird = 8 * kLatentGroup;    // 64 tokens x 192 elements
+constexpr int kLatentTileBytes = 3 * kLatentThird;
+// Offset of chunk c (64 elements) of a tile.
+__host__ __device__ constexpr int latent_chunk(int c) { return c / 3 * kLatentThird + c % 3 * kLatentAtom; }
 
 // Descriptors of the sequences that cross ranges: one per sequence {first range,
 // last range} where there are at most as many sequences as ranges, else one per
@@ -138,17 +145,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int x, int y, int z, int w) {
-  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(y),
-               "r"(z), "r"(w)
-               : "memory");
+__device__ __forceinline__ void l2_prefetch(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+// A look at a barrier's phase, without the wait that try_wait may take.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
       : "memory");
+  return done != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -211,7 +219,7 @@ __device__ __forceinline__ int latent_tiles(int L) { return (L + kLatentTile - 1
 // Shared state of a CTA outside the operand buffers.
 template <int N>
 struct LatentShared {
-  uint64_t tile_full[2], block_empty[8];
+  uint64_t third_full[6], third_empty[6];    // slot 0's thirds, slot 1's
   uint64_t q_full, q_empty, s_full[2], p_full, pv_done;
   uint32_t tmem;
   int stop;  // a wait gave up: every role leaves
@@ -286,11 +294,11 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   const int h0 = hb * a.block_heads, heads = min(a.block_heads, a.num_heads - h0);
 
   if (tid == 0) {
-    for (int i = 0; i < 8; ++i) mbar_init(smem_addr(&sh.block_empty[i]), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_addr(&sh.tile_full[i]), 1);
-      mbar_init(smem_addr(&sh.s_full[i]), 1);
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(smem_addr(&sh.third_full[i]), 1);
+      mbar_init(smem_addr(&sh.third_empty[i]), 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(smem_addr(&sh.s_full[i]), 1);
     mbar_init(smem_addr(&sh.q_full), 1);
     mbar_init(smem_addr(&sh.q_empty), 1);
     mbar_init(smem_addr(&sh.p_full), kLatentSoftmax);
@@ -386,9 +394,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       if (elect_one()) {
         const uint32_t qb = smem_addr(&sh.q_full);
         mbar_arrive_expect_tx(qb, C::Q_BYTES);
-#pragma unroll
-        for (int c = 0; c < kLatentRow / 64; ++c)
-          tma_load_3d(smem_addr(q_mem) + c * (N * 128), &q_map, 64 * c, h0, walk.s, qb);
+        tma_load_4d(smem_addr(q_mem), &q_map, 0, h0, 0, walk.s, qb);
       }
       ++seg;
       // Block ids of the segment, 32 at a time and the next 32 ahead: lane l of
@@ -432,23 +438,27 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
           far_id[j] = x < a.num_blocks && (over < 0 || 4 * over + j < next_nb) ? x : -1;
         }
         if (elect_one()) {
-          const uint32_t fb = smem_addr(&sh.tile_full[tile & 1]);
+          const uint32_t fb = smem_addr(&sh.third_full[3 * (tile & 1)]), eb = smem_addr(&sh.third_empty[3 * (tile & 1)]);
           const uint32_t dst = smem_addr(ring) + (tile & 1) * kLatentTileBytes;
-          const uint32_t eb = smem_addr(&sh.block_empty[4 * (tile & 1)]);
           bool go = true;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (tile >= 2) go = go && latent_wait(eb + 8 * j, ((tile >> 1) - 1) & 1, stop, a.status);
-            // (announced only now: block_empty says that the last use's copies,
-            // and with them that phase of tile_full, are over)
-            if (go && j == 0) mbar_arrive_expect_tx(fb, kLatentTileBytes);
-            if (go) tma_load_4d(dst + j * kLatentBlockBytes, &cache_map, 0, 0, 0, 2 * id[j], fb);
+          for (int c = 0; c < 3; ++c) {
+            if (tile >= 2) go = go && latent_wait(eb + 8 * c, ((tile >> 1) - 1) & 1, stop, a.status);
+            // (announced only now: third_empty says that the last use's copies,
+            // and with them that phase of third_full, are over)
+            if (!go) break;
+            mbar_arrive_expect_tx(fb + 8 * c, kLatentThird);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tma_load_4d(dst + c * kLatentThird + j * (2 * kLatentGroup), &cache_map, 0, 0, 3 * c, 2 * id[j], fb + 8 * c);
           }
           // rows that a later copy takes start their way into L2 now, so that the
           // copy, issued when a place is free, waits for L2 only
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            if (far_id[j] >= 0) tma_prefetch_4d(&cache_map, 0, 0, 0, 2 * far_id[j]);
+            if (far_id[j] >= 0)
+              l2_prefetch(static_cast<const T*>(a.cache) + size_t(far_id[j]) * (kBlock * kLatentRow),
+                          kBlock * kLatentRow * sizeof(T));
         }
         __syncwarp();
         ok = !*stop;
@@ -460,7 +470,9 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       // all issued never completes its phase: its wait runs to the limit.
       for (int i = 0; i < 2; ++i) {
         const int uses = tile >= i ? (tile - i) / 2 + 1 : 0;
-        if (uses > 0) mbar_wait_bounded(smem_addr(&sh.tile_full[i]), (uses - 1) & 1, 10000000ull);
+        if (uses > 0)
+          for (int c = 0; c < 3; ++c)
+            mbar_wait_bounded(smem_addr(&sh.third_full[3 * i + c]), (uses - 1) & 1, 10000000ull);
       }
       if (seg > 0) mbar_wait_bounded(smem_addr(&sh.q_full), (seg - 1) & 1, 10000000ull);
     }
@@ -470,7 +482,10 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       constexpr uint32_t id_s = tc_idesc<T>(kLatentTile, N, false), id_o = tc_idesc<T>(128, N, true);
       const uint64_t q_desc = tc_desc(smem_addr(q_mem), 16, 1024), p_desc = tc_desc(smem_addr(p_mem), 16, 1024);
       const uint64_t key_desc = tc_desc(smem_addr(ring), 16, kLatentGroup);
-      const uint64_t val_desc = tc_desc(smem_addr(ring), kLatentAtom, kLatentGroup);
+      uint64_t val_desc[4];  // dims 128 j .. + 127: chunks 2 j and 2 j + 1
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        val_desc[j] = tc_desc(smem_addr(ring) + latent_chunk(2 * j), latent_chunk(2 * j + 1) - latent_chunk(2 * j), kLatentGroup);
       const int n = int(end - begin);
       int qk = 0, pv = 0, seg = 0;      // tiles whose S^T, O^T are issued; segments whose queries are waited for
       bool seg_first = true;            // tile qk starts a segment
@@ -482,59 +497,74 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       }
       // O^T of tile pv, if its weights are there
       auto outputs = [&]() {
-        if (pv >= qk || !mbar_try_wait(smem_addr(&sh.p_full), pv & 1)) return false;
+        if (pv >= qk || !mbar_test(smem_addr(&sh.p_full), pv & 1)) return false;
         tc_fence_after();
-        const uint64_t val = val_desc + (pv & 1) * (kLatentTileBytes >> 4);
+        const uint32_t at = (pv & 1) * (kLatentTileBytes >> 4);
         const bool first = (starts >> (pv & 1)) & 1u;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // 16 tokens: one block
+        for (int j = 0; j < 4; ++j) {    // 128 dims
 #pragma unroll
-          for (int j = 0; j < 4; ++j)  // 128 dims
-            tc_mma(tmem + j * N, val + k * (kLatentBlockBytes >> 4) + j * (2 * kLatentAtom >> 4), p_desc + 2 * k, id_o,
-                   !(first && k == 0));
-          tc_commit(smem_addr(&sh.block_empty[4 * (pv & 1) + k]));
+          for (int k = 0; k < 4; ++k)    // 16 tokens
+            tc_mma(tmem + j * N, val_desc[j] + at + k * (2 * kLatentGroup >> 4), p_desc + 2 * k, id_o, !(first && k == 0));
+          if (j > 0) tc_commit(smem_addr(&sh.third_empty[3 * (pv & 1) + j - 1]));  // (its last chunk is 3 j - 1)
         }
         tc_commit(smem_addr(&sh.pv_done));
         ++pv;
         return true;
       };
-      unsigned long long idle = 0;
-      while (pv < n) {
-        if (outputs()) {
-          idle = 0;
-        } else if (qk < n && qk < pv + 2 &&  // (S^T's buffer: O^T of tile qk - 2 is issued)
-                   mbar_try_wait(smem_addr(&sh.tile_full[qk & 1]), (qk >> 1) & 1) &&
-                   (!seg_first || mbar_try_wait(smem_addr(&sh.q_full), seg & 1))) {
-          tc_fence_after();
-          const uint32_t d = tmem + 4 * N + (qk & 1) * N;
-          const uint64_t key = key_desc + (qk & 1) * (kLatentTileBytes >> 4);
-#pragma unroll
-          for (int c = 0; c < kLatentRow / 64; ++c) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma(d, key + c * (kLatentAtom >> 4) + 2 * k, q_desc + c * (N * 128 >> 4) + 2 * k, id_s, c + k > 0);
-            if (c == 2 || c == 5) outputs();
-          }
-          tc_commit(smem_addr(&sh.s_full[qk & 1]));
-          starts = (starts & ~(1u << (qk & 1))) | (uint32_t(seg_first) << (qk & 1));
-          seg += seg_first ? 1 : 0;
-          seg_first = ++t == walk.last;
-          if (seg_first) {
-            tc_commit(smem_addr(&sh.q_empty));
-            if (walk.next(a)) t = walk.first;
-          }
-          ++qk;
-          idle = 0;
-        } else {
+      // Waits for a barrier, and issues O^T meanwhile.
+      auto ready = [&](uint32_t bar, uint32_t parity) {
+        unsigned long long t0 = 0;
+        for (int polls = 0; !mbar_test(bar, parity); ++polls) {
+          if (outputs()) polls = 0;
+          if ((polls & 63) != 63) continue;
           const unsigned long long now = global_timer_ns();
-          if (idle == 0) idle = now;
-          if (*stop) break;
-          if (now - idle > kWaitLimitNs) {
+          if (polls == 63) t0 = now;
+          if (*stop) return false;
+          if (now - t0 > kWaitLimitNs) {
             *stop = 1;
             flag(a.status, PKV_DEV_WAIT_TIMEOUT);
-            break;
+            return false;
           }
         }
+        return true;
+      };
+      bool ok = true;
+      while (ok && qk < n) {
+        // S^T's buffer: the weights of tile qk - 2 have been read off it
+        if (qk == pv + 2) {
+          ok = ready(smem_addr(&sh.p_full), pv & 1);
+          if (ok) outputs();
+        }
+        if (ok && seg_first) ok = ready(smem_addr(&sh.q_full), seg & 1);
+        const uint32_t d = tmem + 4 * N + (qk & 1) * N, full = smem_addr(&sh.third_full[3 * (qk & 1)]);
+        const uint64_t key = key_desc + (qk & 1) * (kLatentTileBytes >> 4);
+#pragma unroll
+        for (int c = 0; c < kLatentRow / 64; ++c) {
+          if (c >= 3 && c <= 7) outputs();
+          if (c % 3 == 0) {
+            ok = ok && ready(full + 8 * (c / 3), (qk >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tc_mma(d, key + (latent_chunk(c) >> 4) + 2 * k, q_desc + c * (N * 128 >> 4) + 2 * k, id_s, c + k > 0);
+        }
+        if (!ok) break;
+        tc_commit(smem_addr(&sh.s_full[qk & 1]));
+        starts = (starts & ~(1u << (qk & 1))) | (uint32_t(seg_first) << (qk & 1));
+        seg += seg_first ? 1 : 0;
+        seg_first = ++t == walk.last;
+        if (seg_first) {
+          tc_commit(smem_addr(&sh.q_empty));
+          if (walk.next(a)) t = walk.first;
+        }
+        ++qk;
+      }
+      while (ok && pv < n) {
+        ok = ready(smem_addr(&sh.p_full), pv & 1);
+        if (ok) outputs();
       }
       if (*stop) {  // let the products in flight end before the tensor memory is freed
         const uint32_t bar = smem_addr(&sh.drain);
@@ -644,7 +674,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
           const int dead = min(kLatentTile, (left + kBlock - 1) / kBlock * kBlock) - left;
           for (int i = tid; i < dead * (kLatentDim / 8); i += kLatentSoftmax) {
             const int v = i % (kLatentDim / 8), r = left + i / (kLatentDim / 8);
-            *reinterpret_cast<uint4*>(ring + (tile & 1) * kLatentTileBytes + r / 8 * kLatentGroup + v / 8 * kLatentAtom +
+            *reinterpret_cast<uint4*>(ring + (tile & 1) * kLatentTileBytes + latent_chunk(v / 8) + r / 8 * kLatentGroup +
                                       r % 8 * 128 + v % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
@@ -815,9 +845,17 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
   }
   const int group = tid / LANES, d = (int(blockIdx.z) * LANES + tid % LANES) * 4;
   constexpr int HEADS = Z == 1 ? 2 : 1;
+  constexpr int AHEAD = Z == 1 ? kFewPieces : (kLatentSms + GROUPS - 1) / GROUPS;  // pieces read while the weights are made
   for (int h = HEADS * int(blockIdx.y); h < min(a.num_heads, HEADS * int(blockIdx.y) + HEADS); ++h) {
     float2 ml = make_float2(-INFINITY, 0.f);
     if (tid < n) ml = __ldcg(a.part_ml + slot(tid, h));
+    float4 early[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int i = group + k * GROUPS;
+      early[k] = i < n ? __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i, h) * kLatentDim + d))
+                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     float M = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
@@ -839,15 +877,19 @@ __global__ void __launch_bounds__(256) latent_merge_kernel(const LatentArgs a) {
 #pragma unroll
     for (int i = 1; i < 8; ++i) den += red[i];
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = group; i < n; i += GROUPS) {
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i, h) * kLatentDim + d));
+    auto add = [&](int i, const float4& o) {
       const float wi = weight[i];
       num.x = fmaf(wi, o.x, num.x);
       num.y = fmaf(wi, o.y, num.y);
       num.z = fmaf(wi, o.z, num.z);
       num.w = fmaf(wi, o.w, num.w);
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+      if (group + k * GROUPS < n) add(group + k * GROUPS, early[k]);
+#pragma unroll 8
+    for (int i = group + AHEAD * GROUPS; i < n; i += GROUPS)
+      add(i, __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i, h) * kLatentDim + d)));
     if (group) other[group - 1][tid % LANES] = num;
     __syncthreads();
     if (group) continue;
