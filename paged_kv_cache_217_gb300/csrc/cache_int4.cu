@@ -51,10 +51,29 @@ struct Divisor {
   __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return d == 1 ? n : __umulhi(n, mul) >> shift; }
 };
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) { return fma2(a, make_float2(b, b), make_float2(c, c)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Which row and word a thread has: K and V rows alternate.
 struct Int4Place {
   uint32_t token, head, v;  // v: 0 K, 1 V
   int word;
+  // where the word lies in a tile, as kv4_k_word and kv4_v_word say: r's row
+  // plus (at ^ ((r << shift) & turn))
+  uint32_t at, turn, shift;
 };
 template <int D>
 __device__ __forceinline__ Int4Place int4_place(const Divisor& heads) {
@@ -65,6 +84,9 @@ __device__ __forceinline__ Int4Place int4_place(const Divisor& heads) {
   p.v = row & 1u;
   p.token = heads(row >> 1);
   p.head = (row >> 1) - p.token * heads.d;
+  p.at = uint32_t(p.v ? kv4_v_word<D>(0, p.word) : kv4_k_word<D>(0, p.word));
+  p.turn = D == 256 ? (p.v ? 0x60u : 0x40u) : D == 128 && p.v ? 0x20u : 0u;
+  p.shift = D == 256 && p.v ? 5u : 4u;
   return p;
 }
 
@@ -110,15 +132,21 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
   const float inv = __fdividef(1.f, half_s);
   float x[8];
   Vec8<T>::to_float(u, x);
-  uint32_t codes = 0;
-  bool near = !(half_s >= (sizeof(T) == 2 && std::is_same<T, __half>::value ? 0x1p-14f : 0x1p-100f));
+  // Dims i and i + 4 together. r is the product d inv rounded to an integer (on
+  // top of kMagic), e what the rounding left, low and high the negated codes of
+  // dims 0 .. 3 and 4 .. 7 as base-16 numbers (exact in fp32).
+  float2 sum = make_float2(0.f, 0.f);
+  float worst = 0.f;
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float q = fmaf(x[i], 0.5f, -half_z) * inv, r = q + kMagic;
-    near |= fabsf(q - (r - kMagic)) > 0.49999f;
-    codes = codes * 16u + __float_as_uint(r);  // r's bits are those of kMagic plus the code
+  for (int i = 3; i >= 0; --i) {
+    const float2 d = fma2(make_float2(x[i], x[i + 4]), 0.5f, -half_z);
+    const float2 r = fma2(d, inv, kMagic), minus = fma2(r, -1.f, kMagic);
+    const float2 e = fma2(d, make_float2(inv, inv), minus);
+    sum = fma2(sum, make_float2(16.f, 16.f), minus);
+    worst = max3(worst, fabsf(e.x), fabsf(e.y));
   }
-  codes -= 0x4B400000u * 0x11111111u;
+  uint32_t codes = __byte_perm(__float_as_uint(8388608.f - sum.x), __float_as_uint(8388608.f - sum.y), 0x5410);
+  const bool near = !(half_s >= (std::is_same<T, __half>::value ? 0x1p-14f : 0x1p-100f)) || worst > 0.49999f;
   if (near) {
     codes = 0;
     if (half_s > 0.f) {
@@ -134,12 +162,17 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
 
 // Byte offsets in a tile of a thread's word and of its group's pair, for slot r.
 template <int D>
-__device__ __forceinline__ int word_offset(const Int4Place& p, int r) {
-  return p.v ? kv4_v_word<D>(r, p.word) : kv4_k_word<D>(r, p.word);
+__device__ __forceinline__ uint32_t word_offset(const Int4Place& p, uint32_t r) {
+  return (p.v ? r : uint32_t(kv4_row(int(r)))) * (D / 2) + (p.at ^ ((r << p.shift) & p.turn));
 }
 template <int D>
-__device__ __forceinline__ int pair_offset(const Int4Place& p, int r) {
-  return (16 + p.v) * D + kv4_row(r) * (D / 16) + 4 * (p.word / 8);
+__device__ __forceinline__ uint32_t pair_offset(const Int4Place& p, uint32_t r) {
+  return (16 + p.v) * D + uint32_t(kv4_row(int(r))) * (D / 16) + 4 * (uint32_t(p.word) / 8);
+}
+// The tile of a valid slot.
+template <int D, typename Byte>
+__device__ __forceinline__ Byte* tile_of(Byte* cache, const Int4Place& p, int64_t slot, uint32_t heads) {
+  return cache + p.head * uint32_t(kv4_tile_bytes(D)) + uint64_t(uint32_t(slot >> 4)) * (heads * uint32_t(kv4_tile_bytes(D)));
 }
 
 // U tokens per thread, `stride` apart, all their loads in flight together: large
@@ -159,7 +192,7 @@ reshape_and_cache_int4_kernel(const uint4* __restrict__ k, const uint4* __restri
     const uint32_t t = p.token + u * stride;
     const bool in = p.token < stride && t < tokens;  // (whole groups of 8 lanes; the others help the shuffles)
     slot[u] = in ? __ldg(slots + t) : -1;
-    x[u] = in ? __ldg(src + size_t(t) * heads.d * (D / 8)) : make_uint4(0u, 0u, 0u, 0u);
+    x[u] = in ? __ldg(src + uint64_t(t) * (heads.d * (D / 8))) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -170,8 +203,8 @@ reshape_and_cache_int4_kernel(const uint4* __restrict__ k, const uint4* __restri
       if (p.head == 0 && p.word == 0) flag(status, PKV_DEV_BAD_SLOT);
       continue;
     }
-    unsigned char* tile = cache + ((slot[u] / kBlock) * heads.d + p.head) * kv4_tile_bytes(D);
-    const int r = int(slot[u] % kBlock);
+    unsigned char* tile = tile_of<D>(cache, p, slot[u], heads.d);
+    const uint32_t r = uint32_t(slot[u]) % kBlock;
     *reinterpret_cast<uint32_t*>(tile + word_offset<D>(p, r)) = codes;
     if (p.word % 8 == 0) *reinterpret_cast<uint32_t*>(tile + pair_offset<D>(p, r)) = pair;
   }
@@ -195,8 +228,8 @@ gather_cache_int4_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const uns
     if (slot[u] >= num_slots) {
       if (p.head == 0 && p.word == 0) flag(status, PKV_DEV_BAD_SLOT);
     } else if (slot[u] >= 0) {
-      const unsigned char* tile = cache + ((slot[u] / kBlock) * heads.d + p.head) * kv4_tile_bytes(D);
-      const int r = int(slot[u] % kBlock);
+      const unsigned char* tile = tile_of<D>(cache, p, slot[u], heads.d);
+      const uint32_t r = uint32_t(slot[u]) % kBlock;
       codes[u] = *reinterpret_cast<const uint32_t*>(tile + word_offset<D>(p, r));
       pair[u] = *reinterpret_cast<const uint32_t*>(tile + pair_offset<D>(p, r));
     }
@@ -208,9 +241,14 @@ gather_cache_int4_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const uns
     const float s = from_bits<T>(uint16_t(pair[u] & 0xffffu)), z = from_bits<T>(uint16_t(pair[u] >> 16));
     float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)  // (a code as a float: its bits under those of 2^23)
-      x[i] = fmaf(__uint_as_float(((codes[u] >> (4 * i)) & 15u) | 0x4B000000u) - 8388608.f, s, z);
-    dst[size_t(t) * heads.d * (D / 8)] = Vec8<T>::from_float(x);
+    for (int i = 0; i < 4; ++i) {  // codes i and i + 4 as fp16: their bits under those of 1024
+      const uint32_t bits = ((codes[u] >> (4 * i)) & 0x000f000fu) | 0x64006400u;
+      const float2 c = __half22float2(__hsub2(*reinterpret_cast<const __half2*>(&bits), __float2half2_rn(1024.f)));
+      const float2 y = fma2(c, s, z);
+      x[i] = y.x;
+      x[i + 4] = y.y;
+    }
+    dst[uint64_t(t) * (heads.d * (D / 8))] = Vec8<T>::from_float(x);
   }
 }
 

@@ -40,6 +40,7 @@ WRITE = dict(k=FAKE, v=FAKE, dt=0, cache=FAKE, slots=FAKE, T=4, hkv=4, D=128, nb
 @pytest.mark.parametrize("kw,status", [
     (dict(T=-1), 1), (dict(hkv=0), 1), (dict(nb=0), 1), (dict(D=80), 2), (dict(dt=7), 2), (dict(k=None), 1),
     (dict(v=FAKE + 4), 1), (dict(cache=FAKE + 4), 1), (dict(slots=FAKE + 4), 1), (dict(T=2 ** 31 - 1, hkv=9), 2),
+    (dict(T=1, hkv=2 ** 24), 2),
 ])
 def test_cache_int4_refusals(name, kw, status):
     st, msg = _call(name, WRITE, kw)
