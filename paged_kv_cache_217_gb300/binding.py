@@ -10,6 +10,7 @@ allocation the binding keeps per (device, stream) and grows on demand.
 """
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -459,11 +460,23 @@ def copy_blocks_int8(k_cache, v_cache, k_scale, v_scale, src_dst_pairs):
 # ---------------------------------------------------------------------------
 # 4-bit KV cache: uint8 [num_blocks, Hkv, 18 * D], K and V of a (block, KV head) in one tile
 # ---------------------------------------------------------------------------
+_scratches = {}
+
+
 def _scratch(device, nbytes):
-    """Workspace of one call: a torch allocation of the current stream, which its allocator hands out
-    again only to later work of that stream (and, under capture, only inside the captured graph)."""
+    """Workspace of one call, or None. Eager calls of a stream share one, which grows to the largest need (an
+    allocation a call costs 4 us of host time); a call under capture gets memory of its graph's own, so that
+    graphs replayed at once, or beside eager calls, never share one."""
+    if not nbytes:
+        return None
     import torch
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    key = (device.index, _stream_ptr(device))
+    ws = _scratches.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _scratches[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    return ws
 
 
 def _ptr_bytes(ws):
@@ -484,9 +497,10 @@ def _check_int4(k, v, kv_cache, slot_mapping):
     T, hkv, D = k.shape
     if kv_cache.dtype != torch.uint8 or slot_mapping.dtype != torch.int64:
         raise TypeError("kv_cache must be uint8, slot_mapping int64")
-    if kv_cache.dim() != 3 or tuple(kv_cache.shape[1:]) != (hkv, 18 * D) or tuple(slot_mapping.shape) != (T,):
+    tiles = kv_cache.shape
+    if len(tiles) != 3 or tiles[1] != hkv or tiles[2] != 18 * D or slot_mapping.shape != (T,):
         raise ValueError("kv_cache: [num_blocks, Hkv, 18 * D]; slot_mapping: [T]")
-    return dt, T, hkv, D, kv_cache.shape[0]
+    return dt, T, hkv, D, tiles[0]
 
 
 def reshape_and_cache_int4(k, v, kv_cache, slot_mapping):
@@ -517,6 +531,7 @@ def copy_blocks_int4(kv_cache, src_dst_pairs):
             src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], hkv, tile // 18, nb)
 
 
+@functools.lru_cache(maxsize=1024)
 def int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, sliding_window=0):
     return int(lib().pkv_int4_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
                                              sliding_window))
@@ -539,14 +554,14 @@ def paged_attention_decode_int4(out, q, kv_cache, block_tables, context_lens, sc
         raise TypeError("kv_cache must be uint8")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("block_tables and context_lens must be int32")
-    if q.dim() != 3 or kv_cache.dim() != 3 or out.shape != q.shape or kv_cache.shape[2] != 18 * q.shape[2] \
-            or block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0] \
-            or tuple(context_lens.shape) != (q.shape[0],):
+    shape, tiles, table = q.shape, kv_cache.shape, block_tables.shape
+    if len(shape) != 3 or len(tiles) != 3 or out.shape != shape or tiles[2] != 18 * shape[2] or len(table) != 2 \
+            or table[0] != shape[0] or context_lens.shape != (shape[0],):
         raise ValueError("shape mismatch among out, q, kv_cache, block_tables and context_lens")
     window = max(0, int(sliding_window))
-    S, Hq, D = q.shape
-    nb, hkv = kv_cache.shape[0], kv_cache.shape[1]
-    mb = block_tables.shape[1]
+    S, Hq, D = shape
+    nb, hkv = tiles[0], tiles[1]
+    mb = table[1]
     need = int4_workspace_size(S, Hq, hkv, D, mb, window)
     if workspace is None:
         workspace = _scratch(q.device, need)
@@ -561,7 +576,8 @@ def paged_attention_decode_int4(out, q, kv_cache, block_tables, context_lens, sc
 # latent attention: one row [latent 512, rotary 64] per token, cache [num_blocks, 16, 576]
 # ---------------------------------------------------------------------------
 def _check_latent_cache(cache):
-    if cache.dim() != 3 or tuple(cache.shape[1:]) != (BLOCK_SIZE, LATENT_DIM + ROPE_DIM):
+    shape = cache.shape
+    if len(shape) != 3 or shape[1] != BLOCK_SIZE or shape[2] != LATENT_DIM + ROPE_DIM:
         raise ValueError("a latent cache is [num_blocks, 16, 576]")
 
 
@@ -579,12 +595,13 @@ def latent_cache_write(latent, rope, cache, slot_mapping):
     if latent.device != cache.device or rope.device != cache.device or slot_mapping.dim() != 1:
         raise ValueError("tensors must be on one device, slot_mapping [T]")
     T = slot_mapping.shape[0]
-    if tuple(latent.shape) != (T, LATENT_DIM) or tuple(rope.shape) != (T, ROPE_DIM):
+    if latent.shape != (T, LATENT_DIM) or rope.shape != (T, ROPE_DIM):
         raise ValueError("latent must be [T, 512] and rope [T, 64]")
-    if T and (latent.stride(1) != 1 or rope.stride(1) != 1):
+    (latent_row, one), (rope_row, rope_one) = latent.stride(), rope.stride()
+    if T and (one != 1 or rope_one != 1):
         raise ValueError("rows of latent and rope must be contiguous")
     _launch(cache.device, "latent_cache_write", lib().pkv_latent_cache_write, latent.data_ptr(), rope.data_ptr(),
-            latent.stride(0), rope.stride(0), dt, cache.data_ptr(), slot_mapping.data_ptr(), T, cache.shape[0])
+            latent_row, rope_row, dt, cache.data_ptr(), slot_mapping.data_ptr(), T, cache.shape[0])
 
 
 def copy_blocks_latent(cache, src_dst_pairs):
@@ -599,6 +616,7 @@ def copy_blocks_latent(cache, src_dst_pairs):
             src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], cache.shape[0])
 
 
+@functools.lru_cache(maxsize=1024)
 def latent_workspace_size(num_seqs, num_heads, max_blocks_per_seq):
     return int(lib().pkv_latent_workspace_size(int(num_seqs), int(num_heads), int(max_blocks_per_seq)))
 
@@ -615,12 +633,12 @@ def paged_latent_decode(out, q, cache, block_tables, context_lens, scale, worksp
         raise TypeError("q, out and cache must share one dtype")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("block_tables and context_lens must be int32")
-    if q.dim() != 3 or q.shape[2] != LATENT_DIM + ROPE_DIM or tuple(out.shape) != (*q.shape[:2], LATENT_DIM) \
-            or block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0] \
-            or tuple(context_lens.shape) != (q.shape[0],):
+    shape, table = q.shape, block_tables.shape
+    if len(shape) != 3 or shape[2] != LATENT_DIM + ROPE_DIM or out.shape != (shape[0], shape[1], LATENT_DIM) \
+            or len(table) != 2 or table[0] != shape[0] or context_lens.shape != (shape[0],):
         raise ValueError("q: [S, H, 576]; out: [S, H, 512]; block_tables: [S, max_blocks]; context_lens: [S]")
-    S, H, _ = q.shape
-    mb = block_tables.shape[1]
+    S, H, _ = shape
+    mb = table[1]
     need = latent_workspace_size(S, H, mb)
     if workspace is None:
         workspace = _scratch(q.device, need)
@@ -658,7 +676,7 @@ def extend_block_tables(block_tables, context_lens, new_tokens, free_stack, free
     if block_tables.dim() != 2 or slot_mapping.dim() != 1 or free_stack.dim() != 1:
         raise ValueError("block_tables: [S, max_blocks]; slot_mapping: [n]; free_stack: [num_blocks]")
     S, mb = block_tables.shape
-    if any(tuple(t.shape) != (S,) for t in (context_lens, new_tokens, new_lens)):
+    if context_lens.shape != (S,) or new_tokens.shape != (S,) or new_lens.shape != (S,):
         raise ValueError("context_lens, new_tokens and new_lens must be [S]")
     if free_count.numel() != 1 or new_free_count.numel() != 1:
         raise ValueError("free_count and new_free_count hold one value")
@@ -667,7 +685,7 @@ def extend_block_tables(block_tables, context_lens, new_tokens, free_stack, free
     if refcounts is not None:
         _need_dtype(torch.int32, "refcounts", refcounts)
         _need_dtype(torch.int64, "cow_pairs", cow_pairs)
-        if refcounts.shape != free_stack.shape or tuple(cow_pairs.shape) != (S, 2):
+        if refcounts.shape != free_stack.shape or cow_pairs.shape != (S, 2):
             raise ValueError("refcounts: [num_blocks]; cow_pairs: [S, 2]")
     if info is not None:
         _need_dtype(torch.int32, "info", info)
@@ -696,7 +714,7 @@ def release_sequences(block_tables, context_lens, finished, free_stack, free_cou
     if block_tables.dim() != 2 or free_stack.dim() != 1 or free_count.numel() != 1:
         raise ValueError("block_tables: [S, max_blocks]; free_stack: [num_blocks]; free_count holds one value")
     S, mb = block_tables.shape
-    if any(tuple(t.shape) != (S,) for t in (context_lens, finished)):
+    if context_lens.shape != (S,) or finished.shape != (S,):
         raise ValueError("context_lens and finished must be [S]")
     if refcounts is not None and refcounts.shape != free_stack.shape:
         raise ValueError("refcounts must be [num_blocks]")
