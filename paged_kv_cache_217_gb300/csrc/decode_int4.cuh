@@ -536,20 +536,12 @@ __device__ __forceinline__ I4Seq i4_seq(const Int4Args& a, int L) {
   return q;
 }
 
-// Pieces of one item in a CTA: a warp's last piece (or none: the item began in an
-// earlier CTA), then the first pieces of warps [from, to). slot: where the joined
-// result goes in the workspace, or -1: it is the output.
-struct I4Run {
-  int item, head, from, to, slot;
-};
-
 template <int NW>
 struct I4Shared {
   long long before[NW * 32];     // per thread: where its run of sequences starts in the list
   long long scan[NW], last[NW];  // per warp: ... and the last pair of the item of its last piece
   int len[NW * 32];              // per thread: the length of its run's last sequence
   int fitem[NW], fend[NW], litem[NW];
-  I4Run run[NW + 1];
 };
 
 constexpr int kInt4NoPiece = -1, kInt4NoWork = -2;
@@ -576,6 +568,7 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
   // This CTA's range [cb, ce) of the list of total pairs, this warp's [wb, we),
   // and the sequence in which the latter starts.
   long long cb, ce, total, base;
+  EvenSplit split(0, 1);
   int s, L;
   auto warp_begin = [&](int w) { return cb + (ce - cb) * w / NW; };
   if (a.item_ctas) {  // one item: the list is its own
@@ -593,6 +586,10 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
     cb = 0;
     ce = total = np;
   } else {
+    // The tables' way into L2 begins while the lengths are read (tables of up to
+    // 1 MB: a line a thread).
+    const size_t line = size_t(blockIdx.x * (NW * 32u) + tid) * 32, ids = size_t(a.num_seqs) * a.max_blocks_per_seq;
+    if (ids <= (1u << 18) && line < ids) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.block_tables + line));
     // Each thread sums a run of sequences, a scan of the sums gives every run's
     // place in the list, and each warp searches the places for its own start.
     int zero_len = int(blockIdx.x) < a.num_seqs ? i4_len(a, int(blockIdx.x)) : 1;  // (read along with the others)
@@ -600,11 +597,17 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
     const int run0 = min(a.num_seqs, tid * per), run1 = min(a.num_seqs, run0 + per);
     long long mine = 0;
     int run_len = 0;
-    for (int i = run0; i < run1; ++i) {
-      const int raw = __ldg(a.context_lens + i);
-      run_len = raw < 0 ? 0 : raw > most ? most : raw;
-      if (raw != run_len && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-      mine += (long long)i4_seq(a, run_len).np * Hkv;
+    for (int i0 = run0; i0 < run1; i0 += 4) {
+      int raw[4];  // (loads together)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) raw[j] = i0 + j < run1 ? __ldg(a.context_lens + i0 + j) : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i0 + j >= run1) break;
+        run_len = raw[j] < 0 ? 0 : raw[j] > most ? most : raw[j];
+        if (raw[j] != run_len && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+        mine += (long long)i4_seq(a, run_len).np * Hkv;
+      }
     }
     long long upto = mine;
 #pragma unroll
@@ -623,8 +626,9 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
     }
     sh.before[tid] = before;
     sh.len[tid] = run_len;
-    cb = int(blockIdx.x) * total / a.ctas;
-    ce = (int(blockIdx.x) + 1) * total / a.ctas;
+    split = EvenSplit(total, a.ctas);
+    cb = split.begin(int(blockIdx.x));
+    ce = split.begin(int(blockIdx.x) + 1);
     // Sequences without tokens: zeros, spread over the CTAs.
     for (int i = int(blockIdx.x); i < a.num_seqs;) {
       if (zero_len == 0) {
@@ -777,89 +781,75 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
     sh.last[warp] = base + (long long)(g + 1) * sq.np - 1;
   }
   __syncthreads();
-  // The CTA's runs of pieces: one from each warp's last piece, and (thread NW) the
-  // one of an item that began in an earlier CTA.
-  if (tid <= NW) {
-    I4Run run{kInt4NoPiece, -1, 0, 0, 2 * int(blockIdx.x)};
-    bool end = false;
-    int w = 0;
-    if (tid < NW) {
-      run.item = sh.litem[tid];
-      run.head = tid;
-      w = tid + 1;
-    } else {
-      while (w < NW && sh.fitem[w] == kInt4NoWork) ++w;
-      if (w < NW) run.item = sh.fitem[w];
+  // The runs of pieces to join: one from each warp's last piece (run r of warp r)
+  // and, run NW, the pieces of an item that began in an earlier CTA; each goes on
+  // with the first pieces that belong to its item. Every warp works this out by
+  // itself, and the warps take the runs' rows (32 vectors of 4 dims) in turn.
+  const int fit = lane < NW ? sh.fitem[lane] : kInt4NoWork;
+  const unsigned ends = __ballot_sync(kFull, lane < NW && sh.fend[lane] != 0);
+  const unsigned working = __ballot_sync(kFull, fit != kInt4NoWork);
+  const int early = __shfl_sync(kFull, fit, working ? __ffs(working) - 1 : 0);
+  const int run_item = lane < NW ? sh.litem[lane] : lane == NW ? early : kInt4NoWork;
+  unsigned runs = __ballot_sync(kFull, run_item >= 0);
+  const int rows = a.group * (D / 4), chunks = (rows + 31) / 32;
+  int chunk = warp;
+  bool open = false;
+  for (; runs; runs &= runs - 1) {
+    const int r = __ffs(runs) - 1, it = __shfl_sync(kFull, run_item, r);
+    const unsigned pieces = __ballot_sync(kFull, fit == it);
+    const bool whole = r < NW && ((pieces & ends) != 0u || a.item_ctas);
+    if (r < NW && !whole) {
+      // the merge's descriptor: an item that starts here and goes on, and the CTA
+      // that holds its last pair
+      if (tid == 0) a.desc[blockIdx.x] = make_int2(it, split.of(sh.last[r]));
+      open = true;
     }
-    if (run.item >= 0) {
-      run.from = run.to = w;
-      for (; w < NW && !end; ++w) {
-        if (sh.fitem[w] == kInt4NoWork) continue;
-        if (sh.fitem[w] != run.item) break;
-        run.to = w + 1;
-        end = sh.fend[w] != 0;
+    for (; chunk < chunks; chunk += NW) {
+      const int e = 32 * chunk + lane, h = e / (D / 4), d = e % (D / 4) * 4;
+      if (e >= rows) continue;
+      float M = -INFINITY, den = 0.f;
+      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](const float* p) {
+        const float m = p[H * D + h], l = p[H * D + H + h];
+        const float4 x = *reinterpret_cast<const float4*>(p + h * D + d);
+        const float top = fmaxf(M, m), ref = top == -INFINITY ? 0.f : top;
+        const float wa = fast_exp2(M - ref), wb2 = fast_exp2(m - ref);
+        M = top;
+        den = den * wa + l * wb2;
+        num.x = num.x * wa + x.x * wb2;
+        num.y = num.y * wa + x.y * wb2;
+        num.z = num.z * wa + x.z * wb2;
+        num.w = num.w * wa + x.w * wb2;
+      };
+      // (piece -1: the run's own first, in its warp's ring)
+#pragma unroll 1
+      for (unsigned m = (pieces << 1) | (r < NW ? 1u : 0u); m; m &= m - 1) {
+        const int w = __ffs(m) - 2;
+        add(reinterpret_cast<const float*>(w < 0 ? smem + size_t(r) * STAGES * C::STAGE_BYTES
+                                                 : smem + C::RING_BYTES + size_t(w) * C::PIECE_FLOATS * 4));
       }
-      if (tid < NW) {
-        run.slot = end || a.item_ctas ? -1 : 2 * int(blockIdx.x) + 1;
-        if (!end && !a.item_ctas) {
-          // the merge's descriptor: an item that starts here and goes on, and the
-          // CTA that holds its last pair
-          const long long last = sh.last[tid];
-          long long to = last * a.ctas / total;
-          while ((to + 1) * total / a.ctas <= last) ++to;
-          while (to * total / a.ctas > last) --to;
-          a.desc[blockIdx.x] = make_int2(run.item, int(to));
-        }
-      }
-    }
-    sh.run[tid] = run;
-    // (whoever found an item that goes on has written the descriptor)
-    const unsigned open = __ballot_sync((1u << (NW + 1)) - 1u, run.item >= 0 && tid < NW && !end);
-    if (tid == 0 && open == 0u && !a.item_ctas) a.desc[blockIdx.x] = make_int2(-1, 0);
-  }
-  __syncthreads();
-  const int rows = a.group * (D / 4);
-  for (int e = tid; e < (NW + 1) * rows; e += NW * 32) {
-    const I4Run run = sh.run[e / rows];
-    if (run.item < 0) continue;
-    const int h = e % rows / (D / 4), d = e % (D / 4) * 4;
-    float M = -INFINITY, den = 0.f;
-    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = run.head >= 0 ? run.from - 1 : run.from; w < run.to; ++w) {
-      const float* p;
-      if (w < run.from) {
-        p = reinterpret_cast<const float*>(smem + size_t(run.head) * STAGES * C::STAGE_BYTES);
+      if (whole) {
+        const int is = it / Hkv, ig = it - is * Hkv;
+        const float inv = 1.f / den;
+        T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(is) * a.num_q_heads + ig * a.group + h) * D + d) =
+            *reinterpret_cast<const uint2*>(x);
       } else {
-        if (sh.fitem[w] == kInt4NoWork) continue;
-        p = reinterpret_cast<const float*>(smem + C::RING_BYTES) + w * C::PIECE_FLOATS;
+        const int slot = 2 * int(blockIdx.x) + (r < NW ? 1 : 0);
+        *reinterpret_cast<float4*>(a.part_o + (size_t(slot) * a.group + h) * D + d) = num;
+        if (d == 0) a.part_ml[size_t(slot) * a.group + h] = make_float2(M, den);
       }
-      const float m = p[H * D + h], l = p[H * D + H + h];
-      const float4 x = *reinterpret_cast<const float4*>(p + h * D + d);
-      const float top = fmaxf(M, m), ref = top == -INFINITY ? 0.f : top;
-      const float wa = fast_exp2(M - ref), wb2 = fast_exp2(m - ref);
-      M = top;
-      den = den * wa + l * wb2;
-      num.x = num.x * wa + x.x * wb2;
-      num.y = num.y * wa + x.y * wb2;
-      num.z = num.z * wa + x.z * wb2;
-      num.w = num.w * wa + x.w * wb2;
     }
-    const int is = run.item / Hkv, ig = run.item - is * Hkv;
-    if (run.slot < 0) {
-      const float inv = 1.f / den;
-      T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(is) * a.num_q_heads + ig * a.group + h) * D + d) =
-          *reinterpret_cast<const uint2*>(x);
-    } else {
-      *reinterpret_cast<float4*>(a.part_o + (size_t(run.slot) * a.group + h) * D + d) = num;
-      if (d == 0) a.part_ml[size_t(run.slot) * a.group + h] = make_float2(M, den);
-    }
+    chunk -= chunks;
   }
+  if (tid == 0 && !open && !a.item_ctas) a.desc[blockIdx.x] = make_int2(-1, 0);
 }
 
 // Joins the pieces of the item that starts in CTA blockIdx.x's range and goes on
-// past it, one query head per CTA here: the weights of all pieces first, then 8
-// (D = 64: 16) groups of threads take every 8th piece, 4 dims per thread.
+// past it, one query head per CTA here, 4 dims per thread: few pieces in one round
+// of loads; many by 8 (D = 64: 16) groups of threads, every 8th piece each, the
+// first of which are read while the weights of all are made.
+constexpr int kInt4FewPieces = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
   constexpr int LANES = D / 4, GROUPS = 256 / LANES;
@@ -871,6 +861,45 @@ __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
   if (desc.x < 0) return;
   const int n = desc.y - c0 + 1;
   auto slot = [&](int i) { return (size_t(2) * (c0 + i) + (i == 0 ? 1 : 0)) * a.group + h; };
+  auto write = [&](const float4& num, float den) {
+    const int s = desc.x / a.num_kv_heads, g = desc.x - s * a.num_kv_heads;
+    const float inv = 1.f / den;
+    T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + g * a.group + h) * D + d) =
+        *reinterpret_cast<const uint2*>(x);
+  };
+  if (n <= kInt4FewPieces) {  // one round of loads
+    if (group) return;
+    float2 ml[kInt4FewPieces];
+    float4 o[kInt4FewPieces], num = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, den = 0.f;
+#pragma unroll
+    for (int i = 0; i < kInt4FewPieces; ++i) {
+      ml[i] = i < n ? __ldcg(a.part_ml + slot(i)) : make_float2(-INFINITY, 0.f);
+      o[i] = i < n ? __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D + d)) : num;
+      M = fmaxf(M, ml[i].x);
+    }
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int i = 0; i < kInt4FewPieces; ++i) {
+      const float w = fast_exp2(ml[i].x - ref);
+      den = fmaf(w, ml[i].y, den);
+      num.x = fmaf(w, o[i].x, num.x);
+      num.y = fmaf(w, o[i].y, num.y);
+      num.z = fmaf(w, o[i].z, num.z);
+      num.w = fmaf(w, o[i].w, num.w);
+    }
+    write(num, den);
+    return;
+  }
+  constexpr int AHEAD = 8;  // pieces read while the weights are made
+  float4 early[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    const int i = group + k * GROUPS;
+    early[k] = i < n ? __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D + d))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   float M = -INFINITY;
   for (int i = tid; i < n; i += 256) {
     weight[i] = __ldcg(&a.part_ml[slot(i)].x);
@@ -896,15 +925,19 @@ __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
   if ((tid & 31) == 0) red[tid >> 5] = den;
   __syncthreads();
   float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = group; i < n; i += GROUPS) {
-    const float4 o = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D + d));
+  auto add = [&](int i, const float4& o) {
     const float w = weight[i];
     num.x = fmaf(w, o.x, num.x);
     num.y = fmaf(w, o.y, num.y);
     num.z = fmaf(w, o.z, num.z);
     num.w = fmaf(w, o.w, num.w);
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (group + k * GROUPS < n) add(group + k * GROUPS, early[k]);
+#pragma unroll 4
+  for (int i = group + AHEAD * GROUPS; i < n; i += GROUPS)
+    add(i, __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i) * D + d)));
   other[group][tid % LANES] = num;
   __syncthreads();
   if (group) return;
@@ -919,11 +952,7 @@ __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
     num.z += x.z;
     num.w += x.w;
   }
-  const float inv = 1.f / den;
-  const int s = desc.x / a.num_kv_heads, g = desc.x - s * a.num_kv_heads;
-  T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
-  *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + g * a.group + h) * D + d) =
-      *reinterpret_cast<const uint2*>(x);
+  write(num, den);
 }
 
 }  // namespace pkv

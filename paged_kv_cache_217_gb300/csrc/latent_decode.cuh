@@ -345,8 +345,9 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     if (i < warp) before += sh.scan[i];
     total += sh.scan[i];
   }
-  const long long used = total < a.ranges ? total : a.ranges;  // ranges that get tiles
-  const long long begin = range < used ? range * total / used : 0, end = range < used ? (range + 1) * total / used : 0;
+  const int used = total < a.ranges ? int(total) : a.ranges;  // ranges that get tiles
+  const EvenSplit split(total, used > 0 ? used : 1);
+  const long long begin = range < used ? split.begin(range) : 0, end = range < used ? split.begin(range + 1) : 0;
   if (begin < end && begin >= before && begin < before + mine) {
     long long at = before;
     int s = run0;
@@ -724,11 +725,8 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         // the ranges that hold the rest of this sequence: up to the one with its last tile
         int2 d = make_int2(-1, 0);
         if (!whole) {
-          const long long last = walk.base + walk.n - 1;
-          long long r = last * used / total;
-          while ((r + 1) * total / used <= last) ++r;
-          while (r * total / used > last) --r;
-          d = a.desc_by_seq ? make_int2(range, int(r)) : make_int2(walk.s, int(r));
+          const int r = split.of(walk.base + walk.n - 1);
+          d = a.desc_by_seq ? make_int2(range, r) : make_int2(walk.s, r);
           open = true;
         }
         if (a.desc_by_seq) a.desc[walk.s] = d;
