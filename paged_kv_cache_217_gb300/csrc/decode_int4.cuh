@@ -54,6 +54,7 @@
 
 #include "decode.cuh"
 #include "device_common.cuh"
+#include "even_split.cuh"
 #include "int4_layout.cuh"
 #include "launch.h"
 

@@ -53,6 +53,7 @@
 
 #include "decode_mma.cuh"
 #include "device_common.cuh"
+#include "even_split.cuh"
 #include "launch.h"
 
 namespace pkv {
