@@ -193,3 +193,10 @@ def test_calls_are_reproducible():
     first = c.run()
     for _ in range(3):
         assert torch.equal(c.run(), first)
+
+
+@pytest.mark.parametrize("heads", [129, 200, 513, 1024])
+def test_many_heads(heads):
+    c = Case([130, 1, 0, 700], heads, "bf16", 17)
+    c.check(c.run(), heads=[0, 43, 64, heads // 2, heads - 1])
+    assert B.device_status(clear=True) == 0
