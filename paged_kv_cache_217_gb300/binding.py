@@ -163,12 +163,10 @@ def _dtype_code(t):
 def _need_cuda(*tensors):
     index = tensors[0].get_device()
     for t in tensors:
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a CUDA device")
+        if t.get_device() != index or index < 0:  # (-1: not on a CUDA device)
+            raise ValueError("tensors must be on one device" if t.is_cuda else "tensors must be on a CUDA device")
         if not t.is_contiguous():
             raise ValueError("tensors must be contiguous")
-        if t.get_device() != index:
-            raise ValueError("tensors must be on one device")
 
 
 def _stream_ptr(device):
@@ -592,9 +590,10 @@ def latent_cache_write(latent, rope, cache, slot_mapping):
         raise TypeError("latent, rope and cache must share one dtype")
     if slot_mapping.dtype != torch.int64:
         raise TypeError("slot_mapping must be int64")
-    if latent.device != cache.device or rope.device != cache.device or slot_mapping.dim() != 1:
+    index, slots = cache.get_device(), slot_mapping.shape
+    if latent.get_device() != index or rope.get_device() != index or len(slots) != 1:
         raise ValueError("tensors must be on one device, slot_mapping [T]")
-    T = slot_mapping.shape[0]
+    T = slots[0]
     if latent.shape != (T, LATENT_DIM) or rope.shape != (T, ROPE_DIM):
         raise ValueError("latent must be [T, 512] and rope [T, 64]")
     (latent_row, one), (rope_row, rope_one) = latent.stride(), rope.stride()
