@@ -805,40 +805,41 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
       if (tid == 0) a.desc[blockIdx.x] = make_int2(it, split.of(sh.last[r]));
       open = true;
     }
+    const int is = it / Hkv, ig = it - is * Hkv;
+    T* const out = static_cast<T*>(a.out) + (size_t(is) * a.num_q_heads + ig * a.group) * D;
+    const size_t row = (size_t(2) * blockIdx.x + (r < NW ? 1 : 0)) * a.group;  // of its partial result
+    const unsigned char* const own = smem + size_t(min(r, NW - 1)) * STAGES * C::STAGE_BYTES;  // its first piece
     for (; chunk < chunks; chunk += NW) {
       const int e = 32 * chunk + lane, h = e / (D / 4), d = e % (D / 4) * 4;
       if (e >= rows) continue;
-      float M = -INFINITY, den = 0.f;
-      float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](const float* p) {
-        const float m = p[H * D + h], l = p[H * D + H + h];
-        const float4 x = *reinterpret_cast<const float4*>(p + h * D + d);
-        const float top = fmaxf(M, m), ref = top == -INFINITY ? 0.f : top;
-        const float wa = fast_exp2(M - ref), wb2 = fast_exp2(m - ref);
-        M = top;
-        den = den * wa + l * wb2;
-        num.x = num.x * wa + x.x * wb2;
-        num.y = num.y * wa + x.y * wb2;
-        num.z = num.z * wa + x.z * wb2;
-        num.w = num.w * wa + x.w * wb2;
-      };
-      // (piece -1: the run's own first, in its warp's ring)
-#pragma unroll 1
-      for (unsigned m = (pieces << 1) | (r < NW ? 1u : 0u); m; m &= m - 1) {
-        const int w = __ffs(m) - 2;
-        add(reinterpret_cast<const float*>(w < 0 ? smem + size_t(r) * STAGES * C::STAGE_BYTES
-                                                 : smem + C::RING_BYTES + size_t(w) * C::PIECE_FLOATS * 4));
+      float m[NW + 1], l[NW + 1], M = -INFINITY, den = 0.f;
+      float4 x[NW + 1], num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w <= NW; ++w) {  // (all loads together)
+        const float* p = reinterpret_cast<const float*>(w < NW ? smem + C::RING_BYTES + w * (C::PIECE_FLOATS * 4) : own);
+        const bool on = w < NW ? (pieces >> w) & 1u : r < NW;
+        m[w] = on ? p[H * D + h] : -INFINITY;
+        l[w] = on ? p[H * D + H + h] : 0.f;
+        x[w] = on ? *reinterpret_cast<const float4*>(p + h * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        M = fmaxf(M, m[w]);
+      }
+      const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w <= NW; ++w) {
+        const float wt = fast_exp2(m[w] - ref);
+        den = fmaf(wt, l[w], den);
+        num.x = fmaf(wt, x[w].x, num.x);
+        num.y = fmaf(wt, x[w].y, num.y);
+        num.z = fmaf(wt, x[w].z, num.z);
+        num.w = fmaf(wt, x[w].w, num.w);
       }
       if (whole) {
-        const int is = it / Hkv, ig = it - is * Hkv;
         const float inv = 1.f / den;
-        T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(is) * a.num_q_heads + ig * a.group + h) * D + d) =
-            *reinterpret_cast<const uint2*>(x);
+        T y[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
+        *reinterpret_cast<uint2*>(out + size_t(h) * D + d) = *reinterpret_cast<const uint2*>(y);
       } else {
-        const int slot = 2 * int(blockIdx.x) + (r < NW ? 1 : 0);
-        *reinterpret_cast<float4*>(a.part_o + (size_t(slot) * a.group + h) * D + d) = num;
-        if (d == 0) a.part_ml[size_t(slot) * a.group + h] = make_float2(M, den);
+        *reinterpret_cast<float4*>(a.part_o + (row + h) * D + d) = num;
+        if (d == 0) a.part_ml[row + h] = make_float2(M, den);
       }
     }
     chunk -= chunks;

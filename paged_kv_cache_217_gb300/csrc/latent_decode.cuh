@@ -318,6 +318,12 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  // The tables' way into L2 begins while the lengths are read (tables of up to 1
+  // MB: a line a thread).
+  const size_t line = size_t(blockIdx.x * unsigned(kLatentThreads) + tid) * 32;
+  const size_t ids_held = size_t(a.num_seqs) * a.max_blocks_per_seq;
+  if (ids_held <= (1u << 18) && line < ids_held)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(a.block_tables + line));
   // The tile list: each thread sums a run of sequences, a scan of the sums
   // gives every run's place in the list, and the thread whose run holds this
   // range's first tile finds its sequence.
