@@ -45,9 +45,11 @@
 // written from registers; the pieces of one that spans warps meet in shared
 // memory, of one that spans CTAs in the workspace (int4_merge_kernel). Small
 // batches instead give each item a CTA of its own, without that second kernel.
-// One CTA per item for all batches started up for 3.5 us an item: 74.4 us against
-// INT4_MHA_US for 40 heads and 64 sequences, 22.8 against INT4_GQA_US for 8 KV
-// heads and 256 short ones.
+// One CTA per item for all batches started up for 3.5 us an item: 74.4 us for 40
+// heads and 64 sequences against 57.7 (5.2 of the 6.8 TB/s that a copy reaches),
+// where 256 sequences of 150 tokens x 8 KV heads took 22.8 against 22.3: there
+// the list (2 us), the block ids (1.4), the first copies (1) and the joins (4)
+// stand around 7 us of streaming.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -76,7 +78,8 @@ struct I4Cfg {
 // Warps per CTA, and CTAs that an SM holds. Measured on GB300 at head_dim 128:
 // 2 x 6 warps (168 registers) 61.2 us, 2 x 8 (128, some spilled) 65.1 on the
 // 40-head layer, 115.8 against 118.9 on 96 heads x 3 long sequences; at 256 one
-// CTA of 8 (255 registers) 60.4 us against 67.8 with 6. A prefetch of later tiles
+// CTA of 8 (255 registers) 60.4 us against 67.8 with 6 (all before the joins were
+// shortened, which took 2 to 3 us off each). A prefetch of later tiles
 // into L2 made all of them 5-18 % slower.
 template <int D>
 constexpr int i4_warps() { return D == 256 ? 8 : 6; }

@@ -520,10 +520,10 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         ++pv;
         return true;
       };
-      // Waits for a barrier, and issues O^T meanwhile.
-      auto ready = [&](uint32_t bar, uint32_t parity) {
+      // Waits, for a limited time, until done() says so, and issues O^T meanwhile.
+      auto until = [&](auto done) {
         unsigned long long t0 = 0;
-        for (int polls = 0; !mbar_test(bar, parity); ++polls) {
+        for (int polls = 0; !done(); ++polls) {
           if (outputs()) polls = 0;
           if ((polls & 63) != 63) continue;
           const unsigned long long now = global_timer_ns();
@@ -539,19 +539,16 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       };
       bool ok = true;
       while (ok && qk < n) {
-        // S^T's buffer: the weights of tile qk - 2 have been read off it
-        if (qk == pv + 2) {
-          ok = ready(smem_addr(&sh.p_full), pv & 1);
-          if (ok) outputs();
-        }
-        if (ok && seg_first) ok = ready(smem_addr(&sh.q_full), seg & 1);
+        // S^T's buffer is free once tile qk - 2 has its weights
+        ok = until([&]() { return qk < pv + 2; });
+        if (ok && seg_first) ok = until([&]() { return mbar_test(smem_addr(&sh.q_full), seg & 1); });
         const uint32_t d = tmem + 4 * N + (qk & 1) * N, full = smem_addr(&sh.third_full[3 * (qk & 1)]);
         const uint64_t key = key_desc + (qk & 1) * (kLatentTileBytes >> 4);
 #pragma unroll
         for (int c = 0; c < kLatentRow / 64; ++c) {
           if (c >= 3 && c <= 7) outputs();
           if (c % 3 == 0) {
-            ok = ok && ready(full + 8 * (c / 3), (qk >> 1) & 1);
+            ok = ok && until([&]() { return mbar_test(full + 8 * (c / 3), (qk >> 1) & 1); });
             if (!ok) break;
             tc_fence_after();
           }
@@ -570,10 +567,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         }
         ++qk;
       }
-      while (ok && pv < n) {
-        ok = ready(smem_addr(&sh.p_full), pv & 1);
-        if (ok) outputs();
-      }
+      if (ok) until([&]() { return pv == n; });
       if (*stop) {  // let the products in flight end before the tensor memory is freed
         const uint32_t bar = smem_addr(&sh.drain);
         mbar_init(bar, 1);
