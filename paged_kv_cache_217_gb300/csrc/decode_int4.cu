@@ -6,11 +6,19 @@ namespace pkv {
 namespace {
 
 constexpr int kInt4Stages = 2;
-// Batches of at most kItemCtas items (sequences x KV heads) whose tables hold at
-// most kItemPairs pairs of tiles give each item a CTA.
+// Batches of at most kItemCtas items (sequences x KV heads, one wave of CTAs) whose
+// tables hold at most kItemPairs pairs of tiles give each item a CTA; the others
+// share the list, which starts later and needs a merge but balances. Measured for
+// tables of 2048 tokens, item against list, in us: 8 items of 411 tokens 5.8, 8.3;
+// 64 to 240 items of about 300 tokens 6.6 to 8.0, 8.9 to 10.3; 128 items of 1000
+// tokens 10.5, 11.2; where the lengths vary (1000 x e^(0.3 N(0, 1))) 10.1 to 16.4,
+// 10.6 to 16.9 (128 items 14.0, 12.3). The lengths are on the device, so the
+// tables' width decides. For tables of 8192 tokens (128 items of 5000) 49, 25.
 constexpr int64_t kItemCtas = 304;
 constexpr int kItemPairs = 64;
-constexpr int kMinPairs = 2;  // pairs a warp should have at least, where there are few
+// Pairs a warp should have at least, where there are few: one item of 5000 tokens
+// 7.4 us (2: 8.4, 4: 10.0), of 30000 10.0 (9.4, 10.1).
+constexpr int kMinPairs = 1;
 
 int max_ctas(int head_dim) { return 152 * (head_dim == 256 ? i4_ctas_per_sm<256>() : i4_ctas_per_sm<128>()); }
 int warps(int head_dim) { return head_dim == 256 ? i4_warps<256>() : i4_warps<128>(); }

@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kFusedSeqs = 1024;
-constexpr int kFusedSlots = 4096;
+constexpr int kFusedSlots = 4096;  // 4000 slots of 1000 sequences: 6.2 us, in two kernels 8.7; 16000: 13.5, 8.3
 constexpr int kSlotsPerThread = 4;
 
 // Per-batch results of phase 1, in the workspace (or shared memory).
