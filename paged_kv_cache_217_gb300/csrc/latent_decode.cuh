@@ -400,14 +400,6 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       return bool(__all_sync(kFull, latent_wait(bar, parity, stop, a.status)));
     };
     while (ok && walk.next(a)) {
-      if (seg > 0) ok = wait_all(smem_addr(&sh.q_empty), (seg - 1) & 1);
-      if (!ok) break;
-      if (elect_one()) {
-        const uint32_t qb = smem_addr(&sh.q_full);
-        mbar_arrive_expect_tx(qb, C::Q_BYTES);
-        tma_load_4d(smem_addr(q_mem), &q_map, 0, h0, 0, walk.s, qb);
-      }
-      ++seg;
       // Block ids of the segment, 32 at a time and the next 32 ahead: lane l of
       // `ids` holds the id of block ids_from + l, of `ids_ahead` the one 32 on.
       // Blocks past the end name rows outside the tensor, which read as zeros.
@@ -424,8 +416,17 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       };
       int ids_from = 4 * walk.first;
       int ids = next_seq == walk.s && ids_from == 0 ? (lane < nb ? next_ids : a.num_blocks) : load_ids(ids_from);
-      ids = checked(ids, ids_from + lane);
       int ids_ahead = load_ids(ids_from + 32);
+      // the queries, while the ids are on their way
+      if (seg > 0) ok = wait_all(smem_addr(&sh.q_empty), (seg - 1) & 1);
+      if (!ok) break;
+      if (elect_one()) {
+        const uint32_t qb = smem_addr(&sh.q_full);
+        mbar_arrive_expect_tx(qb, C::Q_BYTES);
+        tma_load_4d(smem_addr(q_mem), &q_map, 0, h0, 0, walk.s, qb);
+      }
+      ++seg;
+      ids = checked(ids, ids_from + lane);
       // the next sequence's first ids, for its rows' way into L2
       next_seq = walk.s + 1;
       next_ids = next_seq < a.num_seqs && lane < a.max_blocks_per_seq
