@@ -151,13 +151,18 @@ def version():
 # ---------------------------------------------------------------------------
 # device calls (torch tensors)
 # ---------------------------------------------------------------------------
+_dtype_codes = {}
+
+
 def _dtype_code(t):
-    import torch
-    if t.dtype == torch.float16:
-        return PKV_F16
-    if t.dtype == torch.bfloat16:
-        return PKV_BF16
-    raise TypeError(f"unsupported dtype {t.dtype} (fp16 or bf16)")
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        import torch
+        _dtype_codes.update({torch.float16: PKV_F16, torch.bfloat16: PKV_BF16})
+        if t.dtype not in _dtype_codes:
+            raise TypeError(f"unsupported dtype {t.dtype} (fp16 or bf16)")
+        code = _dtype_codes[t.dtype]
+    return code
 
 
 def _need_cuda(*tensors):
@@ -169,13 +174,27 @@ def _need_cuda(*tensors):
             raise ValueError("tensors must be contiguous")
 
 
+_handles = None
+
+
+def _torch_handles():
+    """(current device's index, stream handle of a device index): torch's own where it has them (the stream
+    object and the device context of its public calls cost 8 us a launch)."""
+    global _handles
+    if _handles is None:
+        import torch
+        _handles = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                    getattr(torch._C, "_cuda_getCurrentRawStream",
+                            lambda index: torch.cuda.current_stream(index).cuda_stream))
+    return _handles
+
+
 def _stream_ptr(device):
-    import torch
     index = device.index
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None or index is None:
+    if index is None:
+        import torch
         return torch.cuda.current_stream(device).cuda_stream
-    return raw(index)  # (2 us less than building the stream object)
+    return _torch_handles()[1](index)
 
 
 def _launch(device, what, fn, *args):
@@ -183,10 +202,13 @@ def _launch(device, what, fn, *args):
     torch stream as the trailing cudaStream_t: the library looks up per-device
     state (the status word, the no-alloc scratch) on the current device, which
     must be the device of the tensors and of the stream."""
-    import torch
-    if device.index is not None and device.index == torch.cuda.current_device():  # (the context manager costs 6 us)
-        _check(fn(*args, _stream_ptr(device)), what)
+    index, (current, stream) = device.index, _torch_handles()
+    if index is not None and index == current():
+        status = fn(*args, stream(index))
+        if status:
+            _check(status, what)
         return
+    import torch
     with torch.cuda.device(device):
         _check(fn(*args, _stream_ptr(device)), what)
 
