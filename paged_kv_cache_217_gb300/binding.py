@@ -499,8 +499,15 @@ def _scratch(device, nbytes):
     return ws
 
 
-def _ptr_bytes(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+def _call_workspace(t, need, workspace):
+    """(tensor to keep, address, bytes) of a call's workspace on t's device: the caller's or the binding's own."""
+    if not need:
+        return None, None, 0
+    if workspace is None:
+        workspace = _scratch(t.device, need)
+    else:
+        _need_cuda(t, workspace)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def int4_tile_bytes(head_dim):
@@ -583,9 +590,7 @@ def paged_attention_decode_int4(out, q, kv_cache, block_tables, context_lens, sc
     nb, hkv = tiles[0], tiles[1]
     mb = table[1]
     need = int4_workspace_size(S, Hq, hkv, D, mb, window)
-    if workspace is None:
-        workspace = _scratch(q.device, need)
-    ws_ptr, ws_bytes = _ptr_bytes(workspace if need else None)
+    ws, ws_ptr, ws_bytes = _call_workspace(q, need, workspace)
     _launch(q.device, "paged_attention_decode_int4", lib().pkv_paged_attention_decode_int4, out.data_ptr(),
             q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Hq, hkv, D, mb, nb,
             float(scale), dt, window, ws_ptr, ws_bytes)
@@ -661,9 +666,7 @@ def paged_latent_decode(out, q, cache, block_tables, context_lens, scale, worksp
     S, H, _ = shape
     mb = table[1]
     need = latent_workspace_size(S, H, mb)
-    if workspace is None:
-        workspace = _scratch(q.device, need)
-    ws_ptr, ws_bytes = _ptr_bytes(workspace if need else None)
+    ws, ws_ptr, ws_bytes = _call_workspace(q, need, workspace)
     _launch(q.device, "paged_latent_decode", lib().pkv_paged_latent_decode, out.data_ptr(), q.data_ptr(),
             cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, H, mb, cache.shape[0], float(scale),
             dt, ws_ptr, ws_bytes)
@@ -714,9 +717,7 @@ def extend_block_tables(block_tables, context_lens, new_tokens, free_stack, free
             raise ValueError("info holds four values")
     n = slot_mapping.shape[0]
     need = int(lib().pkv_extend_workspace_size(S, n))
-    if workspace is None:
-        workspace = _scratch(block_tables.device, need)
-    ws_ptr, ws_bytes = _ptr_bytes(workspace if need else None)
+    ws, ws_ptr, ws_bytes = _call_workspace(block_tables, need, workspace)
     _launch(block_tables.device, "extend_block_tables", lib().pkv_extend_block_tables, block_tables.data_ptr(),
             context_lens.data_ptr(), new_tokens.data_ptr(), S, mb, free_stack.data_ptr(), free_count.data_ptr(),
             free_stack.shape[0], None if refcounts is None else refcounts.data_ptr(), new_lens.data_ptr(),
@@ -740,9 +741,7 @@ def release_sequences(block_tables, context_lens, finished, free_stack, free_cou
     if refcounts is not None and refcounts.shape != free_stack.shape:
         raise ValueError("refcounts must be [num_blocks]")
     nb = free_stack.shape[0]
-    if workspace is None:
-        workspace = _scratch(block_tables.device, int(lib().pkv_release_workspace_size(nb)))
-    ws_ptr, ws_bytes = _ptr_bytes(workspace)
+    ws, ws_ptr, ws_bytes = _call_workspace(block_tables, int(lib().pkv_release_workspace_size(nb)), workspace)
     _launch(block_tables.device, "release_sequences", lib().pkv_release_sequences, block_tables.data_ptr(),
             context_lens.data_ptr(), finished.data_ptr(), S, mb, free_stack.data_ptr(), free_count.data_ptr(), nb,
             None if refcounts is None else refcounts.data_ptr(), ws_ptr, ws_bytes)

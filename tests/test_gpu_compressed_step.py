@@ -275,3 +275,29 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         B.release_sequences(tab, lens, i32(2), i32(5), i32(1), refcounts=i32(4))
     assert B.device_status(clear=True) == 0
+
+
+def test_workspaces_elsewhere_are_refused():
+    S, mb = 40, 130
+    tab, lens = torch.zeros((S, mb), dtype=torch.int32, device="cuda"), torch.zeros(S, dtype=torch.int32, device="cuda")
+    q4 = torch.zeros((S, 12, 64), dtype=torch.float16, device="cuda")
+    ql = torch.zeros((S, 16, 576), dtype=torch.float16, device="cuda")
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    calls = [
+        lambda ws: B.paged_attention_decode_int4(torch.empty_like(q4), q4, torch.zeros((4, 12, 1152), dtype=torch.uint8,
+                                                 device="cuda"), tab, lens, 1.0, workspace=ws),
+        lambda ws: B.paged_latent_decode(torch.empty((S, 16, 512), dtype=ql.dtype, device="cuda"), ql,
+                                         torch.zeros((4, 16, 576), dtype=ql.dtype, device="cuda"), tab, lens, 1.0,
+                                         workspace=ws),
+        lambda ws: B.extend_block_tables(tab, lens, i32(S), i32(4), i32(1), torch.zeros(5000, dtype=torch.int64,
+                                         device="cuda"), workspace=ws),
+        lambda ws: B.release_sequences(tab, lens, i32(S), i32(4), i32(1), workspace=ws)]
+    size = 64 << 20
+    for call in calls:
+        call(torch.empty(size, dtype=torch.uint8, device="cuda"))
+        for bad in (torch.empty(size, dtype=torch.uint8), torch.empty(2 * size, dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError):
+                call(bad)
+        with pytest.raises(B.PagedKVError):
+            call(torch.empty(size, dtype=torch.uint8, device="cuda")[8:])
+    assert B.device_status(clear=True) == 0
