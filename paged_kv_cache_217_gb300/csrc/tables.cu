@@ -22,6 +22,8 @@
 // by the slot map's 8 bytes a token for prompts. A batch of at most
 // kFusedSeqs sequences and kFusedSlots slots runs both phases in one CTA, with
 // the offsets in shared memory.
+// No kernel here lets its successor start early (griddepcontrol.launch_dependents):
+// the launch plan's kernels read lengths and tables before they wait.
 #include <cuda_runtime.h>
 
 #include <climits>

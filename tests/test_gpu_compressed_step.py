@@ -301,3 +301,45 @@ def test_workspaces_elsewhere_are_refused():
         with pytest.raises(B.PagedKVError):
             call(torch.empty(size, dtype=torch.uint8, device="cuda")[8:])
     assert B.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("S", [6, 160])
+def test_device_tables_feed_the_launch_plan(S):
+    """extend_block_tables, then the 16-bit step's plan, cache write and planned decode, with no wait between:
+    the same bits as over the host manager's tables."""
+    hq, hkv, D, width, nb = 4, 2, 64, 8, 1200
+    rng = np.random.default_rng(S)
+    host = B.BlockManager(nb, rng.permutation(nb).astype(np.int32))
+    prompts = rng.integers(1, 90, S)
+    for s, n in enumerate(prompts):
+        host.add_seq(s, int(n))
+    tables, lens = host.block_tables(range(S), width)
+    free = host.free_stack()
+    stack = np.zeros(nb, np.int32)
+    stack[:len(free)] = free
+    dev = lambda a: torch.as_tensor(np.asarray(a), dtype=torch.int32).cuda()  # noqa: E731
+    tab, ln, stk, cnt, one = dev(tables), dev(lens), dev(stack), dev([len(free)]), dev(np.ones(S))
+    slots = torch.empty(S, dtype=torch.int64, device="cuda")
+    kp, vp = (W.normal_values((nb, hkv, 16, D), "bf16", s, "cuda") for s in (1, 2))
+    k, v = (W.normal_values((8, S, hkv, D), "bf16", s, "cuda") for s in (3, 4))
+    q = W.normal_values((8, S, hq, D), "bf16", 5, "cuda")
+    outs = torch.empty_like(q)
+    kp2, vp2 = kp.clone(), vp.clone()
+    torch.cuda.synchronize()
+    for i in range(8):
+        B.extend_block_tables(tab, ln, one, stk, cnt, slots)
+        B.paged_attention_plan(ln, tab, hq, hkv, D)
+        B.reshape_and_cache(k[i], v[i], kp, vp, slots)
+        B.paged_attention_decode(outs[i], q[i], kp, vp, tab, ln, 0.125, planned=True)
+    torch.cuda.synchronize()
+    for i in range(8):
+        host_slots, pairs = host.append_slots(range(S))
+        assert len(pairs) == 0
+        tables, lens = host.block_tables(range(S), width)
+        B.reshape_and_cache(k[i], v[i], kp2, vp2, torch.from_numpy(host_slots).cuda())
+        t2, l2, out = dev(tables), dev(lens), torch.empty_like(q[i])
+        B.paged_attention_plan(l2, t2, hq, hkv, D)
+        torch.cuda.synchronize()
+        B.paged_attention_decode(out, q[i], kp2, vp2, t2, l2, 0.125, planned=True)
+        assert torch.equal(out, outs[i])
+    assert torch.equal(kp, kp2) and torch.equal(vp, vp2) and B.device_status(clear=True) == 0
