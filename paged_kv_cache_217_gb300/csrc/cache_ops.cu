@@ -217,9 +217,9 @@ __global__ void bounded_wait_selftest_kernel(unsigned long long limit_ns, unsign
 // {kPlanMagic, S, 0, 0}, which the decode kernels check before they use the
 // order. One CTA, one thread per sequence (S <= 1024). Launched with
 // programmatic dependent launch: it lets a decode grid that follows become
-// resident at once, reads only the lengths (which no kernel of this library
-// writes), and waits for its own predecessor before it exits, so its
-// completion implies that predecessor's.
+// resident at once, reads only the lengths and tables (which no
+// kernel of this library writes that lets its successor start early), and waits for
+// its own predecessor before it exits, so its completion implies that predecessor's.
 __global__ void __launch_bounds__(1024)
 seq_order_kernel(const int32_t* __restrict__ lens, int S, int max_len, int window, int short_last,
                  int32_t* __restrict__ order, int4* __restrict__ header, const int32_t* __restrict__ tables,
