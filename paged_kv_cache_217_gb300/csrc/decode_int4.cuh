@@ -192,8 +192,8 @@ __device__ __forceinline__ void i4_load_query(const T* q0, int group, int lane, 
     raw.u[g][0] = raw.u[g][1] = make_uint4(0, 0, 0, 0);
     if (head < group) {
       const uint4* src = reinterpret_cast<const uint4*>(q0 + size_t(head) * D + 64 * g + 16 * t);
-      raw.u[g][0] = __ldg(src);
-      raw.u[g][1] = __ldg(src + 1);
+      raw.u[g][0] = *src;
+      raw.u[g][1] = src[1];
     }
   }
 }
@@ -526,7 +526,7 @@ struct I4Seq {
   int L, t0, nt, np, head;  // length, first tile, tiles, pairs, rows of the first tile before the window
 };
 __device__ __forceinline__ int i4_len(const Int4Args& a, int s) {
-  const int L = __ldg(a.context_lens + s), most = a.max_blocks_per_seq * kBlock;
+  const int L = a.context_lens[s], most = a.max_blocks_per_seq * kBlock;
   return L < 0 ? 0 : L > most ? most : L;
 }
 __device__ __forceinline__ I4Seq i4_seq(const Int4Args& a, int L) {
@@ -567,6 +567,8 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
     mbar_init_fence();
   }
   asm volatile("griddepcontrol.launch_dependents;");
+  // (what follows reads by plain loads: read-only ones are for what no running
+  // kernel writes, and the last kernel may have run until now)
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // This CTA's range [cb, ce) of the list of total pairs, this warp's [wb, we),
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
   auto warp_begin = [&](int w) { return cb + (ce - cb) * w / NW; };
   if (a.item_ctas) {  // one item: the list is its own
     s = int(blockIdx.x) / Hkv;
-    const int raw = __ldg(a.context_lens + s), g = int(blockIdx.x) - s * Hkv;
+    const int raw = a.context_lens[s], g = int(blockIdx.x) - s * Hkv;
     L = i4_len(a, s);
     if (raw != L && g == 0 && tid == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
     const int np = i4_seq(a, L).np;
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
     for (int i0 = run0; i0 < run1; i0 += 4) {
       int raw[4];  // (loads together)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) raw[j] = i0 + j < run1 ? __ldg(a.context_lens + i0 + j) : 0;
+      for (int j = 0; j < 4; ++j) raw[j] = i0 + j < run1 ? a.context_lens[i0 + j] : 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (i0 + j >= run1) break;
@@ -691,7 +693,7 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
       }
       const int at = x - cfrom, cg = at / c.np, j = 2 * (at - cg * c.np) + (lane & 1);
       if (j >= c.nt) return -1;
-      int id = __ldg(a.block_tables + size_t(cs) * a.max_blocks_per_seq + c.t0 + j);
+      int id = a.block_tables[size_t(cs) * a.max_blocks_per_seq + c.t0 + j];
       if (id < 0 || id >= a.num_blocks) {
         flag(a.status, PKV_DEV_BAD_BLOCK_ID);
         id = 0;

@@ -215,7 +215,7 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
 
 // ---- work -------------------------------------------------------------------
 __device__ __forceinline__ int latent_len(const LatentArgs& a, int s) {
-  const int L = __ldg(a.context_lens + s), most = a.max_blocks_per_seq * kBlock;
+  const int L = a.context_lens[s], most = a.max_blocks_per_seq * kBlock;
   return L < 0 ? 0 : L > most ? most : L;
 }
 __device__ __forceinline__ int latent_tiles(int L) { return (L + kLatentTile - 1) / kLatentTile; }
@@ -336,7 +336,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
   long long mine = 0;
   int len = 0;  // of the run's last sequence
   for (int s = run0; s < run1; ++s) {
-    const int raw = __ldg(a.context_lens + s), most = a.max_blocks_per_seq * kBlock;
+    const int raw = a.context_lens[s], most = a.max_blocks_per_seq * kBlock;
     if ((raw < 0 || raw > most) && blockIdx.x == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
     len = raw < 0 ? 0 : raw > most ? most : raw;
     mine += latent_tiles(len);
@@ -407,7 +407,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       const int32_t* row = a.block_tables + size_t(walk.s) * a.max_blocks_per_seq;
       auto load_ids = [&](int from) {
         const int j = from + lane;
-        return j < nb ? __ldg(row + j) : a.num_blocks;
+        return j < nb ? row[j] : a.num_blocks;
       };
       auto checked = [&](int id, int j) {
         if (id >= 0 && (id < a.num_blocks || j >= nb)) return id;
@@ -430,7 +430,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
       // the next sequence's first ids, for its rows' way into L2
       next_seq = walk.s + 1;
       next_ids = next_seq < a.num_seqs && lane < a.max_blocks_per_seq
-                     ? __ldg(a.block_tables + size_t(next_seq) * a.max_blocks_per_seq + lane)
+                     ? a.block_tables[size_t(next_seq) * a.max_blocks_per_seq + lane]
                      : 0;
       const int next_nb = walk.at < walk.end && next_seq < a.num_seqs ? (walk.ahead + kBlock - 1) / kBlock : 0;
       for (int t = walk.first; ok && t < walk.last; ++t, ++tile) {
