@@ -28,10 +28,15 @@
 //  * O^T += C_V^T P~: head dims on M, tokens on K, fp16. V words of tokens t
 //    and t + 4 (t + 8 and t + 12) are merged by halves and masked: 10
 //    instructions for 16 codes (nibble_sums).
-//    P~ = p s 2^e rounded to fp16 once (2^-11 relative, far below the codes'
-//    own step), e a power of two per warp that keeps P~ below 2^15; the score
-//    fragment becomes the weight operand through movmatrix. The offsets' part
-//    sum p z is kept in fp32 per (head, group).
+//    P~ = p s 2^e rounded to fp16 once, e a power of two per warp that keeps P~
+//    below 2^15; the score fragment becomes the weight operand through movmatrix.
+//    The offsets' part sum p z is kept in fp32 per (head, group). With fp16 values
+//    7.5 times what the rounding of P~ left joins it: the products' error is then
+//    2^-11 relative of p s (c - 7.5), which is as large as the values, not of p s
+//    c, several times them (z is as large with the other sign). Outputs of 100
+//    tokens are 0.00025 (relative, rms) from a 64-bit computation, 0.00048 without;
+//    rounding them to fp16 alone gives 0.00021. Rounding to bf16 gives 0.0016, so
+//    there the step is left out (it costs 2 %, 59.0 us against 57.9).
 //  * The running maximum is only a reference: it moves when a score exceeds it
 //    by more than 8 (weights up to 2^8; one vote a step), so most steps need no
 //    cross-lane maximum and no rescaling. Sums and the accumulator are fp32.
@@ -53,6 +58,8 @@
 #pragma once
 
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "decode.cuh"
 #include "device_common.cuh"
@@ -259,7 +266,7 @@ struct I4State {
   float o[D / 16][4];            // O^T fragments in units of 2^-24 / vmul; odd ones hold even + 16 * odd nibbles
   float z[D / kInt4Group][PL];   // this lane's part of sum p z
   float m[PL], l[PL];            // reference maximum (log2 domain), this lane's part of sum p
-  float vbound, vmul;            // P~ = p s vmul, for s below vbound
+  float vbound, vmul, vleft;     // P~ = p s vmul, for s below vbound; 7.5 / vmul
 };
 
 // The scores (log2 domain) of tile rows gr (x[0]) and gr + 8 (x[1]).
@@ -367,6 +374,7 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
       const float mul = __uint_as_float(uint32_t(127 + 7 - E) << 23);
       ratio = mul / st.vmul;  // a power of two: exact
       st.vmul = mul;
+      st.vleft = 7.5f * __uint_as_float(uint32_t(127 - 7 + E) << 23);
       st.vbound = __uint_as_float(uint32_t(127 + E) << 23);
     }
     float r[PL];
@@ -423,7 +431,14 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float s = v[2 * n + r][g].x;
-        const __half2 h = __floats2half2_rn(p[2 * n + r][0] * s, p[2 * n + r][PL - 1] * s);
+        const float x0 = p[2 * n + r][0] * s, x1 = p[2 * n + r][PL - 1] * s;
+        const __half2 h = __floats2half2_rn(x0, x1);
+        if constexpr (std::is_same<T, __half>::value) {
+          // what the rounding left goes with the offsets, as if every code were 7.5
+          const float2 back = __half22float2(h);
+          st.z[g][0] = fmaf(x0 - back.x, st.vleft, st.z[g][0]);
+          if (PL == 2) st.z[g][PL - 1] = fmaf(x1 - back.y, st.vleft, st.z[g][PL - 1]);
+        }
         pb[r] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h));
       }
 #pragma unroll
@@ -517,6 +532,7 @@ __device__ __forceinline__ void i4_clear(I4State<D, H>& st) {
   }
   st.vbound = 0x1p-98f;
   st.vmul = 0x1p105f;
+  st.vleft = 7.5f * 0x1p-105f;
 }
 
 // ---- work ---------------------------------------------------------------------

@@ -355,3 +355,16 @@ def test_a_workspace_of_the_callers():
     assert (ws[-64:] == 0xFF).all()
     with pytest.raises(B.PagedKVError, match="workspace"):
         c.run(workspace=ws[:-65])
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(64, 8, 1), (128, 2, 2), (256, 4, 2)])
+def test_fp16_outputs_are_near_their_own_rounding(D, hq, hkv):
+    """Relative rms error of fp16 outputs. A rounding to fp16 is off by at most 2^-11 relative, uniformly: rms at
+    most a = 2^-11 / sqrt(3), about 0.72 a over mantissas from 1 to 2. The output has one; every weight p s has one,
+    which its value's p s (c - 7.5) takes on, the value less its group's midrange: for 64 normal values of rms v that
+    is at most 1.1 v. Together 0.72 a sqrt(1 + 1.1^2) = 1.07 a at most; sqrt(2) a is allowed. (With codes that are
+    not centred it would be p s c, of rms 2.6 v for a minimum 2.4 v below the mean: 2 a.)"""
+    c = Case([100, 240, 33], hq, hkv, D, "f16", 40)
+    want, _ = O4.decode(W.to_numpy_storage(c.q, "f16"), c.kc, c.kp, c.vc, c.vp, c.tables_np, c.lens_np, c.scale, "f16", 0)
+    err = np.sqrt(((H.to_f64(c.run()) - want) ** 2).mean() / (want ** 2).mean())
+    assert err <= 2.0 ** 0.5 * 2.0 ** -11 / 3 ** 0.5, err
