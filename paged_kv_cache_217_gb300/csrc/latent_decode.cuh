@@ -37,9 +37,10 @@
 // of products a tile) the cache's bytes bound it.
 // The running maximum is a reference that moves only when a score exceeds it
 // by 2^8 (one vote a tile); moving it rescales O^T in tensor memory. Weights
-// are rounded to the cache's type (bf16: 2^-8 relative, one per weight, which
-// averages out over the tokens; their sum is taken before the rounding in
-// fp32).
+// are rounded to the cache's type (bf16: 2^-8 relative, one per weight). Their sum,
+// in fp32, is of the rounded ones, so that the error is that of a weighted mean:
+// delta_t p_t (c_t - out), nothing where one token has all the weight or the rows
+// are alike.
 //
 // Work: the batch's tiles are one list cut into equal ranges, one per CTA (per
 // block of heads), whatever the lengths. A sequence inside one range is written
@@ -211,6 +212,17 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t u);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
 // ---- work -------------------------------------------------------------------
@@ -646,16 +658,13 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
             }
           softmax_sync(half);
         }
-        float p[G8][4];
+        uint32_t p[G8][2];  // weights of rows gr and gr + 8, two heads each
 #pragma unroll
-        for (int i = 0; i < G8; ++i)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float ref = m[i][e] == -INFINITY ? 0.f : m[i][e];
-            p[i][e] = fast_exp2(x[i][e] - ref);
-            p[i][2 + e] = fast_exp2(x[i][2 + e] - ref);
-            l[i][e] += p[i][e] + p[i][2 + e];
-          }
+        for (int i = 0; i < G8; ++i) {
+          const float ref0 = m[i][0] == -INFINITY ? 0.f : m[i][0], ref1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
+          p[i][0] = pack2<T>(fast_exp2(x[i][0] - ref0), fast_exp2(x[i][1] - ref1));
+          p[i][1] = pack2<T>(fast_exp2(x[i][2] - ref0), fast_exp2(x[i][3] - ref1));
+        }
         // P and O^T are free once the previous tile's product is done
         if (tile > 0) latent_wait(smem_addr(&sh.pv_done), (tile - 1) & 1, stop, a.status);
         if (moving && u > walk.first) {
@@ -689,20 +698,24 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         const int b = lane >> 3, chunk = 2 * quarter + (b & 1);
         if constexpr (G8 == 1) {
           const int head = hs + (lane & 7);
-          stsm_x2_trans(smem_addr(p_mem) + head * 128 + ((chunk ^ (head & 7)) << 4), pack2<T>(p[0][0], p[0][1]),
-                        pack2<T>(p[0][2], p[0][3]));
+          stsm_x2_trans(smem_addr(p_mem) + head * 128 + ((chunk ^ (head & 7)) << 4), p[0][0], p[0][1]);
         } else {
 #pragma unroll
           for (int i = 0; i < G8; i += 2) {
             const int head = hs + 8 * (i + (b >> 1)) + (lane & 7);
-            stsm_x4_trans(smem_addr(p_mem) + head * 128 + ((chunk ^ (head & 7)) << 4), pack2<T>(p[i][0], p[i][1]),
-                          pack2<T>(p[i][2], p[i][3]), pack2<T>(p[i + 1][0], p[i + 1][1]),
-                          pack2<T>(p[i + 1][2], p[i + 1][3]));
+            stsm_x4_trans(smem_addr(p_mem) + head * 128 + ((chunk ^ (head & 7)) << 4), p[i][0], p[i][1], p[i + 1][0],
+                          p[i + 1][1]);
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();
         mbar_arrive(smem_addr(&sh.p_full));
+#pragma unroll
+        for (int i = 0; i < G8; ++i) {
+          const float2 a = unpack2<T>(p[i][0]), b = unpack2<T>(p[i][1]);
+          l[i][0] += a.x + b.x;
+          l[i][1] += a.y + b.y;
+        }
       }
       // The segment's sums, then its output: thread = dim, columns = heads.
 #pragma unroll
