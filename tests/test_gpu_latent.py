@@ -200,3 +200,20 @@ def test_many_heads(heads):
     c = Case([130, 1, 0, 700], heads, "bf16", 17)
     c.check(c.run(), heads=[0, 43, 64, heads // 2, heads - 1])
     assert B.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("heads", [16, 128])
+def test_latents_alike_come_back_as_they_are(dtype, heads):
+    """A weighted mean of equal values is the value, whatever the (rounded) weights: they differ here by the rotary
+    parts. The two fp32 sums of n terms are off by n 2^-24 relative each at most, 2^-10.7 together for 5000: under
+    half a bf16 step (2^-9 at least), and under one and a half of fp16 (2^-11 each at least), so that rounds to the
+    value or, in fp16, to one at most two steps (2^-10 each at most) from it."""
+    c = Case([1, 63, 700, 5000], heads, dtype, 19)
+    rows = W.normal_values((4, 512), dtype, 20, "cuda")
+    for s, n in enumerate(c.lens_np.tolist()):
+        ids = torch.from_numpy(c.tables_np[s, :-(-n // 16)].astype(np.int64)).cuda()
+        c.cache[ids, :, :512] = rows[s]
+    out, want = H.to_f64(c.run()), H.to_f64(rows)[:, None]
+    step = 0.0 if dtype == "bf16" else 2.0 ** -9
+    assert (np.abs(out - want) <= step * np.abs(want)).all()
