@@ -18,7 +18,7 @@
 // workspace, and the all-or-nothing checks), then every table entry and slot
 // is filled independently (phase 2), each warp finding its sequences in the
 // offsets by 32 probes a round (a binary search per thread: 11.4 us against 10.3
-// for 700 prompts of 1.2M tokens). Bound by launch latency for a decode step and
+// for 700 prompts of 1.2M tokens, at 4 slots a thread in CTAs of 256). Bound by launch latency for a decode step and
 // by the slot map's 8 bytes a token for prompts. A batch of at most
 // kFusedSeqs sequences and kFusedSlots slots runs both phases in one CTA, with
 // the offsets in shared memory.
@@ -39,7 +39,12 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kFusedSeqs = 1024;
 constexpr int kFusedSlots = 4096;  // 4000 slots of 1000 sequences: 6.2 us, in two kernels 8.7; 16000: 13.5, 8.3
-constexpr int kSlotsPerThread = 4;
+constexpr int kFillThreads = 128;
+// Slots a thread takes at a time. One CTA: 1 while that is one turn (256 slots 4.4
+// us; 4 a thread 5.7), else 4 (4000 slots 6.2; 1 a thread 8.9). A grid: 2 (300000
+// slots 6.6 us; 4 7.0, 8 7.4), from kManySlots 4 (600000 slots 7.3; 2 8.2; 1.2M 9.6;
+// 2 11.4, 8 9.6).
+constexpr int kManySlots = 400000;
 
 // Per-batch results of phase 1, in the workspace (or shared memory).
 struct Scan {
@@ -214,21 +219,22 @@ __device__ __forceinline__ int taken(const ExtendArgs& a, int count, int i) {
 
 // Phase 2: thread `tid` of `threads`. WARP: the offsets are in global memory, so a
 // warp searches them together (in shared memory each thread does).
-template <bool WARP>
+// U: slots a thread takes at a time.
+template <bool WARP, int U>
 __device__ __forceinline__ void fill(const ExtendArgs& a, const Scan& w, int64_t tid, int64_t threads) {
   const int S = a.num_seqs;
   const bool ok = w.head[0] != 0;
   const int count = w.head[1], tokens = w.tok[S], blocks = w.blk[S];
   const int lane = threadIdx.x & 31;
-  for (int64_t w0 = (tid - lane) * kSlotsPerThread; w0 < a.num_slots; w0 += threads * kSlotsPerThread) {
-    const int64_t i0 = w0 + lane * kSlotsPerThread;
-    int64_t slot[kSlotsPerThread];
+  for (int64_t w0 = (tid - lane) * U; w0 < a.num_slots; w0 += threads * U) {
+    const int64_t i0 = w0 + lane * U;
+    int64_t slot[U];
     int s = 0;
     if (!WARP) {
       if (i0 < tokens) s = owner(w.tok, 0, S, int(i0));
     } else if (w0 < tokens) {  // the sequences of the warp's first and last token, then this thread's between them
       const int first = warp_owner(w.tok, S, int(w0));
-      const int last = warp_owner(w.tok, S, int(min(w0 + 32 * kSlotsPerThread, int64_t(tokens)) - 1));
+      const int last = warp_owner(w.tok, S, int(min(w0 + 32 * U, int64_t(tokens)) - 1));
       s = owner(w.tok, first, last + 1, int(min(i0, int64_t(tokens) - 1)));
     }
     int begin = 0, end = 0, L = 0, blk = 0, copied = 0;  // of sequence s
@@ -242,7 +248,7 @@ __device__ __forceinline__ void fill(const ExtendArgs& a, const Scan& w, int64_t
     if (i0 < tokens) enter();
     int at = -1, phys = -1;  // block index and id of the previous token
 #pragma unroll
-    for (int u = 0; u < kSlotsPerThread; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int64_t i = i0 + u;
       slot[u] = -1;
       if (i >= tokens) continue;
@@ -269,13 +275,13 @@ __device__ __forceinline__ void fill(const ExtendArgs& a, const Scan& w, int64_t
       }
       if (phys >= 0) slot[u] = int64_t(phys) * kBlock + pos % kBlock;
     }
-    if (i0 + kSlotsPerThread <= a.num_slots && a.slots_aligned) {
+    if (U > 1 && i0 + U <= a.num_slots && a.slots_aligned) {
       longlong2* dst = reinterpret_cast<longlong2*>(a.slot_mapping + i0);
 #pragma unroll
-      for (int u = 0; u < kSlotsPerThread; u += 2) dst[u / 2] = make_longlong2(slot[u], slot[u + 1]);
+      for (int u = 0; u + 1 < U; u += 2) dst[u / 2] = make_longlong2(slot[u], slot[u + 1]);
     } else {
 #pragma unroll
-      for (int u = 0; u < kSlotsPerThread; ++u)
+      for (int u = 0; u < U; ++u)
         if (i0 + u < a.num_slots) a.slot_mapping[i0 + u] = slot[u];
     }
   }
@@ -321,19 +327,21 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const ExtendArgs a) {
   scan_batch(a, scan_of(a.workspace, a.num_seqs));
 }
 
-__global__ void __launch_bounds__(256) fill_kernel(const ExtendArgs a) {
+template <int U>
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const ExtendArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  fill<true>(a, scan_of(a.workspace, a.num_seqs), int64_t(blockIdx.x) * blockDim.x + threadIdx.x,
+  fill<true, U>(a, scan_of(a.workspace, a.num_seqs), int64_t(blockIdx.x) * blockDim.x + threadIdx.x,
        int64_t(gridDim.x) * blockDim.x);
 }
 
+template <int U>
 __global__ void __launch_bounds__(kThreads) fused_kernel(const ExtendArgs a) {
   __shared__ int32_t ws[6 * kFusedSeqs + 6];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Scan w = scan_of(ws, a.num_seqs);
   scan_batch(a, w);
   __syncthreads();
-  fill<false>(a, w, threadIdx.x, kThreads);
+  fill<false, U>(a, w, threadIdx.x, kThreads);
 }
 
 // ---- release ---------------------------------------------------------------
@@ -422,15 +430,17 @@ size_t extend_workspace_bytes(int num_seqs, int num_slots) {
 
 cudaError_t launch_extend_block_tables(const ExtendArgs& a, cudaStream_t stream) {
   if (a.num_seqs <= kFusedSeqs && a.num_slots <= kFusedSlots)
-    return launch_after(fused_kernel, 1u, unsigned(kThreads), stream, a);
+    return launch_after(a.num_slots <= kThreads ? fused_kernel<1> : fused_kernel<4>, 1u, unsigned(kThreads), stream, a);
   cudaError_t err = launch_after(scan_kernel, 1u, unsigned(kThreads), stream, a);
   if (err != cudaSuccess) return err;
-  // one thread per kSlotsPerThread slots, at most 8 CTAs per SM of a GB300
-  int64_t threads = (int64_t(a.num_slots) + kSlotsPerThread - 1) / kSlotsPerThread;
+  const bool many = a.num_slots >= kManySlots;
+  const int64_t per = many ? 4 : 2;
+  int64_t threads = (int64_t(a.num_slots) + per - 1) / per;
   if (threads < a.num_seqs) threads = a.num_seqs;
-  int64_t ctas = (threads + 255) / 256;
-  if (ctas > 8 * 152) ctas = 8 * 152;
-  return launch_after(fill_kernel, unsigned(ctas < 1 ? 1 : ctas), 256u, stream, a);
+  int64_t ctas = (threads + kFillThreads - 1) / kFillThreads;
+  if (ctas > 16 * 152) ctas = 16 * 152;  // 16 per SM of a GB300
+  return many ? launch_after(fill_kernel<4>, unsigned(ctas), unsigned(kFillThreads), stream, a)
+              : launch_after(fill_kernel<2>, unsigned(ctas < 1 ? 1 : ctas), unsigned(kFillThreads), stream, a);
 }
 
 cudaError_t launch_release_sequences(const ReleaseArgs& a, cudaStream_t stream) {
