@@ -6,8 +6,8 @@
 // 16-byte accesses of the 16-bit rows, and a warp holds the K and V rows of one
 // (token, KV head) at D = 128 (of two at 64; one of the two rows at 256). The 64
 // dims of a group sit in 8 lanes. Writing and reading back 12301 tokens of 8 heads
-// takes 31.6 us for 128 MB (4.1 TB/s); the write issues 170 instructions a warp
-// and token row and fills 60 % of the issue slots, which bounds it. One lane per
+// takes 31.0 us for 128 MB (4.1 TB/s); the write issues 159 instructions a warp
+// and token row and fills 56 % of the issue slots, which bounds it. One lane per
 // D/32 dims of both rows, with the IEEE division of every element, took 63 us; 16
 // dims a lane 32.0, and 4.7 us against 4.2 for a step of 64 tokens.
 #include <cuda_runtime.h>
@@ -131,7 +131,8 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
   const uint32_t nan = round_bits<T>(NAN);
   pair = finite ? uint32_t(s) | (uint32_t(round_bits<T>(float(both.x))) << 16) : nan | (nan << 16);
   const float half_s = 0.5f * from_bits<T>(s);
-  const float inv = __fdividef(1.f, half_s);
+  float inv;  // (approximate; subnormal half_s goes the other way below)
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(half_s));
   float x[8];
   Vec8<T>::to_float(u, x);
   // Dims i and i + 4 together. r is the product d inv rounded to an integer (on
@@ -162,14 +163,10 @@ __device__ __forceinline__ uint32_t quantize8(const uint4& u, uint32_t& pair) {
   return finite ? codes : 0u;
 }
 
-// Byte offsets in a tile of a thread's word and of its group's pair, for slot r.
+// Byte offset in a tile of a thread's word, for slot r in tile row `row`.
 template <int D>
-__device__ __forceinline__ uint32_t word_offset(const Int4Place& p, uint32_t r) {
-  return (p.v ? r : uint32_t(kv4_row(int(r)))) * (D / 2) + (p.at ^ ((r << p.shift) & p.turn));
-}
-template <int D>
-__device__ __forceinline__ uint32_t pair_offset(const Int4Place& p, uint32_t r) {
-  return (16 + p.v) * D + uint32_t(kv4_row(int(r))) * (D / 16) + 4 * (uint32_t(p.word) / 8);
+__device__ __forceinline__ uint32_t word_offset(const Int4Place& p, uint32_t r, uint32_t row) {
+  return (p.v ? r : row) * (D / 2) + (p.at ^ ((r << p.shift) & p.turn));
 }
 // The tile of a valid slot.
 template <int D, typename Byte>
@@ -188,6 +185,8 @@ reshape_and_cache_int4_kernel(const uint4* __restrict__ k, const uint4* __restri
   asm volatile("griddepcontrol.launch_dependents;");
   const Int4Place p = int4_place<D>(heads);
   const uint4* src = (p.v ? v : k) + p.head * (D / 8) + p.word;
+  const uint32_t pairs_at = (16 + p.v) * D + 4 * (uint32_t(p.word) / 8);  // of the group, in row 0
+  const bool lead = p.word % 8 == 0;
   int64_t slot[U];
   uint4 x[U];
 #pragma unroll
@@ -201,15 +200,14 @@ reshape_and_cache_int4_kernel(const uint4* __restrict__ k, const uint4* __restri
   for (int u = 0; u < U; ++u) {
     uint32_t pair;
     const uint32_t codes = quantize8<T>(x[u], pair);
-    if (slot[u] < 0) continue;
-    if (slot[u] >= num_slots) {
-      if (p.head == 0 && p.word == 0) flag(status, PKV_DEV_BAD_SLOT);
+    if (uint64_t(slot[u]) >= uint64_t(num_slots)) {  // (negative ones too)
+      if (slot[u] >= 0 && p.head == 0 && p.word == 0) flag(status, PKV_DEV_BAD_SLOT);
       continue;
     }
     unsigned char* tile = tile_of<D>(cache, p, slot[u], heads.d);
-    const uint32_t r = uint32_t(slot[u]) % kBlock;
-    *reinterpret_cast<uint32_t*>(tile + word_offset<D>(p, r)) = codes;
-    if (p.word % 8 == 0) *reinterpret_cast<uint32_t*>(tile + pair_offset<D>(p, r)) = pair;
+    const uint32_t r = uint32_t(slot[u]) % kBlock, row = uint32_t(kv4_row(int(r)));
+    *reinterpret_cast<uint32_t*>(tile + word_offset<D>(p, r, row)) = codes;
+    if (lead) *reinterpret_cast<uint32_t*>(tile + pairs_at + row * (D / 16)) = pair;
   }
 }
 
@@ -221,6 +219,7 @@ gather_cache_int4_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const uns
   const Int4Place p = int4_place<D>(heads);
   if (p.token >= stride) return;
   uint4* dst = (p.v ? v : k) + p.head * (D / 8) + p.word;
+  const uint32_t pairs_at = (16 + p.v) * D + 4 * (uint32_t(p.word) / 8);
   int64_t slot[U];
   uint32_t codes[U], pair[U];
 #pragma unroll
@@ -232,9 +231,9 @@ gather_cache_int4_kernel(uint4* __restrict__ k, uint4* __restrict__ v, const uns
       if (p.head == 0 && p.word == 0) flag(status, PKV_DEV_BAD_SLOT);
     } else if (slot[u] >= 0) {
       const unsigned char* tile = tile_of<D>(cache, p, slot[u], heads.d);
-      const uint32_t r = uint32_t(slot[u]) % kBlock;
-      codes[u] = *reinterpret_cast<const uint32_t*>(tile + word_offset<D>(p, r));
-      pair[u] = *reinterpret_cast<const uint32_t*>(tile + pair_offset<D>(p, r));
+      const uint32_t r = uint32_t(slot[u]) % kBlock, row = uint32_t(kv4_row(int(r)));
+      codes[u] = *reinterpret_cast<const uint32_t*>(tile + word_offset<D>(p, r, row));
+      pair[u] = *reinterpret_cast<const uint32_t*>(tile + pairs_at + row * (D / 16));
     }
   }
 #pragma unroll
