@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
     for (int i = 0; i < STAGES; ++i) mbar_init(bar_s + 8 * i, 1);
     mbar_init_fence();
   }
+  __syncwarp();  // a warp's other lanes use its barriers; with an item a CTA nothing else orders that
   asm volatile("griddepcontrol.launch_dependents;");
   // (what follows reads by plain loads: read-only ones are for what no running
   // kernel writes, and the last kernel may have run until now)
