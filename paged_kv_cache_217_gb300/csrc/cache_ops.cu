@@ -217,20 +217,22 @@ __global__ void bounded_wait_selftest_kernel(unsigned long long limit_ns, unsign
 // {kPlanMagic, S, 0, 0}, which the decode kernels check before they use the
 // order. One CTA, one thread per sequence (S <= 1024). Launched with
 // programmatic dependent launch: it lets a decode grid that follows become
-// resident at once, reads only the lengths and tables (which no
-// kernel of this library writes that lets its successor start early), and waits for
-// its own predecessor before it exits, so its completion implies that predecessor's.
+// resident at once. Before anything else it waits for its own predecessor: that may
+// write the lengths and tables (pkv_extend_block_tables), whose stores only the wait
+// makes visible, whether or not the predecessor's CTAs have ended, or may still use the
+// plan that this one replaces. Its completion implies the predecessor's. Lengths and
+// tables are read by plain loads, as read-only ones are for what no running kernel writes.
 __global__ void __launch_bounds__(1024)
-seq_order_kernel(const int32_t* __restrict__ lens, int S, int max_len, int window, int short_last,
-                 int32_t* __restrict__ order, int4* __restrict__ header, const int32_t* __restrict__ tables,
-                 int max_blocks, int4* __restrict__ rows) {
+seq_order_kernel(const int32_t* lens, int S, int max_len, int window, int short_last, int32_t* order, int4* header,
+                 const int32_t* tables, int max_blocks, int4* rows) {
   asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ long long part_tiles[32];
   __shared__ int part_long[32], part_rest[32], part_short[32];
   const int s = threadIdx.x, lane = s & 31, warp = s >> 5;
   int tiles = 0, raw_len = 0;
   if (s < S) {
-    int L = __ldg(lens + s);
+    int L = lens[s];
     raw_len = L;
     L = L < 0 ? 0 : (L > max_len ? max_len : L);
     if (window > 0 && L > window) L = window;
@@ -270,13 +272,12 @@ seq_order_kernel(const int32_t* __restrict__ lens, int S, int max_len, int windo
     if (rows) {  // the row of this rank: the sequence, its length and first six block ids (none without tables)
       int id[6];
 #pragma unroll
-      for (int i = 0; i < 6; ++i) id[i] = tables && i < max_blocks ? __ldg(tables + size_t(s) * max_blocks + i) : -1;
+      for (int i = 0; i < 6; ++i) id[i] = tables && i < max_blocks ? tables[size_t(s) * max_blocks + i] : -1;
       rows[2 * rank] = make_int4(tables ? s : -1, raw_len, id[0], id[1]);
       rows[2 * rank + 1] = make_int4(id[2], id[3], id[4], id[5]);
     }
   }
   if (s == 0) *header = make_int4(kPlanMagic, S, 0, 0);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Inclusive scan (sum, or max with MAX) over the threads of a CTA of up to
@@ -329,11 +330,11 @@ __device__ __forceinline__ int cta_inclusive_scan(int v, int* warp_tot) {
 // and zeroes the merge counters [S][Hkv]. One CTA of 1024 threads, S <= 1024,
 // tables of at most kPrefixMaxBlocks blocks; launched like seq_order_kernel.
 __global__ void __launch_bounds__(1024)
-prefix_plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__ tables, int S, int max_blocks,
-                   int Hkv, int slots, int min_blocks, int max_members, int4* __restrict__ header,
-                   int4* __restrict__ groups, int4* __restrict__ chunks, int32_t* __restrict__ others,
-                   unsigned int* __restrict__ counters) {
+prefix_plan_kernel(const int32_t* lens, const int32_t* tables, int S, int max_blocks, int Hkv, int slots,
+                   int min_blocks, int max_members, int4* header, int4* groups, int4* chunks, int32_t* others,
+                   unsigned int* counters) {
   asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ int slen[kOrderMaxSeqs];       // clamped lengths
   __shared__ int lcp[kOrderMaxSeqs];
   __shared__ int cwork[kOrderMaxSeqs / 2];  // per group: tiles of one chunk
@@ -342,7 +343,7 @@ prefix_plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__
   const int tid = threadIdx.x;
   const int max_len = max_blocks * kBlock;
   for (int s = tid; s < S; s += blockDim.x) {
-    int L = __ldg(lens + s);
+    int L = lens[s];
     slen[s] = L < 0 ? 0 : (L > max_len ? max_len : L);
   }
   for (int i = tid; i < S * Hkv; i += blockDim.x) counters[i] = 0u;
@@ -362,8 +363,8 @@ prefix_plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__
       ji[u] = i - si[u] * max_blocks;
       const bool on = i < entries && si[u] > 0 && ji[u] < lcp[si[u]];
       const int32_t* ra = tables + size_t(si[u]) * max_blocks + ji[u];
-      x[u] = on ? __ldg(ra) : 0;
-      y[u] = on ? __ldg(ra - max_blocks) : 0;
+      x[u] = on ? *ra : 0;
+      y[u] = on ? *(ra - max_blocks) : 0;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -474,7 +475,6 @@ prefix_plan_kernel(const int32_t* __restrict__ lens, const int32_t* __restrict__
     }
   }
   if (tid == 0) *header = make_int4(kPlanMagicPrefix, S, nchunks, n_others);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace

@@ -22,9 +22,6 @@
 // by the slot map's 8 bytes a token for prompts. A batch of at most
 // kFusedSeqs sequences and kFusedSlots slots runs both phases in one CTA, with
 // the offsets in shared memory.
-// No kernel here lets its successor start early (griddepcontrol.launch_dependents):
-// the launch plan's kernels read lengths and tables before they wait, which needs a
-// predecessor that completes first.
 #include <cuda_runtime.h>
 
 #include <climits>

@@ -36,3 +36,28 @@ def test_a_warp_waits_for_the_lane_that_initialised_its_barriers(name):
         end = _block_end(text, m.end() - 1)
         if "mbar_init(" in text[m.start():end]:
             assert text[end:].lstrip().startswith("__syncwarp();"), text[m.start():end + 120]
+
+
+# Kernels that programmatic dependent launches start while their predecessor still runs, or right behind it: only
+# griddepcontrol.wait makes the predecessor's stores visible. (launch_dependents itself needs no wait, a prefetch
+# brings no value, and barriers and tensor memory are the CTA's own.)
+GLOBAL = re.compile(r"__ldg\(|__ldcg\(|\b(lens|tables|header|order|rows|counters|groups|chunks|others)\[|"
+                    r"\ba\.(context_lens|block_tables|q|desc|part_ml|part_o|refcounts|free_stack|free_count)\b|\*ra\b")
+
+
+def _kernels(text):
+    for m in re.finditer(r"__global__[^;{]*?\b(\w+)\s*\(([^{;]*)\)\s*\{", text):
+        yield m.group(1), text[m.end():_block_end(text, m.end() - 1)]
+
+
+@pytest.mark.parametrize("name", [n for n in SOURCES if "griddepcontrol.wait" in _source(n)])
+def test_kernels_that_wait_do_so_before_they_touch_memory(name):
+    found = 0
+    for kernel, body in _kernels(_source(name)):
+        at = body.find("griddepcontrol.wait")
+        if at < 0:
+            continue
+        found += 1
+        first = GLOBAL.search(body)
+        assert first is None or first.start() > at, f"{kernel}: {body[first.start():first.start() + 60]!r} before the wait"
+    assert found or name == "decode.cuh"          # (there the wait is a function of its own)
