@@ -251,6 +251,18 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return fn;
 }
 
+// The encoder's call. It asks for a current context, which a host thread that has only
+// looked up its device (and taken cached addresses) does not have yet: cudaSetDevice
+// makes the device's primary context current.
+template <typename... Args>
+CUresult encode_tiled(PFN_cuTensorMapEncodeTiled_v12000 enc, Args... args) {
+  const CUresult r = enc(args...);
+  if (r != CUDA_ERROR_INVALID_CONTEXT) return r;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return r;
+  return enc(args...);
+}
+
 // A pool [num_blocks][num_kv_heads][16][head_dim] seen as a 2-D tensor of
 // num_blocks*num_kv_heads*16 rows by head_dim columns, read in boxes of
 // box_rows (16, 8 or 4) rows x 64 columns with the 128-byte swizzle.
@@ -262,7 +274,7 @@ pkv_status_t pool_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, i
   const cuuint64_t strides[1] = {cuuint64_t(head_dim) * 2};
   const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
   const cuuint32_t elem_strides[2] = {1, 1};
-  const CUresult r = enc(map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+  const CUresult r = encode_tiled(enc, map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                          2, const_cast<void*>(pool), dims, strides, box, elem_strides,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -282,7 +294,7 @@ pkv_status_t latent_tensor_map(CUtensorMap* map, const void* cache, int num_bloc
   const cuuint64_t strides[3] = {row, 128, 8 * row};
   const cuuint32_t box[4] = {64, 8, 3, 2};
   const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
-  const CUresult r = enc(map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+  const CUresult r = encode_tiled(enc, map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                          4, const_cast<void*>(cache), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -301,7 +313,7 @@ pkv_status_t query_tensor_map(CUtensorMap* map, const void* q, int num_seqs, int
   const cuuint64_t strides[3] = {cuuint64_t(width) * 2, 128, cuuint64_t(width) * 2 * cuuint64_t(num_heads)};
   const cuuint32_t box[4] = {64, cuuint32_t(box_heads), cuuint32_t(width / 64), 1};
   const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
-  const CUresult r = enc(map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+  const CUresult r = encode_tiled(enc, map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                          4, const_cast<void*>(q), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -319,7 +331,7 @@ pkv_status_t code_tensor_map(CUtensorMap* map, const void* pool, int64_t rows, i
   const cuuint64_t strides[1] = {cuuint64_t(head_dim)};
   const cuuint32_t box[2] = {cuuint32_t(head_dim < 128 ? head_dim : 128), PKV_BLOCK_SIZE};
   const cuuint32_t elem_strides[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box,
+  const CUresult r = encode_tiled(enc, map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pool), dims, strides, box,
                          elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);

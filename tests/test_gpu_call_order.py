@@ -1,6 +1,8 @@
 """Calls that follow one another with no wait between, or are made by two host threads at once, give what each gives
 alone."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -76,3 +78,43 @@ def test_a_plan_replaces_the_one_before_it():
             B.paged_attention_plan(n, tab, hq, hkv, D, workspace=ws)
             torch.cuda.synchronize()
             assert torch.equal(ws, alone)
+
+
+def _from_threads(jobs, rounds):
+    """Each job `rounds` times from a thread of its own, all started together; its results in order."""
+    start, results, errors = threading.Barrier(len(jobs)), [[] for _ in jobs], []
+
+    def work(i):
+        try:
+            start.wait()
+            for _ in range(rounds):
+                results[i].append(jobs[i]())
+        except BaseException as e:  # noqa: BLE001 (handed to the test)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    if errors:
+        raise errors[0]
+    return results
+
+
+def test_a_thread_whose_first_call_is_a_decode():
+    """The calls that encode tensor maps, from threads that have made no CUDA call before."""
+    q, pool = W.normal_values((3, 8, 64), "f16", 1, "cuda"), W.normal_values((4, 2, 16, 64), "f16", 2, "cuda")
+    ql, rows = W.normal_values((3, 16, 576), "f16", 3, "cuda"), W.normal_values((4, 16, 576), "f16", 4, "cuda")
+    tab, lens = _i32([[0], [2], [3]]), _i32([5, 16, 1])
+    out, ws = torch.zeros((2, 3, 8, 64), dtype=q.dtype, device="cuda"), torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+    outl = torch.zeros((2, 3, 16, 512), dtype=q.dtype, device="cuda")
+    calls = [lambda i: B.paged_attention_decode(out[i], q, pool, pool, tab, lens, 0.1, workspace=ws),
+             lambda i: B.paged_latent_decode(outl[i], ql, rows, tab, lens, 0.1, workspace=ws)]
+    for call in calls:                            # (every tensor is there: the thread's first CUDA call is the decode's)
+        call(0)
+        _from_threads([lambda: call(1)], 1)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], out[1]) and torch.equal(outl[0], outl[1]) and out.any() and outl.any()
+    assert B.device_status(clear=True) == 0
