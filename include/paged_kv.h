@@ -176,7 +176,10 @@ pkv_status_t pkv_selftest_bounded_wait(uint32_t limit_us, pkv_stream_t stream);
  * merges the partials. The library clears the counters on `stream` before
  * each launch that uses them, so the workspace needs no initialisation and
  * may be reused by calls of any shape; calls that use one workspace must not
- * overlap on the GPU.
+ * overlap on the GPU. Several host threads may use one workspace on one stream
+ * (here and in every call below that takes a workspace): the launches of a call
+ * are enqueued together, so that no other thread's come between them. What one
+ * call leaves for a later one (a launch plan) is not kept apart.
  *
  * Launch order: grids of at most 4096 CTAs start the sequences of at least
  * twice the batch's mean length (in 16-token tiles) first. For batches of 128
@@ -306,9 +309,8 @@ int pkv_paged_attention_partition(
  * the split-K, balanced and shared-prefix schedules) are cleared on `stream`
  * by every call (the last by its prefix plan kernel),
  * and everything else a call reads from the array it first writes itself.
- * Calls that overlap on the GPU (different streams, or different host
- * threads) race on it. No cudaMalloc, cudaFree or other allocating routine
- * is called.
+ * Calls that overlap on the GPU (different streams) race on it. No cudaMalloc,
+ * cudaFree or other allocating routine is called.
  */
 #define PKV_NOALLOC_SCRATCH_BYTES (32u << 20) /* 32 MiB */
 

@@ -283,8 +283,9 @@ def paged_attention_plan(context_lens, block_tables, num_q_heads, num_kv_heads, 
                          workspace=None):
     """The decode step's launch plan (pkv_paged_attention_plan) into ``workspace``
     (default: the binding's own workspace of the current stream, which
-    paged_attention_decode(planned=True) then reads). block_tables: int32
-    [S, max_blocks] (read by the shared-prefix schedule's plan)."""
+    paged_attention_decode(planned=True) then reads; threads that plan on one
+    stream pass a workspace each). block_tables: int32 [S, max_blocks] (read by
+    the shared-prefix schedule's plan)."""
     import torch
     _need_cuda(context_lens, block_tables)
     if context_lens.dtype != torch.int32 or context_lens.dim() != 1 or block_tables.dtype != torch.int32 \
@@ -485,7 +486,8 @@ _scratches = {}
 
 def _scratch(device, nbytes):
     """Workspace of one call, or None. Eager calls of a stream share one, which grows to the largest need (an
-    allocation a call costs 4 us of host time); a call under capture gets memory of its graph's own, so that
+    allocation a call costs 4 us of host time), whichever threads make them: the library enqueues a call's
+    launches together. A call under capture gets memory of its graph's own, so that
     graphs replayed at once, or beside eager calls, never share one."""
     if not nbytes:
         return None

@@ -46,6 +46,25 @@ namespace {
 
 using pkv::status_word;
 
+// Held while a call enqueues kernels (or clears) that pass state to one another
+// through its workspace: with a workspace per stream, the launches of two host
+// threads' calls on one stream must not come between one another, or the second
+// kernel of one call would read what the first of the other left. A lock per stream
+// (by its handle; two that share one only wait for each other), so that a launch that
+// waits on a full stream holds up that stream alone.
+class EnqueueLock {
+ public:
+  explicit EnqueueLock(cudaStream_t stream) : lock_(of(stream)) {}
+
+ private:
+  static std::mutex& of(cudaStream_t stream) {
+    static std::mutex mu[64];
+    const uint64_t h = uint64_t(reinterpret_cast<uintptr_t>(stream)) * 0x9E3779B97F4A7C15ull;
+    return mu[h >> 58];
+  }
+  std::lock_guard<std::mutex> lock_;
+};
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int round_pow2_group(int g) {
@@ -551,6 +570,7 @@ pkv_status_t decode_impl(void* out, const void* q, const void* k_pool, const voi
     b.slot_floats = sk.slot_floats;
     b.scale_log2 = scale * 1.4426950408889634f;
     // Arrival counters start at zero on every call; the slots need no initialisation.
+    const EnqueueLock lock(stream);
     cudaError_t err = cudaMemsetAsync(b.counters, 0, sk.counter_bytes, stream);
     if (err != cudaSuccess) return cuda_status(err, "clear arrival counters");
     err = dtype == PKV_F16 ? pkv::launch_decode_sk_f16(b, head_dim, gpad, kmap, vmap, stream)
@@ -597,6 +617,7 @@ pkv_status_t decode_impl(void* out, const void* q, const void* k_pool, const voi
   a.trace_records = g_trace_records;
   a.scale_log2 = scale * 1.4426950408889634f;
 
+  const EnqueueLock lock(stream);
   cudaError_t err = cudaSuccess;
   if (shared_prefix) {
     // The prefix plan (made here, or by pkv_paged_attention_plan for a planned
@@ -825,6 +846,7 @@ pkv_status_t decode_int8_impl(void* out, const void* q, const int8_t* k_cache, c
     st = code_tensor_map(&vmap, v_cache, rows, head_dim);
     if (st != PKV_OK) return st;
   }
+  const EnqueueLock lock(stream);
   cudaError_t err = cudaSuccess;
   int gpad = round_pow2_group(group);
   if (shared_prefix) {
@@ -1018,6 +1040,7 @@ pkv_status_t pkv_paged_attention_decode_int4(void* out, const void* q, const voi
   a.num_blocks = num_blocks;
   a.window = sliding_window > 0 ? sliding_window : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
+  const EnqueueLock lock(stream);
   return cuda_status(pkv::launch_decode_int4(a, dtype == PKV_BF16, head_dim, blocks, workspace, stream),
                      "paged_attention_decode_int4 launch");
 }
@@ -1100,6 +1123,7 @@ pkv_status_t pkv_paged_latent_decode(void* out, const void* q, const void* cache
   st = query_tensor_map(&q_map, q, num_seqs, num_heads, pkv::kLatentRow, dtype,
                         pkv::latent_query_box(num_seqs, num_heads, max_blocks_per_seq));
   if (st != PKV_OK) return st;
+  const EnqueueLock lock(stream);
   return cuda_status(pkv::launch_latent_decode(a, dtype == PKV_BF16, cache_map, q_map, stream),
                      "paged_latent_decode launch");
 }
@@ -1154,6 +1178,7 @@ pkv_status_t pkv_extend_block_tables(int32_t* block_tables, const int32_t* conte
   a.num_blocks = num_blocks;
   a.num_slots = num_slots;
   a.slots_aligned = aligned(slot_mapping, 16) ? 1 : 0;
+  const EnqueueLock lock(stream);
   return cuda_status(pkv::launch_extend_block_tables(a, stream), "extend_block_tables launch");
 }
 
@@ -1193,6 +1218,7 @@ pkv_status_t pkv_release_sequences(int32_t* block_tables, int32_t* context_lens,
   a.num_seqs = num_seqs;
   a.max_blocks = max_blocks_per_seq;
   a.num_blocks = num_blocks;
+  const EnqueueLock lock(stream);
   return cuda_status(pkv::launch_release_sequences(a, stream), "release_sequences launch");
 }
 

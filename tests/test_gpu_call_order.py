@@ -103,6 +103,72 @@ def _from_threads(jobs, rounds):
     return results
 
 
+def _decodes(seed, S, hq, hkv, heads, most, dtype="f16"):
+    """(list-schedule 4-bit decode, latent decode, 16-bit split decode) of one batch, as calls without arguments."""
+    rng = np.random.default_rng(seed)
+    lens_np = rng.integers(1, most, S).astype(np.int32)
+    nb = W.pool_size(lens_np, 1.2) + 1
+    tab, lens = _i32(W.scattered_tables(lens_np, nb, seed)[0]), _i32(lens_np)
+    D = 64
+    pool = torch.empty((nb, hkv, 18 * D), dtype=torch.uint8, device="cuda")
+    k, v = (W.normal_values((nb * 16, hkv, D), dtype, seed + i, "cuda") for i in (1, 2))
+    B.reshape_and_cache_int4(k, v, pool, torch.arange(nb * 16, device="cuda"))
+    rows = W.normal_values((nb, 16, 576), dtype, seed + 3, "cuda")
+    q, ql = W.normal_values((S, hq, D), dtype, seed + 4, "cuda"), W.normal_values((S, heads, 576), dtype, seed + 5, "cuda")
+    kp, vp = (W.normal_values((nb, hkv, 16, D), dtype, seed + i, "cuda") for i in (6, 7))
+    assert B.int4_workspace_size(S, hq, hkv, D, tab.shape[1]) > 0
+    return (lambda: B.paged_attention_decode_int4(torch.empty_like(q), q, pool, tab, lens, 0.1),
+            lambda: B.paged_latent_decode(torch.empty((S, heads, 512), dtype=ql.dtype, device="cuda"), ql, rows, tab,
+                                          lens, 0.07),
+            lambda: B.paged_attention_decode(torch.empty_like(q), q, kp, vp, tab, lens, 0.1, partition_size=128))
+
+
+def _tables(seed, S, n):
+    """An extend of S prompts by two kernels, the release of every other one and the state after both."""
+    rng = np.random.default_rng(seed)
+    new, gone = _i32(rng.integers(1, 2 * n, S)), _i32(rng.integers(0, 2, S))
+    width, total = (2 * n + 15) // 16, int(new.sum())
+    nb = S * width
+    order = _i32(rng.permutation(nb))
+    assert B.lib().pkv_extend_workspace_size(S, total) > 0
+
+    def run():
+        tab = torch.full((S, width), -1, dtype=torch.int32, device="cuda")
+        lens, stack = torch.zeros(S, dtype=torch.int32, device="cuda"), order.clone()
+        count = torch.full((1,), nb, dtype=torch.int32, device="cuda")
+        slots = torch.empty(total, dtype=torch.int64, device="cuda")
+        B.extend_block_tables(tab, lens, new, stack, count, slots)
+        full = tab.clone()
+        B.release_sequences(tab, lens, gone, stack, count)
+        return torch.cat([full.flatten(), tab.flatten(), lens, stack, count]), slots
+    return run
+
+
+def _same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b)) if isinstance(a, tuple) else torch.equal(a, b)
+
+
+@pytest.mark.parametrize("stream", ["default", "own"])
+def test_threads_that_share_a_stream(stream):
+    """Calls of several kernels that pass state through the stream's workspace, each from a thread of its own: the same
+    bits as alone."""
+    jobs = [*_decodes(1, 30, 24, 12, 16, 700), *_decodes(50, 41, 20, 20, 128, 1500), _tables(7, 900, 12),
+            _tables(8, 2000, 4)]
+    alone = [job() for job in jobs]
+    torch.cuda.synchronize()
+    st = torch.cuda.default_stream() if stream == "default" else torch.cuda.Stream()
+
+    def on_stream(job):
+        def run():
+            with torch.cuda.stream(st):
+                return job()
+        return run
+    for round_ in range(3):
+        for want, got in zip(alone, _from_threads([on_stream(j) for j in jobs], 40)):
+            assert all(_same(want, g) for g in got)
+    assert B.device_status(clear=True) == 0
+
+
 def test_a_thread_whose_first_call_is_a_decode():
     """The calls that encode tensor maps, from threads that have made no CUDA call before."""
     q, pool = W.normal_values((3, 8, 64), "f16", 1, "cuda"), W.normal_values((4, 2, 16, 64), "f16", 2, "cuda")

@@ -61,3 +61,18 @@ def test_kernels_that_wait_do_so_before_they_touch_memory(name):
         first = GLOBAL.search(body)
         assert first is None or first.start() > at, f"{kernel}: {body[first.start():first.start() + 60]!r} before the wait"
     assert found or name == "decode.cuh"          # (there the wait is a function of its own)
+
+
+@pytest.mark.parametrize("launch", ["launch_decode_sk_f16", "launch_decode_f16", "launch_decode_int8", "launch_decode_int4",
+                                    "launch_latent_decode", "launch_extend_block_tables", "launch_release_sequences"])
+def test_launches_that_share_a_workspace_are_enqueued_together(launch):
+    """Between the start of the function (or the block) that makes them and the launch the stream's lock is taken,
+    and before it nothing is enqueued."""
+    text = _source("api.cu")
+    for m in re.finditer(rf"pkv::{launch}\(", text):
+        body = text[text.rfind("\n}\n", 0, m.start()):m.start()]
+        at = body.rfind("const EnqueueLock lock(stream);")
+        enqueued = [body.find(w) for w in ("cudaMemsetAsync(", "launch_prefix_plan_ws(context_lens", "launch_seq_order(")]
+        assert at >= 0 and body[at:].count("EnqueueLock") == 1
+        first = min([e for e in enqueued if e >= 0], default=len(body))
+        assert body.find("const EnqueueLock lock(stream);") < first
