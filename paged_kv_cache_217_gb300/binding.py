@@ -492,6 +492,9 @@ def _scratch(device, nbytes):
     if not nbytes:
         return None
     import torch
+    if device.index != _torch_handles()[0]():
+        with torch.cuda.device(device):  # whether the stream is capturing is asked of the current device's
+            return _scratch(device, nbytes)
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, _stream_ptr(device))
