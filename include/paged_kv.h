@@ -560,6 +560,9 @@ pkv_status_t pkv_copy_blocks_int4(
 /*
  * Decode over the 4-bit cache: pkv_paged_attention_decode with every K and V
  * row read as z + c s (in fp32, not rounded to T). q and out are T = dtype.
+ * V of any finite size has its mean; besides a relative 2^-11 of the weights an
+ * element is off by at most 15 2^-31 a token of the largest scale that its group
+ * of 64 dims has in the sequence.
  * sliding_window as for pkv_paged_attention_decode_sliding (<= 0: none). One
  * schedule for all batches: the batch's tiles are cut into equal shares
  * whatever the lengths, so there is no partition size and no launch plan.

@@ -28,8 +28,8 @@
 //  * O^T += C_V^T P~: head dims on M, tokens on K, fp16. V words of tokens t
 //    and t + 4 (t + 8 and t + 12) are merged by halves and masked: 10
 //    instructions for 16 codes (nibble_sums).
-//    P~ = p s 2^e rounded to fp16 once, e a power of two per warp that keeps P~
-//    below 2^15; the score fragment becomes the weight operand through movmatrix.
+//    P~ = p s 2^e rounded to fp16 once, 2^e a power of two per warp and 64 dims that
+//    keeps P~ below 2^15; the score fragment becomes the weight operand through movmatrix.
 //    The offsets' part sum p z is kept in fp32 per (head, group). With fp16 values
 //    7.5 times what the rounding of P~ left joins it: the products' error is then
 //    2^-11 relative of p s (c - 7.5), which is as large as the values, not of p s
@@ -37,6 +37,8 @@
 //    tokens are 0.00025 (relative, rms) from a 64-bit computation, 0.00048 without;
 //    rounding them to fp16 alone gives 0.00021. Rounding to bf16 gives 0.0016, so
 //    there the step is left out (it costs 2 %, 59.0 us against 57.9).
+//    An element far below its 64 dims' largest scale s_max has an absolute error too: P~
+//    below 2^-14 is subnormal in fp16, p s off by up to 2^-31 s_max a token.
 //  * The running maximum is only a reference: it moves when a score exceeds it
 //    by more than 8 (weights up to 2^8; one vote a step), so most steps need no
 //    cross-lane maximum and no rescaling. Sums and the accumulator are fp32.
@@ -51,8 +53,9 @@
 // memory, of one that spans CTAs in the workspace (int4_merge_kernel). Small
 // batches instead give each item a CTA of its own, without that second kernel.
 // One CTA per item for all batches started up for 3.5 us an item: 74.4 us for 40
-// heads and 64 sequences against 57.7 (5.2 of the 6.8 TB/s that a copy reaches),
-// where 256 sequences of 150 tokens x 8 KV heads took 22.8 against 22.3: there
+// heads and 64 sequences against 57.7 (58.9 now, 5.1 of the 6.8 TB/s that a copy
+// reaches), where 256 sequences of 150 tokens x 8 KV heads took 22.8 against 22.3 (22.9
+// now; the powers of two per 64 dims and the lifted sums are the difference): there
 // the list (2 us), the block ids (1.4), the first copies (1) and the joins (4)
 // stand around 7 us of streaming.
 #pragma once
@@ -73,7 +76,7 @@ template <int D, int H, int NW, int STAGES>
 struct I4Cfg {
   static constexpr int TILE_BYTES = kv4_tile_bytes(D);
   static constexpr int STAGE_BYTES = 2 * TILE_BYTES;
-  static constexpr int PIECE_FLOATS = H * (D + 2);  // acc[H][D], m[H], l[H] of a piece
+  static constexpr int PIECE_FLOATS = H * (D + 2);  // means[H][D], m[H], l[H] of a piece
   static constexpr size_t RING_BYTES = size_t(NW) * STAGES * STAGE_BYTES;
   static constexpr size_t PIECE_BYTES = size_t(NW) * PIECE_FLOATS * sizeof(float);
   static constexpr size_t BAR_BYTES = size_t(NW) * STAGES * 8;
@@ -264,10 +267,28 @@ template <int D, int H>
 struct I4State {
   static constexpr int PL = I4Heads<H>::PER_LANE;
   float o[D / 16][4];            // O^T fragments in units of 2^-24 / vmul; odd ones hold even + 16 * odd nibbles
-  float z[D / kInt4Group][PL];   // this lane's part of sum p z
+  float z[D / kInt4Group][PL];   // this lane's part of sum p z, times 2^-40 in the groups of `lifted`
   float m[PL], l[PL];            // reference maximum (log2 domain), this lane's part of sum p
-  float vbound, vmul, vleft;     // P~ = p s vmul, for s below vbound; 7.5 / vmul
+  float vmul[D / kInt4Group];    // per group: P~ = p s vmul, vmul = 2^(7 - E) for s below 2^E
+  uint32_t lifted;               // bit g: see kInt4BigZ
 };
+
+// 2^e / x of a power of two x, all normal numbers.
+__device__ __forceinline__ float pow2_over(int e, float x) {
+  return __uint_as_float((uint32_t(254 + e) << 23) - __float_as_uint(x));
+}
+// a / b of powers of two; 0 where that is below 2^-126. (Exponents only: the quotient next to 2^-126 sends a
+// division through its slow path, 2.5 us of 59 over 64 sequences x 40 heads.)
+__device__ __forceinline__ float pow2_ratio(float a, float b) {
+  return __uint_as_float(uint32_t(max(127 + int(__float_as_uint(a) >> 23) - int(__float_as_uint(b) >> 23), 0)) << 23);
+}
+
+// bf16 values reach 2^128, where the unnormalised sums p v, p up to 2^8, would pass
+// fp32: from an offset of kInt4BigZ or a scale of kInt4BigS on, a group's sums are
+// kept 2^-40 times as large (2^8 2^27 tokens 2^128 2^-40 fits). What leaves a warp --
+// pieces of an item too -- is divided by the sum of the weights, so no larger than the
+// values.
+constexpr float kInt4BigZ = 0x1p80f, kInt4BigS = 0x1p76f;
 
 // The scores (log2 domain) of tile rows gr (x[0]) and gr + 8 (x[1]).
 template <typename T, int D, int H>
@@ -333,7 +354,8 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
   const int t = lane & 3, gr = lane >> 2;
   float x[4][PL];  // rows gr, gr + 8 of the first tile, then of the second
   float2 v[4][GROUPS];
-  float smax = 0.f;
+  constexpr bool WIDE = !std::is_same<T, __half>::value;  // values that sums of p v can pass fp32 with
+  float smax[GROUPS] = {}, zmax = 0.f;
 #pragma unroll
   for (int n = 0; n < 2; ++n) {
     const uint32_t tile = stage + n * TILE;
@@ -350,12 +372,17 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
 #pragma unroll
       for (int g = 0; g < GROUPS; ++g) {
         v[2 * n + r][g] = on ? pair_of<T>(vp[g]) : make_float2(0.f, 0.f);
-        smax = fmaxf(smax, v[2 * n + r][g].x);
+        smax[g] = fmaxf(smax[g], v[2 * n + r][g].x);
+        if (WIDE) zmax = fmaxf(zmax, fabsf(v[2 * n + r][g].y));
       }
     }
   }
   float mx[PL];
-  bool move = smax >= st.vbound;
+  bool move = WIDE && zmax >= kInt4BigZ && st.lifted != (1u << GROUPS) - 1u;
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    move |= smax[g] >= pow2_over(7, st.vmul[g]);
+  }
 #pragma unroll
   for (int e = 0; e < PL; ++e) {
     mx[e] = fmaxf(fmaxf(x[0][e], x[1][e]), fmaxf(x[2][e], x[3][e]));
@@ -366,35 +393,60 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
     for (int off = 4; off < 32; off <<= 1) {
 #pragma unroll
       for (int e = 0; e < PL; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], off));
-      smax = fmaxf(smax, __shfl_xor_sync(kFull, smax, off));
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) smax[g] = fmaxf(smax[g], __shfl_xor_sync(kFull, smax[g], off));
     }
-    float ratio = 1.f;
-    if (smax >= st.vbound) {  // smax in [2^(E-1), 2^E): vbound = 2^E, vmul = 2^(7 - E)
-      const int E = min(max(int((__float_as_uint(smax) >> 23) & 0xffu) - 126, -99), 126);
-      const float mul = __uint_as_float(uint32_t(127 + 7 - E) << 23);
-      ratio = mul / st.vmul;  // a power of two: exact
-      st.vmul = mul;
-      st.vleft = 7.5f * __uint_as_float(uint32_t(127 - 7 + E) << 23);
-      st.vbound = __uint_as_float(uint32_t(127 + E) << 23);
-    }
-    float r[PL];
+    float al[PL];
 #pragma unroll
     for (int e = 0; e < PL; ++e) {
       mx[e] = fmaxf(mx[e], st.m[e]);
       // a head without a score yet has nothing to rescale
-      const float al = st.m[e] == -INFINITY ? 0.f : fast_exp2(st.m[e] - mx[e]);
+      al[e] = st.m[e] == -INFINITY ? 0.f : fast_exp2(st.m[e] - mx[e]);
       st.m[e] = mx[e];
-      st.l[e] *= al;
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g) st.z[g][e] *= al;
-      r[e] = al * ratio;
+      st.l[e] *= al[e];
     }
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      st.o[i][0] *= r[0];
-      st.o[i][1] *= r[PL - 1];
-      st.o[i][2] *= r[0];
-      st.o[i][3] *= r[PL - 1];
+    for (int g = 0; g < GROUPS; ++g) {
+      float ratio = 1.f;
+      if (smax[g] >= pow2_over(7, st.vmul[g])) {  // smax in [2^(E-1), 2^E)
+        const int E = min(max(int((__float_as_uint(smax[g]) >> 23) & 0xffu) - 126, -119), 126);
+        const float mul = __uint_as_float(uint32_t(127 + 7 - E) << 23);
+        ratio = pow2_ratio(mul, st.vmul[g]);  // (0: what is there is nothing to the new scale)
+        st.vmul[g] = mul;
+      }
+      float zr = 1.f;
+      if (WIDE) {
+        float z = smax[g] >= kInt4BigS ? kInt4BigZ : 0.f;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) z = fmaxf(z, fabsf(v[r][g].y));
+        const bool big = __any_sync(kFull, z >= kInt4BigZ);
+        if (big && !(st.lifted >> g & 1u)) {
+          st.lifted |= 1u << g;
+          zr = 0x1p-40f;
+        }
+      }
+      const float r0 = al[0] * ratio, r1 = al[PL - 1] * ratio;
+#pragma unroll
+      for (int e = 0; e < PL; ++e) st.z[g][e] *= al[e] * zr;
+#pragma unroll
+      for (int i = 4 * g; i < 4 * g + 4; ++i) {
+        st.o[i][0] *= r0;
+        st.o[i][1] *= r1;
+        st.o[i][2] *= r0;
+        st.o[i][3] *= r1;
+      }
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r][g].x *= st.vmul[g];
+  if (WIDE && st.lifted != 0u) {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const float zmul = st.lifted >> g & 1u ? 0x1p-40f : 1.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r][g].y *= zmul;
     }
   }
   float p[4][PL];
@@ -410,10 +462,6 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
 #pragma unroll
       for (int r = 0; r < 4; ++r) st.z[g][e] = fmaf(p[r][e], v[r][g].y, st.z[g][e]);
   }
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-#pragma unroll
-    for (int e = 0; e < PL; ++e) p[r][e] *= st.vmul;  // p 2^(7 - E): s < 2^E keeps P~ below 2^15
 
   // O^T += C_V^T P~: K slot 2t + b + 8h of a tile is token 8h + 4b + t.
   const int turn = D == 64 ? 0 : D == 128 ? 4 * (t >> 1) : 2 * t;
@@ -436,8 +484,9 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
         if constexpr (std::is_same<T, __half>::value) {
           // what the rounding left goes with the offsets, as if every code were 7.5
           const float2 back = __half22float2(h);
-          st.z[g][0] = fmaf(x0 - back.x, st.vleft, st.z[g][0]);
-          if (PL == 2) st.z[g][PL - 1] = fmaf(x1 - back.y, st.vleft, st.z[g][PL - 1]);
+          const float left = 7.5f * pow2_over(0, st.vmul[g]);
+          st.z[g][0] = fmaf(x0 - back.x, left, st.z[g][0]);
+          if (PL == 2) st.z[g][PL - 1] = fmaf(x1 - back.y, left, st.z[g][PL - 1]);
         }
         pb[r] = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&h));
       }
@@ -455,7 +504,8 @@ __device__ __forceinline__ void i4_step(uint32_t stage, int lo, int rows, const 
   }
 }
 
-// Sums over a quad's rows what the warp keeps by lane.
+// Sums over a quad's rows what the warp keeps by lane; lifted groups' o takes 2^40 of
+// its unit.
 template <int D, int H>
 __device__ __forceinline__ void i4_reduce(I4State<D, H>& st) {
 #pragma unroll
@@ -467,24 +517,37 @@ __device__ __forceinline__ void i4_reduce(I4State<D, H>& st) {
       for (int g = 0; g < D / kInt4Group; ++g) st.z[g][c] += __shfl_xor_sync(kFull, st.z[g][c], off);
     }
   }
+  if (st.lifted) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st.o[i][e] *= st.lifted >> (i / 4) & 1u ? 0x1p40f : 1.f;
+  }
 }
 
-// The reduced state's values of column c: calls f(dim, four values of dims dim ..
-// dim + 3). Row gr of fragment 4 g + 2 h is dim 64 g + 8 gr + 4 h, of the next
-// one the dim after it, row gr + 8 two dims on.
+// The reduced state's values of column c times inv, which is at most 1 (a weight next
+// to the reference is 1 or more): calls f(dim, four values of dims dim .. dim + 3). Row
+// gr of fragment 4 g + 2 h is dim 64 g + 8 gr + 4 h, of the next one the dim after it,
+// row gr + 8 two dims on. A unit of o is 2^24 / vmul, which alone passes fp32 for scales
+// from 2^110 on; those are lifted (kInt4BigS), and i4_reduce has taken 2^40 of it.
 template <int D, int H, typename F>
-__device__ __forceinline__ void i4_values(const I4State<D, H>& st, int c, int gr, F f) {
-  const float even = 0x1p24f / st.vmul, odd = 0x1p20f / st.vmul;
+__device__ __forceinline__ void i4_values(const I4State<D, H>& st, int c, int gr, float inv, F f) {
 #pragma unroll
   for (int i = 0; i < D / 16; i += 2) {
-    const float z = st.z[i / 4][c];
+    const float k = inv * (st.lifted >> (i / 4) & 1u ? 0x1p40f : 1.f);
+    const float z = st.z[i / 4][c] * k, even = pow2_ratio(st.lifted >> (i / 4) & 1u ? 0x1p-16f : 0x1p24f, st.vmul[i / 4]) * inv,
+                odd = even * 0.0625f;
     f(64 * (i / 4) + 8 * gr + 4 * ((i / 2) & 1),
       make_float4(fmaf(st.o[i][c], even, z), fmaf(st.o[i + 1][c] - st.o[i][c], odd, z), fmaf(st.o[i][2 + c], even, z),
                   fmaf(st.o[i + 1][2 + c] - st.o[i][2 + c], odd, z)));
   }
 }
 
-// A piece of an item in shared memory: acc[H][D], m[H], l[H].
+// Pieces of an item hold weighted means and join with weights w_i l_i / sum w l, each
+// at most 1. A piece without a weight (all scores -inf) has the mean 0.
+__device__ __forceinline__ float i4_inverse(float l) { return l > 0.f ? 1.f / l : 0.f; }
+
+// A piece of an item in shared memory: means[H][D], m[H], l[H].
 template <int D, int H>
 __device__ __forceinline__ void i4_publish(float* piece, I4State<D, H>& st, int lane) {
   using HL = I4Heads<H>;
@@ -493,7 +556,8 @@ __device__ __forceinline__ void i4_publish(float* piece, I4State<D, H>& st, int 
 #pragma unroll
   for (int c = 0; c < HL::PER_LANE; ++c) {
     const int head = HL::head(t, c);
-    i4_values<D, H>(st, c, gr, [&](int dim, const float4& v) { *reinterpret_cast<float4*>(piece + head * D + dim) = v; });
+    i4_values<D, H>(st, c, gr, i4_inverse(st.l[c]),
+                    [&](int dim, const float4& v) { *reinterpret_cast<float4*>(piece + head * D + dim) = v; });
     if (gr == 0) {
       piece[H * D + head] = st.m[c];
       piece[H * D + H + head] = st.l[c];
@@ -511,9 +575,8 @@ __device__ __forceinline__ void i4_write(T* out, int group, I4State<D, H>& st, i
   for (int c = 0; c < HL::PER_LANE; ++c) {
     const int head = HL::head(t, c);
     if (head >= group) continue;
-    const float inv = 1.f / st.l[c];
-    i4_values<D, H>(st, c, gr, [&](int dim, const float4& v) {
-      T x[4] = {T(v.x * inv), T(v.y * inv), T(v.z * inv), T(v.w * inv)};
+    i4_values<D, H>(st, c, gr, 1.f / st.l[c], [&](int dim, const float4& v) {
+      T x[4] = {T(v.x), T(v.y), T(v.z), T(v.w)};
       *reinterpret_cast<uint2*>(out + size_t(head) * D + dim) = *reinterpret_cast<const uint2*>(x);
     });
   }
@@ -530,9 +593,9 @@ __device__ __forceinline__ void i4_clear(I4State<D, H>& st) {
 #pragma unroll
     for (int i = 0; i < D / kInt4Group; ++i) st.z[i][e] = 0.f;
   }
-  st.vbound = 0x1p-98f;
-  st.vmul = 0x1p105f;
-  st.vleft = 7.5f * 0x1p-105f;
+#pragma unroll
+  for (int g = 0; g < D / kInt4Group; ++g) st.vmul[g] = 0x1p126f;
+  st.lifted = 0u;
 }
 
 // ---- work ---------------------------------------------------------------------
@@ -848,16 +911,20 @@ __global__ void __launch_bounds__(NW * 32, i4_ctas_per_sm<D>()) paged_decode_int
       const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
       for (int w = 0; w <= NW; ++w) {
-        const float wt = fast_exp2(m[w] - ref);
-        den = fmaf(wt, l[w], den);
+        l[w] *= fast_exp2(m[w] - ref);
+        den += l[w];
+      }
+      const float inv = whole ? 1.f / den : i4_inverse(den);
+#pragma unroll
+      for (int w = 0; w <= NW; ++w) {
+        const float wt = l[w] * inv;
         num.x = fmaf(wt, x[w].x, num.x);
         num.y = fmaf(wt, x[w].y, num.y);
         num.z = fmaf(wt, x[w].z, num.z);
         num.w = fmaf(wt, x[w].w, num.w);
       }
       if (whole) {
-        const float inv = 1.f / den;
-        T y[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
+        T y[4] = {T(num.x), T(num.y), T(num.z), T(num.w)};
         *reinterpret_cast<uint2*>(out + size_t(h) * D + d) = *reinterpret_cast<const uint2*>(y);
       } else {
         *reinterpret_cast<float4*>(a.part_o + (row + h) * D + d) = num;
@@ -885,10 +952,9 @@ __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
   if (desc.x < 0) return;
   const int n = desc.y - c0 + 1;
   auto slot = [&](int i) { return (size_t(2) * (c0 + i) + (i == 0 ? 1 : 0)) * a.group + h; };
-  auto write = [&](const float4& num, float den) {
+  auto write = [&](const float4& num) {
     const int s = desc.x / a.num_kv_heads, g = desc.x - s * a.num_kv_heads;
-    const float inv = 1.f / den;
-    T x[4] = {T(num.x * inv), T(num.y * inv), T(num.z * inv), T(num.w * inv)};
+    T x[4] = {T(num.x), T(num.y), T(num.z), T(num.w)};
     *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + g * a.group + h) * D + d) =
         *reinterpret_cast<const uint2*>(x);
   };
@@ -906,14 +972,19 @@ __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
     const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
     for (int i = 0; i < kInt4FewPieces; ++i) {
-      const float w = fast_exp2(ml[i].x - ref);
-      den = fmaf(w, ml[i].y, den);
+      ml[i].y *= fast_exp2(ml[i].x - ref);
+      den += ml[i].y;
+    }
+    const float inv = 1.f / den;
+#pragma unroll
+    for (int i = 0; i < kInt4FewPieces; ++i) {
+      const float w = ml[i].y * inv;
       num.x = fmaf(w, o[i].x, num.x);
       num.y = fmaf(w, o[i].y, num.y);
       num.z = fmaf(w, o[i].z, num.z);
       num.w = fmaf(w, o[i].w, num.w);
     }
-    write(num, den);
+    write(num);
     return;
   }
   constexpr int AHEAD = 8;  // pieces read while the weights are made
@@ -939,18 +1010,22 @@ __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
   const float ref = M == -INFINITY ? 0.f : M;
   float den = 0.f;
   for (int i = tid; i < n; i += 256) {
-    const float w = fast_exp2(weight[i] - ref);
+    const float w = fast_exp2(weight[i] - ref) * __ldcg(&a.part_ml[slot(i)].y);
     weight[i] = w;
-    den = fmaf(w, __ldcg(&a.part_ml[slot(i)].y), den);
+    den += w;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(kFull, den, o);
   __syncthreads();
   if ((tid & 31) == 0) red[tid >> 5] = den;
   __syncthreads();
+  den = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) den += red[i];
+  const float inv = 1.f / den;
   float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
   auto add = [&](int i, const float4& o) {
-    const float w = weight[i];
+    const float w = weight[i] * inv;
     num.x = fmaf(w, o.x, num.x);
     num.y = fmaf(w, o.y, num.y);
     num.z = fmaf(w, o.z, num.z);
@@ -965,9 +1040,6 @@ __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
   other[group][tid % LANES] = num;
   __syncthreads();
   if (group) return;
-  den = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) den += red[i];
 #pragma unroll
   for (int i = 1; i < GROUPS; ++i) {
     const float4 x = other[i][tid];
@@ -976,7 +1048,7 @@ __global__ void __launch_bounds__(256) int4_merge_kernel(const Int4Args a) {
     num.z += x.z;
     num.w += x.w;
   }
-  write(num, den);
+  write(num);
 }
 
 }  // namespace pkv
