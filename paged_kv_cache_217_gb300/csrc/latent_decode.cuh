@@ -64,6 +64,10 @@ constexpr int kLatentTile = 64;       // tokens per tile
 constexpr int kLatentSoftmax = 256;   // threads of the softmax warps
 constexpr int kLatentThreads = kLatentSoftmax + 64;
 constexpr float kLatentLazy = 8.f;
+// fp16 weights are 2^7 times as large, 2^(7 + 8) at most: one 2^-21 of the largest still
+// has all its bits (2^-14 without), and what fp16 loses of smaller ones is at most 2^-32
+// of the largest. bf16 reaches far enough as it is.
+constexpr float kLatentHeadroom = 7.f;
 // Tiles between a copy and the prefetch of a later one into L2. 1: 46.9 us for 96
 // sequences x 1500 tokens x 16 heads, 63.3 for 32 x 4000 x 128 (2: 47.9, 63.3; 4:
 // 53.1, 64.4; none: 47.7, 67.7).
@@ -599,6 +603,7 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
     // 4) .. + 15 of S^T, dims 32 (w % 4) .. + 31 of each product of O^T), for
     // heads HALF (w / 4) .. . This thread keeps heads 8 i + 2 t, + 1 of its half.
     constexpr int HALF = N / 2, G8 = HALF / 8;
+    constexpr float kHeadroom = std::is_same<T, __half>::value ? kLatentHeadroom : 0.f;
     const int t = lane & 3, gr = lane >> 2, quarter = warp & 3, half = warp >> 2, hs = half * HALF;
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
     // (After a wait gave up, `stop` lets every later wait return at once: these
@@ -661,7 +666,8 @@ latent_decode_kernel(const LatentArgs a, const __grid_constant__ CUtensorMap cac
         uint32_t p[G8][2];  // weights of rows gr and gr + 8, two heads each
 #pragma unroll
         for (int i = 0; i < G8; ++i) {
-          const float ref0 = m[i][0] == -INFINITY ? 0.f : m[i][0], ref1 = m[i][1] == -INFINITY ? 0.f : m[i][1];
+          const float ref0 = (m[i][0] == -INFINITY ? 0.f : m[i][0]) - kHeadroom;
+          const float ref1 = (m[i][1] == -INFINITY ? 0.f : m[i][1]) - kHeadroom;
           p[i][0] = pack2<T>(fast_exp2(x[i][0] - ref0), fast_exp2(x[i][1] - ref1));
           p[i][1] = pack2<T>(fast_exp2(x[i][2] - ref0), fast_exp2(x[i][3] - ref1));
         }
