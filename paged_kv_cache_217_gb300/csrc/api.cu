@@ -1138,9 +1138,10 @@ pkv_status_t pkv_extend_block_tables(int32_t* block_tables, const int32_t* conte
                                      int32_t* new_free_count, int64_t* slot_mapping, int num_slots, int64_t* cow_pairs,
                                      int32_t* info, void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
   if (num_seqs < 0 || num_slots < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs and num_slots must be >= 0");
-  if (num_seqs == 0 && num_slots == 0) return pkv::ok();
+  // (without sequences and slots the free count and info may still have to be written)
+  if (num_seqs == 0 && num_slots == 0 && new_free_count == free_count && !info) return pkv::ok();
   if (num_seqs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 65535", num_seqs);
-  if (max_blocks_per_seq <= 0 || num_blocks <= 0)
+  if ((max_blocks_per_seq <= 0 && num_seqs > 0) || num_blocks <= 0)
     return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq and num_blocks must be > 0");
   if (int64_t(max_blocks_per_seq) * PKV_BLOCK_SIZE > INT32_MAX / 2)
     return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq too large");
