@@ -516,7 +516,8 @@ pkv_status_t pkv_copy_blocks_int8(
  *     c = clamp(rint((0.5 x - 0.5 z) / (0.5 s)), 0, 15)   (0 where s = 0),
  * in IEEE fp32 (rint: ties to even), so that x ~= z + c s with an error of at
  * most s / 2 for x <= z + 15 s; rounding s down moves the largest x past that
- * by at most 15 s 2^-9 for bf16 (2^-12 for fp16). A group that holds an
+ * by at most 15 s 2^-8 for bf16 (2^-11 for fp16), where s is subnormal by at
+ * most 15 2^-134 (15 2^-25). A group that holds an
  * infinity or NaN reads as NaN. 4.5 bits an element: 18 * head_dim bytes hold
  * the K and V of 16 tokens of one KV head, against 64 * head_dim in 16 bits.
  *

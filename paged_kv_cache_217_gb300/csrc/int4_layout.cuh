@@ -7,10 +7,12 @@
 //     c = clamp(rint((0.5 x - 0.5 z) / (0.5 s)), 0, 15)   (c = 0 where s = 0),
 // all in IEEE fp32; the halves keep the widest bf16 ranges inside fp32. z is
 // one of the inputs, so it is exact, and c is taken against the rounded s, so
-// the rounding of s to T (off by at most half a step, a relative 2^-9 for bf16
-// and 2^-12 for fp16) widens the error of an element only beyond code 15:
-// |x - (z + c s)| <= s / 2 + 15 s * 2^-9. A group that holds an infinity or
-// NaN stores NaN in both, so everything read from it is NaN.
+// the rounding of s to T widens the error of an element only beyond code 15. It is
+// off by at most half a step: a relative 2^-8 for bf16 and 2^-11 for fp16, 2^-134 and
+// 2^-25 where s is subnormal. So |x - (z + c s)| <= s / 2 for x <= z + 15 s, and the
+// largest x passes z + 15 s by at most 15 s 2^-8 (15 s 2^-11; 15 2^-134, 15 2^-25). A
+// group that holds an infinity or NaN stores NaN in both, so everything read from it
+// is NaN.
 //
 // A tile is the 16 slots of one (block, KV head): 18 * D contiguous bytes,
 //     K codes 8 D | V codes 8 D | K pairs D | V pairs D,
