@@ -112,9 +112,10 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
   return v;
 }
 
-// N 32-bit words from shared memory in one load (N = 1, 2, 4) or two (8).
+// N 32-bit words from shared memory in one load.
 template <int N>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "what one load brings");
   if constexpr (N == 1) {
     w[0] = lds_u32(addr);
   } else if constexpr (N == 2) {
