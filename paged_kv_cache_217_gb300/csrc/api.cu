@@ -21,10 +21,8 @@ namespace {
 // Device status word: PKV_DEV_* flags raised by the kernels' index checks.
 __device__ unsigned int g_pkv_status = 0u;
 
-}  // namespace
-
 // Device address of g_pkv_status, looked up once per device with that device current.
-pkv_status_t pkv::status_word(unsigned int** out) {
+pkv_status_t status_word(unsigned int** out) {
   static std::mutex mu;
   static unsigned int* addr[pkv::kMaxDevices] = {};
   int dev = 0;
@@ -41,10 +39,6 @@ pkv_status_t pkv::status_word(unsigned int** out) {
   *out = addr[dev];
   return PKV_OK;
 }
-
-namespace {
-
-using pkv::status_word;
 
 // Held while a call enqueues kernels (or clears) that pass state to one another
 // through its workspace: with a workspace per stream, the launches of two host

@@ -15,7 +15,4 @@ pkv_status_t fail(pkv_status_t st, const char* fmt, ...)
 // Clears the message and returns PKV_OK.
 pkv_status_t ok();
 
-// Address of the current device's status word (PKV_DEV_* flags), looked up once per device.
-pkv_status_t status_word(unsigned int** out);
-
 }  // namespace pkv
