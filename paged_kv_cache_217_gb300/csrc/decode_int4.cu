@@ -8,12 +8,17 @@ namespace {
 constexpr int kInt4Stages = 2;
 // Batches of at most kItemCtas items (sequences x KV heads, one wave of CTAs) whose
 // tables hold at most kItemPairs pairs of tiles give each item a CTA; the others
-// share the list, which starts later and needs a merge but balances. Measured for
-// tables of 2048 tokens, item against list, in us: 8 items of 411 tokens 5.8, 8.3;
-// 64 to 240 items of about 300 tokens 6.6 to 8.0, 8.9 to 10.3; 128 items of 1000
-// tokens 10.5, 11.2; where the lengths vary (1000 x e^(0.3 N(0, 1))) 10.1 to 16.4,
-// 10.6 to 16.9 (128 items 14.0, 12.3). The lengths are on the device, so the
-// tables' width decides. For tables of 8192 tokens (128 items of 5000) 49, 25.
+// share the list, which starts later and needs a merge but balances. The lengths are
+// on the device, so the tables' width decides. Measured for tables of 2048 tokens, item
+// against list, in us (groups of 4 query heads, head_dim 128, bf16):
+//   about 300 tokens, 8 to 304 items: 5.2 to 8.1, 7.2 to 11.1
+//   1000 tokens each: 8 items 8.6, 8.4; 128 10.6, 11.6; 240 11.8, 15.1; 280 12.4, 16.9
+//   1000 x e^(0.3 N(0, 1)) tokens, 8 KV heads: 64 items 10.6, 11.2; 96 14.6, 12.0; 128
+//   14.2, 12.8; 160 14.7, 13.1; 192 13.6, 13.0; 240 16.7, 14.8; 304 17.0, 18.0; 40 KV
+//   heads: 160 10.4, 11.5; 280 14.7, 17.3
+// So the rule gives away 5 to 20 % where few sequences of long and mixed lengths make 96
+// to 240 items (one CTA ends last), and takes up to 35 % elsewhere; a better one needs
+// the lengths. For tables of 8192 tokens (128 items of 5000) 49, 25.
 constexpr int64_t kItemCtas = 304;
 constexpr int kItemPairs = 64;
 // Pairs a warp should have at least, where there are few: one item of 5000 tokens

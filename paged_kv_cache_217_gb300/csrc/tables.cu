@@ -144,6 +144,8 @@ __device__ __forceinline__ void scan_batch(const ExtendArgs& a, const Scan& w) {
         if (raw < 0 || n < 0 || raw + n > max_len) n = 0;
       }
       if (any_sharing && last >= 0) {
+        // (every earlier sequence of the batch: 256 forked ones 7.2 us against 3.8 for a
+        // call without sharing, 1024 19, 4096 187, 65532 44 ms)
         int rank = 0;
         for (int e = 0; e < s; ++e) rank += w.last[e] == last ? 1 : 0;
         cow = a.refcounts[last] - rank > 1 ? 1 : 0;
