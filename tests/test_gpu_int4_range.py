@@ -128,3 +128,29 @@ def test_growing_scores_over_the_largest_values():
     c.q[:, 1] = -1
     c.scale = 0.02
     _check(c, c.run())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_rows_of_any_size_are_written_as_defined(dtype, D):
+    """Every byte of the tiles, for rows of every power of two of the type, groups of ties and of one value."""
+    nb, hkv = 80, 2
+    rng = np.random.default_rng(D)
+    low, high = {"f16": (-24, 15), "bf16": (-133, 127)}[dtype]
+    size = np.exp2(rng.uniform(low, high, size=(nb * 16, hkv, D // 64, 1)))
+    x = rng.uniform(-1, 1, size=(nb * 16, hkv, D // 64, 64)) * size
+    x[::7] = np.rint(x[::7] / size[::7] * 15) * size[::7] / 8          # steps and halves of steps
+    x[::11] = x[::11, :, :, :1]
+    x[::13] += 40 * size[::13]                                         # far from zero
+    limit = 65504.0 if dtype == "f16" else 3.38e38
+    x = O4.round_to(np.clip(x, -limit, limit), dtype).reshape(nb * 16, hkv, D) + 0.0
+    k, v = x, x[::-1]
+    cache = torch.zeros((nb, hkv, 18 * D), dtype=torch.uint8, device="cuda")
+    slots = rng.permutation(nb * 16)
+    B.reshape_and_cache_int4(*(torch.from_numpy(np.ascontiguousarray(a[slots]).astype(np.float32)).cuda().to(
+        H.torch_dtype(dtype)) for a in (k, v)), cache, torch.from_numpy(slots).cuda())
+    dense = []
+    for a in (k, v):
+        dense += [t.reshape(nb, 16, hkv, *t.shape[2:]).swapaxes(1, 2) for t in O4.quantize(a, dtype)]
+    assert np.array_equal(cache.cpu().numpy(), O4.tile_bytes(*dense, dtype))
+    assert B.device_status(clear=True) == 0
