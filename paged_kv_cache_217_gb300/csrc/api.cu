@@ -700,6 +700,7 @@ pkv_status_t pkv_paged_attention_plan(const int32_t* context_lens, const int32_t
   pkv_status_t st = plan_decode(max_blocks_per_seq, p, &plan);
   if (st != PKV_OK) return st;
   if (p == kBalanced) return pkv::ok();  // the balanced schedule takes no plan
+  const EnqueueLock lock(stream);  // (a plan must not come between another call's own plan and its decode)
   if (p == kSharedPrefix) {
     if (!prefix_fits(num_seqs, num_q_heads, num_kv_heads, max_blocks_per_seq))
       return pkv::fail(PKV_ERR_UNSUPPORTED, "these sizes take no shared-prefix schedule");

@@ -144,6 +144,21 @@ def _tables(seed, S, n):
     return run
 
 
+def _plan_and_decode(seed, S):
+    """A plan into the stream's workspace, which nothing uses, then a 16-bit decode that makes its own there."""
+    rng = np.random.default_rng(seed)
+    lens_np = rng.integers(1, 200, S).astype(np.int32)
+    nb = W.pool_size(lens_np, 1.2) + 1
+    tab, lens = _i32(W.scattered_tables(lens_np, nb, seed)[0]), _i32(lens_np)
+    q = W.normal_values((S, 8, 64), "bf16", seed, "cuda")
+    kp, vp = (W.normal_values((nb, 2, 16, 64), "bf16", seed + i, "cuda") for i in (1, 2))
+
+    def run():
+        B.paged_attention_plan(lens, tab, 8, 2, 64)
+        return B.paged_attention_decode(torch.empty_like(q), q, kp, vp, tab, lens, 0.125)
+    return run
+
+
 def _same(a, b):
     return all(torch.equal(x, y) for x, y in zip(a, b)) if isinstance(a, tuple) else torch.equal(a, b)
 
@@ -153,7 +168,7 @@ def test_threads_that_share_a_stream(stream):
     """Calls of several kernels that pass state through the stream's workspace, each from a thread of its own: the same
     bits as alone."""
     jobs = [*_decodes(1, 30, 24, 12, 16, 700), *_decodes(50, 41, 20, 20, 128, 1500), _tables(7, 900, 12),
-            _tables(8, 2000, 4)]
+            _tables(8, 2000, 4), _plan_and_decode(9, 200), _plan_and_decode(10, 150)]
     alone = [job() for job in jobs]
     torch.cuda.synchronize()
     st = torch.cuda.default_stream() if stream == "default" else torch.cuda.Stream()

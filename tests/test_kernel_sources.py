@@ -76,3 +76,14 @@ def test_launches_that_share_a_workspace_are_enqueued_together(launch):
         assert at >= 0 and body[at:].count("EnqueueLock") == 1
         first = min([e for e in enqueued if e >= 0], default=len(body))
         assert body.find("const EnqueueLock lock(stream);") < first
+
+
+@pytest.mark.parametrize("launch", ["launch_prefix_plan_ws(context_lens", "pkv::launch_seq_order("])
+def test_plans_are_enqueued_under_the_lock(launch):
+    """Every plan that is written into a workspace: a decode's own, and pkv_paged_attention_plan's."""
+    text = _source("api.cu")
+    at = [m.start() for m in re.finditer(re.escape(launch), text)]
+    assert len(at) == 3
+    for i in at:
+        body = text[text.rfind("\n}\n", 0, i):i]
+        assert body.count("EnqueueLock lock(") == 1 or (body.count("EnqueueLock lock(") == 2 and "if (balanced) {" in body)
