@@ -94,6 +94,8 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1 } pkv_dtype_t;
 #define PKV_DEV_WAIT_TIMEOUT    0x10u /* a bounded wait on a copy gave up */
 #define PKV_DEV_BAD_PLAN        0x20u /* a planned decode found no plan of its batch size */
 #define PKV_DEV_OUT_OF_BLOCKS   0x40u /* extend_block_tables: the free stack holds too few blocks */
+#define PKV_DEV_BAD_POSITION    0x80u /* rotary_and_cache: a position >= max_positions */
+#define PKV_DEV_BAD_START       0x100u /* query_starts or group_starts decrease or leave the batch */
 
 typedef struct CUstream_st* pkv_stream_t; /* same type as cudaStream_t */
 
@@ -424,6 +426,116 @@ pkv_status_t pkv_copy_blocks(
  * used as a src. PKV_OK or PKV_ERR_INVALID_ARG. */
 pkv_status_t pkv_check_copy_pairs(const int64_t* src_dst_pairs_host, int num_pairs,
                                   int num_blocks);
+
+/*
+ * pkv_reshape_and_cache with the position rotation applied on the way: the
+ * step's queries and keys are rotated by their positions, keys and values go
+ * to their slots (the pages name no position encoding; this is the usual
+ * rotary one). For token t at p = positions[t], every head of q and k and
+ * every pair i < R / 2 of its elements (a, b), R = rotary_dim:
+ *     a' = a c - b s,  b' = b c + a s,
+ *     c = cos_sin[p][i],  s = cos_sin[p][R / 2 + i]
+ * with (a, b) = (x[i], x[i + R / 2]), or (x[2 i], x[2 i + 1]) when interleaved;
+ * elements from R on, and v, are copied. Products and sums are single fp32
+ * operations, the result is rounded once to T. The table is the caller's
+ * (whatever scaling of frequencies it uses).
+ *   q, q_out : T[num_tokens][num_q_heads][head_dim], tokens q_stride and
+ *              q_out_stride elements apart; q_out may be q itself (same
+ *              stride). num_q_heads 0: keys and values only, q and q_out
+ *              ignored.
+ *   k, v     : T[num_tokens][num_kv_heads][head_dim], k_stride and v_stride
+ *              apart (slices of one projection's output need no copy)
+ *   positions: int32[num_tokens]; a position < 0 marks padding: the token is
+ *              left out, its row of q_out included. Positions >= max_positions
+ *              are flagged (PKV_DEV_BAD_POSITION) and taken as the last.
+ *   cos_sin  : fp32[max_positions][rotary_dim], cosines then sines
+ * Slots as for pkv_reshape_and_cache (a slot < 0 keeps the token's K and V out
+ * of the cache; its queries are rotated all the same). head_dim 64, 128 or 256,
+ * rotary_dim a multiple of 16 up to head_dim; strides multiples of 8. q_out
+ * overlaps no other argument.
+ */
+pkv_status_t pkv_rotary_and_cache(
+    void* q_out, const void* q, const void* k, const void* v, int64_t q_out_stride,
+    int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* positions,
+    const float* cos_sin, int max_positions, int rotary_dim, int interleaved,
+    void* k_pool, void* v_pool, const int64_t* slot_mapping, int num_tokens,
+    int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+    pkv_dtype_t dtype, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Prompt and cross attention, decode behind a shared prefix                 */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Attention of several query tokens per sequence over the paged cache: whole
+ * prompts, chunks of long ones, drafted tokens to be verified (causal), and
+ * cross attention to states of another length (not causal). The queries lie
+ * one sequence behind the other: sequence s has the n_s = query_starts[s + 1]
+ * - query_starts[s] tokens from query_starts[s] on, and with causal they are
+ * the last n_s of its L = context_lens[s] tokens, whose K and V are in the
+ * cache already (pkv_reshape_and_cache or pkv_rotary_and_cache first). Query
+ * token i of sequence s, head h (KV head g):
+ *     out = softmax_p( scale * <q, K_s[p]> ) . V_s[p]  over
+ *     causal:  max(0, P - W + 1) <= p <= P,  P = L - n_s + i,
+ *              W = sliding_window (<= 0: no window)
+ *     else:    0 <= p < L  (sliding_window must be <= 0)
+ * A query that sees nothing (L = 0, or n_s > L and P < 0) gets zeros. Softmax
+ * statistics and sums in fp32, weights rounded to T for the tensor cores.
+ * Cached rows that no query of a sequence sees may hold anything; V of a row
+ * that some of a sequence's queries see must be finite for the others too.
+ *   q, out      : T[num_tokens][num_q_heads][head_dim]
+ *   query_starts: int32[num_seqs + 1], not decreasing, within [0, num_tokens]
+ *                 (else clamped and flagged, PKV_DEV_BAD_START); rows of out
+ *                 before the first and from the last on are left as they are
+ * Pools, tables, lengths, types and head_dims as for
+ * pkv_paged_attention_decode; up to 128 query heads per KV head. Table entries
+ * of blocks that no query of a sequence sees are not read. Workspace
+ * (pkv_prompt_workspace_size bytes for the same arguments, 16-byte aligned,
+ * NULL when that is 0): no initialisation; calls that use one workspace must
+ * not overlap on the GPU. The same inputs give the same bits.
+ */
+pkv_status_t pkv_paged_prompt_attention(
+    void* out, const void* q, const void* k_pool, const void* v_pool,
+    const int32_t* block_tables, const int32_t* context_lens,
+    const int32_t* query_starts, int num_tokens, int num_seqs, int num_q_heads,
+    int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, float scale,
+    pkv_dtype_t dtype, int causal, int sliding_window, void* workspace,
+    size_t workspace_bytes, pkv_stream_t stream);
+
+size_t pkv_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads,
+                                 int num_kv_heads, int head_dim,
+                                 int max_blocks_per_seq);
+
+/*
+ * Decode of a batch whose groups share a long prefix (a system prompt, a
+ * document, the samples of one prompt; [S] "並列サンプリングやビームサーチでの
+ * 共有", pkv_bm_add_seq_with_prefix), each prefix read and multiplied once for
+ * all queries of its group. Group i holds the sequences group_starts[i] ..
+ * group_starts[i + 1] - 1 (sequences outside every group are ordinary ones),
+ * and its first prefix_blocks[i] blocks are those of its first sequence's
+ * table, whatever the other members' tables hold there:
+ *     out[s][h] = softmax_p( scale * <q[s][h], K_s[p]> ) . V_s[p],  p < L,
+ * exactly as pkv_paged_attention_decode over such tables. A member shorter
+ * than the prefix sees its own first L tokens of it. There is no limit on a
+ * group's size or on the prefix's length (the shared-prefix schedule, -5, of
+ * pkv_paged_attention_decode finds the sharing by itself, for up to 8 query
+ * rows a group).
+ *   group_starts : int32[num_groups + 1], not decreasing, within [0, num_seqs]
+ *   prefix_blocks: int32[num_groups], clamped to [0, max_blocks_per_seq]
+ * Everything else as for pkv_paged_prompt_attention with one query token per
+ * sequence; workspace pkv_prefix_workspace_size.
+ */
+pkv_status_t pkv_paged_prefix_decode(
+    void* out, const void* q, const void* k_pool, const void* v_pool,
+    const int32_t* block_tables, const int32_t* context_lens,
+    const int32_t* group_starts, const int32_t* prefix_blocks, int num_groups,
+    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+    int max_blocks_per_seq, int num_blocks, float scale, pkv_dtype_t dtype,
+    void* workspace, size_t workspace_bytes, pkv_stream_t stream);
+
+size_t pkv_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads,
+                                 int num_kv_heads, int head_dim,
+                                 int max_blocks_per_seq);
 
 /* ------------------------------------------------------------------------ */
 /* INT8 KV cache ([G] "他のKVキャッシュ最適化との組み合わせ": INT8             */

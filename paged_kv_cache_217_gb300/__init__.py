@@ -31,10 +31,15 @@ from .binding import (  # noqa: F401
     paged_attention_decode_sliding,
     paged_attention_plan,
     paged_latent_decode,
+    paged_prefix_decode,
+    paged_prompt_attention,
+    prefix_workspace_size,
+    prompt_workspace_size,
     release_sequences,
     reshape_and_cache,
     reshape_and_cache_int4,
     reshape_and_cache_int8,
+    rotary_and_cache,
     sliding_workspace_size,
     resolved_partition,
     version,

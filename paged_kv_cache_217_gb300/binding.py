@@ -28,7 +28,7 @@ BALANCED = -2                      # pkv_paged_attention_partition: balanced per
 SHARED_PREFIX = -5                 # pkv_paged_attention_partition: shared-prefix schedule
 
 DEV_FLAGS = {0x1: "BAD_BLOCK_ID", 0x2: "BAD_CONTEXT_LEN", 0x4: "BAD_SLOT", 0x8: "BAD_PAIR",
-             0x10: "WAIT_TIMEOUT", 0x20: "BAD_PLAN", 0x40: "OUT_OF_BLOCKS"}
+             0x10: "WAIT_TIMEOUT", 0x20: "BAD_PLAN", 0x40: "OUT_OF_BLOCKS", 0x80: "BAD_POSITION", 0x100: "BAD_START"}
 LATENT_DIM, ROPE_DIM = 512, 64     # a latent cache row: the latent vector, then the shared rotary part
 
 
@@ -67,6 +67,12 @@ _SIGS = {
     "pkv_paged_attention_sliding_workspace_size": ([_c_int] * 7, _c_sz),
     "pkv_paged_attention_partition": ([_c_int] * 6, _c_int),
     "pkv_reshape_and_cache": ([_c_p] * 5 + [_c_int] * 5 + [_c_p], _c_int),
+    "pkv_rotary_and_cache": ([_c_p] * 4 + [_c_i64] * 4 + [_c_p] * 2 + [_c_int] * 3 + [_c_p] * 3 + [_c_int] * 6 + [_c_p],
+                             _c_int),
+    "pkv_paged_prompt_attention": ([_c_p] * 7 + [_c_int] * 7 + [_c_f] + [_c_int] * 3 + [_c_p, _c_sz, _c_p], _c_int),
+    "pkv_prompt_workspace_size": ([_c_int] * 6, _c_sz),
+    "pkv_paged_prefix_decode": ([_c_p] * 8 + [_c_int] * 7 + [_c_f, _c_int, _c_p, _c_sz, _c_p], _c_int),
+    "pkv_prefix_workspace_size": ([_c_int] * 6, _c_sz),
     "pkv_copy_blocks": ([_c_p] * 3 + [_c_int] * 5 + [_c_p], _c_int),
     "pkv_check_copy_pairs": ([_c_p, _c_int, _c_int], _c_int),
     "pkv_reshape_and_cache_int8": ([_c_p, _c_p, _c_int] + [_c_p] * 5 + [_c_int] * 4 + [_c_p], _c_int),
@@ -599,6 +605,120 @@ def paged_attention_decode_int4(out, q, kv_cache, block_tables, context_lens, sc
     _launch(q.device, "paged_attention_decode_int4", lib().pkv_paged_attention_decode_int4, out.data_ptr(),
             q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), S, Hq, hkv, D, mb, nb,
             float(scale), dt, window, ws_ptr, ws_bytes)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# rotated cache writes, prompt and cross attention, decode behind a shared prefix
+# ---------------------------------------------------------------------------
+def rotary_and_cache(q_out, q, k, v, positions, cos_sin, k_pool, v_pool, slot_mapping, interleaved=False):
+    """reshape_and_cache with queries and keys rotated by position on the way: q_out[t] = R(positions[t]) q[t],
+    k_pool[slot // 16, :, slot % 16] = R(positions[t]) k[t], v as it is.
+
+    q, q_out: [T, Hq, D] (q_out may be q; both None: keys and values only); k, v: [T, Hkv, D]; each may be a
+    slice of one projection's output. positions: int32 [T], < 0 for padding tokens, which are left out whole.
+    cos_sin: float32 [max_positions, rotary_dim], cosines then sines; pairs of elements lie rotary_dim / 2
+    apart, next to each other with ``interleaved``."""
+    import torch
+    _need_cuda(k_pool, v_pool, positions, cos_sin, slot_mapping)
+    dt = _dtype_code(k_pool)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    rows = (k, v) if q is None else (k, v, q, q_out)
+    if any(x.dtype != k_pool.dtype for x in rows) or v_pool.dtype != k_pool.dtype:
+        raise TypeError("q, k, v and pools must share one dtype")
+    if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64 or cos_sin.dtype != torch.float32:
+        raise TypeError("positions must be int32, slot_mapping int64, cos_sin float32")
+    index, pool = k_pool.get_device(), k_pool.shape
+    if len(pool) != 4 or pool[2] != BLOCK_SIZE or v_pool.shape != pool or cos_sin.dim() != 2 or k.dim() != 3 \
+            or (q is not None and q.dim() != 3):
+        raise ValueError("pools must be [num_blocks, num_kv_heads, 16, head_dim], cos_sin [max_positions, rotary_dim]")
+    nb, hkv, _, D = pool
+    T = k.shape[0]
+    hq = 0 if q is None else q.shape[1]
+    if k.shape != (T, hkv, D) or v.shape != k.shape or positions.shape != (T,) or slot_mapping.shape != (T,) \
+            or (q is not None and (q.shape != (T, hq, D) or q_out.shape != q.shape)):
+        raise ValueError("q, q_out: [T, Hq, D]; k, v: [T, Hkv, D]; positions and slot_mapping: [T]")
+    strides = []
+    for x in rows:
+        row, head, one = x.stride()
+        if x.get_device() != index:
+            raise ValueError("tensors must be on one device")
+        if T and (one != 1 or (head != D and x.shape[1] > 1)):
+            raise ValueError("the heads of a token must be contiguous")
+        strides.append(row if T > 1 else x.shape[1] * D)
+    ks, vs, qs, qos = strides if q is not None else (*strides, 0, 0)
+    _launch(k_pool.device, "rotary_and_cache", lib().pkv_rotary_and_cache, None if q is None else q_out.data_ptr(),
+            None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), qos, qs, ks, vs, positions.data_ptr(),
+            cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)), k_pool.data_ptr(),
+            v_pool.data_ptr(), slot_mapping.data_ptr(), T, hq, hkv, D, nb, dt)
+
+
+@functools.lru_cache(maxsize=1024)
+def prompt_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq):
+    return int(lib().pkv_prompt_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim,
+                                               max_blocks_per_seq))
+
+
+@functools.lru_cache(maxsize=1024)
+def prefix_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq):
+    return int(lib().pkv_prefix_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim,
+                                               max_blocks_per_seq))
+
+
+def _check_prompt(out, q, k_pool, v_pool, block_tables, context_lens, *starts):
+    import torch
+    _need_cuda(out, q, k_pool, v_pool, block_tables, context_lens, *starts)
+    dt = _dtype_code(q)
+    if out.dtype != q.dtype or k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
+        raise TypeError("q, out, k_pool and v_pool must share one dtype")
+    _need_dtype(torch.int32, "tables, lengths and starts", block_tables, context_lens, *starts)
+    shape, pool, table = q.shape, k_pool.shape, block_tables.shape
+    if len(pool) != 4 or len(shape) != 3 or pool[2] != BLOCK_SIZE or pool[3] != shape[2] or v_pool.shape != pool:
+        raise ValueError("q must be [tokens, Hq, head_dim], pools [num_blocks, num_kv_heads, 16, head_dim]")
+    if out.shape != shape or len(table) != 2 or context_lens.shape != (table[0],):
+        raise ValueError("shape mismatch among out, q, block_tables and context_lens")
+    return dt, shape, pool, table
+
+
+def paged_prompt_attention(out, q, k_pool, v_pool, block_tables, context_lens, query_starts, scale, causal=True,
+                           sliding_window=0, workspace=None):
+    """out[t, h] = softmax(scale * K_s q[t, h] + mask) V_s over the paged cache, for several query tokens per
+    sequence (in place in ``out``).
+
+    q, out: [T, Hq, D], sequence s's tokens from query_starts[s] to query_starts[s + 1] (int32 [S + 1]).
+    ``causal``: they are the last of its context_lens[s] tokens and see those up to themselves, the last
+    ``sliding_window`` of them when that is > 0 (prompts, chunks of prompts, drafted tokens). Without, they see
+    all context_lens[s] tokens (cross attention to an encoder's states). Queries that see nothing get zeros."""
+    dt, (T, Hq, D), (nb, hkv, _, _), (S, mb) = _check_prompt(out, q, k_pool, v_pool, block_tables, context_lens,
+                                                            query_starts)
+    if query_starts.shape != (S + 1,):
+        raise ValueError("query_starts must be [S + 1]")
+    ws, ws_ptr, ws_bytes = _call_workspace(q, prompt_workspace_size(T, S, Hq, hkv, D, mb), workspace)
+    _launch(q.device, "paged_prompt_attention", lib().pkv_paged_prompt_attention, out.data_ptr(), q.data_ptr(),
+            k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            query_starts.data_ptr(), T, S, Hq, hkv, D, mb, nb, float(scale), dt, int(bool(causal)),
+            max(0, int(sliding_window)), ws_ptr, ws_bytes)
+    return out
+
+
+def paged_prefix_decode(out, q, k_pool, v_pool, block_tables, context_lens, group_starts, prefix_blocks, scale,
+                        workspace=None):
+    """paged_attention_decode of groups of sequences that share their first blocks, each shared prefix computed
+    once for its whole group (in place in ``out``).
+
+    Group i: sequences group_starts[i] .. group_starts[i + 1] - 1 (int32 [groups + 1]), whose first
+    prefix_blocks[i] (int32 [groups]) blocks are those of the group's first sequence. Sequences outside every
+    group are computed by themselves."""
+    dt, (T, Hq, D), (nb, hkv, _, _), (S, mb) = _check_prompt(out, q, k_pool, v_pool, block_tables, context_lens,
+                                                            group_starts, prefix_blocks)
+    n = prefix_blocks.numel()
+    if T != S or prefix_blocks.shape != (n,) or group_starts.shape != (n + 1,):
+        raise ValueError("q must be [S, Hq, head_dim], group_starts [groups + 1], prefix_blocks [groups]")
+    ws, ws_ptr, ws_bytes = _call_workspace(q, prefix_workspace_size(S, n, Hq, hkv, D, mb), workspace)
+    _launch(q.device, "paged_prefix_decode", lib().pkv_paged_prefix_decode, out.data_ptr(), q.data_ptr(),
+            k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            group_starts.data_ptr(), prefix_blocks.data_ptr(), n, S, Hq, hkv, D, mb, nb, float(scale), dt, ws_ptr, ws_bytes)
     return out
 
 

@@ -32,6 +32,8 @@ SOURCES = [
     "cache_int4.cu",
     "decode_int4.cu",
     "latent.cu",
+    "prompt.cu",
+    "rotary.cu",
     "tables.cu",
     "diag.cu",
     "block_manager.cpp",

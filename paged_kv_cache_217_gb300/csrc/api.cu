@@ -1290,6 +1290,178 @@ pkv_status_t pkv_reshape_and_cache(const void* k, const void* v, void* k_pool, v
                      "reshape_and_cache launch");
 }
 
+pkv_status_t pkv_rotary_and_cache(void* q_out, const void* q, const void* k, const void* v, int64_t q_out_stride,
+                                  int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                                  const float* cos_sin, int max_positions, int rotary_dim, int interleaved, void* k_pool,
+                                  void* v_pool, const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                                  int num_kv_heads, int head_dim, int num_blocks, pkv_dtype_t dtype,
+                                  pkv_stream_t stream) {
+  if (num_tokens < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_tokens < 0");
+  if (num_tokens == 0) return pkv::ok();
+  if (num_q_heads < 0 || num_kv_heads <= 0 || num_blocks <= 0 || max_positions <= 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "num_kv_heads, num_blocks and max_positions must be > 0, num_q_heads >= 0");
+  if (num_q_heads > 4096 || num_kv_heads > 4096) return pkv::fail(PKV_ERR_UNSUPPORTED, "more than 4096 heads");
+  if (!supported_head_dim(head_dim)) return pkv::fail(PKV_ERR_UNSUPPORTED, "head_dim %d (64, 128 or 256)", head_dim);
+  if (rotary_dim <= 0 || rotary_dim > head_dim || rotary_dim % 16)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "rotary_dim %d must be a multiple of 16 up to head_dim", rotary_dim);
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return pkv::fail(PKV_ERR_UNSUPPORTED, "dtype %d", int(dtype));
+  if ((num_q_heads && (!q || !q_out)) || !k || !v || !positions || !cos_sin || !k_pool || !v_pool || !slot_mapping)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "NULL pointer");
+  if (k_stride < 0 || v_stride < 0 || k_stride % 8 || v_stride % 8 ||
+      (num_q_heads && (q_stride < 0 || q_stride % 8 || q_out_stride % 8)))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "strides must be non-negative multiples of 8 elements");
+  if (num_q_heads && num_tokens > 1 && q_out_stride < int64_t(num_q_heads) * head_dim)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "rows of q_out overlap");
+  if ((num_q_heads && (!aligned(q, 16) || !aligned(q_out, 16))) || !aligned(k, 16) || !aligned(v, 16) ||
+      !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(cos_sin, 16) || !aligned(positions, 4) ||
+      !aligned(slot_mapping, 8))
+    return pkv::fail(PKV_ERR_INVALID_ARG,
+                     "q, k, v, pools and cos_sin must be 16-byte aligned, positions 4-byte, slot_mapping 8-byte");
+  pkv::RotaryArgs a{};
+  pkv_status_t st = status_word(&a.status);
+  if (st != PKV_OK) return st;
+  a.q_out = q_out;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_out_stride = q_out_stride;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.slots = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.num_blocks = num_blocks;
+  a.max_positions = max_positions;
+  a.rotary_dim = rotary_dim;
+  a.interleaved = interleaved != 0;
+  return cuda_status(pkv::launch_rotary(a, dtype == PKV_BF16, stream), "rotary_and_cache launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+// What both calls of the prompt kernels check, and their launch. `need`: bytes of workspace.
+pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, float scale, pkv_dtype_t dtype, size_t need,
+                         void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (a.num_q_heads <= 0 || a.num_kv_heads <= 0 || a.num_q_heads % a.num_kv_heads != 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
+                     a.num_q_heads, a.num_kv_heads);
+  a.group = a.num_q_heads / a.num_kv_heads;
+  if (a.group > 128) return pkv::fail(PKV_ERR_UNSUPPORTED, "query heads per KV head %d > 128", a.group);
+  if (!supported_head_dim(head_dim)) return pkv::fail(PKV_ERR_UNSUPPORTED, "head_dim %d (64, 128 or 256)", head_dim);
+  if (dtype != PKV_F16 && dtype != PKV_BF16) return pkv::fail(PKV_ERR_UNSUPPORTED, "dtype %d", int(dtype));
+  if (a.max_blocks_per_seq <= 0 || a.num_blocks <= 0)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq and num_blocks must be > 0");
+  if (int64_t(a.max_blocks_per_seq) * PKV_BLOCK_SIZE > INT32_MAX / 2)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq too large");
+  if (a.num_seqs > 65535) return pkv::fail(PKV_ERR_UNSUPPORTED, "num_seqs %d > 65535", a.num_seqs);
+  if (int64_t(a.num_tokens) * a.num_q_heads > INT32_MAX)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "num_tokens * num_q_heads exceeds 2^31 rows");
+  if (int64_t(a.num_blocks) * a.num_kv_heads > INT32_MAX / 4)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "num_blocks * num_kv_heads exceeds 2^29 tiles");
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!std::isfinite(scale) || !std::isfinite(scale_log2)) return pkv::fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (!a.out || !a.q || !a.k_pool || !a.v_pool || !a.block_tables || !a.context_lens)
+    return pkv::fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!aligned(a.out, 16) || !aligned(a.q, 16) || !aligned(a.k_pool, 16) || !aligned(a.v_pool, 16))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "out, q and pools must be 16-byte aligned");
+  if (!aligned(a.block_tables, 4) || !aligned(a.context_lens, 4) || !aligned(a.query_starts, 4) ||
+      !aligned(a.group_starts, 4) || !aligned(a.prefix_blocks, 4))
+    return pkv::fail(PKV_ERR_INVALID_ARG, "tables, lengths and starts must be 4-byte aligned");
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
+                     need, workspace_bytes, workspace);
+  pkv_status_t st = status_word(&a.status);
+  if (st != PKV_OK) return st;
+  a.scale_log2 = scale_log2;
+  const EnqueueLock lock(stream);
+  return cuda_status(pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, stream), what);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int max_blocks_per_seq) {
+  return 0;
+}
+
+pkv_status_t pkv_paged_prompt_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                        const int32_t* block_tables, const int32_t* context_lens,
+                                        const int32_t* query_starts, int num_tokens, int num_seqs, int num_q_heads,
+                                        int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks,
+                                        float scale, pkv_dtype_t dtype, int causal, int sliding_window,
+                                        void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_seqs < 0 || num_tokens < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs or num_tokens < 0");
+  if (num_seqs == 0 || num_tokens == 0) return pkv::ok();
+  if (!query_starts) return pkv::fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  if (!causal && sliding_window > 0)
+    return pkv::fail(PKV_ERR_UNSUPPORTED, "a sliding window needs causal attention");
+  pkv::PromptArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_starts = query_starts;
+  a.num_tokens = num_tokens;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.causal = causal != 0;
+  a.window = sliding_window > 0 ? sliding_window : 0;
+  return prompt_impl("paged_prompt_attention launch", a, head_dim, scale, dtype,
+                     pkv_prompt_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq),
+                     workspace, workspace_bytes, stream);
+}
+
+size_t pkv_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int max_blocks_per_seq) {
+  return 0;
+}
+
+pkv_status_t pkv_paged_prefix_decode(void* out, const void* q, const void* k_pool, const void* v_pool,
+                                     const int32_t* block_tables, const int32_t* context_lens,
+                                     const int32_t* group_starts, const int32_t* prefix_blocks, int num_groups,
+                                     int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                     int max_blocks_per_seq, int num_blocks, float scale, pkv_dtype_t dtype,
+                                     void* workspace, size_t workspace_bytes, pkv_stream_t stream) {
+  if (num_seqs < 0 || num_groups < 0) return pkv::fail(PKV_ERR_INVALID_ARG, "num_seqs or num_groups < 0");
+  if (num_seqs == 0) return pkv::ok();
+  if (num_groups > num_seqs) return pkv::fail(PKV_ERR_INVALID_ARG, "more groups than sequences");
+  if (num_groups > 0 && (!group_starts || !prefix_blocks)) return pkv::fail(PKV_ERR_INVALID_ARG, "NULL tensor pointer");
+  pkv::PromptArgs a{};
+  a.out = out;
+  a.q = q;
+  a.k_pool = k_pool;
+  a.v_pool = v_pool;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.group_starts = group_starts;
+  a.prefix_blocks = prefix_blocks;
+  a.num_groups = num_groups;
+  a.num_tokens = a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  return prompt_impl("paged_prefix_decode launch", a, head_dim, scale, dtype,
+                     pkv_prefix_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq),
+                     workspace, workspace_bytes, stream);
+}
+
 pkv_status_t pkv_copy_blocks(void* k_pool, void* v_pool, const int64_t* src_dst_pairs,
                              int num_pairs, int num_kv_heads, int head_dim, int num_blocks,
                              pkv_dtype_t dtype, pkv_stream_t stream) {

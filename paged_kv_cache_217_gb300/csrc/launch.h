@@ -147,6 +147,47 @@ int latent_query_box(int num_seqs, int num_heads, int max_blocks_per_seq);
 cudaError_t launch_latent_decode(const LatentArgs& a, bool bf16, const CUtensorMap& cache_map,
                                  const CUtensorMap& q_map, cudaStream_t stream);
 
+// The cache write that rotates queries and keys (rotary.cu).
+struct RotaryArgs {
+  void* q_out;
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_out_stride, q_stride, k_stride, v_stride;  // elements between tokens
+  const int32_t* positions;
+  const float* cos_sin;  // [max_positions][rotary_dim]
+  void* k_pool;
+  void* v_pool;
+  const int64_t* slots;
+  unsigned int* status;
+  int num_tokens, num_q_heads, num_kv_heads, head_dim, num_blocks;
+  int max_positions, rotary_dim, interleaved;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, cudaStream_t stream);
+
+// Attention of several query tokens per sequence, and of sequences that share a
+// prefix, over the paged cache (prompt.cuh).
+struct PromptArgs {
+  void* out;
+  const void* q;
+  const void* k_pool;
+  const void* v_pool;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_starts;   // [num_seqs + 1]; null: one query per sequence
+  const int32_t* group_starts;   // [num_groups + 1], and
+  const int32_t* prefix_blocks;  // [num_groups]: sequences that share their first blocks (num_groups 0: none)
+  unsigned int* status;
+  int num_seqs, num_tokens, num_groups;
+  int num_q_heads, num_kv_heads;
+  int group;         // query heads per KV head
+  int max_blocks_per_seq, num_blocks;
+  int causal;
+  int window;        // causal: attend over the last `window` tokens (0 = all)
+  float scale_log2;  // scale * log2(e)
+};
+cudaError_t launch_prompt(const PromptArgs& a, bool bf16, int head_dim, cudaStream_t stream);
+
 // Block tables on the device (tables.cu).
 struct ExtendArgs {
   int32_t* block_tables;
