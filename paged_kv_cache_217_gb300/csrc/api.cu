@@ -334,6 +334,44 @@ pkv_status_t query_tensor_map(CUtensorMap* map, const void* q, int num_seqs, int
   return PKV_OK;
 }
 
+// The queries [num_tokens][num_heads][head_dim] as a 4-D tensor {64 elements, heads,
+// tokens, head_dim / 64 chunks}, read one chunk of `heads` heads x `tokens` tokens a box.
+pkv_status_t prompt_query_map(CUtensorMap* map, const void* q, int num_tokens, int num_heads, int head_dim,
+                              pkv_dtype_t dtype, int heads, int tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t row = cuuint64_t(head_dim) * 2;
+  const cuuint64_t dims[4] = {64, cuuint64_t(num_heads), cuuint64_t(num_tokens), cuuint64_t(head_dim / 64)};
+  const cuuint64_t strides[3] = {row, row * cuuint64_t(num_heads), 128};
+  const cuuint32_t box[4] = {64, cuuint32_t(heads), cuuint32_t(tokens), 1};
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+  const CUresult r = encode_tiled(enc, map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         4, const_cast<void*>(q), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled (prompt queries) failed (CUresult %d)", int(r));
+  return PKV_OK;
+}
+
+// A pool as a 4-D tensor {64 elements, 8 rows, head_dim / 64 chunks, 2 * tiles groups of
+// 8 rows}, read one (block, KV head) tile a box, which lands as two groups of
+// head_dim / 64 swizzled 8-row x 128-byte atoms.
+pkv_status_t prompt_pool_map(CUtensorMap* map, const void* pool, int64_t tiles, int head_dim, pkv_dtype_t dtype) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t row = cuuint64_t(head_dim) * 2;
+  const cuuint64_t dims[4] = {64, 8, cuuint64_t(head_dim / 64), cuuint64_t(tiles) * 2};
+  const cuuint64_t strides[3] = {row, 128, 8 * row};
+  const cuuint32_t box[4] = {64, 8, cuuint32_t(head_dim / 64), 2};
+  const cuuint32_t elem_strides[4] = {1, 1, 1, 1};
+  const CUresult r = encode_tiled(enc, map, dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                         4, const_cast<void*>(pool), dims, strides, box, elem_strides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return pkv::fail(PKV_ERR_CUDA, "cuTensorMapEncodeTiled (pool tiles) failed (CUresult %d)", int(r));
+  return PKV_OK;
+}
+
 // An INT8 code pool seen as a 2-D uint8 tensor of num_blocks*num_kv_heads*16
 // rows by head_dim columns, read in boxes of 16 rows x min(head_dim, 128)
 // bytes with the 128-byte swizzle (the 64-byte one for 64-byte rows).
@@ -1348,8 +1386,8 @@ pkv_status_t pkv_rotary_and_cache(void* q_out, const void* q, const void* k, con
 
 namespace {
 
-// What both calls of the prompt kernels check, and their launch. `need`: bytes of workspace.
-pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, float scale, pkv_dtype_t dtype, size_t need,
+// What both calls of the prompt kernels check, and their launch.
+pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, float scale, pkv_dtype_t dtype,
                          void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (a.num_q_heads <= 0 || a.num_kv_heads <= 0 || a.num_q_heads % a.num_kv_heads != 0)
     return pkv::fail(PKV_ERR_INVALID_ARG, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
@@ -1376,14 +1414,40 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
   if (!aligned(a.block_tables, 4) || !aligned(a.context_lens, 4) || !aligned(a.query_starts, 4) ||
       !aligned(a.group_starts, 4) || !aligned(a.prefix_blocks, 4))
     return pkv::fail(PKV_ERR_INVALID_ARG, "tables, lengths and starts must be 4-byte aligned");
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+  const size_t need = pkv::prompt_workspace_bytes(a, head_dim);
+  if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
     return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
                      need, workspace_bytes, workspace);
   pkv_status_t st = status_word(&a.status);
   if (st != PKV_OK) return st;
   a.scale_log2 = scale_log2;
+  alignas(64) CUtensorMap q_map, k_map, v_map;
+  st = prompt_query_map(&q_map, a.q, a.num_tokens, a.num_q_heads, head_dim, dtype, a.group, pkv::prompt_tile_tokens(a.group));
+  if (st != PKV_OK) return st;
+  const int64_t tiles = int64_t(a.num_blocks) * a.num_kv_heads;
+  st = prompt_pool_map(&k_map, a.k_pool, tiles, head_dim, dtype);
+  if (st != PKV_OK) return st;
+  st = prompt_pool_map(&v_map, a.v_pool, tiles, head_dim, dtype);
+  if (st != PKV_OK) return st;
   const EnqueueLock lock(stream);
-  return cuda_status(pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, stream), what);
+  return cuda_status(pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, q_map, k_map, v_map, stream), what);
+}
+
+// Sizes of a call as prompt_workspace_bytes reads them; false for ones that no call takes.
+bool prompt_sizes(pkv::PromptArgs* a, int num_tokens, int num_seqs, int num_groups, int num_q_heads, int num_kv_heads,
+                  int head_dim, int max_blocks_per_seq) {
+  if (num_tokens <= 0 || num_seqs <= 0 || num_groups < 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 128 || !supported_head_dim(head_dim) ||
+      max_blocks_per_seq <= 0)
+    return false;
+  *a = pkv::PromptArgs{};
+  a->num_tokens = num_tokens;
+  a->num_seqs = num_seqs;
+  a->num_groups = num_groups;
+  a->num_q_heads = num_q_heads;
+  a->num_kv_heads = num_kv_heads;
+  a->max_blocks_per_seq = max_blocks_per_seq;
+  return true;
 }
 
 }  // namespace
@@ -1392,7 +1456,11 @@ extern "C" {
 
 size_t pkv_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                  int max_blocks_per_seq) {
-  return 0;
+  pkv::PromptArgs a;
+  if (!prompt_sizes(&a, num_tokens, num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)) return 0;
+  static const int32_t ragged = 0;
+  a.query_starts = &ragged;  // (only whether there are any matters)
+  return pkv::prompt_workspace_bytes(a, head_dim);
 }
 
 pkv_status_t pkv_paged_prompt_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -1422,14 +1490,14 @@ pkv_status_t pkv_paged_prompt_attention(void* out, const void* q, const void* k_
   a.num_blocks = num_blocks;
   a.causal = causal != 0;
   a.window = sliding_window > 0 ? sliding_window : 0;
-  return prompt_impl("paged_prompt_attention launch", a, head_dim, scale, dtype,
-                     pkv_prompt_workspace_size(num_tokens, num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq),
-                     workspace, workspace_bytes, stream);
+  return prompt_impl("paged_prompt_attention launch", a, head_dim, scale, dtype, workspace, workspace_bytes, stream);
 }
 
 size_t pkv_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads, int num_kv_heads, int head_dim,
                                  int max_blocks_per_seq) {
-  return 0;
+  pkv::PromptArgs a;
+  if (!prompt_sizes(&a, num_seqs, num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)) return 0;
+  return pkv::prompt_workspace_bytes(a, head_dim);
 }
 
 pkv_status_t pkv_paged_prefix_decode(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -1457,9 +1525,7 @@ pkv_status_t pkv_paged_prefix_decode(void* out, const void* q, const void* k_poo
   a.num_kv_heads = num_kv_heads;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = num_blocks;
-  return prompt_impl("paged_prefix_decode launch", a, head_dim, scale, dtype,
-                     pkv_prefix_workspace_size(num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq),
-                     workspace, workspace_bytes, stream);
+  return prompt_impl("paged_prefix_decode launch", a, head_dim, scale, dtype, workspace, workspace_bytes, stream);
 }
 
 pkv_status_t pkv_copy_blocks(void* k_pool, void* v_pool, const int64_t* src_dst_pairs,

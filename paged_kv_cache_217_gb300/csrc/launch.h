@@ -185,8 +185,25 @@ struct PromptArgs {
   int causal;
   int window;        // causal: attend over the last `window` tokens (0 = all)
   float scale_log2;  // scale * log2(e)
+  // set by the launcher: query tokens of a tile of rows and of a block, CTAs, rows of a
+  // slot of partial results, and the workspace's parts
+  int tile_tokens, block_tokens, shares;
+  size_t slot_rows;
+  int4* desc;   // per share, the item that starts in it and goes on past it (prompts)
+  int2* link;   // per item, the shares that hold its pieces (prefix decode)
+  int* more;    // per share, whether it begins inside an item
+  float2* part_ml;
+  float* part_o;
 };
-cudaError_t launch_prompt(const PromptArgs& a, bool bf16, int head_dim, cudaStream_t stream);
+// Query tokens of one copy of Q (128 rows): the second box size of its tensor map.
+inline int prompt_tile_tokens(int group) { return 128 / group; }
+size_t prompt_workspace_bytes(const PromptArgs& a, int head_dim);
+// q_map: q as {64 elements, heads, tokens, head_dim / 64 chunks}, boxes of one KV head's
+// query heads x prompt_tile_tokens; k_map, v_map: a pool as {64 elements, 8 rows,
+// head_dim / 64 chunks, 8-row groups}, boxes of one (block, KV head); 128-byte swizzle,
+// zero fill.
+cudaError_t launch_prompt(PromptArgs a, bool bf16, int head_dim, void* workspace, const CUtensorMap& q_map,
+                          const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
 
 // Block tables on the device (tables.cu).
 struct ExtendArgs {
