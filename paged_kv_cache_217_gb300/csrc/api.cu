@@ -1421,16 +1421,15 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
   pkv_status_t st = status_word(&a.status);
   if (st != PKV_OK) return st;
   a.scale_log2 = scale_log2;
-  alignas(64) CUtensorMap q_map, k_map, v_map;
-  st = prompt_query_map(&q_map, a.q, a.num_tokens, a.num_q_heads, head_dim, dtype, a.group, pkv::prompt_tile_tokens(a.group));
-  if (st != PKV_OK) return st;
+  pkv::PromptMaps maps;
   const int64_t tiles = int64_t(a.num_blocks) * a.num_kv_heads;
-  st = prompt_pool_map(&k_map, a.k_pool, tiles, head_dim, dtype);
-  if (st != PKV_OK) return st;
-  st = prompt_pool_map(&v_map, a.v_pool, tiles, head_dim, dtype);
+  st = prompt_query_map(&maps.q, a.q, a.num_tokens, a.num_q_heads, head_dim, dtype, a.group, pkv::prompt_tile_tokens(a.group));
+  if (st == PKV_OK) st = prompt_query_map(&maps.q1, a.q, a.num_tokens, a.num_q_heads, head_dim, dtype, a.group, 1);
+  if (st == PKV_OK) st = prompt_pool_map(&maps.k, a.k_pool, tiles, head_dim, dtype);
+  if (st == PKV_OK) st = prompt_pool_map(&maps.v, a.v_pool, tiles, head_dim, dtype);
   if (st != PKV_OK) return st;
   const EnqueueLock lock(stream);
-  return cuda_status(pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, q_map, k_map, v_map, stream), what);
+  return cuda_status(pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, maps, stream), what);
 }
 
 // Sizes of a call as prompt_workspace_bytes reads them; false for ones that no call takes.

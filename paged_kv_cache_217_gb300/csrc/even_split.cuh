@@ -8,10 +8,10 @@ namespace pkv {
 struct EvenSplit {
   long long size;  // of a range behind the first `longer`, which have one more
   int longer, parts;
-  __device__ __forceinline__ EvenSplit(long long total, int n) : parts(n) {
-    size = (long long)((unsigned long long)total / unsigned(n));
-    longer = int(total - size * n);
-  }
+  __device__ __forceinline__ EvenSplit(long long total, int n)
+      : EvenSplit(total, n, (long long)((unsigned long long)total / unsigned(n))) {}
+  __device__ __forceinline__ EvenSplit(long long total, int n, long long quotient)
+      : size(quotient), longer(int(total - quotient * n)), parts(n) {}
   __device__ __forceinline__ long long begin(int part) const { return part * size + (part < longer ? part : longer); }
   // The range of entry x (0 <= x < total).
   __device__ __forceinline__ int of(long long x) const {

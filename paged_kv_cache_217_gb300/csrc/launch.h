@@ -198,12 +198,15 @@ struct PromptArgs {
 // Query tokens of one copy of Q (128 rows): the second box size of its tensor map.
 inline int prompt_tile_tokens(int group) { return 128 / group; }
 size_t prompt_workspace_bytes(const PromptArgs& a, int head_dim);
-// q_map: q as {64 elements, heads, tokens, head_dim / 64 chunks}, boxes of one KV head's
-// query heads x prompt_tile_tokens; k_map, v_map: a pool as {64 elements, 8 rows,
-// head_dim / 64 chunks, 8-row groups}, boxes of one (block, KV head); 128-byte swizzle,
-// zero fill.
-cudaError_t launch_prompt(PromptArgs a, bool bf16, int head_dim, void* workspace, const CUtensorMap& q_map,
-                          const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream);
+// Tensor maps of a call, with the 128-byte swizzle and zero fill: q as {64 elements,
+// heads, tokens, head_dim / 64 chunks}, in boxes of one KV head's query heads x
+// prompt_tile_tokens (q) or 1 token (q1); the pools as {64 elements, 8 rows, head_dim /
+// 64 chunks, 8-row groups}, in boxes of one (block, KV head).
+struct PromptMaps {
+  CUtensorMap q, q1, k, v;
+};
+cudaError_t launch_prompt(PromptArgs a, bool bf16, int head_dim, void* workspace, const PromptMaps& maps,
+                          cudaStream_t stream);
 
 // Block tables on the device (tables.cu).
 struct ExtendArgs {

@@ -32,14 +32,13 @@ PromptShape prompt_shape(const PromptArgs& a, int head_dim) {
 }
 
 template <typename T, int D>
-cudaError_t launch_d(const PromptArgs& a, const CUtensorMap& q_map, const CUtensorMap& k_map, const CUtensorMap& v_map,
-                     cudaStream_t stream) {
+cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, cudaStream_t stream) {
   using C = PromptCfg<D>;
   static bool configured[kMaxDevices] = {};
   cudaError_t err = configure_once(prompt_kernel<T, D>, C::SMEM_BYTES, configured);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(prompt_kernel<T, D>, dim3(unsigned(a.shares)), dim3(C::THREADS), C::SMEM_BYTES, stream, a, q_map, k_map,
-                   v_map);
+  err = launch_pdl(prompt_kernel<T, D>, dim3(unsigned(a.shares)), dim3(C::THREADS), C::SMEM_BYTES, stream, a, maps.q,
+                   maps.q1, maps.k, maps.v);
   if (err != cudaSuccess) return err;
   if (!a.query_starts)
     return launch_pdl(prefix_join_kernel<T, D>, dim3(unsigned((int64_t(a.num_seqs) * a.num_q_heads + 7) / 8)), dim3(256), 0,
@@ -49,11 +48,10 @@ cudaError_t launch_d(const PromptArgs& a, const CUtensorMap& q_map, const CUtens
 }
 
 template <typename T>
-cudaError_t launch_t(const PromptArgs& a, int head_dim, const CUtensorMap& q_map, const CUtensorMap& k_map,
-                     const CUtensorMap& v_map, cudaStream_t stream) {
-  if (head_dim == 64) return launch_d<T, 64>(a, q_map, k_map, v_map, stream);
-  if (head_dim == 128) return launch_d<T, 128>(a, q_map, k_map, v_map, stream);
-  return launch_d<T, 256>(a, q_map, k_map, v_map, stream);
+cudaError_t launch_t(const PromptArgs& a, int head_dim, const PromptMaps& maps, cudaStream_t stream) {
+  if (head_dim == 64) return launch_d<T, 64>(a, maps, stream);
+  if (head_dim == 128) return launch_d<T, 128>(a, maps, stream);
+  return launch_d<T, 256>(a, maps, stream);
 }
 
 }  // namespace
@@ -67,8 +65,8 @@ size_t prompt_workspace_bytes(const PromptArgs& a, int head_dim) {
          (p.slot_rows * 2 * p.shares + p.rows) * (sizeof(float2) + size_t(head_dim) * sizeof(float));
 }
 
-cudaError_t launch_prompt(PromptArgs a, bool bf16, int head_dim, void* workspace, const CUtensorMap& q_map,
-                          const CUtensorMap& k_map, const CUtensorMap& v_map, cudaStream_t stream) {
+cudaError_t launch_prompt(PromptArgs a, bool bf16, int head_dim, void* workspace, const PromptMaps& maps,
+                          cudaStream_t stream) {
   const PromptShape p = prompt_shape(a, head_dim);
   a.tile_tokens = p.tile_tokens;
   a.block_tokens = p.block_tokens;
@@ -82,8 +80,7 @@ cudaError_t launch_prompt(PromptArgs a, bool bf16, int head_dim, void* workspace
   at += round16(size_t(p.shares) * sizeof(int));
   a.part_o = reinterpret_cast<float*>(at);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + (p.slot_rows * 2 * p.shares + p.rows) * head_dim);
-  return bf16 ? launch_t<__nv_bfloat16>(a, head_dim, q_map, k_map, v_map, stream)
-              : launch_t<__half>(a, head_dim, q_map, k_map, v_map, stream);
+  return bf16 ? launch_t<__nv_bfloat16>(a, head_dim, maps, stream) : launch_t<__half>(a, head_dim, maps, stream);
 }
 
 }  // namespace pkv

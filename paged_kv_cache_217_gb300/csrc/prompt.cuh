@@ -10,7 +10,7 @@
 // some of its tiles of 128 tokens (64).
 //
 // Warps: two softmax warpgroups (a thread a row of the tile), one warp each that copies
-// K and V, copies Q, and issues the MMAs. Warpgroup w owns S_w and O_w in tensor memory
+// K and V and copies Q, and one for each warpgroup that issues its MMAs. Warpgroup w owns S_w and O_w in tensor memory
 // (S 128 columns, O head_dim). A block of more than 128 rows gives each warpgroup a tile
 // of rows and every K and V tile is used by both; a smaller one (few queries, decode)
 // gives both the same rows and every other tile, joined at the end. With head_dim 256 O
@@ -37,6 +37,7 @@
 #include <cuda.h>
 
 #include "device_common.cuh"
+#include "even_split.cuh"
 #include "latent_decode.cuh"
 #include "launch.h"
 
@@ -49,6 +50,9 @@ constexpr float kPromptLazy = 8.f;
 constexpr float kPromptHeadroom = 7.f;  // fp16 weights are 2^7 times as large (see kLatentHeadroom)
 constexpr int kPromptPieces = 4;   // pieces that the copying warp may be ahead
 constexpr int kPromptNone = -1;
+// A piece of one tile of rows goes to one warpgroup, the next to the other; from this many
+// KV tiles on, or with no piece behind it, to both.
+constexpr int kPromptSplit = 8;
 
 template <int D>
 struct PromptCfg {
@@ -60,11 +64,15 @@ struct PromptCfg {
   static constexpr int SLOTS = D == 64 ? 8 : 4;
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int SOFTMAX = 128 * GROUPS;        // threads
-  static constexpr int THREADS = SOFTMAX + 96;
+  static constexpr int THREADS = SOFTMAX + 128;
+  static constexpr int DEPTH = 3 - GROUPS;            // S buffers of a warpgroup
+  static constexpr int STAGE = 2048;                  // bytes a softmax warp writes its output through
   static constexpr int STEP = CHUNKS * 1024;          // bytes of 8 tokens
-  static constexpr int S_AT = GROUPS * D;             // columns of tensor memory: O, then S
+  static constexpr int S_AT = GROUPS * D;             // columns of tensor memory: O, then two S
   static constexpr int COLUMNS = 512;
-  static constexpr int MISC = 1024 + 1024 * GROUPS;
+  static constexpr int LISTED = THREADS;              // segments that are kept in shared memory
+  static constexpr int STATS_AT = 1024, STAGE_AT = STATS_AT + 1024 * GROUPS, LIST_AT = STAGE_AT + STAGE * 4 * GROUPS;
+  static constexpr int MISC = LIST_AT + LISTED * 32;
   static constexpr size_t SMEM_BYTES = 1024 + size_t(GROUPS) * Q_TILE + size_t(SLOTS) * SLOT + MISC;
   static_assert(S_AT + 2 * TILE <= COLUMNS, "tensor memory");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -75,11 +83,12 @@ enum { kRowsCausal = 0, kRowsAll = 1, kRowsMembers = 2 };
 
 // Queries that share a table: a sequence's; a group's members over their prefix
 // (kRowsMembers); a member over the rest.
-struct PromptSegment {
+struct __align__(16) PromptSegment {
   int q0, nq;   // query tokens
   int table;    // sequence whose table holds the positions
   int lo, len;  // positions [lo, len)
   int kind;
+  long long cost;  // of one head
 };
 
 __device__ __forceinline__ int prompt_clamp(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
@@ -145,11 +154,12 @@ __device__ __forceinline__ void prompt_block(const PromptArgs& a, const PromptSe
     *lo = a.window ? max(0, *base - a.window + 1) : 0;
   }
 }
-// sum over i < n of max(0, x + i T)
+// sum over i < n of max(0, x + i T), x > -2^32
 __device__ __forceinline__ long long prompt_ramp(long long x, int T, int n) {
-  const int skip = x > 0 ? 0 : int(min((long long)n, -x / T + 1));
-  const long long count = n - skip;
-  return count <= 0 ? 0 : count * (x + (long long)skip * T) + T * (count * (count - 1) / 2);
+  const unsigned skip = x > 0 ? 0u : unsigned(-x) / unsigned(T) + 1u;
+  if (skip >= unsigned(n)) return 0;
+  const long long count = n - int(skip);
+  return count * (x + (long long)skip * T) + T * (count * (count - 1) / 2);
 }
 // Cost of the first r blocks of one head of a segment.
 __device__ __forceinline__ long long prompt_cost(const PromptArgs& a, const PromptSegment& g, int r, int T) {
@@ -172,19 +182,32 @@ struct PromptPiece {
   int base;        // position of the first token (causal)
   int kind;
   int slot;        // of the workspace; kPromptNone: the item is whole
+  int mode;
+};
+// Who takes a piece: one warpgroup; both, a tile of rows each; both, every other KV tile each.
+enum { kPieceFirst = 0, kPieceSecond = 1, kPieceRows = 2, kPieceSplit = 3 };
+// The KV tiles of a piece that warpgroup w takes: from `first` in steps of `step`.
+struct PieceTiles {
+  int first, step;
+  bool any;
+  __device__ __forceinline__ PieceTiles(int mode, int tiles, int w)
+      : first(mode == kPieceSplit ? w : 0), step(mode == kPieceSplit ? 2 : 1),
+        any(mode == w || (mode >= kPieceRows && (mode == kPieceRows || w < tiles))) {}
 };
 
 struct PromptShared {
   uint64_t slot_full[8], slot_empty[8];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], join;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], join;
   uint64_t piece_full[kPromptPieces], piece_empty[kPromptPieces];
-  uint64_t drain;  // after a wait gave up
+  uint64_t drain[2];  // after a wait gave up
   PromptPiece piece[kPromptPieces];
   long long scan[12];
   long long first_base;
   int first_seg;
   uint32_t tmem;
-  int stop;  // a wait gave up: every role leaves
+  int stop;    // a wait gave up: every role leaves
+  int lock;    // a warp issues its MMAs
+  int issued;  // K and V tiles whose copies are issued
 };
 static_assert(sizeof(PromptShared) <= 1024, "shared state");
 
@@ -209,15 +232,63 @@ __device__ __forceinline__ void tc_ld_32x32(uint32_t addr, float* r) {
         "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st_32x32(uint32_t addr, const uint32_t* u) {
+// 32 lanes (one a thread) x 16 columns.
+__device__ __forceinline__ void tc_ld_32x16(uint32_t addr, float* r) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(r);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]), "=r"(u[8]),
+        "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st_32x16(uint32_t addr, const uint32_t* u) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
       "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]), "r"(u[9]),
-      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]), "r"(u[17]), "r"(u[18]),
-      "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]), "r"(u[25]), "r"(u[26]), "r"(u[27]),
-      "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
+      "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
       : "memory");
+}
+__device__ __forceinline__ int lds_acquire(uint32_t addr) {
+  int v;
+  asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts_release(uint32_t addr, int v) {
+  asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+__device__ __forceinline__ void st_global_if(bool on, void* p, const uint4& u) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %0, 0;\n\t@p st.global.v4.b32 [%1], {%2, %3, %4, %5};\n\t}" ::"r"(
+                   uint32_t(on)),
+               "l"(p), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+               : "memory");
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ unsigned long long pair(float x, float y) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(unsigned long long p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long x, unsigned long long y, unsigned long long z) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long x, unsigned long long y) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
 }
 // Values that an asynchronous load wrote are used behind its wait only.
 template <int N>
@@ -227,40 +298,67 @@ __device__ __forceinline__ void tc_loaded(float (&x)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(x[i]));
 }
 
+// Waits of a warp, all lanes: false when the limit ran out or another role gave up. The clock
+// is looked at once in 64 tries only: reading it takes longer than most waits.
+__device__ __forceinline__ bool prompt_wait(uint32_t bar, uint32_t parity, volatile int* stop, unsigned int* status) {
+  unsigned long long t0 = 0;
+  for (int tries = 0;; ++tries) {
+    if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    if ((tries & 63) != 63) continue;
+    const unsigned long long now = global_timer_ns();
+    if (tries == 63) t0 = now;
+    bool over = now - t0 > kWaitLimitNs;
+    if (over && !*stop) {
+      *stop = 1;
+      flag(status, PKV_DEV_WAIT_TIMEOUT);
+    }
+    over = *stop;
+    if (__any_sync(kFull, over)) return false;
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
-prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
-              const __grid_constant__ CUtensorMap v_map) {
+prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap q1_map,
+              const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using C = PromptCfg<D>;
   extern __shared__ __align__(1024) unsigned char smem[];
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem) + 1023) & ~uintptr_t(1023));
   unsigned char* q_mem = base;                              // per tile of rows: chunks of [128][64]
   unsigned char* ring = q_mem + C::GROUPS * C::Q_TILE;      // K and V tiles in turn
   PromptShared& sh = *reinterpret_cast<PromptShared*>(ring + C::SLOTS * C::SLOT);
-  float2* const stats = reinterpret_cast<float2*>(ring + C::SLOTS * C::SLOT + 1024);  // [GROUPS][128] of a join
+  unsigned char* const misc = ring + C::SLOTS * C::SLOT;
+  float2* const stats = reinterpret_cast<float2*>(misc + C::STATS_AT);            // [GROUPS][128] of a join
+  unsigned char* const stage = misc + C::STAGE_AT;                                // per softmax warp
+  PromptSegment* const list = reinterpret_cast<PromptSegment*>(misc + C::LIST_AT);  // the segments, where there are few
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int WARP_KV = C::SOFTMAX / 32, WARP_Q = WARP_KV + 1, WARP_MMA = WARP_KV + 2;
 
   if (tid == 0) {
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
       mbar_init(smem_addr(&sh.slot_full[i]), 1);
-      mbar_init(smem_addr(&sh.slot_empty[i]), 1);
+      mbar_init(smem_addr(&sh.slot_empty[i]), 2);
     }
-    mbar_init(smem_addr(&sh.q_full), 1);
-    mbar_init(smem_addr(&sh.q_empty), 1);
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&sh.q_full[i]), 1);
+      mbar_init(smem_addr(&sh.q_empty[i]), 1);
       mbar_init(smem_addr(&sh.s_full[i]), 1);
       mbar_init(smem_addr(&sh.p_full[i]), 128);
       mbar_init(smem_addr(&sh.pv_done[i]), 1);
     }
     mbar_init(smem_addr(&sh.join), C::SOFTMAX);
+#pragma unroll 1
     for (int i = 0; i < kPromptPieces; ++i) {
       mbar_init(smem_addr(&sh.piece_full[i]), 1);
-      mbar_init(smem_addr(&sh.piece_empty[i]), C::SOFTMAX / 32 + 2);
+      mbar_init(smem_addr(&sh.piece_empty[i]), C::SOFTMAX / 32 + 1 + C::GROUPS);
     }
     mbar_init_fence();
     sh.stop = 0;
+    sh.issued = sh.lock = 0;
     asm volatile("prefetch.tensormap [%0];" ::"l"(&q_map) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&q1_map) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&v_map) : "memory");
   }
@@ -275,66 +373,97 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
 
   // The list: each thread sums a run of segments, a scan of the sums gives every
   // run's place, and the thread whose run holds this CTA's share's begin finds its
-  // segment.
+  // segment (walking its run once more where it is longer than one).
+  // (Written to be short: an SM fetches code that it has not run yet at some 30 cycles an
+  // instruction, and all of this comes before the first copy.)
   const int TQ = a.tile_tokens, TB = TQ * C::GROUPS;  // tokens of a tile of rows, and of a block
-  const int segs = a.num_groups + a.num_seqs;
+  const int segs = a.num_groups + a.num_seqs, cta = int(blockIdx.x), ctas = int(gridDim.x);
   const int per = (segs + C::THREADS - 1) / C::THREADS;
   const int run0 = min(segs, tid * per), run1 = min(segs, run0 + per);
-  auto segment_cost = [&](const PromptSegment& g) {
-    return g.nq ? prompt_cost(a, g, (g.nq + TB - 1) / TB, TB) * a.num_kv_heads : 0ll;
-  };
-  long long mine = 0;
-  for (int i = run0; i < run1; ++i) {
-    if (blockIdx.x == 0) {
-      const int s = i - a.num_groups;
-      if (s >= 0 && (a.context_lens[s] < 0 || a.context_lens[s] > a.max_blocks_per_seq * kBlock))
-        flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-      const int32_t* starts = a.query_starts ? a.query_starts : i < a.num_groups ? a.group_starts : nullptr;
-      if (starts && (starts[i] < 0 || starts[i + 1] < starts[i] || starts[i + 1] > a.num_tokens))
-        flag(a.status, PKV_DEV_BAD_START);
-    }
-    mine += segment_cost(prompt_segment(a, i));
-  }
-  long long upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(kFull, upto, o);
-    if (lane >= o) upto += x;
-  }
-  if (lane == 31) sh.scan[warp] = upto;
-  __syncthreads();
-  long long before = upto - mine, total = 0;
-#pragma unroll
-  for (int i = 0; i < C::THREADS / 32; ++i) {
-    if (i < warp) before += sh.scan[i];
-    total += sh.scan[i];
-  }
-  const int cta = int(blockIdx.x), ctas = int(gridDim.x);
-  const long long begin = total * cta / ctas, end = total * (cta + 1) / ctas;
-  if (begin < end && begin >= before && begin < before + mine) {
-    long long at = before;
+  long long at = 0, begin = 0, end = 0, total = 0, quotient = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    PromptSegment g{};
     int i = run0;
-    for (;; ++i) {
-      const long long c = segment_cost(prompt_segment(a, i));
-      if (at + c > begin) break;
-      at += c;
+#pragma unroll 1
+    for (; i < run1; ++i) {
+      g = prompt_segment(a, i);
+      g.cost = g.nq ? prompt_cost(a, g, (g.nq + TB - 1) / TB, TB) : 0;
+      if (pass == 0 && cta == 0) {
+        const int s = i - a.num_groups;
+        if (s >= 0 && (a.context_lens[s] < 0 || a.context_lens[s] > a.max_blocks_per_seq * kBlock))
+          flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+        const int32_t* starts = a.query_starts ? a.query_starts : i < a.num_groups ? a.group_starts : nullptr;
+        if (starts && (starts[i] < 0 || starts[i + 1] < starts[i] || starts[i + 1] > a.num_tokens))
+          flag(a.status, PKV_DEV_BAD_START);
+      }
+      if (pass && at + g.cost * a.num_kv_heads > begin) break;
+      at += g.cost * a.num_kv_heads;
     }
-    sh.first_seg = i;
-    sh.first_base = at;
+    if (pass) {
+      sh.first_seg = i;
+      sh.first_base = at;
+      break;
+    }
+    if (per == 1 && run0 < run1) list[run0] = g;
+    long long upto = at;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) sh.scan[warp] = upto;
+    __syncthreads();
+    const long long mine = at;
+    at = upto - mine;
+#pragma unroll 1
+    for (int j = 0; j < C::THREADS / 32; ++j) {
+      if (j < warp) at += sh.scan[j];
+      total += sh.scan[j];
+    }
+    quotient = total >> 32 ? total / ctas : (long long)(unsigned(total) / unsigned(ctas));
+    const EvenSplit split(total, ctas, quotient);
+    begin = split.begin(cta);
+    end = split.begin(cta + 1);
+    if (begin >= end || begin < at || begin >= at + mine) break;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   volatile int* stop = &sh.stop;
-  auto wait = [&](uint64_t& bar, int phase) { return latent_wait(smem_addr(&bar), uint32_t(phase) & 1, stop, a.status); };
-
+  auto wait = [&](uint64_t& bar, int phase) { return prompt_wait(smem_addr(&bar), uint32_t(phase) & 1, stop, a.status); };
+  auto test = [&](uint64_t& bar, int phase) { return bool(__all_sync(kFull, mbar_test(smem_addr(&bar), uint32_t(phase) & 1))); };
+  // Tile n of the ring has landed (or, unless block, has not yet). Its slot's phase may be looked
+  // at only once its copy is issued, when the phase before is over: of tiles that the other
+  // warpgroup uses alone this one sees nothing.
+  int issued = 0;
+  auto landed = [&](int n, bool block) {
+    unsigned long long t0 = 0;
+    for (int polls = 0; issued <= n; ++polls) {
+      issued = __shfl_sync(kFull, lds_acquire(smem_addr(&sh.issued)), 0);
+      if (issued > n) break;
+      if (!block) return false;
+      if ((polls & 63) != 63) continue;
+      const unsigned long long now = __shfl_sync(kFull, global_timer_ns(), 0);
+      if (polls == 63) t0 = now;
+      if (__any_sync(kFull, *stop)) return false;
+      if (now - t0 > kWaitLimitNs) {
+        *stop = 1;
+        if (lane == 0) flag(a.status, PKV_DEV_WAIT_TIMEOUT);
+        return false;
+      }
+    }
+    uint64_t& bar = sh.slot_full[n % C::SLOTS];
+    return block ? wait(bar, n / C::SLOTS) : test(bar, n / C::SLOTS);
+  };
   if (warp == WARP_KV) {
     // ---- pieces, and the copies of K and V ----
-    const int snap = int(min((long long)kPromptSnap, total / ctas / 16));
+    const EvenSplit split(total, ctas, quotient);
+    const int snap = int(min((long long)kPromptSnap, quotient / 16));
     // generator of pieces
     int seg = sh.first_seg, cached = -64, h = 0, rb = 0, blocks = 0;
-    long long seg_base = sh.first_base, item = 0, per_head = 0;
+    long long seg_base = sh.first_base, item = 0;
     PromptSegment g{}, mine_g{};
     bool open = false;     // g, h, rb, item name the next item
     bool links = false, continued = false;  // what is written to desc
@@ -352,35 +481,52 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
             p.tiles = -1;
             return;
           }
-          if (seg - cached >= 32) {  // the next 32 segments, one a lane
-            cached = seg;
-            if (seg + lane < segs) mine_g = prompt_segment(a, seg + lane);
+          if (per == 1) {
+            g = list[seg];
+          } else {
+            if (seg - cached >= 32) {  // the next 32 segments, one a lane
+              cached = seg;
+              if (seg + lane < segs) {
+                mine_g = prompt_segment(a, seg + lane);
+                mine_g.cost = mine_g.nq ? prompt_cost(a, mine_g, (mine_g.nq + TB - 1) / TB, TB) : 0;
+              }
+            }
+            const int src = seg - cached;
+            g.q0 = __shfl_sync(kFull, mine_g.q0, src);
+            g.nq = __shfl_sync(kFull, mine_g.nq, src);
+            g.table = __shfl_sync(kFull, mine_g.table, src);
+            g.lo = __shfl_sync(kFull, mine_g.lo, src);
+            g.len = __shfl_sync(kFull, mine_g.len, src);
+            g.kind = __shfl_sync(kFull, mine_g.kind, src);
+            g.cost = __shfl_sync(kFull, mine_g.cost, src);
           }
-          const int src = seg - cached;
-          g.q0 = __shfl_sync(kFull, mine_g.q0, src);
-          g.nq = __shfl_sync(kFull, mine_g.nq, src);
-          g.table = __shfl_sync(kFull, mine_g.table, src);
-          g.lo = __shfl_sync(kFull, mine_g.lo, src);
-          g.len = __shfl_sync(kFull, mine_g.len, src);
-          g.kind = __shfl_sync(kFull, mine_g.kind, src);
           ++seg;
           if (g.nq == 0) continue;
           blocks = (g.nq + TB - 1) / TB;
-          per_head = prompt_cost(a, g, blocks, TB);
           h = rb = 0;
           item = seg_base;
           if (begin > seg_base) {  // the share begins inside
-            h = int((begin - seg_base) / per_head);
-            const long long rest = begin - seg_base - h * per_head;
+            h = min(a.num_kv_heads - 1, int(float(begin - seg_base) / float(g.cost)));
+            while (h > 0 && h * g.cost > begin - seg_base) --h;  // (but for the quotient's rounding)
+            while (h + 1 < a.num_kv_heads && (h + 1) * g.cost <= begin - seg_base) ++h;
+            item += h * g.cost;
+            const long long rest = begin - item;
+            long long before = 0;
             int top = blocks - 1;
+#pragma unroll 1
             while (rb < top) {
               const int mid = (rb + top + 1) >> 1;
-              if (prompt_cost(a, g, mid, TB) <= rest) rb = mid;
-              else top = mid - 1;
+              const long long c = prompt_cost(a, g, mid, TB);
+              if (c <= rest) {
+                rb = mid;
+                before = c;
+              } else {
+                top = mid - 1;
+              }
             }
-            item = seg_base + h * per_head + prompt_cost(a, g, rb, TB);
+            item += before;
           }
-          seg_base += per_head * a.num_kv_heads;
+          seg_base += g.cost * a.num_kv_heads;
           open = true;
         }
         if (item >= end) {
@@ -409,11 +555,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
         if (lane == 0) {
           // the shares that hold the rest: up to the one with the item's end
           int last = cta;
-          if (!whole && t0 == 0) {
-            last = int((start + cost - 1) * ctas / total);
-            while (last + 1 < ctas && total * (last + 1) / ctas <= start + cost - 1) ++last;
-            while (total * last / ctas > start + cost - 1) --last;
-          }
+          if (!whole && t0 == 0) last = split.of(start + cost - 1);
           if (a.query_starts) {
             if (!whole && t0 == 0) {
               a.desc[cta] = make_int4(p.q0, p.tokens, p.head, last);
@@ -439,60 +581,69 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
       flag(a.status, PKV_DEV_BAD_BLOCK_ID);
       return 0;
     };
-    auto set_table = [&](const PromptPiece& p) {
-      row = a.block_tables + size_t(table) * a.max_blocks_per_seq;
-      nb = (p.hi + kBlock - 1) / kBlock;
-    };
-    PromptPiece p, next;
+    PromptPiece p{}, next;
     bool ok = true;  // warp-uniform
     int n = 0;       // tiles (K or V) copied
-    int count = 0;   // pieces
-    generate(p);
-    set_table(p);
-    int first_ids = p.tiles > 0 ? load_ids(p.kv0 / kBlock) : 0;
-    for (;;) {
-      if (count >= kPromptPieces) ok = __all_sync(kFull, wait(sh.piece_empty[count % kPromptPieces], count / kPromptPieces - 1));
-      if (!ok) break;
-      if (lane == 0) {
-        sh.piece[count % kPromptPieces] = p;
-        mbar_arrive(smem_addr(&sh.piece_full[count % kPromptPieces]));
-      }
-      ++count;
-      if (p.tiles < 0) break;
-      // the next piece, and its first block ids on their way
-      const int32_t* const this_row = row;
-      const int this_nb = nb;
-      generate(next);
-      set_table(next);
-      const int next_ids = next.tiles > 0 ? load_ids(next.kv0 / kBlock) : 0;
-      const int32_t* const next_row = row;
-      const int next_nb = nb;
-      row = this_row;
-      nb = this_nb;
-      constexpr int B = C::TILE / kBlock;  // blocks of a tile
-      int from = p.kv0 / kBlock, ids = checked(first_ids, from + lane), ahead = p.tiles > 32 / B ? load_ids(from + 32) : 0;
-      for (int t = 0; ok && t < p.tiles; ++t) {
-        const int block = p.kv0 / kBlock + t * B;
-        if (block >= from + 32) {
-          from += 32;
-          ids = checked(ahead, from + lane);
-          ahead = load_ids(from + 32);
+    int given[2] = {0, 0};  // tiles that each warpgroup was given alone
+    constexpr int B = C::TILE / kBlock;  // blocks of a tile
+    int first_ids = 0;
+    for (int count = -1; ok && p.tiles >= 0; ++count) {
+      if (count >= 0) {
+        if (count >= kPromptPieces) ok = wait(sh.piece_empty[count % kPromptPieces], count / kPromptPieces - 1);
+        if (!ok) break;
+        const bool more = open ? item < end : seg < segs && seg_base < end;
+        if (C::GROUPS == 1) p.mode = kPieceFirst;
+        else if (p.tokens > TQ) p.mode = kPieceRows;
+        else if (p.tiles >= kPromptSplit || (p.tiles > 1 && !more)) p.mode = kPieceSplit;
+        else p.mode = given[1] < given[0] ? kPieceSecond : kPieceFirst;
+        if (p.mode == kPieceFirst) given[0] += p.tiles + 1;
+        if (p.mode == kPieceSecond) given[1] += p.tiles + 1;
+        if (lane == 0) {
+          sh.piece[count % kPromptPieces] = p;
+          mbar_arrive(smem_addr(&sh.piece_full[count % kPromptPieces]));
         }
-        int z[B];
-#pragma unroll
-        for (int j = 0; j < B; ++j) z[j] = 2 * (__shfl_sync(kFull, ids, block - from + j) * a.num_kv_heads + p.head);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int slot = n % C::SLOTS;
-          if (n >= C::SLOTS) ok = ok && __all_sync(kFull, wait(sh.slot_empty[slot], n / C::SLOTS - 1));
-          if (!ok) break;
-          if (elect_one()) {
-            const uint32_t bar = smem_addr(&sh.slot_full[slot]), dst = smem_addr(ring) + slot * C::SLOT;
-            mbar_arrive_expect_tx(bar, C::SLOT);
-#pragma unroll
-            for (int j = 0; j < B; ++j) tma_load_4d(dst + j * 2 * C::STEP, kv ? &v_map : &k_map, 0, 0, 0, z[j], bar);
+      }
+      int from = p.kv0 / kBlock, ids = checked(first_ids, from + lane), ahead = p.tiles > 32 / B ? load_ids(from + 32) : 0;
+      const int32_t* next_row = nullptr;
+      int next_nb = 0, next_ids = 0;
+#pragma unroll 1
+      for (int t = 0; t < max(1, p.tiles); ++t) {
+        if (t < p.tiles) {
+          const int block = p.kv0 / kBlock + t * B;
+          if (block >= from + 32) {
+            from += 32;
+            ids = checked(ahead, from + lane);
+            ahead = load_ids(from + 32);
           }
-          __syncwarp();
+          int z[B];
+#pragma unroll
+          for (int j = 0; j < B; ++j) z[j] = 2 * (__shfl_sync(kFull, ids, block - from + j) * a.num_kv_heads + p.head);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const int slot = n % C::SLOTS;
+            if (n >= C::SLOTS) ok = wait(sh.slot_empty[slot], n / C::SLOTS - 1);
+            if (!ok) break;
+            if (elect_one()) {
+              const uint32_t bar = smem_addr(&sh.slot_full[slot]), dst = smem_addr(ring) + slot * C::SLOT;
+              mbar_arrive_expect_tx(bar, C::SLOT);
+#pragma unroll
+              for (int j = 0; j < B; ++j) tma_load_4d(dst + j * 2 * C::STEP, kv ? &v_map : &k_map, 0, 0, 0, z[j], bar);
+              sts_release(smem_addr(&sh.issued), n + 1);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+        if (t == 0) {
+          // the next piece, and its first block ids on their way, once the first copies are
+          const int32_t* const this_row = row;
+          const int this_nb = nb;
+          generate(next);
+          row = next_row = a.block_tables + size_t(table) * a.max_blocks_per_seq;
+          nb = next_nb = (next.hi + kBlock - 1) / kBlock;
+          if (next.tiles > 0) next_ids = load_ids(next.kv0 / kBlock);
+          row = this_row;
+          nb = this_nb;
         }
       }
       if (!ok) break;
@@ -500,11 +651,17 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
       first_ids = next_ids;
       row = next_row;
       nb = next_nb;
+      if (p.tiles < 0) {  // the end is announced
+        ++count;
+        if (count >= kPromptPieces) ok = wait(sh.piece_empty[count % kPromptPieces], count / kPromptPieces - 1);
+        if (ok && lane == 0) {
+          sh.piece[count % kPromptPieces] = p;
+          mbar_arrive(smem_addr(&sh.piece_full[count % kPromptPieces]));
+        }
+      }
     }
-    if (lane == 0 && a.query_starts) {
-      if (!links) a.desc[cta] = make_int4(0, 0, 0, -1);
-      a.more[cta] = continued;
-    } else if (lane == 0) {
+    if (lane == 0) {
+      if (a.query_starts && !links) a.desc[cta] = make_int4(0, 0, 0, -1);
       a.more[cta] = continued;
     }
     if (*stop) {  // wait (bounded) for the copies in flight
@@ -512,107 +669,185 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
         if (n > i) mbar_wait_bounded(smem_addr(&sh.slot_full[i]), uint32_t((n - 1 - i) / C::SLOTS) & 1, 10000000ull);
     }
   } else if (warp == WARP_Q) {
-    // ---- copies of Q ----
-    int loads = 0;
-    for (int count = 0;; ++count) {
-      if (!__all_sync(kFull, wait(sh.piece_full[count % kPromptPieces], count / kPromptPieces))) break;
+    // ---- copies of Q: a tile of rows for each warpgroup that takes the piece ----
+    int loads[2] = {0, 0};
+    bool ok = true;
+    for (int count = 0; ok; ++count) {
+      ok = wait(sh.piece_full[count % kPromptPieces], count / kPromptPieces);
+      if (!ok) break;
       const PromptPiece p = sh.piece[count % kPromptPieces];
       if (p.tiles < 0) break;
-      if (p.tiles > 0) {
-        if (loads > 0 && !__all_sync(kFull, wait(sh.q_empty, loads - 1))) break;
-        ++loads;
+      for (int w = 0; ok && w < C::GROUPS; ++w) {
+        if (p.tiles == 0 || !PieceTiles(p.mode, p.tiles, w).any) continue;
+        if (loads[w] > 0) ok = wait(sh.q_empty[w], loads[w] - 1);
+        if (!ok) break;
+        ++loads[w];
         if (elect_one()) {
-          const int tiles = p.tokens > TQ ? 2 : 1;
-          mbar_arrive_expect_tx(smem_addr(&sh.q_full), uint32_t(tiles * C::CHUNKS * TQ * a.group * 128));
-          for (int t = 0; t < tiles; ++t)
+          const int from = p.mode == kPieceRows ? w * TQ : 0, tokens = min(TQ, p.tokens - from);
+          const uint32_t bar = smem_addr(&sh.q_full[w]), dst = smem_addr(q_mem) + w * C::Q_TILE;
+          // (rows that no copy writes hold what they held: their scores are not used)
+          if (tokens == 1) {
+            mbar_arrive_expect_tx(bar, uint32_t(C::CHUNKS * a.group * 128));
             for (int c = 0; c < C::CHUNKS; ++c)
-              tma_load_4d(smem_addr(q_mem) + t * C::Q_TILE + c * (128 * 128), &q_map, 0, p.head * a.group, p.q0 + t * TQ, c,
-                          smem_addr(&sh.q_full));
+              tma_load_4d(dst + c * (128 * 128), &q1_map, 0, p.head * a.group, p.q0 + from, c, bar);
+          } else {
+            mbar_arrive_expect_tx(bar, uint32_t(C::CHUNKS * TQ * a.group * 128));
+            for (int c = 0; c < C::CHUNKS; ++c)
+              tma_load_4d(dst + c * (128 * 128), &q_map, 0, p.head * a.group, p.q0 + from, c, bar);
+          }
         }
+        __syncwarp();
       }
-      __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&sh.piece_empty[count % kPromptPieces]));
     }
-    if (*stop && loads > 0) mbar_wait_bounded(smem_addr(&sh.q_full), uint32_t(loads - 1) & 1, 10000000ull);
-  } else if (warp == WARP_MMA) {
-    // ---- MMA issue: one lane ----
-    if (elect_one()) {
-      constexpr uint32_t id_s = tc_idesc<T>(128, C::TILE, false), id_o = tc_idesc<T>(128, D, false) | (1u << 16);
-      const uint64_t q_desc = tc_desc(smem_addr(q_mem), 16, 1024);
-      const uint64_t k_desc = tc_desc(smem_addr(ring), 16, C::STEP), v_desc = tc_desc(smem_addr(ring), 1024, C::STEP);
-      int n0 = 0, loads = 0, weights[2] = {0, 0};
-      bool ok = true;
-      for (int count = 0; ok; ++count) {
-        ok = wait(sh.piece_full[count % kPromptPieces], count / kPromptPieces);
-        if (!ok) break;
-        const int tiles = sh.piece[count % kPromptPieces].tiles;
-        const bool rows = C::GROUPS == 2 && sh.piece[count % kPromptPieces].tokens > TQ;  // two tiles of rows
-        if (tiles < 0) break;
-        mbar_arrive(smem_addr(&sh.piece_empty[count % kPromptPieces]));
-        if (tiles == 0) continue;
-        ok = wait(sh.q_full, loads++);
-        const int steps = rows ? 2 * tiles : tiles;
-        auto scores = [&](int j) {
-          const int i = rows ? j >> 1 : j, half = rows ? j & 1 : 0, b = j & 1, n = n0 + 2 * i, slot = n % C::SLOTS;
-          if (half == 0) ok = ok && wait(sh.slot_full[slot], n / C::SLOTS);
-          if (!ok) return;
-          tc_fence_after();
-          const uint64_t q = q_desc + half * (C::Q_TILE >> 4), k = k_desc + slot * (C::SLOT >> 4);
-#pragma unroll
+    if (*stop)
+      for (int w = 0; w < C::GROUPS; ++w)
+        if (loads[w] > 0) mbar_wait_bounded(smem_addr(&sh.q_full[w]), uint32_t(loads[w] - 1) & 1, 10000000ull);
+  } else if (warp >= WARP_MMA && warp < WARP_MMA + C::GROUPS) {
+    // ---- MMA issue: a warp for each warpgroup ----
+    // As soon as the weights are there O += P V, and right behind it S of the next tile (of the
+    // next piece, too). The two warps issue by turns (`lock`), so that while one warpgroup has
+    // its products made the other makes weights: side by side both would wait for both. One lane
+    // issues, the others keep step, so that all of it stays in uniform registers. What the next
+    // products need besides the weights is looked at before these are awaited.
+    const int w = warp - WARP_MMA;
+    constexpr uint32_t id_s = tc_idesc<T>(128, C::TILE, false), id_o = tc_idesc<T>(128, D, false) | (1u << 16);
+    const uint64_t q_desc = tc_desc(smem_addr(q_mem) + w * C::Q_TILE, 16, 1024);
+    const uint64_t k_desc = tc_desc(smem_addr(ring), 16, C::STEP), v_desc = tc_desc(smem_addr(ring), 1024, C::STEP);
+    int count = 0, n0 = 0, behind = 0;  // pieces looked at, ring index of the piece's first tile, its tiles
+    int i = 0, tiles = 0, step = 1;     // the next KV tile of the piece
+    bool rows = false, fresh = false, done = false;
+    int loads = 0, s = 0, o = 0;        // Qs waited for; S and O issued
+    int v0 = 0, v1 = 0;                 // of the S whose O is to come, the older first: V's ring index x 8 + (last of its
+                                        // piece) x 4 + (the other warpgroup uses it too) x 2 + first
+    auto reached = [&](uint64_t& bar, int phase, bool block) { return block ? wait(bar, phase) : test(bar, phase); };
+    // Whether (block: waits until) all that S of the next tile needs is there.
+    auto next_there = [&](bool block) {
+      while (i >= tiles) {  // the next piece
+        if (!reached(sh.piece_full[count % kPromptPieces], count / kPromptPieces, block)) return false;
+        const PromptPiece& p = sh.piece[count % kPromptPieces];
+        const int all = __shfl_sync(kFull, p.tiles, 0), mode = __shfl_sync(kFull, p.mode, 0);
+        if (all < 0) {
+          done = true;
+          return false;
+        }
+        if (elect_one()) mbar_arrive(smem_addr(&sh.piece_empty[count % kPromptPieces]));
+        ++count;
+        n0 += 2 * behind;
+        behind = all;
+        const PieceTiles mine(mode, all, w);
+        i = mine.first;
+        step = mine.step;
+        tiles = mine.any ? all : 0;
+        rows = mode == kPieceRows;
+        fresh = true;
+      }
+      return landed(n0 + 2 * i, block) && (!fresh || reached(sh.q_full[w], loads, block));
+    };
+    bool k_there = false;
+    for (;;) {
+      if (!done && !k_there) k_there = next_there(s == o);
+      bool outputs = false;
+      if (s > o && !(C::DEPTH == 2 && k_there && s < o + 2)) {
+        const int b = C::GROUPS == 2 ? w : o & 1;
+        outputs = landed(v0 >> 3, true) && wait(sh.p_full[b], C::GROUPS == 2 ? o : o >> 1);
+        if (!outputs) break;
+        if (!done && !k_there) k_there = next_there(false);
+      }
+      const bool scores = k_there;
+      if (!outputs && !scores) {
+        if (done || __any_sync(kFull, *stop)) break;
+        continue;
+      }
+      const int slot_o = (v0 >> 3) % C::SLOTS, bo = C::GROUPS == 2 ? w : o & 1;
+      const int ns = n0 + 2 * i, slot_s = ns % C::SLOTS, bs = C::GROUPS == 2 ? w : s & 1;
+      const bool last = i + step >= tiles;
+      tc_fence_after();
+      if (elect_one()) {
+        if (C::GROUPS == 2) {  // (what holds it only issues: a bounded number of tries is enough, and no turn is needed to be right)
+          for (int tries = 0; tries < 4096 && atomicExch(&sh.lock, 1); ++tries) {}
+        }
+        if (outputs) {
+          const uint32_t p = tmem + C::S_AT + bo * C::TILE;
+          const uint64_t d = v_desc + slot_o * (C::SLOT >> 4);
+#pragma unroll 1
+          for (int e = 0; e < C::TILE / 16; ++e)
+            tc_mma_ts(tmem + w * D, p + 8 * e, d + e * (2 * C::STEP >> 4), id_o, !((v0 & 1) && e == 0));
+          // (with two S buffers a move of the reference asks for it at any tile)
+          if (C::GROUPS == 1 || (v0 & 4)) tc_commit(smem_addr(&sh.pv_done[bo]));
+          tc_commit(smem_addr(&sh.slot_empty[slot_o]));
+          if (!(v0 & 2)) tc_commit(smem_addr(&sh.slot_empty[slot_o]));  // (for both)
+        }
+        if (scores) {
+          const uint64_t k = k_desc + slot_s * (C::SLOT >> 4);
+          const uint32_t d = tmem + C::S_AT + bs * C::TILE;
+#pragma unroll 1
           for (int c = 0; c < C::CHUNKS; ++c)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              tc_mma(tmem + C::S_AT + b * C::TILE, q + c * (128 * 128 >> 4) + 2 * e, k + c * (1024 >> 4) + 2 * e, id_s, c + e > 0);
-          tc_commit(smem_addr(&sh.s_full[b]));
-          if (!rows || half == 1) tc_commit(smem_addr(&sh.slot_empty[slot]));
-          if (j == steps - 1) tc_commit(smem_addr(&sh.q_empty));
-        };
-        scores(0);
-        if (ok && steps > 1) scores(1);
-        for (int j = 0; ok && j < steps; ++j) {
-          const int i = rows ? j >> 1 : j, half = rows ? j & 1 : 0, b = j & 1, n = n0 + 2 * i + 1, slot = n % C::SLOTS;
-          ok = wait(sh.p_full[b], weights[b]++);
-          if (half == 0) ok = ok && wait(sh.slot_full[slot], n / C::SLOTS);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t o = tmem + (C::GROUPS == 2 ? b * D : 0), w = tmem + C::S_AT + b * C::TILE;
-          const bool fresh = C::GROUPS == 2 ? j < 2 : j == 0;
-          const uint64_t v = v_desc + slot * (C::SLOT >> 4);
-#pragma unroll
-          for (int e = 0; e < C::TILE / 16; ++e) tc_mma_ts(o, w + 8 * e, v + e * (2 * C::STEP >> 4), id_o, !(fresh && e == 0));
-          tc_commit(smem_addr(&sh.pv_done[b]));
-          if (!rows || half == 1) tc_commit(smem_addr(&sh.slot_empty[slot]));
-          if (j + 2 < steps) scores(j + 2);
+              tc_mma(d, q_desc + c * (128 * 128 >> 4) + 2 * e, k + c * (1024 >> 4) + 2 * e, id_s, c + e > 0);
+          tc_commit(smem_addr(&sh.s_full[bs]));
+          tc_commit(smem_addr(&sh.slot_empty[slot_s]));
+          if (!rows) tc_commit(smem_addr(&sh.slot_empty[slot_s]));
+          if (last) tc_commit(smem_addr(&sh.q_empty[w]));
         }
-        n0 += 2 * tiles;
+        if (C::GROUPS == 2) atomicExch(&sh.lock, 0);
       }
-      if (*stop) {  // let the products in flight end before the tensor memory is freed
-        const uint32_t bar = smem_addr(&sh.drain);
-        mbar_init(bar, 1);
-        mbar_init_fence();
-        tc_commit(bar);
-        mbar_wait_bounded(bar, 0, 10000000ull);
+      __syncwarp();
+      if (outputs) {
+        v0 = v1;
+        ++o;
+      }
+      if (scores) {
+        (s == o ? v0 : v1) = (ns + 1) * 8 + (last ? 4 : 0) + (rows ? 2 : 0) + (fresh ? 1 : 0);
+        loads += fresh ? 1 : 0;
+        fresh = k_there = false;
+        i += step;
+        ++s;
       }
     }
+    if (__any_sync(kFull, *stop) && elect_one()) {  // let the products in flight end before the tensor memory is freed
+      const uint32_t bar = smem_addr(&sh.drain[w]);
+      mbar_init(bar, 1);
+      mbar_init_fence();
+      tc_commit(bar);
+      mbar_wait_bounded(bar, 0, 10000000ull);
+    }
     __syncwarp();
-  } else {
+  } else if (warp < C::SOFTMAX / 32) {
     // ---- softmax and output: a thread a row ----
     constexpr float kHeadroom = std::is_same<T, __half>::value ? kPromptHeadroom : 0.f;
     const int wg = warp >> 2, quarter = warp & 3, r = 32 * quarter + lane;
     const int tok = r / a.group, sub = r - tok * a.group;  // token of the tile, head of the group
     const uint32_t lanes = uint32_t(32 * quarter) << 16;
-    const uint32_t s_base = tmem + C::S_AT + lanes;
-    int steps_done[2] = {0, 0};  // on each S (this warpgroup's, but for head_dim 256)
-    int n0 = 0, joins = 0;
-    for (int count = 0;; ++count) {
-      if (!__all_sync(kFull, wait(sh.piece_full[count % kPromptPieces], count / kPromptPieces))) break;
-      const PromptPiece p = sh.piece[count % kPromptPieces];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.piece_empty[count % kPromptPieces]));
+    // The score's factor is taken in on the way to the exponent; one that is not positive before
+    // the maximum.
+    const bool scaled = !(a.scale_log2 > 0.f);
+    const float factor = scaled ? 1.f : a.scale_log2;
+    int steps = 0, n0 = 0, joins = 0, ends = 0;  // tiles done; ring index of the piece's first tile; pieces waited for
+    // While the first pieces are worked out these warps run their code once over what tensor
+    // memory holds, without waits, signals or results: what an SM has not run yet it fetches line
+    // by line, which took the first tile 4 us.
+    for (int count = -1;; ++count) {
+      const bool dry = count < 0;
+      PromptPiece p{};
+      if (dry) {
+        p.tiles = p.hi = 1 << 20;
+        p.mode = wg;
+        p.slot = kPromptNone;
+      } else {
+        if (!wait(sh.piece_full[count % kPromptPieces], count / kPromptPieces)) break;
+        p = sh.piece[count % kPromptPieces];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.piece_empty[count % kPromptPieces]));
+      }
       if (p.tiles < 0) break;
-      const bool rows = C::GROUPS == 2 && p.tokens > TQ;
+      const PieceTiles share(p.mode, p.tiles, wg);
+      n0 += dry ? 0 : 2 * p.tiles;
+      if (!share.any) continue;
+      const bool rows = p.mode == kPieceRows;
       const int token = tok + (rows ? wg * TQ : 0);
-      const bool valid = tok < TQ && token < p.tokens;
+      const bool valid = tok < TQ && token < p.tokens;  // (dry: none)
       int rlo = 0, rhi = 0x7fffffff;  // positions that this row sees
       if (valid) {
         rlo = p.lo;
@@ -625,76 +860,89 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
         }
       }
       float m = -INFINITY, l = 0.f;
-      // this warpgroup's KV tiles: all of them, or every other one
-      const int stride = rows || C::GROUPS == 1 ? 1 : 2;
       bool ok = true;
-      for (int i = rows || C::GROUPS == 1 ? 0 : wg; i < p.tiles; i += stride) {
-        const int b = C::GROUPS == 2 ? wg : i & 1;
-        ok = __all_sync(kFull, wait(sh.s_full[b], steps_done[b]));
+      for (int i = share.first; i < p.tiles; i += share.step, ++steps) {
+        const int b = C::GROUPS == 2 ? wg : steps & 1;
+        if (!dry) ok = wait(sh.s_full[b], C::GROUPS == 2 ? steps : steps >> 1);
         if (!ok) break;
-        ++steps_done[b];
         tc_fence_after();
-        const uint32_t s_at = s_base + b * C::TILE;
-        float x[C::TILE];
-#pragma unroll
-        for (int c = 0; c < C::TILE; c += 32) tc_ld_32x32(s_at + c, x + c);
-        tc_loaded(x);
+        // (dry: where O will be, which nothing else touches before this warpgroup's first weights)
+        const uint32_t s_at = tmem + lanes + (dry ? wg * D : C::S_AT + b * C::TILE);
         const int c0 = p.kv0 + i * C::TILE;
+        // First the maximum, 32 columns at a time; masked scores are written back. (All loops
+        // stay rolled: unrolled over the tile the code passed what an SM keeps at hand, and every
+        // warp waited for instructions, the MMA warps among them.)
+        const bool mask = !dry && (__any_sync(kFull, c0 + C::TILE > rhi || c0 < rlo) || scaled);
         float top = -INFINITY;
-        if (__any_sync(kFull, c0 < rlo || c0 + C::TILE > rhi)) {
-          const int from = rlo - c0, upto = rhi - c0;
+#pragma unroll 1
+        for (int h = 0; h < C::TILE; h += 32) {
+          float x[32];
+          tc_ld_32x32(s_at + h, x);
+          tc_loaded(x);
+          if (mask) {
+            const uint32_t seen = bits_below(rhi - c0 - h) & ~bits_below(rlo - c0 - h);
 #pragma unroll
-          for (int c = 0; c < C::TILE; ++c) {
-            x[c] = c >= from && c < upto ? x[c] * a.scale_log2 : -INFINITY;
-            top = fmaxf(top, x[c]);
+            for (int c = 0; c < 32; ++c) x[c] = (seen >> c) & 1u ? x[c] * (scaled ? a.scale_log2 : 1.f) : -INFINITY;
+            tc_st_32x16(s_at + h, reinterpret_cast<uint32_t*>(x));
+            tc_st_32x16(s_at + h + 16, reinterpret_cast<uint32_t*>(x + 16));
           }
-        } else {
+          float tops[4] = {top, x[0], x[1], x[2]};
 #pragma unroll
-          for (int c = 0; c < C::TILE; ++c) {
-            x[c] *= a.scale_log2;
-            top = fmaxf(top, x[c]);
-          }
+          for (int c = 3; c < 27; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], x[c + e], x[c + 4 + e]);
+          tops[0] = max3(tops[0], x[27], x[28]);
+          tops[1] = max3(tops[1], x[29], x[30]);
+          top = max3(max3(tops[0], tops[1], tops[2]), tops[3], x[31]);
         }
+        if (mask) tc_wait_st();
+        top *= factor;
         if (__any_sync(kFull, top > m + kPromptLazy)) {
           const float now = fmaxf(m, top), al = m == -INFINITY ? 0.f : fast_exp2(m - now);
           m = now;
           l *= al;
-          if (i >= stride) {  // (all of this O's products so far are done: S came after them; but for head_dim 256)
-            if (C::GROUPS == 1) ok = __all_sync(kFull, wait(sh.pv_done[b ^ 1], steps_done[b ^ 1] - 1));
+          if (i > share.first) {  // (all of this O's products so far are done: S came after them; but for head_dim 256)
+            if (C::GROUPS == 1) ok = wait(sh.pv_done[b ^ 1], (steps - 1) >> 1);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t o_at = tmem + lanes + (C::GROUPS == 2 ? wg * D : 0);
+            const uint32_t o_at = tmem + lanes + wg * D;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tc_ld_32x32(o_at + c, o);
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tc_ld_32x16(o_at + c, o);
               tc_loaded(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= al;
-              tc_st_32x32(o_at + c, reinterpret_cast<uint32_t*>(o));
+              for (int e = 0; e < 16; ++e) o[e] *= al;
+              tc_st_32x16(o_at + c, reinterpret_cast<uint32_t*>(o));
             }
           }
         }
-        const float ref = (m == -INFINITY ? 0.f : m) - kHeadroom;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        // Then the weights: those of 32 columns take 16, where scores already read were.
+        const float ref = kHeadroom - (m == -INFINITY ? 0.f : m);
+        const unsigned long long ref2 = pair(ref, ref), factor2 = pair(factor, factor);
+        unsigned long long sum[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int h = 0; h < C::TILE; h += 32) {
+          float x[32];
+          tc_ld_32x32(s_at + h, x);
+          tc_loaded(x);
+          uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < C::TILE; c += 64) {
-          uint32_t w[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            w[e] = pack2<T>(fast_exp2(x[c + 2 * e] - ref), fast_exp2(x[c + 2 * e + 1] - ref));
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = unpair(fma2(pair(x[2 * e], x[2 * e + 1]), factor2, ref2));
+            w[e] = pack2<T>(fast_exp2(y.x), fast_exp2(y.y));
             const float2 f = unpack2<T>(w[e]);
-            sum[2 * (e & 1)] += f.x;
-            sum[2 * (e & 1) + 1] += f.y;
+            sum[e & 1] = add2(sum[e & 1], pair(f.x, f.y));
           }
-          tc_st_32x32(s_at + c / 2, w);
+          tc_st_32x16(s_at + h / 2, w);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float2 sums = unpair(add2(sum[0], sum[1]));
+        l += sums.x + sums.y;
         if (c0 < p.lo || c0 + C::TILE > p.hi) {
           // rows that no query sees hold whatever the block holds (NaN included): as values
           // they must be zeros
-          const int n = n0 + 2 * i + 1, slot = n % C::SLOTS;
-          ok = __all_sync(kFull, wait(sh.slot_full[slot], n / C::SLOTS));
+          const int n = n0 - 2 * (p.tiles - i) + 1, slot = n % C::SLOTS;
+          ok = landed(n, true);
           if (!ok) break;
           const int low = max(0, p.lo - c0), high = prompt_clamp(p.hi - c0, 0, C::TILE), held = min(C::TILE, (high + kBlock - 1) / kBlock * kBlock);
           for (int e = tid & 127; e < (low + held - high) * (D / 8); e += 128) {
@@ -705,17 +953,15 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         tc_wait_st();
+        if (dry) break;
         tc_fence_before();
         mbar_arrive(smem_addr(&sh.p_full[b]));
       }
       if (!ok) break;
-      const bool joint = C::GROUPS == 2 && !rows && p.tiles > 1;
-      const bool idle = C::GROUPS == 2 && !rows && p.tiles <= 1 && wg == 1;  // nothing to do but to keep count
-      n0 += 2 * p.tiles;
-      if (idle) continue;
-      if (p.tiles > 0) {
-        const int b = C::GROUPS == 2 ? wg : (p.tiles - 1) & 1;
-        if (!__all_sync(kFull, wait(sh.pv_done[b], steps_done[b] - 1))) break;
+      const bool joint = p.mode == kPieceSplit;  // (which has two tiles at least)
+      if (p.tiles > 0 && !dry) {
+        const int last = steps - 1, b = C::GROUPS == 2 ? wg : last & 1;
+        if (!wait(sh.pv_done[b], C::GROUPS == 2 ? ends++ : last >> 1)) break;
         tc_fence_after();
       }
       float mine_f = 1.f, other_f = 0.f;  // factors of this warpgroup's O and of the other's
@@ -723,7 +969,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
         stats[wg * 128 + r] = make_float2(m, l);
         tc_fence_before();
         mbar_arrive(smem_addr(&sh.join));
-        if (!__all_sync(kFull, wait(sh.join, joins++))) break;
+        if (!wait(sh.join, joins++)) break;
         tc_fence_after();
         const float2 o = stats[(wg ^ 1) * 128 + r];
         const float now = fmaxf(m, o.x);
@@ -743,40 +989,60 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
         part_row = p.slot == kPromptNone
                        ? a.slot_rows * size_t(2) * ctas + size_t(p.kind == kRowsMembers ? 0 : 1) * a.num_seqs * a.num_q_heads + out_row
                        : size_t(p.slot) * a.slot_rows + (rows ? wg * 128 : 0) + r;
-        if (valid && col0 == 0) a.part_ml[part_row] = make_float2(m, l);
+        if (valid && (col0 == 0)) a.part_ml[part_row] = make_float2(m, l);
       }
       const uint32_t o_at = tmem + lanes;
+      // Results go through shared memory, so that four lanes write 64 bytes of a row together:
+      // 16-byte column q of row r lies at column (q + r / 2) % 4. This lane then writes column
+      // lane % 4 of rows lane / 4 + 8 k.
+      unsigned char* const mine_s = stage + warp * C::STAGE;
+      int rows_at[4];
+      T* dst_at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        rows_at[k] = __shfl_sync(kFull, valid ? int(out_row) : -1, 8 * k + lane / 4);
+        dst_at[k] = static_cast<T*>(a.out) + size_t(max(0, rows_at[k])) * D + 8 * (lane & 3);
+      }
 #pragma unroll 1
       for (int c = col0; c < col0 + cols; c += 32) {
         float o[32];
         if (p.tiles > 0) {
-          tc_ld_32x32(o_at + (C::GROUPS == 2 ? wg * D : 0) + c, o);
-          tc_loaded(o);
+          tc_ld_32x32(o_at + wg * D + c, o);
           if (joint) {
             float q[32];
             tc_ld_32x32(o_at + (wg ^ 1) * D + c, q);
             tc_loaded(q);
+            tc_loaded(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = o[e] * mine_f + q[e] * other_f;
+          } else {
+            tc_loaded(o);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (!valid) continue;
         if (direct) {
-          T* dst = static_cast<T*>(a.out) + out_row * D + c;
+          uint4 u[4];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint4 u;
-            u.x = pack2<T>(o[e] * inv, o[e + 1] * inv);
-            u.y = pack2<T>(o[e + 2] * inv, o[e + 3] * inv);
-            u.z = pack2<T>(o[e + 4] * inv, o[e + 5] * inv);
-            u.w = pack2<T>(o[e + 6] * inv, o[e + 7] * inv);
-            if (l == 0.f) u = make_uint4(0u, 0u, 0u, 0u);  // (a row that sees nothing of what its tile holds)
-            *reinterpret_cast<uint4*>(dst + e) = u;
+          for (int k = 0; k < 4; ++k) {
+            const float* x = o + 8 * k;
+            u[k] = make_uint4(pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv),
+                              pack2<T>(x[4] * inv, x[5] * inv), pack2<T>(x[6] * inv, x[7] * inv));
           }
-        } else {
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(mine_s + lane * 64 + ((k + lane / 2) & 3) * 16) = u[k];
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int from = 8 * k + lane / 4;
+            u[k] = *reinterpret_cast<const uint4*>(mine_s + from * 64 + (((lane & 3) + from / 2) & 3) * 16);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) st_global_if(rows_at[k] >= 0, dst_at[k] + c, u[k]);
+        } else if (valid) {
           float* dst = a.part_o + part_row * D + c;
 #pragma unroll
           for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
@@ -785,7 +1051,7 @@ prompt_kernel(const PromptArgs a, const __grid_constant__ CUtensorMap q_map, con
       tc_fence_before();
       if (joint) {  // both are read: the next piece may write them
         mbar_arrive(smem_addr(&sh.join));
-        if (!__all_sync(kFull, wait(sh.join, joins++))) break;
+        if (!wait(sh.join, joins++)) break;
         tc_fence_after();
       }
     }
