@@ -70,7 +70,7 @@ struct PromptCfg {
   static constexpr int STEP = CHUNKS * 1024;          // bytes of 8 tokens
   static constexpr int S_AT = GROUPS * D;             // columns of tensor memory: O, then two S
   static constexpr int COLUMNS = 512;
-  static constexpr int LISTED = THREADS;              // segments that are kept in shared memory
+  static constexpr int LISTED = 384;                  // segments that are kept in shared memory
   static constexpr int STATS_AT = 1024, STAGE_AT = STATS_AT + 1024 * GROUPS, LIST_AT = STAGE_AT + STAGE * 4 * GROUPS;
   static constexpr int MISC = LIST_AT + LISTED * 32;
   static constexpr size_t SMEM_BYTES = 1024 + size_t(GROUPS) * Q_TILE + size_t(SLOTS) * SLOT + MISC;
@@ -197,7 +197,7 @@ struct PieceTiles {
 
 struct PromptShared {
   uint64_t slot_full[8], slot_empty[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], join;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], join, warm;
   uint64_t piece_full[kPromptPieces], piece_empty[kPromptPieces];
   uint64_t drain[2];  // after a wait gave up
   PromptPiece piece[kPromptPieces];
@@ -349,6 +349,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       mbar_init(smem_addr(&sh.pv_done[i]), 1);
     }
     mbar_init(smem_addr(&sh.join), C::SOFTMAX);
+    mbar_init(smem_addr(&sh.warm), C::SOFTMAX / 32);
 #pragma unroll 1
     for (int i = 0; i < kPromptPieces; ++i) {
       mbar_init(smem_addr(&sh.piece_full[i]), 1);
@@ -368,28 +369,34 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
   asm volatile("griddepcontrol.launch_dependents;");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // What an SM has not run yet it fetches line by line, some 30 cycles an instruction: cold, this
+  // kernel took 7 us to its first product. So the code is kept short, and while the list is made
+  // the softmax warps, and for the copying warp the one of Q, run theirs once without effect.
+  const bool scanner = warp >= C::SOFTMAX / 32 && warp != WARP_Q;
+  if (scanner) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // The list: each thread sums a run of segments, a scan of the sums gives every
-  // run's place, and the thread whose run holds this CTA's share's begin finds its
-  // segment (walking its run once more where it is longer than one).
-  // (Written to be short: an SM fetches code that it has not run yet at some 30 cycles an
-  // instruction, and all of this comes before the first copy.)
+  // The list: each thread of three warps sums a run of segments, a scan of the sums gives
+  // every run's place, and the thread whose run holds this CTA's share's begin finds its segment.
   const int TQ = a.tile_tokens, TB = TQ * C::GROUPS;  // tokens of a tile of rows, and of a block
   const int segs = a.num_groups + a.num_seqs, cta = int(blockIdx.x), ctas = int(gridDim.x);
-  const int per = (segs + C::THREADS - 1) / C::THREADS;
-  const int run0 = min(segs, tid * per), run1 = min(segs, run0 + per);
-  long long at = 0, begin = 0, end = 0, total = 0, quotient = 0;
+  const bool listed = segs <= C::LISTED;
+  long long begin = 0, end = 0, total = 0, quotient = 0;
+  if (scanner) {
+    const int part = warp == WARP_KV ? 0 : warp - WARP_MMA + 1, runner = part * 32 + lane;
+    const int per = (segs + 95) / 96, run0 = min(segs, runner * per), run1 = min(segs, run0 + per);
+    long long mine = 0;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    PromptSegment g{};
-    int i = run0;
-#pragma unroll 1
-    for (; i < run1; ++i) {
-      g = prompt_segment(a, i);
+    for (int i = run0; i < run1; ++i) {
+      PromptSegment g = prompt_segment(a, i);
       g.cost = g.nq ? prompt_cost(a, g, (g.nq + TB - 1) / TB, TB) : 0;
-      if (pass == 0 && cta == 0) {
+      mine += g.cost * a.num_kv_heads;
+      if (listed) list[i] = g;
+      if (cta == 0) {
         const int s = i - a.num_groups;
         if (s >= 0 && (a.context_lens[s] < 0 || a.context_lens[s] > a.max_blocks_per_seq * kBlock))
           flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
@@ -397,40 +404,41 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         if (starts && (starts[i] < 0 || starts[i + 1] < starts[i] || starts[i + 1] > a.num_tokens))
           flag(a.status, PKV_DEV_BAD_START);
       }
-      if (pass && at + g.cost * a.num_kv_heads > begin) break;
-      at += g.cost * a.num_kv_heads;
     }
-    if (pass) {
-      sh.first_seg = i;
-      sh.first_base = at;
-      break;
-    }
-    if (per == 1 && run0 < run1) list[run0] = g;
-    long long upto = at;
-#pragma unroll 1
+    long long upto = mine;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(kFull, upto, o);
       if (lane >= o) upto += x;
     }
-    if (lane == 31) sh.scan[warp] = upto;
-    __syncthreads();
-    const long long mine = at;
-    at = upto - mine;
-#pragma unroll 1
-    for (int j = 0; j < C::THREADS / 32; ++j) {
-      if (j < warp) at += sh.scan[j];
-      total += sh.scan[j];
-    }
+    if (lane == 31) sh.scan[part] = upto;
+    asm volatile("bar.sync 1, 96;" ::: "memory");
+    const long long s0 = sh.scan[0], s1 = sh.scan[1];
+    total = s0 + s1 + sh.scan[2];
+    long long at = upto - mine + (part > 0 ? s0 : 0) + (part > 1 ? s1 : 0);
     quotient = total >> 32 ? total / ctas : (long long)(unsigned(total) / unsigned(ctas));
     const EvenSplit split(total, ctas, quotient);
     begin = split.begin(cta);
     end = split.begin(cta + 1);
-    if (begin >= end || begin < at || begin >= at + mine) break;
+    if (begin < end && begin >= at && begin < at + mine) {
+      int i = run0;
+#pragma unroll 1
+      for (; i + 1 < run1; ++i) {
+        long long c;
+        if (listed) {
+          c = list[i].cost;
+        } else {
+          const PromptSegment g = prompt_segment(a, i);
+          c = g.nq ? prompt_cost(a, g, (g.nq + TB - 1) / TB, TB) : 0;
+        }
+        if (at + c * a.num_kv_heads > begin) break;
+        at += c * a.num_kv_heads;
+      }
+      sh.first_seg = i;
+      sh.first_base = at;
+    }
+    asm volatile("bar.sync 1, 96;" ::: "memory");
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
   volatile int* stop = &sh.stop;
   auto wait = [&](uint64_t& bar, int phase) { return prompt_wait(smem_addr(&bar), uint32_t(phase) & 1, stop, a.status); };
   auto test = [&](uint64_t& bar, int phase) { return bool(__all_sync(kFull, mbar_test(smem_addr(&bar), uint32_t(phase) & 1))); };
@@ -457,13 +465,19 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     uint64_t& bar = sh.slot_full[n % C::SLOTS];
     return block ? wait(bar, n / C::SLOTS) : test(bar, n / C::SLOTS);
   };
-  if (warp == WARP_KV) {
+  if (warp == WARP_KV || warp == WARP_Q) {
     // ---- pieces, and the copies of K and V ----
+    const bool dry = warp == WARP_Q;  // (only to have the code at hand: a made-up share, and no effect)
+    if (dry) {
+      begin = 3000;
+      end = total = 1 << 20;
+      quotient = 1 << 12;
+    }
     const EvenSplit split(total, ctas, quotient);
     const int snap = int(min((long long)kPromptSnap, quotient / 16));
     // generator of pieces
-    int seg = sh.first_seg, cached = -64, h = 0, rb = 0, blocks = 0;
-    long long seg_base = sh.first_base, item = 0;
+    int seg = dry ? 0 : sh.first_seg, cached = -64, h = 0, rb = 0, blocks = 0;
+    long long seg_base = dry ? 0 : sh.first_base, item = 0;
     PromptSegment g{}, mine_g{};
     bool open = false;     // g, h, rb, item name the next item
     bool links = false, continued = false;  // what is written to desc
@@ -481,7 +495,12 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             p.tiles = -1;
             return;
           }
-          if (per == 1) {
+          if (dry) {
+            g.nq = 5 * TB;
+            g.len = 2048;
+            g.kind = kRowsCausal;
+            g.cost = prompt_cost(a, g, 5, TB);
+          } else if (listed) {
             g = list[seg];
           } else {
             if (seg - cached >= 32) {  // the next 32 segments, one a lane
@@ -552,7 +571,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         p.kv0 = first + t0 * C::TILE;
         const bool whole = t1 - t0 == tiles;
         p.slot = whole ? kPromptNone : 2 * cta + (t0 == 0 ? 1 : 0);
-        if (lane == 0) {
+        if (lane == 0 && !dry) {
           // the shares that hold the rest: up to the one with the item's end
           int last = cta;
           if (!whole && t0 == 0) last = split.of(start + cost - 1);
@@ -639,6 +658,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           const int32_t* const this_row = row;
           const int this_nb = nb;
           generate(next);
+          if (dry) break;
           row = next_row = a.block_tables + size_t(table) * a.max_blocks_per_seq;
           nb = next_nb = (next.hi + kBlock - 1) / kBlock;
           if (next.tiles > 0) next_ids = load_ids(next.kv0 / kBlock);
@@ -646,7 +666,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           nb = this_nb;
         }
       }
-      if (!ok) break;
+      if (!ok || dry) break;
       p = next;
       first_ids = next_ids;
       row = next_row;
@@ -660,7 +680,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         }
       }
     }
-    if (lane == 0) {
+    if (lane == 0 && !dry) {
       if (a.query_starts && !links) a.desc[cta] = make_int4(0, 0, 0, -1);
       a.more[cta] = continued;
     }
@@ -668,8 +688,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       for (int i = 0; i < C::SLOTS; ++i)
         if (n > i) mbar_wait_bounded(smem_addr(&sh.slot_full[i]), uint32_t((n - 1 - i) / C::SLOTS) & 1, 10000000ull);
     }
-  } else if (warp == WARP_Q) {
+  }
+  if (warp == WARP_Q) {
     // ---- copies of Q: a tile of rows for each warpgroup that takes the piece ----
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int loads[2] = {0, 0};
     bool ok = true;
     for (int count = 0; ok; ++count) {
@@ -745,6 +767,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       return landed(n0 + 2 * i, block) && (!fresh || reached(sh.q_full[w], loads, block));
     };
     bool k_there = false;
+    if (!wait(sh.warm, 0)) done = true;  // (the softmax warps' trial uses S and O)
     for (;;) {
       if (!done && !k_there) k_there = next_there(s == o);
       bool outputs = false;
@@ -825,9 +848,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     const bool scaled = !(a.scale_log2 > 0.f);
     const float factor = scaled ? 1.f : a.scale_log2;
     int steps = 0, n0 = 0, joins = 0, ends = 0;  // tiles done; ring index of the piece's first tile; pieces waited for
-    // While the first pieces are worked out these warps run their code once over what tensor
-    // memory holds, without waits, signals or results: what an SM has not run yet it fetches line
-    // by line, which took the first tile 4 us.
     for (int count = -1;; ++count) {
       const bool dry = count < 0;
       PromptPiece p{};
@@ -848,6 +868,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       const bool rows = p.mode == kPieceRows;
       const int token = tok + (rows ? wg * TQ : 0);
       const bool valid = tok < TQ && token < p.tokens;  // (dry: none)
+      const bool busy = dry || __any_sync(kFull, valid);
       int rlo = 0, rhi = 0x7fffffff;  // positions that this row sees
       if (valid) {
         rlo = p.lo;
@@ -866,16 +887,16 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         if (!dry) ok = wait(sh.s_full[b], C::GROUPS == 2 ? steps : steps >> 1);
         if (!ok) break;
         tc_fence_after();
-        // (dry: where O will be, which nothing else touches before this warpgroup's first weights)
-        const uint32_t s_at = tmem + lanes + (dry ? wg * D : C::S_AT + b * C::TILE);
+        const uint32_t s_at = tmem + lanes + C::S_AT + b * C::TILE;
         const int c0 = p.kv0 + i * C::TILE;
         // First the maximum, 32 columns at a time; masked scores are written back. (All loops
         // stay rolled: unrolled over the tile the code passed what an SM keeps at hand, and every
         // warp waited for instructions, the MMA warps among them.)
-        const bool mask = !dry && (__any_sync(kFull, c0 + C::TILE > rhi || c0 < rlo) || scaled);
+        const bool mask = __any_sync(kFull, c0 + C::TILE > rhi || c0 < rlo) || scaled || dry;
         float top = -INFINITY;
+        const int columns = busy ? C::TILE : 0;  // (without a row of its own a warp only keeps step)
 #pragma unroll 1
-        for (int h = 0; h < C::TILE; h += 32) {
+        for (int h = 0; h < columns; h += 32) {
           float x[32];
           tc_ld_32x32(s_at + h, x);
           tc_loaded(x);
@@ -922,7 +943,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         const unsigned long long ref2 = pair(ref, ref), factor2 = pair(factor, factor);
         unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll 1
-        for (int h = 0; h < C::TILE; h += 32) {
+        for (int h = 0; h < columns; h += 32) {
           float x[32];
           tc_ld_32x32(s_at + h, x);
           tc_loaded(x);
@@ -1004,7 +1025,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         dst_at[k] = static_cast<T*>(a.out) + size_t(max(0, rows_at[k])) * D + 8 * (lane & 3);
       }
 #pragma unroll 1
-      for (int c = col0; c < col0 + cols; c += 32) {
+      for (int c = col0; c < (busy ? col0 + cols : 0); c += 32) {
         float o[32];
         if (p.tiles > 0) {
           tc_ld_32x32(o_at + wg * D + c, o);
@@ -1053,6 +1074,11 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         mbar_arrive(smem_addr(&sh.join));
         if (!wait(sh.join, joins++)) break;
         tc_fence_after();
+      }
+      if (dry) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&sh.warm));
+        asm volatile("griddepcontrol.wait;" ::: "memory");
       }
     }
   }
@@ -1109,12 +1135,13 @@ struct PromptJoin {
     }
   }
   // the pieces of a cut item: share `first` holds its start, the others up to `last` what `more` says
-  __device__ __forceinline__ void chain(const PromptArgs& a, int first, int last, int row, int lane) {
+  __device__ __forceinline__ void chain(const PromptArgs& a, bool live, int first, int last, int row, int lane) {
     first = max(0, min(first, a.shares - 1));
     last = max(first, min(last, a.shares - 1));
+#pragma unroll 1
     for (int c = first; c <= last; c += 32) {
       const int mine = c + lane;
-      const bool on = mine <= last && (mine == first || __ldcg(a.more + mine));
+      const bool on = live && mine <= last && (mine == first || __ldcg(a.more + mine));
       add(a, on, size_t(2 * mine + (mine == first ? 1 : 0)) * a.slot_rows + row, min(32, last - c + 1), lane);
     }
   }
@@ -1130,19 +1157,28 @@ struct PromptJoin {
   }
 };
 
-// Items that are cut: CTA (share, y) takes every gridDim.y-th eighth of the rows of the
-// one that starts in the share and goes on past it.
+// Both kernels are resident while the last one still runs, and go through their code once
+// without a piece before they wait for it: what an SM has not run yet it fetches line by line.
+
+// Items that are cut: the warps of CTAs (share, 0 ..) take the rows of the one that starts in
+// the share and goes on past it.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 d = __ldcg(a.desc + blockIdx.x);  // query token, tokens, KV head, last share
-  if (d.w < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = int(blockIdx.y) * 8 + warp; i < d.y * a.group; i += int(gridDim.y) * 8) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = int(blockIdx.y) * 8 + warp, step = int(gridDim.y) * 8;
+#pragma unroll 1
+  for (int i = first - step;; i += step) {  // (the first time without a piece)
+    const bool live = i >= 0;
+    int4 d = make_int4(0, 0, 0, -1);  // query token, tokens, KV head, last share
+    if (live) {
+      if (i == first) asm volatile("griddepcontrol.wait;" ::: "memory");
+      d = __ldcg(a.desc + blockIdx.x);
+      if (d.w < 0 || i >= d.y * a.group) return;
+    }
     const int token = i / a.group, sub = i - token * a.group, tile = token / a.tile_tokens;
     PromptJoin<T, D> j;
-    j.chain(a, int(blockIdx.x), d.w, tile * 128 + (token - tile * a.tile_tokens) * a.group + sub, lane);
-    j.write(a, size_t(d.x + token) * a.num_q_heads + d.z * a.group + sub, lane);
+    j.chain(a, live, int(blockIdx.x), d.w, tile * 128 + (token - tile * a.tile_tokens) * a.group + sub, lane);
+    if (live) j.write(a, size_t(d.x + token) * a.num_q_heads + d.z * a.group + sub, lane);
   }
 }
 
@@ -1150,25 +1186,39 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
 // prefix and its own.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
   if (row >= int64_t(a.num_seqs) * a.num_q_heads) return;
   const int s = int(row / a.num_q_heads), hq = int(row - int64_t(s) * a.num_q_heads), h = hq / a.group, sub = hq - h * a.group;
   const size_t whole = a.slot_rows * size_t(2) * a.shares;  // rows of items that are not cut: prefixes, then own parts
-  PromptJoin<T, D> j;
-  auto item = [&](int kind, int q0, int slot_row) {
-    const int2 link = __ldcg(a.link + (size_t(kind) * a.num_seqs + q0) * a.num_kv_heads + h);
-    if (link.x < 0) j.add(a, lane == 0, whole + (size_t(kind) * a.num_seqs + s) * a.num_q_heads + hq, 1, lane);
-    else j.chain(a, link.x, link.y, slot_row, lane);
-  };
-  int first, end;
-  if (prompt_group(a, s, &first, &end) >= 0) {
-    const int token = (s - first) % a.block_tokens, tile = token / a.tile_tokens;
-    item(0, s - token, tile * 128 + (token - tile * a.tile_tokens) * a.group + sub);
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    PromptJoin<T, D> j;
+    int first = s, end = s;
+    int2 link[2] = {make_int2(-1, -1), make_int2(-1, -1)};
+    int at = 0;
+    if (pass) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      const int2* const links = a.link + h;
+      link[1] = __ldcg(links + (size_t(a.num_seqs) + s) * a.num_kv_heads);
+      if (prompt_group(a, s, &first, &end) >= 0) {
+        const int token = (s - first) % a.block_tokens, tile = token / a.tile_tokens;
+        link[0] = __ldcg(links + size_t(s - token) * a.num_kv_heads);
+        at = tile * 128 + (token - tile * a.tile_tokens) * a.group + sub;
+      } else {
+        first = -1;
+      }
+    }
+#pragma unroll 1
+    for (int kind = first < 0 ? 1 : 0; kind < 2; ++kind) {
+      if (link[kind].x < 0)
+        j.add(a, pass && lane == 0, whole + (size_t(kind) * a.num_seqs + s) * a.num_q_heads + hq, 1, lane);
+      else
+        j.chain(a, pass, link[kind].x, link[kind].y, kind ? sub : at, lane);
+    }
+    if (pass) j.write(a, size_t(row), lane);
   }
-  item(1, s, sub);
-  j.write(a, size_t(row), lane);
 }
 
 }  // namespace pkv
