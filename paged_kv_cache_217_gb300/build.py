@@ -28,6 +28,7 @@ SOURCES = [
     "decode_f16.cu",
     "decode_bf16.cu",
     "decode_int8.cu",
+    "decode_tail.cu",
     "cache_ops.cu",
     "cache_int4.cu",
     "decode_int4.cu",

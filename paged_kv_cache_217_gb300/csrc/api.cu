@@ -1386,6 +1386,22 @@ pkv_status_t pkv_rotary_and_cache(void* q_out, const void* q, const void* k, con
 
 namespace {
 
+// Whether a decode grid takes part in a call of the prompt kernels (which give 128 rows to the 1
+// to 8 query heads of a single token): behind prefixes all that follows them, and in a batch with
+// fewer than two query tokens a sequence those that have one. Measured on GB300, with the grid and
+// without: a token of 24 sequences over 1500 cached ones, 20 heads of 64 (480 pairs of sequence
+// and KV head) 43 and 64 us, of 92 sequences 119 and 201; 64 sequences of 40 heads of 128 behind
+// 2000 tokens, 200 of their own 84 and 117; 64 sequences on 8 KV heads behind 512 tokens (512
+// pairs) with 60, 200 and 800 of their own 30, 44 and 90 and 35, 41 and 95. With fewer pairs than
+// fill the SMs three times a CTA a pair leaves SMs idle, and more CTAs a pair have to be joined:
+// 32 sequences (256 pairs), 200 of their own, 37 and 26.
+constexpr int64_t kTailPairs = 3 * 152;
+bool prompt_tails(const pkv::PromptArgs& a) {
+  if (a.num_q_heads / a.num_kv_heads > 8 || int64_t(a.num_seqs) * a.num_kv_heads < kTailPairs) return false;
+  if (a.query_starts && a.num_tokens >= 2 * int64_t(a.num_seqs)) return false;
+  return int64_t(a.num_blocks) * a.num_kv_heads * PKV_BLOCK_SIZE <= INT32_MAX;
+}
+
 // What both calls of the prompt kernels check, and their launch.
 pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, float scale, pkv_dtype_t dtype,
                          void* workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -1414,6 +1430,7 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
   if (!aligned(a.block_tables, 4) || !aligned(a.context_lens, 4) || !aligned(a.query_starts, 4) ||
       !aligned(a.group_starts, 4) || !aligned(a.prefix_blocks, 4))
     return pkv::fail(PKV_ERR_INVALID_ARG, "tables, lengths and starts must be 4-byte aligned");
+  a.tails = prompt_tails(a);
   const size_t need = pkv::prompt_workspace_bytes(a, head_dim);
   if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
     return pkv::fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) required, got %zu at %p",
@@ -1428,8 +1445,63 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
   if (st == PKV_OK) st = prompt_pool_map(&maps.k, a.k_pool, tiles, head_dim, dtype);
   if (st == PKV_OK) st = prompt_pool_map(&maps.v, a.v_pool, tiles, head_dim, dtype);
   if (st != PKV_OK) return st;
+  const bool prefix = !a.query_starts;
+  pkv::DecodeArgs d{};
+  alignas(64) CUtensorMap kmap[3], vmap[3];
+  if (a.tails) {
+    d.out = a.out;
+    d.q = a.q;
+    d.k_pool = a.k_pool;
+    d.v_pool = a.v_pool;
+    d.block_tables = a.block_tables;
+    d.context_lens = a.context_lens;
+    d.status = a.status;
+    d.num_seqs = a.num_seqs;
+    d.num_q_heads = a.num_q_heads;
+    d.num_kv_heads = a.num_kv_heads;
+    d.group = a.group;
+    d.max_blocks_per_seq = a.max_blocks_per_seq;
+    d.num_blocks = a.num_blocks;
+    d.part_tokens = a.max_blocks_per_seq * PKV_BLOCK_SIZE;  // (one CTA a sequence and KV head)
+    d.max_parts = 1;
+    d.long_first = !prefix && a.num_seqs <= pkv::kRankInCtaMaxSeqs && long_first_grid(a.num_seqs, a.num_kv_heads, 1);
+    d.window = a.window;
+    d.scale_log2 = scale_log2;
+    d.query_rows = a.query_starts;
+    d.num_rows = a.num_tokens;
+    if (prefix && a.num_groups > 0) {
+      const pkv::PromptTails t = pkv::prompt_tails(a, head_dim, workspace);
+      d.from = t.from;
+      d.join_ml = t.ml;
+      d.join_o = t.o;
+    }
+    for (int i = 0; i < 3 && a.group > 1; ++i) {
+      st = pool_tensor_map(&kmap[i], a.k_pool, tiles * PKV_BLOCK_SIZE, head_dim, dtype, PKV_BLOCK_SIZE >> i);
+      if (st == PKV_OK) st = pool_tensor_map(&vmap[i], a.v_pool, tiles * PKV_BLOCK_SIZE, head_dim, dtype, PKV_BLOCK_SIZE >> i);
+      if (st != PKV_OK) return st;
+    }
+  }
   const EnqueueLock lock(stream);
-  return cuda_status(pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, maps, stream), what);
+  // The prefixes come before what is joined to them; sequences with one token go first.
+  cudaError_t err = cudaSuccess;
+  for (int step = 0; step < 2 && err == cudaSuccess; ++step) {
+    if ((step == 0) == prefix) {
+      if (prefix && a.tails && a.num_groups == 0) continue;
+      err = pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, maps, stream);
+    } else if (a.tails) {
+      err = pkv::launch_decode_tail(d, dtype == PKV_BF16, head_dim, round_pow2_group(a.group), kmap, vmap, stream);
+    }
+  }
+  return cuda_status(err, what);
+}
+
+// Bytes that a call of these sizes needs whatever its pools are.
+size_t prompt_bytes(pkv::PromptArgs a, int head_dim) {
+  a.tails = false;
+  const size_t alone = pkv::prompt_workspace_bytes(a, head_dim);
+  a.tails = true;
+  const size_t with_tails = pkv::prompt_workspace_bytes(a, head_dim);
+  return alone > with_tails ? alone : with_tails;
 }
 
 // Sizes of a call as prompt_workspace_bytes reads them; false for ones that no call takes.
@@ -1459,7 +1531,7 @@ size_t pkv_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, 
   if (!prompt_sizes(&a, num_tokens, num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)) return 0;
   static const int32_t ragged = 0;
   a.query_starts = &ragged;  // (only whether there are any matters)
-  return pkv::prompt_workspace_bytes(a, head_dim);
+  return prompt_bytes(a, head_dim);
 }
 
 pkv_status_t pkv_paged_prompt_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -1496,7 +1568,7 @@ size_t pkv_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads, 
                                  int max_blocks_per_seq) {
   pkv::PromptArgs a;
   if (!prompt_sizes(&a, num_seqs, num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)) return 0;
-  return pkv::prompt_workspace_bytes(a, head_dim);
+  return prompt_bytes(a, head_dim);
 }
 
 pkv_status_t pkv_paged_prefix_decode(void* out, const void* q, const void* k_pool, const void* v_pool,

@@ -80,7 +80,21 @@ struct DecodeArgs {
   const int32_t* prefix_others;  // ... the sequences outside any group
   int prefix_slots;              // ... and the grid rows reserved for chunks (num_seqs)
   float scale_log2;     // scale * log2(e)
+  // Tail grids (paged_decode_*_kernel with TAIL) only:
+  const int32_t* query_rows;  // [S + 1]: sequence s's query is row query_rows[s] of q and out, where it has exactly
+                              // one (others are left out); null: row s
+  int num_rows;               // rows of q and out
+  const int32_t* from;        // [S]: positions before from[s] (a multiple of 16, or the length) are left out; null: none
+  const float2* join_ml;      // [S][Hq] (max, sum) and [S][Hq][D] unnormalised sums over positions before from[s], joined
+  const float* join_o;        // to the tail's; null: none
 };
+
+// The row of q and out that holds sequence s's query in a tail grid; -1: not one.
+__device__ __forceinline__ int tail_row(const DecodeArgs& a, int s) {
+  if (!a.query_rows) return s;
+  const int r0 = min(max(a.query_rows[s], 0), a.num_rows), r1 = min(max(a.query_rows[s + 1], r0), a.num_rows);
+  return r1 - r0 == 1 ? r0 : -1;
+}
 
 // Token range a sequence of length L attends over: [first, L), with
 // first = L - window for a sliding window shorter than L, else 0. The tiles
@@ -93,6 +107,16 @@ __device__ __forceinline__ TokenRange token_range(int L, int window) {
   TokenRange r;
   r.first = (window > 0 && L > window) ? L - window : 0;
   r.aligned = r.first & ~(kBlock - 1);
+  return r;
+}
+
+// The same without the positions before `from`.
+__device__ __forceinline__ TokenRange tail_range(TokenRange r, int L, int from) {
+  const int f = min(max(from, 0), L);
+  if (f > r.first) {
+    r.first = f;
+    r.aligned = f == L ? L : f & ~(kBlock - 1);
+  }
   return r;
 }
 
@@ -445,9 +469,33 @@ __device__ __forceinline__ void decode_tile(uint32_t kt, uint32_t vt, int lo, in
 // the partition's (m, l, o) go to the workspace and the last partition of the
 // (sequence, KV head) to arrive merges all of them by log-sum-exp:
 //   M = max_p m_p,  w_p = 2^(m_p - M),  out = sum_p w_p o_p / sum_p w_p l_p.
-template <typename T, int D, int G, int NW>
+// A tail grid joins what precedes the tail to the result, and writes it to row `qrow`.
+template <int D>
+__device__ __forceinline__ void join_before(const DecodeArgs& a, size_t row, int c8, float M, float& den, float (&num)[8]) {
+  const float2 ml = a.join_ml ? __ldcg(a.join_ml + row) : make_float2(-INFINITY, 0.f);
+  const float now = fmaxf(M, ml.x);
+  const float w0 = M == -INFINITY ? 0.f : fast_exp2(M - now), w1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - now);
+  den = den * w0 + ml.y * w1;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) num[c] *= w0;
+  if (w1 > 0.f) {
+    const float4* src = reinterpret_cast<const float4*>(a.join_o + row * D + c8 * 8);
+    const float4 x0 = __ldcg(src), x1 = __ldcg(src + 1);
+    num[0] = fmaf(w1, x0.x, num[0]);
+    num[1] = fmaf(w1, x0.y, num[1]);
+    num[2] = fmaf(w1, x0.z, num[2]);
+    num[3] = fmaf(w1, x0.w, num[3]);
+    num[4] = fmaf(w1, x1.x, num[4]);
+    num[5] = fmaf(w1, x1.y, num[5]);
+    num[6] = fmaf(w1, x1.z, num[6]);
+    num[7] = fmaf(w1, x1.w, num[7]);
+  }
+  if (den == 0.f) den = 1.f;  // nothing is seen: zeros
+}
+
+template <typename T, int D, int G, int NW, bool TAIL = false>
 __device__ __forceinline__ void finish_chunk(const DecodeArgs& a, const unsigned char* smem,
-                                             size_t area_bytes, int s, int g, int part, int nparts) {
+                                             size_t area_bytes, int s, int g, int part, int nparts, int qrow = -1) {
   constexpr int CHUNKS = D / 8;
   const int hq0 = g * a.group;
   const bool direct = nparts == 1;
@@ -480,10 +528,12 @@ __device__ __forceinline__ void finish_chunk(const DecodeArgs& a, const unsigned
     }
     const size_t row = size_t(s) * a.num_q_heads + hq0 + h;
     if (direct) {
+      if constexpr (TAIL) join_before<D>(a, row, c8, M, den, num);
       const float inv = 1.f / den;
 #pragma unroll
       for (int c = 0; c < 8; ++c) num[c] *= inv;
-      reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D)[c8] = Vec8<T>::from_float(num);
+      const size_t out_row = TAIL ? size_t(qrow) * a.num_q_heads + hq0 + h : row;
+      reinterpret_cast<uint4*>(static_cast<T*>(a.out) + out_row * D)[c8] = Vec8<T>::from_float(num);
     } else {
       float4* dst = reinterpret_cast<float4*>(a.part_o + (row * a.max_parts + part) * D + c8 * 8);
       dst[0] = make_float4(num[0], num[1], num[2], num[3]);
@@ -526,15 +576,17 @@ __device__ __forceinline__ void finish_chunk(const DecodeArgs& a, const unsigned
       num[6] = fmaf(w, x1.z, num[6]);
       num[7] = fmaf(w, x1.w, num[7]);
     }
+    if constexpr (TAIL) join_before<D>(a, row, c8, M, den, num);
     const float inv = 1.f / den;
 #pragma unroll
     for (int c = 0; c < 8; ++c) num[c] *= inv;
-    reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D)[c8] = Vec8<T>::from_float(num);
+    const size_t out_row = TAIL ? size_t(qrow) * a.num_q_heads + hq0 + h : row;
+    reinterpret_cast<uint4*>(static_cast<T*>(a.out) + out_row * D)[c8] = Vec8<T>::from_float(num);
   }
   if (threadIdx.x == 0) *counter = 0u;  // leave the workspace ready for the next call
 }
 
-template <typename T, int D, int G, int NW, int STAGES, typename KV = KvHalf<T>>
+template <typename T, int D, int G, int NW, int STAGES, typename KV = KvHalf<T>, bool TAIL = false>
 __global__ void __launch_bounds__(NW * 32)
 paged_decode_kernel(const DecodeArgs a) {
   using C = DecodeCfg<T, D, G, NW, STAGES, KV>;
@@ -550,12 +602,18 @@ paged_decode_kernel(const DecodeArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane & (LPR - 1), r = lane / LPR;
   const int hq0 = g * a.group;
+  int qrow = s;
+  if constexpr (TAIL) {
+    qrow = tail_row(a, s);
+    if (qrow < 0) return;
+  }
 
   // Without a sliding window the first 32 block ids of this warp's tiles do
   // not depend on the length: read them together with it (entries past the
   // sequence are never used).
+  const bool early = a.window == 0 && !(TAIL && a.from);
   int ids_early = 0;
-  if (a.window == 0) {
+  if (early) {
     const int j0 = (blockIdx.z * a.part_tokens) / kBlock + warp + lane * NW;
     if (j0 < a.max_blocks_per_seq) ids_early = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + j0);
   }
@@ -565,14 +623,16 @@ paged_decode_kernel(const DecodeArgs a) {
     if (threadIdx.x == 0 && part == 0 && g == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
     L = L < 0 ? 0 : max_len;
   }
-  const TokenRange tr = token_range(L, a.window);
-  const int nparts = L == 0 ? 1 : (L - tr.aligned + a.part_tokens - 1) / a.part_tokens;
+  TokenRange tr = token_range(L, a.window);
+  if constexpr (TAIL)
+    if (a.from) tr = tail_range(tr, L, a.from[s]);
+  const int nparts = L <= tr.aligned ? 1 : (L - tr.aligned + a.part_tokens - 1) / a.part_tokens;
   if (part >= nparts) return;
   const int pslot = part;  // partition slot of this CTA's partial in the workspace
   trace_mark(tm, 2);
 
   if (L == 0) {  // empty sequence: zeros
-    T* o = static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + hq0) * D;
+    T* o = static_cast<T*>(a.out) + (size_t(qrow) * a.num_q_heads + hq0) * D;
     for (int i = threadIdx.x; i < a.group * D / 8; i += NW * 32)
       reinterpret_cast<uint4*>(o)[i] = make_uint4(0u, 0u, 0u, 0u);
     return;
@@ -599,7 +659,7 @@ paged_decode_kernel(const DecodeArgs a) {
   for (int h = 0; h < G; ++h) {
     if (h < a.group) {
       const uint4 u = __ldg(reinterpret_cast<const uint4*>(
-          static_cast<const T*>(a.q) + (size_t(s) * a.num_q_heads + hq0 + h) * D + sub * 8));
+          static_cast<const T*>(a.q) + (size_t(qrow) * a.num_q_heads + hq0 + h) * D + sub * 8));
       Vec8<T>::to_float(u, qf[h]);
 #pragma unroll
       for (int c = 0; c < 8; ++c) qf[h][c] *= a.scale_log2;
@@ -625,7 +685,7 @@ paged_decode_kernel(const DecodeArgs a) {
   };
   int ids = 0;
   if (lane < n_my) {
-    ids = a.window == 0 ? ids_early : __ldg(trow + warp + lane * NW);
+    ids = early ? ids_early : __ldg(trow + warp + lane * NW);
     if (ids < 0 || ids >= a.num_blocks) {
       flag(a.status, PKV_DEV_BAD_BLOCK_ID);
       ids = 0;
@@ -738,7 +798,7 @@ paged_decode_kernel(const DecodeArgs a) {
   }
   __syncthreads();
 
-  finish_chunk<T, D, G, NW>(a, smem, size_t(STAGES) * C::STAGE_BYTES, s, g, pslot, nparts);
+  finish_chunk<T, D, G, NW, TAIL>(a, smem, size_t(STAGES) * C::STAGE_BYTES, s, g, pslot, nparts, qrow);
   trace_write(a, tm, s, nb);
 }
 

@@ -88,21 +88,21 @@ constexpr int kLongGridWarps = 6;
 constexpr int64_t kLongGridCtas = 1024;
 constexpr int kLongSplitTokens = 12288;
 
-template <typename T, int D, int G, int NW, int STAGES>
+template <typename T, int D, int G, int NW, int STAGES, bool TAIL = false>
 cudaError_t launch_cuda_core_grid(const DecodeArgs& a, dim3 grid, cudaStream_t stream) {
   using C = DecodeCfg<T, D, G, NW, STAGES>;
-  auto kern = paged_decode_kernel<T, D, G, NW, STAGES>;
+  auto kern = paged_decode_kernel<T, D, G, NW, STAGES, KvHalf<T>, TAIL>;
   static bool configured[kMaxDevices] = {};
   cudaError_t err = configure_once(kern, C::SMEM_BYTES, configured);
   if (err != cudaSuccess) return err;
   return launch_pdl(kern, grid, dim3(NW * 32), C::SMEM_BYTES, stream, a);
 }
 
-template <typename T, int D, int G, int MW, int MS>
+template <typename T, int D, int G, int MW, int MS, bool TAIL = false>
 cudaError_t launch_mma_grid(const DecodeArgs& a, dim3 grid, const CUtensorMap* kmap, const CUtensorMap* vmap,
                             cudaStream_t stream) {
   using C = MmaCfg<T, D, MW, MS>;
-  auto kern = paged_decode_mma_kernel<T, D, G, MW, MS>;
+  auto kern = paged_decode_mma_kernel<T, D, G, MW, MS, TAIL>;
   static bool configured[kMaxDevices] = {};
   cudaError_t err = configure_once(kern, C::SMEM_BYTES, configured);
   if (err != cudaSuccess) return err;
@@ -141,6 +141,40 @@ cudaError_t launch_decode_dg(const DecodeArgs& a, const CUtensorMap* kmap, const
     if (err != cudaSuccess) return err;
   }
   return cudaGetLastError();
+}
+
+// Tail grids (query_rows, from, join_*): the shapes of the grids above.
+template <typename T, int D, int G>
+cudaError_t launch_decode_tail_dg(const DecodeArgs& a, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                  cudaStream_t stream) {
+  const dim3 grid(unsigned(a.num_kv_heads), unsigned(a.num_seqs), unsigned(a.max_parts));
+  cudaError_t err;
+  if constexpr (G == 1) err = launch_cuda_core_grid<T, D, G, kGridWarps, kGridStages, true>(a, grid, stream);
+  else err = launch_mma_grid<T, D, G, kMmaWarps, kMmaStages, true>(a, grid, kmap, vmap, stream);
+  return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_decode_tail_d(const DecodeArgs& a, int gpad, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                                 cudaStream_t stream) {
+  switch (gpad) {
+    case 1: return launch_decode_tail_dg<T, D, 1>(a, kmap, vmap, stream);
+    case 2: return launch_decode_tail_dg<T, D, 2>(a, kmap, vmap, stream);
+    case 4: return launch_decode_tail_dg<T, D, 4>(a, kmap, vmap, stream);
+    case 8: return launch_decode_tail_dg<T, D, 8>(a, kmap, vmap, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+template <typename T>
+cudaError_t launch_decode_tail_t(const DecodeArgs& a, int head_dim, int gpad, const CUtensorMap* kmap,
+                                 const CUtensorMap* vmap, cudaStream_t stream) {
+  switch (head_dim) {
+    case 64: return launch_decode_tail_d<T, 64>(a, gpad, kmap, vmap, stream);
+    case 128: return launch_decode_tail_d<T, 128>(a, gpad, kmap, vmap, stream);
+    case 256: return launch_decode_tail_d<T, 256>(a, gpad, kmap, vmap, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 // Slots the shared-prefix plan splits groups against: CTAs of the 3 x 2

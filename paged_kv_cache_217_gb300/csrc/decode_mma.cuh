@@ -215,7 +215,7 @@ __device__ __forceinline__ void zero_rows_outside(uint32_t vt, int lo, int rows,
 template <typename T, int D, int G, int NW, int STAGES>
 __device__ __forceinline__ void prefix_cta(const DecodeArgs& a, const PoolMaps& maps, unsigned char* smem, int gi);
 
-template <typename T, int D, int G, int NW, int STAGES>
+template <typename T, int D, int G, int NW, int STAGES, bool TAIL = false>
 __global__ void __launch_bounds__(NW * 32)
 paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps maps) {
   using C = MmaCfg<T, D, NW, STAGES>;
@@ -263,6 +263,11 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
       prow1 = __ldg(a.plan_rows + 2 * blockIdx.y + 1);
     }
     s = long_first_seq<NW>(a, int(blockIdx.y));
+  }
+  int qrow = s;
+  if constexpr (TAIL) {
+    qrow = tail_row(a, s);
+    if (qrow < 0) return;
   }
   const bool rows_ok = prow0.x == s && phdr.x == kPlanMagic && phdr.y == a.num_seqs;
   const int part = blockIdx.z;
@@ -325,8 +330,9 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
   // not depend on the length: read them together with it (entries past the
   // sequence are never used).
   const int max_len = a.max_blocks_per_seq * kBlock;
+  const bool early = a.window == 0 && !(TAIL && a.from);
   int ids_early = 0;
-  if (a.window == 0) {
+  if (early) {
     const int j0 = (blockIdx.z * a.part_tokens) / kBlock + warp + lane * NW;
     if (j0 < a.max_blocks_per_seq) ids_early = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + j0);
   }
@@ -336,12 +342,12 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
   // copies below and before anything waits for them.
   uint32_t qa[C::KSTEPS][2];
   {
-    const uint32_t* qrow = reinterpret_cast<const uint32_t*>(
-        static_cast<const T*>(a.q) + (size_t(s) * a.num_q_heads + hq0 + gr) * D);
+    const uint32_t* qline = reinterpret_cast<const uint32_t*>(
+        static_cast<const T*>(a.q) + (size_t(qrow) * a.num_q_heads + hq0 + gr) * D);
 #pragma unroll
     for (int ks = 0; ks < C::KSTEPS; ++ks) {
-      qa[ks][0] = gr < a.group ? __ldg(qrow + 8 * ks + t) : 0u;
-      qa[ks][1] = gr < a.group ? __ldg(qrow + 8 * ks + 4 + t) : 0u;
+      qa[ks][0] = gr < a.group ? __ldg(qline + 8 * ks + t) : 0u;
+      qa[ks][1] = gr < a.group ? __ldg(qline + 8 * ks + 4 + t) : 0u;
     }
   }
 
@@ -399,12 +405,14 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
   else
     L = checked_len(L_own);
   auto write_zeros = [&]() {
-    T* o = static_cast<T*>(a.out) + (size_t(s) * a.num_q_heads + hq0) * D;
+    T* o = static_cast<T*>(a.out) + (size_t(qrow) * a.num_q_heads + hq0) * D;
     for (int i = threadIdx.x; i < a.group * D / 8; i += NW * 32)
       reinterpret_cast<uint4*>(o)[i] = make_uint4(0u, 0u, 0u, 0u);
   };
-  const TokenRange tr = token_range(L, a.window);
-  const int nparts = L == 0 ? 1 : (L - tr.aligned + a.part_tokens - 1) / a.part_tokens;
+  TokenRange tr = token_range(L, a.window);
+  if constexpr (TAIL)
+    if (a.from) tr = tail_range(tr, L, a.from[s]);
+  const int nparts = L <= tr.aligned ? 1 : (L - tr.aligned + a.part_tokens - 1) / a.part_tokens;
   if (part >= nparts) return;  // (split grids only; no speculative copies there)
   const int pslot = part;  // partition slot of this CTA's partial in the workspace
   trace_mark(tm, 2);
@@ -433,7 +441,7 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
   auto first_ids = [&]() {
     ids = 0;
     if (lane < n_my) {
-      ids = a.window == 0 ? ids_early : __ldg(trow + warp + lane * NW);
+      ids = early ? ids_early : __ldg(trow + warp + lane * NW);
       if (ids < 0 || ids >= a.num_blocks) {
         flag(a.status, PKV_DEV_BAD_BLOCK_ID);
         ids = 0;
@@ -545,7 +553,7 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
     }
   }
   __syncthreads();
-  finish_chunk<T, D, G, NW>(a, smem, size_t(STAGES) * C::STAGE_BYTES, s, g, pslot, nparts);
+  finish_chunk<T, D, G, NW, TAIL>(a, smem, size_t(STAGES) * C::STAGE_BYTES, s, g, pslot, nparts, qrow);
   trace_write(a, tm, s, nb);
 }
 

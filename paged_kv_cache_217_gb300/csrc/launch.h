@@ -22,6 +22,10 @@ cudaError_t launch_decode_f16(const DecodeArgs& a, int head_dim, int gpad, const
 cudaError_t launch_decode_bf16(const DecodeArgs& a, int head_dim, int gpad, const CUtensorMap* kmap,
                                const CUtensorMap* vmap, cudaStream_t stream);
 
+// The same grids over the tails of sequences (DecodeArgs::query_rows, from, join_ml, join_o).
+cudaError_t launch_decode_tail(const DecodeArgs& a, bool bf16, int head_dim, int gpad, const CUtensorMap* kmap,
+                               const CUtensorMap* vmap, cudaStream_t stream);
+
 // Decode with the balanced persistent schedule (decode_sk.cuh); same gpad rules.
 cudaError_t launch_decode_sk_f16(const SkArgs& a, int head_dim, int gpad, const CUtensorMap* kmap,
                                  const CUtensorMap* vmap, cudaStream_t stream);
@@ -185,6 +189,7 @@ struct PromptArgs {
   int causal;
   int window;        // causal: attend over the last `window` tokens (0 = all)
   float scale_log2;  // scale * log2(e)
+  int tails;         // a decode grid takes sequences with one query token (prompts), and what follows the prefixes
   // set by the launcher: query tokens of a tile of rows and of a block, CTAs, rows of a
   // slot of partial results, and the workspace's parts
   int tile_tokens, block_tokens, shares;
@@ -194,7 +199,16 @@ struct PromptArgs {
   int* more;    // per share, whether it begins inside an item
   float2* part_ml;
   float* part_o;
+  int32_t* from;  // per sequence, where its prefix ends (prefix decode with tails)
 };
+// What a tail grid behind a prefix reads of the workspace: from, and the partial results of
+// the prefixes per (sequence, query head).
+struct PromptTails {
+  const int32_t* from;
+  const float2* ml;
+  const float* o;
+};
+PromptTails prompt_tails(PromptArgs a, int head_dim, void* workspace);
 // Query tokens of one copy of Q (128 rows): the second box size of its tensor map.
 inline int prompt_tile_tokens(int group) { return 128 / group; }
 size_t prompt_workspace_bytes(const PromptArgs& a, int head_dim);

@@ -25,7 +25,8 @@ PromptShape prompt_shape(const PromptArgs& a, int head_dim) {
   p.slot_rows = a.num_tokens > p.tile_tokens ? size_t(128) * groups : 128;
   p.rows = a.query_starts ? 0 : size_t(2) * a.num_seqs * a.num_q_heads;
   // no more shares than tiles
-  const int64_t blocks = int64_t(a.num_tokens) / p.block_tokens + a.num_seqs + (a.num_groups ? a.num_seqs : 0);
+  const int64_t items = a.query_starts ? a.num_seqs : a.num_groups + (a.tails ? 0 : a.num_seqs);
+  const int64_t blocks = int64_t(a.num_tokens) / p.block_tokens + items;
   const int64_t tiles = blocks * a.num_kv_heads * ((int64_t(a.max_blocks_per_seq) * kBlock + tile - 1) / tile + 1);
   p.shares = tiles < kPromptSms ? int(tiles) : kPromptSms;
   return p;
@@ -41,7 +42,7 @@ cudaError_t launch_d(const PromptArgs& a, const PromptMaps& maps, cudaStream_t s
                    maps.q1, maps.k, maps.v);
   if (err != cudaSuccess) return err;
   if (!a.query_starts)
-    return launch_pdl(prefix_join_kernel<T, D>, dim3(unsigned((int64_t(a.num_seqs) * a.num_q_heads + 7) / 8)), dim3(256), 0,
+    return launch_pdl(a.tails ? prefix_join_kernel<T, D, true> : prefix_join_kernel<T, D, false>, dim3(unsigned((int64_t(a.num_seqs) * a.num_q_heads + 7) / 8)), dim3(256), 0,
                       stream, a);
   if (a.shares == 1) return cudaSuccess;  // nothing is cut
   return launch_pdl(prompt_join_kernel<T, D>, dim3(unsigned(a.shares), 8), dim3(256), 0, stream, a);
@@ -56,30 +57,48 @@ cudaError_t launch_t(const PromptArgs& a, int head_dim, const PromptMaps& maps, 
 
 }  // namespace
 
-// Per share: what is cut; per item (prefix decode): where its pieces are; then (maximum,
-// sum) pairs and fp32 accumulators of two slots a share and of kept rows.
+namespace {
+// Per share: what is cut; per item (prefix decode): where its pieces are; whether shares begin
+// inside an item; where prefixes end; then fp32 accumulators and (maximum, sum) pairs of two
+// slots a share and of kept rows.
+size_t lay_out(PromptArgs* a, int head_dim, char* workspace) {
+  const PromptShape p = prompt_shape(*a, head_dim);
+  a->tile_tokens = p.tile_tokens;
+  a->block_tokens = p.block_tokens;
+  a->shares = p.shares;
+  a->slot_rows = p.slot_rows;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    char* const here = workspace + at;
+    at += round16(bytes);
+    return here;
+  };
+  char* const links = take(a->query_starts ? size_t(p.shares) * sizeof(int4) : size_t(2) * a->num_seqs * a->num_kv_heads * sizeof(int2));
+  a->desc = reinterpret_cast<int4*>(links);
+  a->link = reinterpret_cast<int2*>(links);
+  a->more = reinterpret_cast<int*>(take(size_t(p.shares) * sizeof(int)));
+  a->from = reinterpret_cast<int32_t*>(take(size_t(a->num_seqs) * sizeof(int32_t)));
+  const size_t rows = p.slot_rows * 2 * p.shares + p.rows;
+  a->part_o = reinterpret_cast<float*>(take(rows * head_dim * sizeof(float)));
+  a->part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
+  return at;
+}
+}  // namespace
+
 size_t prompt_workspace_bytes(const PromptArgs& a, int head_dim) {
-  const PromptShape p = prompt_shape(a, head_dim);
-  const size_t links = a.query_starts ? size_t(p.shares) * sizeof(int4) : size_t(2) * a.num_seqs * a.num_kv_heads * sizeof(int2);
-  return round16(links) + round16(size_t(p.shares) * sizeof(int)) +
-         (p.slot_rows * 2 * p.shares + p.rows) * (sizeof(float2) + size_t(head_dim) * sizeof(float));
+  PromptArgs b = a;
+  return lay_out(&b, head_dim, nullptr);
+}
+
+PromptTails prompt_tails(PromptArgs a, int head_dim, void* workspace) {
+  lay_out(&a, head_dim, static_cast<char*>(workspace));
+  const size_t kept = a.slot_rows * 2 * a.shares;
+  return {a.from, a.part_ml + kept, a.part_o + kept * head_dim};
 }
 
 cudaError_t launch_prompt(PromptArgs a, bool bf16, int head_dim, void* workspace, const PromptMaps& maps,
                           cudaStream_t stream) {
-  const PromptShape p = prompt_shape(a, head_dim);
-  a.tile_tokens = p.tile_tokens;
-  a.block_tokens = p.block_tokens;
-  a.shares = p.shares;
-  a.slot_rows = p.slot_rows;
-  char* at = static_cast<char*>(workspace);
-  a.desc = reinterpret_cast<int4*>(at);
-  a.link = reinterpret_cast<int2*>(at);
-  at += round16(a.query_starts ? size_t(p.shares) * sizeof(int4) : size_t(2) * a.num_seqs * a.num_kv_heads * sizeof(int2));
-  a.more = reinterpret_cast<int*>(at);
-  at += round16(size_t(p.shares) * sizeof(int));
-  a.part_o = reinterpret_cast<float*>(at);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + (p.slot_rows * 2 * p.shares + p.rows) * head_dim);
+  lay_out(&a, head_dim, static_cast<char*>(workspace));
   return bf16 ? launch_t<__nv_bfloat16>(a, head_dim, maps, stream) : launch_t<__half>(a, head_dim, maps, stream);
 }
 

@@ -51,21 +51,21 @@ constexpr float kPromptHeadroom = 7.f;  // fp16 weights are 2^7 times as large (
 constexpr int kPromptPieces = 4;   // pieces that the copying warp may be ahead
 constexpr int kPromptNone = -1;
 // A piece of one tile of rows goes to one warpgroup, the next to the other; from this many
-// KV tiles on, or with no piece behind it, to both.
-constexpr int kPromptSplit = 8;
+// positions on, or with no piece behind it, to both.
+constexpr int kPromptSplit = 1024;
 
 template <int D>
 struct PromptCfg {
   static constexpr int GROUPS = D == 256 ? 1 : 2;     // softmax warpgroups
-  static constexpr int TILE = D == 256 ? 64 : 128;    // tokens
+  static constexpr int TILE = 64;                     // tokens
   static constexpr int ROWS = 128 * GROUPS;           // of an item
   static constexpr int CHUNKS = D / 64;
   static constexpr int SLOT = TILE * D * 2;           // bytes of a K or V tile
-  static constexpr int SLOTS = D == 64 ? 8 : 4;
+  static constexpr int SLOTS = D == 64 ? 16 : D == 128 ? 8 : 4;
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int SOFTMAX = 128 * GROUPS;        // threads
   static constexpr int THREADS = SOFTMAX + 128;
-  static constexpr int DEPTH = 3 - GROUPS;            // S buffers of a warpgroup
+  static constexpr int DEPTH = TILE == 64 ? 2 : 1;    // S buffers of a warpgroup
   static constexpr int STAGE = 2048;                  // bytes a softmax warp writes its output through
   static constexpr int STEP = CHUNKS * 1024;          // bytes of 8 tokens
   static constexpr int S_AT = GROUPS * D;             // columns of tensor memory: O, then two S
@@ -74,7 +74,7 @@ struct PromptCfg {
   static constexpr int STATS_AT = 1024, STAGE_AT = STATS_AT + 1024 * GROUPS, LIST_AT = STAGE_AT + STAGE * 4 * GROUPS;
   static constexpr int MISC = LIST_AT + LISTED * 32;
   static constexpr size_t SMEM_BYTES = 1024 + size_t(GROUPS) * Q_TILE + size_t(SLOTS) * SLOT + MISC;
-  static_assert(S_AT + 2 * TILE <= COLUMNS, "tensor memory");
+  static_assert(S_AT + GROUPS * DEPTH * TILE <= COLUMNS, "tensor memory");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -116,6 +116,7 @@ __device__ __forceinline__ PromptSegment prompt_segment(const PromptArgs& a, int
   if (a.query_starts) {
     g.q0 = prompt_clamp(a.query_starts[i], 0, a.num_tokens);
     g.nq = prompt_clamp(a.query_starts[i + 1], g.q0, a.num_tokens) - g.q0;
+    if (a.tails && g.nq == 1) g.nq = 0;
     g.table = i;
     g.lo = 0;
     g.len = prompt_len(a, i);
@@ -193,11 +194,12 @@ struct PieceTiles {
   __device__ __forceinline__ PieceTiles(int mode, int tiles, int w)
       : first(mode == kPieceSplit ? w : 0), step(mode == kPieceSplit ? 2 : 1),
         any(mode == w || (mode >= kPieceRows && (mode == kPieceRows || w < tiles))) {}
+  __device__ __forceinline__ bool has(int t) const { return any && (step == 1 || (t & 1) == first); }
 };
 
 struct PromptShared {
-  uint64_t slot_full[8], slot_empty[8];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], join, warm;
+  uint64_t slot_full[16], slot_empty[16];
+  uint64_t q_full[2], q_empty[2], s_full[4], p_full[4], pv_done[4], join, warm;
   uint64_t piece_full[kPromptPieces], piece_empty[kPromptPieces];
   uint64_t drain[2];  // after a wait gave up
   PromptPiece piece[kPromptPieces];
@@ -207,8 +209,12 @@ struct PromptShared {
   uint32_t tmem;
   int stop;    // a wait gave up: every role leaves
   int lock;    // a warp issues its MMAs
-  int issued;  // K and V tiles whose copies are issued
+  // Tiles of each warpgroup in turn: K's slot of the ring (V's is the next) + 32 x phase + 64 x
+  // (first of its piece) + 128 x (last) + 256 x (the other warpgroup uses it too); -1: no more.
+  int tile[2][16];
+  int copies[2];  // K and V copies issued for these
 };
+enum { kTilePhase = 32, kTileFirst = 64, kTileLast = 128, kTileShared = 256 };
 static_assert(sizeof(PromptShared) <= 1024, "shared state");
 
 // ---- tcgen05 ----------------------------------------------------------------
@@ -336,7 +342,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
 
   if (tid == 0) {
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(smem_addr(&sh.slot_full[i]), 1);
       mbar_init(smem_addr(&sh.slot_empty[i]), 2);
     }
@@ -344,6 +350,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&sh.q_full[i]), 1);
       mbar_init(smem_addr(&sh.q_empty[i]), 1);
+    }
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
       mbar_init(smem_addr(&sh.s_full[i]), 1);
       mbar_init(smem_addr(&sh.p_full[i]), 128);
       mbar_init(smem_addr(&sh.pv_done[i]), 1);
@@ -353,11 +362,11 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
 #pragma unroll 1
     for (int i = 0; i < kPromptPieces; ++i) {
       mbar_init(smem_addr(&sh.piece_full[i]), 1);
-      mbar_init(smem_addr(&sh.piece_empty[i]), C::SOFTMAX / 32 + 1 + C::GROUPS);
+      mbar_init(smem_addr(&sh.piece_empty[i]), C::SOFTMAX / 32 + 1);
     }
     mbar_init_fence();
     sh.stop = 0;
-    sh.issued = sh.lock = 0;
+    sh.copies[0] = sh.copies[1] = sh.lock = 0;
     asm volatile("prefetch.tensormap [%0];" ::"l"(&q_map) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&q1_map) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&k_map) : "memory");
@@ -383,7 +392,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
   // The list: each thread of three warps sums a run of segments, a scan of the sums gives
   // every run's place, and the thread whose run holds this CTA's share's begin finds its segment.
   const int TQ = a.tile_tokens, TB = TQ * C::GROUPS;  // tokens of a tile of rows, and of a block
-  const int segs = a.num_groups + a.num_seqs, cta = int(blockIdx.x), ctas = int(gridDim.x);
+  const int segs = a.num_groups + (a.tails && !a.query_starts ? 0 : a.num_seqs), cta = int(blockIdx.x), ctas = int(gridDim.x);
   const bool listed = segs <= C::LISTED;
   long long begin = 0, end = 0, total = 0, quotient = 0;
   if (scanner) {
@@ -442,30 +451,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
   volatile int* stop = &sh.stop;
   auto wait = [&](uint64_t& bar, int phase) { return prompt_wait(smem_addr(&bar), uint32_t(phase) & 1, stop, a.status); };
   auto test = [&](uint64_t& bar, int phase) { return bool(__all_sync(kFull, mbar_test(smem_addr(&bar), uint32_t(phase) & 1))); };
-  // Tile n of the ring has landed (or, unless block, has not yet). Its slot's phase may be looked
-  // at only once its copy is issued, when the phase before is over: of tiles that the other
-  // warpgroup uses alone this one sees nothing.
-  int issued = 0;
-  auto landed = [&](int n, bool block) {
-    unsigned long long t0 = 0;
-    for (int polls = 0; issued <= n; ++polls) {
-      issued = __shfl_sync(kFull, lds_acquire(smem_addr(&sh.issued)), 0);
-      if (issued > n) break;
-      if (!block) return false;
-      if ((polls & 63) != 63) continue;
-      const unsigned long long now = __shfl_sync(kFull, global_timer_ns(), 0);
-      if (polls == 63) t0 = now;
-      if (__any_sync(kFull, *stop)) return false;
-      if (now - t0 > kWaitLimitNs) {
-        *stop = 1;
-        if (lane == 0) flag(a.status, PKV_DEV_WAIT_TIMEOUT);
-        return false;
-      }
-    }
-    uint64_t& bar = sh.slot_full[n % C::SLOTS];
-    return block ? wait(bar, n / C::SLOTS) : test(bar, n / C::SLOTS);
-  };
-  if (warp == WARP_KV || warp == WARP_Q) {
+  // (a batch whose single tokens a decode grid takes may leave nothing here)
+  const bool trial = !(a.tails && a.query_starts);
+  if (warp == WARP_KV || (warp == WARP_Q && trial)) {
     // ---- pieces, and the copies of K and V ----
     const bool dry = warp == WARP_Q;  // (only to have the code at hand: a made-up share, and no effect)
     if (dry) {
@@ -604,6 +592,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     bool ok = true;  // warp-uniform
     int n = 0;       // tiles (K or V) copied
     int given[2] = {0, 0};  // tiles that each warpgroup was given alone
+    int told[2] = {0, 0};   // tiles that each was told of
     constexpr int B = C::TILE / kBlock;  // blocks of a tile
     int first_ids = 0;
     for (int count = -1; ok && p.tiles >= 0; ++count) {
@@ -613,7 +602,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         const bool more = open ? item < end : seg < segs && seg_base < end;
         if (C::GROUPS == 1) p.mode = kPieceFirst;
         else if (p.tokens > TQ) p.mode = kPieceRows;
-        else if (p.tiles >= kPromptSplit || (p.tiles > 1 && !more)) p.mode = kPieceSplit;
+        else if (p.tiles * C::TILE >= kPromptSplit || (p.tiles > 1 && !more)) p.mode = kPieceSplit;
         else p.mode = given[1] < given[0] ? kPieceSecond : kPieceFirst;
         if (p.mode == kPieceFirst) given[0] += p.tiles + 1;
         if (p.mode == kPieceSecond) given[1] += p.tiles + 1;
@@ -637,6 +626,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           int z[B];
 #pragma unroll
           for (int j = 0; j < B; ++j) z[j] = 2 * (__shfl_sync(kFull, ids, block - from + j) * a.num_kv_heads + p.head);
+          const PieceTiles one(p.mode, p.tiles, 0), two(p.mode, p.tiles, 1);
+          const bool uses[2] = {one.has(t), two.has(t)};
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const int slot = n % C::SLOTS;
@@ -647,11 +638,20 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
               mbar_arrive_expect_tx(bar, C::SLOT);
 #pragma unroll
               for (int j = 0; j < B; ++j) tma_load_4d(dst + j * 2 * C::STEP, kv ? &v_map : &k_map, 0, 0, 0, z[j], bar);
-              sts_release(smem_addr(&sh.issued), n + 1);
+#pragma unroll
+              for (int w = 0; w < C::GROUPS; ++w) {
+                if (!uses[w]) continue;
+                if (kv == 0)
+                  sh.tile[w][told[w] % 16] = slot + (n / C::SLOTS & 1 ? kTilePhase : 0) + (t == (w ? two : one).first ? kTileFirst : 0) +
+                                             (t + (w ? two : one).step >= p.tiles ? kTileLast : 0) + (p.mode == kPieceRows ? kTileShared : 0);
+                sts_release(smem_addr(&sh.copies[w]), 2 * told[w] + 1 + kv);
+              }
             }
             __syncwarp();
           }
           if (!ok) break;
+          told[0] += uses[0];
+          told[1] += uses[1];
         }
         if (t == 0) {
           // the next piece, and its first block ids on their way, once the first copies are
@@ -677,6 +677,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         if (ok && lane == 0) {
           sh.piece[count % kPromptPieces] = p;
           mbar_arrive(smem_addr(&sh.piece_full[count % kPromptPieces]));
+          for (int w = 0; w < C::GROUPS; ++w) {
+            sh.tile[w][told[w] % 16] = -1;
+            sts_release(smem_addr(&sh.copies[w]), 2 * told[w] + 1);
+          }
         }
       }
     }
@@ -727,92 +731,83 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         if (loads[w] > 0) mbar_wait_bounded(smem_addr(&sh.q_full[w]), uint32_t(loads[w] - 1) & 1, 10000000ull);
   } else if (warp >= WARP_MMA && warp < WARP_MMA + C::GROUPS) {
     // ---- MMA issue: a warp for each warpgroup ----
-    // As soon as the weights are there O += P V, and right behind it S of the next tile (of the
-    // next piece, too). The two warps issue by turns (`lock`), so that while one warpgroup has
-    // its products made the other makes weights: side by side both would wait for both. One lane
-    // issues, the others keep step, so that all of it stays in uniform registers. What the next
-    // products need besides the weights is looked at before these are awaited.
+    // As soon as the weights are there O += P V, and S of a tile as soon as its K and a buffer
+    // are. The two warps issue by turns (`lock`), so that while one warpgroup has its products
+    // made the other makes weights: side by side both would wait for both. One lane issues, the
+    // others keep step, so that all of it stays in uniform registers. The loop is short, without
+    // waits of its own, and reads what the copying warp has worked out: every instruction between
+    // two products is one that the tensor cores wait for.
     const int w = warp - WARP_MMA;
     constexpr uint32_t id_s = tc_idesc<T>(128, C::TILE, false), id_o = tc_idesc<T>(128, D, false) | (1u << 16);
     const uint64_t q_desc = tc_desc(smem_addr(q_mem) + w * C::Q_TILE, 16, 1024);
     const uint64_t k_desc = tc_desc(smem_addr(ring), 16, C::STEP), v_desc = tc_desc(smem_addr(ring), 1024, C::STEP);
-    int count = 0, n0 = 0, behind = 0;  // pieces looked at, ring index of the piece's first tile, its tiles
-    int i = 0, tiles = 0, step = 1;     // the next KV tile of the piece
-    bool rows = false, fresh = false, done = false;
-    int loads = 0, s = 0, o = 0;        // Qs waited for; S and O issued
-    int v0 = 0, v1 = 0;                 // of the S whose O is to come, the older first: V's ring index x 8 + (last of its
-                                        // piece) x 4 + (the other warpgroup uses it too) x 2 + first
-    auto reached = [&](uint64_t& bar, int phase, bool block) { return block ? wait(bar, phase) : test(bar, phase); };
-    // Whether (block: waits until) all that S of the next tile needs is there.
-    auto next_there = [&](bool block) {
-      while (i >= tiles) {  // the next piece
-        if (!reached(sh.piece_full[count % kPromptPieces], count / kPromptPieces, block)) return false;
-        const PromptPiece& p = sh.piece[count % kPromptPieces];
-        const int all = __shfl_sync(kFull, p.tiles, 0), mode = __shfl_sync(kFull, p.mode, 0);
-        if (all < 0) {
-          done = true;
-          return false;
-        }
-        if (elect_one()) mbar_arrive(smem_addr(&sh.piece_empty[count % kPromptPieces]));
-        ++count;
-        n0 += 2 * behind;
-        behind = all;
-        const PieceTiles mine(mode, all, w);
-        i = mine.first;
-        step = mine.step;
-        tiles = mine.any ? all : 0;
-        rows = mode == kPieceRows;
-        fresh = true;
-      }
-      return landed(n0 + 2 * i, block) && (!fresh || reached(sh.q_full[w], loads, block));
+    const uint32_t copies_at = smem_addr(&sh.copies[w]);
+    int copies = 0, loads = 0;    // copies seen, Qs waited for
+    int s = 0, o = 0;             // S and O issued
+    int next = 0, v0 = 0, v1 = 0; // tile of the next S; of those whose O is to come, the older first
+    bool known = false, scores = false, done = false;
+    unsigned long long t0 = 0;
+    auto reached = [&](uint64_t& bar, int phase, bool asleep) {
+      const uint32_t at = smem_addr(&bar), parity = uint32_t(phase) & 1;
+      return bool(__all_sync(kFull, asleep ? mbar_try_wait(at, parity) : mbar_test(at, parity)));
     };
-    bool k_there = false;
-    if (!wait(sh.warm, 0)) done = true;  // (the softmax warps' trial uses S and O)
-    for (;;) {
-      if (!done && !k_there) k_there = next_there(s == o);
-      bool outputs = false;
-      if (s > o && !(C::DEPTH == 2 && k_there && s < o + 2)) {
-        const int b = C::GROUPS == 2 ? w : o & 1;
-        outputs = landed(v0 >> 3, true) && wait(sh.p_full[b], C::GROUPS == 2 ? o : o >> 1);
-        if (!outputs) break;
-        if (!done && !k_there) k_there = next_there(false);
+    wait(sh.warm, 0);  // (the softmax warps' trial uses S and O)
+    for (int polls = 0;; ++polls) {
+      if (copies < 2 * s + 1 || copies < 2 * o + 2) copies = __shfl_sync(kFull, lds_acquire(copies_at), 0);
+      if (!known && copies > 2 * s) {
+        next = __shfl_sync(kFull, sh.tile[w][s % 16], 0);
+        known = true;
+        done = next < 0;
       }
-      const bool scores = k_there;
-      if (!outputs && !scores) {
-        if (done || __any_sync(kFull, *stop)) break;
+      // (what is the only thing to wait for is waited for asleep: polling takes turns from the softmax warps)
+      if (known && !done && !scores)
+        scores = reached(sh.slot_full[next & 31], next / kTilePhase, s == o) && (!(next & kTileFirst) || reached(sh.q_full[w], loads, s == o));
+      const int bo = w * C::DEPTH + o % C::DEPTH, bs = w * C::DEPTH + s % C::DEPTH;
+      const bool outputs = s > o && copies >= 2 * o + 2 && reached(sh.p_full[bo], o / C::DEPTH, done || s - o == C::DEPTH) &&
+                           test(sh.slot_full[(v0 & 31) + 1], v0 / kTilePhase);
+      const bool more = scores && s - o - (outputs ? 1 : 0) < C::DEPTH;
+      if (!outputs && !more) {
+        if (done && s == o) break;
+        if ((polls & 63) != 63) continue;
+        const unsigned long long now = __shfl_sync(kFull, global_timer_ns(), 0);
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs && lane == 0 && !*stop) {
+          *stop = 1;
+          flag(a.status, PKV_DEV_WAIT_TIMEOUT);
+        }
+        __syncwarp();
+        if (__any_sync(kFull, *stop)) break;
         continue;
       }
-      const int slot_o = (v0 >> 3) % C::SLOTS, bo = C::GROUPS == 2 ? w : o & 1;
-      const int ns = n0 + 2 * i, slot_s = ns % C::SLOTS, bs = C::GROUPS == 2 ? w : s & 1;
-      const bool last = i + step >= tiles;
+      t0 = 0;
       tc_fence_after();
       if (elect_one()) {
         if (C::GROUPS == 2) {  // (what holds it only issues: a bounded number of tries is enough, and no turn is needed to be right)
           for (int tries = 0; tries < 4096 && atomicExch(&sh.lock, 1); ++tries) {}
         }
         if (outputs) {
-          const uint32_t p = tmem + C::S_AT + bo * C::TILE;
-          const uint64_t d = v_desc + slot_o * (C::SLOT >> 4);
+          const uint32_t p = tmem + C::S_AT + bo * C::TILE, slot = (v0 & 31) + 1;
+          const uint64_t d = v_desc + slot * (C::SLOT >> 4);
 #pragma unroll 1
           for (int e = 0; e < C::TILE / 16; ++e)
-            tc_mma_ts(tmem + w * D, p + 8 * e, d + e * (2 * C::STEP >> 4), id_o, !((v0 & 1) && e == 0));
+            tc_mma_ts(tmem + w * D, p + 8 * e, d + e * (2 * C::STEP >> 4), id_o, !((v0 & kTileFirst) && e == 0));
           // (with two S buffers a move of the reference asks for it at any tile)
-          if (C::GROUPS == 1 || (v0 & 4)) tc_commit(smem_addr(&sh.pv_done[bo]));
-          tc_commit(smem_addr(&sh.slot_empty[slot_o]));
-          if (!(v0 & 2)) tc_commit(smem_addr(&sh.slot_empty[slot_o]));  // (for both)
+          if (C::DEPTH == 2 || (v0 & kTileLast)) tc_commit(smem_addr(&sh.pv_done[bo]));
+          tc_commit(smem_addr(&sh.slot_empty[slot]));
+          if (!(v0 & kTileShared)) tc_commit(smem_addr(&sh.slot_empty[slot]));  // (for both)
         }
-        if (scores) {
-          const uint64_t k = k_desc + slot_s * (C::SLOT >> 4);
-          const uint32_t d = tmem + C::S_AT + bs * C::TILE;
+        if (more) {
+          const uint32_t slot = next & 31, d = tmem + C::S_AT + bs * C::TILE;
+          const uint64_t k = k_desc + slot * (C::SLOT >> 4);
 #pragma unroll 1
           for (int c = 0; c < C::CHUNKS; ++c)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               tc_mma(d, q_desc + c * (128 * 128 >> 4) + 2 * e, k + c * (1024 >> 4) + 2 * e, id_s, c + e > 0);
           tc_commit(smem_addr(&sh.s_full[bs]));
-          tc_commit(smem_addr(&sh.slot_empty[slot_s]));
-          if (!rows) tc_commit(smem_addr(&sh.slot_empty[slot_s]));
-          if (last) tc_commit(smem_addr(&sh.q_empty[w]));
+          tc_commit(smem_addr(&sh.slot_empty[slot]));
+          if (!(next & kTileShared)) tc_commit(smem_addr(&sh.slot_empty[slot]));
+          if (next & kTileLast) tc_commit(smem_addr(&sh.q_empty[w]));
         }
         if (C::GROUPS == 2) atomicExch(&sh.lock, 0);
       }
@@ -821,11 +816,10 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         v0 = v1;
         ++o;
       }
-      if (scores) {
-        (s == o ? v0 : v1) = (ns + 1) * 8 + (last ? 4 : 0) + (rows ? 2 : 0) + (fresh ? 1 : 0);
-        loads += fresh ? 1 : 0;
-        fresh = k_there = false;
-        i += step;
+      if (more) {
+        (s == o ? v0 : v1) = next;
+        if (next & kTileFirst) ++loads;
+        known = scores = false;
         ++s;
       }
     }
@@ -848,7 +842,29 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     const bool scaled = !(a.scale_log2 > 0.f);
     const float factor = scaled ? 1.f : a.scale_log2;
     int steps = 0, n0 = 0, joins = 0, ends = 0;  // tiles done; ring index of the piece's first tile; pieces waited for
-    for (int count = -1;; ++count) {
+    // V's phase may be looked at only once its copy is issued, when the one before is over.
+    auto copied = [&](int copies) {
+      unsigned long long t0 = 0;
+      for (int polls = 0; __any_sync(kFull, lds_acquire(smem_addr(&sh.copies[wg])) < copies); ++polls) {
+        if ((polls & 63) != 63) continue;
+        const unsigned long long now = __shfl_sync(kFull, global_timer_ns(), 0);
+        if (polls == 63) t0 = now;
+        if (__any_sync(kFull, *stop)) return false;
+        if (now - t0 > kWaitLimitNs) {
+          *stop = 1;
+          if (lane == 0) flag(a.status, PKV_DEV_WAIT_TIMEOUT);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    auto ready = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&sh.warm));
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
+    if (!trial) ready();
+    for (int count = trial ? -1 : 0;; ++count) {
       const bool dry = count < 0;
       PromptPiece p{};
       if (dry) {
@@ -868,7 +884,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       const bool rows = p.mode == kPieceRows;
       const int token = tok + (rows ? wg * TQ : 0);
       const bool valid = tok < TQ && token < p.tokens;  // (dry: none)
-      const bool busy = dry || __any_sync(kFull, valid);
       int rlo = 0, rhi = 0x7fffffff;  // positions that this row sees
       if (valid) {
         rlo = p.lo;
@@ -883,47 +898,47 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int i = share.first; i < p.tiles; i += share.step, ++steps) {
-        const int b = C::GROUPS == 2 ? wg : steps & 1;
-        if (!dry) ok = wait(sh.s_full[b], C::GROUPS == 2 ? steps : steps >> 1);
+        const int b = wg * C::DEPTH + steps % C::DEPTH;
+        if (!dry) ok = wait(sh.s_full[b], steps / C::DEPTH);
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_at = tmem + lanes + C::S_AT + b * C::TILE;
         const int c0 = p.kv0 + i * C::TILE;
-        // First the maximum, 32 columns at a time; masked scores are written back. (All loops
-        // stay rolled: unrolled over the tile the code passed what an SM keeps at hand, and every
-        // warp waited for instructions, the MMA warps among them.)
+        // Masked scores are written back first, in a loop of its own: few tiles need it.
         const bool mask = __any_sync(kFull, c0 + C::TILE > rhi || c0 < rlo) || scaled || dry;
-        float top = -INFINITY;
-        const int columns = busy ? C::TILE : 0;  // (without a row of its own a warp only keeps step)
+        if (mask) {
 #pragma unroll 1
-        for (int h = 0; h < columns; h += 32) {
-          float x[32];
-          tc_ld_32x32(s_at + h, x);
-          tc_loaded(x);
-          if (mask) {
+          for (int h = 0; h < C::TILE; h += 32) {
+            float x[32];
+            tc_ld_32x32(s_at + h, x);
+            tc_loaded(x);
             const uint32_t seen = bits_below(rhi - c0 - h) & ~bits_below(rlo - c0 - h);
 #pragma unroll
             for (int c = 0; c < 32; ++c) x[c] = (seen >> c) & 1u ? x[c] * (scaled ? a.scale_log2 : 1.f) : -INFINITY;
             tc_st_32x16(s_at + h, reinterpret_cast<uint32_t*>(x));
             tc_st_32x16(s_at + h + 16, reinterpret_cast<uint32_t*>(x + 16));
           }
-          float tops[4] = {top, x[0], x[1], x[2]};
-#pragma unroll
-          for (int c = 3; c < 27; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], x[c + e], x[c + 4 + e]);
-          tops[0] = max3(tops[0], x[27], x[28]);
-          tops[1] = max3(tops[1], x[29], x[30]);
-          top = max3(max3(tops[0], tops[1], tops[2]), tops[3], x[31]);
+          tc_wait_st();
         }
-        if (mask) tc_wait_st();
+        float x[C::TILE];
+#pragma unroll
+        for (int h = 0; h < C::TILE; h += 32) tc_ld_32x32(s_at + h, x + h);
+        tc_loaded(x);
+        float tops[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int c = 4; c < C::TILE - 4; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tops[e] = max3(tops[e], x[c + e], x[c + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tops[e] = fmaxf(tops[e], x[C::TILE - 4 + e]);
+        float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
         top *= factor;
         if (__any_sync(kFull, top > m + kPromptLazy)) {
           const float now = fmaxf(m, top), al = m == -INFINITY ? 0.f : fast_exp2(m - now);
           m = now;
           l *= al;
-          if (i > share.first) {  // (all of this O's products so far are done: S came after them; but for head_dim 256)
-            if (C::GROUPS == 1) ok = wait(sh.pv_done[b ^ 1], (steps - 1) >> 1);
+          if (i > share.first) {  // (with one buffer S came after this O's products so far)
+            if (C::DEPTH == 2) ok = wait(sh.pv_done[b ^ 1], (steps - 1) >> 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t o_at = tmem + lanes + wg * D;
@@ -938,22 +953,19 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             }
           }
         }
-        // Then the weights: those of 32 columns take 16, where scores already read were.
+        // Then the weights, which take half the columns of the scores.
         const float ref = kHeadroom - (m == -INFINITY ? 0.f : m);
         const unsigned long long ref2 = pair(ref, ref), factor2 = pair(factor, factor);
         unsigned long long sum[2] = {0ull, 0ull};
-#pragma unroll 1
-        for (int h = 0; h < columns; h += 32) {
-          float x[32];
-          tc_ld_32x32(s_at + h, x);
-          tc_loaded(x);
+#pragma unroll
+        for (int h = 0; h < C::TILE; h += 32) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float2 y = unpair(fma2(pair(x[2 * e], x[2 * e + 1]), factor2, ref2));
-            w[e] = pack2<T>(fast_exp2(y.x), fast_exp2(y.y));
-            const float2 f = unpack2<T>(w[e]);
-            sum[e & 1] = add2(sum[e & 1], pair(f.x, f.y));
+            const float2 y = unpair(fma2(pair(x[h + 2 * e], x[h + 2 * e + 1]), factor2, ref2));
+            const float2 f = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            w[e] = pack2<T>(f.x, f.y);
+            sum[e & 1] = add2(sum[e & 1], pair(f.x, f.y));  // (unrounded: 4 % of a call's time otherwise, and no nearer)
           }
           tc_st_32x16(s_at + h / 2, w);
         }
@@ -963,7 +975,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           // rows that no query sees hold whatever the block holds (NaN included): as values
           // they must be zeros
           const int n = n0 - 2 * (p.tiles - i) + 1, slot = n % C::SLOTS;
-          ok = landed(n, true);
+          ok = copied(2 * steps + 2) && wait(sh.slot_full[slot], n / C::SLOTS);
           if (!ok) break;
           const int low = max(0, p.lo - c0), high = prompt_clamp(p.hi - c0, 0, C::TILE), held = min(C::TILE, (high + kBlock - 1) / kBlock * kBlock);
           for (int e = tid & 127; e < (low + held - high) * (D / 8); e += 128) {
@@ -981,8 +993,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       if (!ok) break;
       const bool joint = p.mode == kPieceSplit;  // (which has two tiles at least)
       if (p.tiles > 0 && !dry) {
-        const int last = steps - 1, b = C::GROUPS == 2 ? wg : last & 1;
-        if (!wait(sh.pv_done[b], C::GROUPS == 2 ? ends++ : last >> 1)) break;
+        const int last = steps - 1;
+        if (!wait(sh.pv_done[wg * C::DEPTH + last % C::DEPTH], C::DEPTH == 1 ? ends++ : last >> 1)) break;
         tc_fence_after();
       }
       float mine_f = 1.f, other_f = 0.f;  // factors of this warpgroup's O and of the other's
@@ -1010,7 +1022,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         part_row = p.slot == kPromptNone
                        ? a.slot_rows * size_t(2) * ctas + size_t(p.kind == kRowsMembers ? 0 : 1) * a.num_seqs * a.num_q_heads + out_row
                        : size_t(p.slot) * a.slot_rows + (rows ? wg * 128 : 0) + r;
-        if (valid && (col0 == 0)) a.part_ml[part_row] = make_float2(m, l);
+        if (valid && col0 == 0) a.part_ml[part_row] = make_float2(m - kHeadroom, l);  // (l and O are 2^kHeadroom times as large)
       }
       const uint32_t o_at = tmem + lanes;
       // Results go through shared memory, so that four lanes write 64 bytes of a row together:
@@ -1025,7 +1037,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         dst_at[k] = static_cast<T*>(a.out) + size_t(max(0, rows_at[k])) * D + 8 * (lane & 3);
       }
 #pragma unroll 1
-      for (int c = col0; c < (busy ? col0 + cols : 0); c += 32) {
+      for (int c = col0; c < col0 + cols; c += 32) {
         float o[32];
         if (p.tiles > 0) {
           tc_ld_32x32(o_at + wg * D + c, o);
@@ -1075,11 +1087,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         if (!wait(sh.join, joins++)) break;
         tc_fence_after();
       }
-      if (dry) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.warm));
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-      }
+      if (dry) ready();
     }
   }
   tc_fence_before();
@@ -1145,6 +1153,14 @@ struct PromptJoin {
       add(a, on, size_t(2 * mine + (mine == first ? 1 : 0)) * a.slot_rows + row, min(32, last - c + 1), lane);
     }
   }
+  __device__ __forceinline__ void keep(const PromptArgs& a, size_t row, int lane) {
+    if (lane == 0) a.part_ml[row] = make_float2(M, den);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = 4 * lane + 128 * v;
+      if (c < D) *reinterpret_cast<float4*>(a.part_o + row * D + c) = num[v];
+    }
+  }
   __device__ __forceinline__ void write(const PromptArgs& a, size_t row, int lane) {
     const float inv = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll
@@ -1183,8 +1199,8 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
 }
 
 // Decode behind a prefix: a warp a (sequence, query head), over the pieces of its group's
-// prefix and its own.
-template <typename T, int D>
+// prefix and its own; with TAIL the prefix alone, kept in fp32 for the grid that joins the rest.
+template <typename T, int D, bool TAIL>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
   const int lane = threadIdx.x & 31;
@@ -1201,8 +1217,10 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
     if (pass) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
       const int2* const links = a.link + h;
-      link[1] = __ldcg(links + (size_t(a.num_seqs) + s) * a.num_kv_heads);
-      if (prompt_group(a, s, &first, &end) >= 0) {
+      if (!TAIL) link[1] = __ldcg(links + (size_t(a.num_seqs) + s) * a.num_kv_heads);
+      const int group = prompt_group(a, s, &first, &end);
+      if (TAIL && hq == 0 && lane == 0) a.from[s] = group < 0 ? 0 : min(prompt_len(a, s), prompt_prefix(a, group));
+      if (group >= 0) {
         const int token = (s - first) % a.block_tokens, tile = token / a.tile_tokens;
         link[0] = __ldcg(links + size_t(s - token) * a.num_kv_heads);
         at = tile * 128 + (token - tile * a.tile_tokens) * a.group + sub;
@@ -1211,13 +1229,15 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
       }
     }
 #pragma unroll 1
-    for (int kind = first < 0 ? 1 : 0; kind < 2; ++kind) {
+    for (int kind = first < 0 ? 1 : 0; kind < (TAIL ? 1 : 2); ++kind) {
+      if (TAIL && link[kind].x < 0 && pass) return;  // (kept as it is)
       if (link[kind].x < 0)
         j.add(a, pass && lane == 0, whole + (size_t(kind) * a.num_seqs + s) * a.num_q_heads + hq, 1, lane);
       else
         j.chain(a, pass, link[kind].x, link[kind].y, kind ? sub : at, lane);
     }
-    if (pass) j.write(a, size_t(row), lane);
+    if (TAIL && pass) j.keep(a, whole + size_t(row), lane);
+    else if (pass) j.write(a, size_t(row), lane);
   }
 }
 
