@@ -80,7 +80,7 @@ struct DecodeArgs {
   const int32_t* prefix_others;  // ... the sequences outside any group
   int prefix_slots;              // ... and the grid rows reserved for chunks (num_seqs)
   float scale_log2;     // scale * log2(e)
-  // Tail grids (paged_decode_*_kernel with TAIL) only:
+  // Tail grids (paged_decode_*_kernel with TAIL, one CTA a sequence and KV head) only:
   const int32_t* query_rows;  // [S + 1]: sequence s's query is row query_rows[s] of q and out, where it has exactly
                               // one (others are left out); null: row s
   int num_rows;               // rows of q and out
@@ -498,7 +498,7 @@ __device__ __forceinline__ void finish_chunk(const DecodeArgs& a, const unsigned
                                              size_t area_bytes, int s, int g, int part, int nparts, int qrow = -1) {
   constexpr int CHUNKS = D / 8;
   const int hq0 = g * a.group;
-  const bool direct = nparts == 1;
+  const bool direct = TAIL || nparts == 1;  // (tail grids are not split)
   for (int it = threadIdx.x; it < a.group * CHUNKS; it += NW * 32) {
     const int h = it / CHUNKS, c8 = it % CHUNKS;
     float M = -INFINITY;
@@ -576,12 +576,10 @@ __device__ __forceinline__ void finish_chunk(const DecodeArgs& a, const unsigned
       num[6] = fmaf(w, x1.z, num[6]);
       num[7] = fmaf(w, x1.w, num[7]);
     }
-    if constexpr (TAIL) join_before<D>(a, row, c8, M, den, num);
     const float inv = 1.f / den;
 #pragma unroll
     for (int c = 0; c < 8; ++c) num[c] *= inv;
-    const size_t out_row = TAIL ? size_t(qrow) * a.num_q_heads + hq0 + h : row;
-    reinterpret_cast<uint4*>(static_cast<T*>(a.out) + out_row * D)[c8] = Vec8<T>::from_float(num);
+    reinterpret_cast<uint4*>(static_cast<T*>(a.out) + row * D)[c8] = Vec8<T>::from_float(num);
   }
   if (threadIdx.x == 0) *counter = 0u;  // leave the workspace ready for the next call
 }
