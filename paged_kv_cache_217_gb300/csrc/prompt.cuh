@@ -7,22 +7,31 @@
 //     S = Q K^T (fp32),  p = 2^(scale log2(e) S - m),  O += P V,  l += sum p,  out = O / l.
 // One CTA (1 per SM) takes pieces of items. An item is a block of up to 256 rows of one
 // KV head (128 with head_dim 256) and the positions that any of them sees; a piece is
-// some of its tiles of 128 tokens (64).
+// some of its tiles of 64 tokens.
 //
 // Warps: two softmax warpgroups (a thread a row of the tile), one warp each that copies
-// K and V and copies Q, and one for each warpgroup that issues its MMAs. Warpgroup w owns S_w and O_w in tensor memory
-// (S 128 columns, O head_dim). A block of more than 128 rows gives each warpgroup a tile
-// of rows and every K and V tile is used by both; a smaller one (few queries, decode)
-// gives both the same rows and every other tile, joined at the end. With head_dim 256 O
-// leaves room for one warpgroup, whose tiles alternate between two S.
-//  * S_w = Q K^T: both operands in shared memory, K-major, 128-byte swizzle.
-//  * P overwrites S_w as 16-bit values, and is the A operand from there; V is read
+// K and V and copies Q, and one for each warpgroup that issues its MMAs. Warpgroup w owns
+// O_w (head_dim columns of tensor memory) and two S of 64 columns. A block of more than
+// 128 rows gives each warpgroup a tile of rows and every K and V tile is used by both; of
+// smaller ones a long piece gives both the same rows and every other tile, joined at its
+// end, and short ones go to the warpgroups in turn. With head_dim 256 O leaves room for
+// one warpgroup.
+//  * S = Q K^T: both operands in shared memory, K-major, 128-byte swizzle.
+//  * P overwrites S as 16-bit values, and is the A operand from there; V is read
 //    MN-major from the tile as it lies.
-// While one warpgroup works on its scores the tensor cores run the other's products.
-// The running maximum is a reference that moves only when a score exceeds it by 2^8; a
-// move rescales the row's O in tensor memory. Weights are rounded to the type (bf16
-// 2^-8, fp16 2^-11 relative, one rounding a weight), and l is the fp32 sum of the rounded
-// ones, so that the error is that of a weighted mean.
+// While a warpgroup works on its scores the tensor cores run the other's products and its
+// own next scores. The running maximum is a reference that moves only when a score exceeds
+// it by 2^8; a move rescales the row's O in tensor memory (moving it with every new maximum:
+// window 194 -> 212 us, chunk 1454 -> 1549). Weights are rounded to the type (bf16 2^-8, fp16
+// 2^-11 relative, one rounding a weight), and l is the fp32 sum of the weights before that.
+//
+// Bound by the softmax warps: a tile of 64 x 256 scores takes 1700 cycles, of which the
+// products need 900 (head_dim 128) and the exponentials 512 of their unit; the rest are the
+// waits of two warps a scheduler that follow their scores step by step. Measured on GB300
+// (us, in a graph): 2048 tokens behind 15953, 96 heads of 128, 1500 (62 % of the sustained
+// library matrix product's rate); 64 prompts of 150 tokens, 32 heads on 8, 66; 4 chunks
+// of 2000 tokens, windows of 1024, 16 heads of 256 on 8, 191. Tiles of 128 tokens
+// with one S each: 78 for the 64 prompts, 1555 for the chunk.
 //
 // Tiles arrive by TMA, one copy a block, from a 4-D view of the pool {64 elements, 8
 // rows, head_dim / 64 chunks, 8-row groups}: a tile is then groups of swizzle atoms (8
@@ -44,14 +53,19 @@
 namespace pkv {
 
 constexpr int kPromptSms = 152;    // CTAs: one per SM of a GB300
-constexpr int kPromptStart = 128;  // what an item costs besides its positions, in positions
-constexpr int kPromptSnap = 512;   // cuts this near an item's end are moved there
+// What an item costs besides its positions, in positions: 64 prompts of 150 tokens take 94 us with
+// 16, 70 with 128, 74 with 384.
+constexpr int kPromptStart = 128;
+// Cuts this near an item's end are moved there: the same prompts take 82 us with 64, 70 with 256 and
+// 512; windows of 1024 198, 193 and 194.
+constexpr int kPromptSnap = 256;
 constexpr float kPromptLazy = 8.f;
 constexpr float kPromptHeadroom = 7.f;  // fp16 weights are 2^7 times as large (see kLatentHeadroom)
 constexpr int kPromptPieces = 4;   // pieces that the copying warp may be ahead
 constexpr int kPromptNone = -1;
 // A piece of one tile of rows goes to one warpgroup, the next to the other; from this many
-// positions on, or with no piece behind it, to both.
+// positions on, or with no piece behind it, to both. (256 and 4096 differ by less than 1 % in all cases
+// but one, 25.6 and 26.2 us for 8 sequences of 5 drafted tokens.)
 constexpr int kPromptSplit = 1024;
 
 template <int D>
@@ -199,7 +213,7 @@ struct PieceTiles {
 
 struct PromptShared {
   uint64_t slot_full[16], slot_empty[16];
-  uint64_t q_full[2], q_empty[2], s_full[4], p_full[4], pv_done[4], join, warm;
+  uint64_t q_full[2], q_empty[2], s_full[4], p_full[4], pv_done[4], join;
   uint64_t piece_full[kPromptPieces], piece_empty[kPromptPieces];
   uint64_t drain[2];  // after a wait gave up
   PromptPiece piece[kPromptPieces];
@@ -358,7 +372,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       mbar_init(smem_addr(&sh.pv_done[i]), 1);
     }
     mbar_init(smem_addr(&sh.join), C::SOFTMAX);
-    mbar_init(smem_addr(&sh.warm), C::SOFTMAX / 32);
 #pragma unroll 1
     for (int i = 0; i < kPromptPieces; ++i) {
       mbar_init(smem_addr(&sh.piece_full[i]), 1);
@@ -383,11 +396,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   asm volatile("griddepcontrol.launch_dependents;");
-  // What an SM has not run yet it fetches line by line, some 30 cycles an instruction: cold, this
-  // kernel took 7 us to its first product. So the code is kept short, and while the list is made
-  // the softmax warps, and for the copying warp the one of Q, run theirs once without effect.
   const bool scanner = warp >= C::SOFTMAX / 32 && warp != WARP_Q;
-  if (scanner) asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // The list: each thread of three warps sums a run of segments, a scan of the sums gives
   // every run's place, and the thread whose run holds this CTA's share's begin finds its segment.
@@ -451,21 +461,13 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
   volatile int* stop = &sh.stop;
   auto wait = [&](uint64_t& bar, int phase) { return prompt_wait(smem_addr(&bar), uint32_t(phase) & 1, stop, a.status); };
   auto test = [&](uint64_t& bar, int phase) { return bool(__all_sync(kFull, mbar_test(smem_addr(&bar), uint32_t(phase) & 1))); };
-  // (a batch whose single tokens a decode grid takes may leave nothing here)
-  const bool trial = !(a.tails && a.query_starts);
-  if (warp == WARP_KV || (warp == WARP_Q && trial)) {
+  if (warp == WARP_KV) {
     // ---- pieces, and the copies of K and V ----
-    const bool dry = warp == WARP_Q;  // (only to have the code at hand: a made-up share, and no effect)
-    if (dry) {
-      begin = 3000;
-      end = total = 1 << 20;
-      quotient = 1 << 12;
-    }
     const EvenSplit split(total, ctas, quotient);
     const int snap = int(min((long long)kPromptSnap, quotient / 16));
     // generator of pieces
-    int seg = dry ? 0 : sh.first_seg, cached = -64, h = 0, rb = 0, blocks = 0;
-    long long seg_base = dry ? 0 : sh.first_base, item = 0;
+    int seg = sh.first_seg, cached = -64, h = 0, rb = 0, blocks = 0;
+    long long seg_base = sh.first_base, item = 0;
     PromptSegment g{}, mine_g{};
     bool open = false;     // g, h, rb, item name the next item
     bool links = false, continued = false;  // what is written to desc
@@ -483,12 +485,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
             p.tiles = -1;
             return;
           }
-          if (dry) {
-            g.nq = 5 * TB;
-            g.len = 2048;
-            g.kind = kRowsCausal;
-            g.cost = prompt_cost(a, g, 5, TB);
-          } else if (listed) {
+          if (listed) {
             g = list[seg];
           } else {
             if (seg - cached >= 32) {  // the next 32 segments, one a lane
@@ -559,7 +556,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         p.kv0 = first + t0 * C::TILE;
         const bool whole = t1 - t0 == tiles;
         p.slot = whole ? kPromptNone : 2 * cta + (t0 == 0 ? 1 : 0);
-        if (lane == 0 && !dry) {
+        if (lane == 0) {
           // the shares that hold the rest: up to the one with the item's end
           int last = cta;
           if (!whole && t0 == 0) last = split.of(start + cost - 1);
@@ -658,7 +655,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           const int32_t* const this_row = row;
           const int this_nb = nb;
           generate(next);
-          if (dry) break;
           row = next_row = a.block_tables + size_t(table) * a.max_blocks_per_seq;
           nb = next_nb = (next.hi + kBlock - 1) / kBlock;
           if (next.tiles > 0) next_ids = load_ids(next.kv0 / kBlock);
@@ -666,7 +662,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           nb = this_nb;
         }
       }
-      if (!ok || dry) break;
+      if (!ok) break;
       p = next;
       first_ids = next_ids;
       row = next_row;
@@ -684,7 +680,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         }
       }
     }
-    if (lane == 0 && !dry) {
+    if (lane == 0) {
       if (a.query_starts && !links) a.desc[cta] = make_int4(0, 0, 0, -1);
       a.more[cta] = continued;
     }
@@ -692,10 +688,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       for (int i = 0; i < C::SLOTS; ++i)
         if (n > i) mbar_wait_bounded(smem_addr(&sh.slot_full[i]), uint32_t((n - 1 - i) / C::SLOTS) & 1, 10000000ull);
     }
-  }
-  if (warp == WARP_Q) {
+  } else if (warp == WARP_Q) {
     // ---- copies of Q: a tile of rows for each warpgroup that takes the piece ----
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     int loads[2] = {0, 0};
     bool ok = true;
     for (int count = 0; ok; ++count) {
@@ -733,7 +727,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     // ---- MMA issue: a warp for each warpgroup ----
     // As soon as the weights are there O += P V, and S of a tile as soon as its K and a buffer
     // are. The two warps issue by turns (`lock`), so that while one warpgroup has its products
-    // made the other makes weights: side by side both would wait for both. One lane issues, the
+    // made the other makes weights: side by side both would wait for both (a long chunk 1672 us
+    // without, 1454 with; short pieces are even). One lane issues, the
     // others keep step, so that all of it stays in uniform registers. The loop is short, without
     // waits of its own, and reads what the copying warp has worked out: every instruction between
     // two products is one that the tensor cores wait for.
@@ -751,7 +746,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       const uint32_t at = smem_addr(&bar), parity = uint32_t(phase) & 1;
       return bool(__all_sync(kFull, asleep ? mbar_try_wait(at, parity) : mbar_test(at, parity)));
     };
-    wait(sh.warm, 0);  // (the softmax warps' trial uses S and O)
     for (int polls = 0;; ++polls) {
       if (copies < 2 * s + 1 || copies < 2 * o + 2) copies = __shfl_sync(kFull, lds_acquire(copies_at), 0);
       if (!known && copies > 2 * s) {
@@ -858,32 +852,18 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       }
       return true;
     };
-    auto ready = [&]() {
+    for (int count = 0;; ++count) {
+      if (!wait(sh.piece_full[count % kPromptPieces], count / kPromptPieces)) break;
+      const PromptPiece p = sh.piece[count % kPromptPieces];
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&sh.warm));
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-    };
-    if (!trial) ready();
-    for (int count = trial ? -1 : 0;; ++count) {
-      const bool dry = count < 0;
-      PromptPiece p{};
-      if (dry) {
-        p.tiles = p.hi = 1 << 20;
-        p.mode = wg;
-        p.slot = kPromptNone;
-      } else {
-        if (!wait(sh.piece_full[count % kPromptPieces], count / kPromptPieces)) break;
-        p = sh.piece[count % kPromptPieces];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&sh.piece_empty[count % kPromptPieces]));
-      }
+      if (lane == 0) mbar_arrive(smem_addr(&sh.piece_empty[count % kPromptPieces]));
       if (p.tiles < 0) break;
       const PieceTiles share(p.mode, p.tiles, wg);
-      n0 += dry ? 0 : 2 * p.tiles;
+      n0 += 2 * p.tiles;
       if (!share.any) continue;
       const bool rows = p.mode == kPieceRows;
       const int token = tok + (rows ? wg * TQ : 0);
-      const bool valid = tok < TQ && token < p.tokens;  // (dry: none)
+      const bool valid = tok < TQ && token < p.tokens;
       int rlo = 0, rhi = 0x7fffffff;  // positions that this row sees
       if (valid) {
         rlo = p.lo;
@@ -899,13 +879,13 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       bool ok = true;
       for (int i = share.first; i < p.tiles; i += share.step, ++steps) {
         const int b = wg * C::DEPTH + steps % C::DEPTH;
-        if (!dry) ok = wait(sh.s_full[b], steps / C::DEPTH);
+        ok = wait(sh.s_full[b], steps / C::DEPTH);
         if (!ok) break;
         tc_fence_after();
         const uint32_t s_at = tmem + lanes + C::S_AT + b * C::TILE;
         const int c0 = p.kv0 + i * C::TILE;
         // Masked scores are written back first, in a loop of its own: few tiles need it.
-        const bool mask = __any_sync(kFull, c0 + C::TILE > rhi || c0 < rlo) || scaled || dry;
+        const bool mask = __any_sync(kFull, c0 + C::TILE > rhi || c0 < rlo) || scaled;
         if (mask) {
 #pragma unroll 1
           for (int h = 0; h < C::TILE; h += 32) {
@@ -986,13 +966,12 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         tc_wait_st();
-        if (dry) break;
         tc_fence_before();
         mbar_arrive(smem_addr(&sh.p_full[b]));
       }
       if (!ok) break;
       const bool joint = p.mode == kPieceSplit;  // (which has two tiles at least)
-      if (p.tiles > 0 && !dry) {
+      if (p.tiles > 0) {
         const int last = steps - 1;
         if (!wait(sh.pv_done[wg * C::DEPTH + last % C::DEPTH], C::DEPTH == 1 ? ends++ : last >> 1)) break;
         tc_fence_after();
@@ -1087,7 +1066,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         if (!wait(sh.join, joins++)) break;
         tc_fence_after();
       }
-      if (dry) ready();
     }
   }
   tc_fence_before();
