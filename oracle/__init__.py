@@ -35,6 +35,8 @@ Modules:
                     write, decode over the dequantised cache
   memsim         -- memory-utilisation replay: paged blocks against
                     contiguous pre-allocation (slot-by-slot arena)
+  prompt         -- attention of ragged queries over the paged cache (causal,
+                    windowed, cross), tables of shared prefixes, rotation
 
 Every function here is pinned by tests in ``tests/test_oracle*.py`` against
 values and invariants that the pages and mathematics fix (hand-worked
