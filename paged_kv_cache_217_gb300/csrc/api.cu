@@ -1390,7 +1390,7 @@ namespace {
 // to 8 query heads of a single token): behind prefixes all that follows them, and in a batch with
 // fewer than two query tokens a sequence those that have one. Measured on GB300, with the grid and
 // without: a token of 24 sequences over 1500 cached ones, 20 heads of 64 (480 pairs of sequence
-// and KV head) 43 and 64 us, of 92 sequences 119 and 201; 64 sequences of 40 heads of 128 behind
+// and KV head) 38 and 64 us, of 92 sequences 119 and 201; 64 sequences of 40 heads of 128 behind
 // 2000 tokens, 200 of their own 84 and 117; 64 sequences on 8 KV heads behind 512 tokens (512
 // pairs) with 60, 200 and 800 of their own 30, 44 and 90 and 35, 41 and 95. With fewer pairs than
 // fill the SMs three times a CTA a pair leaves SMs idle, and more CTAs a pair have to be joined:
