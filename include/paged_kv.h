@@ -515,11 +515,13 @@ size_t pkv_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads,
  * and its first prefix_blocks[i] blocks are those of its first sequence's
  * table, whatever the other members' tables hold there:
  *     out[s][h] = softmax_p( scale * <q[s][h], K_s[p]> ) . V_s[p],  p < L,
- * exactly as pkv_paged_attention_decode over such tables. A member shorter
- * than the prefix sees its own first L tokens of it. There is no limit on a
- * group's size or on the prefix's length (the shared-prefix schedule, -5, of
- * pkv_paged_attention_decode finds the sharing by itself, for up to 8 query
- * rows a group).
+ * the formula of pkv_paged_attention_decode over such tables. A member shorter
+ * than the prefix sees its own first L tokens of it; where all are, what lies
+ * behind the longest is not read, and its cached rows may hold anything (V of
+ * a row that some member sees must be finite for the group's others too).
+ * There is no limit on a group's size or on the prefix's length (the
+ * shared-prefix schedule, -5, of pkv_paged_attention_decode finds the sharing
+ * by itself, for up to 8 query rows a group).
  *   group_starts : int32[num_groups + 1], not decreasing, within [0, num_seqs]
  *   prefix_blocks: int32[num_groups], clamped to [0, max_blocks_per_seq]
  * Everything else as for pkv_paged_prompt_attention with one query token per

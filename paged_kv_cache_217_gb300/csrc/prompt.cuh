@@ -477,6 +477,15 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       if ((tiles - t) * C::TILE < snap || t > tiles) t = tiles;
       return int(t);
     };
+    // The longest of n <= 256 members: what of their prefix lies behind it none of them sees, so that it is
+    // neither read nor multiplied. (The list counts whole prefixes; its cuts are moved to the tiles there are.)
+    auto longest = [&](int q0, int n) {
+      int top = 0;
+#pragma unroll
+      for (int j = 0; j < 256; j += 32)
+        if (j + lane < n) top = max(top, prompt_len(a, q0 + j + lane));
+      return __reduce_max_sync(kFull, top);
+    };
     int table = 0;  // of the piece generated last
     auto generate = [&](PromptPiece& p) {
       for (;;) {
@@ -539,6 +548,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         }
         prompt_block(a, g, rb, TB, &p.lo, &p.hi, &p.base);
         const long long start = item, cost = kPromptStart + p.hi - p.lo;
+        if (g.kind == kRowsMembers) p.hi = min(p.hi, longest(g.q0 + rb * TB, min(TB, g.nq - rb * TB)));
         const int first = p.lo & ~(kBlock - 1), tiles = p.hi > p.lo ? (p.hi - first + C::TILE - 1) / C::TILE : 0;
         p.q0 = g.q0 + rb * TB;
         p.tokens = min(TB, g.nq - rb * TB);
