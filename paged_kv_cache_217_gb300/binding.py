@@ -698,7 +698,7 @@ def paged_prompt_attention(out, q, k_pool, v_pool, block_tables, context_lens, q
     _launch(q.device, "paged_prompt_attention", lib().pkv_paged_prompt_attention, out.data_ptr(), q.data_ptr(),
             k_pool.data_ptr(), v_pool.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
             query_starts.data_ptr(), T, S, Hq, hkv, D, mb, nb, float(scale), dt, int(bool(causal)),
-            max(0, int(sliding_window)), ws_ptr, ws_bytes)
+            min(max(0, int(sliding_window)), 2 ** 31 - 1), ws_ptr, ws_bytes)
     return out
 
 

@@ -166,7 +166,7 @@ __device__ __forceinline__ void prompt_block(const PromptArgs& a, const PromptSe
   if (g.kind == kRowsCausal) {
     *base = g.len - g.nq + rb * T;
     *hi = max(0, *base + min(T, g.nq - rb * T));
-    *lo = a.window ? max(0, *base - a.window + 1) : 0;
+    *lo = a.window && *base >= a.window ? *base - a.window + 1 : 0;  // (any window up to 2^31 - 1, base < 0 too)
   }
 }
 // sum over i < n of max(0, x + i T), x > -2^32
