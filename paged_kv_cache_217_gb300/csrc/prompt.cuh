@@ -923,7 +923,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         for (int e = 0; e < 4; ++e) tops[e] = fmaxf(tops[e], x[C::TILE - 4 + e]);
         float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
         top *= factor;
-        if (__any_sync(kFull, top > m + kPromptLazy)) {
+        // (rows of no query score what shared memory held before: they ask for no move, or the bits of others
+        // would depend on it)
+        if (__any_sync(kFull, valid && top > m + kPromptLazy)) {
           const float now = fmaxf(m, top), al = m == -INFINITY ? 0.f : fast_exp2(m - now);
           m = now;
           l *= al;
