@@ -490,7 +490,6 @@ __device__ __forceinline__ void join_before(const DecodeArgs& a, size_t row, int
     num[6] = fmaf(w1, x1.z, num[6]);
     num[7] = fmaf(w1, x1.w, num[7]);
   }
-  if (den == 0.f) den = 1.f;  // nothing is seen: zeros
 }
 
 template <typename T, int D, int G, int NW, bool TAIL = false>

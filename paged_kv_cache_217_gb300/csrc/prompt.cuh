@@ -1107,7 +1107,7 @@ struct PromptJoin {
     float now = fmaxf(M, ml.x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) now = fmaxf(now, __shfl_xor_sync(kFull, now, o));
-    if (now == -INFINITY) return;
+    // (a query that holds NaN has sums of NaN behind a maximum of -inf: they are joined, so that it gets NaN)
     scale(M == -INFINITY ? 0.f : fast_exp2(M - now));
     M = now;
     const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - now);
