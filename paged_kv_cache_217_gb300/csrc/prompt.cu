@@ -19,16 +19,16 @@ struct PromptShape {
 
 PromptShape prompt_shape(const PromptArgs& a, int head_dim) {
   PromptShape p;
-  const int groups = head_dim == 256 ? 1 : 2, tile = head_dim == 256 ? 64 : 128;
+  const int groups = head_dim == 256 ? 1 : 2;
   p.tile_tokens = prompt_tile_tokens(a.num_q_heads / a.num_kv_heads);
   p.block_tokens = p.tile_tokens * groups;
   p.slot_rows = a.num_tokens > p.tile_tokens ? size_t(128) * groups : 128;
   p.rows = a.query_starts ? 0 : size_t(2) * a.num_seqs * a.num_q_heads;
-  // no more shares than tiles
   const int64_t items = a.query_starts ? a.num_seqs : a.num_groups + (a.tails ? 0 : a.num_seqs);
   const int64_t blocks = int64_t(a.num_tokens) / p.block_tokens + items;
-  const int64_t tiles = blocks * a.num_kv_heads * ((int64_t(a.max_blocks_per_seq) * kBlock + tile - 1) / tile + 1);
-  p.shares = tiles < kPromptSms ? int(tiles) : kPromptSms;
+  constexpr int kShare = kPromptShareTiles * kPromptTile;
+  const int64_t most = blocks * a.num_kv_heads * ((int64_t(a.max_blocks_per_seq) * kBlock + kShare - 1) / kShare + 1);
+  p.shares = most < kPromptSms ? int(most) : kPromptSms;
   return p;
 }
 

@@ -56,6 +56,12 @@
 namespace pkv {
 
 constexpr int kPromptSms = 152;    // CTAs: one per SM of a GB300
+constexpr int kPromptTile = 64;    // tokens of a KV tile
+// Tiles of a share where there is less work than SMs: every share more is one more piece to join. 5 tokens
+// behind 4000, 8 heads on 1, take 34.3 us with one tile a share, 22.5 with two, 17.8 with three (heads of 256: 32.8,
+// 23.8, 20.3); behind 1000, 8 heads on 2, 14.7, 13.0 and 13.5 (15.9, 13.7, 14.6); one token behind 500, 4 heads of 256
+// on 1, 12.7, 11.2 and 12.4; a prompt of 300 there 20.0, 20.6 and 19.1.
+constexpr int kPromptShareTiles = 2;
 // What an item costs besides its positions, in positions: 64 prompts of 150 tokens take 94 us with
 // 16, 70 with 128, 74 with 384.
 constexpr int kPromptStart = 128;
@@ -74,7 +80,7 @@ constexpr int kPromptSplit = 1024;
 template <int D>
 struct PromptCfg {
   static constexpr int GROUPS = D == 256 ? 1 : 2;     // softmax warpgroups
-  static constexpr int TILE = 64;                     // tokens
+  static constexpr int TILE = kPromptTile;
   static constexpr int ROWS = 128 * GROUPS;           // of an item
   static constexpr int CHUNKS = D / 64;
   static constexpr int SLOT = TILE * D * 2;           // bytes of a K or V tile
@@ -82,7 +88,7 @@ struct PromptCfg {
   static constexpr int Q_TILE = 128 * D * 2;
   static constexpr int SOFTMAX = 128 * GROUPS;        // threads
   static constexpr int THREADS = SOFTMAX + 128;
-  static constexpr int DEPTH = TILE == 64 ? 2 : 1;    // S buffers of a warpgroup
+  static constexpr int DEPTH = 2;                     // S buffers of a warpgroup
   static constexpr int STAGE = 2048;                  // bytes a softmax warp writes its output through
   static constexpr int STEP = CHUNKS * 1024;          // bytes of 8 tokens
   static constexpr int S_AT = GROUPS * D;             // columns of tensor memory: O, then two S
@@ -805,8 +811,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
 #pragma unroll 1
           for (int e = 0; e < C::TILE / 16; ++e)
             tc_mma_ts(tmem + w * D, p + 8 * e, d + e * (2 * C::STEP >> 4), id_o, !((v0 & kTileFirst) && e == 0));
-          // (with two S buffers a move of the reference asks for it at any tile)
-          if (C::DEPTH == 2 || (v0 & kTileLast)) tc_commit(smem_addr(&sh.pv_done[bo]));
+          tc_commit(smem_addr(&sh.pv_done[bo]));
           tc_commit(smem_addr(&sh.slot_empty[slot]));
           if (!(v0 & kTileShared)) tc_commit(smem_addr(&sh.slot_empty[slot]));  // (for both)
         }
@@ -855,7 +860,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     // the maximum.
     const bool scaled = !(a.scale_log2 > 0.f);
     const float factor = scaled ? 1.f : a.scale_log2;
-    int steps = 0, n0 = 0, joins = 0, ends = 0;  // tiles done; ring index of the piece's first tile; pieces waited for
+    int steps = 0, n0 = 0, joins = 0;  // tiles done; ring index of the piece's first tile; joins waited for
     // V's phase may be looked at only once its copy is issued, when the one before is over.
     auto copied = [&](int copies) {
       unsigned long long t0 = 0;
@@ -939,8 +944,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           const float now = fmaxf(m, top), al = m == -INFINITY ? 0.f : fast_exp2(m - now);
           m = now;
           l *= al;
-          if (i > share.first) {  // (with one buffer S came after this O's products so far)
-            if (C::DEPTH == 2) ok = wait(sh.pv_done[b ^ 1], (steps - 1) >> 1);
+          if (i > share.first) {  // O's products so far come before its rescaling
+            ok = wait(sh.pv_done[b ^ 1], (steps - 1) / C::DEPTH);
             if (!ok) break;
             tc_fence_after();
             const uint32_t o_at = tmem + lanes + wg * D;
@@ -994,7 +999,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       const bool joint = p.mode == kPieceSplit;  // (which has two tiles at least)
       if (p.tiles > 0) {
         const int last = steps - 1;
-        if (!wait(sh.pv_done[wg * C::DEPTH + last % C::DEPTH], C::DEPTH == 1 ? ends++ : last >> 1)) break;
+        if (!wait(sh.pv_done[wg * C::DEPTH + last % C::DEPTH], last / C::DEPTH)) break;
         tc_fence_after();
       }
       float mine_f = 1.f, other_f = 0.f;  // factors of this warpgroup's O and of the other's
