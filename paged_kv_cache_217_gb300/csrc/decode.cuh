@@ -461,15 +461,7 @@ __device__ __forceinline__ void decode_tile(uint32_t kt, uint32_t vt, int lo, in
   }
 }
 
-// Epilogue shared by the decode kernels. On entry every warp w has published
-// its running sums for the chunk in its own shared-memory area
-// (smem + w * area_bytes): acc[G][D], then m[G], then l[G] (log2 domain), and
-// the CTA has synchronised. The warps are merged by rescaling each to the
-// common max; a sequence that fits one partition is finished here. Otherwise
-// the partition's (m, l, o) go to the workspace and the last partition of the
-// (sequence, KV head) to arrive merges all of them by log-sum-exp:
-//   M = max_p m_p,  w_p = 2^(m_p - M),  out = sum_p w_p o_p / sum_p w_p l_p.
-// A tail grid joins what precedes the tail to the result, and writes it to row `qrow`.
+// What precedes a row's tail, joined to the tail's maximum, sum and 8 columns of its output.
 template <int D>
 __device__ __forceinline__ void join_before(const DecodeArgs& a, size_t row, int c8, float M, float& den, float (&num)[8]) {
   const float2 ml = a.join_ml ? __ldcg(a.join_ml + row) : make_float2(-INFINITY, 0.f);
@@ -492,6 +484,15 @@ __device__ __forceinline__ void join_before(const DecodeArgs& a, size_t row, int
   }
 }
 
+// Epilogue shared by the decode kernels. On entry every warp w has published
+// its running sums for the chunk in its own shared-memory area
+// (smem + w * area_bytes): acc[G][D], then m[G], then l[G] (log2 domain), and
+// the CTA has synchronised. The warps are merged by rescaling each to the
+// common max; a sequence that fits one partition is finished here. Otherwise
+// the partition's (m, l, o) go to the workspace and the last partition of the
+// (sequence, KV head) to arrive merges all of them by log-sum-exp:
+//   M = max_p m_p,  w_p = 2^(m_p - M),  out = sum_p w_p o_p / sum_p w_p l_p.
+// A tail grid joins what precedes the tail to the result, and writes it to row `qrow`.
 template <typename T, int D, int G, int NW, bool TAIL = false>
 __device__ __forceinline__ void finish_chunk(const DecodeArgs& a, const unsigned char* smem,
                                              size_t area_bytes, int s, int g, int part, int nparts, int qrow = -1) {

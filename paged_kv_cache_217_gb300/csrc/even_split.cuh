@@ -1,4 +1,4 @@
-// The work lists of the 4-bit and the latent decode, cut into ranges.
+// The work lists of the 4-bit and the latent decode and of the prompt kernels, cut into ranges.
 #pragma once
 
 namespace pkv {

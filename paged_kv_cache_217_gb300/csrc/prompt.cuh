@@ -50,8 +50,8 @@
 
 #include "device_common.cuh"
 #include "even_split.cuh"
-#include "latent_decode.cuh"
 #include "launch.h"
+#include "tcgen05.cuh"
 
 namespace pkv {
 
@@ -69,7 +69,9 @@ constexpr int kPromptStart = 128;
 // 512; windows of 1024 198, 193 and 194.
 constexpr int kPromptSnap = 256;
 constexpr float kPromptLazy = 8.f;
-constexpr float kPromptHeadroom = 7.f;  // fp16 weights are 2^7 times as large (see kLatentHeadroom)
+// fp16 weights are 2^7 times as large, 2^(7 + 8) at most: one 2^-21 of the largest still has all its bits, and what
+// fp16 loses of smaller ones is at most 2^-32 of the largest.
+constexpr float kPromptHeadroom = 7.f;
 constexpr int kPromptPieces = 4;   // pieces that the copying warp may be ahead
 constexpr int kPromptNone = -1;
 // A piece of one tile of rows goes to one warpgroup, the next to the other; from this many
