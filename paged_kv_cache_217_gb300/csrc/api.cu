@@ -1387,14 +1387,16 @@ pkv_status_t pkv_rotary_and_cache(void* q_out, const void* q, const void* k, con
 namespace {
 
 // Whether a decode grid takes part in a call of the prompt kernels (which give 128 rows to the 1
-// to 8 query heads of a single token): behind prefixes all that follows them, and in a batch with
-// fewer than two query tokens a sequence those that have one. Measured on GB300, with the grid and
-// without: a token of 24 sequences over 1500 cached ones, 20 heads of 64 (480 pairs of sequence
-// and KV head) 38 and 64 us, of 92 sequences 119 and 201; 64 sequences of 40 heads of 128 behind
-// 2000 tokens, 200 of their own 84 and 117; 64 sequences on 8 KV heads behind 512 tokens (512
-// pairs) with 60, 200 and 800 of their own 30, 44 and 90 and 35, 41 and 95. With fewer pairs than
-// fill the SMs three times a CTA a pair leaves SMs idle, and more CTAs a pair have to be joined:
-// 32 sequences (256 pairs), 200 of their own, 37 and 26.
+// to 8 query heads of a single token): behind prefixes what follows them, and in a batch with
+// fewer than two query tokens a sequence those that have one; on the GPU the kernels keep what is
+// too long for one CTA a KV head. Measured on GB300 (us in a graph, one build), with the grid and
+// without. One token over 1500 cached ones, 20 heads of 64: 24 sequences (480 pairs of sequence
+// and KV head) 38.5 and 62, 92 115 and 199; over 600, 32 heads of 128 on 8: 57 (456 pairs) 34.5
+// and 38, 128 59.5 and 79. Behind 512 shared tokens with 60, 200 and 800 of their own: 57
+// sequences 30.5, 41.4 and 84 against 31.7, 41.3 and 79, 64 31, 43 and 87 against 33, 46 and 83,
+// 128 38, 58 and 124 against 51, 72 and 167, but 32 (256 pairs) 28, 37 and 75 against 23, 26 and
+// 43; 64 of 40 heads, 200 behind 2000, 79 against 112. So behind prefixes the two are even where
+// the pairs fill the SMs three times; single tokens alone would gain from 160 pairs on (27 and 29).
 constexpr int64_t kTailPairs = 3 * 152;
 bool prompt_tails(const pkv::PromptArgs& a) {
   if (a.num_q_heads / a.num_kv_heads > 8 || int64_t(a.num_seqs) * a.num_kv_heads < kTailPairs) return false;
@@ -1469,8 +1471,9 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
     d.scale_log2 = scale_log2;
     d.query_rows = a.query_starts;
     d.num_rows = a.num_tokens;
+    const pkv::PromptTails t = pkv::prompt_tails(a, head_dim, workspace);
+    d.tail_limit = t.limit;
     if (prefix && a.num_groups > 0) {
-      const pkv::PromptTails t = pkv::prompt_tails(a, head_dim, workspace);
       d.from = t.from;
       d.join_ml = t.ml;
       d.join_o = t.o;
@@ -1482,26 +1485,11 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
     }
   }
   const EnqueueLock lock(stream);
-  // The prefixes come before what is joined to them; sequences with one token go first.
-  cudaError_t err = cudaSuccess;
-  for (int step = 0; step < 2 && err == cudaSuccess; ++step) {
-    if ((step == 0) == prefix) {
-      if (prefix && a.tails && a.num_groups == 0) continue;
-      err = pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, maps, stream);
-    } else if (a.tails) {
-      err = pkv::launch_decode_tail(d, dtype == PKV_BF16, head_dim, round_pow2_group(a.group), kmap, vmap, stream);
-    }
-  }
+  // The prompt kernels choose what the grid takes, and prefixes come before what is joined to them.
+  cudaError_t err = pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, maps, stream);
+  if (err == cudaSuccess && a.tails)
+    err = pkv::launch_decode_tail(d, dtype == PKV_BF16, head_dim, round_pow2_group(a.group), kmap, vmap, stream);
   return cuda_status(err, what);
-}
-
-// Bytes that a call of these sizes needs whatever its pools are.
-size_t prompt_bytes(pkv::PromptArgs a, int head_dim) {
-  a.tails = false;
-  const size_t alone = pkv::prompt_workspace_bytes(a, head_dim);
-  a.tails = true;
-  const size_t with_tails = pkv::prompt_workspace_bytes(a, head_dim);
-  return alone > with_tails ? alone : with_tails;
 }
 
 // Sizes of a call as prompt_workspace_bytes reads them; false for ones that no call takes.
@@ -1531,7 +1519,7 @@ size_t pkv_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads, 
   if (!prompt_sizes(&a, num_tokens, num_seqs, 0, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)) return 0;
   static const int32_t ragged = 0;
   a.query_starts = &ragged;  // (only whether there are any matters)
-  return prompt_bytes(a, head_dim);
+  return pkv::prompt_workspace_bytes(a, head_dim);
 }
 
 pkv_status_t pkv_paged_prompt_attention(void* out, const void* q, const void* k_pool, const void* v_pool,
@@ -1568,7 +1556,7 @@ size_t pkv_prefix_workspace_size(int num_seqs, int num_groups, int num_q_heads, 
                                  int max_blocks_per_seq) {
   pkv::PromptArgs a;
   if (!prompt_sizes(&a, num_seqs, num_seqs, num_groups, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq)) return 0;
-  return prompt_bytes(a, head_dim);
+  return pkv::prompt_workspace_bytes(a, head_dim);
 }
 
 pkv_status_t pkv_paged_prefix_decode(void* out, const void* q, const void* k_pool, const void* v_pool,

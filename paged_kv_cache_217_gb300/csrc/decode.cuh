@@ -84,6 +84,7 @@ struct DecodeArgs {
   const int32_t* query_rows;  // [S + 1]: sequence s's query is row query_rows[s] of q and out, where it has exactly
                               // one (others are left out); null: row s
   int num_rows;               // rows of q and out
+  const int* tail_limit;      // longer tails are left out
   const int32_t* from;        // [S]: positions before from[s] (a multiple of 16, or the length) are left out; null: none
   const float2* join_ml;      // [S][Hq] (max, sum) and [S][Hq][D] unnormalised sums over positions before from[s], joined
   const float* join_o;        // to the tail's; null: none
@@ -616,14 +617,17 @@ paged_decode_kernel(const DecodeArgs a) {
     if (j0 < a.max_blocks_per_seq) ids_early = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + j0);
   }
   int L = a.context_lens[s];
+  const int tail_limit = TAIL ? __ldcg(a.tail_limit) : 0;
   const int max_len = a.max_blocks_per_seq * kBlock;
   if (L < 0 || L > max_len) {
     if (threadIdx.x == 0 && part == 0 && g == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
     L = L < 0 ? 0 : max_len;
   }
   TokenRange tr = token_range(L, a.window);
-  if constexpr (TAIL)
+  if constexpr (TAIL) {
     if (a.from) tr = tail_range(tr, L, a.from[s]);
+    if (L - tr.first > tail_limit) return;
+  }
   const int nparts = L <= tr.aligned ? 1 : (L - tr.aligned + a.part_tokens - 1) / a.part_tokens;
   if (part >= nparts) return;
   const int pslot = part;  // partition slot of this CTA's partial in the workspace

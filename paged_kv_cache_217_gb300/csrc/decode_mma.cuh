@@ -337,6 +337,7 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
     if (j0 < a.max_blocks_per_seq) ids_early = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + j0);
   }
   int L = a.context_lens[s];
+  const int tail_limit = TAIL ? __ldcg(a.tail_limit) : 0;
   // Q as the A operand: row gr holds query head hq0 + gr (zero past the group);
   // the block ids, the length and Q are all requested before the speculative
   // copies below and before anything waits for them.
@@ -410,8 +411,10 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
       reinterpret_cast<uint4*>(o)[i] = make_uint4(0u, 0u, 0u, 0u);
   };
   TokenRange tr = token_range(L, a.window);
-  if constexpr (TAIL)
+  if constexpr (TAIL) {
     if (a.from) tr = tail_range(tr, L, a.from[s]);
+    if (L - tr.first > tail_limit) return;
+  }
   const int nparts = L <= tr.aligned ? 1 : (L - tr.aligned + a.part_tokens - 1) / a.part_tokens;
   if (part >= nparts) return;  // (split grids only; no speculative copies there)
   const int pslot = part;  // partition slot of this CTA's partial in the workspace

@@ -189,7 +189,8 @@ struct PromptArgs {
   int causal;
   int window;        // causal: attend over the last `window` tokens (0 = all)
   float scale_log2;  // scale * log2(e)
-  int tails;         // a decode grid takes sequences with one query token (prompts), and what follows the prefixes
+  int tails;         // a decode grid takes sequences with one query token (prompts), and what follows the prefixes, but
+                     // for the longest
   // set by the launcher: query tokens of a tile of rows and of a block, CTAs, rows of a
   // slot of partial results, and the workspace's parts
   int tile_tokens, block_tokens, shares;
@@ -200,10 +201,12 @@ struct PromptArgs {
   float2* part_ml;
   float* part_o;
   int32_t* from;  // per sequence, where its prefix ends (prefix decode with tails)
+  int* limit;     // positions up to which the decode grid takes a single token (tails)
 };
-// What a tail grid behind a prefix reads of the workspace: from, and the partial results of
-// the prefixes per (sequence, query head).
+// What a tail grid reads of the workspace: the limit; behind prefixes from, and their partial
+// results per (sequence, query head).
 struct PromptTails {
+  const int* limit;
   const int32_t* from;
   const float2* ml;
   const float* o;

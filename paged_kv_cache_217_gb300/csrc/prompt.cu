@@ -24,8 +24,7 @@ PromptShape prompt_shape(const PromptArgs& a, int head_dim) {
   p.block_tokens = p.tile_tokens * groups;
   p.slot_rows = a.num_tokens > p.tile_tokens ? size_t(128) * groups : 128;
   p.rows = a.query_starts ? 0 : size_t(2) * a.num_seqs * a.num_q_heads;
-  const int64_t items = a.query_starts ? a.num_seqs : a.num_groups + (a.tails ? 0 : a.num_seqs);
-  const int64_t blocks = int64_t(a.num_tokens) / p.block_tokens + items;
+  const int64_t blocks = int64_t(a.num_tokens) / p.block_tokens + a.num_groups + a.num_seqs;
   constexpr int kShare = kPromptShareTiles * kPromptTile;
   const int64_t most = blocks * a.num_kv_heads * ((int64_t(a.max_blocks_per_seq) * kBlock + kShare - 1) / kShare + 1);
   p.shares = most < kPromptSms ? int(most) : kPromptSms;
@@ -59,7 +58,7 @@ cudaError_t launch_t(const PromptArgs& a, int head_dim, const PromptMaps& maps, 
 
 namespace {
 // Per share: what is cut; per item (prefix decode): where its pieces are; whether shares begin
-// inside an item; where prefixes end; then fp32 accumulators and (maximum, sum) pairs of two
+// inside an item; where prefixes end; what the decode grid takes; then fp32 accumulators and (maximum, sum) pairs of two
 // slots a share and of kept rows.
 size_t lay_out(PromptArgs* a, int head_dim, char* workspace) {
   const PromptShape p = prompt_shape(*a, head_dim);
@@ -78,6 +77,7 @@ size_t lay_out(PromptArgs* a, int head_dim, char* workspace) {
   a->link = reinterpret_cast<int2*>(links);
   a->more = reinterpret_cast<int*>(take(size_t(p.shares) * sizeof(int)));
   a->from = reinterpret_cast<int32_t*>(take(size_t(a->num_seqs) * sizeof(int32_t)));
+  a->limit = reinterpret_cast<int*>(take(sizeof(int)));
   const size_t rows = p.slot_rows * 2 * p.shares + p.rows;
   a->part_o = reinterpret_cast<float*>(take(rows * head_dim * sizeof(float)));
   a->part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
@@ -93,7 +93,7 @@ size_t prompt_workspace_bytes(const PromptArgs& a, int head_dim) {
 PromptTails prompt_tails(PromptArgs a, int head_dim, void* workspace) {
   lay_out(&a, head_dim, static_cast<char*>(workspace));
   const size_t kept = a.slot_rows * 2 * a.shares;
-  return {a.from, a.part_ml + kept, a.part_o + kept * head_dim};
+  return {a.limit, a.from, a.part_ml + kept, a.part_o + kept * head_dim};
 }
 
 cudaError_t launch_prompt(PromptArgs a, bool bf16, int head_dim, void* workspace, const PromptMaps& maps,

@@ -68,6 +68,14 @@ constexpr int kPromptStart = 128;
 // Cuts this near an item's end are moved there: the same prompts take 82 us with 64, 70 with 256 and
 // 512; windows of 1024 198, 193 and 194.
 constexpr int kPromptSnap = 256;
+// A decode grid gives a single token one CTA a KV head, whose rate is near an SM's share of the memory's. One that
+// would take kTailShares times as long as an even share of all single tokens is cut into pieces here instead. 60 tokens
+// over 600 positions and one over 65000, 32 heads on 8: 991 us uncut, 95 cut, over 8000 143 and 58; 64 places with two
+// tokens over 30000 469 and 66; behind a prefix 63 x 100 and one of 20000 329 and 66. Finding out costs tokens of equal
+// lengths nothing measurable, and what follows prefixes 2 us.
+constexpr int kTailShares = 2;
+constexpr int kTailShort = 1024;  // (never worth that: 59 over 100 and one over 1000 26.9 us, over 1500 35.0 uncut and 29.7)
+constexpr int kTailAll = 0x7fffffff;
 constexpr float kPromptLazy = 8.f;
 // fp16 weights are 2^7 times as large, 2^(7 + 8) at most: one 2^-21 of the largest still has all its bits, and what
 // fp16 loses of smaller ones is at most 2^-32 of the largest.
@@ -141,7 +149,6 @@ __device__ __forceinline__ PromptSegment prompt_segment(const PromptArgs& a, int
   if (a.query_starts) {
     g.q0 = prompt_clamp(a.query_starts[i], 0, a.num_tokens);
     g.nq = prompt_clamp(a.query_starts[i + 1], g.q0, a.num_tokens) - g.q0;
-    if (a.tails && g.nq == 1) g.nq = 0;
     g.table = i;
     g.lo = 0;
     g.len = prompt_len(a, i);
@@ -165,6 +172,12 @@ __device__ __forceinline__ PromptSegment prompt_segment(const PromptArgs& a, int
     g.kind = kRowsAll;
   }
   return g;
+}
+
+// Whether the decode grid takes a segment: one query token of a sequence that sees up to `limit` positions.
+__device__ __forceinline__ bool prompt_single(const PromptArgs& a, const PromptSegment& g, int limit) {
+  if (!a.tails || g.kind == kRowsMembers || g.nq != 1) return false;
+  return (a.window ? min(g.len - g.lo, a.window) : g.len - g.lo) <= limit;
 }
 
 // Positions [lo, hi) that block rb of T tokens of a segment sees, and the position of
@@ -228,9 +241,11 @@ struct PromptShared {
   uint64_t piece_full[kPromptPieces], piece_empty[kPromptPieces];
   uint64_t drain[2];  // after a wait gave up
   PromptPiece piece[kPromptPieces];
-  long long scan[12];
+  long long scan[3];
+  float sums[4];
+  int most[4];
   long long first_base;
-  int first_seg;
+  int first_seg, limit;
   uint32_t tmem;
   int stop;    // a wait gave up: every role leaves
   int lock;    // a warp issues its MMAs
@@ -420,39 +435,97 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
   // The list: each thread of three warps sums a run of segments, a scan of the sums gives
   // every run's place, and the thread whose run holds this CTA's share's begin finds its segment.
   const int TQ = a.tile_tokens, TB = TQ * C::GROUPS;  // tokens of a tile of rows, and of a block
-  const int segs = a.num_groups + (a.tails && !a.query_starts ? 0 : a.num_seqs), cta = int(blockIdx.x), ctas = int(gridDim.x);
-  const bool listed = segs <= C::LISTED;
+  const int cta = int(blockIdx.x), ctas = int(gridDim.x);
   long long begin = 0, end = 0, total = 0, quotient = 0;
+  // The decode grid takes single tokens of up to `limit` positions: all, until it is known that some are too long.
+  int limit = kTailAll, segs = a.num_groups + (a.tails && !a.query_starts ? 0 : a.num_seqs);
+  auto segment = [&](int i) {
+    PromptSegment g = prompt_segment(a, i);
+    if (prompt_single(a, g, limit)) g.nq = 0;
+    g.cost = g.nq ? prompt_cost(a, g, (g.nq + TB - 1) / TB, TB) : 0;
+    return g;
+  };
+  if (a.tails && warp < 4) {
+    // meanwhile softmax warps sum what single tokens see, and one of them works out the limit
+    float sum = 0.f;  // (fp32 is near enough for a limit)
+    int most = 0;
+#pragma unroll 1
+    for (int s = tid; s < a.num_seqs; s += 128) {
+      int n = prompt_len(a, s);
+      if (a.window) n = min(n, a.window);
+      if (a.query_starts) {
+        const int q0 = prompt_clamp(a.query_starts[s], 0, a.num_tokens);
+        if (prompt_clamp(a.query_starts[s + 1], q0, a.num_tokens) - q0 != 1) n = 0;
+      } else {
+        int first, last;
+        const int group = prompt_group(a, s, &first, &last);
+        if (group >= 0) n -= min(n, prompt_prefix(a, group));
+      }
+      sum += float(n);
+      most = max(most, n);
+    }
+    most = __reduce_max_sync(kFull, most);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) {
+      sh.sums[warp] = sum;
+      sh.most[warp] = most;
+    }
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+    if (warp == 0) {
+      const float even = (sh.sums[0] + sh.sums[1] + sh.sums[2] + sh.sums[3]) * (float(a.num_kv_heads) / kPromptSms);
+      const float least = fmaxf(kTailShort, kTailShares * even);
+      const int top = max(max(sh.most[0], sh.most[1]), max(sh.most[2], sh.most[3]));
+      if (lane == 0) {
+        sh.limit = float(top) <= least ? kTailAll : int(least);
+        if (cta == 0) *a.limit = sh.limit;
+      }
+      asm volatile("bar.arrive 1, 128;" ::: "memory");
+    }
+  }
   if (scanner) {
     const int part = warp == WARP_KV ? 0 : warp - WARP_MMA + 1, runner = part * 32 + lane;
-    const int per = (segs + 95) / 96, run0 = min(segs, runner * per), run1 = min(segs, run0 + per);
-    long long mine = 0;
+    int run0, run1;
+    bool listed;
+    long long at, mine;
+    for (bool again = false;;) {
+      const int per = (segs + 95) / 96;
+      run0 = min(segs, runner * per);
+      run1 = min(segs, run0 + per);
+      listed = segs <= C::LISTED;
+      mine = 0;
 #pragma unroll 1
-    for (int i = run0; i < run1; ++i) {
-      PromptSegment g = prompt_segment(a, i);
-      g.cost = g.nq ? prompt_cost(a, g, (g.nq + TB - 1) / TB, TB) : 0;
-      mine += g.cost * a.num_kv_heads;
-      if (listed) list[i] = g;
-      if (cta == 0) {
-        const int s = i - a.num_groups;
-        if (s >= 0 && (a.context_lens[s] < 0 || a.context_lens[s] > a.max_blocks_per_seq * kBlock))
-          flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
-        const int32_t* starts = a.query_starts ? a.query_starts : i < a.num_groups ? a.group_starts : nullptr;
-        if (starts && (starts[i] < 0 || starts[i + 1] < starts[i] || starts[i + 1] > a.num_tokens))
-          flag(a.status, PKV_DEV_BAD_START);
+      for (int i = run0; i < run1; ++i) {
+        const PromptSegment g = segment(i);
+        mine += g.cost * a.num_kv_heads;
+        if (listed) list[i] = g;
+        if (cta == 0) {
+          const int s = i - a.num_groups;
+          if (s >= 0 && (a.context_lens[s] < 0 || a.context_lens[s] > a.max_blocks_per_seq * kBlock))
+            flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);
+          const int32_t* starts = a.query_starts ? a.query_starts : i < a.num_groups ? a.group_starts : nullptr;
+          if (starts && (starts[i] < 0 || starts[i + 1] < starts[i] || starts[i + 1] > a.num_tokens))
+            flag(a.status, PKV_DEV_BAD_START);
+        }
       }
-    }
-    long long upto = mine;
+      at = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(kFull, upto, o);
-      if (lane >= o) upto += x;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(kFull, at, o);
+        if (lane >= o) at += x;
+      }
+      if (lane == 31) sh.scan[part] = at;
+      asm volatile("bar.sync 1, %0;" ::"r"(a.tails && !again ? 128 : 96) : "memory");
+      if (!a.tails || again) break;
+      again = true;
+      limit = sh.limit;
+      if (limit == kTailAll) break;
+      segs = a.num_groups + a.num_seqs;
+      asm volatile("bar.sync 1, 96;" ::: "memory");
     }
-    if (lane == 31) sh.scan[part] = upto;
-    asm volatile("bar.sync 1, 96;" ::: "memory");
     const long long s0 = sh.scan[0], s1 = sh.scan[1];
     total = s0 + s1 + sh.scan[2];
-    long long at = upto - mine + (part > 0 ? s0 : 0) + (part > 1 ? s1 : 0);
+    at += (part > 0 ? s0 : 0) + (part > 1 ? s1 : 0) - mine;
     quotient = total >> 32 ? total / ctas : (long long)(unsigned(total) / unsigned(ctas));
     const EvenSplit split(total, ctas, quotient);
     begin = split.begin(cta);
@@ -461,13 +534,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       int i = run0;
 #pragma unroll 1
       for (; i + 1 < run1; ++i) {
-        long long c;
-        if (listed) {
-          c = list[i].cost;
-        } else {
-          const PromptSegment g = prompt_segment(a, i);
-          c = g.nq ? prompt_cost(a, g, (g.nq + TB - 1) / TB, TB) : 0;
-        }
+        const long long c = listed ? list[i].cost : segment(i).cost;
         if (at + c * a.num_kv_heads > begin) break;
         at += c * a.num_kv_heads;
       }
@@ -482,6 +549,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
   if (warp == WARP_KV) {
     // ---- pieces, and the copies of K and V ----
     const EvenSplit split(total, ctas, quotient);
+    const bool listed = segs <= C::LISTED;
     const int snap = int(min((long long)kPromptSnap, quotient / 16));
     // generator of pieces
     int seg = sh.first_seg, cached = -64, h = 0, rb = 0, blocks = 0;
@@ -517,10 +585,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
           } else {
             if (seg - cached >= 32) {  // the next 32 segments, one a lane
               cached = seg;
-              if (seg + lane < segs) {
-                mine_g = prompt_segment(a, seg + lane);
-                mine_g.cost = mine_g.nq ? prompt_cost(a, mine_g, (mine_g.nq + TB - 1) / TB, TB) : 0;
-              }
+              if (seg + lane < segs) mine_g = segment(seg + lane);
             }
             const int src = seg - cached;
             g.q0 = __shfl_sync(kFull, mine_g.q0, src);
@@ -1159,6 +1224,14 @@ struct PromptJoin {
       add(a, on, size_t(2 * mine + (mine == first ? 1 : 0)) * a.slot_rows + row, min(32, last - c + 1), lane);
     }
   }
+  // a sequence's part behind its prefix: cut, or whole
+  __device__ __forceinline__ void own(const PromptArgs& a, int s, int hq, int h, int sub, int lane) {
+    const int2 at = __ldcg(a.link + h + (size_t(a.num_seqs) + s) * a.num_kv_heads);
+    if (at.x >= 0)
+      chain(a, at.x, at.y, sub, lane);
+    else
+      add(a, lane == 0, a.slot_rows * size_t(2) * a.shares + (size_t(a.num_seqs) + s) * a.num_q_heads + hq, 1, lane);
+  }
   __device__ __forceinline__ void keep(const PromptArgs& a, size_t row, int lane) {
     if (lane == 0) a.part_ml[row] = make_float2(M, den);
 #pragma unroll
@@ -1200,8 +1273,19 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(const PromptArgs a) {
   }
 }
 
+// A sequence behind a prefix that is too long for the decode grid: what is kept of its prefix and its own pieces.
+template <typename T, int D>
+__device__ __noinline__ void prefix_join_long(const PromptArgs& a, size_t kept, int s, int hq, int lane) {
+  const int h = hq / a.group;
+  PromptJoin<T, D> j;
+  j.add(a, lane == 0, kept, 1, lane);
+  j.own(a, s, hq, h, hq - h * a.group, lane);
+  j.write(a, size_t(s) * a.num_q_heads + hq, lane);
+}
+
 // Decode behind a prefix: a warp a (sequence, query head), over the pieces of its group's
-// prefix and its own; with TAIL the prefix alone, kept in fp32 for the grid that joins the rest.
+// prefix and its own; with TAIL, where a decode grid takes the rest, the prefix alone, kept in
+// fp32 for the grid.
 template <typename T, int D, bool TAIL>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   asm volatile("griddepcontrol.launch_dependents;");
@@ -1212,29 +1296,29 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PromptArgs a) {
   const size_t whole = a.slot_rows * size_t(2) * a.shares;  // rows of items that are not cut: prefixes, then own parts
   asm volatile("griddepcontrol.wait;" ::: "memory");
   PromptJoin<T, D> j;
-  const int2* const links = a.link + h;
+  const int limit = TAIL ? __ldcg(a.limit) : 0;
   int first, end;
   const int group = prompt_group(a, s, &first, &end);
   if (TAIL && hq == 0 && lane == 0) a.from[s] = group < 0 ? 0 : min(prompt_len(a, s), prompt_prefix(a, group));
+  bool kept = false;  // as it is to be kept
   if (group >= 0) {
     const int token = (s - first) % a.block_tokens, tile = token / a.tile_tokens;
-    const int2 at = __ldcg(links + size_t(s - token) * a.num_kv_heads);
+    const int2 at = __ldcg(a.link + h + size_t(s - token) * a.num_kv_heads);
     if (at.x >= 0)
       j.chain(a, at.x, at.y, tile * 128 + (token - tile * a.tile_tokens) * a.group + sub, lane);
     else if (TAIL)
-      return;  // (kept as it is)
+      kept = true;
     else
       j.add(a, lane == 0, whole + size_t(row), 1, lane);
   }
   if (TAIL) {
-    j.keep(a, whole + size_t(row), lane);
+    if (!kept) j.keep(a, whole + size_t(row), lane);
+    if (limit == kTailAll) return;
+    const int len = prompt_len(a, s);
+    if ((group < 0 ? len : len - prompt_prefix(a, group)) > limit) prefix_join_long<T, D>(a, whole + size_t(row), s, hq, lane);
     return;
   }
-  const int2 own = __ldcg(links + (size_t(a.num_seqs) + s) * a.num_kv_heads);
-  if (own.x >= 0)
-    j.chain(a, own.x, own.y, sub, lane);
-  else
-    j.add(a, lane == 0, whole + (size_t(a.num_seqs) + s) * a.num_q_heads + hq, 1, lane);
+  j.own(a, s, hq, h, sub, lane);
   j.write(a, size_t(row), lane);
 }
 
