@@ -480,7 +480,8 @@ pkv_status_t pkv_rotary_and_cache(
  *              W = sliding_window (<= 0: no window)
  *     else:    0 <= p < L  (sliding_window must be <= 0)
  * A query that sees nothing (L = 0, or n_s > L and P < 0) gets zeros. Softmax
- * statistics and sums in fp32, weights rounded to T for the tensor cores.
+ * statistics and sums in fp32, weights rounded to T for the tensor cores and
+ * summed as rounded.
  * Cached rows that no query of a sequence sees may hold anything; V of a row
  * that some of a sequence's queries see must be finite for the others too.
  *   q, out      : T[num_tokens][num_q_heads][head_dim]
@@ -525,7 +526,8 @@ size_t pkv_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads,
  *   group_starts : int32[num_groups + 1], not decreasing, within [0, num_seqs]
  *   prefix_blocks: int32[num_groups], clamped to [0, max_blocks_per_seq]
  * Everything else as for pkv_paged_prompt_attention with one query token per
- * sequence; workspace pkv_prefix_workspace_size.
+ * sequence, its rounded weights too (pkv_paged_attention_decode keeps them in
+ * fp32); workspace pkv_prefix_workspace_size.
  */
 pkv_status_t pkv_paged_prefix_decode(
     void* out, const void* q, const void* k_pool, const void* v_pool,

@@ -1447,7 +1447,9 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
   if (st == PKV_OK) st = prompt_pool_map(&maps.k, a.k_pool, tiles, head_dim, dtype);
   if (st == PKV_OK) st = prompt_pool_map(&maps.v, a.v_pool, tiles, head_dim, dtype);
   if (st != PKV_OK) return st;
-  const bool prefix = !a.query_starts;
+  // (without any group the grid takes everything, as paged_attention_decode's does: the prompt
+  // kernels with nothing to do took 64 sequences of 100 tokens from 7 to 15 us)
+  const bool prefix = !a.query_starts, alone = prefix && a.tails && a.num_groups == 0;
   pkv::DecodeArgs d{};
   alignas(64) CUtensorMap kmap[3], vmap[3];
   if (a.tails) {
@@ -1472,8 +1474,8 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
     d.query_rows = a.query_starts;
     d.num_rows = a.num_tokens;
     const pkv::PromptTails t = pkv::prompt_tails(a, head_dim, workspace);
-    d.tail_limit = t.limit;
-    if (prefix && a.num_groups > 0) {
+    if (!alone) d.tail_limit = t.limit;
+    if (prefix && !alone) {
       d.from = t.from;
       d.join_ml = t.ml;
       d.join_o = t.o;
@@ -1486,7 +1488,8 @@ pkv_status_t prompt_impl(const char* what, pkv::PromptArgs a, int head_dim, floa
   }
   const EnqueueLock lock(stream);
   // The prompt kernels choose what the grid takes, and prefixes come before what is joined to them.
-  cudaError_t err = pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, maps, stream);
+  cudaError_t err = cudaSuccess;
+  if (!alone) err = pkv::launch_prompt(a, dtype == PKV_BF16, head_dim, workspace, maps, stream);
   if (err == cudaSuccess && a.tails)
     err = pkv::launch_decode_tail(d, dtype == PKV_BF16, head_dim, round_pow2_group(a.group), kmap, vmap, stream);
   return cuda_status(err, what);

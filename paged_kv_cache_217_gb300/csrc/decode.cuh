@@ -38,6 +38,7 @@
 //    position L - W and masks the rows before it (token_range).
 #pragma once
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -84,7 +85,7 @@ struct DecodeArgs {
   const int32_t* query_rows;  // [S + 1]: sequence s's query is row query_rows[s] of q and out, where it has exactly
                               // one (others are left out); null: row s
   int num_rows;               // rows of q and out
-  const int* tail_limit;      // longer tails are left out
+  const int* tail_limit;      // longer tails are left out; null: none is
   const int32_t* from;        // [S]: positions before from[s] (a multiple of 16, or the length) are left out; null: none
   const float2* join_ml;      // [S][Hq] (max, sum) and [S][Hq][D] unnormalised sums over positions before from[s], joined
   const float* join_o;        // to the tail's; null: none
@@ -617,7 +618,7 @@ paged_decode_kernel(const DecodeArgs a) {
     if (j0 < a.max_blocks_per_seq) ids_early = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + j0);
   }
   int L = a.context_lens[s];
-  const int tail_limit = TAIL ? __ldcg(a.tail_limit) : 0;
+  const int tail_limit = TAIL && a.tail_limit ? __ldcg(a.tail_limit) : INT_MAX;
   const int max_len = a.max_blocks_per_seq * kBlock;
   if (L < 0 || L > max_len) {
     if (threadIdx.x == 0 && part == 0 && g == 0) flag(a.status, PKV_DEV_BAD_CONTEXT_LEN);

@@ -337,7 +337,7 @@ paged_decode_mma_kernel(const DecodeArgs a, const __grid_constant__ PoolMaps map
     if (j0 < a.max_blocks_per_seq) ids_early = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + j0);
   }
   int L = a.context_lens[s];
-  const int tail_limit = TAIL ? __ldcg(a.tail_limit) : 0;
+  const int tail_limit = TAIL && a.tail_limit ? __ldcg(a.tail_limit) : INT_MAX;
   // Q as the A operand: row gr holds query head hq0 + gr (zero past the group);
   // the block ids, the length and Q are all requested before the speculative
   // copies below and before anything waits for them.

@@ -22,7 +22,7 @@
 // While a warpgroup works on its scores the tensor cores run the other's products and its
 // own next scores. The running maximum is a reference that moves only when a score exceeds
 // it by 2^8; a move rescales the row's O in tensor memory (moving it with every new maximum:
-// window 194 -> 212 us, chunk 1454 -> 1549). Weights are rounded to the type (bf16 2^-8, fp16
+// window 190 -> 209 us, chunk 1470 -> 1580). Weights are rounded to the type (bf16 2^-8, fp16
 // 2^-11 relative, one rounding a weight), and l is the fp32 sum of the rounded ones, so that a
 // mean of equal values is that value and the roundings of a few large weights fall out. (The sum
 // of unrounded ones: 64 prompts 69.1 -> 66.8 us, 32 cross prompts 95.7 -> 94.3, else under 1 %;
@@ -31,10 +31,11 @@
 // Bound by the softmax warps: a tile of 64 x 256 scores takes 1700 cycles, of which the
 // products need 900 (head_dim 128) and the exponentials 512 of their unit; the rest are the
 // waits of two warps a scheduler that follow their scores step by step. Measured on GB300
-// (us, in a graph): 2048 tokens behind 15953, 96 heads of 128, 1500 (62 % of the sustained
-// library matrix product's rate); 64 prompts of 150 tokens, 32 heads on 8, 66; 4 chunks
-// of 2000 tokens, windows of 1024, 16 heads of 256 on 8, 191. Tiles of 128 tokens
-// with one S each: 78 for the 64 prompts, 1555 for the chunk.
+// (us, in a graph): 2048 tokens behind 15953, 96 heads of 128, 1470 to 1510 (1150 TFLOP/s, 61 %
+// of the library matrix product's burst rate and 68 % of its sustained one); 64 prompts of 150
+// tokens, 32 heads on 8, 69; 4 chunks of 2000 tokens, windows of 1024, 16 heads of 256 on 8, 190.
+// Tiles of 128 tokens with one S each, on an earlier build: 78 and 72 for the 64 prompts, 1555
+// and 1540 for the chunk. The pairs of figures below are of one build each.
 //
 // Tiles arrive by TMA, one copy a block, from a 4-D view of the pool {64 elements, 8
 // rows, head_dim / 64 chunks, 8-row groups}: a tile is then groups of swizzle atoms (8
@@ -62,11 +63,11 @@ constexpr int kPromptTile = 64;    // tokens of a KV tile
 // 23.8, 20.3); behind 1000, 8 heads on 2, 14.7, 13.0 and 13.5 (15.9, 13.7, 14.6); one token behind 500, 4 heads of 256
 // on 1, 12.7, 11.2 and 12.4; a prompt of 300 there 20.0, 20.6 and 19.1.
 constexpr int kPromptShareTiles = 2;
-// What an item costs besides its positions, in positions: 64 prompts of 150 tokens take 94 us with
-// 16, 70 with 128, 74 with 384.
+// What an item costs besides its positions, in positions: 64 prompts of 150 tokens take 92 us with
+// 16, 69 with 128, 72 with 384.
 constexpr int kPromptStart = 128;
-// Cuts this near an item's end are moved there: the same prompts take 82 us with 64, 70 with 256 and
-// 512; windows of 1024 198, 193 and 194.
+// Cuts this near an item's end are moved there: the same prompts take 82 us with 64, 69 with 256 and
+// 512; windows of 1024 196, 190 and 192.
 constexpr int kPromptSnap = 256;
 // A decode grid gives a single token one CTA a KV head, whose rate is near an SM's share of the memory's. One that
 // would take kTailShares times as long as an even share of all single tokens is cut into pieces here instead. 60 tokens
@@ -84,14 +85,13 @@ constexpr int kPromptPieces = 4;   // pieces that the copying warp may be ahead
 constexpr int kPromptNone = -1;
 // A piece of one tile of rows goes to one warpgroup, the next to the other; from this many
 // positions on, or with no piece behind it, to both. (256 and 4096 differ by less than 1 % in all cases
-// but one, 25.6 and 26.2 us for 8 sequences of 5 drafted tokens.)
+// but one: 8 sequences of 5 drafted tokens take 25.7 us with 256, 26.2 with 1024, 26.1 with 4096.)
 constexpr int kPromptSplit = 1024;
 
 template <int D>
 struct PromptCfg {
   static constexpr int GROUPS = D == 256 ? 1 : 2;     // softmax warpgroups
   static constexpr int TILE = kPromptTile;
-  static constexpr int ROWS = 128 * GROUPS;           // of an item
   static constexpr int CHUNKS = D / 64;
   static constexpr int SLOT = TILE * D * 2;           // bytes of a K or V tile
   static constexpr int SLOTS = D == 64 ? 16 : D == 128 ? 8 : 4;
@@ -521,7 +521,6 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
       limit = sh.limit;
       if (limit == kTailAll) break;
       segs = a.num_groups + a.num_seqs;
-      asm volatile("bar.sync 1, 96;" ::: "memory");
     }
     const long long s0 = sh.scan[0], s1 = sh.scan[1];
     total = s0 + s1 + sh.scan[2];
@@ -820,8 +819,9 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     // ---- MMA issue: a warp for each warpgroup ----
     // As soon as the weights are there O += P V, and S of a tile as soon as its K and a buffer
     // are. The two warps issue by turns (`lock`), so that while one warpgroup has its products
-    // made the other makes weights: side by side both would wait for both (a long chunk 1672 us
-    // without, 1454 with; short pieces are even). One lane issues, the
+    // made the other makes weights: side by side both would wait for both (a long chunk 1670 us
+    // without, 1470 with; documents 104 and 100; short pieces are even, but heads of 64 fall into one
+    // of two rhythms: 32 cross prompts 96 or 113, without turns 96). One lane issues, the
     // others keep step, so that all of it stays in uniform registers. The loop is short, without
     // waits of its own, and reads what the copying warp has worked out: every instruction between
     // two products is one that the tensor cores wait for.
