@@ -820,8 +820,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     // As soon as the weights are there O += P V, and S of a tile as soon as its K and a buffer
     // are. The two warps issue by turns (`lock`), so that while one warpgroup has its products
     // made the other makes weights: side by side both would wait for both (a long chunk 1670 us
-    // without, 1470 with; documents 104 and 100; short pieces are even, but heads of 64 fall into one
-    // of two rhythms: 32 cross prompts 96 or 113, without turns 96). One lane issues, the
+    // without, 1470 with; documents 104 and 100; 2048 tokens behind 8000, 32 heads of 64, 240 and 234;
+    // 32 cross prompts 97 and 96; short pieces are even). One lane issues, the
     // others keep step, so that all of it stays in uniform registers. The loop is short, without
     // waits of its own, and reads what the copying warp has worked out: every instruction between
     // two products is one that the tensor cores wait for.
