@@ -76,6 +76,9 @@ constexpr int kPromptSnap = 256;
 // lengths nothing measurable, and what follows prefixes 2 us.
 constexpr int kTailShares = 2;
 constexpr int kTailShort = 1024;  // (never worth that: 59 over 100 and one over 1000 26.9 us, over 1500 35.0 uncut and 29.7)
+// The list is then made again, which takes as long as half a position a sequence: 3 long ones (up to 20000) among 16000
+// short ones 363 us uncut and 336, among 65535 853 and 1319.
+constexpr float kTailList = 0.5f;
 constexpr int kTailAll = 0x7fffffff;
 constexpr float kPromptLazy = 8.f;
 // fp16 weights are 2^7 times as large, 2^(7 + 8) at most: one 2^-21 of the largest still has all its bits, and what
@@ -383,7 +386,8 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
   unsigned char* const misc = ring + C::SLOTS * C::SLOT;
   float2* const stats = reinterpret_cast<float2*>(misc + C::STATS_AT);            // [GROUPS][128] of a join
   unsigned char* const stage = misc + C::STAGE_AT;                                // per softmax warp
-  PromptSegment* const list = reinterpret_cast<PromptSegment*>(misc + C::LIST_AT);  // the segments, where there are few
+  PromptSegment* const list = reinterpret_cast<PromptSegment*>(misc + C::LIST_AT);  // the segments, where there are few,
+  long long* const runs = reinterpret_cast<long long*>(list);                       // else the costs of the 96 runs of them
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int WARP_KV = C::SOFTMAX / 32, WARP_Q = WARP_KV + 1, WARP_MMA = WARP_KV + 2;
 
@@ -474,7 +478,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
     asm volatile("bar.sync 2, 128;" ::: "memory");
     if (warp == 0) {
       const float even = (sh.sums[0] + sh.sums[1] + sh.sums[2] + sh.sums[3]) * (float(a.num_kv_heads) / kPromptSms);
-      const float least = fmaxf(kTailShort, kTailShares * even);
+      const float least = fmaxf(fmaxf(kTailShort, float(a.num_seqs) * kTailList), kTailShares * even);
       const int top = max(max(sh.most[0], sh.most[1]), max(sh.most[2], sh.most[3]));
       if (lane == 0) {
         sh.limit = float(top) <= least ? kTailAll : int(least);
@@ -515,6 +519,7 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
         if (lane >= o) at += x;
       }
       if (lane == 31) sh.scan[part] = at;
+      if (!listed) runs[runner] = mine;
       asm volatile("bar.sync 1, %0;" ::"r"(a.tails && !again ? 128 : 96) : "memory");
       if (!a.tails || again) break;
       again = true;
@@ -586,6 +591,14 @@ prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUte
               cached = seg;
               if (seg + lane < segs) mine_g = segment(seg + lane);
             }
+            // (what the grid takes is passed over, 32 at a time or a run: 4000 tokens of which 3 are cut 561 us without)
+            const uint32_t rest = __ballot_sync(kFull, cached + lane < segs && mine_g.nq > 0) >> (seg - cached);
+            if (rest == 0) {
+              const int per = (segs + 95) / 96;
+              for (seg = cached + 32; seg < segs && runs[seg / per] == 0;) seg = (seg / per + 1) * per;
+              continue;
+            }
+            seg += __ffs(rest) - 1;
             const int src = seg - cached;
             g.q0 = __shfl_sync(kFull, mine_g.q0, src);
             g.nq = __shfl_sync(kFull, mine_g.nq, src);

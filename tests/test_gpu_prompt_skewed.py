@@ -70,6 +70,25 @@ def test_behind_prefixes(starts, blocks, hq, hkv, d, dtype):
         assert torch.equal(again, out)
 
 
+@pytest.mark.parametrize("seqs", [500, 3000, 9001])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 2)])
+@pytest.mark.parametrize("at", [(0, 1, -1), (-1,), (0,), (400, 401, 2), (3,)])
+def test_few_among_thousands(at, hq, hkv, seqs):
+    """More than are listed in shared memory, long runs of which the grid takes; prompts among them, too."""
+    lens = np.random.default_rng(seqs).integers(0, 12, seqs)
+    new = np.ones(seqs, int)
+    new[7::1000] = 5
+    for i in at:
+        lens[i] = 2500
+    c = P.Case(lens, new, hq, hkv, 64, "bf16", seed=115)
+    rows = set(range(0, int(new.sum()), 37)) | {int(c.starts_np[i % seqs]) for i in at} | {int(c.starts_np[7]) + i for i in range(5)}
+    c.check(c.run(), heads=[hq - 1], wanted=rows)
+    held = lens.copy()
+    held[10] = 64
+    p = P.prefix_case(held, hq, hkv, 64, "bf16", [10, seqs - 5], [3], seed=116)
+    p.check(P.prefix_run(p), causal=False, heads=[0], tables=p.shared, wanted=set(range(0, seqs, 41)) | {i % seqs for i in at})
+
+
 def test_replayed_with_other_lengths():
     """A captured call: which tokens are long is read on the GPU."""
     seqs = 240
