@@ -524,6 +524,7 @@ size_t pkv_prompt_workspace_size(int num_tokens, int num_seqs, int num_q_heads,
  * shared-prefix schedule, -5, of pkv_paged_attention_decode finds the sharing
  * by itself, for up to 8 query rows a group).
  *   group_starts : int32[num_groups + 1], not decreasing, within [0, num_seqs]
+ *                  (num_groups at most num_seqs)
  *   prefix_blocks: int32[num_groups], clamped to [0, max_blocks_per_seq]
  * Everything else as for pkv_paged_prompt_attention with one query token per
  * sequence, its rounded weights too (pkv_paged_attention_decode keeps them in
